@@ -1,0 +1,82 @@
+"""64-bit definitions of the operators around the scan (include/selscan_ops.h), in torch on
+the CPU, token by token and value by value.
+
+TEST INFRASTRUCTURE ONLY, like the rest of this package: the HIP library never uses it, and it
+shares no code with it.
+"""
+from __future__ import annotations
+
+import torch
+
+F64 = torch.float64
+
+
+def _gates(x, r, i, A, reset):
+    s, g = 1.0 / (1.0 + torch.exp(-r)), 1.0 / (1.0 + torch.exp(-i))
+    la = A * s
+    a, w = torch.exp(la), torch.sqrt(-torch.expm1(2.0 * la))
+    if reset is not None:
+        on = (reset != 0).unsqueeze(-1)
+        a, w = a.masked_fill(on, 0.0), w.masked_fill(on, 1.0)
+    return s, g, la, a, w
+
+
+def glr_fwd(x, r, i, A, state=None, reset=None):
+    """(y, final state, checkpoints): h_t = a_t h_{t-1} + w_t sigmoid(i_t) x_t one token after
+    the other, the state in front of a reset token not read."""
+    x, r, i, A = (t.detach().cpu().to(F64) if not t.requires_grad else t for t in (x, r, i, A))
+    B, L, D = x.shape
+    reset = None if reset is None else reset.cpu()
+    s, g, la, a, w = _gates(x, r, i, A, reset)
+    h = torch.zeros(B, D, dtype=F64) if state is None else (state if state.requires_grad else state.cpu().to(F64))
+    ys, ck = [], []
+    for t in range(L):
+        if t % 64 == 0:
+            ck.append(h)
+        b = w[:, t] * g[:, t] * x[:, t]
+        old = a[:, t] * h
+        if reset is not None:
+            old = torch.where((reset[:, t] != 0)[:, None], torch.zeros_like(old), old)
+        h = old + b
+        ys.append(h)
+    return torch.stack(ys, 1), h, torch.stack(ck, 1)
+
+
+def glr_bwd(x, r, i, A, dy, state=None, reset=None, dstate_final=None):
+    """Gradients by the chain rule in reverse order, and for each the size its terms reach
+    (what its rounding errors are measured against): {name: (value, scale)}."""
+    x, r, i, A, dy = (t.detach().cpu().to(F64) for t in (x, r, i, A, dy))
+    B, L, D = x.shape
+    reset = None if reset is None else reset.cpu()
+    s, g, la, a, w = _gates(x, r, i, A, reset)
+    h0 = torch.zeros(B, D, dtype=F64) if state is None else state.cpu().to(F64)
+    y, _, _ = glr_fwd(x, r, i, A, h0, reset)
+    before = torch.cat([h0[:, None], y[:, :-1]], 1)
+    K = torch.zeros(B, D, dtype=F64) if dstate_final is None else dstate_final.cpu().to(F64)
+    G = torch.zeros_like(x)
+    for t in range(L - 1, -1, -1):
+        G[:, t] = dy[:, t] + K
+        K = a[:, t] * G[:, t]
+        if reset is not None:
+            K = torch.where((reset[:, t] != 0)[:, None], torch.zeros_like(K), K)
+    v = g * x
+    q = torch.where(w > 0, a * a / w, torch.zeros_like(w))
+    dla = G * (a * before - q * v)
+    size = G.abs() * (a * before.abs() + q * v.abs())
+    if reset is not None:
+        on = (reset != 0).unsqueeze(-1)
+        dla, size = dla.masked_fill(on, 0.0), size.masked_fill(on, 0.0)
+    top = G.abs().amax((0, 1))                                       # per channel
+
+    def pair(val, scale):
+        return val, scale
+
+    return {"dx": pair(G * w * g, top), "di": pair(G * w * v * (1 - g), top * v.abs().amax((0, 1))),
+            "dr": pair(dla * la * (1 - s), (size * la.abs()).amax((0, 1))),
+            "dA": pair((dla * s).sum((0, 1)), (size * s).sum((0, 1))), "dstate_init": pair(K, top)}
+
+
+def memory(r, A, reset=None):
+    """Longest memory among the channels, in tokens: 1 / min(1 - a)."""
+    la = A.cpu().to(F64) / (1.0 + torch.exp(-r.detach().cpu().to(F64)))
+    return float((1.0 / (-torch.expm1(la)).clamp_min(1e-30)).max())

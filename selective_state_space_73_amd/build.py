@@ -23,6 +23,10 @@ SOURCES = KERNEL_UNITS + [os.path.join(CSRC, "selscan_api.cpp"), os.path.join(CS
 HEADERS = [os.path.join(CSRC, "selscan_device.h"), os.path.join(CSRC, "selscan_bwd.h"),
            os.path.join(CSRC, "selscan_block.h"), os.path.join(CSRC, "selscan_gemm.h"),
            os.path.join(CSRC, "selscan_internal.h"), os.path.join(INCLUDE, "selscan.h")]
+# the operators around the scan (include/selscan_ops.h), in the same library
+OPS_UNITS = sorted(glob.glob(os.path.join(CSRC, "ops_*.hip")))
+OPS_SOURCES = OPS_UNITS + sorted(glob.glob(os.path.join(CSRC, "ops_*.cpp")))
+OPS_HEADERS = sorted(glob.glob(os.path.join(CSRC, "ops_*.h"))) + [os.path.join(INCLUDE, "selscan_ops.h")]
 LIBS = []
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -45,9 +49,9 @@ def _run(cmd):
 
 
 def kernel_digest() -> str:
-    """sha256 over the sources that decide what a launch does (the kernels' code,
-    launch constants and the chunking rule of the C ABI layer), so that measurements
-    taken on one build can be matched to it later."""
+    """sha256 over the sources that decide what a launch of the scan or the block does (the
+    kernels' code, launch constants and the chunking rule of the C ABI layer), so that
+    measurements taken on one build can be matched to it later."""
     h = hashlib.sha256()
     for path in sorted(SOURCES + HEADERS[:5]):
         with open(path, "rb") as f:
@@ -65,7 +69,7 @@ def build(verbose: bool = False, jobs: int = 0) -> str:
     spills, occupancy) of the kernel units is kept in _build/kernel_resources.txt."""
     os.makedirs(OBJDIR, exist_ok=True)
     cmds, objs = [], []
-    for src in SOURCES:
+    for src in SOURCES + OPS_SOURCES:
         obj = os.path.join(OBJDIR, os.path.basename(src) + ".o")
         cmd = [HIPCC, *COMMON, *DEVICE_FLAGS, "-Rpass-analysis=kernel-resource-usage", "-c", src, "-o", obj]
         if src.endswith(".cpp"):
@@ -116,7 +120,7 @@ def is_stale() -> bool:
     if not os.path.exists(LIB):
         return True
     t = os.path.getmtime(LIB)
-    return any(os.path.getmtime(s) > t for s in SOURCES + HEADERS)
+    return any(os.path.getmtime(s) > t for s in SOURCES + HEADERS + OPS_SOURCES + OPS_HEADERS)
 
 
 if __name__ == "__main__":

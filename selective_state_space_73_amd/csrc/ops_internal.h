@@ -1,0 +1,37 @@
+// Internal interface between the C-ABI layer of the operators (include/selscan_ops.h) and
+// their HIP kernels.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "selscan_internal.h"
+#include "selscan_ops.h"
+
+namespace selscan {
+
+constexpr int kGlrCols = 128;       // channels per workgroup of the recurrence kernels (2 per lane)
+constexpr int kGlrFwdWaves = 8;     // waves of a forward workgroup, each with its own run of tokens
+constexpr int kGlrFwdTokens = 16;   // tokens per wave of the forward
+constexpr int kGlrBwdWaves = 8;
+constexpr int kGlrBwdTokens = 8;    // tokens per wave of the backward
+constexpr int64_t kGlrFwdChunk = kGlrFwdWaves * kGlrFwdTokens;
+constexpr int64_t kGlrBwdChunk = kGlrBwdWaves * kGlrBwdTokens;
+
+// One launch of the recurrence, already validated by the C-ABI layer.
+struct LaunchGlr {
+    enum Pass { kFwd, kBwd, kStep } pass;
+    bool bf16;
+    bool vec;                    // every row starts on two elements and D is even: two channels per access
+    int64_t batch, L, D;
+    ss_view x, r, i;
+    const float* A; const uint8_t* reset; void* y; float* state; float* ckpt;
+    ss_glr_grads g;
+    int64_t nchunks;             // chunks per batch row
+    unsigned* ticket;            // workspace: next tile to take (several chunks only)
+    uint64_t* slots;             // workspace: [nchunks, B, D] published chunk results (several chunks only)
+    float* part;                 // workspace of the backward: [nchunks, B, D] parts of dA
+    void* stream;
+};
+hipError_t launch_glr(const LaunchGlr& p);
+
+}  // namespace selscan

@@ -1,0 +1,286 @@
+"""GPU: the gated linear recurrence against its 64-bit definition.
+
+Tolerances. One step rounds a and b = w sigmoid(i) x to 32 bits; with u = 2^-24 the exponent
+of a sigmoid of |r| <= 6 carries at most 6 log2(e) u ln 2 + its own exp2, addition and
+reciprocal (1 ulp = 2 u each): under 16 u in all, so b is off by at most 2^-19 of itself (two
+sigmoids, the root and two products). a = 1 + e has the rounding of the sum (u) and 16 u of e;
+the latter adds at most 16 u |e| / (1 - a) = 16 u over a channel's whole memory, the former,
+with the product's and the sum's own rounding, 4 u for each token the state remembers, at most
+min(L, 1 / (1 - a)). All relative to the largest state. Hence
+    rel(L, memory) = 2^-18 + 4 * 2^-24 * min(L, memory),
+twice that for products of two such quantities (gradients: a state and an adjoint), plus half
+a step of the I/O type for what is stored in it.
+"""
+import pytest
+import torch
+
+from oracle import ops as O
+
+pytestmark = pytest.mark.gpu
+
+ss = pytest.importorskip("selective_state_space_73_amd")
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+HALF = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8}
+
+
+def rel(L, mem):
+    return 2.0 ** -18 + 4 * 2.0 ** -24 * min(L, mem)
+
+
+def make(B, L, D, io, seed=0, fused=False, lo=0.02, hi=3.0, view=False):
+    g = torch.Generator().manual_seed(1000 + seed)
+    n = lambda *s: torch.randn(*s, generator=g).to(DT[io]).cuda()  # noqa: E731
+    if fused:
+        x, r, i = n(B, L, 3 * D).split(D, dim=-1)
+    elif view:                                  # odd strides and an odd start
+        big = n(3, B, L + 2, D + 5)
+        x, r, i = (big[k, :, 1:L + 1, 3:3 + D] for k in range(3))
+    else:
+        x, r, i = n(B, L, D), n(B, L, D), n(B, L, D)
+    A = -torch.exp(torch.rand(D, generator=g) * 5 - 4).clamp(lo, hi).cuda()
+    h0 = torch.randn(B, D, generator=g).cuda()
+    return x, r, i, A, h0, n(B, L, D), torch.randn(B, D, generator=g).cuda(), g
+
+
+def resets(kind, B, L, g):
+    if kind is None:
+        return None
+    if kind == "all":
+        return torch.ones(B, L, dtype=torch.uint8).cuda()
+    z = (torch.rand(B, L, generator=g) < (0.5 if kind == "dense" else 0.02)).to(torch.uint8)
+    if kind == "ends":
+        z.zero_()
+        z[:, 0] = 7                             # any nonzero value
+        z[:, -1] = 1
+    return z.cuda()
+
+
+def near(got, want, tol, io, scale=None):
+    got, want = got.detach().double().cpu(), want.double()
+    scale = want.abs().amax() if scale is None else scale
+    bound = tol * scale + HALF[io] * want.abs() * (1 + tol) + 1e-30
+    worst = ((got - want).abs() / bound).max().item()
+    print(f"worst error over bound {worst:.3f}", flush=True)
+    assert torch.isfinite(got).all() and worst <= 1.0
+
+
+SHAPES = [(1, 1, 1), (2, 1, 6), (1, 3, 2), (2, 15, 130), (1, 16, 128), (1, 17, 127), (3, 64, 66), (1, 127, 129),
+          (1, 128, 256), (2, 129, 64), (2, 300, 131), (1, 1025, 7), (5, 513, 320)]
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("B,L,D", SHAPES)
+@pytest.mark.parametrize("kind", [None, "dense", "rare", "ends"])
+def test_forward(B, L, D, io, kind):
+    x, r, i, A, h0, _, _, g = make(B, L, D, io, seed=L + D)
+    rs = resets(kind, B, L, g)
+    tol = rel(L, O.memory(r, A))
+    ck = torch.full(ss.glr_ckpt_shape(B, L, D), float("nan"), device="cuda")
+    h = h0.clone()
+    y = ss.ss_glr_fwd(x, r, i, A, state=h, reset=rs, ckpt=ck)
+    yw, hw, cw = O.glr_fwd(x, r, i, A, h0, rs)
+    top = torch.maximum(yw.abs().max(), h0.abs().max().double().cpu())
+    near(y, yw, tol, io, top)
+    near(h, hw, tol, "f32", top)
+    near(ck, cw, tol, "f32", top)
+    # without a state: from zero, nothing returned
+    near(ss.ss_glr_fwd(x, r, i, A, reset=rs), O.glr_fwd(x, r, i, A, None, rs)[0], tol, io, top)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("B,L,D", SHAPES)
+@pytest.mark.parametrize("kind", [None, "dense", "ends"])
+def test_backward(B, L, D, io, kind):
+    x, r, i, A, h0, dy, dh, g = make(B, L, D, io, seed=7 * L + D)
+    rs = resets(kind, B, L, g)
+    tol = 2 * rel(L, O.memory(r, A))
+    ck = torch.empty(ss.glr_ckpt_shape(B, L, D), device="cuda")
+    ss.ss_glr_fwd(x, r, i, A, state=h0.clone(), reset=rs, ckpt=ck)
+    got = ss.ss_glr_bwd(x, r, i, A, ck, dy, reset=rs, dstate_final=dh)
+    want = O.glr_bwd(x, r, i, A, dy, h0, rs, dh)
+    for k, (val, scale) in want.items():
+        print(k, end=" ")
+        near(got[k], val, 4 * tol, io if k in ("dx", "dr", "di") else "f32", scale)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("how", ["fused", "view"])
+@pytest.mark.parametrize("D", [64, 33])
+def test_strided_inputs(how, io, D):
+    B, L = 2, 200
+    x, r, i, A, h0, dy, dh, _ = make(B, L, D, io, seed=D, fused=how == "fused", view=how == "view")
+    c = [t.contiguous() for t in (x, r, i)]
+    outs = []
+    for t in ((x, r, i), c):
+        ck = torch.empty(ss.glr_ckpt_shape(B, L, D), device="cuda")
+        h = h0.clone()
+        y = ss.ss_glr_fwd(*t, A, state=h, ckpt=ck)
+        outs.append([y, h, ck, *ss.ss_glr_bwd(*t, A, ck, dy, dstate_final=dh).values()])
+        outs[-1].append(ss.ss_glr_step(*(q[:, 3] for q in t), A, h.clone()))
+    for a, b in zip(*outs):
+        near(a, b.double().cpu(), 2 * rel(L, 50), io)      # one definition, two ways of reading: each within its own bound
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("S,D", [(1, 1), (1, 2), (3, 129), (64, 512), (257, 34)])
+def test_step(S, D, io):
+    x, r, i, A, h0, _, _, g = make(S, 4, D, io, seed=S)
+    rs = (torch.rand(S, generator=g) < 0.3).to(torch.uint8).cuda()
+    h = h0.clone()
+    hw = h0
+    for t in range(4):
+        xt, rt, it = (q[:, t] for q in (x, r, i))
+        y = ss.ss_glr_step(xt, rt, it, A, h, reset=rs if t == 2 else None)
+        yw, hw, _ = O.glr_fwd(xt[:, None], rt[:, None], it[:, None], A, hw, rs[:, None] if t == 2 else None)
+        near(y, yw[:, 0], rel(4, 4), io, hw.abs().max() + h0.abs().max().double().cpu())
+        near(h, hw, rel(4, 4), "f32", hw.abs().max() + h0.abs().max().double().cpu())
+
+
+def test_pieces_equal_the_whole():
+    B, L, D = 2, 700, 96
+    x, r, i, A, h0, _, _, _ = make(B, L, D, "f32")
+    whole, h = h0.clone(), h0.clone()
+    y = ss.ss_glr_fwd(x, r, i, A, state=whole)
+    parts = [ss.ss_glr_fwd(x[:, a:b], r[:, a:b], i[:, a:b], A, state=h) for a, b in ((0, 1), (1, 130), (130, 700))]
+    tol = 2 * rel(L, O.memory(r, A))
+    near(torch.cat(parts, 1), y.double().cpu(), tol, "f32")
+    near(h, whole.double().cpu(), tol, "f32")
+
+
+def test_reset_keeps_a_bad_document_to_itself():
+    """NaN and infinity in one document, an empty state of NaN in front of the first."""
+    B, L, D = 1, 600, 40
+    x, r, i, A, h0, dy, _, _ = make(B, L, D, "f32")
+    rs = torch.zeros(B, L, dtype=torch.uint8, device="cuda")
+    rs[0, 0] = rs[0, 200] = rs[0, 433] = 1
+    x[0, 250, 3] = float("nan")
+    x[0, 300, 4] = float("inf")
+    h0[:] = float("nan")
+    ck = torch.empty(ss.glr_ckpt_shape(B, L, D), device="cuda")
+    y = ss.ss_glr_fwd(x, r, i, A, state=h0, reset=rs, ckpt=ck)
+    yw, _, _ = O.glr_fwd(x, r, i, A, None, rs)
+    tol = rel(L, O.memory(r, A))
+    near(y[:, :200], yw[:, :200], tol, "f32")
+    near(y[:, 433:], yw[:, 433:], tol, "f32")
+    assert torch.isnan(y[0, 250:433, 3]).all() and not torch.isfinite(y[0, 300:433, 4]).any()
+    assert torch.isfinite(y[0, 200:433, 5:]).all() and torch.isfinite(h0).all()
+    # the gradient of a bad document stays in it too
+    dy[0, 220] = float("nan")
+    g = ss.ss_glr_bwd(x, r, i, A, ck, dy, reset=rs)
+    assert torch.isfinite(g["dx"][:, :200]).all() and torch.isfinite(g["dx"][:, 433:]).all()
+    assert torch.isfinite(g["dstate_init"]).all() and (g["dstate_init"] == 0).all()
+
+
+def test_extreme_gates():
+    """Gates far out, a decay of exactly 1 (A = 0), decays that underflow."""
+    B, L, D = 1, 140, 8
+    x, r, i, A, h0, dy, dh, _ = make(B, L, D, "f32")
+    A[0] = 0.0
+    A[1] = -1e4
+    r[:, :, 2] = 80.0
+    r[:, :, 3] = -80.0
+    i[:, :, 4] = -90.0
+    i[:, :, 5] = 90.0
+    A[6] = -1e-30
+    ck = torch.empty(ss.glr_ckpt_shape(B, L, D), device="cuda")
+    h = h0.clone()
+    y = ss.ss_glr_fwd(x, r, i, A, state=h, ckpt=ck)
+    yw, _, _ = O.glr_fwd(x, r, i, A, h0)
+    # exp2 of 80 log2(e) carries 80 u of its argument: 2^-17 in all
+    tol = 2.0 ** -16 + 4 * 2.0 ** -24 * L
+    near(y, yw, tol, "f32")
+    assert torch.equal(y[0, -1, 0], h0[0, 0]) and torch.equal(h[0, 0], h0[0, 0])
+    got = ss.ss_glr_bwd(x, r, i, A, ck, dy, dstate_final=dh)
+    for k, (val, scale) in O.glr_bwd(x, r, i, A, dy, h0, None, dh).items():
+        print(k, end=" ")
+        keep = [1, 2, 3, 4, 5, 7]                # A = 0 and 1e-30: the write term's slope is infinite, or nearly so
+        near(got[k][..., keep], val[..., keep], 8 * tol, "f32", scale[keep])
+        assert torch.isfinite(got[k]).all()
+
+
+def test_results_do_not_depend_on_timing():
+    """Several hundred chunks of few channels, so that workgroups wait for each other, while
+    other work comes and goes on a second stream: bit-equal every time."""
+    B, L, D = 1, 20000, 260
+    x, r, i, A, h0, dy, dh, _ = make(B, L, D, "bf16")
+    side = torch.cuda.Stream()
+    junk = torch.randn(2048, 2048, device="cuda")
+    first = None
+    for n in range(4):
+        if n % 2:
+            with torch.cuda.stream(side):
+                for _ in range(5):
+                    junk = junk * 1.0001
+        ck = torch.empty(ss.glr_ckpt_shape(B, L, D), device="cuda")
+        h = h0.clone()
+        y = ss.ss_glr_fwd(x, r, i, A, state=h, ckpt=ck)
+        now = [y, h, ck, *ss.ss_glr_bwd(x, r, i, A, ck, dy, dstate_final=dh).values()]
+        torch.cuda.synchronize()
+        if first is None:
+            first = now
+            yw, hw, _ = O.glr_fwd(x[:, :, :8], r[:, :, :8], i[:, :, :8], A[:8], h0[:, :8])
+            near(y[:, :, :8], yw, rel(L, O.memory(r, A)), "bf16")
+        assert all(torch.equal(a, b) for a, b in zip(first, now))
+
+
+def test_two_streams_and_given_buffers():
+    B, L, D = 1, 1000, 130
+    sets = [make(B, L, D, "f32", seed=k) for k in (1, 2)]
+    want = [ss.ss_glr_fwd(s[0], s[1], s[2], s[3]) for s in sets]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    dims = ss.ss_glr_dims(B, L, D, ss.SS_F32, 0)
+    torch.cuda.synchronize()
+    got = []
+    for k in range(6):
+        s = sets[k % 2]
+        ws = torch.full((ss.ss_glr_workspace_bytes(dims) + 64,), 0xAB, dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        got.append(ss.ss_glr_fwd(s[0], s[1], s[2], s[3], workspace=ws, stream=streams[k % 2]))
+    torch.cuda.synchronize()
+    for k, y in enumerate(got):
+        assert torch.equal(y, want[k % 2])
+    y = torch.full((B, L, D + 0), 9.0, device="cuda")
+    assert ss.ss_glr_fwd(*sets[0][:4], y=y) is y and torch.equal(y, want[0])
+
+
+def test_graph_replays():
+    """A captured training step and decode step, replayed between eager work on the same
+    tensors: every replay equals the eager result."""
+    B, L, D = 2, 300, 130
+    x, r, i, A, h0, dy, dh, _ = make(B, L, D, "bf16")
+    ck = torch.empty(ss.glr_ckpt_shape(B, L, D), device="cuda")
+
+    def step(h):
+        y = ss.ss_glr_fwd(x, r, i, A, state=h, ckpt=ck)
+        g = ss.ss_glr_bwd(x, r, i, A, ck, dy, dstate_final=dh)
+        z = ss.ss_glr_step(x[:, 0], r[:, 0], i[:, 0], A, h)
+        return [y, z, *g.values()]
+
+    h = h0.clone()
+    step(h)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step(h)
+    for n in range(4):
+        x.copy_(torch.randn_like(x))
+        h.copy_(h0)
+        eager = [t.clone() for t in step(h)]
+        he = h.clone()
+        torch.cuda.synchronize()
+        h.copy_(h0)
+        for t in outs:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(h, he) and all(torch.equal(a, b) for a, b in zip(outs, eager))
+
+
+def test_outputs_end_where_they_should():
+    """Nothing behind the last token or channel is touched."""
+    B, L, D = 1, 77, 30
+    x, r, i, A, h0, dy, _, _ = make(B, L, D, "f32")
+    buf = torch.full((B * L * D + 256,), 5.0, device="cuda")
+    y = buf[128:128 + B * L * D].view(B, L, D)
+    ss.ss_glr_fwd(x, r, i, A, y=y)
+    assert (buf[:128] == 5.0).all() and (buf[128 + B * L * D:] == 5.0).all()
