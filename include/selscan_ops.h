@@ -4,6 +4,9 @@
  *
  *   ss_glr_fwd, ss_glr_bwd, ss_glr_step   a gated linear recurrence: forward over whole
  *                                         sequences, its gradients, one decode token
+ *   ss_quant_q8                           rounding to 8-bit floating point with block scales
+ *   ss_norm_q8                            the same behind a residual's addition and RMS norm
+ *   ss_gemm_q8                            the product of two such matrices
  *
  * Ownership, ordering, errors: as in selscan.h. Every pointer inside a struct is a DEVICE
  * pointer owned by the caller, arguments are validated on the host before anything is
@@ -97,6 +100,62 @@ typedef struct {
  * Outputs are overwritten; none may overlap an input, another output or the workspace. */
 ss_status ss_glr_bwd(const ss_glr_dims* dims, const ss_glr_args* args, const ss_glr_grads* grads, void* workspace,
                      size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * 8-bit floating point with block scales. A matrix v [M, K] is held as q [M, K], one e4m3
+ * byte a value (4 exponent bits, 3 stored mantissa bits, largest finite value 448, no
+ * infinity), and fp32 scales; it stands for scale * q. A scale covers 128 consecutive
+ * columns of one row (scale [M, ceil(K/128)], activations) or of 128 consecutive rows
+ * ("square": scale [ceil(M/128), ceil(K/128)], weights); blocks at the ends are smaller.
+ *   scale = max(max |v| / 448, 2^-126),   q = e4m3(v / scale), to nearest, ties to even.
+ * A NaN becomes a NaN and leaves its block's scale alone; an infinity makes its block's scale
+ * infinite (its finite values stand for NaN then). All matrices are contiguous row-major. */
+typedef struct {
+    int64_t rows;       /* M, >= 1                                                      */
+    int64_t cols;       /* K, 1 <= K < 2^31                                              */
+    int32_t io_dtype;   /* ss_dtype of x (and residual, sum)                             */
+    int32_t square;     /* ss_quant_q8: 0 = blocks of 1 x 128, 1 = 128 x 128             */
+    float   eps;        /* ss_norm_q8: > 0                                               */
+    int32_t reserved;   /* 0                                                             */
+} ss_q8_dims;
+
+ss_status ss_quant_q8(const ss_q8_dims* dims, const void* x, void* q, float* scale, void* stream);
+
+/* The norm in front of a layer: with s = x + residual (in fp32),
+ *   n = s / sqrt(mean over the row of s^2 + eps) * w,
+ * rounded in blocks of 1 x 128. The norm takes s before it is rounded to the I/O dtype. */
+typedef struct {
+    const void*  x;         /* [M,K] io                                                     */
+    const void*  residual;  /* [M,K] io or NULL: s = x                                      */
+    const float* w;         /* [K]                                                          */
+    void*        q;         /* [M,K] bytes OUT                                              */
+    float*       scale;     /* [M, ceil(K/128)] OUT                                         */
+    void*        sum;       /* [M,K] io OUT: s; required with a residual, else NULL.
+                               May be x or residual itself (in place)                       */
+} ss_norm_q8_args;
+
+ss_status ss_norm_q8(const ss_q8_dims* dims, const ss_norm_q8_args* args, void* stream);
+
+/* y[m,n] = sum_k (xs[m, k/128] xq[m,k]) (ws[n/128, k/128] wq[n,k])  (+ residual[m,n]).
+ * Products and sums of a block on the matrix cores in fp32, blocks added in fp32 in order
+ * of k (in a fixed order of several such sums where M is small). */
+typedef struct {
+    int64_t m, n;       /* rows of X and of W, 1 <= m, n < 2^31                          */
+    int64_t k;          /* a multiple of 16, < 2^31                                      */
+    int32_t y_dtype;    /* ss_dtype of y and residual                                    */
+    int32_t reserved;   /* 0                                                             */
+} ss_gemm_q8_dims;
+
+typedef struct {
+    const void*  xq;        /* [M,K] e4m3, 16-byte aligned                                  */
+    const float* xs;        /* [M, ceil(K/128)]                                             */
+    const void*  wq;        /* [N,K] e4m3, 16-byte aligned                                  */
+    const float* ws;        /* [ceil(N/128), ceil(K/128)]                                   */
+    const void*  residual;  /* [M,N] of y_dtype, 16-byte aligned, or NULL; may be y itself  */
+    void*        y;         /* [M,N] OUT, 16-byte aligned                                   */
+} ss_gemm_q8_args;
+
+ss_status ss_gemm_q8(const ss_gemm_q8_dims* dims, const ss_gemm_q8_args* args, void* stream);
 
 #ifdef __cplusplus
 }

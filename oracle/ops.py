@@ -80,3 +80,47 @@ def memory(r, A, reset=None):
     """Longest memory among the channels, in tokens: 1 / min(1 - a)."""
     la = A.cpu().to(F64) / (1.0 + torch.exp(-r.detach().cpu().to(F64)))
     return float((1.0 / (-torch.expm1(la)).clamp_min(1e-30)).max())
+
+
+# ---------------------------------------------------------------------------
+# 8-bit floating point with block scales
+
+Q8_MAX, Q8_TINY = 448.0, 2.0 ** -126
+
+
+def rms_norm(x, w, residual=None, eps=1e-5):
+    """(n, s): s = x + residual, n = s / sqrt(mean(s^2) + eps) * w."""
+    s = x.cpu().to(F64)
+    if residual is not None:
+        s = s + residual.cpu().to(F64)
+    return s / torch.sqrt((s * s).mean(-1, keepdim=True) + eps) * w.cpu().to(F64), s
+
+
+def block_tops(v, square=False):
+    """Largest |v| of every block, NaN left out, block by block."""
+    v = v.cpu().to(F64).abs()
+    M, K = v.shape
+    rows = 128 if square else 1
+    out = torch.zeros(-(-M // rows), -(-K // 128), dtype=F64)
+    for a in range(out.shape[0]):
+        for b in range(out.shape[1]):
+            blk = v[a * rows:(a + 1) * rows, b * 128:(b + 1) * 128]
+            out[a, b] = torch.nan_to_num(blk, nan=0.0, posinf=float("inf")).max()
+    return out
+
+
+def spread(scale, M, K, square=False):
+    """A scale per value."""
+    row = torch.arange(M) // (128 if square else 1)
+    return scale.cpu().to(F64)[row][:, torch.arange(K) // 128]
+
+
+def values(q, scale, square=False):
+    """What q and its scales stand for."""
+    return q.cpu().to(torch.float32).to(F64) * spread(scale, q.shape[0], q.shape[1], square)
+
+
+def half_step(v, scale):
+    """Half the distance of neighbouring e4m3 values at v / scale, times scale: 2^-4 of |v| at
+    most, 2^-10 scale below the smallest normal value."""
+    return torch.maximum(v.abs() * 2.0 ** -4, scale * 2.0 ** -10)

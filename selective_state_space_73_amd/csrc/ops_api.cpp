@@ -6,6 +6,7 @@
 #include <cstdarg>
 #include <cstdint>
 #include <cstdio>
+#include <initializer_list>
 
 #include "ops_internal.h"
 
@@ -180,6 +181,43 @@ ss_status glr_forward(const ss_glr_dims* d, const ss_glr_args* a, void* workspac
     return launched(selscan::launch_glr(p));
 }
 
+// ---------------------------------------------------------------------------
+// 8-bit floating point with block scales
+
+constexpr int64_t kMaxGrid = INT32_MAX;
+
+ss_status check_q8_dims(const ss_q8_dims* d, bool norm) {
+    if (!d) return fail(SS_ERR_INVALID_ARG, "dims is NULL");
+    if (d->rows < 1 || d->cols < 1) return fail(SS_ERR_INVALID_ARG, "rows and cols must be positive");
+    if (d->cols > INT32_MAX || d->rows > kMaxGrid) return fail(SS_ERR_INVALID_ARG, "rows or cols too large");
+    if (d->rows > INT64_MAX / 16 / d->cols) return fail(SS_ERR_INVALID_ARG, "rows x cols too large");
+    if (d->io_dtype != SS_F32 && d->io_dtype != SS_BF16) return fail(SS_ERR_UNSUPPORTED, "io_dtype %d unknown", d->io_dtype);
+    if (d->reserved != 0) return fail(SS_ERR_INVALID_ARG, "reserved must be 0");
+    if (norm && !(d->eps > 0.0f)) return fail(SS_ERR_INVALID_ARG, "eps must be positive");
+    if (norm && d->square != 0) return fail(SS_ERR_INVALID_ARG, "square must be 0 for the norm");
+    if (d->square != 0 && d->square != 1) return fail(SS_ERR_INVALID_ARG, "square must be 0 or 1");
+    if (d->square && ceil_div(d->rows, 128) > 65535) return fail(SS_ERR_INVALID_ARG, "too many rows of squares");
+    return SS_OK;
+}
+
+// whether a row of 8 elements can be one access wherever it starts
+bool q8_vec(const ss_q8_dims& d, std::initializer_list<const void*> io16, const void* q) {
+    bool v = d.cols % 8 == 0 && ((uintptr_t)q & 7u) == 0;
+    for (const void* p : io16) v = v && ((uintptr_t)p & 15u) == 0;
+    return v;
+}
+
+ss_status check_gemm_q8_dims(const ss_gemm_q8_dims* d) {
+    if (!d) return fail(SS_ERR_INVALID_ARG, "dims is NULL");
+    if (d->m < 1 || d->n < 1 || d->k < 1) return fail(SS_ERR_INVALID_ARG, "m, n and k must be positive");
+    if (d->m > INT32_MAX || d->n > INT32_MAX || d->k > INT32_MAX) return fail(SS_ERR_INVALID_ARG, "m, n or k too large");
+    if (d->k % 16) return fail(SS_ERR_UNSUPPORTED, "k %lld is not a multiple of 16", (long long)d->k);
+    if (d->y_dtype != SS_F32 && d->y_dtype != SS_BF16) return fail(SS_ERR_UNSUPPORTED, "y_dtype %d unknown", d->y_dtype);
+    if (d->reserved != 0) return fail(SS_ERR_INVALID_ARG, "reserved must be 0");
+    if (ceil_div(d->m, 128) > INT32_MAX / ceil_div(d->n, 128)) return fail(SS_ERR_INVALID_ARG, "m x n too large");
+    return SS_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -233,6 +271,80 @@ ss_status ss_glr_bwd(const ss_glr_dims* dims, const ss_glr_args* args, const ss_
     p.g = *g;
     glr_attach(p, l, workspace);
     return launched(selscan::launch_glr(p));
+}
+
+ss_status ss_quant_q8(const ss_q8_dims* dims, const void* x, void* q, float* scale, void* stream) {
+    ss_status s = check_q8_dims(dims, false);
+    if (s != SS_OK) return s;
+    if (!x || !q || !scale) return fail(SS_ERR_INVALID_ARG, "x, q or scale is NULL");
+    const size_t es = io_size(dims->io_dtype), M = (size_t)dims->rows, K = (size_t)dims->cols, KB = (K + 127) / 128;
+    if ((uintptr_t)x % es || ((uintptr_t)scale & 3u)) return fail(SS_ERR_INVALID_ARG, "x or scale not aligned to its element");
+    const Range ins[] = {{x, M * K * es, "x"}};
+    const Range outs[] = {{q, M * K, "q"}, {scale, (dims->square ? (M + 127) / 128 : M) * KB * 4, "scale"}};
+    if ((s = check_overlaps(outs, 2, ins, 1)) != SS_OK) return s;
+    selscan::LaunchQ8 p{};
+    p.bf16 = dims->io_dtype == SS_BF16;
+    p.square = dims->square != 0;
+    p.vec = q8_vec(*dims, {x}, q);
+    p.x = x; p.q = static_cast<uint8_t*>(q); p.scale = scale;
+    p.M = dims->rows; p.K = dims->cols;
+    p.stream = stream;
+    return launched(selscan::launch_q8(p));
+}
+
+ss_status ss_norm_q8(const ss_q8_dims* dims, const ss_norm_q8_args* a, void* stream) {
+    ss_status s = check_q8_dims(dims, true);
+    if (s != SS_OK) return s;
+    if (!a) return fail(SS_ERR_INVALID_ARG, "args is NULL");
+    if (!a->x || !a->w || !a->q || !a->scale) return fail(SS_ERR_INVALID_ARG, "x, w, q or scale is NULL");
+    if (a->residual && !a->sum) return fail(SS_ERR_INVALID_ARG, "sum is required with a residual");
+    if (!a->residual && a->sum) return fail(SS_ERR_INVALID_ARG, "sum given without a residual");
+    const size_t es = io_size(dims->io_dtype), M = (size_t)dims->rows, K = (size_t)dims->cols, KB = (K + 127) / 128;
+    const void* io[] = {a->x, a->residual, a->sum};
+    for (const void* p : io)
+        if ((uintptr_t)p % es) return fail(SS_ERR_INVALID_ARG, "x, residual or sum not aligned to its element");
+    if (((uintptr_t)a->w & 3u) || ((uintptr_t)a->scale & 3u)) return fail(SS_ERR_INVALID_ARG, "w or scale not 4-byte aligned");
+    const Range ins[] = {{a->x, M * K * es, "x"}, {a->residual, M * K * es, "residual"}, {a->w, K * 4, "w"}};
+    const Range outs[] = {{a->q, M * K, "q"}, {a->scale, M * KB * 4, "scale"}};
+    const Range sum{a->sum, M * K * es, "sum"};
+    if ((s = check_overlaps(outs, 2, ins, 3)) != SS_OK) return s;
+    if ((s = check_overlaps(outs, 2, &sum, 1)) != SS_OK) return s;
+    for (const Range& r : ins)
+        if (overlap(sum, r) && !(a->sum == r.p && r.bytes == sum.bytes && r.p != (const void*)a->w))
+            return fail(SS_ERR_INVALID_ARG, "sum overlaps %s (only sum == x or sum == residual is allowed)", r.name);
+    selscan::LaunchQ8 p{};
+    p.bf16 = dims->io_dtype == SS_BF16;
+    p.vec = q8_vec(*dims, {a->x, a->residual, a->sum, a->w}, a->q);
+    p.x = a->x; p.res = a->residual; p.w = a->w; p.eps = dims->eps;
+    p.q = static_cast<uint8_t*>(a->q); p.scale = a->scale; p.sum = a->sum;
+    p.M = dims->rows; p.K = dims->cols;
+    p.stream = stream;
+    return launched(selscan::launch_q8(p));
+}
+
+ss_status ss_gemm_q8(const ss_gemm_q8_dims* dims, const ss_gemm_q8_args* a, void* stream) {
+    ss_status s = check_gemm_q8_dims(dims);
+    if (s != SS_OK) return s;
+    if (!a) return fail(SS_ERR_INVALID_ARG, "args is NULL");
+    if (!a->xq || !a->xs || !a->wq || !a->ws || !a->y) return fail(SS_ERR_INVALID_ARG, "xq, xs, wq, ws or y is NULL");
+    const void* al[] = {a->xq, a->wq, a->residual, a->y};
+    for (const void* p : al)
+        if ((uintptr_t)p & 15u) return fail(SS_ERR_INVALID_ARG, "xq, wq, residual and y must be 16-byte aligned");
+    if (((uintptr_t)a->xs & 3u) || ((uintptr_t)a->ws & 3u)) return fail(SS_ERR_INVALID_ARG, "xs or ws not 4-byte aligned");
+    const size_t M = (size_t)dims->m, N = (size_t)dims->n, K = (size_t)dims->k, KB = (K + 127) / 128;
+    const size_t yb = M * N * io_size(dims->y_dtype);
+    const Range ins[] = {{a->xq, M * K, "xq"}, {a->xs, M * KB * 4, "xs"}, {a->wq, N * K, "wq"},
+                         {a->ws, (N + 127) / 128 * KB * 4, "ws"}, {a->residual == a->y ? nullptr : a->residual, yb, "residual"}};
+    const Range y{a->y, yb, "y"};
+    if ((s = check_overlaps(&y, 1, ins, 5)) != SS_OK) return s;
+    selscan::LaunchGemmQ8 p{};
+    p.y_bf16 = dims->y_dtype == SS_BF16;
+    p.xq = static_cast<const uint8_t*>(a->xq); p.xs = a->xs;
+    p.wq = static_cast<const uint8_t*>(a->wq); p.ws = a->ws;
+    p.R = a->residual; p.Y[0] = a->y; p.Y[1] = nullptr;
+    p.split = dims->n; p.M = dims->m; p.N = dims->n; p.K = dims->k;
+    p.stream = stream;
+    return launched(selscan::launch_gemm_q8(p));
 }
 
 }  // extern "C"

@@ -34,4 +34,27 @@ struct LaunchGlr {
 };
 hipError_t launch_glr(const LaunchGlr& p);
 
+// Rounding to 8 bits, with (w given) or without the norm in front.
+constexpr int64_t kQ8WaveRows = 1024;    // rows from which a row has one wave, not a workgroup of four
+struct LaunchQ8 {
+    bool bf16, vec, square;
+    const void* x; const void* res; const float* w; float eps;
+    uint8_t* q; float* scale; void* sum;
+    int64_t M, K;
+    void* stream;
+};
+hipError_t launch_q8(const LaunchQ8& p);
+
+// Y[M, N] = (xq xs)(wq ws)^T (+ R). Y may lie in two matrices side by side: columns
+// [0, split) in Y[0] and the rest in Y[1] (split = N: one matrix).
+struct LaunchGemmQ8 {
+    bool y_bf16;
+    const uint8_t* xq; const float* xs; const uint8_t* wq; const float* ws;
+    const void* R; void* Y[2];
+    int64_t split, M, N, K;
+    void* stream;
+};
+constexpr int64_t kGemmQ8ThinRows = 256;   // rows of X up to which W goes straight to registers
+hipError_t launch_gemm_q8(const LaunchGemmQ8& p);
+
 }  // namespace selscan

@@ -1,0 +1,253 @@
+// Device code of the 8-bit rounding, alone (ss_quant_q8) and behind the residual's addition
+// and the RMS norm (ss_norm_q8).
+//
+//   s = x + residual;  n = s / sqrt(mean(s^2) + eps) * w
+//   per block: scale = max(max |n| / 448, 2^-126),  q = e4m3(n / scale)
+//
+// Both are bound by memory: a value is read once, kept in registers through the sums and
+// maxima it takes part in, and its byte is written once.
+#pragma once
+#include "ops_internal.h"
+#include "selscan_device.h"
+
+namespace selscan {
+
+constexpr float kQ8Max = 448.0f;             // largest finite e4m3 value
+constexpr float kQ8TinyScale = 0x1p-126f;    // smallest scale: its reciprocal is finite
+
+__device__ __forceinline__ float q8_scale(float top) { return __builtin_fmaxf(top / kQ8Max, kQ8TinyScale); }
+
+// four values times `inv` as four e4m3 bytes, each rounded to the nearest (ties to even)
+__device__ __forceinline__ uint32_t q8_pack(float a, float b, float c, float d, float inv) {
+    int v = __builtin_amdgcn_cvt_pk_fp8_f32(a * inv, b * inv, 0, false);
+    v = __builtin_amdgcn_cvt_pk_fp8_f32(c * inv, d * inv, v, true);
+    return (uint32_t)v;
+}
+
+typedef uint32_t q8_u4 __attribute__((ext_vector_type(4)));
+typedef uint32_t q8_u2 __attribute__((ext_vector_type(2)));
+typedef float q8_f4 __attribute__((ext_vector_type(4)));
+
+// Eight consecutive values of a row from column c on; zeros past the end. VEC: the row starts
+// on 16 bytes and K is a multiple of 8.
+template <typename T, bool VEC>
+__device__ __forceinline__ void ld8(const T* row, int64_t c, int64_t K, float* v) {
+    if constexpr (VEC) {
+        if (c >= K) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+        } else if constexpr (sizeof(T) == 2) {
+            const q8_u4 u = *reinterpret_cast<const q8_u4*>(row + c);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                v[2 * j] = __builtin_bit_cast(float, u[j] << 16);
+                v[2 * j + 1] = __builtin_bit_cast(float, u[j] & 0xffff0000u);
+            }
+        } else {
+            const q8_f4 a = *reinterpret_cast<const q8_f4*>(row + c), b = *reinterpret_cast<const q8_f4*>(row + c + 4);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) { v[j] = a[j]; v[4 + j] = b[j]; }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = c + j < K ? IO<T>::ld(row + c + j) : 0.0f;
+    }
+}
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void st8(T* row, int64_t c, int64_t K, const float* v) {
+    if constexpr (VEC && sizeof(T) == 2) {
+        typedef float f8 __attribute__((ext_vector_type(8)));
+        typedef __bf16 b8 __attribute__((ext_vector_type(8)));
+        f8 f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = v[j];
+        if (c < K) *reinterpret_cast<b8*>(row + c) = __builtin_convertvector(f, b8);
+    } else if constexpr (VEC) {
+        if (c < K) {
+            *reinterpret_cast<q8_f4*>(row + c) = q8_f4{v[0], v[1], v[2], v[3]};
+            *reinterpret_cast<q8_f4*>(row + c + 4) = q8_f4{v[4], v[5], v[6], v[7]};
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (c + j < K) IO<T>::st(row + c + j, v[j]);
+    }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void st8_q(uint8_t* row, int64_t c, int64_t K, const float* v, float inv) {
+    const q8_u2 u{q8_pack(v[0], v[1], v[2], v[3], inv), q8_pack(v[4], v[5], v[6], v[7], inv)};
+    if constexpr (VEC) {
+        if (c < K) *reinterpret_cast<q8_u2*>(row + c) = u;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (c + j < K) row[c + j] = (uint8_t)(u[j / 4] >> (8 * (j % 4)));
+    }
+}
+
+// largest |v| among the 16 lanes that hold one block of 128
+__device__ __forceinline__ float top16(const float* v) {
+    float t = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) t = __builtin_fmaxf(t, __builtin_fabsf(v[j]));
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) t = __builtin_fmaxf(t, __shfl_xor(t, o, 64));
+    return t;
+}
+
+struct Q8Args {
+    const void* x; const void* res; const float* w; uint8_t* q; float* scale; void* sum;
+    int64_t M, K, KB;
+    float eps;
+};
+
+// A row per G lanes (64 or 256), eight consecutive columns per lane and step, so that 16
+// neighbouring lanes hold one block. NV > 0: the row fits in NV steps and stays in registers.
+// NV = 0: longer rows are read again for each pass over them.
+template <typename T, bool VEC, bool NORM, bool RES, int G, int NV>
+__global__ void __launch_bounds__(256)
+k_q8_rows(const Q8Args p) {
+    constexpr int S = G * 8;                            // columns of one step
+    const int lane = threadIdx.x % G;
+    const int64_t row = (int64_t)blockIdx.x * (256 / G) + threadIdx.x / G;
+    if (G == 64 && row >= p.M) return;                  // whole waves; 256-lane groups have a grid of M
+    const T* x = static_cast<const T*>(p.x) + row * p.K;
+    const T* res = RES ? static_cast<const T*>(p.res) + row * p.K : nullptr;
+    const int64_t steps = NV ? NV : (p.K + S - 1) / S;
+
+    float v[NV ? NV : 1][8];
+    auto load = [&](int64_t k, float* o) {
+        const int64_t c = k * S + 8 * lane;
+        ld8<T, VEC>(x, c, p.K, o);
+        if constexpr (RES) {
+            float r[8];
+            ld8<T, VEC>(res, c, p.K, r);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] += r[j];
+        }
+    };
+    float rn = 1.0f;
+    if constexpr (NV > 0) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) load(k, v[k]);
+    }
+    if constexpr (NORM) {
+        float ss = 0.0f;
+        if constexpr (NV > 0) {
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) ss = __builtin_fmaf(v[k][j], v[k][j], ss);
+        } else {
+            for (int64_t k = 0; k < steps; ++k) {
+                load(k, v[0]);
+                float t = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) t = __builtin_fmaf(v[0][j], v[0][j], t);
+                ss += t;
+            }
+        }
+#pragma unroll
+        for (int o = 32; o >= 1; o >>= 1) ss += __shfl_xor(ss, o, 64);
+        if constexpr (G == 256) {
+            __shared__ float part[4];
+            if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = ss;
+            __syncthreads();
+            ss = (part[0] + part[1]) + (part[2] + part[3]);
+        }
+        rn = 1.0f / __builtin_sqrtf(ss / (float)p.K + p.eps);
+    }
+    auto finish = [&](int64_t k, float* o) {
+        const int64_t c = k * S + 8 * lane;
+        if constexpr (RES) st8<T, VEC>(static_cast<T*>(p.sum) + row * p.K, c, p.K, o);
+        if constexpr (NORM) {
+            float w[8];
+            ld8<float, VEC>(p.w, c, p.K, w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] = o[j] * rn * w[j];
+        }
+        const float scale = q8_scale(top16(o));
+        st8_q<VEC>(p.q + row * p.K, c, p.K, o, 1.0f / scale);
+        if (lane % 16 == 0 && c < p.K) p.scale[row * p.KB + c / 128] = scale;
+    };
+    if constexpr (NV > 0) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) finish(k, v[k]);
+    } else {
+        for (int64_t k = 0; k < steps; ++k) {
+            load(k, v[0]);
+            finish(k, v[0]);
+        }
+    }
+}
+
+// One 128 x 128 square per workgroup: 16 lanes across, 16 rows down, eight times.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256)
+k_q8_square(const Q8Args p) {
+    const int cx = threadIdx.x % 16 * 8, ry = threadIdx.x / 16;
+    const int64_t c = (int64_t)blockIdx.x * 128 + cx, r0 = (int64_t)blockIdx.y * 128 + ry;
+    float v[8][8], top = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const int64_t r = r0 + 16 * k;
+        if (r < p.M) {
+            ld8<T, VEC>(static_cast<const T*>(p.x) + r * p.K, c, p.K, v[k]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[k][j] = 0.0f;
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top = __builtin_fmaxf(top, __builtin_fabsf(v[k][j]));
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, o, 64));
+    __shared__ float part[4];
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = top;
+    __syncthreads();
+    top = __builtin_fmaxf(__builtin_fmaxf(part[0], part[1]), __builtin_fmaxf(part[2], part[3]));
+    const float scale = q8_scale(top), inv = 1.0f / scale;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        if (r0 + 16 * k < p.M) st8_q<VEC>(p.q + (r0 + 16 * k) * p.K, c, p.K, v[k], inv);
+    if (threadIdx.x == 0) p.scale[(int64_t)blockIdx.y * p.KB + blockIdx.x] = scale;
+}
+
+template <typename T, bool VEC, bool NORM, bool RES>
+hipError_t launch_q8_rows(const LaunchQ8& p, const Q8Args& a) {
+    hipStream_t st = static_cast<hipStream_t>(p.stream);
+    const bool wave = p.M >= kQ8WaveRows && p.K <= 64 * 8 * 8;
+    const int64_t steps = (p.K + (wave ? 512 : 2048) - 1) / (wave ? 512 : 2048);
+    const dim3 grid((unsigned)(wave ? (p.M + 3) / 4 : p.M));
+    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, a); };
+    if (wave) {
+        if (steps <= 1) go(k_q8_rows<T, VEC, NORM, RES, 64, 1>);
+        else if (steps <= 2) go(k_q8_rows<T, VEC, NORM, RES, 64, 2>);
+        else if (steps <= 5) go(k_q8_rows<T, VEC, NORM, RES, 64, 5>);
+        else go(k_q8_rows<T, VEC, NORM, RES, 64, 8>);
+    } else {
+        if (steps <= 1) go(k_q8_rows<T, VEC, NORM, RES, 256, 1>);
+        else if (steps <= 2) go(k_q8_rows<T, VEC, NORM, RES, 256, 2>);
+        else if (steps <= 4) go(k_q8_rows<T, VEC, NORM, RES, 256, 4>);
+        else go(k_q8_rows<T, VEC, NORM, RES, 256, 0>);
+    }
+    return hipGetLastError();
+}
+
+template <typename T, bool VEC>
+hipError_t launch_q8_t(const LaunchQ8& p) {
+    Q8Args a{p.x, p.res, p.w, p.q, p.scale, p.sum, p.M, p.K, (p.K + 127) / 128, p.eps};
+    if (p.square) {
+        hipLaunchKernelGGL((k_q8_square<T, VEC>), dim3((unsigned)a.KB, (unsigned)((p.M + 127) / 128)), dim3(256), 0,
+                           static_cast<hipStream_t>(p.stream), a);
+        return hipGetLastError();
+    }
+    if (!p.w) return launch_q8_rows<T, VEC, false, false>(p, a);
+    return p.res ? launch_q8_rows<T, VEC, true, true>(p, a) : launch_q8_rows<T, VEC, true, false>(p, a);
+}
+
+}  // namespace selscan

@@ -17,10 +17,12 @@ import torch
 from . import SS_BF16, SS_F32, SelscanError, lib
 
 GLR_CKPT = 64    # SS_GLR_CKPT
+Q8_BLOCK = 128   # columns that share a scale
 
 _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
 _F32 = torch.float32
+_Q8 = torch.float8_e4m3fn
 
 
 class ss_glr_dims(ctypes.Structure):
@@ -40,6 +42,23 @@ class ss_glr_grads(ctypes.Structure):
     _fields_ = [(n, _vp) for n in ("dy", "dstate_final", "dx", "dr", "di", "dA", "dstate_init")]
 
 
+class ss_q8_dims(ctypes.Structure):
+    _fields_ = [("rows", _i64), ("cols", _i64), ("io_dtype", ctypes.c_int32), ("square", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class ss_norm_q8_args(ctypes.Structure):
+    _fields_ = [(n, _vp) for n in ("x", "residual", "w", "q", "scale", "sum")]
+
+
+class ss_gemm_q8_dims(ctypes.Structure):
+    _fields_ = [("m", _i64), ("n", _i64), ("k", _i64), ("y_dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class ss_gemm_q8_args(ctypes.Structure):
+    _fields_ = [(n, _vp) for n in ("xq", "xs", "wq", "ws", "residual", "y")]
+
+
 def _declare():
     P = ctypes.POINTER
     lib.ss_glr_workspace_bytes.argtypes = [P(ss_glr_dims), ctypes.c_int]
@@ -47,7 +66,10 @@ def _declare():
     lib.ss_glr_fwd.argtypes = [P(ss_glr_dims), P(ss_glr_args), _vp, ctypes.c_size_t, _vp]
     lib.ss_glr_step.argtypes = [P(ss_glr_dims), P(ss_glr_args), _vp]
     lib.ss_glr_bwd.argtypes = [P(ss_glr_dims), P(ss_glr_args), P(ss_glr_grads), _vp, ctypes.c_size_t, _vp]
-    for name in ("ss_glr_fwd", "ss_glr_step", "ss_glr_bwd"):
+    lib.ss_quant_q8.argtypes = [P(ss_q8_dims), _vp, _vp, _vp, _vp]
+    lib.ss_norm_q8.argtypes = [P(ss_q8_dims), P(ss_norm_q8_args), _vp]
+    lib.ss_gemm_q8.argtypes = [P(ss_gemm_q8_dims), P(ss_gemm_q8_args), _vp]
+    for name in ("ss_glr_fwd", "ss_glr_step", "ss_glr_bwd", "ss_quant_q8", "ss_norm_q8", "ss_gemm_q8"):
         getattr(lib, name).restype = ctypes.c_int
 
 
@@ -235,5 +257,92 @@ def ss_glr_bwd(x: torch.Tensor, r: torch.Tensor, i: torch.Tensor, A: torch.Tenso
     return out
 
 
+# ---------------------------------------------------------------------------
+# 8-bit floating point with block scales
+
+def _rows(x: torch.Tensor, name: str) -> tuple:
+    """(rows, columns) of a contiguous tensor whose last dimension is the row."""
+    if not x.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if x.dim() < 1 or not x.is_contiguous():
+        raise ValueError(f"{name} must be contiguous, with at least one dimension")
+    K = x.shape[-1]
+    return (x.numel() // K if K else 0), K
+
+
+def ss_quant_q8(x: torch.Tensor, *, square: bool = False, q: Optional[torch.Tensor] = None,
+                scale: Optional[torch.Tensor] = None, stream=None) -> tuple:
+    """Round x [..., K] (float32 or bfloat16, contiguous) to 8-bit floating point. Returns (q,
+    scale): q of x's shape in torch.float8_e4m3fn and float32 scales of blocks of 128 columns,
+    [..., ceil(K/128)]; with square (x [N,K]) of 128 x 128, [ceil(N/128), ceil(K/128)]. x stands
+    for scale * q. q and scale are allocated where not given. Asynchronous."""
+    M, K = _rows(x, "x")
+    KB, dev = -(-K // Q8_BLOCK), x.device
+    if square and x.dim() != 2:
+        raise ValueError("a square rounding takes x [N, K]")
+    sshape = (-(-M // Q8_BLOCK), KB) if square else x.shape[:-1] + (KB,)
+    with _On(dev, stream) as handle:
+        if q is None:
+            q = torch.empty(x.shape, dtype=_Q8, device=dev)
+        if scale is None:
+            scale = torch.empty(sshape, dtype=_F32, device=dev)
+        dims = ss_q8_dims(M, K, _io(x, "x"), int(bool(square)), 0.0, 0)
+        _check(lib.ss_quant_q8(ctypes.byref(dims), x.data_ptr(), _same(q, x.shape, _Q8, dev, "q"),
+                               _same(scale, sshape, _F32, dev, "scale"), handle))
+    return q, scale
+
+
+def ss_norm_q8(x: torch.Tensor, w: torch.Tensor, *, residual: Optional[torch.Tensor] = None, eps: float = 1e-5,
+               q: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None,
+               sum_out: Optional[torch.Tensor] = None, stream=None) -> tuple:
+    """RMS norm of s = x + residual (s = x without one), times w, rounded to 8-bit floating
+    point in blocks of 128 columns: x, residual [..., K] (float32 or bfloat16, contiguous), w [K]
+    float32. Returns (q, scale, s): q and scale as from ss_quant_q8, s in x's dtype (None
+    without a residual). sum_out receives s; it may be x or residual itself. Asynchronous."""
+    M, K = _rows(x, "x")
+    shape, dt, dev = x.shape, x.dtype, x.device
+    sshape = shape[:-1] + (-(-K // Q8_BLOCK),)
+    if residual is None and sum_out is not None:
+        raise ValueError("sum_out given without a residual")
+    with _On(dev, stream) as handle:
+        if q is None:
+            q = torch.empty(shape, dtype=_Q8, device=dev)
+        if scale is None:
+            scale = torch.empty(sshape, dtype=_F32, device=dev)
+        if residual is not None and sum_out is None:
+            sum_out = torch.empty(shape, dtype=dt, device=dev)
+        dims = ss_q8_dims(M, K, _io(x, "x"), 0, eps, 0)
+        args = ss_norm_q8_args(x.data_ptr(), _opt(residual, shape, dt, dev, "residual"), _same(w, (K,), _F32, dev, "w"),
+                               _same(q, shape, _Q8, dev, "q"), _same(scale, sshape, _F32, dev, "scale"),
+                               _opt(sum_out, shape, dt, dev, "sum_out"))
+        _check(lib.ss_norm_q8(ctypes.byref(dims), ctypes.byref(args), handle))
+    return q, scale, sum_out
+
+
+def ss_gemm_q8(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor, *,
+               residual: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+               out_dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+    """y = X W^T (+ residual) of 8-bit matrices: xq [..., K] and xs [..., ceil(K/128)] as from
+    ss_quant_q8 or ss_norm_q8, wq [N,K] and ws [ceil(N/128), ceil(K/128)] as from
+    ss_quant_q8(square=True); K a multiple of 16. Returns y [..., N] in out_dtype (float32 or
+    bfloat16; out's own where given); residual has y's shape and dtype and may be out itself.
+    Asynchronous."""
+    M, K = _rows(xq, "xq")
+    if wq.dim() != 2:
+        raise ValueError("wq must be [N, K]")
+    N, dev, lead, KB = wq.shape[0], xq.device, xq.shape[:-1], -(-K // Q8_BLOCK)
+    with _On(dev, stream) as handle:
+        if out is None:
+            out = torch.empty(lead + (N,), dtype=out_dtype, device=dev)
+        yshape, dt = lead + (N,), out.dtype
+        dims = ss_gemm_q8_dims(M, N, K, _io(out, "out"), 0)
+        args = ss_gemm_q8_args(_same(xq, xq.shape, _Q8, dev, "xq"), _same(xs, lead + (KB,), _F32, dev, "xs"),
+                               _same(wq, (N, K), _Q8, dev, "wq"), _same(ws, (-(-N // Q8_BLOCK), KB), _F32, dev, "ws"),
+                               _opt(residual, yshape, dt, dev, "residual"), _same(out, yshape, dt, dev, "out"))
+        _check(lib.ss_gemm_q8(ctypes.byref(dims), ctypes.byref(args), handle))
+    return out
+
+
 __all__ = ["GLR_CKPT", "ss_glr_dims", "ss_view", "ss_glr_args", "ss_glr_grads", "glr_ckpt_shape",
-           "ss_glr_workspace_bytes", "ss_glr_fwd", "ss_glr_step", "ss_glr_bwd"]
+           "ss_glr_workspace_bytes", "ss_glr_fwd", "ss_glr_step", "ss_glr_bwd", "Q8_BLOCK", "ss_q8_dims",
+           "ss_norm_q8_args", "ss_gemm_q8_dims", "ss_gemm_q8_args", "ss_quant_q8", "ss_norm_q8", "ss_gemm_q8"]

@@ -25,7 +25,7 @@ def last():
 def test_header_symbols_are_exported():
     text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
     names = set(re.findall(r"^(?:size_t|ss_status|int)\s+(ss_[a-z0-9_]+)\s*\(", text, flags=re.M))
-    assert {"ss_glr_fwd", "ss_glr_bwd", "ss_glr_step", "ss_glr_workspace_bytes"} <= names
+    assert {"ss_glr_fwd", "ss_glr_bwd", "ss_glr_step", "ss_glr_workspace_bytes", "ss_quant_q8", "ss_norm_q8", "ss_gemm_q8"} <= names
     out = subprocess.run(["nm", "-D", "--defined-only", ss.LIB_PATH], capture_output=True, text=True, check=True).stdout
     exported = {line.split()[-1] for line in out.splitlines() if line.strip()}
     assert names <= exported
@@ -144,3 +144,68 @@ def test_binding_refuses_host_tensors():
         ss.ss_glr_fwd(t[0], t[0], t[0], torch.zeros(8))
     with pytest.raises(TypeError):
         ss.ss_glr_fwd(t.half(), t, t, torch.zeros(8))
+
+
+# ---------------------------------------------------------------------------
+# 8-bit floating point with block scales
+
+def qdims(**kw):
+    d = dict(rows=70, cols=300, io_dtype=ss.SS_BF16, square=0, eps=1e-5, reserved=0)
+    d.update(kw)
+    return ss.ss_q8_dims(*d.values())
+
+
+def quant(dims=None, x=BASE, q=BASE + GAP, scale=BASE + 2 * GAP):
+    return ss.lib.ss_quant_q8(ctypes.byref(dims or qdims()), x, q, scale, None)
+
+
+def norm(dims=None, **kw):
+    a = dict(x=BASE, residual=BASE + GAP, w=BASE + 2 * GAP, q=BASE + 3 * GAP, scale=BASE + 4 * GAP, sum=BASE + 5 * GAP)
+    a.update(kw)
+    return ss.lib.ss_norm_q8(ctypes.byref(dims or qdims()), ctypes.byref(ss.ss_norm_q8_args(*a.values())), None)
+
+
+def test_rounding_refusals():
+    for kw, status in [(dict(rows=0), 1), (dict(cols=0), 1), (dict(cols=1 << 31), 1), (dict(rows=1 << 31), 1),
+                       (dict(io_dtype=3), 2), (dict(square=2), 1), (dict(reserved=1), 1),
+                       (dict(rows=65536 * 128, square=1), 1)]:
+        assert quant(qdims(**kw)) == status, kw
+    for kw in (dict(x=None), dict(q=None), dict(scale=None), dict(x=BASE + 1), dict(scale=BASE + 2 * GAP + 2),
+               dict(q=BASE + 16), dict(scale=BASE + GAP + 128)):
+        assert quant(**kw) == 1, kw
+    assert ss.lib.ss_quant_q8(None, BASE, BASE + GAP, BASE + 2 * GAP, None) == 1
+
+
+def test_norm_refusals():
+    for kw in (dict(eps=0.0), dict(eps=float("nan")), dict(square=1), dict(rows=0), dict(reserved=3)):
+        assert norm(qdims(**kw)) == 1, kw
+    for kw in (dict(x=None), dict(w=None), dict(q=None), dict(scale=None), dict(sum=None), dict(residual=None),
+               dict(x=BASE + 1), dict(w=BASE + 2 * GAP + 2), dict(q=BASE), dict(scale=BASE + 3 * GAP), dict(sum=BASE + 3 * GAP),
+               dict(sum=BASE + 64), dict(sum=BASE + GAP + 64), dict(sum=BASE + 2 * GAP)):
+        assert norm(**kw) == 1, kw
+    assert ss.lib.ss_norm_q8(ctypes.byref(qdims()), None, None) == 1
+
+
+def test_product_refusals():
+    def call(dims=None, **kw):
+        d = dict(m=70, n=130, k=272, y_dtype=ss.SS_BF16, reserved=0)
+        d.update(dims or {})
+        a = dict(xq=BASE, xs=BASE + GAP, wq=BASE + 2 * GAP, ws=BASE + 3 * GAP, residual=None, y=BASE + 4 * GAP)
+        a.update(kw)
+        return ss.lib.ss_gemm_q8(ctypes.byref(ss.ss_gemm_q8_dims(*d.values())), ctypes.byref(ss.ss_gemm_q8_args(*a.values())), None)
+
+    for d, status in [(dict(m=0), 1), (dict(n=0), 1), (dict(k=0), 1), (dict(k=264), 2), (dict(k=1 << 31), 1),
+                      (dict(m=1 << 31), 1), (dict(y_dtype=2), 2), (dict(reserved=1), 1), (dict(m=(1 << 31) - 1, n=(1 << 31) - 1), 1)]:
+        assert call(d) == status, d
+    for kw in (dict(xq=None), dict(xs=None), dict(wq=None), dict(ws=None), dict(y=None), dict(xq=BASE + 8), dict(wq=BASE + 2 * GAP + 4),
+               dict(y=BASE + 4 * GAP + 8), dict(residual=BASE + 5 * GAP + 2), dict(xs=BASE + GAP + 2), dict(y=BASE),
+               dict(y=BASE + 2 * GAP + 32), dict(y=BASE + 3 * GAP), dict(residual=BASE + 4 * GAP + 16)):
+        assert call(**kw) == 1, kw
+
+
+def test_binding_refuses_host_operands():
+    t = torch.zeros(4, 128)
+    for call in (lambda: ss.ss_quant_q8(t), lambda: ss.ss_norm_q8(t, torch.ones(128)),
+                 lambda: ss.ss_gemm_q8(t.to(torch.float8_e4m3fn), t, t.to(torch.float8_e4m3fn), t)):
+        with pytest.raises(ValueError):
+            call()
