@@ -9,12 +9,14 @@ the outputs.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import struct
 from typing import Optional
 
 import torch
 
-from . import SS_BF16, SS_F32, SelscanError, lib
+from . import LIB_PATH, SS_BF16, SS_F32, SelscanError, lib
 
 GLR_CKPT = 64    # SS_GLR_CKPT
 Q8_BLOCK = 128   # columns that share a scale
@@ -76,6 +78,37 @@ def _declare():
 _declare()
 
 
+# What a call costs on the host is time a decode step waits for, so the calls below build
+# their argument structs with struct.pack (the layouts above, "P" a pointer, 0 for NULL) and
+# pass the bytes: about a third of the time of filling ctypes structures. The C calls copy
+# what they need before they return.
+_raw = ctypes.CDLL(LIB_PATH)
+_bytes, _size = ctypes.c_char_p, ctypes.c_size_t
+for _name, _args in (("ss_glr_fwd", [_bytes, _bytes, _vp, _size, _vp]), ("ss_glr_step", [_bytes, _bytes, _vp]),
+                     ("ss_glr_bwd", [_bytes, _bytes, _bytes, _vp, _size, _vp]), ("ss_quant_q8", [_bytes, _vp, _vp, _vp, _vp]),
+                     ("ss_norm_q8", [_bytes, _bytes, _vp]), ("ss_gemm_q8", [_bytes, _bytes, _vp])):
+    getattr(_raw, _name).argtypes, getattr(_raw, _name).restype = _args, ctypes.c_int
+_raw.ss_glr_workspace_bytes.argtypes, _raw.ss_glr_workspace_bytes.restype = [_bytes, ctypes.c_int], _size
+
+
+def _packer(fmt: str, cls):
+    s = struct.Struct(fmt)
+    assert s.size == ctypes.sizeof(cls), cls
+    return s.pack
+
+
+_pack_glr_dims = _packer("qqqii", ss_glr_dims)
+_pack_glr_args = _packer("PqqPqqPqqPPPPP", ss_glr_args)
+_pack_glr_grads = _packer("PPPPPPP", ss_glr_grads)
+_pack_q8_dims = _packer("qqiifi", ss_q8_dims)
+_pack_norm_args = _packer("PPPPPP", ss_norm_q8_args)
+_pack_gemm_dims = _packer("qqqii", ss_gemm_q8_dims)
+_pack_gemm_args = _packer("PPPPPP", ss_gemm_q8_args)
+
+_stream_of = torch._C._cuda_getCurrentRawStream
+_current = torch._C._cuda_getDevice
+
+
 def _check(status: int):
     if status != 0:
         raise SelscanError(status, lib.ss_last_error().decode())
@@ -89,102 +122,89 @@ def _io(t: torch.Tensor, name: str) -> int:
     raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
 
 
-def _same(t: torch.Tensor, shape, dtype, device, name: str) -> int:
-    """The data pointer of a contiguous tensor of this shape, dtype and device."""
-    if t.device != device or not t.is_cuda:
-        raise ValueError(f"{name} must be on {device}, a GPU" if t.is_cuda else f"{name} must be a device tensor")
+def _gpu(t: torch.Tensor, name: str) -> int:
+    """The index of the GPU a tensor is on."""
+    idx = t.get_device()
+    if idx < 0 or not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor, got {t.device}")
+    return idx
+
+
+def _elsewhere(idx: int, stream) -> bool:
+    """Whether a call has to move to another device or to an explicit stream first."""
+    return stream is not None or idx != _current()
+
+
+@contextlib.contextmanager
+def _placed(idx: int, stream):
+    if stream is not None and stream.device.index != idx:
+        raise ValueError(f"stream is on {stream.device}, the tensors are on cuda:{idx}")
+    with torch.cuda.device(idx):
+        if stream is None:
+            yield
+        else:
+            with torch.cuda.stream(stream):
+                yield
+
+
+def _wrong(t: torch.Tensor, shape, dtype, idx: int, name: str):
+    if t.get_device() != idx:
+        raise ValueError(f"{name} must be on cuda:{idx}, got {t.device}")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}, contiguous")
+
+
+def _same(t: torch.Tensor, shape, dtype, idx: int, name: str) -> int:
+    """The data pointer of a contiguous tensor of this shape, dtype and device."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != idx or not t.is_contiguous():
+        _wrong(t, shape, dtype, idx, name)
     return t.data_ptr()
 
 
-def _opt(t: Optional[torch.Tensor], shape, dtype, device, name: str) -> Optional[int]:
-    return None if t is None else _same(t, shape, dtype, device, name)
+def _opt(t: Optional[torch.Tensor], shape, dtype, idx: int, name: str) -> int:
+    return 0 if t is None else _same(t, shape, dtype, idx, name)
 
 
-class _On:
-    """The device and stream of a call: the device is made current where it is not, outputs
-    are allocated on an explicit stream."""
-    __slots__ = ("handle", "_ctx")
-
-    def __init__(self, device: torch.device, stream):
-        ctx = []
-        if device.type != "cuda":
-            raise ValueError(f"the tensors must be on a GPU, got {device}")
-        if stream is not None:
-            if stream.device != device:
-                raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
-            ctx.append(torch.cuda.stream(stream))
-            self.handle = stream.cuda_stream or None
-        else:
-            self.handle = torch.cuda.current_stream(device).cuda_stream or None
-            if device.index != torch.cuda.current_device():
-                ctx.append(torch.cuda.device(device))
-        self._ctx = ctx
-
-    def __enter__(self):
-        for c in self._ctx:
-            c.__enter__()
-        return self.handle
-
-    def __exit__(self, *e):
-        for c in reversed(self._ctx):
-            c.__exit__(*e)
-
-
-def _workspace(given: Optional[torch.Tensor], need: int, device) -> Optional[torch.Tensor]:
+def _workspace(given: Optional[torch.Tensor], need: int, like: torch.Tensor):
+    """(tensor to keep alive, pointer, bytes)."""
     if given is None:
-        return torch.empty(need, dtype=torch.uint8, device=device) if need else None
-    if not given.is_cuda or given.device != device:
-        raise ValueError(f"workspace must be on {device}")
-    if not given.is_contiguous() or given.numel() * given.element_size() < need:
+        if not need:
+            return None, None, 0
+        given = like.new_empty(need, dtype=torch.uint8)
+    elif given.get_device() != like.get_device():
+        raise ValueError(f"workspace must be on {like.device}")
+    elif not given.is_contiguous() or given.numel() * given.element_size() < need:
         raise ValueError(f"workspace must be contiguous, of at least {need} bytes")
-    return given
-
-
-def _ws_args(ws: Optional[torch.Tensor]):
-    return (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
+    return given, given.data_ptr(), given.numel() * given.element_size()
 
 
 # ---------------------------------------------------------------------------
 # gated linear recurrence
 
-def _view(t: torch.Tensor, shape, dtype, device, name: str) -> ss_view:
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a device tensor")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+def _view(t: torch.Tensor, shape, dtype, idx: int, name: str) -> tuple:
+    """(pointer, batch stride, token stride) of a view whose channels are contiguous."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != idx:
+        _wrong(t, shape, dtype, idx, name)
     st = t.stride()
     if st[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name}: channels must be contiguous (last stride 1)")
-    return ss_view(t.data_ptr(), st[0], st[1] if len(st) == 3 else 0)
+    return t.data_ptr(), st[0], st[1]
 
 
-def _glr_args(x, r, i, A, reset, y, state, ckpt, dims: ss_glr_dims):
-    shape, dt, dev = x.shape, x.dtype, x.device
-    B, D = shape[0], shape[-1]
-    lead = shape[:-1]
-    if reset is not None and reset.dtype is torch.bool:
-        reset = reset.view(torch.uint8)
-    return ss_glr_args(
-        _view(x, shape, dt, dev, "x"), _view(r, shape, dt, dev, "r"), _view(i, shape, dt, dev, "i"),
-        _same(A, (D,), _F32, dev, "A"), _opt(reset, lead, torch.uint8, dev, "reset"),
-        _opt(y, shape, dt, dev, "y"), _opt(state, (B, D), _F32, dev, "state"),
-        _opt(ckpt, glr_ckpt_shape(B, shape[1], D), _F32, dev, "ckpt") if len(shape) == 3 else None)
+def _glr_reset(reset: Optional[torch.Tensor], shape, idx: int) -> int:
+    if reset is None:
+        return 0
+    return _same(reset, shape, torch.bool if reset.dtype is torch.bool else torch.uint8, idx, "reset")
 
 
-def _glr_dims(x: torch.Tensor, dim: int) -> ss_glr_dims:
-    if x.dim() != dim:
-        raise ValueError("x must be [batch, seqlen, d]" if dim == 3 else "x must be [streams, d]")
-    return ss_glr_dims(x.shape[0], x.shape[1] if dim == 3 else 1, x.shape[-1], _io(x, "x"), 0)
+def _glr_pack(x, r, i, A, reset, y, state, ckpt, shape, idx) -> bytes:
+    dt, B, D = x.dtype, shape[0], shape[-1]
+    return _pack_glr_args(
+        *_view(x, shape, dt, idx, "x"), *_view(r, shape, dt, idx, "r"), *_view(i, shape, dt, idx, "i"),
+        _same(A, (D,), _F32, idx, "A"), _glr_reset(reset, shape[:-1], idx), _opt(y, shape, dt, idx, "y"),
+        _opt(state, (B, D), _F32, idx, "state"),
+        0 if ckpt is None else _same(ckpt, glr_ckpt_shape(B, shape[1], D), _F32, idx, "ckpt"))
 
 
 def glr_ckpt_shape(batch: int, seqlen: int, d: int) -> tuple:
@@ -209,14 +229,19 @@ def ss_glr_fwd(x: torch.Tensor, r: torch.Tensor, i: torch.Tensor, A: torch.Tenso
     (zero initial state otherwise); reset [B,L] uint8 or bool: a_t = 0 at its nonzero tokens,
     where a new document starts; ckpt: float32 tensor of glr_ckpt_shape that receives the
     checkpoints ss_glr_bwd needs. Returns y [B,L,D] in the I/O dtype. Asynchronous."""
-    dims = _glr_dims(x, 3)
-    with _On(x.device, stream) as handle:
-        if y is None:
-            y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        args = _glr_args(x, r, i, A, reset, y, state, ckpt, dims)
-        dref = ctypes.byref(dims)
-        ws, ws_bytes = _ws_args(_workspace(workspace, lib.ss_glr_workspace_bytes(dref, 0), x.device))
-        _check(lib.ss_glr_fwd(dref, ctypes.byref(args), ws, ws_bytes, handle))
+    idx = _gpu(x, "x")
+    if _elsewhere(idx, stream):
+        with _placed(idx, stream):
+            return ss_glr_fwd(x, r, i, A, state=state, reset=reset, ckpt=ckpt, y=y, workspace=workspace)
+    if x.dim() != 3:
+        raise ValueError("x must be [batch, seqlen, d]")
+    B, L, D = shape = x.shape
+    dims = _pack_glr_dims(B, L, D, _io(x, "x"), 0)
+    if y is None:
+        y = x.new_empty(shape)
+    args = _glr_pack(x, r, i, A, reset, y, state, ckpt, shape, idx)
+    keep, ws, ws_bytes = _workspace(workspace, _raw.ss_glr_workspace_bytes(dims, 0), x)
+    _check(_raw.ss_glr_fwd(dims, args, ws, ws_bytes, _stream_of(idx)))
     return y
 
 
@@ -224,12 +249,19 @@ def ss_glr_step(x: torch.Tensor, r: torch.Tensor, i: torch.Tensor, A: torch.Tens
                 reset: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """One token of each stream: x, r, i [S,D] (rows at any stride); state [S,D] float32,
     updated in place; reset [S]. Returns y [S,D]."""
-    dims = _glr_dims(x, 2)
-    with _On(x.device, stream) as handle:
-        if y is None:
-            y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        args = _glr_args(x, r, i, A, reset, y, state, None, dims)
-        _check(lib.ss_glr_step(ctypes.byref(dims), ctypes.byref(args), handle))
+    idx = _gpu(x, "x")
+    if _elsewhere(idx, stream):
+        with _placed(idx, stream):
+            return ss_glr_step(x, r, i, A, state, reset=reset, y=y)
+    if x.dim() != 2:
+        raise ValueError("x must be [streams, d]")
+    shape = x.shape
+    if y is None:
+        y = x.new_empty(shape)
+    if state is None:
+        raise ValueError("state is required")
+    args = _glr_pack(x, r, i, A, reset, y, state, None, shape, idx)
+    _check(_raw.ss_glr_step(_pack_glr_dims(shape[0], 1, shape[1], _io(x, "x"), 0), args, _stream_of(idx)))
     return y
 
 
@@ -241,20 +273,25 @@ def ss_glr_bwd(x: torch.Tensor, r: torch.Tensor, i: torch.Tensor, A: torch.Tenso
     is the initial state). dy [B,L,D] in the I/O dtype, dstate_final [B,D] float32 the
     gradient of the returned state. Returns a dict of new tensors: dx, dr, di (I/O dtype), dA
     [D] and dstate_init [B,D] (float32). Asynchronous."""
-    dims = _glr_dims(x, 3)
-    B, _, D = shape = x.shape
-    dt, dev = x.dtype, x.device
-    with _On(dev, stream) as handle:
-        out = {k: torch.empty(shape, dtype=dt, device=dev) for k in ("dx", "dr", "di")}
-        out["dA"] = torch.empty(D, dtype=_F32, device=dev)
-        out["dstate_init"] = torch.empty(B, D, dtype=_F32, device=dev)
-        args = _glr_args(x, r, i, A, reset, None, None, ckpt, dims)
-        g = ss_glr_grads(_same(dy, shape, dt, dev, "dy"), _opt(dstate_final, (B, D), _F32, dev, "dstate_final"),
-                         *(out[k].data_ptr() for k in ("dx", "dr", "di", "dA", "dstate_init")))
-        dref = ctypes.byref(dims)
-        ws, ws_bytes = _ws_args(_workspace(workspace, lib.ss_glr_workspace_bytes(dref, 1), dev))
-        _check(lib.ss_glr_bwd(dref, ctypes.byref(args), ctypes.byref(g), ws, ws_bytes, handle))
-    return out
+    idx = _gpu(x, "x")
+    if _elsewhere(idx, stream):
+        with _placed(idx, stream):
+            return ss_glr_bwd(x, r, i, A, ckpt, dy, reset=reset, dstate_final=dstate_final, workspace=workspace)
+    if x.dim() != 3:
+        raise ValueError("x must be [batch, seqlen, d]")
+    if ckpt is None:
+        raise ValueError("ckpt is required")
+    B, L, D = shape = x.shape
+    dt = x.dtype
+    dims = _pack_glr_dims(B, L, D, _io(x, "x"), 0)
+    args = _glr_pack(x, r, i, A, reset, None, None, ckpt, shape, idx)
+    dx, dr, di = x.new_empty(shape), x.new_empty(shape), x.new_empty(shape)
+    dA, dh = A.new_empty(D), A.new_empty((B, D))
+    grads = _pack_glr_grads(_same(dy, shape, dt, idx, "dy"), _opt(dstate_final, (B, D), _F32, idx, "dstate_final"),
+                            dx.data_ptr(), dr.data_ptr(), di.data_ptr(), dA.data_ptr(), dh.data_ptr())
+    keep, ws, ws_bytes = _workspace(workspace, _raw.ss_glr_workspace_bytes(dims, 1), x)
+    _check(_raw.ss_glr_bwd(dims, args, grads, ws, ws_bytes, _stream_of(idx)))
+    return {"dx": dx, "dr": dr, "di": di, "dA": dA, "dstate_init": dh}
 
 
 # ---------------------------------------------------------------------------
@@ -262,8 +299,6 @@ def ss_glr_bwd(x: torch.Tensor, r: torch.Tensor, i: torch.Tensor, A: torch.Tenso
 
 def _rows(x: torch.Tensor, name: str) -> tuple:
     """(rows, columns) of a contiguous tensor whose last dimension is the row."""
-    if not x.is_cuda:
-        raise ValueError(f"{name} must be a device tensor")
     if x.dim() < 1 or not x.is_contiguous():
         raise ValueError(f"{name} must be contiguous, with at least one dimension")
     K = x.shape[-1]
@@ -276,19 +311,22 @@ def ss_quant_q8(x: torch.Tensor, *, square: bool = False, q: Optional[torch.Tens
     scale): q of x's shape in torch.float8_e4m3fn and float32 scales of blocks of 128 columns,
     [..., ceil(K/128)]; with square (x [N,K]) of 128 x 128, [ceil(N/128), ceil(K/128)]. x stands
     for scale * q. q and scale are allocated where not given. Asynchronous."""
+    idx = _gpu(x, "x")
+    if _elsewhere(idx, stream):
+        with _placed(idx, stream):
+            return ss_quant_q8(x, square=square, q=q, scale=scale)
     M, K = _rows(x, "x")
-    KB, dev = -(-K // Q8_BLOCK), x.device
-    if square and x.dim() != 2:
+    shape, KB = x.shape, -(-K // Q8_BLOCK)
+    if square and len(shape) != 2:
         raise ValueError("a square rounding takes x [N, K]")
-    sshape = (-(-M // Q8_BLOCK), KB) if square else x.shape[:-1] + (KB,)
-    with _On(dev, stream) as handle:
-        if q is None:
-            q = torch.empty(x.shape, dtype=_Q8, device=dev)
-        if scale is None:
-            scale = torch.empty(sshape, dtype=_F32, device=dev)
-        dims = ss_q8_dims(M, K, _io(x, "x"), int(bool(square)), 0.0, 0)
-        _check(lib.ss_quant_q8(ctypes.byref(dims), x.data_ptr(), _same(q, x.shape, _Q8, dev, "q"),
-                               _same(scale, sshape, _F32, dev, "scale"), handle))
+    sshape = (-(-M // Q8_BLOCK), KB) if square else shape[:-1] + (KB,)
+    if q is None:
+        q = x.new_empty(shape, dtype=_Q8)
+    if scale is None:
+        scale = x.new_empty(sshape, dtype=_F32)
+    dims = _pack_q8_dims(M, K, _io(x, "x"), 1 if square else 0, 0.0, 0)
+    _check(_raw.ss_quant_q8(dims, x.data_ptr(), _same(q, shape, _Q8, idx, "q"), _same(scale, sshape, _F32, idx, "scale"),
+                            _stream_of(idx)))
     return q, scale
 
 
@@ -299,23 +337,26 @@ def ss_norm_q8(x: torch.Tensor, w: torch.Tensor, *, residual: Optional[torch.Ten
     point in blocks of 128 columns: x, residual [..., K] (float32 or bfloat16, contiguous), w [K]
     float32. Returns (q, scale, s): q and scale as from ss_quant_q8, s in x's dtype (None
     without a residual). sum_out receives s; it may be x or residual itself. Asynchronous."""
+    idx = _gpu(x, "x")
+    if _elsewhere(idx, stream):
+        with _placed(idx, stream):
+            return ss_norm_q8(x, w, residual=residual, eps=eps, q=q, scale=scale, sum_out=sum_out)
     M, K = _rows(x, "x")
-    shape, dt, dev = x.shape, x.dtype, x.device
+    shape, dt = x.shape, x.dtype
     sshape = shape[:-1] + (-(-K // Q8_BLOCK),)
-    if residual is None and sum_out is not None:
-        raise ValueError("sum_out given without a residual")
-    with _On(dev, stream) as handle:
-        if q is None:
-            q = torch.empty(shape, dtype=_Q8, device=dev)
-        if scale is None:
-            scale = torch.empty(sshape, dtype=_F32, device=dev)
-        if residual is not None and sum_out is None:
-            sum_out = torch.empty(shape, dtype=dt, device=dev)
-        dims = ss_q8_dims(M, K, _io(x, "x"), 0, eps, 0)
-        args = ss_norm_q8_args(x.data_ptr(), _opt(residual, shape, dt, dev, "residual"), _same(w, (K,), _F32, dev, "w"),
-                               _same(q, shape, _Q8, dev, "q"), _same(scale, sshape, _F32, dev, "scale"),
-                               _opt(sum_out, shape, dt, dev, "sum_out"))
-        _check(lib.ss_norm_q8(ctypes.byref(dims), ctypes.byref(args), handle))
+    if q is None:
+        q = x.new_empty(shape, dtype=_Q8)
+    if scale is None:
+        scale = x.new_empty(sshape, dtype=_F32)
+    if residual is None:
+        if sum_out is not None:
+            raise ValueError("sum_out given without a residual")
+    elif sum_out is None:
+        sum_out = x.new_empty(shape)
+    args = _pack_norm_args(x.data_ptr(), _opt(residual, shape, dt, idx, "residual"), _same(w, (K,), _F32, idx, "w"),
+                           _same(q, shape, _Q8, idx, "q"), _same(scale, sshape, _F32, idx, "scale"),
+                           _opt(sum_out, shape, dt, idx, "sum_out"))
+    _check(_raw.ss_norm_q8(_pack_q8_dims(M, K, _io(x, "x"), 0, eps, 0), args, _stream_of(idx)))
     return q, scale, sum_out
 
 
@@ -327,19 +368,23 @@ def ss_gemm_q8(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: torch.T
     ss_quant_q8(square=True); K a multiple of 16. Returns y [..., N] in out_dtype (float32 or
     bfloat16; out's own where given); residual has y's shape and dtype and may be out itself.
     Asynchronous."""
+    idx = _gpu(xq, "xq")
+    if _elsewhere(idx, stream):
+        with _placed(idx, stream):
+            return ss_gemm_q8(xq, xs, wq, ws, residual=residual, out=out, out_dtype=out_dtype)
     M, K = _rows(xq, "xq")
     if wq.dim() != 2:
         raise ValueError("wq must be [N, K]")
-    N, dev, lead, KB = wq.shape[0], xq.device, xq.shape[:-1], -(-K // Q8_BLOCK)
-    with _On(dev, stream) as handle:
-        if out is None:
-            out = torch.empty(lead + (N,), dtype=out_dtype, device=dev)
-        yshape, dt = lead + (N,), out.dtype
-        dims = ss_gemm_q8_dims(M, N, K, _io(out, "out"), 0)
-        args = ss_gemm_q8_args(_same(xq, xq.shape, _Q8, dev, "xq"), _same(xs, lead + (KB,), _F32, dev, "xs"),
-                               _same(wq, (N, K), _Q8, dev, "wq"), _same(ws, (-(-N // Q8_BLOCK), KB), _F32, dev, "ws"),
-                               _opt(residual, yshape, dt, dev, "residual"), _same(out, yshape, dt, dev, "out"))
-        _check(lib.ss_gemm_q8(ctypes.byref(dims), ctypes.byref(args), handle))
+    N, shape, KB = wq.shape[0], xq.shape, -(-K // Q8_BLOCK)
+    lead = shape[:-1]
+    yshape = lead + (N,)
+    if out is None:
+        out = xq.new_empty(yshape, dtype=out_dtype)
+    dt = out.dtype
+    args = _pack_gemm_args(_same(xq, shape, _Q8, idx, "xq"), _same(xs, lead + (KB,), _F32, idx, "xs"),
+                           _same(wq, (N, K), _Q8, idx, "wq"), _same(ws, (-(-N // Q8_BLOCK), KB), _F32, idx, "ws"),
+                           _opt(residual, yshape, dt, idx, "residual"), _same(out, yshape, dt, idx, "out"))
+    _check(_raw.ss_gemm_q8(_pack_gemm_dims(M, N, K, _io(out, "out"), 0), args, _stream_of(idx)))
     return out
 
 

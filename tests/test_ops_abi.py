@@ -142,8 +142,8 @@ def test_binding_refuses_host_tensors():
         ss.ss_glr_fwd(t, t, t, torch.zeros(8))
     with pytest.raises(ValueError):
         ss.ss_glr_fwd(t[0], t[0], t[0], torch.zeros(8))
-    with pytest.raises(TypeError):
-        ss.ss_glr_fwd(t.half(), t, t, torch.zeros(8))
+    with pytest.raises(ValueError):
+        ss.ss_glr_step(t[0], t[0], t[0], torch.zeros(8), t[0])
 
 
 # ---------------------------------------------------------------------------
