@@ -141,7 +141,7 @@ ss_status ss_norm_q8(const ss_q8_dims* dims, const ss_norm_q8_args* args, void* 
  * of k (in a fixed order of several such sums where M is small). */
 typedef struct {
     int64_t m, n;       /* rows of X and of W, 1 <= m, n < 2^31                          */
-    int64_t k;          /* a multiple of 16, < 2^31                                      */
+    int64_t k;          /* a multiple of 16, <= 2^23                                     */
     int32_t y_dtype;    /* ss_dtype of y and residual                                    */
     int32_t reserved;   /* 0                                                             */
 } ss_gemm_q8_dims;

@@ -210,7 +210,8 @@ bool q8_vec(const ss_q8_dims& d, std::initializer_list<const void*> io16, const 
 ss_status check_gemm_q8_dims(const ss_gemm_q8_dims* d) {
     if (!d) return fail(SS_ERR_INVALID_ARG, "dims is NULL");
     if (d->m < 1 || d->n < 1 || d->k < 1) return fail(SS_ERR_INVALID_ARG, "m, n and k must be positive");
-    if (d->m > INT32_MAX || d->n > INT32_MAX || d->k > INT32_MAX) return fail(SS_ERR_INVALID_ARG, "m, n or k too large");
+    // rows of one tile are addressed by 32-bit offsets: 256 k < 2^32
+    if (d->m > INT32_MAX || d->n > INT32_MAX || d->k > (int64_t(1) << 23)) return fail(SS_ERR_INVALID_ARG, "m, n or k too large");
     if (d->k % 16) return fail(SS_ERR_UNSUPPORTED, "k %lld is not a multiple of 16", (long long)d->k);
     if (d->y_dtype != SS_F32 && d->y_dtype != SS_BF16) return fail(SS_ERR_UNSUPPORTED, "y_dtype %d unknown", d->y_dtype);
     if (d->reserved != 0) return fail(SS_ERR_INVALID_ARG, "reserved must be 0");

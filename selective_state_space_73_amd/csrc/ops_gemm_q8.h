@@ -60,6 +60,17 @@ template <> struct GqFrag<float> {
     }
 };
 
+// 64 lanes' 16-byte chunks from a matrix straight into 1024 consecutive bytes of LDS: byte
+// offset voff (per lane) + soff from the base, which may lie anywhere in memory.
+struct GqSource {
+    __amdgpu_buffer_rsrc_t r;
+    __device__ __forceinline__ explicit GqSource(const uint8_t* p)
+        : r(__builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, -1, kBufDword3)) {}
+    __device__ __forceinline__ void to_lds(gq_i4* lds, unsigned voff, unsigned soff) const {
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, lds, 16, voff, soff, 0, 0);
+    }
+};
+
 struct GemmQ8Args {
     const uint8_t* xq; const float* xs; const uint8_t* wq; const float* ws;
     const void* R; void* Y0; void* Y1;
@@ -67,29 +78,28 @@ struct GemmQ8Args {
     int KB;                       // blocks along k
 };
 
-// Four consecutive columns n .. n + 3 of row m, n a multiple of 4.
-template <typename T, bool RES>
-__device__ __forceinline__ void gq_store(const GemmQ8Args& p, int64_t m, int64_t n, gq_f4 v) {
+// W consecutive columns n .. n + W - 1 of row m, n a multiple of W.
+template <typename T, bool RES, int W>
+__device__ __forceinline__ void gq_store(const GemmQ8Args& p, int64_t m, int64_t n, const float* v) {
     if (m >= p.M || n >= p.N) return;
     const bool one = n >= p.split;
     const int64_t ld = one ? p.N - p.split : p.split, c = one ? n - p.split : n;
-    T* y = static_cast<T*>(one ? p.Y1 : p.Y0) + m * ld + c;
-    const T* r = RES ? static_cast<const T*>(p.R) + m * ld + c : nullptr;
-    const bool whole = c + 4 <= ld && ((ld | p.split) & 3) == 0;      // the base is 16-byte aligned: aligned to four elements
-    if (whole) {
-        typedef T t4 __attribute__((ext_vector_type(4)));
-        if (RES) {
-            const t4 rv = *reinterpret_cast<const t4*>(r);
+    if (c + W <= ld && ((ld | p.split) & (W - 1)) == 0) {        // bases are 16-byte aligned: whole and aligned accesses
+        constexpr int A = 16 / sizeof(T) < W ? 16 / sizeof(T) : W;    // elements of one access
+        typedef T ta __attribute__((ext_vector_type(A)));
+        T* y = static_cast<T*>(one ? p.Y1 : p.Y0) + m * ld + c;
+        const T* r = RES ? static_cast<const T*>(p.R) + m * ld + c : nullptr;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] += IO<T>::cvt(rv[j]);
+        for (int h = 0; h < W; h += A) {
+            ta o, rv;
+            if (RES) rv = *reinterpret_cast<const ta*>(r + h);
+#pragma unroll
+            for (int j = 0; j < A; ++j) o[j] = IO<T>::bits(RES ? v[h + j] + IO<T>::cvt(rv[j]) : v[h + j]);
+            *reinterpret_cast<ta*>(y + h) = o;
         }
-        t4 o;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) o[j] = IO<T>::bits(v[j]);
-        *reinterpret_cast<t4*>(y) = o;
     } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < W; ++j) {
             if (n + j >= p.N) break;
             const bool o2 = n + j >= p.split;
             const int64_t l2 = o2 ? p.N - p.split : p.split, at = m * l2 + (o2 ? n + j - p.split : n + j);
@@ -100,60 +110,120 @@ __device__ __forceinline__ void gq_store(const GemmQ8Args& p, int64_t m, int64_t
     }
 }
 
+// Workgroups go to the eight XCDs in turn, each with an L2 of its own: an XCD takes a
+// contiguous run of the tiles, in groups of kGqGroup tile rows, so that the tiles it works on
+// at one time share rows of X and of W.
+constexpr int kGqGroup = 4;
+struct GqTile { int m, n; };
+__device__ __forceinline__ GqTile gq_tile(unsigned id, int tiles_m, int tiles_n) {
+    const unsigned total = (unsigned)tiles_m * (unsigned)tiles_n;
+    const unsigned xcd = id & 7u, per = total >> 3, rest = total & 7u;
+    const unsigned t = xcd * per + (xcd < rest ? xcd : rest) + (id >> 3);
+    const unsigned in_group = kGqGroup * (unsigned)tiles_n;
+    const unsigned g = t / in_group, first = g * kGqGroup;
+    const unsigned rows = (unsigned)tiles_m - first < kGqGroup ? (unsigned)tiles_m - first : kGqGroup;
+    const unsigned at = t - g * in_group;
+    return GqTile{(int)(first + at % rows), (int)(at / rows)};
+}
+
 // ---------------------------------------------------------------------------
-// Many rows: a workgroup of WN x WM waves, each with 16 NF rows of W and 16 MF rows of X, the
-// blocks of both staged in LDS, double buffered. Rows past the end repeat the last one, chunks
-// past K are zero.
+// Many rows: a workgroup of WN x WM waves, each with 16 NF rows of W and 16 MF rows of X. A
+// block of both (128 bytes of each row) goes from memory straight into LDS, into one of two
+// buffers while the waves multiply the other.
+//
+// W's rows are dealt to the 16 x 16 products so that a lane ends up with eight consecutive
+// columns of Y, four from each of two products: product a takes row
+// 32 (a / 2) + 8 (i / 4) + 4 (a % 2) + i % 4 as its row i. A row's eight 16-byte chunks lie in
+// LDS at chunk ^ key(row), with a key that spreads the 16 rows a fragment read touches at one
+// chunk over the banks; the transfers write LDS in lane order, so the permutation is in what
+// they fetch. Rows past the end repeat the last one, chunks past K are zero.
+__device__ __forceinline__ int gq_key_w(int row) { return (row >> 1 & 1) | (row >> 3 & 3) << 1; }
+__device__ __forceinline__ int gq_key_x(int row) { return row >> 1 & 7; }
+
 template <typename T, bool RES, int NF, int MF, int WN, int WM>
-__global__ void __launch_bounds__(64 * WN * WM)
+__global__ void __launch_bounds__(64 * WN * WM, 2)
 k_gemm_q8(const GemmQ8Args p, int tiles_m, int tiles_n) {
     constexpr int TN = 16 * NF * WN, TM = 16 * MF * WM, TH = 64 * WN * WM;
-    constexpr int CW = TN * 8 / TH, CX = TM * 8 / TH;             // 16-byte chunks per thread and stage
+    constexpr int CW = TN * 8 / TH, CX = TM * 8 / TH;             // 16-byte chunks per thread and block
     static_assert(128 % (16 * NF) == 0, "one scale of W per wave");
+    using Frag = GqFrag<T>;
     __shared__ gq_i4 sW[2][TN * 8], sX[2][TM * 8];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wn = wave / WM, wm = wave % WM;
-    const int tm = blockIdx.x % tiles_m, tn = blockIdx.x / tiles_m;
-    const int64_t m0 = (int64_t)tm * TM, n0 = (int64_t)tn * TN;
+    const int fr = lane & 15, fc = lane >> 4;
+    const int wr = 8 * (fr >> 2) + (fr & 3);                      // row i = fr of product 0; its key is every product's
+    const int cw0 = wr * 8 + (fc ^ gq_key_w(wr)), cw1 = wr * 8 + ((fc + 4) ^ gq_key_w(wr));
+    const int cx0 = fr * 8 + (fc ^ gq_key_x(fr)), cx1 = fr * 8 + ((fc + 4) ^ gq_key_x(fr));
+    auto frag_w = [&](int buf, int a) {
+        const int row0 = wn * 16 * NF + 32 * (a / 2) + 4 * (a % 2);
+        Frag f;
+        f.set(sW[buf][row0 * 8 + cw0], sW[buf][row0 * 8 + cw1]);
+        return f;
+    };
+    auto frag_x = [&](int buf, int b) {
+        const int row0 = wm * 16 * MF + 16 * b;
+        Frag f;
+        f.set(sX[buf][row0 * 8 + cx0], sX[buf][row0 * 8 + cx1]);
+        return f;
+    };
 
-    gq_i4 rw[CW], rx[CX];
-    auto fetch = [&](int kb) {
+    // where the next block comes from: a tile's rows, as byte offsets of this thread's chunks in
+    // the tile's first block, and their scales
+    int64_t m0, n0;
+    GqSource from_w(p.wq), from_x(p.xq);
+    unsigned ow[CW], ox[CX], xo[MF];
+    const float* xsb;
+    const float* wsb;
+    auto aim = [&](int id) {
+        const GqTile tile = gq_tile((unsigned)id, tiles_m, tiles_n);
+        m0 = (int64_t)tile.m * TM;
+        n0 = (int64_t)tile.n * TN;
+        from_w = GqSource(p.wq + n0 * p.K);
+        from_x = GqSource(p.xq + m0 * p.K);
+        const int rows_w = (int)(p.N - n0 < TN ? p.N - n0 : TN), rows_x = (int)(p.M - m0 < TM ? p.M - m0 : TM);
 #pragma unroll
         for (int i = 0; i < CW; ++i) {
-            const int idx = tid + TH * i, r = idx >> 3, ch = (idx & 7) ^ (r & 7);
-            const int64_t row = n0 + r < p.N ? n0 + r : p.N - 1, k = (int64_t)kb * 128 + 16 * ch;
-            rw[i] = k < p.K ? *reinterpret_cast<const gq_i4*>(p.wq + row * p.K + k) : gq_i4{0, 0, 0, 0};
+            const int idx = tid + TH * i, r = idx >> 3, row = r < rows_w ? r : rows_w - 1;
+            ow[i] = (unsigned)row * (unsigned)p.K + 16u * ((idx & 7) ^ gq_key_w(r));
         }
 #pragma unroll
         for (int i = 0; i < CX; ++i) {
-            const int idx = tid + TH * i, r = idx >> 3, ch = (idx & 7) ^ (r & 7);
-            const int64_t row = m0 + r < p.M ? m0 + r : p.M - 1, k = (int64_t)kb * 128 + 16 * ch;
-            rx[i] = k < p.K ? *reinterpret_cast<const gq_i4*>(p.xq + row * p.K + k) : gq_i4{0, 0, 0, 0};
+            const int idx = tid + TH * i, r = idx >> 3, row = r < rows_x ? r : rows_x - 1;
+            ox[i] = (unsigned)row * (unsigned)p.K + 16u * ((idx & 7) ^ gq_key_x(r));
+        }
+        xsb = p.xs + m0 * p.KB;
+#pragma unroll
+        for (int b = 0; b < MF; ++b) {
+            const int r = wm * 16 * MF + 16 * b + fr;
+            xo[b] = (unsigned)(r < rows_x ? r : rows_x - 1) * (unsigned)p.KB;
+        }
+        const int64_t nw = n0 + wn * 16 * NF;
+        wsb = p.ws + (nw < p.N ? nw : p.N - 1) / 128 * p.KB;
+    };
+    auto stage = [&](int kb, int buf) {
+        const unsigned k0 = (unsigned)kb * 128u;
+#pragma unroll
+        for (int i = 0; i < CX; ++i) from_x.to_lds(&sX[buf][64 * wave + TH * i], ox[i], k0);
+#pragma unroll
+        for (int i = 0; i < CW; ++i) from_w.to_lds(&sW[buf][64 * wave + TH * i], ow[i], k0);
+    };
+    auto stage_end = [&](int kb, int buf) {                       // the last block of a K that is no multiple of 128
+        const unsigned k0 = (unsigned)kb * 128u;
+        const int left = (int)(p.K - k0) / 16;                    // its chunks
+#pragma unroll
+        for (int i = 0; i < CX; ++i) {
+            const int idx = tid + TH * i;
+            if (((idx & 7) ^ gq_key_x(idx >> 3)) < left) from_x.to_lds(&sX[buf][64 * wave + TH * i], ox[i], k0);
+            else sX[buf][idx] = gq_i4{0, 0, 0, 0};
+        }
+#pragma unroll
+        for (int i = 0; i < CW; ++i) {
+            const int idx = tid + TH * i;
+            if (((idx & 7) ^ gq_key_w(idx >> 3)) < left) from_w.to_lds(&sW[buf][64 * wave + TH * i], ow[i], k0);
+            else sW[buf][idx] = gq_i4{0, 0, 0, 0};
         }
     };
-    auto stash = [&](int buf) {
-#pragma unroll
-        for (int i = 0; i < CW; ++i) sW[buf][tid + TH * i] = rw[i];
-#pragma unroll
-        for (int i = 0; i < CX; ++i) sX[buf][tid + TH * i] = rx[i];
-    };
-    const int fr = lane & 15, fc = lane >> 4;
-    using Frag = GqFrag<T>;
-    auto frag = [&](const gq_i4* s, int row0) {
-        const int r = row0 + fr;
-        Frag f;
-        f.set(s[r * 8 + (fc ^ (r & 7))], s[r * 8 + ((fc + 4) ^ (r & 7))]);
-        return f;
-    };
-    const float* xs[MF];
-#pragma unroll
-    for (int b = 0; b < MF; ++b) {
-        const int64_t m = m0 + wm * 16 * MF + 16 * b + fr;
-        xs[b] = p.xs + (m < p.M ? m : p.M - 1) * p.KB;
-    }
-    const int64_t nw = n0 + wn * 16 * NF;
-    const float* ws = p.ws + (nw < p.N ? nw : p.N - 1) / 128 * p.KB;
 
     gq_f4 acc[NF][MF];
 #pragma unroll
@@ -161,153 +231,261 @@ k_gemm_q8(const GemmQ8Args p, int tiles_m, int tiles_n) {
 #pragma unroll
         for (int b = 0; b < MF; ++b) acc[a][b] = gq_f4{0.f, 0.f, 0.f, 0.f};
 
-    fetch(0);
-    stash(0);
-    float sc[MF];
+    const int tiles = tiles_m * tiles_n;
+    int id = blockIdx.x, kb = 0, buf = 0;
+    aim(id);
+    float nx[MF], nws = wsb[0];                                   // the next block's scales
 #pragma unroll
-    for (int b = 0; b < MF; ++b) sc[b] = xs[b][0] * ws[0];
-    __syncthreads();
-    for (int kb = 0; kb < p.KB; ++kb) {
-        const int buf = kb & 1;
-        const bool more = kb + 1 < p.KB;
-        float nx[MF], nwv = 0.0f;
+    for (int b = 0; b < MF; ++b) nx[b] = xsb[xo[b]];
+    if (p.K >= 128) stage(0, 0);
+    else stage_end(0, 0);
+    while (true) {
+        __syncthreads();                                          // this block is in LDS, the last one's readers are done
+        float sc[MF];
+#pragma unroll
+        for (int b = 0; b < MF; ++b) sc[b] = nx[b] * nws;
+        const bool last = kb + 1 == p.KB;                         // block of this tile
+        const int64_t m_now = m0, n_now = n0;
+        const int next = last ? id + (int)gridDim.x : id;
+        const int k_next = last ? 0 : kb + 1;
+        const bool more = next < tiles;
+        const bool whole = more && (unsigned)k_next * 128u + 128u <= (unsigned)p.K;
         if (more) {
-            fetch(kb + 1);
+            if (last) aim(next);
+            nws = wsb[k_next];
 #pragma unroll
-            for (int b = 0; b < MF; ++b) nx[b] = xs[b][kb + 1];
-            nwv = ws[kb + 1];
+            for (int b = 0; b < MF; ++b) nx[b] = xsb[xo[b] + k_next];
+            if (!whole) stage_end(k_next, buf ^ 1);
         }
+        __builtin_amdgcn_sched_barrier(0);
         Frag fx[MF];
 #pragma unroll
-        for (int b = 0; b < MF; ++b) fx[b] = frag(sX[buf], wm * 16 * MF + 16 * b);
+        for (int b = 0; b < MF; ++b) fx[b] = frag_x(buf, b);
+        Frag fw = frag_w(buf, 0);
+        // behind the first fragment reads (in front of them, or spread over the products, measured slower)
+        if (whole) stage(k_next, buf ^ 1);
+        gq_f4 q[MF];                                              // the last product row's results, on their way to acc
 #pragma unroll
-        for (int a = 0; a < NF; ++a) {
-            const Frag fw = frag(sW[buf], wn * 16 * NF + 16 * a);
+        for (int a = 0; a <= NF; ++a) {
+            gq_f4 t[MF];
+            if (a < NF) {
+                const Frag cur = fw;
+                if (a + 1 < NF) fw = frag_w(buf, a + 1);
+#pragma unroll
+                for (int b = 0; b < MF; ++b) t[b] = Frag::dot(cur, fx[b]);
+            }
+            if (a > 0) {
+#pragma unroll
+                for (int b = 0; b < MF; ++b) {
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) acc[a - 1][b][v] = __builtin_fmaf(q[b][v], sc[b], acc[a - 1][b][v]);
+                    asm volatile("" : "+v"(acc[a - 1][b]));   // here, and not behind all the products, whose results do not fit
+                }
+            }
+#pragma unroll
+            for (int b = 0; b < MF; ++b) q[b] = t[b];
+            // one matrix instruction, then the four additions that run in its shadow
+            if (a + 1 < NF) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
 #pragma unroll
             for (int b = 0; b < MF; ++b) {
-                const gq_f4 q = Frag::dot(fw, fx[b]);
+                if (a < NF) __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                if (a > 0) __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        buf ^= 1;
+        if (!last) {
+            ++kb;
+            continue;
+        }
+        // the tile is done: its stores run under the next tile's first blocks
 #pragma unroll
-                for (int v = 0; v < 4; ++v) acc[a][b][v] = __builtin_fmaf(q[v], sc[b], acc[a][b][v]);
+        for (int a = 0; a < NF; a += 2)
+#pragma unroll
+            for (int b = 0; b < MF; ++b) {
+                const float v[8] = {acc[a][b][0], acc[a][b][1], acc[a][b][2], acc[a][b][3],
+                                    acc[a + 1][b][0], acc[a + 1][b][1], acc[a + 1][b][2], acc[a + 1][b][3]};
+                gq_store<T, RES, 8>(p, m_now + wm * 16 * MF + 16 * b + fr, n_now + (wn * NF + a) * 16 + 8 * fc, v);
+                acc[a][b] = acc[a + 1][b] = gq_f4{0.f, 0.f, 0.f, 0.f};
+            }
+        if (next >= tiles) break;
+        id = next;
+        kb = 0;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Few tiles: KS groups of WN x WM waves share a workgroup's tile and take the blocks of k in
+// turn, each with LDS buffers of its own, so that a CU has enough bytes on their way while the
+// grid is short; their sums meet in LDS and are added in order. Staged as above; row i of
+// product a is row 16 a + i of the wave's rows of W.
+template <typename T, bool RES, int NF, int MF, int WN, int WM, int KS>
+__global__ void __launch_bounds__(64 * WN * WM * KS)
+k_gemm_q8_split(const GemmQ8Args p, int tiles_m, int tiles_n) {
+    constexpr int TN = 16 * NF * WN, TM = 16 * MF * WM, TH = 64 * WN * WM;
+    constexpr int CW = (TN * 8 + TH - 1) / TH, CX = (TM * 8 + TH - 1) / TH;
+    constexpr int LD = TN + 4;                                    // row of the sums: 4 floats on, against bank conflicts
+    static_assert(128 % TN == 0 && (TN * 8) % 64 == 0 && (TM * 8) % 64 == 0, "one scale of W; whole transfers");
+    static_assert(TM * LD * 4 <= 2 * (TN + TM) * 128, "the sums fit in the block buffers");
+    using Frag = GqFrag<T>;
+    __shared__ gq_i4 lds[KS][2 * (TN + TM) * 8];
+    const int tid = threadIdx.x % TH, lane = tid & 63;
+    const int grp = __builtin_amdgcn_readfirstlane(threadIdx.x / TH);
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wn = wave / WM, wm = wave % WM;
+    const int fr = lane & 15, fc = lane >> 4;
+    const GqTile tile = gq_tile(blockIdx.x, tiles_m, tiles_n);
+    const int64_t m0 = (int64_t)tile.m * TM, n0 = (int64_t)tile.n * TN;
+    auto sW = [&](int buf) { return lds[grp] + buf * TN * 8; };
+    auto sX = [&](int buf) { return lds[grp] + (2 * TN + buf * TM) * 8; };
+
+    const GqSource from_w(p.wq + n0 * p.K), from_x(p.xq + m0 * p.K);
+    const int rows_w = (int)(p.N - n0 < TN ? p.N - n0 : TN), rows_x = (int)(p.M - m0 < TM ? p.M - m0 : TM);
+    unsigned ow[CW], ox[CX];
+#pragma unroll
+    for (int i = 0; i < CW; ++i) {
+        const int idx = tid + TH * i, r = idx >> 3, row = r < rows_w ? r : rows_w - 1;
+        ow[i] = (unsigned)row * (unsigned)p.K + 16u * ((idx & 7) ^ gq_key_x(r));
+    }
+#pragma unroll
+    for (int i = 0; i < CX; ++i) {
+        const int idx = tid + TH * i, r = idx >> 3, row = r < rows_x ? r : rows_x - 1;
+        ox[i] = (unsigned)row * (unsigned)p.K + 16u * ((idx & 7) ^ gq_key_x(r));
+    }
+    auto stage = [&](int kb, int buf) {
+        const unsigned k0 = (unsigned)kb * 128u;
+        const int left = (int)(p.K - k0 < 128 ? (p.K - k0) / 16 : 8);       // chunks of this block
+#pragma unroll
+        for (int i = 0; i < CW; ++i) {
+            const int idx = tid + TH * i;
+            if (64 * wave + TH * i < TN * 8) {                    // uniform: whole waves
+                if (((idx & 7) ^ gq_key_x(idx >> 3)) < left) from_w.to_lds(sW(buf) + 64 * wave + TH * i, ow[i], k0);
+                else sW(buf)[idx] = gq_i4{0, 0, 0, 0};
             }
         }
-        if (more) {
-            stash(buf ^ 1);
 #pragma unroll
-            for (int b = 0; b < MF; ++b) sc[b] = nx[b] * nwv;
+        for (int i = 0; i < CX; ++i) {
+            const int idx = tid + TH * i;
+            if (64 * wave + TH * i < TM * 8) {
+                if (((idx & 7) ^ gq_key_x(idx >> 3)) < left) from_x.to_lds(sX(buf) + 64 * wave + TH * i, ox[i], k0);
+                else sX(buf)[idx] = gq_i4{0, 0, 0, 0};
+            }
         }
-        __syncthreads();
+    };
+    const int c0 = fr * 8 + (fc ^ gq_key_x(fr)), c1 = fr * 8 + ((fc + 4) ^ gq_key_x(fr));
+    auto frag = [&](const gq_i4* s, int row0) {
+        Frag f;
+        f.set(s[row0 * 8 + c0], s[row0 * 8 + c1]);
+        return f;
+    };
+    const float* xsb = p.xs + m0 * p.KB;
+    const float* wsb = p.ws + n0 / 128 * p.KB;
+    unsigned xo[MF];
+#pragma unroll
+    for (int b = 0; b < MF; ++b) {
+        const int r = wm * 16 * MF + 16 * b + fr;
+        xo[b] = (unsigned)(r < rows_x ? r : rows_x - 1) * (unsigned)p.KB;
     }
+    gq_f4 acc[NF][MF];
+#pragma unroll
+    for (int a = 0; a < NF; ++a)
+#pragma unroll
+        for (int b = 0; b < MF; ++b) acc[a][b] = gq_f4{0.f, 0.f, 0.f, 0.f};
+
+    float nx[MF], nws = 0.0f;
+    auto begin = [&](int kb, int buf) {
+        if (kb < p.KB) {
+            nws = wsb[kb];
+#pragma unroll
+            for (int b = 0; b < MF; ++b) nx[b] = xsb[xo[b] + kb];
+            stage(kb, buf);
+        }
+    };
+    begin(grp, 0);
+    const int steps = (p.KB + KS - 1) / KS;
+    for (int s = 0; s < steps; ++s) {
+        __syncthreads();                                          // this block is in LDS, the last one's readers are done
+        const int kb = s * KS + grp, buf = s & 1;
+        float sc[MF];
+#pragma unroll
+        for (int b = 0; b < MF; ++b) sc[b] = nx[b] * nws;
+        begin(kb + KS, buf ^ 1);
+        if (kb < p.KB) {
+            Frag fx[MF];
+#pragma unroll
+            for (int b = 0; b < MF; ++b) fx[b] = frag(sX(buf), wm * 16 * MF + 16 * b);
+#pragma unroll
+            for (int a = 0; a < NF; ++a) {
+                const Frag fw = frag(sW(buf), wn * 16 * NF + 16 * a);
+#pragma unroll
+                for (int b = 0; b < MF; ++b) {
+                    const gq_f4 q = Frag::dot(fw, fx[b]);
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) acc[a][b][v] = __builtin_fmaf(q[v], sc[b], acc[a][b][v]);
+                }
+            }
+        }
+    }
+    __syncthreads();                                              // every block is read: the buffers hold the sums now
 #pragma unroll
     for (int a = 0; a < NF; ++a)
 #pragma unroll
         for (int b = 0; b < MF; ++b)
-            gq_store<T, RES>(p, m0 + wm * 16 * MF + 16 * b + fr, nw + 16 * a + 4 * fc, acc[a][b]);
-}
-
-// ---------------------------------------------------------------------------
-// Few rows: W is read once, straight into registers. A workgroup has 16 NF rows of W and 16 MF
-// rows of X; its WK waves take the blocks of k in turn and add their sums in LDS, in order.
-template <typename T, bool RES, int NF, int MF, int WK>
-__global__ void __launch_bounds__(64 * WK)
-k_gemm_q8_thin(const GemmQ8Args p) {
-    __shared__ gq_f4 part[WK][NF * MF][64];
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int fr = lane & 15, fc = lane >> 4;
-    const int64_t n0 = (int64_t)blockIdx.x * (16 * NF), m0 = (int64_t)blockIdx.y * (16 * MF);
-    const uint8_t* w[NF];
-    const uint8_t* x[MF];
-    const float* xs[MF];
-#pragma unroll
-    for (int a = 0; a < NF; ++a) {
-        const int64_t n = n0 + 16 * a + fr;
-        w[a] = p.wq + (n < p.N ? n : p.N - 1) * p.K;
-    }
-#pragma unroll
-    for (int b = 0; b < MF; ++b) {
-        const int64_t m = m0 + 16 * b + fr, at = m < p.M ? m : p.M - 1;
-        x[b] = p.xq + at * p.K;
-        xs[b] = p.xs + at * p.KB;
-    }
-    static_assert(128 % (16 * NF) == 0, "one scale of W per workgroup");
-    const float* ws = p.ws + n0 / 128 * p.KB;
-
-    gq_f4 acc[NF][MF];
-#pragma unroll
-    for (int a = 0; a < NF; ++a)
-#pragma unroll
-        for (int b = 0; b < MF; ++b) acc[a][b] = gq_f4{0.f, 0.f, 0.f, 0.f};
-
-    struct Stage { gq_i4 w[NF][2], x[MF][2]; float s[MF], ws; };
-    auto load = [&](int kb, Stage& s) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int64_t k = (int64_t)kb * 128 + 16 * (fc + 4 * h);
-            const bool in = k < p.K;
-#pragma unroll
-            for (int a = 0; a < NF; ++a) s.w[a][h] = in ? *reinterpret_cast<const gq_i4*>(w[a] + k) : gq_i4{0, 0, 0, 0};
-#pragma unroll
-            for (int b = 0; b < MF; ++b) s.x[b][h] = in ? *reinterpret_cast<const gq_i4*>(x[b] + k) : gq_i4{0, 0, 0, 0};
-        }
-#pragma unroll
-        for (int b = 0; b < MF; ++b) s.s[b] = xs[b][kb];
-        s.ws = ws[kb];
-    };
-    auto use = [&](const Stage& s) {
-        GqFrag<T> fw[NF];
-#pragma unroll
-        for (int a = 0; a < NF; ++a) fw[a].set(s.w[a][0], s.w[a][1]);
-#pragma unroll
-        for (int b = 0; b < MF; ++b) {
-            GqFrag<T> fx;
-            fx.set(s.x[b][0], s.x[b][1]);
-            const float sc = s.s[b] * s.ws;
-#pragma unroll
-            for (int a = 0; a < NF; ++a) {
-                const gq_f4 q = GqFrag<T>::dot(fw[a], fx);
-#pragma unroll
-                for (int v = 0; v < 4; ++v) acc[a][b][v] = __builtin_fmaf(q[v], sc, acc[a][b][v]);
-            }
-        }
-    };
-    // two blocks in flight
-    Stage s0, s1;
-    if (wave < p.KB) load(wave, s0);
-    for (int kb = wave; kb < p.KB; kb += 2 * WK) {
-        const bool second = kb + WK < p.KB;
-        if (second) load(kb + WK, s1);
-        use(s0);
-        if (kb + 2 * WK < p.KB) load(kb + 2 * WK, s0);
-        if (second) use(s1);
-    }
-#pragma unroll
-    for (int a = 0; a < NF; ++a)
-#pragma unroll
-        for (int b = 0; b < MF; ++b) part[wave][a * MF + b][lane] = acc[a][b];
+            *reinterpret_cast<gq_f4*>(reinterpret_cast<float*>(lds[grp]) + (wm * 16 * MF + 16 * b + fr) * LD + wn * 16 * NF +
+                                      16 * a + 4 * fc) = acc[a][b];
     __syncthreads();
-    for (int t = wave; t < NF * MF; t += WK) {
-        gq_f4 v = part[0][t][lane];
+    for (int i = threadIdx.x; i < TM * TN / 8; i += TH * KS) {
+        const int r = i / (TN / 8), c = i % (TN / 8) * 8;
+        float v[8];
 #pragma unroll
-        for (int k = 1; k < WK; ++k) v += part[k][t][lane];
-        const int a = t / MF, b = t % MF;
-        gq_store<T, RES>(p, m0 + 16 * b + fr, n0 + 16 * a + 4 * fc, v);
+        for (int h = 0; h < 8; h += 4) {
+            gq_f4 t = *reinterpret_cast<const gq_f4*>(reinterpret_cast<const float*>(lds[0]) + r * LD + c + h);
+#pragma unroll
+            for (int g = 1; g < KS; ++g) t += *reinterpret_cast<const gq_f4*>(reinterpret_cast<const float*>(lds[g]) + r * LD + c + h);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[h + j] = t[j];
+        }
+        gq_store<T, RES, 8>(p, m0 + r, n0 + c, v);
     }
 }
 
+// Which kernel (measured on both sides of each rule, microseconds, K the repository's widths):
+//  - up to 256 tiles of 64 x 64 the waves of a workgroup split k: M 64, N 10240, K 2560 9.1
+//    against 11.9 unsplit, M 201, N 2561, K 5120 19.0 against 24.0; up to 96, tiles of 32 x 32 with eight
+//    groups: M 64, N 2560, K 5120 10.0 against 16.1 with 64-wide tiles and four. Up to 16 and
+//    32 rows of X take tiles that do not repeat rows: M 16, N 10240, K 2560 6.6 against 8.1.
+//  - tiles of 128 x 128 once there are 160 (fp32 outputs: 512): M 1024, N 2560, K 5120 43
+//    against 49 with 64 x 64, M 512, N 2560, K 5120 (80 tiles) 43 against 31.
+//  - tiles of 256 x 256, one per CU and round at 20 units of time, against 128 x 128, two per
+//    CU and round at 13: M 1024, N 10240, K 2560 42 (160 tiles) against 48 (640), M 2048 80
+//    (320) against 75 (1280), M 16384, N 2560, K 5120 267 (640) against 345 (2560).
 template <typename T, bool RES>
 hipError_t launch_gemm_q8_t(const LaunchGemmQ8& p) {
     const GemmQ8Args a{p.xq, p.xs, p.wq, p.ws, p.R, p.Y[0], p.Y[1], p.split, p.M, p.N, p.K, (int)((p.K + 127) / 128)};
     hipStream_t st = static_cast<hipStream_t>(p.stream);
-    if (p.M <= kGemmQ8ThinRows) {
-        const unsigned gn = (unsigned)((p.N + 31) / 32);
-        if (p.M <= 16) hipLaunchKernelGGL((k_gemm_q8_thin<T, RES, 2, 1, 8>), dim3(gn, 1), dim3(512), 0, st, a);
-        else if (p.M <= 32) hipLaunchKernelGGL((k_gemm_q8_thin<T, RES, 2, 2, 4>), dim3(gn, 1), dim3(256), 0, st, a);
-        else hipLaunchKernelGGL((k_gemm_q8_thin<T, RES, 2, 4, 4>), dim3(gn, (unsigned)((p.M + 63) / 64)), dim3(256), 0, st, a);
-    } else {
-        const int tm = (int)((p.M + 127) / 128), tn = (int)((p.N + 127) / 128);
-        hipLaunchKernelGGL((k_gemm_q8<T, RES, 4, 4, 2, 2>), dim3((unsigned)(tm * tn)), dim3(256), 0, st, a, tm, tn);
+    auto count = [&](int64_t m, int64_t n) { return ((p.M + m - 1) / m) * ((p.N + n - 1) / n); };
+    auto go = [&](auto kernel, int m, int n, int threads, int64_t most) {
+        const int tm = (int)((p.M + m - 1) / m), tn = (int)((p.N + n - 1) / n);
+        const int64_t tiles = (int64_t)tm * tn;
+        hipLaunchKernelGGL(kernel, dim3((unsigned)(tiles < most ? tiles : most)), dim3((unsigned)threads), 0, st, a, tm, tn);
+        return hipGetLastError();
+    };
+    constexpr int64_t kAll = INT32_MAX;
+    const int64_t t64 = count(64, 64), t128 = count(128, 128);
+    if (t64 <= 256) {
+        const bool few = t64 <= 96;
+        if (p.M <= 16) return few ? go(k_gemm_q8_split<T, RES, 1, 1, 2, 1, 8>, 16, 32, 1024, kAll)
+                                  : go(k_gemm_q8_split<T, RES, 1, 1, 4, 1, 4>, 16, 64, 1024, kAll);
+        if (few) return go(k_gemm_q8_split<T, RES, 1, 2, 2, 1, 8>, 32, 32, 1024, kAll);
+        if (p.M <= 32) return go(k_gemm_q8_split<T, RES, 1, 2, 4, 1, 4>, 32, 64, 1024, kAll);
+        return go(k_gemm_q8_split<T, RES, 2, 2, 2, 2, 4>, 64, 64, 1024, kAll);
     }
-    return hipGetLastError();
+    // the grids below are multiples of the eight XCDs: a workgroup's tiles stay on one
+    if (t128 < (sizeof(T) == 2 ? 160 : 512)) return go(k_gemm_q8<T, RES, 2, 2, 2, 2>, 64, 64, 256, 2048);
+    if constexpr (sizeof(T) == 2) {
+        if (20 * ((count(256, 256) + 255) / 256) <= 13 * ((t128 + 511) / 512)) return go(k_gemm_q8<T, RES, 8, 4, 2, 4>, 256, 256, 512, 256);
+    }
+    return go(k_gemm_q8<T, RES, 4, 4, 2, 2>, 128, 128, 256, 512);
 }
 
 }  // namespace selscan

@@ -54,7 +54,6 @@ struct LaunchGemmQ8 {
     int64_t split, M, N, K;
     void* stream;
 };
-constexpr int64_t kGemmQ8ThinRows = 256;   // rows of X up to which W goes straight to registers
 hipError_t launch_gemm_q8(const LaunchGemmQ8& p);
 
 }  // namespace selscan
