@@ -34,14 +34,12 @@ namespace selscan {
 // ---------------------------------------------------------------------------
 // gates
 
-// expm1(v) for |v| below kEm1Small by its Taylor polynomial (the first dropped term is
-// below 2^-26 of the result); elsewhere exp(v) - 1, which loses at most two bits there.
-constexpr float kEm1Small = 0.35f;
+// expm1(v) near 0: its Taylor polynomial up to v^5 (the first dropped term, v^5 / 720 of the
+// result, is below 2^-24 for |v| < kEm1Small, and a decay remembers 1 / |v| tokens of it).
+// Further out exp(v) - 1 loses three bits at most.
+constexpr float kEm1Small = 0.125f;
 __device__ __forceinline__ float expm1_small(float v) {
-    float p = 1.0f / 5040.0f;
-    p = __builtin_fmaf(p, v, 1.0f / 720.0f);
-    p = __builtin_fmaf(p, v, 1.0f / 120.0f);
-    p = __builtin_fmaf(p, v, 1.0f / 24.0f);
+    float p = __builtin_fmaf(v, 1.0f / 120.0f, 1.0f / 24.0f);
     p = __builtin_fmaf(p, v, 1.0f / 6.0f);
     p = __builtin_fmaf(p, v, 0.5f);
     p = __builtin_fmaf(p, v, 1.0f);
@@ -52,60 +50,75 @@ __device__ __forceinline__ float sigmoid(float v) { return rcp_fast(1.0f + exp2_
 
 struct Gate { float s, g, la, a, w2; };   // sigmoid(r), sigmoid(i), A s, exp(A s), 1 - a^2
 
-// The decay near 1 is what a long memory is made of: there a = 1 + expm1(A s), so that its
-// error is the rounding of the sum alone, and 1 - a^2 = -e (2 + e) with e = expm1(A s) keeps
-// its relative accuracy where 1 - a * a would cancel.
-__device__ __forceinline__ Gate glr_gate(float r, float i, float A) {
+// The decay near 1 is what a long memory is made of: a = 1 + expm1(A s) has the rounding of the
+// sum alone there, and 1 - a^2 = -e (1 + a) with e = expm1(A s) keeps its relative accuracy
+// where 1 - a * a would cancel.
+// `bias` is added to A s: 0, or minus infinity for a reset, which gives a = 0 and 1 - a^2 = 1.
+__device__ __forceinline__ Gate glr_gate(float r, float i, float A, float bias) {
     Gate q;
     q.s = sigmoid(r);
     q.g = sigmoid(i);
-    q.la = A * q.s;
-    const float ex = exp2_fast(kLog2e * q.la);
-    const float e = __builtin_fabsf(q.la) < kEm1Small ? expm1_small(q.la) : ex - 1.0f;
-    q.a = __builtin_fabsf(q.la) < kEm1Small ? 1.0f + e : ex;
-    q.w2 = -e * (2.0f + e);
+    q.la = __builtin_fmaf(A, q.s, bias);
+    const float far = exp2_fast(kLog2e * q.la) - 1.0f, near = expm1_small(q.la);
+    const float e = __builtin_fabsf(q.la) < kEm1Small ? near : far;
+    q.a = 1.0f + e;
+    q.w2 = -__builtin_fmaf(e, q.a, e);
     return q;
 }
 
 // ---------------------------------------------------------------------------
 // two channels of one row: loads, stores, conversions
 
+// Rows are addressed by a base that is uniform over the wave and 32-bit byte offsets of the
+// lane's channels (D is at most 2^26), which the memory instructions add themselves.
+template <typename T> __device__ __forceinline__ const T& at_byte(const void* row, unsigned off) {
+    return *reinterpret_cast<const T*>(static_cast<const char*>(row) + off);
+}
+template <typename T> __device__ __forceinline__ T& at_byte(void* row, unsigned off) {
+    return *reinterpret_cast<T*>(static_cast<char*>(row) + off);
+}
 template <typename T, bool VEC> struct Pair;
 template <> struct Pair<float, true> {
     typedef float v2 __attribute__((ext_vector_type(2)));
     v2 v;
-    __device__ __forceinline__ void ld(const float* p, int c0, int) { v = *reinterpret_cast<const v2*>(p + c0); }
+    __device__ __forceinline__ void ld(const void* row, unsigned c0, unsigned) { v = at_byte<v2>(row, 4 * c0); }
     __device__ __forceinline__ float get(int j) const { return v[j]; }
-    static __device__ __forceinline__ void st(float* p, int c0, int, bool ok0, bool, float a, float b) {
-        if (ok0) *reinterpret_cast<v2*>(p + c0) = v2{a, b};
+    __device__ __forceinline__ void set(float f) { v = v2{f, f}; }
+    static __device__ __forceinline__ void st(void* row, unsigned c0, unsigned, bool ok0, bool, float a, float b) {
+        if (ok0) at_byte<v2>(row, 4 * c0) = v2{a, b};
     }
 };
 template <> struct Pair<uint16_t, true> {
     typedef __bf16 b2 __attribute__((ext_vector_type(2)));
     typedef float f2 __attribute__((ext_vector_type(2)));
     uint32_t v;
-    __device__ __forceinline__ void ld(const uint16_t* p, int c0, int) { v = *reinterpret_cast<const uint32_t*>(p + c0); }
+    __device__ __forceinline__ void ld(const void* row, unsigned c0, unsigned) { v = at_byte<uint32_t>(row, 2 * c0); }
     __device__ __forceinline__ float get(int j) const {
         return __builtin_bit_cast(float, j ? (v & 0xffff0000u) : (v << 16));
     }
-    static __device__ __forceinline__ void st(uint16_t* p, int c0, int, bool ok0, bool, float a, float b) {
-        if (ok0) *reinterpret_cast<b2*>(p + c0) = __builtin_convertvector((f2{a, b}), b2);
+    __device__ __forceinline__ void set(float f) { v = (uint32_t)IO<uint16_t>::bits(f) * 0x10001u; }
+    static __device__ __forceinline__ void st(void* row, unsigned c0, unsigned, bool ok0, bool, float a, float b) {
+        if (ok0) at_byte<b2>(row, 2 * c0) = __builtin_convertvector((f2{a, b}), b2);
     }
 };
 template <typename T> struct Pair<T, false> {
     T v[2];
-    __device__ __forceinline__ void ld(const T* p, int c0, int c1) { v[0] = p[c0]; v[1] = p[c1]; }
+    __device__ __forceinline__ void ld(const void* row, unsigned c0, unsigned c1) {
+        v[0] = at_byte<T>(row, (unsigned)sizeof(T) * c0);
+        v[1] = at_byte<T>(row, (unsigned)sizeof(T) * c1);
+    }
     __device__ __forceinline__ float get(int j) const { return IO<T>::cvt(v[j]); }
-    static __device__ __forceinline__ void st(T* p, int c0, int c1, bool ok0, bool ok1, float a, float b) {
-        if (ok0) IO<T>::st(p + c0, a);
-        if (ok1) IO<T>::st(p + c1, b);
+    __device__ __forceinline__ void set(float f) { v[0] = v[1] = IO<T>::bits(f); }
+    static __device__ __forceinline__ void st(void* row, unsigned c0, unsigned c1, bool ok0, bool ok1, float a, float b) {
+        if (ok0) at_byte<T>(row, (unsigned)sizeof(T) * c0) = IO<T>::bits(a);
+        if (ok1) at_byte<T>(row, (unsigned)sizeof(T) * c1) = IO<T>::bits(b);
     }
 };
 
 // The two channels of a lane: next to each other where rows allow one access for both,
 // else 64 apart, so that a wave's accesses stay contiguous. Lanes past the last channel
 // repeat it (their loads stay in range) and store nothing.
-struct Chan { int c[2]; bool ok[2]; };
+struct Chan { unsigned c[2]; bool ok[2]; };
 template <bool VEC>
 __device__ __forceinline__ Chan lane_chan(int col, int lane, int D) {
     Chan q;
@@ -113,7 +126,7 @@ __device__ __forceinline__ Chan lane_chan(int col, int lane, int D) {
     for (int j = 0; j < 2; ++j) {
         const int c = col * kGlrCols + (VEC ? 2 * lane + j : lane + 64 * j);
         q.ok[j] = c < D;
-        q.c[j] = q.ok[j] ? c : (VEC ? D - 2 + j : D - 1);
+        q.c[j] = (unsigned)(q.ok[j] ? c : (VEC ? D - 2 + j : D - 1));
     }
     return q;
 }
@@ -147,43 +160,54 @@ __device__ __forceinline__ void word_store(uint64_t* p, uint64_t v) {
     __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// The state in front of a chunk, for one channel: `word` is the word of the chunk just in
-// front, the n words of the chunks in front lie `stride` apart towards it, and the first of
-// them always ends up as a state. Looks back for the nearest state in groups of kLook words
-// loaded together, waiting where a word is still empty, then folds forward from it.
-constexpr int kLook = 8;
-__device__ __forceinline__ float look_back(const uint64_t* word, int64_t stride, int n) {
-    int back = 0;                                  // words between `word` and the one looked at
-    for (bool found = false; !found;) {
-        uint64_t v[kLook];
+// The state in front of a chunk, for the CH channels of a wave (of whom the first `valid` exist).
+// `row` holds the words of the chunk just in front, the n rows of the chunks in front lie
+// `stride` apart towards it, and the first of them always ends up as states. The wave's 64 lanes
+// read 64 / CH rows at once (lane l channel l % CH, row l / CH, nearest first), go on to the
+// rows in front of these until every channel has met a state with no empty word nearer by, and
+// start over where one is empty. Then they fold forward over the rows read: a word that is a
+// state replaces what was folded so far, so that what lies in front of a channel's nearest
+// state, or has become a state since, does not matter. Every lane of a channel gets its state.
+template <int CH>
+__device__ __forceinline__ float look_back(const uint64_t* row, int64_t stride, int n, int valid, int lane) {
+    constexpr int kRows = 64 / CH;
+    constexpr uint32_t kAll = CH == 32 ? ~0u : (1u << CH) - 1u;
+    const uint32_t want = valid >= CH ? kAll : (1u << valid) - 1u;
+    const int ch = lane % CH < valid ? lane % CH : valid - 1, at = lane / CH;
+    auto load = [&](int first) { return word_load(row + (int64_t)(first + at < n ? first + at : n - 1) * stride + ch); };
+    uint64_t v;
+    int first = 0;                                 // rows between `row` and those read
+    uint32_t done = 0;                             // channels that have met a state
+    while (true) {
+        v = load(first);
+        const uint64_t st = __ballot(word_tag(v) == kStateTag), em = __ballot(v == kEmpty);
+        uint32_t open = want & ~done;              // channels that have met neither a state nor an empty word
 #pragma unroll
-        for (int q = 0; q < kLook; ++q) {
-            const int k = back + q < n ? back + q : n - 1;
-            v[q] = word_load(word + (int64_t)k * stride);
+        for (int i = 0; i < kRows; ++i) {
+            const uint32_t s = (uint32_t)(st >> (i * CH)) & kAll, e = (uint32_t)(em >> (i * CH)) & kAll;
+            done |= open & s;
+            open &= ~(s | e);
         }
-        bool stop = false;
-#pragma unroll
-        for (int q = 0; q < kLook; ++q) {
-            if (!stop) {
-                if (word_tag(v[q]) == kStateTag) found = stop = true;
-                else if (v[q] == kEmpty) { stop = true; __builtin_amdgcn_s_sleep(1); }
-                else if (back < n - 1) ++back;
-            }
+        if (done == want) break;
+        if (want & ~done & ~open) {
+            first = 0;                             // words nearer by may have become states meanwhile
+            done = 0;
+            __builtin_amdgcn_s_sleep(1);
+        } else {
+            first += kRows;
         }
     }
     float h = 0.0f;
-    // from the state forward; a word read now may have become a state itself, equal to the fold
-    for (int k = back; k >= 0; k -= kLook) {
-        uint64_t v[kLook];
+    while (true) {
 #pragma unroll
-        for (int q = 0; q < kLook; ++q) v[q] = word_load(word + (int64_t)(k - q > 0 ? k - q : 0) * stride);
-#pragma unroll
-        for (int q = 0; q < kLook; ++q)
-            if (k - q >= 0)
-                h = word_tag(v[q]) == kStateTag ? word_lo(v[q])
-                                                : fold(__builtin_bit_cast(float, word_tag(v[q])), h, word_lo(v[q]));
+        for (int i = kRows - 1; i >= 0; --i) {
+            const float t = word_tag(v) == kStateTag ? word_lo(v) : fold(__builtin_bit_cast(float, word_tag(v)), h, word_lo(v));
+            h = __shfl(t, i * CH + lane % CH, 64);
+        }
+        if (first == 0) return h;
+        first -= kRows;
+        v = load(first);
     }
-    return h;
 }
 
 __global__ void __launch_bounds__(256)
@@ -217,21 +241,38 @@ __device__ __forceinline__ Tile tile_at(const GlrArgs& p, unsigned t) {
     return q;
 }
 
-// Bit k: token t0 + k of batch row b resets. One load for the wave, a lane per token.
+// A lane per token: whether token t0 + lane of batch row b resets. The ballot over it has bit k
+// set where token t0 + k does.
 template <int TT>
-__device__ __forceinline__ uint32_t reset_bits(const GlrArgs& p, int b, int64_t t0, int lane) {
-    if (!p.reset) return 0u;
+__device__ __forceinline__ bool reset_at(const GlrArgs& p, int b, int64_t t0, int lane) {
     const int64_t t = t0 + lane;
-    const bool on = lane < TT && t < p.L && p.reset[(int64_t)b * p.L + t] != 0;
-    return (uint32_t)__ballot(on);
+    return p.reset && lane < TT && t < p.L && p.reset[(int64_t)b * p.L + t] != 0;
 }
+
+// Tokens of the run that starts at t0: TT of them, fewer at the end, 0 past it.
+__device__ __forceinline__ int run_tokens(const GlrArgs& p, int64_t t0, int TT) {
+    const int64_t left = p.L - t0;
+    return left < TT ? (left > 0 ? (int)left : 0) : TT;
+}
+
+// A run's rows: a base and a step that is uniform over the wave, past the last token a step of
+// zero, so that every address is one of the sequence's.
+template <typename T>
+struct Rows {
+    const char* at;
+    int64_t step;
+    __device__ __forceinline__ Rows(const void* p, int64_t sb, int64_t st, int b, int64_t t)
+        : at(static_cast<const char*>(p) + (b * sb + t * st) * (int64_t)sizeof(T)), step(st * (int64_t)sizeof(T)) {}
+    __device__ __forceinline__ void next(bool more) { at += more ? step : 0; }
+};
 
 // ---------------------------------------------------------------------------
 // forward. LOOK: several chunks per batch row, tiles taken by ticket; else one chunk, a
-// workgroup per tile.
+// workgroup per tile. Loading the next tile's rows before the wait for the state in front was
+// slower: the look-back's loads return behind them, and every chunk after this one waits for it.
 
 template <typename T, bool VEC, int TT, int NW, bool LOOK>
-__global__ void __launch_bounds__(NW * 64)
+__global__ void __launch_bounds__(NW * 64, 4)
 k_glr_fwd(const GlrArgs p) {
     using V = Pair<T, VEC>;
     __shared__ float2 s_map[NW][kGlrCols];        // (P, S) of each wave's run
@@ -239,27 +280,27 @@ k_glr_fwd(const GlrArgs p) {
     __shared__ unsigned s_next;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const T* X = static_cast<const T*>(p.x);
-    const T* R = static_cast<const T*>(p.r);
-    const T* I = static_cast<const T*>(p.i);
 
-    V vx[TT], vr[TT], vi[TT];
-    uint32_t resets = 0;
+    V vx[TT], vr[TT], vi[TT];                     // a run's rows
     float A[2];
+    bool reset = false;
     auto fetch = [&](unsigned t) {
         const Tile q = tile_at(p, t);
         const Chan c = lane_chan<VEC>(q.col, lane, p.D);
-        const int64_t t0 = (int64_t)q.chunk * (NW * TT) + wave * TT;
+        const int64_t t0 = (int64_t)q.chunk * (NW * TT) + wave * TT, tb = t0 < p.L ? t0 : p.L - 1;
+        const int n = run_tokens(p, t0, TT);
+        Rows<T> rx(p.x, p.xb, p.xt, q.b, tb), rr(p.r, p.rb, p.rt, q.b, tb), ri(p.i, p.ib, p.it, q.b, tb);
 #pragma unroll
         for (int k = 0; k < TT; ++k) {
-            const int64_t tk = t0 + k < p.L ? t0 + k : p.L - 1;
-            vx[k].ld(X + q.b * p.xb + tk * p.xt, c.c[0], c.c[1]);
-            vr[k].ld(R + q.b * p.rb + tk * p.rt, c.c[0], c.c[1]);
-            vi[k].ld(I + q.b * p.ib + tk * p.it, c.c[0], c.c[1]);
+            vx[k].ld(rx.at, c.c[0], c.c[1]);
+            vr[k].ld(rr.at, c.c[0], c.c[1]);
+            vi[k].ld(ri.at, c.c[0], c.c[1]);
+            const bool more = k + 1 < n;
+            rx.next(more); rr.next(more); ri.next(more);
         }
         A[0] = p.A[c.c[0]];
         A[1] = p.A[c.c[1]];
-        resets = reset_bits<TT>(p, q.b, t0, lane);
+        reset = reset_at<TT>(p, q.b, t0, lane);
     };
 
     unsigned tile = blockIdx.x;
@@ -269,8 +310,8 @@ k_glr_fwd(const GlrArgs p) {
         tile = __builtin_amdgcn_readfirstlane(s_next);
         __syncthreads();
     }
-    if (tile < p.tiles) fetch(tile);
     while (tile < p.tiles) {
+        fetch(tile);
         unsigned next = p.tiles;
         if constexpr (LOOK) {
             if (tid == 0) next = __hip_atomic_fetch_add(p.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -278,91 +319,115 @@ k_glr_fwd(const GlrArgs p) {
         const Tile q = tile_at(p, tile);
         const Chan c = lane_chan<VEC>(q.col, lane, p.D);
         const int64_t t0 = (int64_t)q.chunk * (NW * TT) + wave * TT;
-        const int n = (int)(p.L - t0 < TT ? p.L - t0 : TT);      // tokens of this run, 0 or less past the end
-        const uint32_t rs = resets;
+        const int n = run_tokens(p, t0, TT);
+        const uint32_t rs = (uint32_t)__ballot(reset);
+        // tokens past the end leave the state as it is: a = exp(A sigmoid(-inf)) = 1, w = 0; a reset
+        // token's r is not looked at
+        if (n < TT) {
+#pragma unroll
+            for (int k = 0; k < TT; ++k)
+                if (k >= n) { vx[k].set(0.0f); vr[k].set(-__builtin_inff()); vi[k].set(0.0f); }
+        }
+        if (rs) {
+#pragma unroll
+            for (int k = 0; k < TT; ++k)
+                if (rs >> k & 1u) vr[k].set(0.0f);
+        }
 
         // the run from a zero state: h[k] the local state, P[k] what a state in front is multiplied by
         float P[TT][2], h[TT][2];
 #pragma unroll
         for (int k = 0; k < TT; ++k) {
+            const bool on = rs >> k & 1u;
+            const float bias = on ? -__builtin_inff() : 0.0f;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const Gate g = glr_gate(vr[k].get(j), vi[k].get(j), A[j]);
-                const float v = g.g * vx[k].get(j);
-                const float Pp = k ? P[k - 1][j] : 1.0f, hp = k ? h[k - 1][j] : 0.0f;
-                if (k < n) {                                      // uniform over the wave
-                    if (rs >> k & 1u) {
-                        P[k][j] = -0.0f;
-                        h[k][j] = v;
-                    } else {
-                        P[k][j] = g.a * Pp;
-                        h[k][j] = __builtin_fmaf(g.a, hp, __builtin_amdgcn_sqrtf(g.w2) * v);
-                    }
-                } else {
-                    P[k][j] = Pp;
-                    h[k][j] = hp;
-                }
+                const Gate g = glr_gate(vr[k].get(j), vi[k].get(j), A[j], bias);
+                P[k][j] = k ? g.a * P[k - 1][j] : g.a;
+                h[k][j] = __builtin_amdgcn_sqrtf(g.w2) * (g.g * vx[k].get(j));
+                if (k) h[k][j] = __builtin_fmaf(g.a, on ? 0.0f : h[k - 1][j], h[k][j]);
             }
+            __builtin_amdgcn_sched_barrier(0);                    // token by token: other waves fill the pipes, and registers are few
         }
 #pragma unroll
-        for (int j = 0; j < 2; ++j) s_map[wave][lane_slot<VEC>(lane, j)] = make_float2(P[TT - 1][j], h[TT - 1][j]);
+        for (int j = 0; j < 2; ++j) s_map[wave][lane_slot<VEC>(lane, j)] = make_float2(rs ? -0.0f : P[TT - 1][j], h[TT - 1][j]);
         if (LOOK && tid == 0) s_next = next;
         __syncthreads();
-        if constexpr (LOOK) {
-            next = __builtin_amdgcn_readfirstlane(s_next);
-            if (next < p.tiles) fetch(next);                      // the next tile's loads run under what follows
-        }
+        if constexpr (LOOK) next = __builtin_amdgcn_readfirstlane(s_next);
 
-        // the states in front of the runs: one lane per channel
-        if (tid < kGlrCols && q.col * kGlrCols + tid < p.D) {
-            const int64_t bd = (int64_t)q.b * p.D + q.col * kGlrCols + tid;
-            const int64_t BD = (int64_t)p.B * p.D;
-            float2 m[NW];
-#pragma unroll
-            for (int w = 0; w < NW; ++w) m[w] = s_map[w][tid];
-            float in;
-            if (LOOK && q.chunk > 0) {
-                float cp = 1.0f, cs = 0.0f;
-#pragma unroll
-                for (int w = 0; w < NW; ++w) {
-                    cs = fold(m[w].x, cs, m[w].y);
-                    cp = fold_p(m[w].x, cp);
+        // the states in front of the runs: each wave for 128 / NW channels
+        {
+            constexpr int CH = kGlrCols / NW;
+            const int ch = wave * CH + lane % CH;
+            const int valid = p.D - q.col * kGlrCols - wave * CH;    // channels that exist from this wave's first on
+            if (valid > 0) {
+                const int64_t bd0 = (int64_t)q.b * p.D + q.col * kGlrCols + wave * CH, BD = (int64_t)p.B * p.D;
+                const bool mine = lane < CH && lane < valid;         // the lane that writes for its channel
+                float in = 0.0f;
+                if (LOOK && q.chunk > 0) {
+                    float cp = 1.0f, cs = 0.0f;
+#pragma unroll 4
+                    for (int w = 0; w < NW; ++w) {
+                        const float2 m = s_map[w][ch];
+                        cs = fold(m.x, cs, m.y);
+                        cp = fold_p(m.x, cp);
+                    }
+                    uint64_t* row = p.slots + (int64_t)q.chunk * BD + bd0;
+                    const bool pass = mine && q.chunk + 1 < p.nchunks;
+                    if (pass) word_store(row + lane, map_word(cp, cs));
+                    in = look_back<CH>(row - BD, -BD, q.chunk, valid, lane);
+                    if (pass) word_store(row + lane, state_word(fold(cp, in, cs)));
+                } else if (mine && p.state) {
+                    in = p.state[bd0 + lane];
                 }
-                uint64_t* word = p.slots + (int64_t)q.chunk * BD + bd;
-                if (q.chunk + 1 < p.nchunks) word_store(word, map_word(cp, cs));
-                in = look_back(word - BD, -BD, q.chunk);
-                if (q.chunk + 1 < p.nchunks) word_store(word, state_word(fold(cp, in, cs)));
-            } else {
-                in = p.state ? p.state[bd] : 0.0f;
+                if (mine) {
+                    float hh = in;
+#pragma unroll 4
+                    for (int w = 0; w < NW; ++w) {
+                        const float2 m = s_map[w][ch];
+                        s_in[w][ch] = hh;
+                        hh = fold(m.x, hh, m.y);
+                    }
+                    if (LOOK && q.chunk == 0) word_store(p.slots + bd0 + lane, state_word(hh));
+                }
             }
-            float hh = in;
-#pragma unroll
-            for (int w = 0; w < NW; ++w) {
-                s_in[w][tid] = hh;
-                hh = fold(m[w].x, hh, m[w].y);
-            }
-            if (LOOK && q.chunk == 0) word_store(p.slots + bd, state_word(hh));
         }
         __syncthreads();
 
         float in[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) in[j] = s_in[wave][lane_slot<VEC>(lane, j)];
-        if (p.ckpt && n > 0 && t0 % SS_GLR_CKPT == 0)
-            Pair<float, VEC>::st(p.ckpt + ((int64_t)q.b * p.nck + t0 / SS_GLR_CKPT) * p.D, c.c[0], c.c[1], c.ok[0], c.ok[1],
-                                 in[0], in[1]);
-        T* yrow = static_cast<T*>(p.y) + ((int64_t)q.b * p.L + t0) * p.D;
+        // The state in front of token 64 m of a batch row is checkpoint m: the one behind token k_ck
+        // of this run, if it is one of its tokens and not the sequence's last. The state behind the
+        // last token, k_end, is the final one.
+        const int k_ck = p.ckpt && n > 0 ? SS_GLR_CKPT - 1 - (int)(t0 % SS_GLR_CKPT) : -1;
+        const int k_end = n > 0 && t0 + n == p.L ? n - 1 : -1;
+        auto put_ckpt = [&](int64_t t, float a, float b) {
+            Pair<float, VEC>::st(p.ckpt + ((int64_t)q.b * p.nck + t / SS_GLR_CKPT) * p.D, c.c[0], c.c[1], c.ok[0], c.ok[1], a, b);
+        };
+        if (p.ckpt && t0 == 0) put_ckpt(0, in[0], in[1]);
+        char* yrow = static_cast<char*>(p.y) + ((int64_t)q.b * p.L + t0) * p.D * (int64_t)sizeof(T);
+        const int64_t ystep = (int64_t)p.D * (int64_t)sizeof(T);
+        auto put = [&](auto plain) {
+            constexpr bool kPlain = decltype(plain)::value;       // whole run, no reset
+            const int k_rs = rs ? __builtin_ctz(rs) : TT;         // from the first reset on the state in front does not count
 #pragma unroll
-        for (int k = 0; k < TT; ++k) {
-            if (k < n) {
-                float o[2];
+            for (int k = 0; k < TT; ++k) {
+                if (kPlain || k < n) {
+                    float o[2];
 #pragma unroll
-                for (int j = 0; j < 2; ++j) o[j] = rs ? fold(P[k][j], in[j], h[k][j]) : __builtin_fmaf(P[k][j], in[j], h[k][j]);
-                V::st(yrow + (int64_t)k * p.D, c.c[0], c.c[1], c.ok[0], c.ok[1], o[0], o[1]);
-                if (p.state && t0 + k == p.L - 1)
-                    Pair<float, VEC>::st(p.state + (int64_t)q.b * p.D, c.c[0], c.c[1], c.ok[0], c.ok[1], o[0], o[1]);
+                    for (int j = 0; j < 2; ++j)
+                        o[j] = kPlain || k < k_rs ? __builtin_fmaf(P[k][j], in[j], h[k][j]) : h[k][j];
+                    V::st(yrow, c.c[0], c.c[1], c.ok[0], c.ok[1], o[0], o[1]);
+                    yrow += ystep;
+                    if (k == k_ck && k != k_end) put_ckpt(t0 + k + 1, o[0], o[1]);
+                    if (k == k_end && p.state)
+                        Pair<float, VEC>::st(p.state + (int64_t)q.b * p.D, c.c[0], c.c[1], c.ok[0], c.ok[1], o[0], o[1]);
+                }
             }
-        }
+        };
+        if (n == TT && rs == 0) put(Tag<true>{});
+        else put(Tag<false>{});
         if constexpr (!LOOK) break;
         tile = next;
     }
@@ -421,12 +486,12 @@ k_glr_bwd(const GlrArgs p) {
             }
             A[0] = p.A[c.c[0]];
             A[1] = p.A[c.c[1]];
-            rs = reset_bits<TT>(p, q.b, t0, lane);
+            rs = (uint32_t)__ballot(reset_at<TT>(p, q.b, t0, lane));
 #pragma unroll
             for (int k = 0; k < TT; ++k)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const Gate e = glr_gate(vr[k].get(j), vi[k].get(j), A[j]);
+                    const Gate e = glr_gate(vr[k].get(j), vi[k].get(j), A[j], 0.0f);
                     s[k][j] = e.s;
                     g[k][j] = e.g;
                     a[k][j] = e.a;
@@ -460,40 +525,46 @@ k_glr_bwd(const GlrArgs p) {
         }
         __syncthreads();
 
-        if (tid < kGlrCols && q.col * kGlrCols + tid < p.D) {
-            const int ch = q.col * kGlrCols + tid;
-            const int64_t bd = (int64_t)q.b * p.D + ch;
-            const int64_t BD = (int64_t)p.B * p.D;
-            float mp[NW], mb[NW];
-#pragma unroll
-            for (int v = 0; v < NW; ++v) { mp[v] = s_p[v][tid]; mb[v] = s_b[v][tid]; }
-            float cp = 1.0f, cs = 0.0f;
-#pragma unroll
-            for (int v = NW - 1; v >= 0; --v) {
-                cs = fold(mp[v], cs, mb[v]);
-                cp = fold_p(mp[v], cp);
-            }
-            uint64_t* word = p.slots + (int64_t)q.chunk * BD + bd;
-            float in;
-            if (LOOK && q.chunk + 1 < p.nchunks) {
-                if (q.chunk > 0) word_store(word, map_word(cp, cs));
-                in = look_back(word + BD, BD, p.nchunks - 1 - q.chunk);
-            } else {
-                in = p.dstate_final ? p.dstate_final[bd] : 0.0f;
-            }
-            if (LOOK && q.chunk > 0) word_store(word, state_word(fold(cp, in, cs)));
-#pragma unroll
-            for (int v = NW - 1; v >= 0; --v) {
-                s_k[v][tid] = in;
-                in = fold(mp[v], in, mb[v]);
-            }
-            float h = 0.0f;
-#pragma unroll
-            for (int v = 0; v < NW; ++v) {
-                const int64_t tv = (int64_t)q.chunk * (NW * TT) + v * TT;
-                if (v * TT % SS_GLR_CKPT == 0) h = tv < p.L ? p.ckpt[((int64_t)q.b * p.nck + tv / SS_GLR_CKPT) * p.D + ch] : 0.0f;
-                s_h[v][tid] = h;
-                h = fold(mp[v], h, s_f[v][tid]);
+        {
+            constexpr int CH = kGlrCols / NW;
+            const int ch = wave * CH + lane % CH;
+            const int valid = p.D - q.col * kGlrCols - wave * CH;
+            if (valid > 0) {
+                const int64_t bd0 = (int64_t)q.b * p.D + q.col * kGlrCols + wave * CH, BD = (int64_t)p.B * p.D;
+                const bool mine = lane < CH && lane < valid;
+                float in = 0.0f;
+                if (LOOK && q.chunk + 1 < p.nchunks) {
+                    float cp = 1.0f, cs = 0.0f;
+#pragma unroll 4
+                    for (int v = NW - 1; v >= 0; --v) {
+                        cs = fold(s_p[v][ch], cs, s_b[v][ch]);
+                        cp = fold_p(s_p[v][ch], cp);
+                    }
+                    uint64_t* row = p.slots + (int64_t)q.chunk * BD + bd0;
+                    const bool pass = mine && q.chunk > 0;
+                    if (pass) word_store(row + lane, map_word(cp, cs));
+                    in = look_back<CH>(row + BD, BD, p.nchunks - 1 - q.chunk, valid, lane);
+                    if (pass) word_store(row + lane, state_word(fold(cp, in, cs)));
+                } else if (mine && p.dstate_final) {
+                    in = p.dstate_final[bd0 + lane];
+                }
+                if (mine) {
+#pragma unroll 4
+                    for (int v = NW - 1; v >= 0; --v) {
+                        s_k[v][ch] = in;
+                        in = fold(s_p[v][ch], in, s_b[v][ch]);
+                    }
+                    if (LOOK && q.chunk + 1 == p.nchunks) word_store(p.slots + (int64_t)q.chunk * BD + bd0 + lane, state_word(in));
+                    float h = 0.0f;
+#pragma unroll 4
+                    for (int v = 0; v < NW; ++v) {
+                        const int64_t tv = (int64_t)q.chunk * (NW * TT) + v * TT;
+                        if (v * TT % SS_GLR_CKPT == 0)
+                            h = tv < p.L ? p.ckpt[((int64_t)q.b * p.nck + tv / SS_GLR_CKPT) * p.D + q.col * kGlrCols + ch] : 0.0f;
+                        s_h[v][ch] = h;
+                        h = fold(s_p[v][ch], h, s_f[v][ch]);
+                    }
+                }
             }
         }
         __syncthreads();
@@ -594,14 +665,13 @@ k_glr_step(const GlrArgs p) {
     r.ld(static_cast<const T*>(p.r) + b * p.rb, c.c[0], c.c[1]);
     i.ld(static_cast<const T*>(p.i) + b * p.ib, c.c[0], c.c[1]);
     h.ld(p.state + (int64_t)b * p.D, c.c[0], c.c[1]);
-    if (VEC) A.ld(p.A, c.c[0], c.c[1]);
-    else { A.ld(p.A, c.c[0], c.c[1]); }
+    A.ld(p.A, c.c[0], c.c[1]);
     const bool rs = p.reset && p.reset[b] != 0;
     float o[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        const Gate g = glr_gate(r.get(j), i.get(j), A.get(j));
-        const float v = g.g * x.get(j);
+        const Gate g = glr_gate(r.get(j), i.get(j), A.get(j), 0.0f);
+        const float v = g.g * x.get(j);                               // what a reset leaves
         o[j] = rs ? v : __builtin_fmaf(g.a, h.get(j), __builtin_amdgcn_sqrtf(g.w2) * v);
     }
     F::st(p.state + (int64_t)b * p.D, c.c[0], c.c[1], c.ok[0], c.ok[1], o[0], o[1]);
@@ -648,9 +718,12 @@ hipError_t launch_glr_t(const LaunchGlr& p) {
     }
     const dim3 grid(look && a.tiles > kGlrGroups ? kGlrGroups : a.tiles);
     if (p.pass == LaunchGlr::kFwd) {
-        const dim3 block(kGlrFwdWaves * 64);
-        if (look) hipLaunchKernelGGL((k_glr_fwd<T, VEC, kGlrFwdTokens, kGlrFwdWaves, true>), grid, block, 0, st, a);
-        else hipLaunchKernelGGL((k_glr_fwd<T, VEC, kGlrFwdTokens, kGlrFwdWaves, false>), grid, block, 0, st, a);
+        // runs of 16 tokens and two workgroups per CU where a row's two channels fit one register
+        // (B 8, L 2048, D 5120, bf16: 162 us against 196 with 16 waves of 8 tokens), else runs of 8 (fp32, B 8,
+        // L 2048, D 2560: 144 against 153)
+        constexpr int TT = sizeof(T) == 2 && VEC ? 16 : 8, NW = kGlrFwdChunk / TT;
+        if (look) hipLaunchKernelGGL((k_glr_fwd<T, VEC, TT, NW, true>), grid, dim3(NW * 64), 0, st, a);
+        else hipLaunchKernelGGL((k_glr_fwd<T, VEC, TT, NW, false>), grid, dim3(NW * 64), 0, st, a);
     } else {
         const dim3 block(kGlrBwdWaves * 64);
         if (look) hipLaunchKernelGGL((k_glr_bwd<T, VEC, kGlrBwdTokens, kGlrBwdWaves, true>), grid, block, 0, st, a);

@@ -10,12 +10,10 @@
 namespace selscan {
 
 constexpr int kGlrCols = 128;       // channels per workgroup of the recurrence kernels (2 per lane)
-constexpr int kGlrFwdWaves = 8;     // waves of a forward workgroup, each with its own run of tokens
-constexpr int kGlrFwdTokens = 16;   // tokens per wave of the forward
+constexpr int kGlrFwdChunk = 128;   // tokens of a forward chunk
 constexpr int kGlrBwdWaves = 8;
 constexpr int kGlrBwdTokens = 8;    // tokens per wave of the backward
-constexpr int64_t kGlrFwdChunk = kGlrFwdWaves * kGlrFwdTokens;
-constexpr int64_t kGlrBwdChunk = kGlrBwdWaves * kGlrBwdTokens;
+constexpr int kGlrBwdChunk = kGlrBwdWaves * kGlrBwdTokens;
 
 // One launch of the recurrence, already validated by the C-ABI layer.
 struct LaunchGlr {
