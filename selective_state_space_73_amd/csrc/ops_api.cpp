@@ -64,7 +64,7 @@ ss_status check_glr_dims(const ss_glr_dims* d, GlrCall call) {
         return fail(SS_ERR_INVALID_ARG, "seqlen %lld not below 2^31", (long long)d->seqlen);
     if (d->io_dtype != SS_F32 && d->io_dtype != SS_BF16) return fail(SS_ERR_UNSUPPORTED, "io_dtype %d unknown", d->io_dtype);
     if (d->reserved != 0) return fail(SS_ERR_INVALID_ARG, "reserved must be 0");
-    const int64_t chunk = call == kBwd ? selscan::kGlrBwdChunk : selscan::kGlrFwdChunk;
+    const int64_t chunk = call == kBwd ? selscan::glr_bwd_chunk(d->batch, d->d) : selscan::kGlrFwdChunk;
     const int64_t n = call == kStep ? 1 : ceil_div(d->seqlen, chunk);
     const int64_t cols = ceil_div(d->d, selscan::kGlrCols);
     if (d->batch > INT32_MAX / (n * cols)) return fail(SS_ERR_INVALID_ARG, "batch x seqlen x d too large");
@@ -73,10 +73,11 @@ ss_status check_glr_dims(const ss_glr_dims* d, GlrCall call) {
 
 // Workspace of the chunked passes: the ticket, one word per chunk and channel (more than one
 // chunk), the backward's parts of dA.
-struct GlrLayout { int64_t nchunks; size_t off_slots, off_part, total; };
+struct GlrLayout { int64_t chunk, nchunks; size_t off_slots, off_part, total; };
 GlrLayout glr_layout(const ss_glr_dims& d, bool backward) {
     GlrLayout l{};
-    l.nchunks = ceil_div(d.seqlen, backward ? selscan::kGlrBwdChunk : selscan::kGlrFwdChunk);
+    l.chunk = backward ? selscan::glr_bwd_chunk(d.batch, d.d) : selscan::kGlrFwdChunk;
+    l.nchunks = ceil_div(d.seqlen, l.chunk);
     const size_t words = (size_t)l.nchunks * (size_t)d.batch * (size_t)d.d;
     size_t off = 0;
     if (l.nchunks > 1) {
@@ -149,6 +150,7 @@ selscan::LaunchGlr glr_launch(const ss_glr_dims& d, const ss_glr_args& a, bool e
 
 void glr_attach(selscan::LaunchGlr& p, const GlrLayout& l, void* workspace) {
     char* ws = static_cast<char*>(workspace);
+    p.chunk = l.chunk;
     p.nchunks = l.nchunks;
     if (l.nchunks > 1) {
         p.ticket = reinterpret_cast<unsigned*>(ws);
@@ -167,7 +169,7 @@ ss_status glr_forward(const ss_glr_dims* d, const ss_glr_args* a, void* workspac
     ss_status s = check_glr_dims(d, call);
     if (s == SS_OK) s = check_glr_args(*d, a, call, &in);
     if (s != SS_OK) return s;
-    const GlrLayout l = call == kStep ? GlrLayout{1, 0, 0, 0} : glr_layout(*d, false);
+    const GlrLayout l = call == kStep ? GlrLayout{1, 1, 0, 0, 0} : glr_layout(*d, false);
     if ((s = check_workspace(workspace, workspace_bytes, l.total)) != SS_OK) return s;
     const size_t B = (size_t)d->batch, L = call == kStep ? 1 : (size_t)d->seqlen, D = (size_t)d->d;
     const size_t nck = call == kStep ? 0 : (size_t)ceil_div(d->seqlen, SS_GLR_CKPT);

@@ -48,22 +48,24 @@ __device__ __forceinline__ float expm1_small(float v) {
 
 __device__ __forceinline__ float sigmoid(float v) { return rcp_fast(1.0f + exp2_fast(-kLog2e * v)); }
 
-struct Gate { float s, g, la, a, w2; };   // sigmoid(r), sigmoid(i), A s, exp(A s), 1 - a^2
-
 // The decay near 1 is what a long memory is made of: a = 1 + expm1(A s) has the rounding of the
 // sum alone there, and 1 - a^2 = -e (1 + a) with e = expm1(A s) keeps its relative accuracy
-// where 1 - a * a would cancel.
-// `bias` is added to A s: 0, or minus infinity for a reset, which gives a = 0 and 1 - a^2 = 1.
+// where 1 - a * a would cancel. `bias` is added to A s: 0, or minus infinity for a reset, which
+// gives a = 0 and 1 - a^2 = 1.
+struct Decay { float a, w2; };            // exp(A s), 1 - a^2
+__device__ __forceinline__ Decay glr_decay(float s, float A, float bias) {
+    const float la = __builtin_fmaf(A, s, bias);
+    const float far = exp2_fast(kLog2e * la) - 1.0f, near = expm1_small(la);
+    const float e = __builtin_fabsf(la) < kEm1Small ? near : far;
+    const float a = 1.0f + e;
+    return Decay{a, -__builtin_fmaf(e, a, e)};
+}
+
+struct Gate { float s, g, a, w2; };       // sigmoid(r), sigmoid(i), and the decay
 __device__ __forceinline__ Gate glr_gate(float r, float i, float A, float bias) {
-    Gate q;
-    q.s = sigmoid(r);
-    q.g = sigmoid(i);
-    q.la = __builtin_fmaf(A, q.s, bias);
-    const float far = exp2_fast(kLog2e * q.la) - 1.0f, near = expm1_small(q.la);
-    const float e = __builtin_fabsf(q.la) < kEm1Small ? near : far;
-    q.a = 1.0f + e;
-    q.w2 = -__builtin_fmaf(e, q.a, e);
-    return q;
+    const float s = sigmoid(r);
+    const Decay d = glr_decay(s, A, bias);
+    return Gate{s, sigmoid(i), d.a, d.w2};
 }
 
 // ---------------------------------------------------------------------------
@@ -77,6 +79,9 @@ template <typename T> __device__ __forceinline__ const T& at_byte(const void* ro
 template <typename T> __device__ __forceinline__ T& at_byte(void* row, unsigned off) {
     return *reinterpret_cast<T*>(static_cast<char*>(row) + off);
 }
+// renew(): the compiler may not carry over what it has computed from the values before (converted
+// copies of a whole run, kept from one pass over it to the next, would take the registers of
+// another workgroup).
 template <typename T, bool VEC> struct Pair;
 template <> struct Pair<float, true> {
     typedef float v2 __attribute__((ext_vector_type(2)));
@@ -84,6 +89,7 @@ template <> struct Pair<float, true> {
     __device__ __forceinline__ void ld(const void* row, unsigned c0, unsigned) { v = at_byte<v2>(row, 4 * c0); }
     __device__ __forceinline__ float get(int j) const { return v[j]; }
     __device__ __forceinline__ void set(float f) { v = v2{f, f}; }
+    __device__ __forceinline__ void renew() { asm volatile("" : "+v"(v)); }
     static __device__ __forceinline__ void st(void* row, unsigned c0, unsigned, bool ok0, bool, float a, float b) {
         if (ok0) at_byte<v2>(row, 4 * c0) = v2{a, b};
     }
@@ -97,21 +103,40 @@ template <> struct Pair<uint16_t, true> {
         return __builtin_bit_cast(float, j ? (v & 0xffff0000u) : (v << 16));
     }
     __device__ __forceinline__ void set(float f) { v = (uint32_t)IO<uint16_t>::bits(f) * 0x10001u; }
+    __device__ __forceinline__ void renew() { asm volatile("" : "+v"(v)); }
     static __device__ __forceinline__ void st(void* row, unsigned c0, unsigned, bool ok0, bool, float a, float b) {
         if (ok0) at_byte<b2>(row, 2 * c0) = __builtin_convertvector((f2{a, b}), b2);
     }
 };
-template <typename T> struct Pair<T, false> {
-    T v[2];
+template <> struct Pair<float, false> {
+    float v[2];
     __device__ __forceinline__ void ld(const void* row, unsigned c0, unsigned c1) {
-        v[0] = at_byte<T>(row, (unsigned)sizeof(T) * c0);
-        v[1] = at_byte<T>(row, (unsigned)sizeof(T) * c1);
+        v[0] = at_byte<float>(row, 4 * c0);
+        v[1] = at_byte<float>(row, 4 * c1);
     }
-    __device__ __forceinline__ float get(int j) const { return IO<T>::cvt(v[j]); }
-    __device__ __forceinline__ void set(float f) { v[0] = v[1] = IO<T>::bits(f); }
+    __device__ __forceinline__ float get(int j) const { return v[j]; }
+    __device__ __forceinline__ void set(float f) { v[0] = v[1] = f; }
+    __device__ __forceinline__ void renew() { asm volatile("" : "+v"(v[0]), "+v"(v[1])); }
     static __device__ __forceinline__ void st(void* row, unsigned c0, unsigned c1, bool ok0, bool ok1, float a, float b) {
-        if (ok0) at_byte<T>(row, (unsigned)sizeof(T) * c0) = IO<T>::bits(a);
-        if (ok1) at_byte<T>(row, (unsigned)sizeof(T) * c1) = IO<T>::bits(b);
+        if (ok0) at_byte<float>(row, 4 * c0) = a;
+        if (ok1) at_byte<float>(row, 4 * c1) = b;
+    }
+};
+template <> struct Pair<uint16_t, false> {
+    typedef uint16_t u2 __attribute__((ext_vector_type(2)));      // one register: the loads fill its halves
+    u2 v;
+    __device__ __forceinline__ void ld(const void* row, unsigned c0, unsigned c1) {
+        v = u2{at_byte<uint16_t>(row, 2 * c0), at_byte<uint16_t>(row, 2 * c1)};
+    }
+    __device__ __forceinline__ float get(int j) const {
+        const uint32_t u = __builtin_bit_cast(uint32_t, v);
+        return __builtin_bit_cast(float, j ? (u & 0xffff0000u) : (u << 16));
+    }
+    __device__ __forceinline__ void set(float f) { v = u2{IO<uint16_t>::bits(f), IO<uint16_t>::bits(f)}; }
+    __device__ __forceinline__ void renew() { asm volatile("" : "+v"(v)); }
+    static __device__ __forceinline__ void st(void* row, unsigned c0, unsigned c1, bool ok0, bool ok1, float a, float b) {
+        if (ok0) at_byte<uint16_t>(row, 2 * c0) = IO<uint16_t>::bits(a);
+        if (ok1) at_byte<uint16_t>(row, 2 * c1) = IO<uint16_t>::bits(b);
     }
 };
 
@@ -434,16 +459,21 @@ k_glr_fwd(const GlrArgs p) {
 }
 
 // ---------------------------------------------------------------------------
-// backward: the same tiles, taken from the last chunk to the first. The states in front of
-// the runs come from the forward's checkpoints and the runs' maps; what passes from a token
-// to the one before it is K_t = a_t g_t, whose map over a run is K -> P K + S with the
-// forward's P. Sums of dA over a run stay in registers, over a chunk in LDS; k_glr_da adds
-// the chunks.
+// backward: the same tiles, taken from the last chunk to the first. The states in front of the
+// runs come from the forward's checkpoints and the runs' maps; what passes from a token to the
+// one before it is K_t = a_t g_t, and over a run K -> P K + S with the forward's P and
+// S = sum_k P_k dy_k, P_k the product of the decays up to token k. The first pass over a run
+// keeps the sigmoids and, of the state in front of each token, its part from within the run and
+// the factor of what comes from outside; the second, backward in time, has the true states and
+// takes the decay and write coefficient from the sigmoids again (half of a gate's cost, for
+// four registers a token). Sums of dA over a run stay in registers, over a chunk in LDS;
+// k_glr_da adds the chunks.
 
 template <typename T, bool VEC, int TT, int NW, bool LOOK>
-__global__ void __launch_bounds__(NW * 64)
+__global__ void __launch_bounds__(NW * 64, NW > 8 ? 4 : 2)
 k_glr_bwd(const GlrArgs p) {
-    static_assert(SS_GLR_CKPT % TT == 0 && (NW * TT) % SS_GLR_CKPT == 0, "checkpoints lie at starts of runs");
+    constexpr int CK = NW * TT / SS_GLR_CKPT;                     // checkpoints of a chunk
+    static_assert(SS_GLR_CKPT % TT == 0 && CK * SS_GLR_CKPT == NW * TT, "checkpoints lie at starts of runs");
     using V = Pair<T, VEC>;
     __shared__ float s_p[NW][kGlrCols], s_f[NW][kGlrCols], s_b[NW][kGlrCols];   // P and both S of each run
     __shared__ float s_h[NW][kGlrCols], s_k[NW][kGlrCols];                      // state in front, K from behind
@@ -451,177 +481,188 @@ k_glr_bwd(const GlrArgs p) {
     __shared__ unsigned s_next;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const T* X = static_cast<const T*>(p.x);
-    const T* R = static_cast<const T*>(p.r);
-    const T* I = static_cast<const T*>(p.i);
-    const T* DY = static_cast<const T*>(p.dy);
+    constexpr int CH = kGlrCols / NW;                             // channels that a wave joins runs for
 
-    for (unsigned tile = blockIdx.x;;) {
+    unsigned tile = blockIdx.x;
+    if constexpr (LOOK) {
+        if (tid == 0) s_next = __hip_atomic_fetch_add(p.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __syncthreads();
+        tile = __builtin_amdgcn_readfirstlane(s_next);
+        __syncthreads();
+    }
+    while (tile < p.tiles) {
+        unsigned next = p.tiles;
         if constexpr (LOOK) {
-            __syncthreads();                                     // the last tile's s_next and s_a are read
-            if (tid == 0) s_next = __hip_atomic_fetch_add(p.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            __syncthreads();
-            tile = __builtin_amdgcn_readfirstlane(s_next);
-            if (tile >= p.tiles) break;
+            if (tid == 0) next = __hip_atomic_fetch_add(p.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         }
         Tile q = tile_at(p, tile);
         q.chunk = p.nchunks - 1 - q.chunk;
         const Chan c = lane_chan<VEC>(q.col, lane, p.D);
         const int64_t t0 = (int64_t)q.chunk * (NW * TT) + wave * TT;
-        const int n = (int)(p.L - t0 < TT ? p.L - t0 : TT);
+        const int n = run_tokens(p, t0, TT);
+        const int64_t bd0 = (int64_t)q.b * p.D + q.col * kGlrCols + wave * CH, BD = (int64_t)p.B * p.D;
+        const int valid = p.D - q.col * kGlrCols - wave * CH;     // channels that exist from this wave's first on
+        const bool mine = lane < CH && lane < valid;              // the lane that writes for its channel
 
         V vx[TT], vd[TT];
-        float s[TT][2], g[TT][2], a[TT][2], w[TT][2];
-        float A[2], P[2] = {1.0f, 1.0f}, Sf[2] = {0.0f, 0.0f}, Sb[2] = {0.0f, 0.0f};
+        float s[TT][2], g[TT][2], A[2];
+        float P[TT][2], h[TT][2];                                 // in front of token k: state h + P times the run's
+        float ck[CK];
         uint32_t rs;
+        int k_rs;
         {
             V vr[TT], vi[TT];
+            const int64_t tb = t0 < p.L ? t0 : p.L - 1;
+            Rows<T> rx(p.x, p.xb, p.xt, q.b, tb), rr(p.r, p.rb, p.rt, q.b, tb), ri(p.i, p.ib, p.it, q.b, tb),
+                rd(p.dy, p.L * p.D, p.D, q.b, tb);
 #pragma unroll
             for (int k = 0; k < TT; ++k) {
-                const int64_t tk = t0 + k < p.L ? t0 + k : p.L - 1;
-                vx[k].ld(X + q.b * p.xb + tk * p.xt, c.c[0], c.c[1]);
-                vr[k].ld(R + q.b * p.rb + tk * p.rt, c.c[0], c.c[1]);
-                vi[k].ld(I + q.b * p.ib + tk * p.it, c.c[0], c.c[1]);
-                vd[k].ld(DY + ((int64_t)q.b * p.L + tk) * p.D, c.c[0], c.c[1]);
+                vx[k].ld(rx.at, c.c[0], c.c[1]);
+                vr[k].ld(rr.at, c.c[0], c.c[1]);
+                vi[k].ld(ri.at, c.c[0], c.c[1]);
+                vd[k].ld(rd.at, c.c[0], c.c[1]);
+                const bool more = k + 1 < n;
+                rx.next(more); rr.next(more); ri.next(more); rd.next(more);
             }
             A[0] = p.A[c.c[0]];
             A[1] = p.A[c.c[1]];
-            rs = (uint32_t)__ballot(reset_at<TT>(p, q.b, t0, lane));
 #pragma unroll
-            for (int k = 0; k < TT; ++k)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const Gate e = glr_gate(vr[k].get(j), vi[k].get(j), A[j], 0.0f);
-                    s[k][j] = e.s;
-                    g[k][j] = e.g;
-                    a[k][j] = e.a;
-                    w[k][j] = __builtin_amdgcn_sqrtf(e.w2);
-                    if (k < n) {
-                        const float v = e.g * vx[k].get(j);
-                        if (rs >> k & 1u) {
-                            a[k][j] = 0.0f;
-                            w[k][j] = 1.0f;
-                            P[j] = -0.0f;
-                            Sf[j] = v;
-                        } else {
-                            P[j] *= e.a;
-                            Sf[j] = __builtin_fmaf(e.a, Sf[j], w[k][j] * v);
-                        }
-                    }
-                }
-        }
-#pragma unroll
-        for (int k = TT - 1; k >= 0; --k)
-            if (k < n)
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    Sb[j] = (rs >> k & 1u) ? 0.0f : a[k][j] * (vd[k].get(j) + Sb[j]);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int at = lane_slot<VEC>(lane, j);
-            s_p[wave][at] = P[j];
-            s_f[wave][at] = Sf[j];
-            s_b[wave][at] = Sb[j];
-        }
-        __syncthreads();
-
-        {
-            constexpr int CH = kGlrCols / NW;
-            const int ch = wave * CH + lane % CH;
-            const int valid = p.D - q.col * kGlrCols - wave * CH;
-            if (valid > 0) {
-                const int64_t bd0 = (int64_t)q.b * p.D + q.col * kGlrCols + wave * CH, BD = (int64_t)p.B * p.D;
-                const bool mine = lane < CH && lane < valid;
-                float in = 0.0f;
-                if (LOOK && q.chunk + 1 < p.nchunks) {
-                    float cp = 1.0f, cs = 0.0f;
-#pragma unroll 4
-                    for (int v = NW - 1; v >= 0; --v) {
-                        cs = fold(s_p[v][ch], cs, s_b[v][ch]);
-                        cp = fold_p(s_p[v][ch], cp);
-                    }
-                    uint64_t* row = p.slots + (int64_t)q.chunk * BD + bd0;
-                    const bool pass = mine && q.chunk > 0;
-                    if (pass) word_store(row + lane, map_word(cp, cs));
-                    in = look_back<CH>(row + BD, BD, p.nchunks - 1 - q.chunk, valid, lane);
-                    if (pass) word_store(row + lane, state_word(fold(cp, in, cs)));
-                } else if (mine && p.dstate_final) {
-                    in = p.dstate_final[bd0 + lane];
-                }
-                if (mine) {
-#pragma unroll 4
-                    for (int v = NW - 1; v >= 0; --v) {
-                        s_k[v][ch] = in;
-                        in = fold(s_p[v][ch], in, s_b[v][ch]);
-                    }
-                    if (LOOK && q.chunk + 1 == p.nchunks) word_store(p.slots + (int64_t)q.chunk * BD + bd0 + lane, state_word(in));
-                    float h = 0.0f;
-#pragma unroll 4
-                    for (int v = 0; v < NW; ++v) {
-                        const int64_t tv = (int64_t)q.chunk * (NW * TT) + v * TT;
-                        if (v * TT % SS_GLR_CKPT == 0)
-                            h = tv < p.L ? p.ckpt[((int64_t)q.b * p.nck + tv / SS_GLR_CKPT) * p.D + q.col * kGlrCols + ch] : 0.0f;
-                        s_h[v][ch] = h;
-                        h = fold(s_p[v][ch], h, s_f[v][ch]);
-                    }
-                }
+            for (int m = 0; m < CK; ++m) {
+                const int64_t ci = (int64_t)q.chunk * CK + m;
+                ck[m] = mine && ci < p.nck ? p.ckpt[((int64_t)q.b * p.nck + ci) * p.D + q.col * kGlrCols + wave * CH + lane] : 0.0f;
             }
-        }
-        __syncthreads();
-
-        // the run again, now with the true states: hb[k] the state before token k
-        float hb[TT][2], K[2], dA[2] = {0.0f, 0.0f};
+            rs = (uint32_t)__ballot(reset_at<TT>(p, q.b, t0, lane));
+            k_rs = rs ? __builtin_ctz(rs) : TT;
+            if (n < TT) {                                         // past the end: a = 1, w = 0, no gradient
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            float h = s_h[wave][lane_slot<VEC>(lane, j)];
-            K[j] = s_k[wave][lane_slot<VEC>(lane, j)];
+                for (int k = 0; k < TT; ++k)
+                    if (k >= n) { vx[k].set(0.0f); vr[k].set(-__builtin_inff()); vi[k].set(0.0f); vd[k].set(0.0f); }
+            }
+            if (rs) {
+#pragma unroll
+                for (int k = 0; k < TT; ++k)
+                    if (rs >> k & 1u) vr[k].set(0.0f);
+            }
+            float Pk[2] = {1.0f, 1.0f}, Sf[2] = {0.0f, 0.0f}, Sb[2] = {0.0f, 0.0f};
 #pragma unroll
             for (int k = 0; k < TT; ++k) {
-                hb[k][j] = h;
-                const float b = w[k][j] * (g[k][j] * vx[k].get(j));
-                h = (rs >> k & 1u) ? b : __builtin_fmaf(a[k][j], h, b);
-            }
-        }
-        const int64_t row0 = ((int64_t)q.b * p.L + t0) * p.D;
-#pragma unroll
-        for (int k = TT - 1; k >= 0; --k) {
-            if (k < n) {
-                float dx[2], dr[2], di[2];
+                const bool on = rs >> k & 1u;
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const float x = vx[k].get(j), G = vd[k].get(j) + K[j];
-                    const float gw = G * w[k][j], v = g[k][j] * x;
-                    dx[j] = gw * g[k][j];
-                    di[j] = gw * (v * (1.0f - g[k][j]));
-                    if (rs >> k & 1u) {
-                        K[j] = 0.0f;
-                        dr[j] = 0.0f;
-                    } else {
-                        const float rw = w[k][j] > 0.0f ? rcp_fast(w[k][j]) : 0.0f;
-                        K[j] = a[k][j] * G;
-                        const float dla = K[j] * (hb[k][j] - a[k][j] * rw * v);
-                        dr[j] = dla * (A[j] * s[k][j]) * (1.0f - s[k][j]);
-                        dA[j] = __builtin_fmaf(dla, s[k][j], dA[j]);
+                    const Gate e = glr_gate(vr[k].get(j), vi[k].get(j), A[j], on ? -__builtin_inff() : 0.0f);
+                    s[k][j] = e.s;
+                    g[k][j] = e.g;
+                    P[k][j] = Pk[j];
+                    h[k][j] = Sf[j];
+                    Pk[j] *= e.a;
+                    Sf[j] = __builtin_fmaf(e.a, on ? 0.0f : Sf[j], __builtin_amdgcn_sqrtf(e.w2) * (e.g * vx[k].get(j)));
+                    Sb[j] = k < k_rs ? __builtin_fmaf(Pk[j], vd[k].get(j), Sb[j]) : Sb[j];
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int at = lane_slot<VEC>(lane, j);
+                s_p[wave][at] = rs ? -0.0f : Pk[j];
+                s_f[wave][at] = Sf[j];
+                s_b[wave][at] = Sb[j];
+            }
+        }
+        if (LOOK && tid == 0) s_next = next;
+        __syncthreads();
+        if constexpr (LOOK) next = __builtin_amdgcn_readfirstlane(s_next);
+
+        if (valid > 0) {
+            const int ch = wave * CH + lane % CH;
+            float in = 0.0f;
+            if (LOOK && q.chunk + 1 < p.nchunks) {
+                float cp = 1.0f, cs = 0.0f;
+#pragma unroll 4
+                for (int v = NW - 1; v >= 0; --v) {
+                    cs = fold(s_p[v][ch], cs, s_b[v][ch]);
+                    cp = fold_p(s_p[v][ch], cp);
+                }
+                uint64_t* row = p.slots + (int64_t)q.chunk * BD + bd0;
+                const bool pass = mine && q.chunk > 0;
+                if (pass) word_store(row + lane, map_word(cp, cs));
+                in = look_back<CH>(row + BD, BD, p.nchunks - 1 - q.chunk, valid, lane);
+                if (pass) word_store(row + lane, state_word(fold(cp, in, cs)));
+            } else if (mine && p.dstate_final) {
+                in = p.dstate_final[bd0 + lane];
+            }
+            if (mine) {
+#pragma unroll 4
+                for (int v = NW - 1; v >= 0; --v) {
+                    s_k[v][ch] = in;
+                    in = fold(s_p[v][ch], in, s_b[v][ch]);
+                }
+                if (LOOK && q.chunk + 1 == p.nchunks) word_store(p.slots + (int64_t)q.chunk * BD + bd0 + lane, state_word(in));
+#pragma unroll
+                for (int m = 0; m < CK; ++m) {
+                    float hh = ck[m];
+#pragma unroll 4
+                    for (int v = m * (NW / CK); v < (m + 1) * (NW / CK); ++v) {
+                        s_h[v][ch] = hh;
+                        hh = fold(s_p[v][ch], hh, s_f[v][ch]);
                     }
                 }
-                const int64_t o = row0 + (int64_t)k * p.D;
-                V::st(static_cast<T*>(p.dx) + o, c.c[0], c.c[1], c.ok[0], c.ok[1], dx[0], dx[1]);
-                V::st(static_cast<T*>(p.dr) + o, c.c[0], c.c[1], c.ok[0], c.ok[1], dr[0], dr[1]);
-                V::st(static_cast<T*>(p.di) + o, c.c[0], c.c[1], c.ok[0], c.ok[1], di[0], di[1]);
             }
+        }
+        __syncthreads();
+
+        float K[2], dA[2] = {0.0f, 0.0f}, in[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            in[j] = s_h[wave][lane_slot<VEC>(lane, j)];
+            K[j] = s_k[wave][lane_slot<VEC>(lane, j)];
+        }
+        const int64_t o1 = (((int64_t)q.b * p.L + t0 + n) * p.D) * (int64_t)sizeof(T), step = (int64_t)p.D * (int64_t)sizeof(T);
+        char* px = static_cast<char*>(p.dx) + o1;                 // behind the run's last row
+        char* pr = static_cast<char*>(p.dr) + o1;
+        char* pi = static_cast<char*>(p.di) + o1;
+#pragma unroll
+        for (int k = TT - 1; k >= 0; --k) {
+            const bool on = rs >> k & 1u;
+            float dx[2], dr[2], di[2];
+            vx[k].renew();
+            vd[k].renew();
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                asm volatile("" : "+v"(s[k][j]), "+v"(g[k][j]));      // see renew()
+                const Decay e = glr_decay(s[k][j], A[j], on ? -__builtin_inff() : 0.0f);
+                // 1 / w, and w from it; both 0 where w is (the slope there is taken as 0)
+                const float rw = e.w2 > 0.0f ? __builtin_amdgcn_rsqf(e.w2) : 0.0f, w = e.w2 * rw;
+                const float before = k <= k_rs ? __builtin_fmaf(P[k][j], in[j], h[k][j]) : h[k][j];
+                const float x = vx[k].get(j), G = vd[k].get(j) + K[j];
+                const float gw = G * w, v = g[k][j] * x;
+                dx[j] = gw * g[k][j];
+                di[j] = gw * (v * (1.0f - g[k][j]));
+                K[j] = on ? 0.0f : e.a * G;
+                const float dla = on ? 0.0f : K[j] * (before - e.a * rw * v);
+                dr[j] = dla * (A[j] * s[k][j]) * (1.0f - s[k][j]);
+                dA[j] = __builtin_fmaf(dla, s[k][j], dA[j]);
+            }
+            if (k < n) {
+                px -= step; pr -= step; pi -= step;
+                V::st(px, c.c[0], c.c[1], c.ok[0], c.ok[1], dx[0], dx[1]);
+                V::st(pr, c.c[0], c.c[1], c.ok[0], c.ok[1], dr[0], dr[1]);
+                V::st(pi, c.c[0], c.c[1], c.ok[0], c.ok[1], di[0], di[1]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
         }
         if (p.dstate_init && t0 == 0)
             Pair<float, VEC>::st(p.dstate_init + (int64_t)q.b * p.D, c.c[0], c.c[1], c.ok[0], c.ok[1], K[0], K[1]);
 #pragma unroll
         for (int j = 0; j < 2; ++j) s_a[wave][lane_slot<VEC>(lane, j)] = dA[j];
         __syncthreads();
-        if (tid < kGlrCols && q.col * kGlrCols + tid < p.D) {
-            float t = s_a[0][tid];
+        if (mine) {
+            float t = s_a[0][wave * CH + lane];
 #pragma unroll
-            for (int v = 1; v < NW; ++v) t += s_a[v][tid];
-            p.part[((int64_t)q.chunk * p.B + q.b) * p.D + q.col * kGlrCols + tid] = t;
+            for (int v = 1; v < NW; ++v) t += s_a[v][wave * CH + lane];
+            p.part[(int64_t)q.chunk * BD + bd0 + lane] = t;
         }
         if constexpr (!LOOK) break;
+        tile = next;
     }
 }
 
@@ -721,13 +762,14 @@ hipError_t launch_glr_t(const LaunchGlr& p) {
         // runs of 16 tokens and two workgroups per CU where a row's two channels fit one register
         // (B 8, L 2048, D 5120, bf16: 162 us against 196 with 16 waves of 8 tokens), else runs of 8 (fp32, B 8,
         // L 2048, D 2560: 144 against 153)
-        constexpr int TT = sizeof(T) == 2 && VEC ? 16 : 8, NW = kGlrFwdChunk / TT;
+        constexpr int TT = sizeof(T) == 2 ? 16 : 8, NW = kGlrFwdChunk / TT;
         if (look) hipLaunchKernelGGL((k_glr_fwd<T, VEC, TT, NW, true>), grid, dim3(NW * 64), 0, st, a);
         else hipLaunchKernelGGL((k_glr_fwd<T, VEC, TT, NW, false>), grid, dim3(NW * 64), 0, st, a);
     } else {
-        const dim3 block(kGlrBwdWaves * 64);
-        if (look) hipLaunchKernelGGL((k_glr_bwd<T, VEC, kGlrBwdTokens, kGlrBwdWaves, true>), grid, block, 0, st, a);
-        else hipLaunchKernelGGL((k_glr_bwd<T, VEC, kGlrBwdTokens, kGlrBwdWaves, false>), grid, block, 0, st, a);
+        constexpr int TT = 16;
+        auto go = [&](auto kernel, int waves) { hipLaunchKernelGGL(kernel, grid, dim3((unsigned)waves * 64), 0, st, a); };
+        if (p.chunk == 64) look ? go(k_glr_bwd<T, VEC, TT, 64 / TT, true>, 64 / TT) : go(k_glr_bwd<T, VEC, TT, 64 / TT, false>, 64 / TT);
+        else look ? go(k_glr_bwd<T, VEC, TT, 128 / TT, true>, 128 / TT) : go(k_glr_bwd<T, VEC, TT, 128 / TT, false>, 128 / TT);
         hipLaunchKernelGGL(k_glr_da, dim3((unsigned)((p.D + 63) / 64)), dim3(1024), 0, st, p.part, p.g.dA,
                            p.nchunks * p.batch, (int)p.D);
     }

@@ -11,9 +11,10 @@ namespace selscan {
 
 constexpr int kGlrCols = 128;       // channels per workgroup of the recurrence kernels (2 per lane)
 constexpr int kGlrFwdChunk = 128;   // tokens of a forward chunk
-constexpr int kGlrBwdWaves = 8;
-constexpr int kGlrBwdTokens = 8;    // tokens per wave of the backward
-constexpr int kGlrBwdChunk = kGlrBwdWaves * kGlrBwdTokens;
+// Tokens of a backward chunk. With many rows of tiles the shorter one, whose four waves a CU has
+// twice (B 8, L 2048, D 5120, bf16: 313 us against 351 with 128); with few, half as many chunks
+// to wait for (B 1, L 65536, D 1024: 322 against 380).
+inline int64_t glr_bwd_chunk(int64_t B, int64_t D) { return B * ((D + kGlrCols - 1) / kGlrCols) >= 32 ? 64 : 128; }
 
 // One launch of the recurrence, already validated by the C-ABI layer.
 struct LaunchGlr {
@@ -24,7 +25,7 @@ struct LaunchGlr {
     ss_view x, r, i;
     const float* A; const uint8_t* reset; void* y; float* state; float* ckpt;
     ss_glr_grads g;
-    int64_t nchunks;             // chunks per batch row
+    int64_t chunk, nchunks;      // tokens of a chunk, chunks per batch row
     unsigned* ticket;            // workspace: next tile to take (several chunks only)
     uint64_t* slots;             // workspace: [nchunks, B, D] published chunk results (several chunks only)
     float* part;                 // workspace of the backward: [nchunks, B, D] parts of dA
