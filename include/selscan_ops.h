@@ -107,7 +107,9 @@ ss_status ss_glr_bwd(const ss_glr_dims* dims, const ss_glr_args* args, const ss_
  * infinity), and fp32 scales; it stands for scale * q. A scale covers 128 consecutive
  * columns of one row (scale [M, ceil(K/128)], activations) or of 128 consecutive rows
  * ("square": scale [ceil(M/128), ceil(K/128)], weights); blocks at the ends are smaller.
- *   scale = max(max |v| / 448, 2^-126),   q = e4m3(v / scale), to nearest, ties to even.
+ *   scale = max(max |v| / 448, 2^-126),   q = e4m3(v / scale), to nearest, ties to even
+ * (of the quotient itself, from 2^-6 on: it is not rounded to fp32 first, nor taken by the
+ * stored scale's rounding).
  * A NaN becomes a NaN and leaves its block's scale alone; an infinity makes its block's scale
  * infinite (its finite values stand for NaN then). All matrices are contiguous row-major. */
 typedef struct {

@@ -2,7 +2,7 @@
 // and the RMS norm (ss_norm_q8).
 //
 //   s = x + residual;  n = s / sqrt(mean(s^2) + eps) * w
-//   per block: scale = max(max |n| / 448, 2^-126),  q = e4m3(n / scale)
+//   per block: scale = max(max |n| / 448, 2^-126),  q = e4m3(n / scale), from the unrounded scale
 //
 // Both are bound by memory: a value is read once, kept in registers through the sums and
 // maxima it takes part in, and its byte is written once.
@@ -15,25 +15,57 @@ namespace selscan {
 constexpr float kQ8Max = 448.0f;             // largest finite e4m3 value
 constexpr float kQ8TinyScale = 0x1p-126f;    // smallest scale: its reciprocal is finite
 
-__device__ __forceinline__ float q8_scale(float top) { return __builtin_fmaxf(top / kQ8Max, kQ8TinyScale); }
-
-// four values times `inv` as four e4m3 bytes, each rounded to the nearest (ties to even)
-__device__ __forceinline__ uint32_t q8_pack(float a, float b, float c, float d, float inv) {
-    int v = __builtin_amdgcn_cvt_pk_fp8_f32(a * inv, b * inv, 0, false);
-    v = __builtin_amdgcn_cvt_pk_fp8_f32(c * inv, d * inv, v, true);
-    return (uint32_t)v;
+// A block's scale, and 448 / max |v| (2^126 under the smallest scale) as the sum of two floats.
+struct Q8Scale { float scale, hi, lo; };
+__device__ __forceinline__ Q8Scale q8_scale(float top) {
+    const float s = top / kQ8Max;
+    if (s < kQ8TinyScale) return Q8Scale{kQ8TinyScale, 0x1p126f, 0.0f};
+    const float hi = kQ8Max / top;
+    return Q8Scale{s, hi, __builtin_fmaf(-hi, top, kQ8Max) * (hi / kQ8Max)};
+}
+// v / scale where its side of an fp32 step counts: not rounded to nearest, but to the odd one of
+// the two fp32 neighbours where the quotient is between them.
+__device__ __forceinline__ float q8_odd(float v, const Q8Scale& s) {
+    const float t = v * s.hi;
+    const float rest = __builtin_fmaf(v, s.lo, __builtin_fmaf(v, s.hi, -t));
+    const int b = __builtin_bit_cast(int, t);
+    const int away = (__builtin_bit_cast(int, rest) ^ b) >> 31 | 1;       // towards the remainder: 1 away from 0, -1 back
+    return __builtin_bit_cast(float, (b & 1) || rest == 0.0f ? b : b + away);
+}
+// Eight values as eight e4m3 bytes, each quotient rounded to the nearest (ties to even). The
+// product with the rounded 448 / max |v| is within two fp32 steps of the quotient; where it is
+// that near to the middle between two e4m3 values (a few in a million), it may go to the wrong
+// one. From 2^-6 on the middles are the fp32 numbers whose last 20 bits are a one and zeros; a
+// wave that comes near one takes its values to odd, where no middle is met that is none.
+// (Below, where e4m3 has steps of 2^-9, it is left at that.)
+__device__ __forceinline__ bool q8_near_middle(const float* v, const Q8Scale& s) {
+    uint32_t least = ~0u;                          // last 20 bits, counted from two below a middle
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const uint32_t from = (__builtin_bit_cast(uint32_t, v[j] * s.hi) << 12) + 0x80002000u;
+        least = from < least ? from : least;
+    }
+    return least <= 0x4000u;
+}
+__device__ __forceinline__ uint64_t q8_eight(const float* v, const Q8Scale& s, bool odd) {
+    float t[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) t[j] = odd ? q8_odd(v[j], s) : v[j] * s.hi;
+    int a = __builtin_amdgcn_cvt_pk_fp8_f32(t[0], t[1], 0, false), b = __builtin_amdgcn_cvt_pk_fp8_f32(t[4], t[5], 0, false);
+    a = __builtin_amdgcn_cvt_pk_fp8_f32(t[2], t[3], a, true);
+    b = __builtin_amdgcn_cvt_pk_fp8_f32(t[6], t[7], b, true);
+    return (uint64_t)(uint32_t)b << 32 | (uint32_t)a;
 }
 
 typedef uint32_t q8_u4 __attribute__((ext_vector_type(4)));
-typedef uint32_t q8_u2 __attribute__((ext_vector_type(2)));
 typedef float q8_f4 __attribute__((ext_vector_type(4)));
 
 // Eight consecutive values of a row from column c on; zeros past the end. VEC: the row starts
-// on 16 bytes and K is a multiple of 8.
-template <typename T, bool VEC>
+// on 16 bytes and K is a multiple of 8. INSIDE: with VEC, c is known to be in the row.
+template <typename T, bool VEC, bool INSIDE = false>
 __device__ __forceinline__ void ld8(const T* row, int64_t c, int64_t K, float* v) {
     if constexpr (VEC) {
-        if (c >= K) {
+        if (!INSIDE && c >= K) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] = 0.0f;
         } else if constexpr (sizeof(T) == 2) {
@@ -76,14 +108,13 @@ __device__ __forceinline__ void st8(T* row, int64_t c, int64_t K, const float* v
 }
 
 template <bool VEC>
-__device__ __forceinline__ void st8_q(uint8_t* row, int64_t c, int64_t K, const float* v, float inv) {
-    const q8_u2 u{q8_pack(v[0], v[1], v[2], v[3], inv), q8_pack(v[4], v[5], v[6], v[7], inv)};
+__device__ __forceinline__ void st8_q(uint8_t* row, int64_t c, int64_t K, uint64_t u) {
     if constexpr (VEC) {
-        if (c < K) *reinterpret_cast<q8_u2*>(row + c) = u;
+        if (c < K) *reinterpret_cast<uint64_t*>(row + c) = u;
     } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            if (c + j < K) row[c + j] = (uint8_t)(u[j / 4] >> (8 * (j % 4)));
+            if (c + j < K) row[c + j] = (uint8_t)(u >> (8 * j));
     }
 }
 
@@ -168,9 +199,12 @@ k_q8_rows(const Q8Args p) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) o[j] = o[j] * rn * w[j];
         }
-        const float scale = q8_scale(top16(o));
-        st8_q<VEC>(p.q + row * p.K, c, p.K, o, 1.0f / scale);
-        if (lane % 16 == 0 && c < p.K) p.scale[row * p.KB + c / 128] = scale;
+        const Q8Scale scale = q8_scale(top16(o));
+        uint64_t u;
+        if (__any(q8_near_middle(o, scale))) u = q8_eight(o, scale, true);
+        else u = q8_eight(o, scale, false);
+        st8_q<VEC>(p.q + row * p.K, c, p.K, u);
+        if (lane % 16 == 0 && c < p.K) p.scale[row * p.KB + c / 128] = scale.scale;
     };
     if constexpr (NV > 0) {
 #pragma unroll
@@ -183,38 +217,50 @@ k_q8_rows(const Q8Args p) {
     }
 }
 
-// One 128 x 128 square per workgroup: 16 lanes across, 16 rows down, eight times.
+// One 128 x 128 square per workgroup: 16 lanes across, the rows in turn. Lanes past the last
+// row or column hold the last one instead, which leaves the largest magnitude as it is and the
+// loads without branches between them.
+constexpr int kSquareThreads = 512;
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kSquareThreads)
 k_q8_square(const Q8Args p) {
+    constexpr int DOWN = kSquareThreads / 16, N = 128 / DOWN;
     const int cx = threadIdx.x % 16 * 8, ry = threadIdx.x / 16;
     const int64_t c = (int64_t)blockIdx.x * 128 + cx, r0 = (int64_t)blockIdx.y * 128 + ry;
-    float v[8][8], top = 0.0f;
+    const int64_t held = VEC && c >= p.K ? p.K - 8 : c;
+    auto row = [&](int k) {
+        const int64_t r = r0 + DOWN * k;
+        return static_cast<const T*>(p.x) + (r < p.M ? r : p.M - 1) * p.K;
+    };
+    float v[N][8], top = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        const int64_t r = r0 + 16 * k;
-        if (r < p.M) {
-            ld8<T, VEC>(static_cast<const T*>(p.x) + r * p.K, c, p.K, v[k]);
-        } else {
+    for (int k = 0; k < N; ++k) ld8<T, VEC, true>(row(k), held, p.K, v[k]);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[k][j] = 0.0f;
-        }
-    }
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
+    for (int k = 0; k < N; ++k)
 #pragma unroll
         for (int j = 0; j < 8; ++j) top = __builtin_fmaxf(top, __builtin_fabsf(v[k][j]));
 #pragma unroll
     for (int o = 32; o >= 1; o >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, o, 64));
-    __shared__ float part[4];
+    __shared__ float part[kSquareThreads / 64];
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = top;
     __syncthreads();
-    top = __builtin_fmaxf(__builtin_fmaxf(part[0], part[1]), __builtin_fmaxf(part[2], part[3]));
-    const float scale = q8_scale(top), inv = 1.0f / scale;
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-        if (r0 + 16 * k < p.M) st8_q<VEC>(p.q + (r0 + 16 * k) * p.K, c, p.K, v[k], inv);
-    if (threadIdx.x == 0) p.scale[(int64_t)blockIdx.y * p.KB + blockIdx.x] = scale;
+    for (int k = 0; k < kSquareThreads / 64; ++k) top = __builtin_fmaxf(top, part[k]);
+    const Q8Scale scale = q8_scale(top);
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        const int64_t r = r0 + DOWN * k;
+        uint64_t u;
+        if (__any(q8_near_middle(v[k], scale))) {      // values taken again: few waves come here
+            float w[8];
+            ld8<T, VEC, true>(row(k), held, p.K, w);
+            u = q8_eight(w, scale, true);
+        } else {
+            u = q8_eight(v[k], scale, false);
+        }
+        if (r < p.M) st8_q<VEC>(p.q + r * p.K, c, p.K, u);
+    }
+    if (threadIdx.x == 0) p.scale[(int64_t)blockIdx.y * p.KB + blockIdx.x] = scale.scale;
 }
 
 template <typename T, bool VEC, bool NORM, bool RES>
@@ -242,7 +288,7 @@ template <typename T, bool VEC>
 hipError_t launch_q8_t(const LaunchQ8& p) {
     Q8Args a{p.x, p.res, p.w, p.q, p.scale, p.sum, p.M, p.K, (p.K + 127) / 128, p.eps};
     if (p.square) {
-        hipLaunchKernelGGL((k_q8_square<T, VEC>), dim3((unsigned)a.KB, (unsigned)((p.M + 127) / 128)), dim3(256), 0,
+        hipLaunchKernelGGL((k_q8_square<T, VEC>), dim3((unsigned)a.KB, (unsigned)((p.M + 127) / 128)), dim3(kSquareThreads), 0,
                            static_cast<hipStream_t>(p.stream), a);
         return hipGetLastError();
     }
