@@ -7,6 +7,7 @@
  *   ss_quant_q8                           rounding to 8-bit floating point with block scales
  *   ss_norm_q8                            the same behind a residual's addition and RMS norm
  *   ss_gemm_q8                            the product of two such matrices
+ *   ss_block_q8_fwd, ss_block_q8_step     the block around the scan with such projections
  *
  * Ownership, ordering, errors: as in selscan.h. Every pointer inside a struct is a DEVICE
  * pointer owned by the caller, arguments are validated on the host before anything is
@@ -158,6 +159,30 @@ typedef struct {
 } ss_gemm_q8_args;
 
 ss_status ss_gemm_q8(const ss_gemm_q8_dims* dims, const ss_gemm_q8_args* args, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The block around the scan (ss_block_fwd, ss_block_step) with its input and output
+ * projections as 8-bit products: RMSNorm(x) and the scan's output y are rounded in blocks of
+ * 1 x 128, W_in [2 Di, d_model] and W_out [d_model, Di] are e4m3 with scales of 128 x 128 (as
+ * ss_quant_q8 with square = 1 makes them). Everything else, and the types of x, out, W_x, W_dt
+ * and the states, is as there. d_model and d_inner are multiples of 16. */
+typedef struct {
+    ss_block_weights w;     /* W_in and W_out point to e4m3 bytes, 16-byte aligned          */
+    const float* S_in;      /* [ceil(2 Di/128), ceil(d_model/128)]                          */
+    const float* S_out;     /* [ceil(d_model/128), ceil(Di/128)]                            */
+} ss_block_q8_weights;
+
+/* Bytes of workspace; 0 for invalid sizes. */
+size_t ss_block_q8_workspace_bytes(const ss_block_dims* dims, int step);
+
+/* x, out [B,L,d_model]; states as for ss_block_fwd (NULL: zero, not returned). out may be x
+ * (in place); nothing else that is written may overlap anything. */
+ss_status ss_block_q8_fwd(const ss_block_dims* dims, const ss_block_q8_weights* weights, const void* x, void* out,
+                          float* ssm_state, float* conv_state, void* workspace, size_t workspace_bytes, void* stream);
+
+/* One token of each stream: x, out [B,d_model]; both states required and updated. */
+ss_status ss_block_q8_step(const ss_block_dims* dims, const ss_block_q8_weights* weights, const void* x, void* out,
+                           float* ssm_state, float* conv_state, void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -6,7 +6,11 @@ shares no code with it.
 """
 from __future__ import annotations
 
+import numpy as np
 import torch
+
+from . import block as _block
+from . import default as _default
 
 F64 = torch.float64
 
@@ -124,3 +128,35 @@ def half_step(v, scale):
     """Half the distance of neighbouring e4m3 values at v / scale, times scale: 2^-4 of |v| at
     most, 2^-10 scale below the smallest normal value."""
     return torch.maximum(v.abs() * 2.0 ** -4, scale * 2.0 ** -10)
+
+
+# ---------------------------------------------------------------------------
+# the block with 8-bit projections, in pieces that a rounding separates
+
+def block_core(xi, z, W, R, ssm_state, conv_state, zoh=False):
+    """From the input projection's two halves [B,L,Di] to the scan's output, as in the block:
+    (y [B,L,Di], final ssm_state [B,Di,N], final conv_state [B,Di,3]), numpy float64. W: the
+    block's weights as numpy arrays; states as such or None."""
+    N = W["A"].shape[1]
+    u, cs = _block.conv_silu(xi, W["conv_w"], W["conv_b"], conv_state)
+    xp = u @ np.asarray(W["W_x"], np.float64).T
+    dr, Bm, Cm = xp[..., :R], xp[..., R:R + N], xp[..., R + N:]
+    delta = dr @ np.asarray(W["W_dt"], np.float64).T
+    h0 = np.zeros((xi.shape[0], xi.shape[2], N)) if ssm_state is None else ssm_state
+    y, hs, _ = _default().conv_scan_fwd(u, delta, W["A"], Bm, Cm, delta_bias=W["dt_bias"], D=W["D"], z=z, ssm_state=h0,
+                                             zoh=zoh)
+    return y, hs, cs
+
+
+def rounded_product(y, slack, wq, ws, out_half):
+    """(y W^T, how far the 8-bit product of y may be from it), element by element, for y [M,K]
+    (64-bit) known to +-slack [M,K] before it is rounded to 8 bits: half a step (taken from the
+    true value: slack once more covers the difference) for each value, then fp32 sums of K terms,
+    and for a 16-bit output (out_half > 2^-24) the small terms the matrix cores drop beside
+    large ones, 2^-10 of the terms' sizes; the output's own rounding is the caller's."""
+    w = values(wq, ws, square=True).abs()
+    y = torch.as_tensor(y, dtype=F64)
+    per = spread(block_tops(y) / Q8_MAX, *y.shape).clamp_min(Q8_TINY)
+    off = half_step(y, per) + 2 * torch.as_tensor(slack, dtype=F64)
+    sums = 2.0 ** -15 + (2.0 ** -10 if out_half > 2.0 ** -24 else 0.0)
+    return y @ values(wq, ws, square=True).T, off @ w.T + sums * ((y.abs() + off) @ w.T)

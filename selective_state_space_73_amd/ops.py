@@ -16,7 +16,8 @@ from typing import Optional
 
 import torch
 
-from . import LIB_PATH, SS_BF16, SS_F32, SelscanError, lib
+from . import (LIB_PATH, SS_BF16, SS_EULER, SS_F32, SS_ZOH, SelscanError, block_dims, lib, ss_block_dims,
+               ss_block_weights)
 
 GLR_CKPT = 64    # SS_GLR_CKPT
 Q8_BLOCK = 128   # columns that share a scale
@@ -61,6 +62,10 @@ class ss_gemm_q8_args(ctypes.Structure):
     _fields_ = [(n, _vp) for n in ("xq", "xs", "wq", "ws", "residual", "y")]
 
 
+class ss_block_q8_weights(ctypes.Structure):
+    _fields_ = [("w", ss_block_weights), ("S_in", _vp), ("S_out", _vp)]
+
+
 def _declare():
     P = ctypes.POINTER
     lib.ss_glr_workspace_bytes.argtypes = [P(ss_glr_dims), ctypes.c_int]
@@ -71,7 +76,12 @@ def _declare():
     lib.ss_quant_q8.argtypes = [P(ss_q8_dims), _vp, _vp, _vp, _vp]
     lib.ss_norm_q8.argtypes = [P(ss_q8_dims), P(ss_norm_q8_args), _vp]
     lib.ss_gemm_q8.argtypes = [P(ss_gemm_q8_dims), P(ss_gemm_q8_args), _vp]
-    for name in ("ss_glr_fwd", "ss_glr_step", "ss_glr_bwd", "ss_quant_q8", "ss_norm_q8", "ss_gemm_q8"):
+    lib.ss_block_q8_workspace_bytes.argtypes = [P(ss_block_dims), ctypes.c_int]
+    lib.ss_block_q8_workspace_bytes.restype = ctypes.c_size_t
+    block = [P(ss_block_dims), P(ss_block_q8_weights), _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]
+    lib.ss_block_q8_fwd.argtypes = lib.ss_block_q8_step.argtypes = block
+    for name in ("ss_glr_fwd", "ss_glr_step", "ss_glr_bwd", "ss_quant_q8", "ss_norm_q8", "ss_gemm_q8", "ss_block_q8_fwd",
+                 "ss_block_q8_step"):
         getattr(lib, name).restype = ctypes.c_int
 
 
@@ -388,6 +398,80 @@ def ss_gemm_q8(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: torch.T
     return out
 
 
+# ---------------------------------------------------------------------------
+# the block with 8-bit projections
+
+def block_q8_weights(W: dict, *, stream=None) -> dict:
+    """The block's weights with its two wide projections rounded to 8 bits: W as ss_block_fwd
+    takes it (BLOCK_WEIGHTS) -> a dict whose W_in and W_out are float8_e4m3fn and whose S_in
+    and S_out hold their scales; the other entries are W's own tensors. Done once per model."""
+    out = dict(W)
+    for name, scale in (("W_in", "S_in"), ("W_out", "S_out")):
+        out[name], out[scale] = ss_quant_q8(W[name], square=True, stream=stream)
+    return out
+
+
+def ss_block_q8_workspace_bytes(dims: ss_block_dims, step: bool = False) -> int:
+    return int(lib.ss_block_q8_workspace_bytes(ctypes.byref(dims), int(bool(step))))
+
+
+def _block_q8(step, x, W, dt_rank, ssm_state, conv_state, out, workspace, norm_eps, zoh, stream):
+    idx = _gpu(x, "x")
+    if _elsewhere(idx, stream):
+        with _placed(idx, stream):
+            return _block_q8(step, x, W, dt_rank, ssm_state, conv_state, out, workspace, norm_eps, zoh, None)
+    if x.dim() != (2 if step else 3):
+        raise ValueError("x must be [streams, d_model]" if step else "x must be [batch, seqlen, d_model]")
+    io, shape = x.dtype, x.shape
+    B, L, dm = shape[0], 1 if step else shape[1], shape[-1]
+    if W["W_in"].dim() != 2 or W["A"].dim() != 2:
+        raise ValueError("W_in must be [2 d_inner, d_model] and A [d_inner, d_state]")
+    di, N, R = W["W_in"].shape[0] // 2, W["A"].shape[1], dt_rank
+    KM, KI = -(-dm // Q8_BLOCK), -(-di // Q8_BLOCK)
+    dims = block_dims(B, L, dm, di, N, R, _io(x, "x"), norm_eps, SS_ZOH if zoh else SS_EULER)
+
+    def given(name, shape, dtype, key=None):
+        return _same(W[key or name], shape, dtype, idx, name)
+
+    def maybe(name, shape, key=None):
+        return _opt(W.get(key or name), shape, _F32, idx, name)
+
+    w = ss_block_q8_weights(ss_block_weights(
+        norm_w=given("norm_w", (dm,), _F32), W_in=given("W_in", (2 * di, dm), _Q8), conv_w=given("conv_w", (di, 4), _F32),
+        conv_b=maybe("conv_b", (di,)), W_x=given("W_x", (R + 2 * N, di), io), W_dt=given("W_dt", (di, R), io),
+        dt_bias=maybe("dt_bias", (di,)), A=given("A", (di, N), _F32), Dskip=maybe("D", (di,)),
+        W_out=given("W_out", (dm, di), _Q8)),
+        given("S_in", (-(-2 * di // Q8_BLOCK), KM), _F32), given("S_out", (KM, KI), _F32))
+    xp = _same(x, shape, io, idx, "x")
+    if out is None:
+        out = x.new_empty(shape)
+    keep, ws, ws_bytes = _workspace(workspace, ss_block_q8_workspace_bytes(dims, step), x)
+    fn = lib.ss_block_q8_step if step else lib.ss_block_q8_fwd
+    _check(fn(ctypes.byref(dims), ctypes.byref(w), xp, _same(out, shape, io, idx, "out"),
+              _opt(ssm_state, (B, di, N), _F32, idx, "ssm_state") or None,
+              _opt(conv_state, (B, di, 3), _F32, idx, "conv_state") or None, ws, ws_bytes, _stream_of(idx)))
+    return out
+
+
+def ss_block_q8_fwd(x: torch.Tensor, W: dict, dt_rank: int, *, ssm_state: Optional[torch.Tensor] = None,
+                    conv_state: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None, norm_eps: float = 1e-5, zoh: bool = False,
+                    stream=None) -> torch.Tensor:
+    """ss_block_fwd with 8-bit input and output projections: x [B,L,d_model] (float32 or
+    bfloat16, contiguous) -> out, same shape; W from block_q8_weights; d_model and d_inner
+    multiples of 16. States float32, read and updated when given; out may be x. Asynchronous."""
+    return _block_q8(False, x, W, dt_rank, ssm_state, conv_state, out, workspace, norm_eps, zoh, stream)
+
+
+def ss_block_q8_step(x: torch.Tensor, W: dict, dt_rank: int, ssm_state: torch.Tensor, conv_state: torch.Tensor, *,
+                     out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                     norm_eps: float = 1e-5, zoh: bool = False, stream=None) -> torch.Tensor:
+    """One token per stream through the block with 8-bit projections: x [S,d_model] -> out
+    [S,d_model]; both states required and updated in place."""
+    return _block_q8(True, x, W, dt_rank, ssm_state, conv_state, out, workspace, norm_eps, zoh, stream)
+
+
 __all__ = ["GLR_CKPT", "ss_glr_dims", "ss_view", "ss_glr_args", "ss_glr_grads", "glr_ckpt_shape",
            "ss_glr_workspace_bytes", "ss_glr_fwd", "ss_glr_step", "ss_glr_bwd", "Q8_BLOCK", "ss_q8_dims",
-           "ss_norm_q8_args", "ss_gemm_q8_dims", "ss_gemm_q8_args", "ss_quant_q8", "ss_norm_q8", "ss_gemm_q8"]
+           "ss_norm_q8_args", "ss_gemm_q8_dims", "ss_gemm_q8_args", "ss_quant_q8", "ss_norm_q8", "ss_gemm_q8",
+           "ss_block_q8_weights", "block_q8_weights", "ss_block_q8_workspace_bytes", "ss_block_q8_fwd", "ss_block_q8_step"]

@@ -209,3 +209,69 @@ def test_binding_refuses_host_operands():
                  lambda: ss.ss_gemm_q8(t.to(torch.float8_e4m3fn), t, t.to(torch.float8_e4m3fn), t)):
         with pytest.raises(ValueError):
             call()
+
+
+# ---------------------------------------------------------------------------
+# the block with 8-bit projections
+
+WEIGHTS = ("norm_w", "W_in", "conv_w", "conv_b", "W_x", "W_dt", "dt_bias", "A", "Dskip", "W_out")
+
+
+def bdims(**kw):
+    d = dict(batch=2, seqlen=16, d_model=64, d_inner=128, d_state=16, d_conv=4, dt_rank=4, io_dtype=ss.SS_F32,
+             discretization=ss.SS_EULER, norm_eps=1e-5)
+    d.update(kw)
+    return ss.ss_block_dims(*d.values())
+
+
+def bcall(dims=None, step=False, ws=WS, ws_bytes=None, weights=True, **kw):
+    dims = dims or bdims()
+    w = {n: BASE + k * GAP for k, n in enumerate(WEIGHTS)}
+    o = dict(S_in=BASE + 20 * GAP, S_out=BASE + 21 * GAP, x=BASE + 22 * GAP, out=BASE + 23 * GAP, h=BASE + 24 * GAP, c=BASE + 25 * GAP)
+    for k, v in kw.items():
+        (w if k in w else o)[k] = v
+    q = ss.ss_block_q8_weights(ss.ss_block_weights(*w.values()), o["S_in"], o["S_out"])
+    need = ss.ss_block_q8_workspace_bytes(dims, step) if ws_bytes is None else ws_bytes
+    fn = ss.lib.ss_block_q8_step if step else ss.lib.ss_block_q8_fwd
+    return fn(ctypes.byref(dims), ctypes.byref(q) if weights else None, o["x"], o["out"], o["h"], o["c"], ws, need, None)
+
+
+@pytest.mark.parametrize("step", [False, True])
+def test_block_refusals(step):
+    for kw, status in [(dict(batch=0), 1), (dict(d_model=0), 1), (dict(d_inner=0), 1), (dict(dt_rank=0), 1), (dict(d_model=72), 2),
+                       (dict(d_inner=136), 2), (dict(d_state=12), 2), (dict(d_conv=3), 2), (dict(io_dtype=2), 2), (dict(norm_eps=0.0), 1),
+                       (dict(norm_eps=float("nan")), 1), (dict(discretization=7), None), (dict(dt_rank=5000), 1),
+                       (dict(d_inner=1 << 24), 1), (dict(d_model=1 << 21), 1), (dict(batch=1 << 31), 1)]:
+        got = bcall(bdims(**kw), step, ws_bytes=1 << 40)
+        assert got == status if status else got != 0, kw
+        assert ss.ss_block_q8_workspace_bytes(bdims(**kw), step) == 0, kw
+    assert bcall(step=step, weights=False) == 1
+    for n in ("norm_w", "W_in", "conv_w", "W_x", "W_dt", "A", "W_out", "S_in", "S_out", "x", "out"):
+        assert bcall(step=step, **{n: None}) == 1 and n in last(), n
+    for n, at in [("W_in", 8), ("W_x", 8), ("W_dt", 8), ("W_out", 8), ("S_in", 2), ("S_out", 2), ("norm_w", 2), ("conv_w", 2), ("A", 2),
+                  ("x", 8), ("out", 8), ("h", 8), ("c", 2), ("conv_b", 2), ("dt_bias", 2), ("Dskip", 2)]:
+        assert bcall(step=step, **{n: BASE + 30 * GAP + at}) == 1 and "aligned" in last(), n
+    for a, b in [("out", "x"), ("out", "W_in"), ("out", "S_out"), ("h", "x"), ("h", "out"), ("c", "h"), ("c", "A"), ("h", "conv_b")]:
+        at = {n: BASE + k * GAP for k, n in enumerate(WEIGHTS)}
+        at.update(S_in=BASE + 20 * GAP, S_out=BASE + 21 * GAP, x=BASE + 22 * GAP, out=BASE + 23 * GAP, h=BASE + 24 * GAP)
+        assert bcall(step=step, **{a: at[b] - 16}) == 1 and "overlaps" in last(), (a, b)
+    need = ss.ss_block_q8_workspace_bytes(bdims(), step)
+    assert bcall(step=step, ws_bytes=need - 1) == 3 and bcall(step=step, ws=None) == 3
+    assert bcall(step=step, ws=WS + 128) == 1
+    assert bcall(step=step, ws=BASE + 22 * GAP) == 1 and "workspace overlaps x" in last()
+
+
+def test_block_step_needs_states_and_workspace_holds_everything():
+    assert bcall(step=True, h=None) == 1 and bcall(step=True, c=None) == 1
+    a = lambda v: (v + 255) // 256 * 256  # noqa: E731
+    M, dm, di, R, N = 32, 64, 128, 4, 16
+    want = a(M * dm) + a(M * 4) + 5 * a(M * di * 4) + a(M * R * 4) + 2 * a(M * N * 4) + a(M * di) + a(M * 4)
+    assert ss.ss_block_q8_workspace_bytes(bdims()) == want
+    assert ss.ss_block_q8_workspace_bytes(bdims(seqlen=0)) == 0 and ss.ss_block_q8_workspace_bytes(bdims(seqlen=0), True) > 0
+
+
+def test_block_binding_refuses_host_operands():
+    with pytest.raises(ValueError):
+        ss.ss_block_q8_fwd(torch.zeros(1, 2, 32), {}, 2)
+    with pytest.raises(ValueError):
+        ss.block_q8_weights({"W_in": torch.zeros(64, 32), "W_out": torch.zeros(32, 32)})

@@ -73,3 +73,40 @@ def test_recurrence_pieces_and_resets():
     yc, _, _ = O.glr_fwd(c, c, c, torch.tensor([-0.5], dtype=F64), torch.ones(1, 1, dtype=F64))
     want = torch.exp(-0.25 * torch.arange(1, 7, dtype=F64))
     assert torch.allclose(yc[0, :, 0], want, rtol=1e-14)
+
+
+# ---------------------------------------------------------------------------
+# the block in pieces
+
+@pytest.mark.parametrize("states", [False, True])
+def test_block_core_is_the_block_between_its_projections(states):
+    import workloads as W
+    from oracle import block as ob
+    spec = W.BlockSpec("core", 2, 9, 32, d_state=8, dt_rank=3, io_dtype="f32", seed=5)
+    w, x, di = W.gen_block_weights(spec), W.gen_block_input(spec), spec.d_inner
+    st = W.gen_states(2, di, 8, seed=3)
+    st = (st["ssm_state"], st["conv_state"]) if states else (None, None)
+    p = ob.rms_norm(x, w["norm_w"]) @ w["W_in"].T.astype("float64")
+    y, h, c = O.block_core(p[..., :di], p[..., di:], w, 3, *st)
+    out, hr, cr = ob.block_forward(x, w, 3, *st)
+    assert abs(x + y @ w["W_out"].T.astype("float64") - out).max() < 1e-12
+    assert abs(h - hr).max() < 1e-12 and abs(c - cr).max() < 1e-12
+
+
+def test_rounded_product_bound_holds_and_is_tight():
+    """The bound covers torch's rounding of a disturbed y, and with an identity it is no more
+    than a tenth above what values at midpoints reach."""
+    g = torch.Generator().manual_seed(4)
+    y = torch.randn(6, 256, generator=g).double()
+    slack = 1e-5 * torch.ones_like(y)
+    for w in (torch.eye(256), torch.randn(40, 256, generator=g)):
+        top = (O.block_tops(w, True) / O.Q8_MAX).clamp_min(O.Q8_TINY)
+        wq = (w.double() / O.spread(top, *w.shape, square=True)).float().to(torch.float8_e4m3fn)
+        want, off = O.rounded_product(y, slack, wq, top, 2.0 ** -24)
+        z = y + slack * (2 * torch.rand(y.shape, generator=g).double() - 1)
+        s = (O.block_tops(z) / O.Q8_MAX).clamp_min(O.Q8_TINY)
+        zq = (z / O.spread(s, *z.shape)).float().to(torch.float8_e4m3fn)
+        err = (O.values(zq, s) @ O.values(wq, top, square=True).T - want).abs()
+        assert (err <= off).all()
+        if w.shape[0] == 256:
+            assert (err / off).max() > 0.9
