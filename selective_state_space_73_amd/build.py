@@ -27,6 +27,9 @@ HEADERS = [os.path.join(CSRC, "selscan_device.h"), os.path.join(CSRC, "selscan_b
 OPS_UNITS = sorted(glob.glob(os.path.join(CSRC, "ops_*.hip")))
 OPS_SOURCES = OPS_UNITS + sorted(glob.glob(os.path.join(CSRC, "ops_*.cpp")))
 OPS_HEADERS = sorted(glob.glob(os.path.join(CSRC, "ops_*.h"))) + [os.path.join(INCLUDE, "selscan_ops.h")]
+# the operators' Python binding, a C extension against torch (host code, compiled by g++)
+BINDING = os.path.join(CSRC, "binding.cpp")
+BINDING_LIB = os.path.join(PKG, "_binding.so")
 LIBS = []
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -59,13 +62,25 @@ def kernel_digest() -> str:
     return h.hexdigest()
 
 
+def binding_commands(obj: str, out: str) -> tuple:
+    """The binding's compile command, and the link against libselscan.so next to it."""
+    import sysconfig
+
+    from torch.utils.cpp_extension import include_paths, library_paths
+    inc = [f for p in [*include_paths(), "/opt/rocm/include", sysconfig.get_paths()["include"]] for f in ("-isystem", p)]
+    return (["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1", "-I", INCLUDE, *inc,
+             "-c", BINDING, "-o", obj],
+            ["g++", "-shared", "-o", out, obj, "-L", PKG, "-lselscan", "-Wl,-rpath,$ORIGIN",
+             *[f for p in library_paths() for f in ("-L", p)], "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch", "-ltorch_python"])
+
+
 OBJDIR = os.path.join(PKG, "_build")
 RESOURCES = os.path.join(OBJDIR, "kernel_resources.txt")
 
 
 def build(verbose: bool = False, jobs: int = 0) -> str:
     """Compile every source (in parallel) and link libselscan.so next to this file.
-    Always rebuilds. The compiler's per-kernel resource report (registers, scratch,
+    Always rebuilds (the operators' binding, _binding.so, as well). The compiler's per-kernel resource report (registers, scratch,
     spills, occupancy) of the kernel units is kept in _build/kernel_resources.txt."""
     os.makedirs(OBJDIR, exist_ok=True)
     cmds, objs = [], []
@@ -83,6 +98,8 @@ def build(verbose: bool = False, jobs: int = 0) -> str:
         obj = os.path.join(OBJDIR, os.path.basename(src) + ".o")
         cmds.append([HIPCC, *COMMON, *DEVICE_FLAGS, "-c", src, "-o", obj])
         probe_objs.append(obj)
+    binding, link_binding = binding_commands(os.path.join(OBJDIR, "binding.cpp.o"), BINDING_LIB + ".tmp")
+    cmds.append(binding)
     jobs = jobs or min(len(cmds), os.cpu_count() or 1, 16)
     with ThreadPoolExecutor(max_workers=jobs) as ex:
         reports = [r.stderr for r in ex.map(_run, cmds)]
@@ -94,6 +111,8 @@ def build(verbose: bool = False, jobs: int = 0) -> str:
     tmp = PROBE_LIB + ".tmp"
     _run([HIPCC, "-shared", "-fPIC", f"--offload-arch={ARCH}", "-o", tmp, *probe_objs])
     os.replace(tmp, PROBE_LIB)
+    _run(link_binding)
+    os.replace(BINDING_LIB + ".tmp", BINDING_LIB)
     return LIB
 
 
@@ -117,10 +136,10 @@ def kernel_resources(path: str = RESOURCES) -> dict:
 
 
 def is_stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING_LIB):
         return True
-    t = os.path.getmtime(LIB)
-    return any(os.path.getmtime(s) > t for s in SOURCES + HEADERS + OPS_SOURCES + OPS_HEADERS)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING_LIB))
+    return any(os.path.getmtime(s) > t for s in SOURCES + HEADERS + OPS_SOURCES + OPS_HEADERS + [BINDING])
 
 
 if __name__ == "__main__":

@@ -2,7 +2,8 @@
 
 Argument marshalling only, as for the scan: tensors are checked for device, dtype, shape and
 layout, their data pointers and torch's current HIP stream are passed to the C ABI, and the
-computation runs in the library's HIP kernels. Every call runs on the device of its tensors,
+computation runs in the library's HIP kernels. For the recurrence and the 8-bit calls, of which
+a decode step makes many small ones, that is done by the C extension csrc/binding.cpp. Every call runs on the device of its tensors,
 whichever is current. With an explicit ``stream`` the outputs and the workspace are allocated
 on that stream; the caller orders it against the streams that made the inputs and that use
 the outputs.
@@ -11,13 +12,14 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
-import struct
 from typing import Optional
 
 import torch
 
-from . import (LIB_PATH, SS_BF16, SS_EULER, SS_F32, SS_ZOH, SelscanError, block_dims, lib, ss_block_dims,
+from . import (SS_BF16, SS_EULER, SS_F32, SS_ZOH, SelscanError, block_dims, lib, ss_block_dims,
                ss_block_weights)
+from ._binding import gemm as _gemm, glr_bwd as _glr_bwd, glr_fwd as _glr_fwd, glr_step as _glr_step
+from ._binding import norm as _norm, quant as _quant
 
 GLR_CKPT = 64    # SS_GLR_CKPT
 Q8_BLOCK = 128   # columns that share a scale
@@ -26,6 +28,8 @@ _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
 _F32 = torch.float32
 _Q8 = torch.float8_e4m3fn
+_stream_of = torch._C._cuda_getCurrentRawStream
+_current = torch._C._cuda_getDevice
 
 
 class ss_glr_dims(ctypes.Structure):
@@ -88,40 +92,16 @@ def _declare():
 _declare()
 
 
-# What a call costs on the host is time a decode step waits for, so the calls below build
-# their argument structs with struct.pack (the layouts above, "P" a pointer, 0 for NULL) and
-# pass the bytes: about a third of the time of filling ctypes structures. The C calls copy
-# what they need before they return.
-_raw = ctypes.CDLL(LIB_PATH)
-_bytes, _size = ctypes.c_char_p, ctypes.c_size_t
-for _name, _args in (("ss_glr_fwd", [_bytes, _bytes, _vp, _size, _vp]), ("ss_glr_step", [_bytes, _bytes, _vp]),
-                     ("ss_glr_bwd", [_bytes, _bytes, _bytes, _vp, _size, _vp]), ("ss_quant_q8", [_bytes, _vp, _vp, _vp, _vp]),
-                     ("ss_norm_q8", [_bytes, _bytes, _vp]), ("ss_gemm_q8", [_bytes, _bytes, _vp])):
-    getattr(_raw, _name).argtypes, getattr(_raw, _name).restype = _args, ctypes.c_int
-_raw.ss_glr_workspace_bytes.argtypes, _raw.ss_glr_workspace_bytes.restype = [_bytes, ctypes.c_int], _size
-
-
-def _packer(fmt: str, cls):
-    s = struct.Struct(fmt)
-    assert s.size == ctypes.sizeof(cls), cls
-    return s.pack
-
-
-_pack_glr_dims = _packer("qqqii", ss_glr_dims)
-_pack_glr_args = _packer("PqqPqqPqqPPPPP", ss_glr_args)
-_pack_glr_grads = _packer("PPPPPPP", ss_glr_grads)
-_pack_q8_dims = _packer("qqiifi", ss_q8_dims)
-_pack_norm_args = _packer("PPPPPP", ss_norm_q8_args)
-_pack_gemm_dims = _packer("qqqii", ss_gemm_q8_dims)
-_pack_gemm_args = _packer("PPPPPP", ss_gemm_q8_args)
-
-_stream_of = torch._C._cuda_getCurrentRawStream
-_current = torch._C._cuda_getDevice
-
-
 def _check(status: int):
     if status != 0:
         raise SelscanError(status, lib.ss_last_error().decode())
+
+
+def _done(result):
+    """A binding call's result; an int is the status of a refused call."""
+    if type(result) is int:
+        _check(result)
+    return result
 
 
 def _io(t: torch.Tensor, name: str) -> int:
@@ -192,31 +172,6 @@ def _workspace(given: Optional[torch.Tensor], need: int, like: torch.Tensor):
 # ---------------------------------------------------------------------------
 # gated linear recurrence
 
-def _view(t: torch.Tensor, shape, dtype, idx: int, name: str) -> tuple:
-    """(pointer, batch stride, token stride) of a view whose channels are contiguous."""
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != idx:
-        _wrong(t, shape, dtype, idx, name)
-    st = t.stride()
-    if st[-1] != 1 and shape[-1] > 1:
-        raise ValueError(f"{name}: channels must be contiguous (last stride 1)")
-    return t.data_ptr(), st[0], st[1]
-
-
-def _glr_reset(reset: Optional[torch.Tensor], shape, idx: int) -> int:
-    if reset is None:
-        return 0
-    return _same(reset, shape, torch.bool if reset.dtype is torch.bool else torch.uint8, idx, "reset")
-
-
-def _glr_pack(x, r, i, A, reset, y, state, ckpt, shape, idx) -> bytes:
-    dt, B, D = x.dtype, shape[0], shape[-1]
-    return _pack_glr_args(
-        *_view(x, shape, dt, idx, "x"), *_view(r, shape, dt, idx, "r"), *_view(i, shape, dt, idx, "i"),
-        _same(A, (D,), _F32, idx, "A"), _glr_reset(reset, shape[:-1], idx), _opt(y, shape, dt, idx, "y"),
-        _opt(state, (B, D), _F32, idx, "state"),
-        0 if ckpt is None else _same(ckpt, glr_ckpt_shape(B, shape[1], D), _F32, idx, "ckpt"))
-
-
 def glr_ckpt_shape(batch: int, seqlen: int, d: int) -> tuple:
     """Shape of the recurrence's checkpoints (float32): the state before every 64th token."""
     return (batch, -(-seqlen // GLR_CKPT), d)
@@ -239,40 +194,20 @@ def ss_glr_fwd(x: torch.Tensor, r: torch.Tensor, i: torch.Tensor, A: torch.Tenso
     (zero initial state otherwise); reset [B,L] uint8 or bool: a_t = 0 at its nonzero tokens,
     where a new document starts; ckpt: float32 tensor of glr_ckpt_shape that receives the
     checkpoints ss_glr_bwd needs. Returns y [B,L,D] in the I/O dtype. Asynchronous."""
-    idx = _gpu(x, "x")
-    if _elsewhere(idx, stream):
-        with _placed(idx, stream):
+    if stream is not None:
+        with _placed(_gpu(x, "x"), stream):
             return ss_glr_fwd(x, r, i, A, state=state, reset=reset, ckpt=ckpt, y=y, workspace=workspace)
-    if x.dim() != 3:
-        raise ValueError("x must be [batch, seqlen, d]")
-    B, L, D = shape = x.shape
-    dims = _pack_glr_dims(B, L, D, _io(x, "x"), 0)
-    if y is None:
-        y = x.new_empty(shape)
-    args = _glr_pack(x, r, i, A, reset, y, state, ckpt, shape, idx)
-    keep, ws, ws_bytes = _workspace(workspace, _raw.ss_glr_workspace_bytes(dims, 0), x)
-    _check(_raw.ss_glr_fwd(dims, args, ws, ws_bytes, _stream_of(idx)))
-    return y
+    return _done(_glr_fwd(x, r, i, A, state, reset, ckpt, y, workspace))
 
 
 def ss_glr_step(x: torch.Tensor, r: torch.Tensor, i: torch.Tensor, A: torch.Tensor, state: torch.Tensor, *,
                 reset: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """One token of each stream: x, r, i [S,D] (rows at any stride); state [S,D] float32,
     updated in place; reset [S]. Returns y [S,D]."""
-    idx = _gpu(x, "x")
-    if _elsewhere(idx, stream):
-        with _placed(idx, stream):
+    if stream is not None:
+        with _placed(_gpu(x, "x"), stream):
             return ss_glr_step(x, r, i, A, state, reset=reset, y=y)
-    if x.dim() != 2:
-        raise ValueError("x must be [streams, d]")
-    shape = x.shape
-    if y is None:
-        y = x.new_empty(shape)
-    if state is None:
-        raise ValueError("state is required")
-    args = _glr_pack(x, r, i, A, reset, y, state, None, shape, idx)
-    _check(_raw.ss_glr_step(_pack_glr_dims(shape[0], 1, shape[1], _io(x, "x"), 0), args, _stream_of(idx)))
-    return y
+    return _done(_glr_step(x, r, i, A, state, reset, y))
 
 
 def ss_glr_bwd(x: torch.Tensor, r: torch.Tensor, i: torch.Tensor, A: torch.Tensor, ckpt: torch.Tensor,
@@ -283,37 +218,15 @@ def ss_glr_bwd(x: torch.Tensor, r: torch.Tensor, i: torch.Tensor, A: torch.Tenso
     is the initial state). dy [B,L,D] in the I/O dtype, dstate_final [B,D] float32 the
     gradient of the returned state. Returns a dict of new tensors: dx, dr, di (I/O dtype), dA
     [D] and dstate_init [B,D] (float32). Asynchronous."""
-    idx = _gpu(x, "x")
-    if _elsewhere(idx, stream):
-        with _placed(idx, stream):
+    if stream is not None:
+        with _placed(_gpu(x, "x"), stream):
             return ss_glr_bwd(x, r, i, A, ckpt, dy, reset=reset, dstate_final=dstate_final, workspace=workspace)
-    if x.dim() != 3:
-        raise ValueError("x must be [batch, seqlen, d]")
-    if ckpt is None:
-        raise ValueError("ckpt is required")
-    B, L, D = shape = x.shape
-    dt = x.dtype
-    dims = _pack_glr_dims(B, L, D, _io(x, "x"), 0)
-    args = _glr_pack(x, r, i, A, reset, None, None, ckpt, shape, idx)
-    dx, dr, di = x.new_empty(shape), x.new_empty(shape), x.new_empty(shape)
-    dA, dh = A.new_empty(D), A.new_empty((B, D))
-    grads = _pack_glr_grads(_same(dy, shape, dt, idx, "dy"), _opt(dstate_final, (B, D), _F32, idx, "dstate_final"),
-                            dx.data_ptr(), dr.data_ptr(), di.data_ptr(), dA.data_ptr(), dh.data_ptr())
-    keep, ws, ws_bytes = _workspace(workspace, _raw.ss_glr_workspace_bytes(dims, 1), x)
-    _check(_raw.ss_glr_bwd(dims, args, grads, ws, ws_bytes, _stream_of(idx)))
-    return {"dx": dx, "dr": dr, "di": di, "dA": dA, "dstate_init": dh}
+    return dict(zip(("dx", "dr", "di", "dA", "dstate_init"),
+                    _done(_glr_bwd(x, r, i, A, ckpt, dy, reset, dstate_final, workspace))))
 
 
 # ---------------------------------------------------------------------------
 # 8-bit floating point with block scales
-
-def _rows(x: torch.Tensor, name: str) -> tuple:
-    """(rows, columns) of a contiguous tensor whose last dimension is the row."""
-    if x.dim() < 1 or not x.is_contiguous():
-        raise ValueError(f"{name} must be contiguous, with at least one dimension")
-    K = x.shape[-1]
-    return (x.numel() // K if K else 0), K
-
 
 def ss_quant_q8(x: torch.Tensor, *, square: bool = False, q: Optional[torch.Tensor] = None,
                 scale: Optional[torch.Tensor] = None, stream=None) -> tuple:
@@ -321,23 +234,10 @@ def ss_quant_q8(x: torch.Tensor, *, square: bool = False, q: Optional[torch.Tens
     scale): q of x's shape in torch.float8_e4m3fn and float32 scales of blocks of 128 columns,
     [..., ceil(K/128)]; with square (x [N,K]) of 128 x 128, [ceil(N/128), ceil(K/128)]. x stands
     for scale * q. q and scale are allocated where not given. Asynchronous."""
-    idx = _gpu(x, "x")
-    if _elsewhere(idx, stream):
-        with _placed(idx, stream):
+    if stream is not None:
+        with _placed(_gpu(x, "x"), stream):
             return ss_quant_q8(x, square=square, q=q, scale=scale)
-    M, K = _rows(x, "x")
-    shape, KB = x.shape, -(-K // Q8_BLOCK)
-    if square and len(shape) != 2:
-        raise ValueError("a square rounding takes x [N, K]")
-    sshape = (-(-M // Q8_BLOCK), KB) if square else shape[:-1] + (KB,)
-    if q is None:
-        q = x.new_empty(shape, dtype=_Q8)
-    if scale is None:
-        scale = x.new_empty(sshape, dtype=_F32)
-    dims = _pack_q8_dims(M, K, _io(x, "x"), 1 if square else 0, 0.0, 0)
-    _check(_raw.ss_quant_q8(dims, x.data_ptr(), _same(q, shape, _Q8, idx, "q"), _same(scale, sshape, _F32, idx, "scale"),
-                            _stream_of(idx)))
-    return q, scale
+    return _done(_quant(x, square, q, scale))
 
 
 def ss_norm_q8(x: torch.Tensor, w: torch.Tensor, *, residual: Optional[torch.Tensor] = None, eps: float = 1e-5,
@@ -347,27 +247,10 @@ def ss_norm_q8(x: torch.Tensor, w: torch.Tensor, *, residual: Optional[torch.Ten
     point in blocks of 128 columns: x, residual [..., K] (float32 or bfloat16, contiguous), w [K]
     float32. Returns (q, scale, s): q and scale as from ss_quant_q8, s in x's dtype (None
     without a residual). sum_out receives s; it may be x or residual itself. Asynchronous."""
-    idx = _gpu(x, "x")
-    if _elsewhere(idx, stream):
-        with _placed(idx, stream):
+    if stream is not None:
+        with _placed(_gpu(x, "x"), stream):
             return ss_norm_q8(x, w, residual=residual, eps=eps, q=q, scale=scale, sum_out=sum_out)
-    M, K = _rows(x, "x")
-    shape, dt = x.shape, x.dtype
-    sshape = shape[:-1] + (-(-K // Q8_BLOCK),)
-    if q is None:
-        q = x.new_empty(shape, dtype=_Q8)
-    if scale is None:
-        scale = x.new_empty(sshape, dtype=_F32)
-    if residual is None:
-        if sum_out is not None:
-            raise ValueError("sum_out given without a residual")
-    elif sum_out is None:
-        sum_out = x.new_empty(shape)
-    args = _pack_norm_args(x.data_ptr(), _opt(residual, shape, dt, idx, "residual"), _same(w, (K,), _F32, idx, "w"),
-                           _same(q, shape, _Q8, idx, "q"), _same(scale, sshape, _F32, idx, "scale"),
-                           _opt(sum_out, shape, dt, idx, "sum_out"))
-    _check(_raw.ss_norm_q8(_pack_q8_dims(M, K, _io(x, "x"), 0, eps, 0), args, _stream_of(idx)))
-    return q, scale, sum_out
+    return _done(_norm(x, w, residual, eps, q, scale, sum_out))
 
 
 def ss_gemm_q8(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor, *,
@@ -378,24 +261,10 @@ def ss_gemm_q8(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: torch.T
     ss_quant_q8(square=True); K a multiple of 16. Returns y [..., N] in out_dtype (float32 or
     bfloat16; out's own where given); residual has y's shape and dtype and may be out itself.
     Asynchronous."""
-    idx = _gpu(xq, "xq")
-    if _elsewhere(idx, stream):
-        with _placed(idx, stream):
+    if stream is not None:
+        with _placed(_gpu(xq, "xq"), stream):
             return ss_gemm_q8(xq, xs, wq, ws, residual=residual, out=out, out_dtype=out_dtype)
-    M, K = _rows(xq, "xq")
-    if wq.dim() != 2:
-        raise ValueError("wq must be [N, K]")
-    N, shape, KB = wq.shape[0], xq.shape, -(-K // Q8_BLOCK)
-    lead = shape[:-1]
-    yshape = lead + (N,)
-    if out is None:
-        out = xq.new_empty(yshape, dtype=out_dtype)
-    dt = out.dtype
-    args = _pack_gemm_args(_same(xq, shape, _Q8, idx, "xq"), _same(xs, lead + (KB,), _F32, idx, "xs"),
-                           _same(wq, (N, K), _Q8, idx, "wq"), _same(ws, (-(-N // Q8_BLOCK), KB), _F32, idx, "ws"),
-                           _opt(residual, yshape, dt, idx, "residual"), _same(out, yshape, dt, idx, "out"))
-    _check(_raw.ss_gemm_q8(_pack_gemm_dims(M, N, K, _io(out, "out"), 0), args, _stream_of(idx)))
-    return out
+    return _done(_gemm(xq, xs, wq, ws, residual, out, out_dtype))
 
 
 # ---------------------------------------------------------------------------
