@@ -64,7 +64,8 @@ ss_status check_glr_dims(const ss_glr_dims* d, GlrCall call) {
         return fail(SS_ERR_INVALID_ARG, "seqlen %lld not below 2^31", (long long)d->seqlen);
     if (d->io_dtype != SS_F32 && d->io_dtype != SS_BF16) return fail(SS_ERR_UNSUPPORTED, "io_dtype %d unknown", d->io_dtype);
     if (d->reserved != 0) return fail(SS_ERR_INVALID_ARG, "reserved must be 0");
-    const int64_t chunk = call == kBwd ? selscan::glr_bwd_chunk(d->batch, d->d) : selscan::kGlrFwdChunk;
+    const int64_t chunk = call == kBwd ? selscan::glr_bwd_chunk(d->batch, d->seqlen, d->d)
+                                       : selscan::glr_fwd_chunk(d->io_dtype == SS_BF16, d->batch, d->seqlen, d->d);
     const int64_t n = call == kStep ? 1 : ceil_div(d->seqlen, chunk);
     const int64_t cols = ceil_div(d->d, selscan::kGlrCols);
     if (d->batch > INT32_MAX / (n * cols)) return fail(SS_ERR_INVALID_ARG, "batch x seqlen x d too large");
@@ -76,7 +77,7 @@ ss_status check_glr_dims(const ss_glr_dims* d, GlrCall call) {
 struct GlrLayout { int64_t chunk, nchunks; size_t off_slots, off_part, total; };
 GlrLayout glr_layout(const ss_glr_dims& d, bool backward) {
     GlrLayout l{};
-    l.chunk = backward ? selscan::glr_bwd_chunk(d.batch, d.d) : selscan::kGlrFwdChunk;
+    l.chunk = backward ? selscan::glr_bwd_chunk(d.batch, d.seqlen, d.d) : selscan::glr_fwd_chunk(d.io_dtype == SS_BF16, d.batch, d.seqlen, d.d);
     l.nchunks = ceil_div(d.seqlen, l.chunk);
     const size_t words = (size_t)l.nchunks * (size_t)d.batch * (size_t)d.d;
     size_t off = 0;

@@ -196,7 +196,7 @@ __device__ __forceinline__ void word_store(uint64_t* p, uint64_t v) {
 template <int CH>
 __device__ __forceinline__ float look_back(const uint64_t* row, int64_t stride, int n, int valid, int lane) {
     constexpr int kRows = 64 / CH;
-    constexpr uint32_t kAll = CH == 32 ? ~0u : (1u << CH) - 1u;
+    constexpr uint32_t kAll = (uint32_t)((uint64_t(1) << CH) - 1u);
     const uint32_t want = valid >= CH ? kAll : (1u << valid) - 1u;
     const int ch = lane % CH < valid ? lane % CH : valid - 1, at = lane / CH;
     auto load = [&](int first) { return word_load(row + (int64_t)(first + at < n ? first + at : n - 1) * stride + ch); };
@@ -292,27 +292,20 @@ struct Rows {
 };
 
 // ---------------------------------------------------------------------------
-// forward. LOOK: several chunks per batch row, tiles taken by ticket; else one chunk, a
-// workgroup per tile. Loading the next tile's rows before the wait for the state in front was
-// slower: the look-back's loads return behind them, and every chunk after this one waits for it.
+// forward
 
-template <typename T, bool VEC, int TT, int NW, bool LOOK>
-__global__ void __launch_bounds__(NW * 64, 4)
-k_glr_fwd(const GlrArgs p) {
+// A wave's run of TT tokens: its rows, then the two factors of y_k = h[k] + P[k] * (state in front).
+template <typename T, bool VEC, int TT>
+struct FwdRun {
     using V = Pair<T, VEC>;
-    __shared__ float2 s_map[NW][kGlrCols];        // (P, S) of each wave's run
-    __shared__ float s_in[NW][kGlrCols];          // state in front of each wave's run
-    __shared__ unsigned s_next;
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-
-    V vx[TT], vr[TT], vi[TT];                     // a run's rows
+    V vx[TT], vr[TT], vi[TT];
     float A[2];
-    bool reset = false;
-    auto fetch = [&](unsigned t) {
-        const Tile q = tile_at(p, t);
-        const Chan c = lane_chan<VEC>(q.col, lane, p.D);
-        const int64_t t0 = (int64_t)q.chunk * (NW * TT) + wave * TT, tb = t0 < p.L ? t0 : p.L - 1;
+    bool reset;
+    float P[TT][2], h[TT][2];
+
+    // all rows at once; a run past the end loads the last one
+    __device__ __forceinline__ void fetch(const GlrArgs& p, const Tile& q, const Chan& c, int64_t t0, int lane) {
+        const int64_t tb = t0 < p.L ? t0 : p.L - 1;
         const int n = run_tokens(p, t0, TT);
         Rows<T> rx(p.x, p.xb, p.xt, q.b, tb), rr(p.r, p.rb, p.rt, q.b, tb), ri(p.i, p.ib, p.it, q.b, tb);
 #pragma unroll
@@ -326,26 +319,10 @@ k_glr_fwd(const GlrArgs p) {
         A[0] = p.A[c.c[0]];
         A[1] = p.A[c.c[1]];
         reset = reset_at<TT>(p, q.b, t0, lane);
-    };
-
-    unsigned tile = blockIdx.x;
-    if constexpr (LOOK) {
-        if (tid == 0) s_next = __hip_atomic_fetch_add(p.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        __syncthreads();
-        tile = __builtin_amdgcn_readfirstlane(s_next);
-        __syncthreads();
     }
-    while (tile < p.tiles) {
-        fetch(tile);
-        unsigned next = p.tiles;
-        if constexpr (LOOK) {
-            if (tid == 0) next = __hip_atomic_fetch_add(p.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        }
-        const Tile q = tile_at(p, tile);
-        const Chan c = lane_chan<VEC>(q.col, lane, p.D);
-        const int64_t t0 = (int64_t)q.chunk * (NW * TT) + wave * TT;
-        const int n = run_tokens(p, t0, TT);
-        const uint32_t rs = (uint32_t)__ballot(reset);
+
+    // the run from a zero state: h[k] the local state, P[k] what a state in front is multiplied by
+    __device__ __forceinline__ void reduce(int n, uint32_t rs) {
         // tokens past the end leave the state as it is: a = exp(A sigmoid(-inf)) = 1, w = 0; a reset
         // token's r is not looked at
         if (n < TT) {
@@ -358,9 +335,6 @@ k_glr_fwd(const GlrArgs p) {
             for (int k = 0; k < TT; ++k)
                 if (rs >> k & 1u) vr[k].set(0.0f);
         }
-
-        // the run from a zero state: h[k] the local state, P[k] what a state in front is multiplied by
-        float P[TT][2], h[TT][2];
 #pragma unroll
         for (int k = 0; k < TT; ++k) {
             const bool on = rs >> k & 1u;
@@ -374,11 +348,116 @@ k_glr_fwd(const GlrArgs p) {
             }
             __builtin_amdgcn_sched_barrier(0);                    // token by token: other waves fill the pipes, and registers are few
         }
+    }
+    __device__ __forceinline__ float2 map(uint32_t rs, int j) const { return make_float2(rs ? -0.0f : P[TT - 1][j], h[TT - 1][j]); }
+
+    __device__ __forceinline__ void put(const GlrArgs& p, const Tile& q, const Chan& c, int64_t t0, uint32_t rs, const float* in) const {
+        const int n = run_tokens(p, t0, TT);
+        // The state in front of token 64 m of a batch row is checkpoint m: the one behind token k_ck
+        // of this run, if it is one of its tokens and not the sequence's last. The state behind the
+        // last token, k_end, is the final one.
+        const int k_ck = p.ckpt && n > 0 ? SS_GLR_CKPT - 1 - (int)(t0 % SS_GLR_CKPT) : -1;
+        const int k_end = n > 0 && t0 + n == p.L ? n - 1 : -1;
+        auto put_ckpt = [&](int64_t t, float a, float b) {
+            Pair<float, VEC>::st(p.ckpt + ((int64_t)q.b * p.nck + t / SS_GLR_CKPT) * p.D, c.c[0], c.c[1], c.ok[0], c.ok[1], a, b);
+        };
+        if (p.ckpt && t0 == 0) put_ckpt(0, in[0], in[1]);
+        char* yrow = static_cast<char*>(p.y) + ((int64_t)q.b * p.L + t0) * p.D * (int64_t)sizeof(T);
+        const int64_t ystep = (int64_t)p.D * (int64_t)sizeof(T);
+        auto go = [&](auto plain) {
+            constexpr bool kPlain = decltype(plain)::value;       // whole run, no reset
+            const int k_rs = rs ? __builtin_ctz(rs) : TT;         // from the first reset on the state in front does not count
 #pragma unroll
-        for (int j = 0; j < 2; ++j) s_map[wave][lane_slot<VEC>(lane, j)] = make_float2(rs ? -0.0f : P[TT - 1][j], h[TT - 1][j]);
-        if (LOOK && tid == 0) s_next = next;
+            for (int k = 0; k < TT; ++k) {
+                if (kPlain || k < n) {
+                    float o[2];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        o[j] = kPlain || k < k_rs ? __builtin_fmaf(P[k][j], in[j], h[k][j]) : h[k][j];
+                    V::st(yrow, c.c[0], c.c[1], c.ok[0], c.ok[1], o[0], o[1]);
+                    yrow += ystep;
+                    if (k == k_ck && k != k_end) put_ckpt(t0 + k + 1, o[0], o[1]);
+                    if (k == k_end && p.state)
+                        Pair<float, VEC>::st(p.state + (int64_t)q.b * p.D, c.c[0], c.c[1], c.ok[0], c.ok[1], o[0], o[1]);
+                }
+            }
+        };
+        if (n == TT && rs == 0) go(Tag<true>{});
+        else go(Tag<false>{});
+    }
+};
+
+// One chunk per batch row: a workgroup per tile.
+template <typename T, bool VEC, int TT, int NW>
+__global__ void __launch_bounds__(NW * 64, 4)
+k_glr_fwd(const GlrArgs p) {
+    static_assert(NW % 4 == 0, "the runs' maps are read four at a time");
+    __shared__ float2 s_map[NW][kGlrCols];        // (P, S) of each wave's run
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const Tile q = tile_at(p, blockIdx.x);
+    const Chan c = lane_chan<VEC>(q.col, lane, p.D);
+    const int64_t t0 = wave * TT;
+    FwdRun<T, VEC, TT> run;
+    run.fetch(p, q, c, t0, lane);
+    float in[2] = {0.0f, 0.0f};
+    if (p.state) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) in[j] = p.state[(int64_t)q.b * p.D + c.c[j]];
+    }
+    const uint32_t rs = (uint32_t)__ballot(run.reset);
+    run.reduce(run_tokens(p, t0, TT), rs);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) s_map[wave][lane_slot<VEC>(lane, j)] = run.map(rs, j);
+    asm volatile("" : "+v"(in[0]), "+v"(in[1]));  // every wave has the initial state, which one overwrites
+    __syncthreads();
+    for (int w = 0; w < wave; w += 4) {
+        float2 m[4][2];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) m[i][j] = s_map[w + i][lane_slot<VEC>(lane, j)];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                if (w + i < wave) in[j] = fold(m[i][j].x, in[j], m[i][j].y);
+    }
+    run.put(p, q, c, t0, rs, in);
+}
+
+// Several chunks per batch row, tiles taken by ticket. Loading the next tile's rows before the
+// wait for the state in front was slower: the look-back's loads return behind them, and every
+// chunk after this one waits for it. So was a wave of its own for the look-back with the next
+// rows in flight meanwhile (B 1, L 131072, D 2048: 700 us against 620): a word's way between two
+// workgroups is through memory, and takes longer the fuller the memory's queues are.
+template <typename T, bool VEC, int TT, int NW>
+__global__ void __launch_bounds__(NW * 64, 4)
+k_glr_scan(const GlrArgs p) {
+    __shared__ float2 s_map[NW][kGlrCols];        // (P, S) of each wave's run
+    __shared__ float s_in[NW][kGlrCols];          // state in front of each wave's run
+    __shared__ unsigned s_next;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    if (tid == 0) s_next = __hip_atomic_fetch_add(p.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    unsigned tile = __builtin_amdgcn_readfirstlane(s_next);
+    __syncthreads();
+    while (tile < p.tiles) {
+        const Tile q = tile_at(p, tile);
+        const Chan c = lane_chan<VEC>(q.col, lane, p.D);
+        const int64_t t0 = (int64_t)q.chunk * (NW * TT) + wave * TT;
+        FwdRun<T, VEC, TT> run;
+        run.fetch(p, q, c, t0, lane);
+        unsigned next = 0;
+        if (tid == 0) next = __hip_atomic_fetch_add(p.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        const uint32_t rs = (uint32_t)__ballot(run.reset);
+        run.reduce(run_tokens(p, t0, TT), rs);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) s_map[wave][lane_slot<VEC>(lane, j)] = run.map(rs, j);
+        if (tid == 0) s_next = next;
         __syncthreads();
-        if constexpr (LOOK) next = __builtin_amdgcn_readfirstlane(s_next);
+        tile = __builtin_amdgcn_readfirstlane(s_next);
 
         // the states in front of the runs: each wave for 128 / NW channels
         {
@@ -389,7 +468,7 @@ k_glr_fwd(const GlrArgs p) {
                 const int64_t bd0 = (int64_t)q.b * p.D + q.col * kGlrCols + wave * CH, BD = (int64_t)p.B * p.D;
                 const bool mine = lane < CH && lane < valid;         // the lane that writes for its channel
                 float in = 0.0f;
-                if (LOOK && q.chunk > 0) {
+                if (q.chunk > 0) {
                     float cp = 1.0f, cs = 0.0f;
 #pragma unroll 4
                     for (int w = 0; w < NW; ++w) {
@@ -413,48 +492,15 @@ k_glr_fwd(const GlrArgs p) {
                         s_in[w][ch] = hh;
                         hh = fold(m.x, hh, m.y);
                     }
-                    if (LOOK && q.chunk == 0) word_store(p.slots + bd0 + lane, state_word(hh));
+                    if (q.chunk == 0) word_store(p.slots + bd0 + lane, state_word(hh));
                 }
             }
         }
         __syncthreads();
-
         float in[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) in[j] = s_in[wave][lane_slot<VEC>(lane, j)];
-        // The state in front of token 64 m of a batch row is checkpoint m: the one behind token k_ck
-        // of this run, if it is one of its tokens and not the sequence's last. The state behind the
-        // last token, k_end, is the final one.
-        const int k_ck = p.ckpt && n > 0 ? SS_GLR_CKPT - 1 - (int)(t0 % SS_GLR_CKPT) : -1;
-        const int k_end = n > 0 && t0 + n == p.L ? n - 1 : -1;
-        auto put_ckpt = [&](int64_t t, float a, float b) {
-            Pair<float, VEC>::st(p.ckpt + ((int64_t)q.b * p.nck + t / SS_GLR_CKPT) * p.D, c.c[0], c.c[1], c.ok[0], c.ok[1], a, b);
-        };
-        if (p.ckpt && t0 == 0) put_ckpt(0, in[0], in[1]);
-        char* yrow = static_cast<char*>(p.y) + ((int64_t)q.b * p.L + t0) * p.D * (int64_t)sizeof(T);
-        const int64_t ystep = (int64_t)p.D * (int64_t)sizeof(T);
-        auto put = [&](auto plain) {
-            constexpr bool kPlain = decltype(plain)::value;       // whole run, no reset
-            const int k_rs = rs ? __builtin_ctz(rs) : TT;         // from the first reset on the state in front does not count
-#pragma unroll
-            for (int k = 0; k < TT; ++k) {
-                if (kPlain || k < n) {
-                    float o[2];
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        o[j] = kPlain || k < k_rs ? __builtin_fmaf(P[k][j], in[j], h[k][j]) : h[k][j];
-                    V::st(yrow, c.c[0], c.c[1], c.ok[0], c.ok[1], o[0], o[1]);
-                    yrow += ystep;
-                    if (k == k_ck && k != k_end) put_ckpt(t0 + k + 1, o[0], o[1]);
-                    if (k == k_end && p.state)
-                        Pair<float, VEC>::st(p.state + (int64_t)q.b * p.D, c.c[0], c.c[1], c.ok[0], c.ok[1], o[0], o[1]);
-                }
-            }
-        };
-        if (n == TT && rs == 0) put(Tag<true>{});
-        else put(Tag<false>{});
-        if constexpr (!LOOK) break;
-        tile = next;
+        run.put(p, q, c, t0, rs, in);
     }
 }
 
@@ -754,21 +800,30 @@ hipError_t launch_glr_t(const LaunchGlr& p) {
     }
     if (look) {
         const int64_t n = p.nchunks * p.batch * p.D;
-        const int64_t groups = (n + 1023) / 1024;
+        const int64_t groups = (n + 255) / 256;
         hipLaunchKernelGGL(k_glr_clear, dim3((unsigned)(groups < 2048 ? groups : 2048)), dim3(256), 0, st, p.slots, n, p.ticket);
     }
     const dim3 grid(look && a.tiles > kGlrGroups ? kGlrGroups : a.tiles);
+    auto go = [&](auto kernel, int64_t waves) { hipLaunchKernelGGL(kernel, grid, dim3((unsigned)waves * 64), 0, st, a); };
     if (p.pass == LaunchGlr::kFwd) {
-        // runs of 16 tokens and two workgroups per CU where a row's two channels fit one register
-        // (B 8, L 2048, D 5120, bf16: 162 us against 196 with 16 waves of 8 tokens), else runs of 8 (fp32, B 8,
-        // L 2048, D 2560: 144 against 153)
-        constexpr int TT = sizeof(T) == 2 ? 16 : 8, NW = kGlrFwdChunk / TT;
-        if (look) hipLaunchKernelGGL((k_glr_fwd<T, VEC, TT, NW, true>), grid, dim3(NW * 64), 0, st, a);
-        else hipLaunchKernelGGL((k_glr_fwd<T, VEC, TT, NW, false>), grid, dim3(NW * 64), 0, st, a);
+        // One chunk is a matter of latency: 16 waves with runs of 8 tokens, of 4 up to 64 tokens (B 1, L 64,
+        // D 512, fp32: 5.5 us against 8.2 with runs of 8). Several: runs of 16 tokens where a row's two
+        // channels fit one register (B 8, L 2048, D 5120, bf16: 162 us against 196 with 16 waves of 8
+        // tokens), else runs of 8 (fp32, B 8, L 2048, D 2560: 144 against 153)
+        if (!look) {
+            if (p.L <= 64) go(k_glr_fwd<T, VEC, 4, 16>, 16);
+            else go(k_glr_fwd<T, VEC, 8, 16>, 16);
+        } else if constexpr (sizeof(T) == 2) {
+            if (p.chunk == 256) go(k_glr_scan<T, VEC, 16, 16>, 16);
+            else go(k_glr_scan<T, VEC, 16, 8>, 8);
+        } else {
+            go(k_glr_scan<T, VEC, 8, 16>, 16);
+        }
     } else {
+        // runs of 16 tokens; one chunk of up to 64 in runs of 4 (B 1, L 64, D 512: 10.7 us against 13.1,
+        // B 256, L 64, D 4096, bf16: 266 both; of 8 for up to 128, B 2, D 1024: 15.4 against 14.6)
         constexpr int TT = 16;
-        auto go = [&](auto kernel, int waves) { hipLaunchKernelGGL(kernel, grid, dim3((unsigned)waves * 64), 0, st, a); };
-        if (p.chunk == 64) look ? go(k_glr_bwd<T, VEC, TT, 64 / TT, true>, 64 / TT) : go(k_glr_bwd<T, VEC, TT, 64 / TT, false>, 64 / TT);
+        if (p.chunk == 64) look ? go(k_glr_bwd<T, VEC, TT, 64 / TT, true>, 64 / TT) : go(k_glr_bwd<T, VEC, 4, 16, false>, 16);
         else look ? go(k_glr_bwd<T, VEC, TT, 128 / TT, true>, 128 / TT) : go(k_glr_bwd<T, VEC, TT, 128 / TT, false>, 128 / TT);
         hipLaunchKernelGGL(k_glr_da, dim3((unsigned)((p.D + 63) / 64)), dim3(1024), 0, st, p.part, p.g.dA,
                            p.nchunks * p.batch, (int)p.D);
