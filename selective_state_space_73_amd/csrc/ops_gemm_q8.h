@@ -19,6 +19,8 @@
 // 32 bytes of an operand may be any two 16-byte chunks of the block as long as both operands
 // take the same two: lane l takes chunks l / 16 and l / 16 + 4 of its row.
 #pragma once
+#include <type_traits>
+
 #include "ops_internal.h"
 #include "selscan_device.h"
 
@@ -68,6 +70,9 @@ struct GqSource {
         : r(__builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, -1, kBufDword3)) {}
     __device__ __forceinline__ void to_lds(gq_i4* lds, unsigned voff, unsigned soff) const {
         __builtin_amdgcn_raw_ptr_buffer_load_lds(r, lds, 16, voff, soff, 0, 0);
+    }
+    __device__ __forceinline__ void to_lds4(gq_i4* lds, unsigned voff, unsigned soff) const {      // four bytes a lane
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, lds, 4, voff, soff, 0, 0);
     }
 };
 
@@ -316,19 +321,24 @@ k_gemm_q8(const GemmQ8Args p, int tiles_m, int tiles_n) {
 
 // ---------------------------------------------------------------------------
 // Few tiles: KS groups of WN x WM waves share a workgroup's tile and take the blocks of k in
-// turn, each with LDS buffers of its own, so that a CU has enough bytes on their way while the
-// grid is short; their sums meet in LDS and are added in order. Staged as above; row i of
-// product a is row 16 a + i of the wave's rows of W.
+// turn, each with two LDS buffers of its own, so that a CU has enough bytes on their way and
+// waves enough to read and multiply them while the grid is short. What bounds it is the waves'
+// instructions (three buffers with as many fewer groups were slower by a tenth), so a whole
+// block's transfers have no conditions, the scales come by transfers as well (the first wave of a
+// group fetches them) and a step knows its buffer. The groups' sums meet in LDS and are added in
+// order. Staged as above; row i of product a is row 16 a + i of the wave's rows of W.
 template <typename T, bool RES, int NF, int MF, int WN, int WM, int KS>
 __global__ void __launch_bounds__(64 * WN * WM * KS)
 k_gemm_q8_split(const GemmQ8Args p, int tiles_m, int tiles_n) {
     constexpr int TN = 16 * NF * WN, TM = 16 * MF * WM, TH = 64 * WN * WM;
     constexpr int CW = (TN * 8 + TH - 1) / TH, CX = (TM * 8 + TH - 1) / TH;
     constexpr int LD = TN + 4;                                    // row of the sums: 4 floats on, against bank conflicts
-    static_assert(128 % TN == 0 && (TN * 8) % 64 == 0 && (TM * 8) % 64 == 0, "one scale of W; whole transfers");
-    static_assert(TM * LD * 4 <= 2 * (TN + TM) * 128, "the sums fit in the block buffers");
+    constexpr int BUF = (TN + TM) * 8 + 32;                       // chunks of a buffer: W, X, 64 scales of X, 64 times that of W
+    static_assert(128 % TN == 0 && (TN * 8) % 64 == 0 && (TM * 8) % 64 == 0 && TM <= 64, "one scale of W; whole transfers");
+    static_assert(TM * LD * 4 <= 2 * BUF * 16, "the sums fit in the block buffers");
+    static_assert(TN * 8 % TH == 0 && (TM * 8 % TH == 0 || CX == 1), "no condition on W's transfers, one on X's");
     using Frag = GqFrag<T>;
-    __shared__ gq_i4 lds[KS][2 * (TN + TM) * 8];
+    __shared__ gq_i4 lds[KS][2 * BUF];
     const int tid = threadIdx.x % TH, lane = tid & 63;
     const int grp = __builtin_amdgcn_readfirstlane(threadIdx.x / TH);
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -336,10 +346,9 @@ k_gemm_q8_split(const GemmQ8Args p, int tiles_m, int tiles_n) {
     const int fr = lane & 15, fc = lane >> 4;
     const GqTile tile = gq_tile(blockIdx.x, tiles_m, tiles_n);
     const int64_t m0 = (int64_t)tile.m * TM, n0 = (int64_t)tile.n * TN;
-    auto sW = [&](int buf) { return lds[grp] + buf * TN * 8; };
-    auto sX = [&](int buf) { return lds[grp] + (2 * TN + buf * TM) * 8; };
 
     const GqSource from_w(p.wq + n0 * p.K), from_x(p.xq + m0 * p.K);
+    const GqSource from_ws(reinterpret_cast<const uint8_t*>(p.ws + n0 / 128 * p.KB)), from_xs(reinterpret_cast<const uint8_t*>(p.xs + m0 * p.KB));
     const int rows_w = (int)(p.N - n0 < TN ? p.N - n0 : TN), rows_x = (int)(p.M - m0 < TM ? p.M - m0 : TM);
     unsigned ow[CW], ox[CX];
 #pragma unroll
@@ -352,25 +361,35 @@ k_gemm_q8_split(const GemmQ8Args p, int tiles_m, int tiles_n) {
         const int idx = tid + TH * i, r = idx >> 3, row = r < rows_x ? r : rows_x - 1;
         ox[i] = (unsigned)row * (unsigned)p.K + 16u * ((idx & 7) ^ gq_key_x(r));
     }
-    auto stage = [&](int kb, int buf) {
+    const unsigned os = (unsigned)(lane < rows_x ? lane : rows_x - 1) * (unsigned)p.KB * 4u;
+    auto stage = [&](int kb, gq_i4* to) {
+        if (kb >= p.KB) return;
         const unsigned k0 = (unsigned)kb * 128u;
-        const int left = (int)(p.K - k0 < 128 ? (p.K - k0) / 16 : 8);       // chunks of this block
-#pragma unroll
-        for (int i = 0; i < CW; ++i) {
-            const int idx = tid + TH * i;
-            if (64 * wave + TH * i < TN * 8) {                    // uniform: whole waves
-                if (((idx & 7) ^ gq_key_x(idx >> 3)) < left) from_w.to_lds(sW(buf) + 64 * wave + TH * i, ow[i], k0);
-                else sW(buf)[idx] = gq_i4{0, 0, 0, 0};
-            }
+        const int left = ((int)p.K - (int)k0) / 16;               // chunks from this block on
+        if (wave == 0) {
+            from_xs.to_lds4(to + (TN + TM) * 8, os, (unsigned)kb * 4u);
+            from_ws.to_lds4(to + (TN + TM) * 8 + 16, 0u, (unsigned)kb * 4u);
         }
+        auto part = [&](auto whole) {                             // a whole block, or one that K ends in
 #pragma unroll
-        for (int i = 0; i < CX; ++i) {
-            const int idx = tid + TH * i;
-            if (64 * wave + TH * i < TM * 8) {
-                if (((idx & 7) ^ gq_key_x(idx >> 3)) < left) from_x.to_lds(sX(buf) + 64 * wave + TH * i, ox[i], k0);
-                else sX(buf)[idx] = gq_i4{0, 0, 0, 0};
+            for (int i = 0; i < CW; ++i) {
+                const int idx = tid + TH * i;
+                if (decltype(whole)::value || ((idx & 7) ^ gq_key_x(idx >> 3)) < left)
+                    from_w.to_lds(to + 64 * wave + TH * i, ow[i], k0);
+                else to[idx] = gq_i4{0, 0, 0, 0};
             }
-        }
+#pragma unroll
+            for (int i = 0; i < CX; ++i) {
+                const int idx = tid + TH * i;
+                if (TM * 8 % TH == 0 || 64 * wave < TM * 8) {       // uniform: whole waves
+                    if (decltype(whole)::value || ((idx & 7) ^ gq_key_x(idx >> 3)) < left)
+                        from_x.to_lds(to + TN * 8 + 64 * wave + TH * i, ox[i], k0);
+                    else to[TN * 8 + idx] = gq_i4{0, 0, 0, 0};
+                }
+            }
+        };
+        if (left >= 8) part(std::true_type{});
+        else part(std::false_type{});
     };
     const int c0 = fr * 8 + (fc ^ gq_key_x(fr)), c1 = fr * 8 + ((fc + 4) ^ gq_key_x(fr));
     auto frag = [&](const gq_i4* s, int row0) {
@@ -378,53 +397,41 @@ k_gemm_q8_split(const GemmQ8Args p, int tiles_m, int tiles_n) {
         f.set(s[row0 * 8 + c0], s[row0 * 8 + c1]);
         return f;
     };
-    const float* xsb = p.xs + m0 * p.KB;
-    const float* wsb = p.ws + n0 / 128 * p.KB;
-    unsigned xo[MF];
-#pragma unroll
-    for (int b = 0; b < MF; ++b) {
-        const int r = wm * 16 * MF + 16 * b + fr;
-        xo[b] = (unsigned)(r < rows_x ? r : rows_x - 1) * (unsigned)p.KB;
-    }
     gq_f4 acc[NF][MF];
 #pragma unroll
     for (int a = 0; a < NF; ++a)
 #pragma unroll
         for (int b = 0; b < MF; ++b) acc[a][b] = gq_f4{0.f, 0.f, 0.f, 0.f};
 
-    float nx[MF], nws = 0.0f;
-    auto begin = [&](int kb, int buf) {
-        if (kb < p.KB) {
-            nws = wsb[kb];
-#pragma unroll
-            for (int b = 0; b < MF; ++b) nx[b] = xsb[xo[b] + kb];
-            stage(kb, buf);
-        }
-    };
-    begin(grp, 0);
-    const int steps = (p.KB + KS - 1) / KS;
-    for (int s = 0; s < steps; ++s) {
+    auto step = [&](int kb, auto which) {
+        const gq_i4* buf = lds[grp] + decltype(which)::value * BUF;
         __syncthreads();                                          // this block is in LDS, the last one's readers are done
-        const int kb = s * KS + grp, buf = s & 1;
+        stage(kb + KS, lds[grp] + (1 - decltype(which)::value) * BUF);
+        if (kb >= p.KB) return;
+        const float* scales = reinterpret_cast<const float*>(buf + (TN + TM) * 8);
+        const float sw = scales[64 + lane];
         float sc[MF];
+        Frag fx[MF];
 #pragma unroll
-        for (int b = 0; b < MF; ++b) sc[b] = nx[b] * nws;
-        begin(kb + KS, buf ^ 1);
-        if (kb < p.KB) {
-            Frag fx[MF];
+        for (int b = 0; b < MF; ++b) {
+            sc[b] = scales[wm * 16 * MF + 16 * b + fr] * sw;
+            fx[b] = frag(buf + TN * 8, wm * 16 * MF + 16 * b);
+        }
 #pragma unroll
-            for (int b = 0; b < MF; ++b) fx[b] = frag(sX(buf), wm * 16 * MF + 16 * b);
+        for (int a = 0; a < NF; ++a) {
+            const Frag fw = frag(buf, wn * 16 * NF + 16 * a);
 #pragma unroll
-            for (int a = 0; a < NF; ++a) {
-                const Frag fw = frag(sW(buf), wn * 16 * NF + 16 * a);
+            for (int b = 0; b < MF; ++b) {
+                const gq_f4 q = Frag::dot(fw, fx[b]);
 #pragma unroll
-                for (int b = 0; b < MF; ++b) {
-                    const gq_f4 q = Frag::dot(fw, fx[b]);
-#pragma unroll
-                    for (int v = 0; v < 4; ++v) acc[a][b][v] = __builtin_fmaf(q[v], sc[b], acc[a][b][v]);
-                }
+                for (int v = 0; v < 4; ++v) acc[a][b][v] = __builtin_fmaf(q[v], sc[b], acc[a][b][v]);
             }
         }
+    };
+    stage(grp, lds[grp]);
+    for (int kb = grp; kb - grp < p.KB; kb += 2 * KS) {
+        step(kb, std::integral_constant<int, 0>{});
+        if (kb - grp + KS < p.KB) step(kb + KS, std::integral_constant<int, 1>{});
     }
     __syncthreads();                                              // every block is read: the buffers hold the sums now
 #pragma unroll
@@ -449,16 +456,21 @@ k_gemm_q8_split(const GemmQ8Args p, int tiles_m, int tiles_n) {
     }
 }
 
-// Which kernel (measured on both sides of each rule, microseconds, K the repository's widths):
-//  - up to 256 tiles of 64 x 64 the waves of a workgroup split k: M 64, N 10240, K 2560 9.1
-//    against 11.9 unsplit, M 201, N 2561, K 5120 19.0 against 24.0; up to 96, tiles of 32 x 32 with eight
-//    groups: M 64, N 2560, K 5120 10.0 against 16.1 with 64-wide tiles and four. Up to 16 and
-//    32 rows of X take tiles that do not repeat rows: M 16, N 10240, K 2560 6.6 against 8.1.
-//  - tiles of 128 x 128 once there are 160 (fp32 outputs: 512): M 1024, N 2560, K 5120 43
-//    against 49 with 64 x 64, M 512, N 2560, K 5120 (80 tiles) 43 against 31.
-//  - tiles of 256 x 256, one per CU and round at 20 units of time, against 128 x 128, two per
-//    CU and round at 13: M 1024, N 10240, K 2560 42 (160 tiles) against 48 (640), M 2048 80
-//    (320) against 75 (1280), M 16384, N 2560, K 5120 267 (640) against 345 (2560).
+// Which kernel (measured, microseconds, bf16 outputs; fp32 ones are 10 to 60 percent above with the
+// same order). The smallest of these tiles of which there are no more than CUs, so that each has a
+// CU to itself, whose waves split k four or eight ways:
+//  - 16 x 32: M 16, N 2560, K 5120 5.2 (16 x 64: 7.1), M 32 5.4 (32 x 32: 6.2);
+//  - 16 x 64 where X has no more rows: M 16, N 10240, K 2560 5.5 (64 x 64: 6.9; fp32 6.0, 32 x 64 6.6);
+//  - 32 x 32: M 64, N 2560, K 5120 6.5 (32 x 64: 7.9);
+//  - 32 x 64: M 32, N 10240, K 2560 5.4 (64 x 64: 6.8);
+//  - 64 x 64: M 201, N 2561, K 5120 12.0 (split two ways 17.2, 32 x 64 20.7), M 64, N 10240, K 2560 7.2 (9.4).
+// With more, k split two ways and two workgroups to a CU or more: 32 x 64 for a single row of tiles
+// (M 64, N 40960, K 2560 20.5; 64 x 64: 23.3), else the least of what n = tiles / CUs, rounded
+// up, cost per 2560 of K:
+//  - 64 x 64, about 5 n + 1 (fp32 7 n + 2): M 192, N 10240 12.1 (n 2), M 512 28.6 (5), M 1024 49.9 (10);
+//  - 128 x 128, 13 n + 8 (22 n): M 512, N 10240 31.3 (n 2), M 1024 48.7 (3), M 2048 74.4 (5);
+//  - 256 x 256, 40 n: M 1024, N 10240 42 (n 1), M 2048 80 (2), M 16384, N 2560 123 (3); not for fp32.
+constexpr int64_t kGqCUs = 256;
 template <typename T, bool RES>
 hipError_t launch_gemm_q8_t(const LaunchGemmQ8& p) {
     const GemmQ8Args a{p.xq, p.xs, p.wq, p.ws, p.R, p.Y[0], p.Y[1], p.split, p.M, p.N, p.K, (int)((p.K + 127) / 128)};
@@ -471,21 +483,23 @@ hipError_t launch_gemm_q8_t(const LaunchGemmQ8& p) {
         return hipGetLastError();
     };
     constexpr int64_t kAll = INT32_MAX;
-    const int64_t t64 = count(64, 64), t128 = count(128, 128);
-    if (t64 <= 256) {
-        const bool few = t64 <= 96;
-        if (p.M <= 16) return few ? go(k_gemm_q8_split<T, RES, 1, 1, 2, 1, 8>, 16, 32, 1024, kAll)
-                                  : go(k_gemm_q8_split<T, RES, 1, 1, 4, 1, 4>, 16, 64, 1024, kAll);
-        if (few) return go(k_gemm_q8_split<T, RES, 1, 2, 2, 1, 8>, 32, 32, 1024, kAll);
-        if (p.M <= 32) return go(k_gemm_q8_split<T, RES, 1, 2, 4, 1, 4>, 32, 64, 1024, kAll);
-        return go(k_gemm_q8_split<T, RES, 2, 2, 2, 2, 4>, 64, 64, 1024, kAll);
+    if (count(16, 32) <= kGqCUs) return go(k_gemm_q8_split<T, RES, 2, 1, 1, 1, 8>, 16, 32, 512, kAll);
+    if (p.M <= 16 && count(16, 64) <= kGqCUs) return go(k_gemm_q8_split<T, RES, 1, 1, 4, 1, 4>, 16, 64, 1024, kAll);
+    if (count(32, 32) <= kGqCUs) return go(k_gemm_q8_split<T, RES, 2, 2, 1, 1, 8>, 32, 32, 512, kAll);
+    if (count(32, 64) <= kGqCUs) return go(k_gemm_q8_split<T, RES, 2, 2, 2, 1, 4>, 32, 64, 512, kAll);
+    if (count(64, 64) <= kGqCUs) return go(k_gemm_q8_split<T, RES, 2, 4, 2, 1, 4>, 64, 64, 512, kAll);
+    if (p.M <= 64) return go(k_gemm_q8_split<T, RES, 2, 2, 2, 1, 2>, 32, 64, 256, kAll);
+    auto turns = [&](int64_t m, int64_t n) { return (count(m, n) + kGqCUs - 1) / kGqCUs; };
+    constexpr bool kHalf = sizeof(T) == 2;
+    const int64_t t64 = kHalf ? 5 * turns(64, 64) + 1 : 7 * turns(64, 64) + 2;
+    const int64_t t128 = kHalf ? 13 * turns(128, 128) + 8 : 22 * turns(128, 128);
+    // the grids of the persistent kernels are multiples of the eight XCDs: a workgroup's tiles stay on one
+    if constexpr (kHalf) {
+        const int64_t t256 = 40 * turns(256, 256);
+        if (t256 <= t64 && t256 <= t128) return go(k_gemm_q8<T, RES, 8, 4, 2, 4>, 256, 256, 512, kGqCUs);
     }
-    // the grids below are multiples of the eight XCDs: a workgroup's tiles stay on one
-    if (t128 < (sizeof(T) == 2 ? 160 : 512)) return go(k_gemm_q8<T, RES, 2, 2, 2, 2>, 64, 64, 256, 2048);
-    if constexpr (sizeof(T) == 2) {
-        if (20 * ((count(256, 256) + 255) / 256) <= 13 * ((t128 + 511) / 512)) return go(k_gemm_q8<T, RES, 8, 4, 2, 4>, 256, 256, 512, 256);
-    }
-    return go(k_gemm_q8<T, RES, 4, 4, 2, 2>, 128, 128, 256, 512);
+    if (t64 < t128) return go(k_gemm_q8_split<T, RES, 2, 4, 2, 1, 2>, 64, 64, 256, kAll);
+    return go(k_gemm_q8<T, RES, 4, 4, 2, 2>, 128, 128, 256, 2 * kGqCUs);
 }
 
 }  // namespace selscan

@@ -201,6 +201,13 @@ def test_product(M, N, K, io):
     assert ss.ss_gemm_q8(*ops, residual=r, out=r) is r and torch.equal(r, y)      # in place
 
 
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("M,N,K", [(40, 16500, 272), (64, 16448, 144), (16, 16390, 400), (7, 8200, 1040), (31, 8195, 656), (96, 2570, 528),
+                                   (180, 9000, 208), (150, 6001, 16), (2100, 7001, 144), (1300, 2049, 2064)])
+def test_product_of_sizes_at_which_tiles_change(M, N, K, io):
+    test_product(M, N, K, io)
+
+
 def test_product_picks_every_element():
     """One value in X and one in W: the output is their product at one place, zero elsewhere,
     for places all over the tiles."""
