@@ -69,6 +69,9 @@ ss_status check_glr_dims(const ss_glr_dims* d, GlrCall call) {
     const int64_t n = call == kStep ? 1 : ceil_div(d->seqlen, chunk);
     const int64_t cols = ceil_div(d->d, selscan::kGlrCols);
     if (d->batch > INT32_MAX / (n * cols)) return fail(SS_ERR_INVALID_ARG, "batch x seqlen x d too large");
+    // one launch holds fewer than 2^32 lanes: 1024 a tile where a row is one chunk, 64 in a step
+    if (n == 1 && d->batch * cols >= (int64_t(1) << (call == kStep ? 26 : 22)))
+        return fail(SS_ERR_INVALID_ARG, "batch %lld too large for one call", (long long)d->batch);
     return SS_OK;
 }
 
@@ -199,7 +202,8 @@ ss_status check_q8_dims(const ss_q8_dims* d, bool norm) {
     if (norm && !(d->eps > 0.0f)) return fail(SS_ERR_INVALID_ARG, "eps must be positive");
     if (norm && d->square != 0) return fail(SS_ERR_INVALID_ARG, "square must be 0 for the norm");
     if (d->square != 0 && d->square != 1) return fail(SS_ERR_INVALID_ARG, "square must be 0 or 1");
-    if (d->square && ceil_div(d->rows, 128) > 65535) return fail(SS_ERR_INVALID_ARG, "too many rows of squares");
+    if (d->square && (ceil_div(d->rows, 128) > 65535 || d->cols >= (int64_t(1) << 29)))
+        return fail(SS_ERR_INVALID_ARG, "too many squares for one call");
     return SS_OK;
 }
 

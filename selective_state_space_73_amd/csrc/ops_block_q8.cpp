@@ -56,7 +56,8 @@ ss_status check_dims(const ss_block_dims* d, bool step) {
     if (d->d_conv != 4) return fail(SS_ERR_UNSUPPORTED, "d_conv %d: only 4 is built", d->d_conv);
     if (d->io_dtype != SS_F32 && d->io_dtype != SS_BF16) return fail(SS_ERR_UNSUPPORTED, "io_dtype %d unknown", d->io_dtype);
     const int64_t L = step ? 1 : d->seqlen, wide = 2 * d->d_inner > d->d_model ? 2 * d->d_inner : d->d_model;
-    if (d->batch > INT32_MAX / L || blocks(d->batch * L) > INT32_MAX / blocks(wide))
+    // (the small projections' grids have a row of 64 tokens per y)
+    if (d->batch > INT32_MAX / L || d->batch * L > 65535 * 64 || blocks(d->batch * L) > INT32_MAX / blocks(wide))
         return fail(SS_ERR_INVALID_ARG, "batch x seqlen too large for these widths");
     const ss_dims sd = scan_dims(*d, step);
     return selscan::validate_dims(&sd, step);

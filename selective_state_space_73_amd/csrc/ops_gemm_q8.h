@@ -488,7 +488,9 @@ hipError_t launch_gemm_q8_t(const LaunchGemmQ8& p) {
     if (count(32, 32) <= kGqCUs) return go(k_gemm_q8_split<T, RES, 2, 2, 1, 1, 8>, 32, 32, 512, kAll);
     if (count(32, 64) <= kGqCUs) return go(k_gemm_q8_split<T, RES, 2, 2, 2, 1, 4>, 32, 64, 512, kAll);
     if (count(64, 64) <= kGqCUs) return go(k_gemm_q8_split<T, RES, 2, 4, 2, 1, 4>, 64, 64, 512, kAll);
-    if (p.M <= 64) return go(k_gemm_q8_split<T, RES, 2, 2, 2, 1, 2>, 32, 64, 256, kAll);
+    // (a launch holds fewer than 2^32 lanes: more than 2^22 tiles go to the persistent kernels)
+    constexpr int64_t kMost = int64_t(1) << 22;
+    if (p.M <= 64 && count(32, 64) <= kMost) return go(k_gemm_q8_split<T, RES, 2, 2, 2, 1, 2>, 32, 64, 256, kAll);
     auto turns = [&](int64_t m, int64_t n) { return (count(m, n) + kGqCUs - 1) / kGqCUs; };
     constexpr bool kHalf = sizeof(T) == 2;
     const int64_t t64 = kHalf ? 5 * turns(64, 64) + 1 : 7 * turns(64, 64) + 2;
@@ -498,7 +500,7 @@ hipError_t launch_gemm_q8_t(const LaunchGemmQ8& p) {
         const int64_t t256 = 40 * turns(256, 256);
         if (t256 <= t64 && t256 <= t128) return go(k_gemm_q8<T, RES, 8, 4, 2, 4>, 256, 256, 512, kGqCUs);
     }
-    if (t64 < t128) return go(k_gemm_q8_split<T, RES, 2, 4, 2, 1, 2>, 64, 64, 256, kAll);
+    if (t64 < t128 && count(64, 64) <= kMost) return go(k_gemm_q8_split<T, RES, 2, 4, 2, 1, 2>, 64, 64, 256, kAll);
     return go(k_gemm_q8<T, RES, 4, 4, 2, 2>, 128, 128, 256, 2 * kGqCUs);
 }
 

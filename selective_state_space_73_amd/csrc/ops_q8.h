@@ -268,8 +268,19 @@ hipError_t launch_q8_rows(const LaunchQ8& p, const Q8Args& a) {
     hipStream_t st = static_cast<hipStream_t>(p.stream);
     const bool wave = p.M >= kQ8WaveRows && p.K <= 64 * 8 * 8;
     const int64_t steps = (p.K + (wave ? 512 : 2048) - 1) / (wave ? 512 : 2048);
-    const dim3 grid((unsigned)(wave ? (p.M + 3) / 4 : p.M));
-    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, a); };
+    // a launch holds fewer than 2^32 lanes: rows past 2^22 go to launches of their own
+    auto go = [&](auto kernel) {
+        for (int64_t r = 0; r < p.M; r += kQ8LaunchRows) {
+            Q8Args b = a;
+            b.M = p.M - r < kQ8LaunchRows ? p.M - r : kQ8LaunchRows;
+            b.x = static_cast<const T*>(a.x) + r * p.K;
+            if (a.res) b.res = static_cast<const T*>(a.res) + r * p.K;
+            if (a.sum) b.sum = static_cast<T*>(a.sum) + r * p.K;
+            b.q = a.q + r * p.K;
+            b.scale = a.scale + r * a.KB;
+            hipLaunchKernelGGL(kernel, dim3((unsigned)(wave ? (b.M + 3) / 4 : b.M)), dim3(256), 0, st, b);
+        }
+    };
     if (wave) {
         if (steps <= 1) go(k_q8_rows<T, VEC, NORM, RES, 64, 1>);
         else if (steps <= 2) go(k_q8_rows<T, VEC, NORM, RES, 64, 2>);

@@ -294,3 +294,20 @@ def test_outputs_end_where_they_should():
     y = buf[128:128 + B * L * D].view(B, L, D)
     ss.ss_glr_fwd(x, r, i, A, y=y)
     assert (buf[:128] == 5.0).all() and (buf[128 + B * L * D:] == 5.0).all()
+
+
+def test_offsets_past_32_bits():
+    """y of 4.3 GB from inputs that are the same for every token (views with a stride of zero):
+    h_t = a^t h_0 + b (1 - a^t) / (1 - a) in closed form."""
+    B, L, D = 1, (1 << 19) + 77, 4096
+    x, r, i, A, h0, _, _, _ = make(B, 1, D, "bf16", seed=77)
+    h = h0.clone()
+    y = ss.ss_glr_fwd(x.expand(B, L, D), r.expand(B, L, D), i.expand(B, L, D), A, state=h)
+    s, la = 1 / (1 + torch.exp(-r.double().cpu()[0, 0])), A.double().cpu()
+    la = la * s
+    b = torch.sqrt(-torch.expm1(2 * la)) * x.double().cpu()[0, 0] / (1 + torch.exp(-i.double().cpu()[0, 0]))
+    tol = rel(L, O.memory(r, A))
+    for t in (1, 2, 255, 256, 257, 4096, L // 2 + 1, L - 1, L):
+        want = torch.exp(t * la) * h0.double().cpu()[0] + b * torch.expm1(t * la) / torch.expm1(la)
+        near(y[0, t - 1], want, tol, "bf16")
+    near(h[0], want, tol, "f32")

@@ -274,3 +274,35 @@ def test_product_streams_graph_and_ends():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(outs, eager))
+
+
+# ---------------------------------------------------------------------------
+# sizes past 32 bits
+
+def test_rounding_more_rows_than_one_launch_takes():
+    M, K = (1 << 22) + 9, 16
+    x = torch.randn(M, K, device="cuda", generator=torch.Generator("cuda").manual_seed(3))
+    q, s = ss.ss_quant_q8(x)
+    w = rand(K, seed=4)
+    nq, ns, t = ss.ss_norm_q8(x, w, residual=x)
+    for rows in (slice(0, 40), slice((1 << 22) - 20, M)):
+        check_q(x[rows], q[rows], s[rows])
+        n, total = O.rms_norm(x[rows], w, x[rows])
+        check_q(n, nq[rows], ns[rows], rel=2.0 ** -15 + 2.0 ** -23, top_rel=2.0 ** -15)
+        assert torch.equal(t[rows].cpu().double(), total)
+
+
+def test_product_with_offsets_past_32_bits():
+    M, N, K = (1 << 20) + 5, 2064, 16                                   # y: 4.3 GB
+    xq, xs, wq, ws = operands(M, N, K, seed=11)
+    y = ss.ss_gemm_q8(xq, xs, wq, ws)
+    for rows in (slice(0, 70), slice(M - 70, M)):
+        check_y(y[rows], xq[rows], xs[rows], wq, ws)
+    del y
+    M, N, K = 1030, 16, 1 << 22                                         # xq: 4.3 GB
+    g = torch.Generator("cuda").manual_seed(12)
+    xq = torch.randint(0, 0x78, (M, K), dtype=torch.uint8, device="cuda", generator=g).view(F8)
+    wq = torch.randint(0, 0x78, (N, K), dtype=torch.uint8, device="cuda", generator=g).view(F8)
+    xs, ws = torch.rand(M, K // 128, device="cuda", generator=g), torch.rand(1, K // 128, device="cuda", generator=g)
+    y = ss.ss_gemm_q8(xq, xs, wq, ws, out_dtype=torch.float32)
+    check_y(y[-3:], xq[-3:], xs[-3:], wq, ws, io="f32")

@@ -275,3 +275,13 @@ def test_block_binding_refuses_host_operands():
         ss.ss_block_q8_fwd(torch.zeros(1, 2, 32), {}, 2)
     with pytest.raises(ValueError):
         ss.block_q8_weights({"W_in": torch.zeros(64, 32), "W_out": torch.zeros(32, 32)})
+
+
+def test_more_lanes_than_one_launch_holds_are_refused():
+    wide = ss.ss_view(BASE, 128, 128)
+    views = dict(x=wide, r=ss.ss_view(BASE + 1 * GAP, 0, 0), i=ss.ss_view(BASE + 2 * GAP, 0, 0))
+    for which, batch in (("fwd", 1 << 22), ("bwd", 1 << 22), ("step", 1 << 26)):
+        assert gcall(which, gdims(batch=batch, seqlen=1, d=2), gargs(**views)) == 1 and "too large" in last(), which
+    assert ss.ss_glr_workspace_bytes(gdims(batch=1 << 22, seqlen=1, d=2)) == 0
+    assert ss.lib.ss_quant_q8(ctypes.byref(qdims(rows=1, cols=1 << 29, square=1)), BASE, BASE + 64 * GAP, BASE + 99 * GAP, None) == 1
+    assert bcall(bdims(batch=65535, seqlen=65), ws_bytes=1 << 60) == 1 and "too large" in last()
