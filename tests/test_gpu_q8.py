@@ -306,3 +306,26 @@ def test_product_with_offsets_past_32_bits():
     xs, ws = torch.rand(M, K // 128, device="cuda", generator=g), torch.rand(1, K // 128, device="cuda", generator=g)
     y = ss.ss_gemm_q8(xq, xs, wq, ws, out_dtype=torch.float32)
     check_y(y[-3:], xq[-3:], xs[-3:], wq, ws, io="f32")
+
+
+def test_empty_tensors_are_refused():
+    e = lambda *s: torch.empty(*s, device="cuda")  # noqa: E731
+    q8 = lambda *s: e(*s).to(F8)  # noqa: E731
+    for call in (lambda: ss.ss_quant_q8(e(0, 128)), lambda: ss.ss_quant_q8(e(4, 0)), lambda: ss.ss_quant_q8(e(0, 128), square=True),
+                 lambda: ss.ss_norm_q8(e(0, 64), e(64)), lambda: ss.ss_gemm_q8(q8(0, 128), e(0, 1), q8(8, 128), e(1, 1)),
+                 lambda: ss.ss_gemm_q8(q8(8, 128), e(8, 1), q8(0, 128), e(0, 1)), lambda: ss.ss_gemm_q8(q8(4, 0), e(4, 0), q8(4, 0), e(1, 0)),
+                 lambda: ss.ss_glr_fwd(*[e(0, 4, 8)] * 3, e(8)), lambda: ss.ss_glr_fwd(*[e(2, 0, 8)] * 3, e(8)),
+                 lambda: ss.ss_glr_fwd(*[e(2, 4, 0)] * 3, e(0)), lambda: ss.ss_glr_step(*[e(0, 8)] * 3, e(8), e(0, 8)),
+                 lambda: ss.ss_glr_bwd(*[e(2, 0, 8)] * 3, e(8), e(2, 0, 8), e(2, 0, 8))):
+        with pytest.raises((ValueError, ss.SelscanError)):
+            call()
+
+
+def test_calls_in_inference_mode_and_with_gradients_recorded():
+    x = rand(40, 256, io="bf16", seed=1)
+    q, s = ss.ss_quant_q8(x)
+    with torch.inference_mode():
+        q1, s1 = ss.ss_quant_q8(x.clone())
+    q2, s2 = ss.ss_quant_q8(x.clone().requires_grad_())
+    for a, b in ((q1, s1), (q2, s2)):
+        assert torch.equal(a.view(torch.uint8), q.view(torch.uint8)) and torch.equal(b, s) and not b.requires_grad
