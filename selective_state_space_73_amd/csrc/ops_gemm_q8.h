@@ -142,6 +142,11 @@ __device__ __forceinline__ GqTile gq_tile(unsigned id, int tiles_m, int tiles_n)
 // LDS at chunk ^ key(row), with a key that spreads the 16 rows a fragment read touches at one
 // chunk over the banks; the transfers write LDS in lane order, so the permutation is in what
 // they fetch. Rows past the end repeat the last one, chunks past K are zero.
+//
+// 256 x 256 tiles, eight waves of 128 x 64: M 16384, N 10240, K 2560 465 us = 1.85 PFLOP/s, half of
+// what the matrix instructions alone reach. The transfers cost 100 us (344 without; not for
+// misses: 422 with every block from the L2), the epilogue 24, the rest is LDS reads behind the
+// barrier of each block, which two waves a SIMD hide in part.
 __device__ __forceinline__ int gq_key_w(int row) { return (row >> 1 & 1) | (row >> 3 & 3) << 1; }
 __device__ __forceinline__ int gq_key_x(int row) { return row >> 1 & 7; }
 

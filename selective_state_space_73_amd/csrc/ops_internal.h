@@ -44,7 +44,6 @@ struct LaunchGlr {
 hipError_t launch_glr(const LaunchGlr& p);
 
 // Rounding to 8 bits, with (w given) or without the norm in front.
-constexpr int64_t kQ8WaveRows = 1024;    // rows from which a row has one wave, not a workgroup of four
 constexpr int64_t kQ8LaunchRows = int64_t(1) << 22;
 struct LaunchQ8 {
     bool bf16, vec, square;

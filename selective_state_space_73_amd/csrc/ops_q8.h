@@ -136,7 +136,9 @@ struct Q8Args {
 
 // A row per G lanes (64 or 256), eight consecutive columns per lane and step, so that 16
 // neighbouring lanes hold one block. NV > 0: the row fits in NV steps and stays in registers.
-// NV = 0: longer rows are read again for each pass over them.
+// NV = 0: longer rows are read again for each pass over them. Bound by memory with many rows
+// (norm with residual, bf16, M 16384, K 2560, from memory: 58 us, 5.0 TB/s), by the latency of a load, the row's
+// sum and a store with few (M 64: 3.9 us).
 template <typename T, bool VEC, bool NORM, bool RES, int G, int NV>
 __global__ void __launch_bounds__(256)
 k_q8_rows(const Q8Args p) {
@@ -149,12 +151,15 @@ k_q8_rows(const Q8Args p) {
     const int64_t steps = NV ? NV : (p.K + S - 1) / S;
 
     float v[NV ? NV : 1][8];
+    auto column = [&](int64_t k) { return k * S + 8 * lane; };
+    // Lanes past the end of a row hold its last eight columns, which leaves a block's largest
+    // magnitude as it is, and the loads have no branches between them; the sum leaves them out.
+    auto inside = [&](int64_t k) { return VEC && column(k) >= p.K ? p.K - 8 : column(k); };
     auto load = [&](int64_t k, float* o) {
-        const int64_t c = k * S + 8 * lane;
-        ld8<T, VEC>(x, c, p.K, o);
+        ld8<T, VEC, true>(x, inside(k), p.K, o);
         if constexpr (RES) {
             float r[8];
-            ld8<T, VEC>(res, c, p.K, r);
+            ld8<T, VEC, true>(res, inside(k), p.K, r);
 #pragma unroll
             for (int j = 0; j < 8; ++j) o[j] += r[j];
         }
@@ -166,18 +171,19 @@ k_q8_rows(const Q8Args p) {
     }
     if constexpr (NORM) {
         float ss = 0.0f;
+        auto squares = [&](int64_t k, const float* o) {
+            float t = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) t = __builtin_fmaf(o[j], o[j], t);
+            ss += column(k) < p.K ? t : 0.0f;
+        };
         if constexpr (NV > 0) {
 #pragma unroll
-            for (int k = 0; k < NV; ++k)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) ss = __builtin_fmaf(v[k][j], v[k][j], ss);
+            for (int k = 0; k < NV; ++k) squares(k, v[k]);
         } else {
             for (int64_t k = 0; k < steps; ++k) {
                 load(k, v[0]);
-                float t = 0.0f;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) t = __builtin_fmaf(v[0][j], v[0][j], t);
-                ss += t;
+                squares(k, v[0]);
             }
         }
 #pragma unroll
@@ -191,11 +197,11 @@ k_q8_rows(const Q8Args p) {
         rn = 1.0f / __builtin_sqrtf(ss / (float)p.K + p.eps);
     }
     auto finish = [&](int64_t k, float* o) {
-        const int64_t c = k * S + 8 * lane;
+        const int64_t c = column(k);
         if constexpr (RES) st8<T, VEC>(static_cast<T*>(p.sum) + row * p.K, c, p.K, o);
         if constexpr (NORM) {
             float w[8];
-            ld8<float, VEC>(p.w, c, p.K, w);
+            ld8<float, VEC, true>(p.w, inside(k), p.K, w);
 #pragma unroll
             for (int j = 0; j < 8; ++j) o[j] = o[j] * rn * w[j];
         }
@@ -219,7 +225,9 @@ k_q8_rows(const Q8Args p) {
 
 // One 128 x 128 square per workgroup: 16 lanes across, the rows in turn. Lanes past the last
 // row or column hold the last one instead, which leaves the largest magnitude as it is and the
-// loads without branches between them.
+// loads without branches between them. Bound by memory and the test for midpoints, which 1600
+// workgroups on 1024 places do not hide (10240 x 2560, bf16: 18.2 us, 4.3 TB/s; 15.2 without the test;
+// 256 and 1024 threads 19.3 and 19.0).
 constexpr int kSquareThreads = 512;
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kSquareThreads)
@@ -266,7 +274,12 @@ k_q8_square(const Q8Args p) {
 template <typename T, bool VEC, bool NORM, bool RES>
 hipError_t launch_q8_rows(const LaunchQ8& p, const Q8Args& a) {
     hipStream_t st = static_cast<hipStream_t>(p.stream);
-    const bool wave = p.M >= kQ8WaveRows && p.K <= 64 * 8 * 8;
+    // A wave per row where one step holds it (norm with residual, bf16: M 16384, K 512 11.4 us against
+    // 25.4 with four waves; M 64 2.7 both) or, with rows enough, two steps (K 1024: M 16384 19.0
+    // against 27.8, M 512 3.7 against 3.2) or five, where four waves need a second step for less than
+    // a third of it (K 2560: M 16384 40.1 against 52.8, M 1024 6.9 against 6.0). Else four waves
+    // (K 2048: M 4096 11.5 against 12.9; K 4096: M 16384 74 against 78).
+    const bool wave = p.K <= 512 || (p.M >= 1024 && p.K <= 1024) || (p.M >= 2048 && p.K > 2048 && p.K <= 2560);
     const int64_t steps = (p.K + (wave ? 512 : 2048) - 1) / (wave ? 512 : 2048);
     // a launch holds fewer than 2^32 lanes: rows past 2^22 go to launches of their own
     auto go = [&](auto kernel) {
@@ -284,8 +297,7 @@ hipError_t launch_q8_rows(const LaunchQ8& p, const Q8Args& a) {
     if (wave) {
         if (steps <= 1) go(k_q8_rows<T, VEC, NORM, RES, 64, 1>);
         else if (steps <= 2) go(k_q8_rows<T, VEC, NORM, RES, 64, 2>);
-        else if (steps <= 5) go(k_q8_rows<T, VEC, NORM, RES, 64, 5>);
-        else go(k_q8_rows<T, VEC, NORM, RES, 64, 8>);
+        else go(k_q8_rows<T, VEC, NORM, RES, 64, 5>);
     } else {
         if (steps <= 1) go(k_q8_rows<T, VEC, NORM, RES, 256, 1>);
         else if (steps <= 2) go(k_q8_rows<T, VEC, NORM, RES, 256, 2>);
