@@ -60,6 +60,7 @@ ss_status check_glr_dims(const ss_glr_dims* d, GlrCall call) {
     if (d->batch < 1 || d->d < 1 || (call != kStep && d->seqlen < 1))
         return fail(SS_ERR_INVALID_ARG, "batch, seqlen and d must be positive");
     if (d->d > (int64_t(1) << 26)) return fail(SS_ERR_INVALID_ARG, "d %lld above 2^26", (long long)d->d);
+    if (d->batch > INT32_MAX) return fail(SS_ERR_INVALID_ARG, "batch %lld not below 2^31", (long long)d->batch);
     if (call != kStep && d->seqlen >= (int64_t(1) << 31))
         return fail(SS_ERR_INVALID_ARG, "seqlen %lld not below 2^31", (long long)d->seqlen);
     if (d->io_dtype != SS_F32 && d->io_dtype != SS_BF16) return fail(SS_ERR_UNSUPPORTED, "io_dtype %d unknown", d->io_dtype);

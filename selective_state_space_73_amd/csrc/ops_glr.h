@@ -818,6 +818,8 @@ hipError_t launch_glr_t(const LaunchGlr& p) {
         if (!look) {
             if (p.L <= 64) go(k_glr_fwd<T, VEC, 4, 16>, 16);
             else go(k_glr_fwd<T, VEC, 8, 16>, 16);
+        } else if (p.chunk == 64) {
+            go(k_glr_scan<T, VEC, 8, 8>, 8);
         } else if constexpr (sizeof(T) == 2) {
             if (p.chunk == 256) go(k_glr_scan<T, VEC, 16, 16>, 16);
             else go(k_glr_scan<T, VEC, 16, 8>, 8);
@@ -825,11 +827,17 @@ hipError_t launch_glr_t(const LaunchGlr& p) {
             go(k_glr_scan<T, VEC, 8, 16>, 16);
         }
     } else {
-        // runs of 16 tokens; one chunk of up to 64 in runs of 4 (B 1, L 64, D 512: 10.7 us against 13.1,
-        // B 256, L 64, D 4096, bf16: 266 both; of 8 for up to 128, B 2, D 1024: 15.4 against 14.6)
-        constexpr int TT = 16;
-        if (p.chunk == 64) look ? go(k_glr_bwd<T, VEC, TT, 64 / TT, true>, 64 / TT) : go(k_glr_bwd<T, VEC, 4, 16, false>, 16);
-        else look ? go(k_glr_bwd<T, VEC, TT, 128 / TT, true>, 128 / TT) : go(k_glr_bwd<T, VEC, TT, 128 / TT, false>, 128 / TT);
+        // runs of 16 tokens, with few tiles of 8; one chunk (64 tokens then) in runs of 4 (B 1, L 64,
+        // D 512: 10.7 us against 13.1 with 16; B 256, L 64, D 4096, bf16: 266 both)
+        if (!look) {
+            go(k_glr_bwd<T, VEC, 4, 16, false>, 16);
+        } else if (glr_fine(true, p.batch, p.L, p.D)) {
+            go(k_glr_bwd<T, VEC, 8, 8, true>, 8);
+        } else if (p.chunk == 64) {
+            go(k_glr_bwd<T, VEC, 16, 4, true>, 4);
+        } else {
+            go(k_glr_bwd<T, VEC, 16, 8, true>, 8);
+        }
         hipLaunchKernelGGL(k_glr_da, dim3((unsigned)((p.D + 63) / 64)), dim3(1024), 0, st, p.part, p.g.dA,
                            p.nchunks * p.batch, (int)p.D);
     }

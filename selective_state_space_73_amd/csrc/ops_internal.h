@@ -10,6 +10,17 @@
 namespace selscan {
 
 constexpr int kGlrCols = 128;       // channels per workgroup of the recurrence kernels (2 per lane)
+// Few tiles: chunks of 64 tokens, whose runs of 8 by eight waves spread over more CUs (a CU's
+// arithmetic is what the time goes to there), as long as the chunks to wait for are not too many.
+// Forward, up to one such tile a CU: B 1, L 300, D 512, fp32 10.4 us against 14.2 with chunks of
+// 128, bf16 10.2 against 12.9; with 320 tiles (L 600, D 4096) 20.3 against 17.1, with L 4800, D 100
+// 20.2 against 18.1. Backward, up to 640 (two workgroups a CU): B 1, L 300, D 512 15.0 against
+// 20.8, B 3, L 1001, D 1537 (624 tiles) 47 against 51.6; B 8, L 500, D 2000 (1024) 58 against 55,
+// B 1, L 20000, D 512 78 against 68.
+inline bool glr_fine(bool backward, int64_t B, int64_t L, int64_t D) {
+    return L <= (backward ? 4096 : 2048) && B * ((D + kGlrCols - 1) / kGlrCols) * ((L + 63) / 64) <= (backward ? 640 : 256);
+}
+
 // Tokens of a forward chunk. Few rows of tiles, long sequences: twice as many, half as many
 // chunks to wait for (bf16: B 1, L 131072, D 2048 555 us against 620 with 128, B 3, L 16384,
 // D 512 64 against 73, B 1, L 262144, D 128 125 against 221); shorter, or with tiles enough, two
@@ -17,13 +28,14 @@ constexpr int kGlrCols = 128;       // channels per workgroup of the recurrence 
 // 20.2 with 256, B 8, L 2048, D 5120 165 against 180). fp32 runs have half the tokens, and a
 // workgroup no room for more waves.
 inline int64_t glr_fwd_chunk(bool bf16, int64_t B, int64_t L, int64_t D) {
+    if (L > 128 && glr_fine(false, B, L, D)) return 64;
     return bf16 && L >= 4096 && B * ((D + kGlrCols - 1) / kGlrCols) < 64 ? 256 : 128;
 }
 // Tokens of a backward chunk. With many rows of tiles the shorter one, whose four waves a CU has
 // twice (B 8, L 2048, D 5120, bf16: 313 us against 351 with 128); with few, half as many chunks
 // to wait for (B 1, L 65536, D 1024: 322 against 380).
 inline int64_t glr_bwd_chunk(int64_t B, int64_t L, int64_t D) {
-    return L <= 64 || B * ((D + kGlrCols - 1) / kGlrCols) >= 32 ? 64 : 128;
+    return glr_fine(true, B, L, D) || B * ((D + kGlrCols - 1) / kGlrCols) >= 32 ? 64 : 128;
 }
 
 // One launch of the recurrence, already validated by the C-ABI layer.

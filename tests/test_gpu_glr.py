@@ -104,7 +104,8 @@ def test_backward(B, L, D, io, kind):
 
 
 @pytest.mark.parametrize("io", ["f32", "bf16"])
-@pytest.mark.parametrize("B,L,D", [(2, 2, 4), (1, 61, 130), (2, 65, 9), (3, 113, 258), (1, 4096, 6), (1, 4097, 131), (2, 4356, 64)])
+@pytest.mark.parametrize("B,L,D", [(2, 2, 4), (1, 61, 130), (2, 65, 9), (3, 113, 258), (1, 4096, 6), (1, 4097, 131), (2, 4356, 64),
+                                   (1, 2048, 10), (1, 2049, 12), (2, 449, 2050), (3, 66, 4100), (33, 70, 128)])
 @pytest.mark.parametrize("kind", [None, "rare", "ends"])
 def test_lengths_at_which_tiles_change(B, L, D, io, kind):
     test_forward(B, L, D, io, kind)
