@@ -57,50 +57,78 @@ __device__ __forceinline__ uint64_t q8_eight(const float* v, const Q8Scale& s, b
     return (uint64_t)(uint32_t)b << 32 | (uint32_t)a;
 }
 
-typedef uint32_t q8_u4 __attribute__((ext_vector_type(4)));
-typedef float q8_f4 __attribute__((ext_vector_type(4)));
+// VEC: rows start on 16 bytes and K is a multiple of 8. Else accesses of eight values are still
+// one instruction (two for fp32), at the alignment of an element, which the memory pipeline takes
+// (M 16384, K 2561, bf16, norm with residual: 59 us; element by element 189).
+template <bool VEC> struct Q8Wide;
+template <> struct Q8Wide<true> {
+    typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+    typedef float f4 __attribute__((ext_vector_type(4)));
+    typedef __bf16 b8 __attribute__((ext_vector_type(8)));
+    typedef uint64_t u8;
+};
+template <> struct Q8Wide<false> {
+    typedef uint32_t u4 __attribute__((ext_vector_type(4), aligned(2)));
+    typedef float f4 __attribute__((ext_vector_type(4), aligned(4)));
+    typedef __bf16 b8 __attribute__((ext_vector_type(8), aligned(2)));
+    typedef uint64_t u8 __attribute__((aligned(1)));
+};
 
-// Eight consecutive values of a row from column c on; zeros past the end. VEC: the row starts
-// on 16 bytes and K is a multiple of 8. INSIDE: with VEC, c is known to be in the row.
-template <typename T, bool VEC, bool INSIDE = false>
+// Eight values of a row from column c on, or its last eight (K < 8 without VEC: what it has, then
+// zeros): no condition between the loads of one lane. ends8 puts the lanes at the end right.
+template <typename T, bool VEC>
 __device__ __forceinline__ void ld8(const T* row, int64_t c, int64_t K, float* v) {
-    if constexpr (VEC) {
-        if (!INSIDE && c >= K) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-        } else if constexpr (sizeof(T) == 2) {
-            const q8_u4 u = *reinterpret_cast<const q8_u4*>(row + c);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                v[2 * j] = __builtin_bit_cast(float, u[j] << 16);
-                v[2 * j + 1] = __builtin_bit_cast(float, u[j] & 0xffff0000u);
-            }
-        } else {
-            const q8_f4 a = *reinterpret_cast<const q8_f4*>(row + c), b = *reinterpret_cast<const q8_f4*>(row + c + 4);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) { v[j] = a[j]; v[4 + j] = b[j]; }
-        }
-    } else {
+    using W = Q8Wide<VEC>;
+    if (!VEC && K < 8) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = c + j < K ? IO<T>::ld(row + c + j) : 0.0f;
+        return;
+    }
+    const T* at = row + (c + 8 <= K ? c : K - 8);
+    if constexpr (sizeof(T) == 2) {
+        const typename W::u4 u = *reinterpret_cast<const typename W::u4*>(at);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[2 * j] = __builtin_bit_cast(float, u[j] << 16);
+            v[2 * j + 1] = __builtin_bit_cast(float, u[j] & 0xffff0000u);
+        }
+    } else {
+        const typename W::f4 a = *reinterpret_cast<const typename W::f4*>(at), b = *reinterpret_cast<const typename W::f4*>(at + 4);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) { v[j] = a[j]; v[4 + j] = b[j]; }
+    }
+}
+// The eight values as they belong to column c: zeros past the end. With VEC only whole eights lie
+// past it, which stand for nothing, and whose copies leave their block's largest magnitude as it is.
+template <bool VEC>
+__device__ __forceinline__ void ends8(int64_t c, int64_t K, float* v) {
+    if (!VEC && K >= 8 && c + 8 > K) {
+        const int by = c < K ? (int)(c + 8 - K) : 8;               // columns to move down: c's is at place `by`
+#pragma unroll
+        for (int s = 1; s <= 8; s *= 2)
+            if (by & s) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = j + s < 8 ? v[j + s] : 0.0f;
+            }
     }
 }
 
 template <typename T, bool VEC>
 __device__ __forceinline__ void st8(T* row, int64_t c, int64_t K, const float* v) {
-    if constexpr (VEC && sizeof(T) == 2) {
-        typedef float f8 __attribute__((ext_vector_type(8)));
-        typedef __bf16 b8 __attribute__((ext_vector_type(8)));
-        f8 f;
+    using W = Q8Wide<VEC>;
+    if (c + 8 <= K) {
+        if constexpr (sizeof(T) == 2) {
+            typedef float f8 __attribute__((ext_vector_type(8)));
+            typedef __bf16 b8 __attribute__((ext_vector_type(8)));
+            f8 f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = v[j];
-        if (c < K) *reinterpret_cast<b8*>(row + c) = __builtin_convertvector(f, b8);
-    } else if constexpr (VEC) {
-        if (c < K) {
-            *reinterpret_cast<q8_f4*>(row + c) = q8_f4{v[0], v[1], v[2], v[3]};
-            *reinterpret_cast<q8_f4*>(row + c + 4) = q8_f4{v[4], v[5], v[6], v[7]};
+            for (int j = 0; j < 8; ++j) f[j] = v[j];
+            *reinterpret_cast<typename W::b8*>(row + c) = __builtin_convertvector(f, b8);
+        } else {
+            *reinterpret_cast<typename W::f4*>(row + c) = typename W::f4{v[0], v[1], v[2], v[3]};
+            *reinterpret_cast<typename W::f4*>(row + c + 4) = typename W::f4{v[4], v[5], v[6], v[7]};
         }
-    } else {
+    } else if constexpr (!VEC) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             if (c + j < K) IO<T>::st(row + c + j, v[j]);
@@ -109,9 +137,9 @@ __device__ __forceinline__ void st8(T* row, int64_t c, int64_t K, const float* v
 
 template <bool VEC>
 __device__ __forceinline__ void st8_q(uint8_t* row, int64_t c, int64_t K, uint64_t u) {
-    if constexpr (VEC) {
-        if (c < K) *reinterpret_cast<uint64_t*>(row + c) = u;
-    } else {
+    if (c + 8 <= K) {
+        *reinterpret_cast<typename Q8Wide<VEC>::u8*>(row + c) = u;
+    } else if constexpr (!VEC) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             if (c + j < K) row[c + j] = (uint8_t)(u >> (8 * j));
@@ -152,14 +180,11 @@ k_q8_rows(const Q8Args p) {
 
     float v[NV ? NV : 1][8];
     auto column = [&](int64_t k) { return k * S + 8 * lane; };
-    // Lanes past the end of a row hold its last eight columns, which leaves a block's largest
-    // magnitude as it is, and the loads have no branches between them; the sum leaves them out.
-    auto inside = [&](int64_t k) { return VEC && column(k) >= p.K ? p.K - 8 : column(k); };
     auto load = [&](int64_t k, float* o) {
-        ld8<T, VEC, true>(x, inside(k), p.K, o);
+        ld8<T, VEC>(x, column(k), p.K, o);
         if constexpr (RES) {
             float r[8];
-            ld8<T, VEC, true>(res, inside(k), p.K, r);
+            ld8<T, VEC>(res, column(k), p.K, r);
 #pragma unroll
             for (int j = 0; j < 8; ++j) o[j] += r[j];
         }
@@ -168,6 +193,8 @@ k_q8_rows(const Q8Args p) {
     if constexpr (NV > 0) {
 #pragma unroll
         for (int k = 0; k < NV; ++k) load(k, v[k]);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) ends8<VEC>(column(k), p.K, v[k]);
     }
     if constexpr (NORM) {
         float ss = 0.0f;
@@ -183,6 +210,7 @@ k_q8_rows(const Q8Args p) {
         } else {
             for (int64_t k = 0; k < steps; ++k) {
                 load(k, v[0]);
+                ends8<VEC>(column(k), p.K, v[0]);
                 squares(k, v[0]);
             }
         }
@@ -201,7 +229,8 @@ k_q8_rows(const Q8Args p) {
         if constexpr (RES) st8<T, VEC>(static_cast<T*>(p.sum) + row * p.K, c, p.K, o);
         if constexpr (NORM) {
             float w[8];
-            ld8<float, VEC, true>(p.w, inside(k), p.K, w);
+            ld8<float, VEC>(p.w, c, p.K, w);
+            ends8<VEC>(c, p.K, w);
 #pragma unroll
             for (int j = 0; j < 8; ++j) o[j] = o[j] * rn * w[j];
         }
@@ -218,6 +247,7 @@ k_q8_rows(const Q8Args p) {
     } else {
         for (int64_t k = 0; k < steps; ++k) {
             load(k, v[0]);
+            ends8<VEC>(column(k), p.K, v[0]);
             finish(k, v[0]);
         }
     }
@@ -235,14 +265,15 @@ k_q8_square(const Q8Args p) {
     constexpr int DOWN = kSquareThreads / 16, N = 128 / DOWN;
     const int cx = threadIdx.x % 16 * 8, ry = threadIdx.x / 16;
     const int64_t c = (int64_t)blockIdx.x * 128 + cx, r0 = (int64_t)blockIdx.y * 128 + ry;
-    const int64_t held = VEC && c >= p.K ? p.K - 8 : c;
     auto row = [&](int k) {
         const int64_t r = r0 + DOWN * k;
         return static_cast<const T*>(p.x) + (r < p.M ? r : p.M - 1) * p.K;
     };
     float v[N][8], top = 0.0f;
 #pragma unroll
-    for (int k = 0; k < N; ++k) ld8<T, VEC, true>(row(k), held, p.K, v[k]);
+    for (int k = 0; k < N; ++k) ld8<T, VEC>(row(k), c, p.K, v[k]);
+#pragma unroll
+    for (int k = 0; k < N; ++k) ends8<VEC>(c, p.K, v[k]);
 #pragma unroll
     for (int k = 0; k < N; ++k)
 #pragma unroll
@@ -261,7 +292,8 @@ k_q8_square(const Q8Args p) {
         uint64_t u;
         if (__any(q8_near_middle(v[k], scale))) {      // values taken again: few waves come here
             float w[8];
-            ld8<T, VEC, true>(row(k), held, p.K, w);
+            ld8<T, VEC>(row(k), c, p.K, w);
+            ends8<VEC>(c, p.K, w);
             u = q8_eight(w, scale, true);
         } else {
             u = q8_eight(v[k], scale, false);
