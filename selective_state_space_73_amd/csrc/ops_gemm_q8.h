@@ -89,9 +89,9 @@ __device__ __forceinline__ void gq_store(const GemmQ8Args& p, int64_t m, int64_t
     if (m >= p.M || n >= p.N) return;
     const bool one = n >= p.split;
     const int64_t ld = one ? p.N - p.split : p.split, c = one ? n - p.split : n;
-    if (c + W <= ld && ((ld | p.split) & (W - 1)) == 0) {        // bases are 16-byte aligned: whole and aligned accesses
+    if (c + W <= ld) {                                           // in one matrix: whole accesses, wherever the row starts
         constexpr int A = 16 / sizeof(T) < W ? 16 / sizeof(T) : W;    // elements of one access
-        typedef T ta __attribute__((ext_vector_type(A)));
+        typedef T ta __attribute__((ext_vector_type(A), aligned(sizeof(T))));
         T* y = static_cast<T*>(one ? p.Y1 : p.Y0) + m * ld + c;
         const T* r = RES ? static_cast<const T*>(p.R) + m * ld + c : nullptr;
 #pragma unroll
