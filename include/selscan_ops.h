@@ -109,8 +109,9 @@ ss_status ss_glr_bwd(const ss_glr_dims* dims, const ss_glr_args* args, const ss_
  * columns of one row (scale [M, ceil(K/128)], activations) or of 128 consecutive rows
  * ("square": scale [ceil(M/128), ceil(K/128)], weights); blocks at the ends are smaller.
  *   scale = max(max |v| / 448, 2^-126),   q = e4m3(v / scale), to nearest, ties to even
- * (of the quotient itself, from 2^-6 on: it is not rounded to fp32 first, nor taken by the
- * stored scale's rounding).
+ * (of the quotient 448 v / max |v| itself: neither it nor the scale is rounded to fp32 first.
+ * With fp32 v, and behind the norm, quotients below 2^-6 that lie within two fp32 steps of the
+ * middle between two e4m3 values may go to either).
  * A NaN becomes a NaN and leaves its block's scale alone; an infinity makes its block's scale
  * infinite (its finite values stand for NaN then). All matrices are contiguous row-major. */
 typedef struct {

@@ -130,6 +130,21 @@ def half_step(v, scale):
     return torch.maximum(v.abs() * 2.0 ** -4, scale * 2.0 ** -10)
 
 
+def nearest(v, top):
+    """The e4m3 value nearest to 448 v / top (to v 2^126 under the smallest scale), ties to even,
+    for v of at most 24 bits and top >= |v| of its block, element by element: 448 v and a midpoint
+    times top both fit in 53 bits, so the two sides are compared exactly."""
+    v, top = v.cpu().to(F64), top.cpu().to(F64).clamp_min(Q8_MAX * Q8_TINY)
+    a = Q8_MAX * v.abs()
+    step = torch.ldexp(torch.ones_like(a), (torch.frexp(a / top)[1] - 4).clamp_min(-9))
+    k = torch.floor(a / top / step)
+    k = torch.where(k * step * top > a, k - 1, k)                   # the quotient itself was rounded
+    k = torch.where((k + 1) * step * top <= a, k + 1, k)
+    mid = (k + 0.5) * step * top
+    up = (a > mid) | ((a == mid) & (k % 2 == 1))
+    return torch.copysign((k + up.to(F64)) * step, v)
+
+
 # ---------------------------------------------------------------------------
 # the block with 8-bit projections, in pieces that a rounding separates
 

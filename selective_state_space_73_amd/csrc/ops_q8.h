@@ -2,7 +2,7 @@
 // and the RMS norm (ss_norm_q8).
 //
 //   s = x + residual;  n = s / sqrt(mean(s^2) + eps) * w
-//   per block: scale = max(max |n| / 448, 2^-126),  q = e4m3(n / scale), from the unrounded scale
+//   per block: scale = max(max |n| / 448, 2^-126),  q = e4m3(448 n / max |n|)
 //
 // Both are bound by memory: a value is read once, kept in registers through the sums and
 // maxima it takes part in, and its byte is written once.
@@ -15,46 +15,70 @@ namespace selscan {
 constexpr float kQ8Max = 448.0f;             // largest finite e4m3 value
 constexpr float kQ8TinyScale = 0x1p-126f;    // smallest scale: its reciprocal is finite
 
-// A block's scale, and 448 / max |v| (2^126 under the smallest scale) as the sum of two floats.
-struct Q8Scale { float scale, hi, lo; };
+// A block's scale, its largest magnitude (448 2^-126 under the smallest scale) and 448 over that.
+struct Q8Scale { float scale, hi, top; };
 __device__ __forceinline__ Q8Scale q8_scale(float top) {
-    const float s = top / kQ8Max;
-    if (s < kQ8TinyScale) return Q8Scale{kQ8TinyScale, 0x1p126f, 0.0f};
-    const float hi = kQ8Max / top;
-    return Q8Scale{s, hi, __builtin_fmaf(-hi, top, kQ8Max) * (hi / kQ8Max)};
+    if (top < kQ8Max * kQ8TinyScale) return Q8Scale{kQ8TinyScale, 0x1p126f, kQ8Max * kQ8TinyScale};
+    return Q8Scale{top / kQ8Max, kQ8Max / top, top};
 }
-// v / scale where its side of an fp32 step counts: not rounded to nearest, but to the odd one of
-// the two fp32 neighbours where the quotient is between them.
-__device__ __forceinline__ float q8_odd(float v, const Q8Scale& s) {
-    const float t = v * s.hi;
-    const float rest = __builtin_fmaf(v, s.lo, __builtin_fmaf(v, s.hi, -t));
-    const int b = __builtin_bit_cast(int, t);
-    const int away = (__builtin_bit_cast(int, rest) ^ b) >> 31 | 1;       // towards the remainder: 1 away from 0, -1 back
-    return __builtin_bit_cast(float, (b & 1) || rest == 0.0f ? b : b + away);
+// t = v hi is within 1.5 fp32 steps of the quotient 448 v / top (a rounded reciprocal, a rounded
+// product), so that it goes to the right e4m3 value unless it lies that near to the middle between
+// two. How middles are decided depends on where v comes from.
+//
+// A bf16 v over a bf16 top (8 bits each): if 448 v and middle * top (5 bits) differ, both whole
+// multiples of one power of two, they do by 2^-13 of themselves at least. So t rounded to 16 bits is
+// a middle where the quotient is one, and on the quotient's side of it everywhere else.
+__device__ __forceinline__ float q8_to16(float t) {
+    return __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, t) + 0x80u) & ~0xffu);
 }
-// Eight values as eight e4m3 bytes, each quotient rounded to the nearest (ties to even). The
-// product with the rounded 448 / max |v| is within two fp32 steps of the quotient; where it is
-// that near to the middle between two e4m3 values (a few in a million), it may go to the wrong
-// one. From 2^-6 on the middles are the fp32 numbers whose last 20 bits are a one and zeros; a
-// wave that comes near one takes its values to odd, where no middle is met that is none.
-// (Below, where e4m3 has steps of 2^-9, it is left at that.)
+// Any v: from 2^-6 on the middles are the fp32 numbers whose last 20 bits are a one and zeros. A
+// t within two steps of one (a few in a million) is decided by 448 v against middle * top, each
+// exactly as the sum of two floats, at top's exponent. (Below, where e4m3 has steps of 2^-9, it is
+// left at t.)
+__device__ __forceinline__ uint32_t q8_past_middle(float t) {         // two steps below a middle on: 0x1000 a step
+    return (__builtin_bit_cast(uint32_t, t) << 12) + 0x80002000u;
+}
 __device__ __forceinline__ bool q8_near_middle(const float* v, const Q8Scale& s) {
-    uint32_t least = ~0u;                          // last 20 bits, counted from two below a middle
+    uint32_t least = ~0u;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const uint32_t from = (__builtin_bit_cast(uint32_t, v[j] * s.hi) << 12) + 0x80002000u;
+        const uint32_t from = q8_past_middle(v[j] * s.hi);
         least = from < least ? from : least;
     }
     return least <= 0x4000u;
 }
-__device__ __forceinline__ uint64_t q8_eight(const float* v, const Q8Scale& s, bool odd) {
-    float t[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) t[j] = odd ? q8_odd(v[j], s) : v[j] * s.hi;
+__device__ __forceinline__ float q8_decided(float v, const Q8Scale& s) {
+    const float t = v * s.hi;
+    const uint32_t b = __builtin_bit_cast(uint32_t, t), m = ((b & 0x7fffffffu) + 4u) & ~7u;
+    const float a = __builtin_ldexpf(__builtin_fabsf(v), -__builtin_amdgcn_frexp_expf(s.top)), c = __builtin_amdgcn_frexp_mantf(s.top);
+    const float mid = __builtin_bit_cast(float, m);
+    const float p = kQ8Max * a, q = mid * c;
+    const float d = p != q ? p - q : __builtin_fmaf(kQ8Max, a, -p) - __builtin_fmaf(mid, c, -q);
+    const uint32_t side = m + (d > 0.0f ? 1u : 0u) - (d < 0.0f ? 1u : 0u);
+    return q8_past_middle(t) <= 0x4000u ? __builtin_bit_cast(float, side | (b & 0x80000000u)) : t;
+}
+__device__ __forceinline__ uint64_t q8_bytes(const float* t) {
     int a = __builtin_amdgcn_cvt_pk_fp8_f32(t[0], t[1], 0, false), b = __builtin_amdgcn_cvt_pk_fp8_f32(t[4], t[5], 0, false);
     a = __builtin_amdgcn_cvt_pk_fp8_f32(t[2], t[3], a, true);
     b = __builtin_amdgcn_cvt_pk_fp8_f32(t[6], t[7], b, true);
     return (uint64_t)(uint32_t)b << 32 | (uint32_t)a;
+}
+// Eight values as eight e4m3 bytes, each quotient rounded to the nearest, ties to even. SHORT: bf16
+// values of bf16 blocks.
+template <bool SHORT>
+__device__ __forceinline__ uint64_t q8_eight(const float* v, const Q8Scale& s) {
+    float t[8];
+    if constexpr (SHORT) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) t[j] = q8_to16(v[j] * s.hi);
+    } else if (__any(q8_near_middle(v, s))) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) t[j] = q8_decided(v[j], s);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) t[j] = v[j] * s.hi;
+    }
+    return q8_bytes(t);
 }
 
 // VEC: rows start on 16 bytes and K is a multiple of 8. Else accesses of eight values are still
@@ -235,10 +259,7 @@ k_q8_rows(const Q8Args p) {
             for (int j = 0; j < 8; ++j) o[j] = o[j] * rn * w[j];
         }
         const Q8Scale scale = q8_scale(top16(o));
-        uint64_t u;
-        if (__any(q8_near_middle(o, scale))) u = q8_eight(o, scale, true);
-        else u = q8_eight(o, scale, false);
-        st8_q<VEC>(p.q + row * p.K, c, p.K, u);
+        st8_q<VEC>(p.q + row * p.K, c, p.K, q8_eight<!NORM && sizeof(T) == 2>(o, scale));
         if (lane % 16 == 0 && c < p.K) p.scale[row * p.KB + c / 128] = scale.scale;
     };
     if constexpr (NV > 0) {
@@ -255,9 +276,8 @@ k_q8_rows(const Q8Args p) {
 
 // One 128 x 128 square per workgroup: 16 lanes across, the rows in turn. Lanes past the last
 // row or column hold the last one instead, which leaves the largest magnitude as it is and the
-// loads without branches between them. Bound by memory and the test for midpoints, which 1600
-// workgroups on 1024 places do not hide (10240 x 2560, bf16: 18.2 us, 4.3 TB/s; 15.2 without the test;
-// 256 and 1024 threads 19.3 and 19.0).
+// loads without branches between them. Bound by memory (10240 x 2560, bf16: 14.0 us, 5.6 TB/s,
+// part of it from the last cache).
 constexpr int kSquareThreads = 512;
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kSquareThreads)
@@ -289,15 +309,7 @@ k_q8_square(const Q8Args p) {
 #pragma unroll
     for (int k = 0; k < N; ++k) {
         const int64_t r = r0 + DOWN * k;
-        uint64_t u;
-        if (__any(q8_near_middle(v[k], scale))) {      // values taken again: few waves come here
-            float w[8];
-            ld8<T, VEC>(row(k), c, p.K, w);
-            ends8<VEC>(c, p.K, w);
-            u = q8_eight(w, scale, true);
-        } else {
-            u = q8_eight(v[k], scale, false);
-        }
+        const uint64_t u = q8_eight<sizeof(T) == 2>(v[k], scale);
         if (r < p.M) st8_q<VEC>(p.q + r * p.K, c, p.K, u);
     }
     if (threadIdx.x == 0) p.scale[(int64_t)blockIdx.y * p.KB + blockIdx.x] = scale.scale;
