@@ -166,12 +166,11 @@ def block_core(xi, z, W, R, ssm_state, conv_state, zoh=False):
 def rounded_product(y, slack, wq, ws, out_half):
     """(y W^T, how far the 8-bit product of y may be from it), element by element, for y [M,K]
     (64-bit) known to +-slack [M,K] before it is rounded to 8 bits: half a step (taken from the
-    true value: slack once more covers the difference) for each value, then fp32 sums of K terms,
-    and for a 16-bit output (out_half > 2^-24) the small terms the matrix cores drop beside
-    large ones, 2^-10 of the terms' sizes; the output's own rounding is the caller's."""
+    true value: slack once more covers the difference) for each value, then fp32 sums of K terms;
+    the output's own rounding (out_half) is the caller's."""
     w = values(wq, ws, square=True).abs()
     y = torch.as_tensor(y, dtype=F64)
     per = spread(block_tops(y) / Q8_MAX, *y.shape).clamp_min(Q8_TINY)
     off = half_step(y, per) + 2 * torch.as_tensor(slack, dtype=F64)
-    sums = 2.0 ** -15 + (2.0 ** -10 if out_half > 2.0 ** -24 else 0.0)
+    sums = 2.0 ** -15
     return y @ values(wq, ws, square=True).T, off @ w.T + sums * ((y.abs() + off) @ w.T)

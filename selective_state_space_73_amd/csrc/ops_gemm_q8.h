@@ -7,13 +7,13 @@
 // holds one row m of X (l % 16) and four consecutive rows n of W (4 (l / 16) + v): its block
 // scale is one number.
 //
-// Precision of a block's sum. v_mfma_f32_16x16x128_f8f6f4 (as the older 16x16x32 fp8 form)
-// adds the products of eight neighbouring k on a common exponent and drops what lies below
-// 2^-13 of the largest of them (measured: a second product survives at 2^-13 and is lost at
-// 2^-14 within eight k, at 2^-23 and 2^-24 further apart); normal data come out 1.5e-5 off, in
-// the 2-norm. Outputs in bf16, which are rounded by 2^-9 or so anyway, take it. Outputs in
-// fp32 convert the operands to bf16, which holds every e4m3 value, and take the bf16 form,
-// whose products and sums keep fp32 (1e-8 off), at half the rate.
+// Precision of a block's sum. The 8-bit matrix instructions add the products of eight neighbouring k
+// on a common exponent and drop what lies below 2^-13 of the largest (measured: a second product
+// survives at 2^-13 and is lost at 2^-14 within eight k, at 2^-23 and 2^-24 further apart): two
+// large products that cancel take a small one with them. So both operands are converted to bf16,
+// which holds every e4m3 value, for the bf16 instruction, whose products and sums keep fp32 (1e-8
+// off), at half the rate: bf16 out, M 16384, N 10240, K 2560 867 us against 478, M 64 with W from memory
+// 11.7 against 11.2.
 //
 // Both operands are k-contiguous and a sum over k has no order of its own here, so a lane's
 // 32 bytes of an operand may be any two 16-byte chunks of the block as long as both operands
@@ -26,23 +26,13 @@
 
 namespace selscan {
 
-typedef int gq_i8 __attribute__((ext_vector_type(8)));
 typedef int gq_i4 __attribute__((ext_vector_type(4)));
 typedef float gq_f4 __attribute__((ext_vector_type(4)));
 typedef __bf16 gq_b8 __attribute__((ext_vector_type(8)));
 typedef __bf16 gq_b2 __attribute__((ext_vector_type(2)));
 
-// A lane's 32 bytes of one operand, as the matrix instruction of an output type takes them.
-template <typename T> struct GqFrag;
-template <> struct GqFrag<uint16_t> {
-    gq_i8 v;
-    __device__ __forceinline__ void set(gq_i4 a, gq_i4 b) { v = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7); }
-    static __device__ __forceinline__ gq_f4 dot(const GqFrag& a, const GqFrag& b) {
-        // operand formats 0, 0: e4m3; block exponents 0: the unscaled instruction
-        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a.v, b.v, gq_f4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
-    }
-};
-template <> struct GqFrag<float> {
+// A lane's 32 bytes of one operand as four operands of the bf16 instruction.
+struct GqFrag {
     gq_b8 v[4];
     __device__ __forceinline__ void set(gq_i4 a, gq_i4 b) {
 #pragma unroll
@@ -54,13 +44,16 @@ template <> struct GqFrag<float> {
             v[j / 2][4 * (j % 2) + 2] = hi[0]; v[j / 2][4 * (j % 2) + 3] = hi[1];
         }
     }
-    static __device__ __forceinline__ gq_f4 dot(const GqFrag& a, const GqFrag& b) {
-        gq_f4 q{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) q = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v[j], b.v[j], q, 0, 0, 0);
-        return q;
-    }
 };
+// A block's products of one row fragment with N column fragments, the N sums taking turns.
+template <int N>
+__device__ __forceinline__ void gq_dot(const GqFrag& a, const GqFrag (&x)[N], gq_f4 (&q)[N]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int b = 0; b < N; ++b)
+            q[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v[j], x[b].v[j], j ? q[b] : gq_f4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+}
 
 // 64 lanes' 16-byte chunks from a matrix straight into 1024 consecutive bytes of LDS: byte
 // offset voff (per lane) + soff from the base, which may lie anywhere in memory.
@@ -143,10 +136,9 @@ __device__ __forceinline__ GqTile gq_tile(unsigned id, int tiles_m, int tiles_n)
 // chunk over the banks; the transfers write LDS in lane order, so the permutation is in what
 // they fetch. Rows past the end repeat the last one, chunks past K are zero.
 //
-// 256 x 256 tiles, eight waves of 128 x 64: M 16384, N 10240, K 2560 465 us = 1.85 PFLOP/s, half of
-// what the matrix instructions alone reach. The transfers cost 100 us (344 without; not for
-// misses: 422 with every block from the L2), the epilogue 24, the rest is LDS reads behind the
-// barrier of each block, which two waves a SIMD hide in part.
+// 128 x 128 tiles, four waves of 64 x 64: M 16384, N 10240, K 2560, bf16 out 867 us = 0.99 PFLOP/s (fp32 out
+// 914), where a bf16 library product of 8192^3 reaches 1.16: bound by the bf16 matrix instructions
+// and the conversions (two vector instructions for each of them). Tiles of 256 x 256 spill.
 __device__ __forceinline__ int gq_key_w(int row) { return (row >> 1 & 1) | (row >> 3 & 3) << 1; }
 __device__ __forceinline__ int gq_key_x(int row) { return row >> 1 & 7; }
 
@@ -156,7 +148,7 @@ k_gemm_q8(const GemmQ8Args p, int tiles_m, int tiles_n) {
     constexpr int TN = 16 * NF * WN, TM = 16 * MF * WM, TH = 64 * WN * WM;
     constexpr int CW = TN * 8 / TH, CX = TM * 8 / TH;             // 16-byte chunks per thread and block
     static_assert(128 % (16 * NF) == 0, "one scale of W per wave");
-    using Frag = GqFrag<T>;
+    using Frag = GqFrag;
     __shared__ gq_i4 sW[2][TN * 8], sX[2][TM * 8];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -281,8 +273,7 @@ k_gemm_q8(const GemmQ8Args p, int tiles_m, int tiles_n) {
             if (a < NF) {
                 const Frag cur = fw;
                 if (a + 1 < NF) fw = frag_w(buf, a + 1);
-#pragma unroll
-                for (int b = 0; b < MF; ++b) t[b] = Frag::dot(cur, fx[b]);
+                gq_dot(cur, fx, t);
             }
             if (a > 0) {
 #pragma unroll
@@ -294,12 +285,12 @@ k_gemm_q8(const GemmQ8Args p, int tiles_m, int tiles_n) {
             }
 #pragma unroll
             for (int b = 0; b < MF; ++b) q[b] = t[b];
-            // one matrix instruction, then the four additions that run in its shadow
+            // one matrix instruction, then two of the additions and conversions that run in its shadow
             if (a + 1 < NF) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
 #pragma unroll
-            for (int b = 0; b < MF; ++b) {
+            for (int b = 0; b < 4 * MF; ++b) {
                 if (a < NF) __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                if (a > 0) __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+                __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);
             }
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -342,7 +333,7 @@ k_gemm_q8_split(const GemmQ8Args p, int tiles_m, int tiles_n) {
     static_assert(128 % TN == 0 && (TN * 8) % 64 == 0 && (TM * 8) % 64 == 0 && TM <= 64, "one scale of W; whole transfers");
     static_assert(TM * LD * 4 <= 2 * BUF * 16, "the sums fit in the block buffers");
     static_assert(TN * 8 % TH == 0 && (TM * 8 % TH == 0 || CX == 1), "no condition on W's transfers, one on X's");
-    using Frag = GqFrag<T>;
+    using Frag = GqFrag;
     __shared__ gq_i4 lds[KS][2 * BUF];
     const int tid = threadIdx.x % TH, lane = tid & 63;
     const int grp = __builtin_amdgcn_readfirstlane(threadIdx.x / TH);
@@ -425,12 +416,12 @@ k_gemm_q8_split(const GemmQ8Args p, int tiles_m, int tiles_n) {
 #pragma unroll
         for (int a = 0; a < NF; ++a) {
             const Frag fw = frag(buf, wn * 16 * NF + 16 * a);
+            gq_f4 q[MF];
+            gq_dot(fw, fx, q);
 #pragma unroll
-            for (int b = 0; b < MF; ++b) {
-                const gq_f4 q = Frag::dot(fw, fx[b]);
+            for (int b = 0; b < MF; ++b)
 #pragma unroll
-                for (int v = 0; v < 4; ++v) acc[a][b][v] = __builtin_fmaf(q[v], sc[b], acc[a][b][v]);
-            }
+                for (int v = 0; v < 4; ++v) acc[a][b][v] = __builtin_fmaf(q[b][v], sc[b], acc[a][b][v]);
         }
     };
     stage(grp, lds[grp]);
@@ -461,20 +452,22 @@ k_gemm_q8_split(const GemmQ8Args p, int tiles_m, int tiles_n) {
     }
 }
 
-// Which kernel (measured, microseconds, bf16 outputs; fp32 ones are 10 to 60 percent above with the
-// same order). The smallest of these tiles of which there are no more than CUs, so that each has a
-// CU to itself, whose waves split k four or eight ways:
-//  - 16 x 32: M 16, N 2560, K 5120 5.2 (16 x 64: 7.1), M 32 5.4 (32 x 32: 6.2);
-//  - 16 x 64 where X has no more rows: M 16, N 10240, K 2560 5.5 (64 x 64: 6.9; fp32 6.0, 32 x 64 6.6);
-//  - 32 x 32: M 64, N 2560, K 5120 6.5 (32 x 64: 7.9);
-//  - 32 x 64: M 32, N 10240, K 2560 5.4 (64 x 64: 6.8);
-//  - 64 x 64: M 201, N 2561, K 5120 12.0 (split two ways 17.2, 32 x 64 20.7), M 64, N 10240, K 2560 7.2 (9.4).
+// Which kernel (measured, microseconds, bf16 outputs; fp32 ones are up to 5 percent above). The smallest
+// of these tiles of which there are no more than CUs, so that each has a CU to itself, whose waves
+// split k four or eight ways (at K 128 and 512 they are within 0.6 of each other, 3.8 to 4.8):
+//  - 16 x 32: M 16, N 2560, K 2048 4.3 (16 x 64: 5.8), K 8192 10.4 (16.7);
+//  - 16 x 64 where X has no more rows: M 16, N 10240, K 2048 6.9 (64 x 64: 7.8, 16 x 32 8.6), K 8192 18.9 (21.1, 22.8);
+//  - 32 x 32: M 64, N 2560, K 2048 5.0 (32 x 64: 6.0), K 8192 11.9 (16.7);
+//  - 32 x 64: M 32, N 10240, K 2048 7.2 (64 x 64: 8.2), K 8192 19.6 (21.4);
+//  - 64 x 64: M 200, N 2560, K 2048 7.8 (32 x 64: 10.7, split two ways 9.1), K 8192 22.0 (31.7, 28.9).
 // With more, k split two ways and two workgroups to a CU or more: 32 x 64 for a single row of tiles
-// (M 64, N 40960, K 2560 20.5; 64 x 64: 23.3), else the least of what n = tiles / CUs, rounded
-// up, cost per 2560 of K:
-//  - 64 x 64, about 5 n + 1 (fp32 7 n + 2): M 192, N 10240 12.1 (n 2), M 512 28.6 (5), M 1024 49.9 (10);
-//  - 128 x 128, 13 n + 8 (22 n): M 512, N 10240 31.3 (n 2), M 1024 48.7 (3), M 2048 74.4 (5);
-//  - 256 x 256, 40 n: M 1024, N 10240 42 (n 1), M 2048 80 (2), M 16384, N 2560 123 (3); not for fp32.
+// (M 64, N 40960, K 512 8.4, K 2048 20.2; 64 x 64: 9.5, 21.2; 128 x 128: 11.4, 31.9), else the cheaper by
+// n = tiles / CUs, rounded up, and KB = blocks of k, in twentieths of a microsecond:
+//  - 64 x 64: n (16 + 6 KB) + 2 KB;
+//  - 128 x 128: n (28 + 19 KB) + 3 KB.
+// 64 x 64 against 128 x 128 at K 128, 512, 2048, 8192: M 192, N 10240 4.7 4.8, 6.1 8.0, 14.2 22.2, 45.6 77.4;
+// M 512 9.2 6.9, 12.3 12.4, 32.2 35.3, 110 128; M 1024 15.5 9.7, 21.8 16.9, 60.4 51.6, 215 190; M 2048 27.3 14.4,
+// 40.3 26.6, 114 88, 413 319; M 1500, N 3000 9.0 6.5, 12.2 11.9, 30.3 34.0, 104 124.
 constexpr int64_t kGqCUs = 256;
 template <typename T, bool RES>
 hipError_t launch_gemm_q8_t(const LaunchGemmQ8& p) {
@@ -497,14 +490,9 @@ hipError_t launch_gemm_q8_t(const LaunchGemmQ8& p) {
     constexpr int64_t kMost = int64_t(1) << 22;
     if (p.M <= 64 && count(32, 64) <= kMost) return go(k_gemm_q8_split<T, RES, 2, 2, 2, 1, 2>, 32, 64, 256, kAll);
     auto turns = [&](int64_t m, int64_t n) { return (count(m, n) + kGqCUs - 1) / kGqCUs; };
-    constexpr bool kHalf = sizeof(T) == 2;
-    const int64_t t64 = kHalf ? 5 * turns(64, 64) + 1 : 7 * turns(64, 64) + 2;
-    const int64_t t128 = kHalf ? 13 * turns(128, 128) + 8 : 22 * turns(128, 128);
-    // the grids of the persistent kernels are multiples of the eight XCDs: a workgroup's tiles stay on one
-    if constexpr (kHalf) {
-        const int64_t t256 = 40 * turns(256, 256);
-        if (t256 <= t64 && t256 <= t128) return go(k_gemm_q8<T, RES, 8, 4, 2, 4>, 256, 256, 512, kGqCUs);
-    }
+    const int64_t kb = a.KB;
+    const int64_t t64 = turns(64, 64) * (16 + 6 * kb) + 2 * kb, t128 = turns(128, 128) * (28 + 19 * kb) + 3 * kb;
+    // the grid of the persistent kernel is a multiple of the eight XCDs: a workgroup's tiles stay on one
     if (t64 < t128 && count(64, 64) <= kMost) return go(k_gemm_q8_split<T, RES, 2, 4, 2, 1, 2>, 64, 64, 256, kAll);
     return go(k_gemm_q8<T, RES, 4, 4, 2, 2>, 128, 128, 256, 2 * kGqCUs);
 }
