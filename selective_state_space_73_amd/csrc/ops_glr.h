@@ -50,14 +50,15 @@ __device__ __forceinline__ float sigmoid(float v) { return rcp_fast(1.0f + exp2_
 
 // The decay near 1 is what a long memory is made of: a = 1 + expm1(A s) has the rounding of the
 // sum alone there, and 1 - a^2 = -e (1 + a) with e = expm1(A s) keeps its relative accuracy
-// where 1 - a * a would cancel. `bias` is added to A s: 0, or minus infinity for a reset, which
-// gives a = 0 and 1 - a^2 = 1.
+// where 1 - a * a would cancel. Further out a is the exponential itself: a sum with 1 would leave a
+// small decay, which the gradients have as a factor, whole steps of 2^-24. `bias` is added to A s:
+// 0, or minus infinity for a reset, which gives a = 0 and 1 - a^2 = 1.
 struct Decay { float a, w2; };            // exp(A s), 1 - a^2
 __device__ __forceinline__ Decay glr_decay(float s, float A, float bias) {
     const float la = __builtin_fmaf(A, s, bias);
-    const float far = exp2_fast(kLog2e * la) - 1.0f, near = expm1_small(la);
-    const float e = __builtin_fabsf(la) < kEm1Small ? near : far;
-    const float a = 1.0f + e;
+    const float far = exp2_fast(kLog2e * la), near = expm1_small(la);
+    const bool small = __builtin_fabsf(la) < kEm1Small;
+    const float e = small ? near : far - 1.0f, a = small ? 1.0f + near : far;
     return Decay{a, -__builtin_fmaf(e, a, e)};
 }
 

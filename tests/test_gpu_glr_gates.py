@@ -1,0 +1,75 @@
+"""GPU: the gated linear recurrence's gates far out: decays that are small, gates that are nearly
+shut or open, write coefficients that underflow.
+
+Tolerances, relative to each element. With u = 2^-24: exp2 of an argument c carries |c| u ln 2 by
+the argument's rounding; so for gates of |r| <= q a sigmoid and its complement are off by at most
+2 (q + 4) u (argument, exp2, addition, reciprocal, product). A decay exp(A s) is off by
+|A s| (4 + the sigmoid's) u. A gradient here is a product of one decay or write coefficient, both
+sigmoids, one complement and inputs, 12 roundings, with no sums that cancel. For |A s| <= 20 and
+q <= 20 that is under (20 * 56 + 4 * 48 + 12) u < 2^-13.
+"""
+import pytest
+import torch
+
+from oracle import ops as O
+
+pytestmark = pytest.mark.gpu
+
+ss = pytest.importorskip("selective_state_space_73_amd")
+REL = 2.0 ** -13
+
+
+def close(got, want, rel=REL, floor=1e-36):
+    got, want = got.detach().double().cpu(), want.double().cpu()
+    worst = ((got - want).abs() / (rel * want.abs() + floor)).max().item()
+    print(f"worst error over bound {worst:.3g}", flush=True)
+    assert torch.isfinite(got).all() and worst <= 1.0
+
+
+def both(x, r, i, A, h0, dy, dh, reset=None):
+    x, r, i, dy = (t.cuda() for t in (x, r, i, dy))
+    B, L, D = x.shape
+    ck = torch.empty(ss.glr_ckpt_shape(B, L, D), device="cuda")
+    h = h0.cuda().clone()
+    y = ss.ss_glr_fwd(x, r, i, A.cuda(), state=h, reset=reset, ckpt=ck)
+    return y, h, ss.ss_glr_bwd(x, r, i, A.cuda(), ck, dy, reset=reset, dstate_final=dh.cuda())
+
+
+@pytest.mark.parametrize("L", [1, 2, 5])
+@pytest.mark.parametrize("D", [64, 33])
+def test_small_decays(L, D):
+    """exp(A s) between e^-20 and e^-8, nothing written: a state of a^L, gradients with a factor a."""
+    g = torch.Generator().manual_seed(L)
+    x = torch.zeros(1, L, D)
+    r, i = torch.randn(1, L, D, generator=g), torch.randn(1, L, D, generator=g)
+    A = -torch.linspace(8, 20, D) / torch.sigmoid(r[0].max(0).values)
+    if L > 2:
+        A = A / 3                                                       # a^L stays far from the smallest number
+    h0, dh = 1 + torch.rand(1, D, generator=g), 1 + torch.rand(1, D, generator=g)
+    dy = torch.zeros(1, L, D)
+    y, h, got = both(x, r, i, A, h0, dy, dh)
+    yw, hw, _ = O.glr_fwd(x, r, i, A, h0)
+    close(y, yw)
+    close(h, hw)
+    want = O.glr_bwd(x, r, i, A, dy, h0, None, dh)
+    for k in ("dr", "dA", "dstate_init"):
+        print(k, end=" ")
+        close(got[k], want[k][0])
+    hs = h0.cuda().clone()
+    ys = ss.ss_glr_step(x[:, 0].cuda(), r[:, 0].cuda(), i[:, 0].cuda(), A.cuda(), hs)
+    close(ys, yw[:, 0])
+    assert torch.equal(ys, hs)
+
+
+@pytest.mark.parametrize("L", [1, 40])
+def test_decays_from_long_memories_to_none(L):
+    """exp(A s) from 1 - 2^-20 to e^-20, element by element, over the place where its evaluation changes."""
+    D = 2048
+    la = -torch.logspace(-6, 1.3, D)
+    r = torch.zeros(1, L, D)
+    A = 2 * la / L
+    x, i = torch.zeros(1, L, D), torch.zeros(1, L, D)
+    h0 = torch.ones(1, D)
+    y, _, got = both(x, r, i, A, h0, torch.zeros(1, L, D), torch.ones(1, D))
+    close(y, O.glr_fwd(x, r, i, A, h0)[0])
+    close(got["dstate_init"], O.glr_bwd(x, r, i, A, torch.zeros(1, L, D), h0, None, torch.ones(1, D))["dstate_init"][0])
