@@ -97,7 +97,7 @@ typedef struct {
  * the initial state is read from the first checkpoint). With g_t the gradient of h_t,
  *   g_t = dy_t + a_{t+1} g_{t+1},        v_t = sigmoid(i_t) x_t,
  *   d(A s_t) = g_t (a_t h_{t-1} - (a_t^2 / w_t) v_t)   (0 at a reset; without the second
- *                                                      term where A s_t = 0 makes w_t = 0).
+ *                                        term where w_t^2 is 0 or below the smallest normal fp32).
  * Outputs are overwritten; none may overlap an input, another output or the workspace. */
 ss_status ss_glr_bwd(const ss_glr_dims* dims, const ss_glr_args* args, const ss_glr_grads* grads, void* workspace,
                      size_t workspace_bytes, void* stream);

@@ -681,8 +681,9 @@ k_glr_bwd(const GlrArgs p) {
             for (int j = 0; j < 2; ++j) {
                 asm volatile("" : "+v"(s[k][j]), "+v"(g[k][j]));      // see renew()
                 const Decay e = glr_decay(s[k][j], A[j], on ? -__builtin_inff() : 0.0f);
-                // 1 / w, and w from it; both 0 where w is (the slope there is taken as 0)
-                const float rw = e.w2 > 0.0f ? __builtin_amdgcn_rsqf(e.w2) : 0.0f, w = e.w2 * rw;
+                // 1 / w, and w from it; both 0 where w^2 is 0 or below the smallest normal number (whose
+                // root the instruction takes as that of 0): the slope there is taken as 0
+                const float rw = e.w2 >= 0x1p-126f ? __builtin_amdgcn_rsqf(e.w2) : 0.0f, w = e.w2 * rw;
                 const float before = k <= k_rs ? __builtin_fmaf(P[k][j], in[j], h[k][j]) : h[k][j];
                 const float x = vx[k].get(j), G = vd[k].get(j) + K[j];
                 const float gw = G * w, v = g[k][j] * x;

@@ -73,3 +73,25 @@ def test_decays_from_long_memories_to_none(L):
     y, _, got = both(x, r, i, A, h0, torch.zeros(1, L, D), torch.ones(1, D))
     close(y, O.glr_fwd(x, r, i, A, h0)[0])
     close(got["dstate_init"], O.glr_bwd(x, r, i, A, torch.zeros(1, L, D), h0, None, torch.ones(1, D))["dstate_init"][0])
+
+
+@pytest.mark.parametrize("L", [3, 130])
+def test_write_coefficients_that_underflow(L):
+    """1 - a^2 below the smallest normal number: a token that leaves the state as it is, with finite
+    gradients, which the other tokens' are not touched by."""
+    r = torch.zeros(1, L, 8)
+    r[0, 1] = torch.tensor([-83.0, -84.0, -85.0, -86.0, -87.0, -87.3, -87.5, -88.0])
+    for a in (-0.1, -0.05, -0.01, -1e-4):
+        g = torch.Generator().manual_seed(L)
+        n = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+        x, i, h0, dy, dh = n(1, L, 8), n(1, L, 8), n(1, 8), n(1, L, 8), n(1, 8)
+        A = torch.full((8,), a)
+        y, h, got = both(x, r, i, A, h0, dy, dh)
+        assert torch.isfinite(y).all() and torch.isfinite(h).all()
+        want = O.glr_bwd(x, r, i, A, dy, h0, None, dh)
+        for k, (val, scale) in want.items():
+            print(k, end=" ")
+            assert torch.isfinite(got[k]).all()
+            # its terms' sizes, as for ordinary gates; what the token itself adds is under 2^-60 of them
+            err = (got[k].double().cpu() - val).abs()
+            assert (err <= (2.0 ** -13 + 4 * 2.0 ** -24 * L) * scale + 2.0 ** -40).all()
