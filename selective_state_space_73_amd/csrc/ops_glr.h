@@ -48,6 +48,19 @@ __device__ __forceinline__ float expm1_small(float v) {
 
 __device__ __forceinline__ float sigmoid(float v) { return rcp_fast(1.0f + exp2_fast(-kLog2e * v)); }
 
+// A gate for the backward, which needs sigmoid(v) and its slope sigmoid(v) sigmoid(-v), each to its
+// last digits: `half` is sigmoid(v) where that is the smaller of the two factors, else -sigmoid(-v)
+// (2^-126 more, so that it is never 0), from which the fraction makes the larger one again.
+struct Sides { float open, half; };
+__device__ __forceinline__ Sides gate_sides(float v) {
+    const float E = exp2_fast(-kLog2e * v), open = rcp_fast(1.0f + E), shut = __builtin_fmaf(E, open, 0x1p-126f);
+    return Sides{open, v > 0.0f ? -shut : open};
+}
+__device__ __forceinline__ float gate_open(float half) { return __builtin_amdgcn_fractf(half); }     // half, or 1 + half under 0
+__device__ __forceinline__ float gate_slope(float half) {
+    return __builtin_fabsf(half) * (1.0f - __builtin_fabsf(half));
+}
+
 // The decay near 1 is what a long memory is made of: a = 1 + expm1(A s) has the rounding of the
 // sum alone there, and 1 - a^2 = -e (1 + a) with e = expm1(A s) keeps its relative accuracy
 // where 1 - a * a would cancel. Further out a is the exponential itself: a sum with 1 would leave a
@@ -62,11 +75,10 @@ __device__ __forceinline__ Decay glr_decay(float s, float A, float bias) {
     return Decay{a, -__builtin_fmaf(e, a, e)};
 }
 
-struct Gate { float s, g, a, w2; };       // sigmoid(r), sigmoid(i), and the decay
+struct Gate { float g, a, w2; };          // sigmoid(i), and the decay
 __device__ __forceinline__ Gate glr_gate(float r, float i, float A, float bias) {
-    const float s = sigmoid(r);
-    const Decay d = glr_decay(s, A, bias);
-    return Gate{s, sigmoid(i), d.a, d.w2};
+    const Decay d = glr_decay(sigmoid(r), A, bias);
+    return Gate{sigmoid(i), d.a, d.w2};
 }
 
 // ---------------------------------------------------------------------------
@@ -556,7 +568,7 @@ k_glr_bwd(const GlrArgs p) {
         const bool mine = lane < CH && lane < valid;              // the lane that writes for its channel
 
         V vx[TT], vd[TT];
-        float s[TT][2], g[TT][2], A[2];
+        float s[TT][2], g[TT][2], A[2];                           // the halves of both gates
         float P[TT][2], h[TT][2];                                 // in front of token k: state h + P times the run's
         float ck[CK];
         uint32_t rs;
@@ -600,13 +612,16 @@ k_glr_bwd(const GlrArgs p) {
                 const bool on = rs >> k & 1u;
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const Gate e = glr_gate(vr[k].get(j), vi[k].get(j), A[j], on ? -__builtin_inff() : 0.0f);
-                    s[k][j] = e.s;
-                    g[k][j] = e.g;
+                    const Sides sr = gate_sides(vr[k].get(j)), si = gate_sides(vi[k].get(j));
+                    s[k][j] = sr.half;
+                    g[k][j] = si.half;
+                    asm volatile("" : "+v"(s[k][j]), "+v"(g[k][j]));  // now, and not what they are made of kept instead
+                    const Decay e = glr_decay(sr.open, A[j], on ? -__builtin_inff() : 0.0f);
                     P[k][j] = Pk[j];
                     h[k][j] = Sf[j];
                     Pk[j] *= e.a;
-                    Sf[j] = __builtin_fmaf(e.a, on ? 0.0f : Sf[j], __builtin_amdgcn_sqrtf(e.w2) * (e.g * vx[k].get(j)));
+                    Sf[j] = __builtin_fmaf(e.a, on ? 0.0f : Sf[j],
+                                            __builtin_amdgcn_sqrtf(e.w2) * (si.open * vx[k].get(j)));
                     Sb[j] = k < k_rs ? __builtin_fmaf(Pk[j], vd[k].get(j), Sb[j]) : Sb[j];
                 }
                 __builtin_amdgcn_sched_barrier(0);
@@ -680,19 +695,20 @@ k_glr_bwd(const GlrArgs p) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 asm volatile("" : "+v"(s[k][j]), "+v"(g[k][j]));      // see renew()
-                const Decay e = glr_decay(s[k][j], A[j], on ? -__builtin_inff() : 0.0f);
+                const float sr = gate_open(s[k][j]), gi = gate_open(g[k][j]);
+                const Decay e = glr_decay(sr, A[j], on ? -__builtin_inff() : 0.0f);
                 // 1 / w, and w from it; both 0 where w^2 is 0 or below the smallest normal number (whose
                 // root the instruction takes as that of 0): the slope there is taken as 0
                 const float rw = e.w2 >= 0x1p-126f ? __builtin_amdgcn_rsqf(e.w2) : 0.0f, w = e.w2 * rw;
                 const float before = k <= k_rs ? __builtin_fmaf(P[k][j], in[j], h[k][j]) : h[k][j];
                 const float x = vx[k].get(j), G = vd[k].get(j) + K[j];
-                const float gw = G * w, v = g[k][j] * x;
-                dx[j] = gw * g[k][j];
-                di[j] = gw * (v * (1.0f - g[k][j]));
+                const float gw = G * w, v = gi * x;
+                dx[j] = gw * gi;
+                di[j] = gw * (x * gate_slope(g[k][j]));
                 K[j] = on ? 0.0f : e.a * G;
                 const float dla = on ? 0.0f : K[j] * (before - e.a * rw * v);
-                dr[j] = dla * (A[j] * s[k][j]) * (1.0f - s[k][j]);
-                dA[j] = __builtin_fmaf(dla, s[k][j], dA[j]);
+                dr[j] = dla * (A[j] * gate_slope(s[k][j]));
+                dA[j] = __builtin_fmaf(dla, sr, dA[j]);
             }
             if (k < n) {
                 px -= step; pr -= step; pi -= step;

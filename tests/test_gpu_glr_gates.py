@@ -95,3 +95,25 @@ def test_write_coefficients_that_underflow(L):
             # its terms' sizes, as for ordinary gates; what the token itself adds is under 2^-60 of them
             err = (got[k].double().cpu() - val).abs()
             assert (err <= (2.0 ** -13 + 4 * 2.0 ** -24 * L) * scale + 2.0 ** -40).all()
+
+
+@pytest.mark.parametrize("L", [1, 70])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_gradients_of_gates_far_out(L, sign):
+    """r or i between 8 and 20: their gradients hold the small factor 1 - sigmoid to its last digits."""
+    D = 64
+    far = sign * torch.linspace(8, 20, D).expand(1, L, D).contiguous()
+    x, zero = torch.zeros(1, L, D), torch.zeros(1, L, D)
+    A = -torch.linspace(0.1, 2, D) / L
+    if sign < 0:
+        A = A * L                                                        # decays near 1
+    h0, dh = torch.ones(1, D), torch.ones(1, D)
+    _, _, got = both(x, far, zero, A, h0, zero, dh)
+    want = O.glr_bwd(x, far, zero, A, zero, h0, None, dh)
+    close(got["dr"], want["dr"][0])
+    x = 1 + torch.rand(1, L, D, generator=torch.Generator().manual_seed(3))
+    dy = torch.ones(1, L, D)
+    _, _, got = both(x, zero, far, A - 0.3, h0, dy, dh)
+    want = O.glr_bwd(x, zero, far, A - 0.3, dy, h0, None, dh)
+    close(got["di"], want["di"][0])
+    close(got["dx"], want["dx"][0])
