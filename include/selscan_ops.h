@@ -35,7 +35,8 @@ extern "C" {
  *   h_t = a_t * h_{t-1} + w_t * sigmoid(i_t) * x_t
  *   y_t = h_t
  *
- * A[d] <= 0 (not checked; a positive value gives NaN through the square root). A reset
+ * A[d] <= 0 (not checked; a positive value gives NaN through the square root; minus infinity
+ * is a channel without memory, a = 0 but where the sigmoid is 0 itself). A reset
  * token starts a new document: the state before it is not read, so that not even a NaN
  * passes it. Elsewhere non-finite values propagate to the later tokens of their channel.
  *

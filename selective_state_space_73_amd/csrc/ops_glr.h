@@ -67,6 +67,9 @@ __device__ __forceinline__ float gate_slope(float half) {
 // small decay, which the gradients have as a factor, whole steps of 2^-24. `bias` is added to A s:
 // 0, or minus infinity for a reset, which gives a = 0 and 1 - a^2 = 1.
 struct Decay { float a, w2; };            // exp(A s), 1 - a^2
+// A of a channel without memory, minus infinity, as the lowest number: times the 0 that stands for
+// a shut gate (a token past the end is one) it leaves the state as it is.
+__device__ __forceinline__ float glr_rate(float A) { return A < -0x1.fffffep127f ? -0x1.fffffep127f : A; }
 __device__ __forceinline__ Decay glr_decay(float s, float A, float bias) {
     const float la = __builtin_fmaf(A, s, bias);
     const float far = exp2_fast(kLog2e * la), near = expm1_small(la);
@@ -329,8 +332,8 @@ struct FwdRun {
             const bool more = k + 1 < n;
             rx.next(more); rr.next(more); ri.next(more);
         }
-        A[0] = p.A[c.c[0]];
-        A[1] = p.A[c.c[1]];
+        A[0] = glr_rate(p.A[c.c[0]]);
+        A[1] = glr_rate(p.A[c.c[1]]);
         reset = reset_at<TT>(p, q.b, t0, lane);
     }
 
@@ -587,8 +590,8 @@ k_glr_bwd(const GlrArgs p) {
                 const bool more = k + 1 < n;
                 rx.next(more); rr.next(more); ri.next(more); rd.next(more);
             }
-            A[0] = p.A[c.c[0]];
-            A[1] = p.A[c.c[1]];
+            A[0] = glr_rate(p.A[c.c[0]]);
+            A[1] = glr_rate(p.A[c.c[1]]);
 #pragma unroll
             for (int m = 0; m < CK; ++m) {
                 const int64_t ci = (int64_t)q.chunk * CK + m;
@@ -780,7 +783,7 @@ k_glr_step(const GlrArgs p) {
     float o[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        const Gate g = glr_gate(r.get(j), i.get(j), A.get(j), 0.0f);
+        const Gate g = glr_gate(r.get(j), i.get(j), glr_rate(A.get(j)), 0.0f);
         const float v = g.g * x.get(j);                               // what a reset leaves
         o[j] = rs ? v : __builtin_fmaf(g.a, h.get(j), __builtin_amdgcn_sqrtf(g.w2) * v);
     }

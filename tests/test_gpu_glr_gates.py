@@ -117,3 +117,29 @@ def test_gradients_of_gates_far_out(L, sign):
     want = O.glr_bwd(x, zero, far, A - 0.3, dy, h0, None, dh)
     close(got["di"], want["di"][0])
     close(got["dx"], want["dx"][0])
+
+
+@pytest.mark.parametrize("L", [1, 7, 70, 200])
+@pytest.mark.parametrize("D", [6, 5])
+def test_a_channel_without_memory(L, D):
+    """A = -infinity is a decay of 0: y = sigmoid(i) x, and gradients that end at their token."""
+    g = torch.Generator().manual_seed(L)
+    n = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    x, r, i, h0, dy, dh = n(2, L, D), n(2, L, D), n(2, L, D), n(2, D), n(2, L, D), n(2, D)
+    A = -torch.rand(D, generator=g) - 0.5
+    A[2] = -float("inf")
+    y, h, got = both(x, r, i, A, h0, dy, dh)
+    s = torch.sigmoid(i.double())
+    v = s * x.double()
+    G = dy.double().clone()
+    G[:, -1] += dh.double()
+    close(y[..., 2], v[..., 2])
+    close(h[:, 2], v[:, -1, 2])
+    close(got["dx"][..., 2], (G * s)[..., 2])
+    close(got["di"][..., 2], (G * v * (1 - s))[..., 2])
+    assert (got["dr"][..., 2] == 0).all() and got["dA"][2] == 0 and (got["dstate_init"][:, 2] == 0).all()
+    other = [k for k in range(D) if k != 2]
+    fin = A.clone()
+    fin[2] = -1.0
+    for a, b in zip((y, h, *got.values()), (lambda t: (t[0], t[1], *t[2].values()))(both(x, r, i, fin, h0, dy, dh))):
+        assert torch.equal(a[..., other], b[..., other])
