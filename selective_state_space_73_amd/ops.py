@@ -3,8 +3,8 @@
 Argument marshalling only, as for the scan: tensors are checked for device, dtype, shape and
 layout, their data pointers and torch's current HIP stream are passed to the C ABI, and the
 computation runs in the library's HIP kernels. For the recurrence and the 8-bit calls, of which
-a decode step makes many small ones, that is done by the C extension csrc/binding.cpp. Every call runs on the device of its tensors,
-whichever is current. With an explicit ``stream`` the outputs and the workspace are allocated
+a decode step makes many small ones, that is done by the C extension csrc/binding.cpp, which the
+first such call loads. Every call runs on the device of its tensors, whichever is current. With an explicit ``stream`` the outputs and the workspace are allocated
 on that stream; the caller orders it against the streams that made the inputs and that use
 the outputs.
 """
@@ -18,8 +18,6 @@ import torch
 
 from . import (SS_BF16, SS_EULER, SS_F32, SS_ZOH, SelscanError, block_dims, lib, ss_block_dims,
                ss_block_weights)
-from ._binding import gemm as _gemm, glr_bwd as _glr_bwd, glr_fwd as _glr_fwd, glr_step as _glr_step
-from ._binding import norm as _norm, quant as _quant
 
 GLR_CKPT = 64    # SS_GLR_CKPT
 Q8_BLOCK = 128   # columns that share a scale
@@ -28,8 +26,6 @@ _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
 _F32 = torch.float32
 _Q8 = torch.float8_e4m3fn
-_stream_of = torch._C._cuda_getCurrentRawStream
-_current = torch._C._cuda_getDevice
 
 
 class ss_glr_dims(ctypes.Structure):
@@ -97,6 +93,27 @@ def _check(status: int):
         raise SelscanError(status, lib.ss_last_error().decode())
 
 
+_EXTENSION = ("glr_fwd", "glr_step", "glr_bwd", "quant", "norm", "gemm")
+
+
+def _of_extension(name: str):
+    """A call of the C extension, which its first use loads: the scan and the blocks need
+    libselscan.so alone, whatever Python and torch the extension was built for."""
+    def first(*args):
+        try:
+            from . import _binding
+        except ImportError as e:
+            raise ImportError("the operators' extension _binding.so is missing or was built for another Python or "
+                              "torch: run __graft_entry__.build()") from e
+        for n in _EXTENSION:
+            globals()["_" + n] = getattr(_binding, n)
+        return globals()["_" + name](*args)
+    return first
+
+
+_glr_fwd, _glr_step, _glr_bwd, _quant, _norm, _gemm = map(_of_extension, _EXTENSION)
+
+
 def _done(result):
     """A binding call's result; an int is the status of a refused call."""
     if type(result) is int:
@@ -122,7 +139,7 @@ def _gpu(t: torch.Tensor, name: str) -> int:
 
 def _elsewhere(idx: int, stream) -> bool:
     """Whether a call has to move to another device or to an explicit stream first."""
-    return stream is not None or idx != _current()
+    return stream is not None or idx != torch._C._cuda_getDevice()
 
 
 @contextlib.contextmanager
@@ -318,7 +335,8 @@ def _block_q8(step, x, W, dt_rank, ssm_state, conv_state, out, workspace, norm_e
     fn = lib.ss_block_q8_step if step else lib.ss_block_q8_fwd
     _check(fn(ctypes.byref(dims), ctypes.byref(w), xp, _same(out, shape, io, idx, "out"),
               _opt(ssm_state, (B, di, N), _F32, idx, "ssm_state") or None,
-              _opt(conv_state, (B, di, 3), _F32, idx, "conv_state") or None, ws, ws_bytes, _stream_of(idx)))
+              _opt(conv_state, (B, di, 3), _F32, idx, "conv_state") or None, ws, ws_bytes,
+              torch._C._cuda_getCurrentRawStream(idx)))
     return out
 
 
