@@ -83,7 +83,7 @@ __device__ __forceinline__ uint64_t q8_eight(const float* v, const Q8Scale& s) {
 
 // VEC: rows start on 16 bytes and K is a multiple of 8. Else accesses of eight values are still
 // one instruction (two for fp32), at the alignment of an element, which the memory pipeline takes
-// (M 16384, K 2561, bf16, norm with residual: 59 us; element by element 189).
+// (M 16384, K 2561, bf16, norm with residual, in the last cache: 59 us; element by element 189).
 template <bool VEC> struct Q8Wide;
 template <> struct Q8Wide<true> {
     typedef uint32_t u4 __attribute__((ext_vector_type(4)));
@@ -189,7 +189,7 @@ struct Q8Args {
 // A row per G lanes (64 or 256), eight consecutive columns per lane and step, so that 16
 // neighbouring lanes hold one block. NV > 0: the row fits in NV steps and stays in registers.
 // NV = 0: longer rows are read again for each pass over them. Bound by memory with many rows
-// (norm with residual, bf16, M 16384, K 2560, from memory: 58 us, 5.0 TB/s), by the latency of a load, the row's
+// (norm with residual, bf16, M 16384, K 2560, from memory: 56 us, 5.3 TB/s), by the latency of a load, the row's
 // sum and a store with few (M 64: 3.9 us).
 template <typename T, bool VEC, bool NORM, bool RES, int G, int NV>
 __global__ void __launch_bounds__(256)
@@ -318,12 +318,13 @@ k_q8_square(const Q8Args p) {
 template <typename T, bool VEC, bool NORM, bool RES>
 hipError_t launch_q8_rows(const LaunchQ8& p, const Q8Args& a) {
     hipStream_t st = static_cast<hipStream_t>(p.stream);
-    // A wave per row where one step holds it (norm with residual, bf16: M 16384, K 512 11.4 us against
-    // 25.4 with four waves; M 64 2.7 both) or, with rows enough, two steps (K 1024: M 16384 19.0
-    // against 27.8, M 512 3.7 against 3.2) or five, where four waves need a second step for less than
-    // a third of it (K 2560: M 16384 40.1 against 52.8, M 1024 6.9 against 6.0). Else four waves
-    // (K 2048: M 4096 11.5 against 12.9; K 4096: M 16384 74 against 78).
-    const bool wave = p.K <= 512 || (p.M >= 1024 && p.K <= 1024) || (p.M >= 2048 && p.K > 2048 && p.K <= 2560);
+    // A wave per row where one step holds it (from memory, norm with residual, K 512: M 16384 13.6 us
+    // in bf16 and 22.0 in fp32 against 22.9 and 27.2 with four waves, M 512 3.8 against 4.0 and 3.9) or,
+    // with rows enough, two (K 768: M 16384 19.3 and 31.7 against 26.0 and 32.1, M 4096 7.2 and 11.2
+    // against 8.4 and 10.9, M 1024 4.1 and 4.7 against 3.9 and 4.1). Else four waves (M 16384: K 1536 32.1 and 57.9
+    // against 33.3 and 62.8, K 2560 53.1 and 97.9 against 54.2 and 105.7, K 4096 83.6 and 154 against 95.8 and
+    // 167; M 1024, K 2560 6.1 and 10.1 against 7.3 and 11.6).
+    const bool wave = p.K <= 512 || (p.M >= 4096 && p.K <= 1024);
     const int64_t steps = (p.K + (wave ? 512 : 2048) - 1) / (wave ? 512 : 2048);
     // a launch holds fewer than 2^32 lanes: rows past 2^22 go to launches of their own
     auto go = [&](auto kernel) {
@@ -340,8 +341,7 @@ hipError_t launch_q8_rows(const LaunchQ8& p, const Q8Args& a) {
     };
     if (wave) {
         if (steps <= 1) go(k_q8_rows<T, VEC, NORM, RES, 64, 1>);
-        else if (steps <= 2) go(k_q8_rows<T, VEC, NORM, RES, 64, 2>);
-        else go(k_q8_rows<T, VEC, NORM, RES, 64, 5>);
+        else go(k_q8_rows<T, VEC, NORM, RES, 64, 2>);
     } else {
         if (steps <= 1) go(k_q8_rows<T, VEC, NORM, RES, 256, 1>);
         else if (steps <= 2) go(k_q8_rows<T, VEC, NORM, RES, 256, 2>);

@@ -61,6 +61,22 @@ def test_bf16_values(M, K, square):
 
 
 @gpu
+@pytest.mark.parametrize("M,K", [(4095, 1024), (4096, 1024), (4097, 520), (4096, 1025), (4096, 513), (1030, 512), (1029, 513),
+                                 (2050, 2560), (2049, 2561), (4099, 2568)])
+def test_rows_at_sizes_at_which_kernels_change(M, K):
+    test_bf16_values(M, K, False)
+    x = torch.randn(M, K, generator=torch.Generator().manual_seed(K)).bfloat16().cuda()
+    w = (1 + 0.1 * torch.randn(K, generator=torch.Generator().manual_seed(1))).cuda()
+    q, scale, s = ss.ss_norm_q8(x, w, residual=x)
+    n, total = O.rms_norm(x, w, x)
+    assert torch.equal(s.cpu().double(), total)                   # 2 x: exact
+    # n is off by at most (K / 4096 + 1) 64 2^-24, and so is the scale
+    tol = (K / 4096 + 1) * 64 * 2.0 ** -24
+    per = O.spread(scale, M, K)
+    assert ((O.values(q, scale) - n).abs() <= O.half_step(n, per) + (tol + 2.0 ** -23) * n.abs()).all()
+
+
+@gpu
 @pytest.mark.parametrize("io", ["bf16", "f32"])
 def test_every_bf16_pair(io):
     """All largest magnitudes of one binade with all smaller values of fourteen (in fp32, those of
