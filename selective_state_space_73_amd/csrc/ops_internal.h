@@ -14,11 +14,13 @@ constexpr int kGlrCols = 128;       // channels per workgroup of the recurrence 
 // arithmetic is what the time goes to there), as long as the chunks to wait for are not too many.
 // Forward, up to one such tile a CU: B 1, L 300, D 512, fp32 10.4 us against 14.2 with chunks of
 // 128, bf16 10.2 against 12.9; with 320 tiles (L 600, D 4096) 20.3 against 17.1, with L 4800, D 100
-// 20.2 against 18.1. Backward, up to 640 (two workgroups a CU): B 1, L 300, D 512 15.0 against
-// 20.8, B 3, L 1001, D 1537 (624 tiles) 47 against 51.6; B 8, L 500, D 2000 (1024) 58 against 55,
-// B 1, L 20000, D 512 78 against 68.
+// 20.2 against 18.1. Backward, one workgroup a CU against two of the other kernel's, up to the
+// crossover between three and four of its rounds (us in bf16 and fp32, then the other kernel's): 300 tiles
+// (B 1, L 300, D 7680) 28 34, 32 37; 512 (B 1, L 2000, D 2048) 37 45, 42 55; 640 (B 8, L 500, D 1280) 43 52, 50 60;
+// 768 (B 4, L 1000, D 1536) 48 58, 53 66; 896 (B 1, L 1000, D 7168) 53 65, 55 68 and (B 1, L 2000, D 3584) 55 67, 52 67;
+// 960 (B 4, L 1000, D 1920) 56 67, 56 70; 1008 (B 2, L 4000, D 1024) 61 76, 60 77; 1024 (B 8, L 500, D 2048) 59 71, 55 72.
 inline bool glr_fine(bool backward, int64_t B, int64_t L, int64_t D) {
-    return L <= (backward ? 4096 : 2048) && B * ((D + kGlrCols - 1) / kGlrCols) * ((L + 63) / 64) <= (backward ? 640 : 256);
+    return L <= (backward ? 4096 : 2048) && B * ((D + kGlrCols - 1) / kGlrCols) * ((L + 63) / 64) <= (backward ? 896 : 256);
 }
 
 // Tokens of a forward chunk. Few rows of tiles, long sequences: twice as many, half as many

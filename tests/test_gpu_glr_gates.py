@@ -11,6 +11,7 @@ q <= 20 that is under (20 * 56 + 4 * 48 + 12) u < 2^-13.
 import pytest
 import torch
 
+import test_gpu_glr as ordinary
 from oracle import ops as O
 
 pytestmark = pytest.mark.gpu
@@ -143,3 +144,10 @@ def test_a_channel_without_memory(L, D):
     fin[2] = -1.0
     for a, b in zip((y, h, *got.values()), (lambda t: (t[0], t[1], *t[2].values()))(both(x, r, i, fin, h0, dy, dh))):
         assert torch.equal(a[..., other], b[..., other])
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("B,L,D", [(4, 193, 7160), (4, 250, 7171), (3, 513, 4300), (1, 4096, 1790), (1, 4090, 1795)])
+def test_backward_on_both_sides_of_the_tile_limit(B, L, D, io):
+    """896 tiles of 64 tokens and more (ordinary inputs)."""
+    ordinary.test_backward(B, L, D, io, "rare")
