@@ -12,7 +12,7 @@
 // survives at 2^-13 and is lost at 2^-14 within eight k, at 2^-23 and 2^-24 further apart): two
 // large products that cancel take a small one with them. So both operands are converted to bf16,
 // which holds every e4m3 value, for the bf16 instruction, whose products and sums keep fp32 (1e-8
-// off), at half the rate: bf16 out, M 16384, N 10240, K 2560 867 us against 478, M 64 with W from memory
+// off), at half the rate: bf16 out, M 16384, N 10240, K 2560 860 us against 470, M 64 with W from memory
 // 11.7 against 11.2.
 //
 // Both operands are k-contiguous and a sum over k has no order of its own here, so a lane's
@@ -136,9 +136,11 @@ __device__ __forceinline__ GqTile gq_tile(unsigned id, int tiles_m, int tiles_n)
 // chunk over the banks; the transfers write LDS in lane order, so the permutation is in what
 // they fetch. Rows past the end repeat the last one, chunks past K are zero.
 //
-// 128 x 128 tiles, four waves of 64 x 64: M 16384, N 10240, K 2560, bf16 out 867 us = 0.99 PFLOP/s (fp32 out
-// 914), where a bf16 library product of 8192^3 reaches 1.16: bound by the bf16 matrix instructions
-// and the conversions (two vector instructions for each of them). Tiles of 256 x 256 spill.
+// 128 x 128 tiles, four waves of 64 x 64: M 16384, N 10240, K 2560, bf16 out 860 us = 1.0 PFLOP/s (fp32 out
+// 910), where a bf16 library product of 8192^3 reaches 1.16. The matrix units are busy 44 percent of
+// the time and the other vector instructions, half of them conversions, take another 43 (counters):
+// a SIMD's two waves hardly overlap the two. Tiles of 256 x 256 spill; 128 x 256 take 830 here, and
+// 17 percent more at M 2048.
 __device__ __forceinline__ int gq_key_w(int row) { return (row >> 1 & 1) | (row >> 3 & 3) << 1; }
 __device__ __forceinline__ int gq_key_x(int row) { return row >> 1 & 7; }
 

@@ -527,13 +527,13 @@ k_glr_scan(const GlrArgs p) {
 // runs come from the forward's checkpoints and the runs' maps; what passes from a token to the
 // one before it is K_t = a_t g_t, and over a run K -> P K + S with the forward's P and
 // S = sum_k P_k dy_k, P_k the product of the decays up to token k. The first pass over a run
-// keeps the sigmoids and, of the state in front of each token, its part from within the run and
+// keeps half of each gate and, of the state in front of each token, its part from within the run and
 // the factor of what comes from outside; the second, backward in time, has the true states and
-// takes the decay and write coefficient from the sigmoids again (half of a gate's cost, for
+// takes the decay and write coefficient from the gates again (half of a gate's cost, for
 // four registers a token). Sums of dA over a run stay in registers, over a chunk in LDS;
-// k_glr_da adds the chunks. B 8, L 2048, D 5120, bf16: 300 us, 3.9 TB/s over the seven tensors; two
-// waves a SIMD (224 registers), whose arithmetic (about 180 us of it) overlaps with the loads of
-// one other workgroup.
+// k_glr_da adds the chunks. B 8, L 2048, D 5120, bf16: 317 us, 3.7 TB/s over the seven tensors; two
+// waves a SIMD (225 registers), whose arithmetic (70 percent of the vector units' time) overlaps with
+// the loads of one other workgroup.
 
 template <typename T, bool VEC, int TT, int NW, bool LOOK>
 __global__ void __launch_bounds__(NW * 64, NW > 8 ? 4 : 2)
@@ -759,7 +759,7 @@ k_glr_da(const float* __restrict__ part, float* __restrict__ dA, int64_t rows, i
 
 // ---------------------------------------------------------------------------
 // one token per stream: a lane per two channels; memory and a launch's latency (S 64, D 8192, bf16:
-// 3.4 us for 8.4 MB)
+// 3.5 us for 8.4 MB)
 
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256)
@@ -834,7 +834,7 @@ hipError_t launch_glr_t(const LaunchGlr& p) {
     if (p.pass == LaunchGlr::kFwd) {
         // One chunk is a matter of latency: 16 waves with runs of 8 tokens, of 4 up to 64 tokens (B 1, L 64,
         // D 512, fp32: 5.5 us against 8.2 with runs of 8). Several: runs of 16 tokens where a row's two
-        // channels fit one register (B 8, L 2048, D 5120, bf16: 162 us against 196 with 16 waves of 8
+        // channels fit one register (B 8, L 2048, D 5120, bf16: 164 us against 196 with 16 waves of 8
         // tokens), else runs of 8 (fp32, B 8, L 2048, D 2560: 144 against 153)
         if (!look) {
             if (p.L <= 64) go(k_glr_fwd<T, VEC, 4, 16>, 16);

@@ -24,7 +24,7 @@ inline bool glr_fine(bool backward, int64_t B, int64_t L, int64_t D) {
 }
 
 // Tokens of a forward chunk. Few rows of tiles, long sequences: twice as many, half as many
-// chunks to wait for (bf16: B 1, L 131072, D 2048 555 us against 620 with 128, B 3, L 16384,
+// chunks to wait for (bf16: B 1, L 131072, D 2048 557 us against 620 with 128, B 3, L 16384,
 // D 512 64 against 73, B 1, L 262144, D 128 125 against 221); shorter, or with tiles enough, two
 // workgroups a CU are better than one of twice the waves (B 1, L 1024, D 2048 14.8 us against
 // 20.2 with 256, B 8, L 2048, D 5120 165 against 180). fp32 runs have half the tokens, and a
@@ -34,8 +34,8 @@ inline int64_t glr_fwd_chunk(bool bf16, int64_t B, int64_t L, int64_t D) {
     return bf16 && L >= 4096 && B * ((D + kGlrCols - 1) / kGlrCols) < 64 ? 256 : 128;
 }
 // Tokens of a backward chunk. With many rows of tiles the shorter one, whose four waves a CU has
-// twice (B 8, L 2048, D 5120, bf16: 313 us against 351 with 128); with few, half as many chunks
-// to wait for (B 1, L 65536, D 1024: 322 against 380).
+// twice (a call with B 8, L 2048, D 5120, bf16: 337 us against 378 with 128, fp32 473 against 488); with
+// few, half as many chunks to wait for (B 1, L 65536, D 1024, bf16: 348 against 396, fp32 475 against 487).
 inline int64_t glr_bwd_chunk(int64_t B, int64_t L, int64_t D) {
     return glr_fine(true, B, L, D) || B * ((D + kGlrCols - 1) / kGlrCols) >= 32 ? 64 : 128;
 }

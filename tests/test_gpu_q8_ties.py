@@ -136,3 +136,26 @@ def test_norm_of_unit_rows(io, K):
     top = O.spread(O.block_tops(v), 3, K)
     on = 448.0 * v.double().abs() >= 2.0 ** -6 * top
     assert ((q.cpu().double() == O.nearest(v, top)) | ~on).all()
+
+
+@gpu
+@pytest.mark.parametrize("square", [False, True])
+def test_bf16_values_that_are_not_finite(square):
+    """A NaN (of any kind) becomes one and leaves its block's scale alone, an infinity takes its
+    block's values along, both signs of zero stay zero."""
+    x = torch.randn(4, 384, generator=torch.Generator().manual_seed(9)).bfloat16()
+    want = x.clone()
+    want[0, 3], want[1, 4], want[1, 5] = 0, 0, 0
+    x[0, 3] = float("nan")
+    x[1, 4:6] = torch.tensor([0x7FFF, -1], dtype=torch.int16).view(torch.bfloat16)
+    x[2, 7], want[2, 7] = -0.0, 0.0
+    q, s = ss.ss_quant_q8(x.cuda(), square=square)
+    clean, cs = ss.ss_quant_q8(want.cuda(), square=square)
+    assert torch.isnan(q[0, 3].float()) and torch.isnan(q[1, 4:6].float()).all()
+    q = torch.where(torch.isnan(q.float()), 0.0, q.float())
+    assert torch.equal(q, clean.float()) and torch.equal(s, cs)
+    x[3, 130] = float("-inf")
+    q, s = ss.ss_quant_q8(x.cuda(), square=square)
+    row = 0 if square else 3
+    assert torch.isinf(s[row, 1]) and torch.isnan(O.values(q, s, square)[row, 128:256]).all()
+    assert torch.equal(torch.nan_to_num(q.float()[3, :128]), clean.float()[3, :128])
