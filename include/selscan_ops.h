@@ -8,6 +8,10 @@
  *   ss_norm_q8                            the same behind a residual's addition and RMS norm
  *   ss_gemm_q8                            the product of two such matrices
  *   ss_block_q8_fwd, ss_block_q8_step     the block around the scan with such projections
+ *   ss_gdr_fwd, ss_gdr_bwd, ss_gdr_step   the gated delta rule: forward over whole sequences, its
+ *                                         gradients, one decode token
+ *   ss_gnorm_fwd, ss_gnorm_bwd            the norms behind and before a layer with its gate, its
+ *                                         scale and the residual, and their gradients
  *
  * Ownership, ordering, errors: as in selscan.h. Every pointer inside a struct is a DEVICE
  * pointer owned by the caller, arguments are validated on the host before anything is
@@ -185,6 +189,145 @@ ss_status ss_block_q8_fwd(const ss_block_dims* dims, const ss_block_q8_weights* 
 /* One token of each stream: x, out [B,d_model]; both states required and updated. */
 ss_status ss_block_q8_step(const ss_block_dims* dims, const ss_block_q8_weights* weights, const void* x, void* out,
                            float* ssm_state, float* conv_state, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Gated delta rule, one state S [dk, dv] per batch row and head h; head h of v uses the keys and
+ * queries of head h / (heads / k_heads). Per token t, with g the logarithm of the decay:
+ *
+ *   k^ = k / sqrt(sum k^2 + eps), q^ likewise       k and q themselves where eps = 0
+ *   S' = exp(g_t) S_{t-1}                            0 where reset[b,t] != 0
+ *   u  = beta_t (v_t - S'^T k^_t)
+ *   S_t = S' + k^_t u^T
+ *   y_t = scale S_t^T q^_t
+ *
+ * A log decay of -200 or less (minus infinity among them) is a decay of 0, as a reset is. A decay
+ * of 0 leaves out what it multiplies between chunks of 64 tokens (tokens 0 to 63, 64 to 127, ...) and
+ * in a step, so that not even a NaN passes it there; within a chunk, and everywhere else, values that are
+ * not finite propagate. g > 0, beta and the lengths of keys that are used as they are (eps = 0) are
+ * the caller's: with |k^| <= 1 and 0 <= beta <= 2 no state grows; nothing is checked.
+ *
+ * q, k and v are views whose last dimension is contiguous and whose rows, tokens and heads lie at any
+ * strides (columns of one projection's output, [B, H, L, d] layouts); every other tensor is contiguous
+ * row-major. q, k, v, y and the gradients of q, k, v and y have the I/O dtype (fp32 or bf16); gates,
+ * states, checkpoints and their gradients are fp32. Sums and states are fp32 (bf16 inputs: products
+ * on the bf16 matrix instructions, operands that are made in fp32 as sums of two or three bf16 terms). */
+
+#define SS_GDR_CHUNK 64   /* tokens between two checkpoints */
+
+typedef struct {
+    int64_t batch;      /* B (streams for ss_gdr_step), >= 1                            */
+    int64_t seqlen;     /* 0 <= L < 2^31; ignored by ss_gdr_step                         */
+    int32_t k_heads;    /* heads of q and k, >= 1                                        */
+    int32_t heads;      /* H heads of v, a multiple of k_heads                           */
+    int32_t dk, dv;     /* 1 <= dk <= 256, 1 <= dv <= 512                                */
+    int32_t io_dtype;   /* ss_dtype of q, k, v, y and their gradients                    */
+    float   scale;      /* of y; finite                                                  */
+    float   eps;        /* >= 0, finite; 0: q and k are used as they are                 */
+    int32_t reserved;   /* 0                                                             */
+} ss_gdr_dims;
+
+typedef struct {          /* [B, L, heads, d] view: element (b, t, h, d) at p + b batch_stride + t token_stride + h head_stride + d */
+    const void* p;        /* aligned to its element                                          */
+    int64_t batch_stride; /* in elements, >= 0; ignored where B = 1                          */
+    int64_t token_stride; /* in elements, >= 0; ignored where L = 1 and by ss_gdr_step       */
+    int64_t head_stride;  /* in elements, >= 0; ignored where there is one head              */
+} ss_head_view;
+
+typedef struct {
+    ss_head_view   q, k;     /* [B,L,k_heads,dk]                                             */
+    ss_head_view   v;        /* [B,L,H,dv]                                                   */
+    const float*   g;        /* [B,L,H] log decays                                           */
+    const float*   beta;     /* [B,L,H]                                                      */
+    const uint8_t* reset;    /* [B,L] ([B] for ss_gdr_step) or NULL (no resets)              */
+    void*          y;        /* [B,L,H,dv] io OUT; must not overlap any input                */
+    float*         state;    /* [B,H,dk,dv] IN/OUT, or NULL: zero initial state, final not returned.
+                                Required by ss_gdr_step; not used by ss_gdr_bwd              */
+    float*         ckpt;     /* ss_gdr_ckpt_floats values for the backward (the states before tokens 0, 64,
+                                128, ..., [B,H,ceil(L/64),dk,dv], then u_t / beta_t, [B,L,H,dv]):
+                                OUT of ss_gdr_fwd (NULL: not written), IN of ss_gdr_bwd      */
+} ss_gdr_args;
+
+/* Values of the checkpoints; 0 for invalid dims. */
+size_t ss_gdr_ckpt_floats(const ss_gdr_dims* dims);
+
+/* Bytes of device workspace of ss_gdr_fwd (backward = 0) or ss_gdr_bwd; 0 for invalid dims or L = 0. */
+size_t ss_gdr_workspace_bytes(const ss_gdr_dims* dims, int backward);
+
+/* L = 0: y is empty and the state stays as it is. */
+ss_status ss_gdr_fwd(const ss_gdr_dims* dims, const ss_gdr_args* args, void* workspace, size_t workspace_bytes,
+                     void* stream);
+
+/* One token for every stream: q, k [B,k_heads,dk], v [B,H,dv], g, beta [B,H], y [B,H,dv]; state updated in place. */
+ss_status ss_gdr_step(const ss_gdr_dims* dims, const ss_gdr_args* args, void* stream);
+
+typedef struct {
+    const void*  dy;           /* [B,L,H,dv] io: gradient of y (required)                        */
+    const float* dstate_final; /* [B,H,dk,dv] or NULL (zero): gradient of the returned state     */
+    void*  dq;                 /* [B,L,k_heads,dk] io OUT (required), summed over the heads that share it */
+    void*  dk;                 /* [B,L,k_heads,dk] io OUT (required), likewise                   */
+    void*  dv;                 /* [B,L,H,dv] io OUT (required)                                    */
+    float* dg;                 /* [B,L,H] OUT (required); 0 at resets                             */
+    float* dbeta;              /* [B,L,H] OUT (required)                                          */
+    float* dstate_init;        /* [B,H,dk,dv] OUT or NULL: gradient of the initial state          */
+} ss_gdr_grads;
+
+/* Gradients of sum(dy * y) + sum(dstate_final * state_out) for the forward's inputs in `args`, whose
+ * ckpt are the checkpoints that forward wrote (y and state are ignored). With W_t the gradient of S_t,
+ *   W_t' = W_t + scale q^ dy^T,  dv = beta W_t'^T k^,  dk^ = W_t' u - S' dv,  dq^ = scale S_t dy,
+ *   dbeta = (dv / beta) . (u / beta),  dS' = W_t' - k^ dv^T,  dg = <S', dS'>,  W_{t-1} = exp(g) dS'.
+ * Outputs are overwritten; none may overlap an input, another output or the workspace. */
+ss_status ss_gdr_bwd(const ss_gdr_dims* dims, const ss_gdr_args* args, const ss_gdr_grads* grads, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The norms behind and before a layer, with its gate, its scale and the residual. Rows of M, columns of
+ * K, in groups of `group` consecutive columns (heads; K: one group):
+ *
+ *   p = y / sqrt(mean over the group of y^2 + eps) * w      w [group], the same for every group
+ *   h = p * gate * sigmoid(gate)                            h = p without a gate
+ *   s = residual + scale * h                                scale [K]; without one 1, without a residual 0
+ *   n = s / sqrt(mean over the row of s^2 + eps) * w_next   where n is asked for
+ *
+ * in fp32, with s and n each rounded once (n from s before it is rounded). All matrices are contiguous
+ * row-major in the I/O dtype, weights and their gradients fp32. */
+typedef struct {
+    int64_t rows;       /* M, 1 <= M < 2^31                                              */
+    int64_t cols;       /* K, 1 <= K <= 16384                                            */
+    int64_t group;      /* a divisor of K                                                */
+    int32_t io_dtype;   /* ss_dtype of y, gate, residual, s, n and their gradients       */
+    float   eps;        /* > 0, finite                                                   */
+} ss_gnorm_dims;
+
+typedef struct {
+    const void*  y;        /* [M,K] io                                                     */
+    const float* w;        /* [group]                                                      */
+    const void*  gate;     /* [M,K] io or NULL                                             */
+    const void*  residual; /* [M,K] io or NULL                                             */
+    const float* scale;    /* [K] or NULL                                                  */
+    const float* w_next;   /* [K]; NULL: n is not made                                     */
+    void*        s;        /* [M,K] io OUT; may be y, gate or residual itself. Not used by ss_gnorm_bwd */
+    void*        n;        /* [M,K] io OUT; required with w_next, else NULL. Not used by ss_gnorm_bwd   */
+} ss_gnorm_args;
+
+ss_status ss_gnorm_fwd(const ss_gnorm_dims* dims, const ss_gnorm_args* args, void* stream);
+
+typedef struct {
+    const void* ds;        /* [M,K] io or NULL (zero): gradient of s                        */
+    const void* dn;        /* [M,K] io or NULL (zero): gradient of n; only with w_next. One of the two is required */
+    void*  dy;             /* [M,K] io OUT (required)                                       */
+    void*  dgate;          /* [M,K] io OUT; required with a gate, else NULL                 */
+    void*  dresidual;      /* [M,K] io OUT; required with a residual, else NULL             */
+    float* dw;             /* [group] OUT (required), summed over rows and groups           */
+    float* dscale;         /* [K] OUT; required with a scale, else NULL                     */
+    float* dw_next;        /* [K] OUT; required with w_next, else NULL                      */
+} ss_gnorm_grads;
+
+size_t ss_gnorm_workspace_bytes(const ss_gnorm_dims* dims);   /* of ss_gnorm_bwd; 0 for invalid dims */
+
+/* Gradients of sum(ds * s) + sum(dn * n) for the forward's inputs, from these alone. Outputs are overwritten;
+ * none may overlap an input, another output or the workspace. */
+ss_status ss_gnorm_bwd(const ss_gnorm_dims* dims, const ss_gnorm_args* args, const ss_gnorm_grads* grads, void* workspace,
+                       size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -19,6 +19,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
 #include <sstream>
 
 #include "selscan_ops.h"
@@ -308,8 +309,181 @@ PyObject* gemm(PyObject*, PyObject* const* v, Py_ssize_t n) {
     });
 }
 
+// ---------------------------------------------------------------------------
+// gated delta rule
+
+ss_head_view head_view(const Call& c, const at::Tensor& t, at::IntArrayRef shape, at::ScalarType type, const char* name) {
+    if (!t.is_cuda() || t.device().index() != c.idx || t.scalar_type() != type || t.sizes() != shape) c.wrong(t, shape, type, name);
+    const at::IntArrayRef st = t.strides();
+    if (st.back() != 1 && shape.back() > 1) refuse(PyExc_ValueError, name, ": the last dimension must be contiguous (stride 1)");
+    return shape.size() == 4 ? ss_head_view{t.data_ptr(), st[0], st[1], st[2]} : ss_head_view{t.data_ptr(), st[0], 0, st[1]};
+}
+
+struct Gdr { ss_gdr_dims d; ss_gdr_args a; at::ScalarType dt; int64_t B, L, H; };
+
+// q, k, v, g, beta, reset, scale, eps; q [B,L,k_heads,dk] and v [B,L,heads,dv], without L for one token
+bool gdr_inputs(const Call& c, PyObject* const* v, PyObject* reset, PyObject* scale, PyObject* eps, bool step, Gdr* out) {
+    const at::Tensor &q = tensor(v[0], "q"), &k = tensor(v[1], "k"), &x = tensor(v[2], "v");
+    const int64_t n = step ? 3 : 4;
+    if (q.dim() != n || x.dim() != n)
+        refuse(PyExc_ValueError, step ? "q must be [streams, k_heads, dk] and v [streams, heads, dv]"
+                                      : "q must be [batch, seqlen, k_heads, dk] and v [batch, seqlen, heads, dv]");
+    const int64_t B = q.size(0), L = step ? 1 : q.size(1), Hk = q.size(n - 2), K = q.size(n - 1), H = x.size(n - 2), V = x.size(n - 1);
+    if (Hk > INT32_MAX || H > INT32_MAX || K > INT32_MAX || V > INT32_MAX) refuse(PyExc_ValueError, "heads, dk or dv too large");
+    const double sc = scale == Py_None ? 1.0 / std::sqrt((double)K) : PyFloat_AsDouble(scale);
+    if (sc == -1.0 && PyErr_Occurred()) return false;
+    const double ep = eps == Py_None ? 0.0 : PyFloat_AsDouble(eps);
+    if (ep == -1.0 && PyErr_Occurred()) return false;
+    out->dt = q.scalar_type();
+    out->B = B; out->L = L; out->H = H;
+    out->d = ss_gdr_dims{B, L, (int32_t)Hk, (int32_t)H, (int32_t)K, (int32_t)V, io_of(out->dt, "q"), (float)sc, (float)ep, 0};
+    ss_gdr_args& a = out->a;
+    a = ss_gdr_args{};
+    a.q = head_view(c, q, q.sizes(), out->dt, "q");
+    a.k = head_view(c, k, q.sizes(), out->dt, "k");
+    c10::SmallVector<int64_t, 4> shape(q.sizes().begin(), q.sizes().end() - 2);
+    if (reset != Py_None) {
+        const at::Tensor& t = tensor(reset, "reset");
+        const auto type = t.scalar_type() == at::ScalarType::Bool ? at::ScalarType::Bool : at::ScalarType::Byte;
+        a.reset = c.same<const uint8_t>(t, shape, type, "reset");
+    }
+    shape.push_back(H);
+    a.g = c.given<float>(v[3], shape, kF32, "g");
+    a.beta = c.given<float>(v[4], shape, kF32, "beta");
+    shape.push_back(V);
+    a.v = head_view(c, x, shape, out->dt, "v");
+    return true;
+}
+
+// q, k, v, g, beta, scale, eps, state, reset, ckpt, y, workspace -> y
+PyObject* gdr_fwd(PyObject*, PyObject* const* v, Py_ssize_t n) {
+    return guarded(n, 12, [&]() -> PyObject* {
+        const Call c(tensor(v[0], "q"), "q");
+        Gdr x;
+        if (!gdr_inputs(c, v, v[8], v[5], v[6], false, &x)) return nullptr;
+        x.a.state = c.maybe<float>(v[7], {x.B, x.H, x.d.dk, x.d.dv}, kF32, "state");
+        if (v[9] != Py_None) x.a.ckpt = c.given<float>(v[9], {(int64_t)ss_gdr_ckpt_floats(&x.d)}, kF32, "ckpt");
+        const at::Tensor y = c.output(v[10], {x.B, x.L, x.H, x.d.dv}, x.dt, "y");
+        x.a.y = y.data_ptr();
+        const at::Tensor ws = c.workspace(v[11], ss_gdr_workspace_bytes(&x.d, 0));
+        const ss_status s = ss_gdr_fwd(&x.d, &x.a, ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? ws.nbytes() : 0, c.stream());
+        return s ? status(s) : v[10] != Py_None ? Py_NewRef(v[10]) : THPVariable_Wrap(y);
+    });
+}
+
+// q, k, v, g, beta, scale, eps, state, reset, y -> y
+PyObject* gdr_step(PyObject*, PyObject* const* v, Py_ssize_t n) {
+    return guarded(n, 10, [&]() -> PyObject* {
+        const Call c(tensor(v[0], "q"), "q");
+        Gdr x;
+        if (!gdr_inputs(c, v, v[8], v[5], v[6], true, &x)) return nullptr;
+        if (v[7] == Py_None) refuse(PyExc_ValueError, "state is required");
+        x.a.state = c.given<float>(v[7], {x.B, x.H, x.d.dk, x.d.dv}, kF32, "state");
+        const at::Tensor y = c.output(v[9], {x.B, x.H, x.d.dv}, x.dt, "y");
+        x.a.y = y.data_ptr();
+        const ss_status s = ss_gdr_step(&x.d, &x.a, c.stream());
+        return s ? status(s) : v[9] != Py_None ? Py_NewRef(v[9]) : THPVariable_Wrap(y);
+    });
+}
+
+// q, k, v, g, beta, scale, eps, ckpt, dy, reset, dstate_final, workspace -> dq, dk, dv, dg, dbeta, dstate_init
+PyObject* gdr_bwd(PyObject*, PyObject* const* v, Py_ssize_t n) {
+    return guarded(n, 12, [&]() -> PyObject* {
+        const Call c(tensor(v[0], "q"), "q");
+        Gdr x;
+        if (!gdr_inputs(c, v, v[9], v[5], v[6], false, &x)) return nullptr;
+        if (v[7] == Py_None) refuse(PyExc_ValueError, "ckpt is required");
+        const int64_t Hk = x.d.k_heads, K = x.d.dk, V = x.d.dv;
+        x.a.ckpt = c.given<float>(v[7], {(int64_t)ss_gdr_ckpt_floats(&x.d)}, kF32, "ckpt");
+        ss_gdr_grads g{};
+        g.dy = c.given(v[8], {x.B, x.L, x.H, V}, x.dt, "dy");
+        g.dstate_final = c.maybe<float>(v[10], {x.B, x.H, K, V}, kF32, "dstate_final");
+        const at::Tensor dq = c.empty({x.B, x.L, Hk, K}, x.dt), dk = c.empty({x.B, x.L, Hk, K}, x.dt);
+        const at::Tensor dv = c.empty({x.B, x.L, x.H, V}, x.dt), dg = c.empty({x.B, x.L, x.H}, kF32), db = c.empty({x.B, x.L, x.H}, kF32);
+        const at::Tensor dh = c.empty({x.B, x.H, K, V}, kF32);
+        g.dq = dq.data_ptr(); g.dk = dk.data_ptr(); g.dv = dv.data_ptr();
+        g.dg = static_cast<float*>(dg.data_ptr());
+        g.dbeta = static_cast<float*>(db.data_ptr());
+        g.dstate_init = static_cast<float*>(dh.data_ptr());
+        const at::Tensor ws = c.workspace(v[11], ss_gdr_workspace_bytes(&x.d, 1));
+        const ss_status s = ss_gdr_bwd(&x.d, &x.a, &g, ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? ws.nbytes() : 0, c.stream());
+        return s ? status(s) : results(dq, dk, dv, dg, db, dh);
+    });
+}
+
+// ---------------------------------------------------------------------------
+// the norms around a layer
+
+struct Gnorm { ss_gnorm_dims d; ss_gnorm_args a; at::ScalarType dt; };
+
+// y, w, gate, residual, scale, w_next, eps
+bool gnorm_inputs(const Call& c, PyObject* const* v, Gnorm* out) {
+    const at::Tensor &y = tensor(v[0], "y"), &w = tensor(v[1], "w");
+    const Rows r = rows_of(y, "y");
+    const double eps = PyFloat_AsDouble(v[6]);
+    if (eps == -1.0 && PyErr_Occurred()) return false;
+    if (w.dim() != 1) refuse(PyExc_ValueError, "w must be [group]");
+    out->dt = y.scalar_type();
+    out->d = ss_gnorm_dims{r.M, r.K, w.size(0), io_of(out->dt, "y"), (float)eps};
+    ss_gnorm_args& a = out->a;
+    a = ss_gnorm_args{};
+    a.y = y.data_ptr();
+    a.w = c.same<float>(w, {w.size(0)}, kF32, "w");
+    a.gate = c.maybe(v[2], y.sizes(), out->dt, "gate");
+    a.residual = c.maybe(v[3], y.sizes(), out->dt, "residual");
+    a.scale = c.maybe<float>(v[4], {r.K}, kF32, "scale");
+    a.w_next = c.maybe<float>(v[5], {r.K}, kF32, "w_next");
+    return true;
+}
+
+// y, w, gate, residual, scale, w_next, eps, s, n -> s, n
+PyObject* gnorm_fwd(PyObject*, PyObject* const* v, Py_ssize_t n) {
+    return guarded(n, 9, [&]() -> PyObject* {
+        const at::Tensor& y = tensor(v[0], "y");
+        const Call c(y, "y");
+        Gnorm x;
+        if (!gnorm_inputs(c, v, &x)) return nullptr;
+        if (v[5] == Py_None && v[8] != Py_None) refuse(PyExc_ValueError, "n given without w_next");
+        const at::Tensor s = c.output(v[7], y.sizes(), x.dt, "s");
+        at::Tensor m;
+        if (v[5] != Py_None) m = c.output(v[8], y.sizes(), x.dt, "n");
+        x.a.s = s.data_ptr();
+        x.a.n = m.defined() ? m.data_ptr() : nullptr;
+        const ss_status e = ss_gnorm_fwd(&x.d, &x.a, c.stream());
+        return e ? status(e) : results(s, m);
+    });
+}
+
+// y, w, gate, residual, scale, w_next, eps, ds, dn, workspace -> dy, dw, dgate, dresidual, dscale, dw_next
+PyObject* gnorm_bwd(PyObject*, PyObject* const* v, Py_ssize_t n) {
+    return guarded(n, 10, [&]() -> PyObject* {
+        const at::Tensor& y = tensor(v[0], "y");
+        const Call c(y, "y");
+        Gnorm x;
+        if (!gnorm_inputs(c, v, &x)) return nullptr;
+        ss_gnorm_grads g{};
+        g.ds = c.maybe(v[7], y.sizes(), x.dt, "ds");
+        g.dn = c.maybe(v[8], y.sizes(), x.dt, "dn");
+        const at::Tensor dy = c.empty(y.sizes(), x.dt), dw = c.empty({x.d.group}, kF32);
+        at::Tensor dz, dr, da, dm;
+        if (x.a.gate) dz = c.empty(y.sizes(), x.dt);
+        if (x.a.residual) dr = c.empty(y.sizes(), x.dt);
+        if (x.a.scale) da = c.empty({x.d.cols}, kF32);
+        if (x.a.w_next) dm = c.empty({x.d.cols}, kF32);
+        auto at_of = [](const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; };
+        g.dy = dy.data_ptr(); g.dgate = at_of(dz); g.dresidual = at_of(dr);
+        g.dw = static_cast<float*>(dw.data_ptr());
+        g.dscale = static_cast<float*>(at_of(da));
+        g.dw_next = static_cast<float*>(at_of(dm));
+        const at::Tensor ws = c.workspace(v[9], ss_gnorm_workspace_bytes(&x.d));
+        const ss_status e = ss_gnorm_bwd(&x.d, &x.a, &g, at_of(ws), ws.defined() ? ws.nbytes() : 0, c.stream());
+        return e ? status(e) : results(dy, dw, dz, dr, da, dm);
+    });
+}
+
 #define FN(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
-PyMethodDef kMethods[] = {FN(glr_fwd), FN(glr_step), FN(glr_bwd), FN(quant), FN(norm), FN(gemm), {nullptr, nullptr, 0, nullptr}};
+PyMethodDef kMethods[] = {FN(glr_fwd), FN(glr_step), FN(glr_bwd), FN(quant), FN(norm), FN(gemm), FN(gdr_fwd), FN(gdr_step),
+                           FN(gdr_bwd), FN(gnorm_fwd), FN(gnorm_bwd), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -1,0 +1,1117 @@
+// Device code of the gated delta rule (ss_gdr_fwd, ss_gdr_bwd, ss_gdr_step).
+//
+//   S' = e^g_t S_{t-1},  u_t = beta_t (v_t - S'^T k_t),  S_t = S' + k_t u_t^T,  y_t = scale S_t^T q_t
+//
+// Chunks of 64 tokens. With G the running sum of g inside a chunk, D_ij = e^(G_i - G_j) for i >= j and
+// S0 the state in front of it, x_t = u_t / beta_t solves a triangular system that needs no state,
+//
+//   (1 + N) X = V - e^G (K S0),    N_ij = beta_j D_ij (k_i . k_j), i > j
+//   Y = scale e^G (Q S0) + (P beta) X,    P_ij = scale D_ij (q_i . k_j), i >= j
+//   S = e^G_last S0 + (beta e^(G_last - G) K)^T X
+//
+// k_gdr_prep makes (1 + N)^-1, P and the tokens' factors for every chunk at once; k_gdr_walk goes from
+// chunk to chunk with the state in registers. The columns of S are independent, so a head is split over
+// workgroups by them. q and k enter the matrix cores as they came; their lengths are factors of tokens.
+//
+// Layout of the matrix instructions (16 x 16 tiles, 32 terms of a sum): lane l = 16 g + m holds row m of
+// A, or column m of B, at the terms 4 g + r and 16 + 4 g + r, r < 4, of its 32 (any order of the terms
+// is right as long as both operands have the same). The result's lane holds column m at rows 4 g + r: two
+// tiles of a result below each other are the next product's B without a move between lanes. So
+// a wave keeps its columns of the state and everything that is made from them in registers, and
+// only A operands, which all waves share, lie in LDS, in the order in which lanes read them.
+#pragma once
+#include "ops_layer_internal.h"
+#include "selscan_device.h"
+
+namespace selscan {
+
+typedef float gf4 __attribute__((ext_vector_type(4)));
+typedef float gf8 __attribute__((ext_vector_type(8)));
+typedef __bf16 gb8 __attribute__((ext_vector_type(8)));
+typedef short gs4 __attribute__((ext_vector_type(4)));
+typedef uint32_t gu4 __attribute__((ext_vector_type(4)));
+
+constexpr int kGdrC = SS_GDR_CHUNK;           // 64
+static_assert(kGdrC == 64, "a wave is a chunk's tokens");
+
+// Operands by I/O type. fp32: the fp32 matrix instructions, as they are. bf16: q, k, v and gradients of y
+// are exact operands; what is made in fp32 (states, inverses, solutions) goes in as a sum of bf16 terms,
+// three of them where the result is a state or a gradient in fp32 (24 bits, and the six largest of the
+// nine products of two such: 2^-24 of their size is left out), two where it is only stored in
+// bf16. Six bf16 products cost 2.7 times less than one fp32 product.
+template <typename T> struct Mx;
+
+template <> struct Mx<uint16_t> {
+    static constexpr int NT = 3, NP = 2;                        // terms of the inverse, of P
+    typedef gb8 F;
+    template <int N> struct S { gb8 t[N]; };
+    static __device__ __forceinline__ F ld(const uint16_t* p) { return *reinterpret_cast<const gb8*>(p); }
+    template <int N>
+    static __device__ __forceinline__ S<N> split(gf8 v) {
+        S<N> s;
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            s.t[k] = __builtin_convertvector(v, gb8);
+            if (k + 1 < N) v -= __builtin_convertvector(s.t[k], gf8);
+        }
+        return s;
+    }
+    static __device__ __forceinline__ gf4 mm(const gb8& a, const gb8& b, gf4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+    }
+    // an exact operand by a sum of terms
+    template <int N>
+    static __device__ __forceinline__ gf4 mul(const F& a, const S<N>& b, gf4 c) {
+#pragma unroll
+        for (int k = N - 1; k >= 0; --k) c = mm(a, b.t[k], c);
+        return c;
+    }
+    template <int N>
+    static __device__ __forceinline__ gf4 mul(const S<N>& a, const F& b, gf4 c) {
+#pragma unroll
+        for (int k = N - 1; k >= 0; --k) c = mm(a.t[k], b, c);
+        return c;
+    }
+    template <int N>
+    static __device__ __forceinline__ gf4 mul(const S<N>& a, const S<N>& b, gf4 c) {
+        if constexpr (N == 3) {
+            c = mm(a.t[1], b.t[1], c);
+            c = mm(a.t[2], b.t[0], c);
+            c = mm(a.t[0], b.t[2], c);
+        }
+        c = mm(a.t[1], b.t[0], c);
+        c = mm(a.t[0], b.t[1], c);
+        return mm(a.t[0], b.t[0], c);
+    }
+    // The transposed operand from tiles that lie for the other one: row d0 + m of A, from tokens' rows of
+    // [tile][kd][lane][8]; tokens of the tiles 2 s and 2 s + 1 are the terms.
+    template <int KD>
+    static __device__ __forceinline__ F ldt(const uint16_t* tiles, int s, int dt, int lane) {
+        const int g = lane >> 4, i = lane & 15;
+        gs4 a[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint16_t* p = tiles + (((2 * s + h) * KD + (dt >> 1)) * 64 + (i & 3) * 16 + 4 * g + (i >> 2)) * 8 + (dt & 1) * 4;
+            a[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((gs4 __attribute__((address_space(3)))*)p);
+        }
+        typedef short gs8 __attribute__((ext_vector_type(8)));
+        return __builtin_bit_cast(gb8, gs8{a[0][0], a[0][1], a[0][2], a[0][3], a[1][0], a[1][1], a[1][2], a[1][3]});
+    }
+};
+
+template <> struct Mx<float> {
+    static constexpr int NT = 1, NP = 1;
+    typedef gf8 F;
+    template <int N> struct S { gf8 t[1]; };
+    static __device__ __forceinline__ F ld(const float* p) { return *reinterpret_cast<const gf8*>(p); }
+    template <int N>
+    static __device__ __forceinline__ S<N> split(gf8 v) { return S<N>{{v}}; }
+    static __device__ __forceinline__ gf4 mm(const gf8& a, const gf8& b, gf4 c) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[j], b[j], c, 0, 0, 0);
+        return c;
+    }
+    template <int N>
+    static __device__ __forceinline__ gf4 mul(const F& a, const S<N>& b, gf4 c) { return mm(a, b.t[0], c); }
+    template <int N>
+    static __device__ __forceinline__ gf4 mul(const S<N>& a, const F& b, gf4 c) { return mm(a.t[0], b, c); }
+    template <int N>
+    static __device__ __forceinline__ gf4 mul(const S<N>& a, const S<N>& b, gf4 c) { return mm(a.t[0], b.t[0], c); }
+    template <int KD>
+    static __device__ __forceinline__ F ldt(const float* tiles, int s, int dt, int lane) {
+        const int g = lane >> 4, i = lane & 15;
+        F a;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            a[j] = tiles[(((2 * s + (j >> 2)) * KD + (dt >> 1)) * 64 + (i >> 2) * 16 + 4 * g + (j & 3)) * 8 + (dt & 1) * 4 + (i & 3)];
+        return a;
+    }
+};
+
+__device__ __forceinline__ gf8 gdr_pair(gf4 a, gf4 b) { return gf8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}; }
+
+// The blocks of a lower triangle of 64 x 64 that hold anything, 16 rows by 32 columns: (row tile, column
+// pair) 00 10 20 21 30 31; of an upper triangle 00 01 10 11 21 31.
+__device__ __forceinline__ constexpr int gdr_low(int mt, int s) { return mt < 2 ? mt : 2 * mt - 2 + s; }
+__device__ __forceinline__ constexpr int gdr_up(int mt, int s) { return mt < 2 ? 2 * mt + s : mt + 2; }
+
+// Eight values of a row at d, zeros past dk or (none) in a row that is not there.
+template <typename T>
+__device__ __forceinline__ void gdr_row8(const T* row, int d, int dk, bool vec, bool there, T* out) {
+    if (there && vec && d < dk) {
+        if constexpr (sizeof(T) == 2) {
+            *reinterpret_cast<gu4*>(out) = *reinterpret_cast<const gu4*>(row + d);
+        } else {
+            *reinterpret_cast<gu4*>(out) = *reinterpret_cast<const gu4*>(row + d);
+            *reinterpret_cast<gu4*>(out + 4) = *reinterpret_cast<const gu4*>(row + d + 4);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) out[j] = there && d + j < dk ? row[d + j] : T(0);
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ float gdr_f(T v) { return IO<T>::ld(&v); }
+
+// 64 rows of one head from token t0 on, in the order of A operands. KD = padded width / 32.
+template <typename T, int KD, int NTH = 256>
+__device__ __forceinline__ void gdr_stage(T* tiles, const ss_head_view& v, int64_t b, int64_t t0, int64_t L, int head, int dk, bool vec) {
+    constexpr int PER = KD * 4;                      // accesses of eight values a row
+    const T* base = static_cast<const T*>(v.p) + b * v.batch_stride + head * v.head_stride;
+#pragma unroll
+    for (int it = 0; it < kGdrC * PER / NTH; ++it) {
+        const int id = it * NTH + threadIdx.x, t = id / PER, d = id % PER * 8;
+        alignas(16) T x[8];
+        gdr_row8<T>(base + (t0 + t) * v.token_stride, d, dk, vec, t0 + t < L, x);
+        const int g = d >> 2 & 3, h = d >> 4 & 1;
+        T* at = tiles + (((t >> 4) * KD + (d >> 5)) * 64 + g * 16 + (t & 15)) * 8 + h * 4;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) { at[j] = x[j]; at[128 + j] = x[4 + j]; }
+    }
+}
+
+// Factors of a chunk's tokens that k_gdr_prep leaves, rows of 64 floats.
+enum GdrCo { kA1, kA2, kA3, kA3b, kBeta, kRq, kRk, kEnd, kGdrCo };
+// kA1 e^G / |k|;  kA2 scale e^G / |q|;  kA3b e^(G_last - G) / |k|;  kA3 = beta kA3b;  kEnd e^G_last (all 64)
+
+// ---------------------------------------------------------------------------
+// A chunk of one head: its factors, (1 + N)^-1 and P. Sums of g in 64 bits: a reset, or a decay of
+// any size, is a term of -200 at least (e^-200 is 0 in fp32), and the differences of what
+// follows keep their digits. The inverse: blocks of 16 on the diagonal row by row, one wave each, and
+// below them block by block, T_ij = -T_ii sum_l N_il T_lj, in fp32 products.
+// BACK: the transposed operands, and D / |k_j|, N / beta and P tile by tile as the results lie.
+template <typename T, int DKP, bool BACK>
+__global__ void __launch_bounds__(256)
+k_gdr_prep(const LaunchGdr p) {
+    constexpr int KD = DKP / 32, LD = 65;
+    constexpr int kTiles = 2 * 64 * DKP * (int)sizeof(T), kMats = 3 * 64 * LD * 4;
+    __shared__ alignas(16) char lds[kTiles > kMats ? kTiles : kMats];
+    __shared__ double sg[64];
+    __shared__ float sco[kGdrCo][64];
+    T *tk = reinterpret_cast<T*>(lds), *tq = tk + 64 * DKP;
+    float (*mn)[LD] = reinterpret_cast<float (*)[LD]>(lds), (*mt_)[LD] = mn + 64, (*mp)[LD] = mn + 128;
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, g = lane >> 4, m = lane & 15;
+    const int64_t id = blockIdx.x, nc = p.nchunks;
+    const int64_t n = id % nc, bh = id / nc, b = bh / p.H, t0 = n * kGdrC;
+    const int h = (int)(bh % p.H), hk = h / (p.H / p.Hk);
+
+    gdr_stage<T, KD>(tk, p.k, b, t0, p.L, hk, p.dk, p.vec);
+    gdr_stage<T, KD>(tq, p.q, b, t0, p.L, hk, p.dk, p.vec);
+    if (w == 0) {
+        const int64_t t = t0 + lane;
+        double G = 0.0;
+        float beta = 0.0f;
+        if (t < p.L) {
+            const int64_t at = (b * p.L + t) * p.H + h;
+            G = (double)p.g[at];
+            beta = p.beta[at];
+            if (G < -200.0 || (p.reset && p.reset[b * p.L + t])) G = -200.0;
+        }
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const double u = __shfl_up(G, o, 64);
+            if (lane >= o) G += u;
+        }
+        sg[lane] = G;
+        const double last = __shfl(G, 63, 64);
+        sco[kBeta][lane] = beta;
+        sco[kA1][lane] = expf((float)G);
+        sco[kA3b][lane] = expf((float)(last - G));
+        sco[kEnd][lane] = expf((float)last);
+    }
+    __syncthreads();
+    // lengths: wave 0 of k's rows, wave 1 of q's; a lane sums one row from LDS
+    if (w < 2) {
+        const T* tl = w ? tq : tk;
+        float r = 1.0f;
+        if (p.eps > 0.0f) {
+            float s = 0.0f;
+            for (int d = 0; d < KD; ++d)
+#pragma unroll
+                for (int gg = 0; gg < 4; ++gg)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float x = gdr_f<T>(tl[(((lane >> 4) * KD + d) * 64 + gg * 16 + (lane & 15)) * 8 + j]);
+                        s = __builtin_fmaf(x, x, s);
+                    }
+            r = 1.0f / sqrtf(s + p.eps);
+        }
+        sco[w ? kRq : kRk][lane] = r;
+    }
+    // products of keys, and of queries and keys, of the lower triangle's ten tiles
+    gf4 akk[3], aqk[3];
+#pragma unroll
+    for (int u = 0; u < 3; ++u) {
+        akk[u] = aqk[u] = gf4{0, 0, 0, 0};
+        const int tile = w + 4 * u;
+        if (tile < 10) {
+            const int mt = tile < 1 ? 0 : tile < 3 ? 1 : tile < 6 ? 2 : 3, nt = tile - mt * (mt + 1) / 2;
+#pragma unroll
+            for (int s = 0; s < KD; ++s) {
+                const auto kb = Mx<T>::ld(tk + ((nt * KD + s) * 64 + lane) * 8);
+                akk[u] = Mx<T>::mm(Mx<T>::ld(tk + ((mt * KD + s) * 64 + lane) * 8), kb, akk[u]);
+                aqk[u] = Mx<T>::mm(Mx<T>::ld(tq + ((mt * KD + s) * 64 + lane) * 8), kb, aqk[u]);
+            }
+        }
+    }
+    __syncthreads();
+    if (tid < 64) {
+        const float rk = sco[kRk][tid], rq = sco[kRq][tid], e = sco[kA1][tid];
+        sco[kA1][tid] = e * rk;
+        sco[kA2][tid] = e * rq * p.scale;
+        sco[kA3b][tid] *= rk;
+        sco[kA3][tid] = sco[kA3b][tid] * sco[kBeta][tid];
+    }
+    __syncthreads();
+    float* co = p.co + id * (kGdrCo * 64);
+    for (int e = tid; e < kGdrCo * 64; e += 256) co[e] = sco[e >> 6][e & 63];
+    // tiles of N / beta (no beta yet) and P to LDS; zeros on and above N's diagonal, above P's
+    for (int e = tid; e < 64 * 64; e += 256) {
+        const int i = e >> 6, j = e & 63;
+        if ((j >> 4) > (i >> 4)) mn[i][j] = mp[i][j] = mt_[i][j] = 0.0f;
+    }
+#pragma unroll
+    for (int u = 0; u < 3; ++u) {
+        const int tile = w + 4 * u;
+        if (tile < 10) {
+            const int mt = tile < 1 ? 0 : tile < 3 ? 1 : tile < 6 ? 2 : 3, nt = tile - mt * (mt + 1) / 2;
+            const int j = nt * 16 + m;
+            const float rk = sco[kRk][j];
+            gf4 vd, vn, vp;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int i = mt * 16 + 4 * g + r;
+                const float d = i >= j ? expf((float)(sg[i] - sg[j])) * rk : 0.0f;
+                // a factor of 0 is a decay to nothing: what it multiplies is left out, whatever it is
+                vd[r] = d;
+                mn[i][j] = vn[r] = i > j && d != 0.0f ? akk[u][r] * sco[kRk][i] * d : 0.0f;
+                mp[i][j] = vp[r] = i >= j && d != 0.0f ? aqk[u][r] * (sco[kRq][i] * p.scale) * d : 0.0f;
+            }
+            if constexpr (BACK) {
+                gf4* raw = reinterpret_cast<gf4*>(p.raw + (id * 30 + tile) * 256) + lane;
+                raw[0] = vd;
+                raw[640] = vn;
+                raw[1280] = vp;
+            }
+        }
+    }
+    __syncthreads();
+    // the inverse's diagonal blocks: lane m of wave w has column m of block w
+    if (lane < 16) {
+        float x[16];
+        const int o = w * 16;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float s = i == lane ? 1.0f : 0.0f;
+#pragma unroll
+            for (int l = 0; l < i; ++l) s = __builtin_fmaf(-mn[o + i][o + l] * sco[kBeta][o + l], x[l], s);
+            x[i] = s;
+            mt_[o + i][o + lane] = s;
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int lev = 1; lev < 4; ++lev) {
+        if (w + lev < 4) {
+            const int j = w, i = w + lev;
+            gf4 acc = {0, 0, 0, 0}, out = {0, 0, 0, 0};
+            for (int l = j; l < i; ++l)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int c = 16 * l + 4 * g + r;
+                    acc = __builtin_amdgcn_mfma_f32_16x16x4f32(mn[16 * i + m][c] * sco[kBeta][c], mt_[c][16 * j + m], acc, 0, 0, 0);
+                }
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                out = __builtin_amdgcn_mfma_f32_16x16x4f32(-mt_[16 * i + m][16 * i + 4 * g + r], acc[r], out, 0, 0, 0);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) mt_[16 * i + 4 * g + r][16 * j + m] = out[r];
+        }
+        __syncthreads();
+    }
+    // out, in the order of operands: T and P beta, or their transposes
+    float *ot = p.wT + id * (6 * 512), *op = p.wP + id * (6 * 512);
+    for (int e = tid; e < 6 * 512; e += 256) {
+        const int blk = e >> 9, l = e >> 3 & 63, j = e & 7;
+        int mt, s;
+        if constexpr (BACK) { mt = blk < 4 ? blk >> 1 : blk - 2; s = blk < 4 ? blk & 1 : 1; }
+        else { mt = blk < 2 ? blk : (blk + 2) >> 1; s = blk < 2 ? 0 : blk & 1; }
+        const int row = mt * 16 + (l & 15), col = s * 32 + (j >> 2) * 16 + 4 * (l >> 4) + (j & 3);
+        const int a = BACK ? col : row, c = BACK ? row : col;
+        ot[e] = mt_[a][c];
+        op[e] = mp[a][c] * sco[kBeta][c];
+    }
+}
+
+// ---------------------------------------------------------------------------
+// From chunk to chunk: a workgroup holds 64 CT columns of one head's state, a wave 16 CT of them.
+template <typename T, int DKP, int CT, bool CK>
+__global__ void __launch_bounds__(256)
+k_gdr_walk(const LaunchGdr p) {
+    using M = Mx<T>;
+    constexpr int KD = DKP / 32, ND = DKP / 16;
+    __shared__ alignas(16) T tk[64 * DKP], tq[64 * DKP];
+    __shared__ alignas(16) T tt[M::NT][6 * 512], tp[M::NP][6 * 512];
+    __shared__ alignas(16) float sco[kGdrCo][64];
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, g = lane >> 4, m = lane & 15;
+    const int64_t BH = p.B * p.H, bh = blockIdx.x % BH, b = bh / p.H, nc = p.nchunks;
+    const int h = (int)(bh % p.H), hk = h / (p.H / p.Hk);
+    const int col0 = ((int)(blockIdx.x / BH) * 4 + w) * (16 * CT) + m;
+    const T* vb = static_cast<const T*>(p.v.p) + b * p.v.batch_stride + h * p.v.head_stride;
+    T* yb = static_cast<T*>(p.y) + (b * p.L * p.H + h) * p.dv;
+    float* st = p.state ? p.state + bh * p.dk * p.dv : nullptr;
+
+    gf4 S[CT][ND];
+#pragma unroll
+    for (int c = 0; c < CT; ++c)
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = d * 16 + 4 * g + r, col = col0 + 16 * c;
+                S[c][d][r] = st && row < p.dk && col < p.dv ? st[row * p.dv + col] : 0.0f;
+            }
+
+    for (int64_t n = 0; n < nc; ++n) {
+        const int64_t t0 = n * kGdrC, id = bh * nc + n;
+        __syncthreads();
+        gdr_stage<T, KD>(tk, p.k, b, t0, p.L, hk, p.dk, p.vec);
+        gdr_stage<T, KD>(tq, p.q, b, t0, p.L, hk, p.dk, p.vec);
+        for (int e = tid; e < 6 * 64; e += 256) {
+            const auto x = M::template split<M::NT>(*reinterpret_cast<const gf8*>(p.wT + id * 3072 + e * 8));
+            const auto y = M::template split<M::NP>(*reinterpret_cast<const gf8*>(p.wP + id * 3072 + e * 8));
+#pragma unroll
+            for (int k = 0; k < M::NT; ++k) *reinterpret_cast<typename M::F*>(&tt[k][e * 8]) = x.t[k];
+#pragma unroll
+            for (int k = 0; k < M::NP; ++k) *reinterpret_cast<typename M::F*>(&tp[k][e * 8]) = y.t[k];
+        }
+        for (int e = tid; e < kGdrCo * 64; e += 256) sco[e >> 6][e & 63] = p.co[id * (kGdrCo * 64) + e];
+        gf4 V[CT][4];
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int64_t t = t0 + 16 * i + 4 * g + r;
+                    V[c][i][r] = t < p.L && col0 + 16 * c < p.dv ? IO<T>::ld(vb + t * p.v.token_stride + col0 + 16 * c) : 0.0f;
+                }
+        __syncthreads();
+        if constexpr (CK) {
+            float* ck = p.ckpt + (bh * nc + n) * p.dk * p.dv;
+#pragma unroll
+            for (int c = 0; c < CT; ++c)
+#pragma unroll
+                for (int d = 0; d < ND; ++d)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int row = d * 16 + 4 * g + r, col = col0 + 16 * c;
+                        if (row < p.dk && col < p.dv) ck[(int64_t)row * p.dv + col] = S[c][d][r];
+                    }
+        }
+        // K S0 and Q S0
+        gf4 ks[CT][4] = {}, qs[CT][4] = {};
+#pragma unroll
+        for (int s = 0; s < KD; ++s) {
+            typename M::template S<3> sb[CT];
+#pragma unroll
+            for (int c = 0; c < CT; ++c) sb[c] = M::template split<3>(gdr_pair(S[c][2 * s], S[c][2 * s + 1]));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const auto kf = M::ld(tk + ((i * KD + s) * 64 + lane) * 8), qf = M::ld(tq + ((i * KD + s) * 64 + lane) * 8);
+#pragma unroll
+                for (int c = 0; c < CT; ++c) {
+                    ks[c][i] = M::template mul<3>(kf, sb[c], ks[c][i]);
+                    if constexpr (sizeof(T) == 2) qs[c][i] = M::mm(qf, sb[c].t[0], M::mm(qf, sb[c].t[1], qs[c][i]));
+                    else qs[c][i] = M::mm(qf, sb[c].t[0], qs[c][i]);
+                }
+            }
+        }
+        // X = T (V - e^G K S0); a factor of 0 leaves out what it multiplies
+        gf4 X[CT][4] = {};
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const gf4 a1 = *reinterpret_cast<const gf4*>(&sco[kA1][16 * i + 4 * g]), a2 = *reinterpret_cast<const gf4*>(&sco[kA2][16 * i + 4 * g]);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    V[c][i][r] -= a1[r] != 0.0f ? a1[r] * ks[c][i][r] : 0.0f;
+                    qs[c][i][r] = a2[r] != 0.0f ? a2[r] * qs[c][i][r] : 0.0f;
+                }
+            }
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            typename M::template S<M::NT> rb[CT];
+#pragma unroll
+            for (int c = 0; c < CT; ++c) rb[c] = M::template split<M::NT>(gdr_pair(V[c][2 * s], V[c][2 * s + 1]));
+#pragma unroll
+            for (int i = 2 * s; i < 4; ++i) {
+                typename M::template S<M::NT> tf;
+#pragma unroll
+                for (int k = 0; k < M::NT; ++k) tf.t[k] = M::ld(&tt[k][(gdr_low(i, s) * 64 + lane) * 8]);
+#pragma unroll
+                for (int c = 0; c < CT; ++c) X[c][i] = M::mul(tf, rb[c], X[c][i]);
+            }
+        }
+        // Y
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            typename M::template S<M::NP> xb[CT];
+#pragma unroll
+            for (int c = 0; c < CT; ++c) xb[c] = M::template split<M::NP>(gdr_pair(X[c][2 * s], X[c][2 * s + 1]));
+#pragma unroll
+            for (int i = 2 * s; i < 4; ++i) {
+                typename M::template S<M::NP> pf;
+#pragma unroll
+                for (int k = 0; k < M::NP; ++k) pf.t[k] = M::ld(&tp[k][(gdr_low(i, s) * 64 + lane) * 8]);
+#pragma unroll
+                for (int c = 0; c < CT; ++c) qs[c][i] = M::mul(pf, xb[c], qs[c][i]);
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int64_t t = t0 + 16 * i + 4 * g + r;
+                    const int col = col0 + 16 * c;
+                    if (t < p.L && col < p.dv) {
+                        IO<T>::st(yb + t * p.H * p.dv + col, qs[c][i][r]);
+                        if constexpr (CK) p.ckptX[((b * p.L + t) * p.H + h) * p.dv + col] = X[c][i][r];
+                    }
+                }
+        // the next state
+        const float end = sco[kEnd][0];
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+#pragma unroll
+            for (int d = 0; d < ND; ++d) S[c][d] = end != 0.0f ? S[c][d] * end : gf4{0, 0, 0, 0};
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            typename M::template S<3> xb[CT];
+            const gf4 a = *reinterpret_cast<const gf4*>(&sco[kA3][32 * s + 4 * g]), e = *reinterpret_cast<const gf4*>(&sco[kA3][32 * s + 16 + 4 * g]);
+#pragma unroll
+            for (int c = 0; c < CT; ++c) xb[c] = M::template split<3>(gdr_pair(X[c][2 * s] * a, X[c][2 * s + 1] * e));
+#pragma unroll
+            for (int d = 0; d < ND; ++d) {
+                const auto kf = M::template ldt<KD>(tk, s, d, lane);
+#pragma unroll
+                for (int c = 0; c < CT; ++c) S[c][d] = M::template mul<3>(kf, xb[c], S[c][d]);
+            }
+        }
+    }
+    if (st) {
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+#pragma unroll
+            for (int d = 0; d < ND; ++d)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int row = d * 16 + 4 * g + r, col = col0 + 16 * c;
+                    if (row < p.dk && col < p.dv) st[row * p.dv + col] = S[c][d][r];
+                }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// The backward from chunk to chunk, the last first, with W the gradient of the state behind a chunk in
+// registers as the forward has the state:
+//   dX = (P beta)^T dY + beta e^(G_last - G) K W,  dV = T^T dX,
+//   W' = e^G_last W + (scale e^G Q)^T dY - (e^G K)^T dV
+template <typename T, int DKP, int CT>
+__global__ void __launch_bounds__(256)
+k_gdr_walk_back(const LaunchGdr p) {
+    using M = Mx<T>;
+    constexpr int KD = DKP / 32, ND = DKP / 16;
+    __shared__ alignas(16) T tk[64 * DKP], tq[64 * DKP];
+    __shared__ alignas(16) T tt[M::NT][6 * 512], tp[M::NT][6 * 512];
+    __shared__ alignas(16) float sco[kGdrCo][64];
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, g = lane >> 4, m = lane & 15;
+    const int64_t BH = p.B * p.H, bh = blockIdx.x % BH, b = bh / p.H, nc = p.nchunks;
+    const int h = (int)(bh % p.H), hk = h / (p.H / p.Hk);
+    const int col0 = ((int)(blockIdx.x / BH) * 4 + w) * (16 * CT) + m;
+    const T* dyb = static_cast<const T*>(p.gr.dy) + (b * p.L * p.H + h) * p.dv;
+    T* dvb = static_cast<T*>(p.gr.dv) + (b * p.L * p.H + h) * p.dv;
+    float* wvb = p.wV + (b * p.L * p.H + h) * p.dv;
+
+    gf4 S[CT][ND];
+#pragma unroll
+    for (int c = 0; c < CT; ++c)
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = d * 16 + 4 * g + r, col = col0 + 16 * c;
+                S[c][d][r] = p.gr.dstate_final && row < p.dk && col < p.dv ? p.gr.dstate_final[(bh * p.dk + row) * p.dv + col] : 0.0f;
+            }
+
+    for (int64_t n = nc - 1; n >= 0; --n) {
+        const int64_t t0 = n * kGdrC, id = bh * nc + n;
+        __syncthreads();
+        gdr_stage<T, KD>(tk, p.k, b, t0, p.L, hk, p.dk, p.vec);
+        gdr_stage<T, KD>(tq, p.q, b, t0, p.L, hk, p.dk, p.vec);
+        for (int e = tid; e < 6 * 64; e += 256) {
+            const auto x = M::template split<M::NT>(*reinterpret_cast<const gf8*>(p.wT + id * 3072 + e * 8));
+            const auto y = M::template split<M::NT>(*reinterpret_cast<const gf8*>(p.wP + id * 3072 + e * 8));
+#pragma unroll
+            for (int k = 0; k < M::NT; ++k) *reinterpret_cast<typename M::F*>(&tt[k][e * 8]) = x.t[k];
+#pragma unroll
+            for (int k = 0; k < M::NT; ++k) *reinterpret_cast<typename M::F*>(&tp[k][e * 8]) = y.t[k];
+        }
+        for (int e = tid; e < kGdrCo * 64; e += 256) sco[e >> 6][e & 63] = p.co[id * (kGdrCo * 64) + e];
+        gf4 dY[CT][4];
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int64_t t = t0 + 16 * i + 4 * g + r;
+                    dY[c][i][r] = t < p.L && col0 + 16 * c < p.dv ? IO<T>::ld(dyb + t * p.H * p.dv + col0 + 16 * c) : 0.0f;
+                }
+        float* ws = p.wS + id * p.dk * p.dv;
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+#pragma unroll
+            for (int d = 0; d < ND; ++d)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int row = d * 16 + 4 * g + r, col = col0 + 16 * c;
+                    if (row < p.dk && col < p.dv) ws[row * p.dv + col] = S[c][d][r];
+                }
+        __syncthreads();
+        gf4 dX[CT][4] = {};
+#pragma unroll
+        for (int s = 0; s < KD; ++s) {
+            typename M::template S<3> sb[CT];
+#pragma unroll
+            for (int c = 0; c < CT; ++c) sb[c] = M::template split<3>(gdr_pair(S[c][2 * s], S[c][2 * s + 1]));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const auto kf = M::ld(tk + ((i * KD + s) * 64 + lane) * 8);
+#pragma unroll
+                for (int c = 0; c < CT; ++c) dX[c][i] = M::template mul<3>(kf, sb[c], dX[c][i]);
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const gf4 a3 = *reinterpret_cast<const gf4*>(&sco[kA3][16 * i + 4 * g]);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) dX[c][i][r] = a3[r] != 0.0f ? a3[r] * dX[c][i][r] : 0.0f;
+            }
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            typename M::template S<1> ob[CT];           // exact: one term
+#pragma unroll
+            for (int c = 0; c < CT; ++c) ob[c] = M::template split<1>(gdr_pair(dY[c][2 * s], dY[c][2 * s + 1]));
+#pragma unroll
+            for (int i = 0; i < 2 * s + 2; ++i) {
+                typename M::template S<M::NT> pf;
+#pragma unroll
+                for (int k = 0; k < M::NT; ++k) pf.t[k] = M::ld(&tp[k][(gdr_up(i, s) * 64 + lane) * 8]);
+#pragma unroll
+                for (int c = 0; c < CT; ++c) dX[c][i] = M::template mul<M::NT>(pf, ob[c].t[0], dX[c][i]);
+            }
+        }
+        gf4 dV[CT][4] = {};
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            typename M::template S<M::NT> xb[CT];
+#pragma unroll
+            for (int c = 0; c < CT; ++c) xb[c] = M::template split<M::NT>(gdr_pair(dX[c][2 * s], dX[c][2 * s + 1]));
+#pragma unroll
+            for (int i = 0; i < 2 * s + 2; ++i) {
+                typename M::template S<M::NT> tf;
+#pragma unroll
+                for (int k = 0; k < M::NT; ++k) tf.t[k] = M::ld(&tt[k][(gdr_up(i, s) * 64 + lane) * 8]);
+#pragma unroll
+                for (int c = 0; c < CT; ++c) dV[c][i] = M::mul(tf, xb[c], dV[c][i]);
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int64_t t = t0 + 16 * i + 4 * g + r;
+                    const int col = col0 + 16 * c;
+                    if (t < p.L && col < p.dv) {
+                        IO<T>::st(dvb + t * p.H * p.dv + col, dV[c][i][r]);
+                        wvb[t * p.H * p.dv + col] = dV[c][i][r];
+                    }
+                }
+        const float end = sco[kEnd][0];
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+#pragma unroll
+            for (int d = 0; d < ND; ++d) S[c][d] = end != 0.0f ? S[c][d] * end : gf4{0, 0, 0, 0};
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            typename M::template S<3> ob[CT], vb[CT];
+#pragma unroll
+            for (int c = 0; c < CT; ++c) {
+                gf4 o[2], v[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const gf4 a1 = *reinterpret_cast<const gf4*>(&sco[kA1][32 * s + 16 * e + 4 * g]);
+                    const gf4 a2 = *reinterpret_cast<const gf4*>(&sco[kA2][32 * s + 16 * e + 4 * g]);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        o[e][r] = a2[r] != 0.0f ? a2[r] * dY[c][2 * s + e][r] : 0.0f;
+                        v[e][r] = a1[r] != 0.0f ? -a1[r] * dV[c][2 * s + e][r] : 0.0f;
+                    }
+                }
+                ob[c] = M::template split<3>(gdr_pair(o[0], o[1]));
+                vb[c] = M::template split<3>(gdr_pair(v[0], v[1]));
+            }
+#pragma unroll
+            for (int d = 0; d < ND; ++d) {
+                const auto kf = M::template ldt<KD>(tk, s, d, lane), qf = M::template ldt<KD>(tq, s, d, lane);
+#pragma unroll
+                for (int c = 0; c < CT; ++c) S[c][d] = M::template mul<3>(kf, vb[c], M::template mul<3>(qf, ob[c], S[c][d]));
+            }
+        }
+    }
+    if (p.gr.dstate_init) {
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+#pragma unroll
+            for (int d = 0; d < ND; ++d)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int row = d * 16 + 4 * g + r, col = col0 + 16 * c;
+                    if (row < p.dk && col < p.dv) p.gr.dstate_init[(bh * p.dk + row) * p.dv + col] = S[c][d][r];
+                }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// The gradients of a chunk's keys, queries and gates, all chunks at once, from the states in front (S0) and
+// their gradients behind (W), X and dV:
+//   dq = a2 dY S0^T + E' K,     dk = a3 X W^T - a1 dV S0^T + E'^T Q + (F + F^T) K
+//   E = dY X^T (i >= j), F = -dV X^T (i > j), each times beta_j and what P and N have beside the product of their rows
+//   dbeta_j = k_j . (a3b X W^T)_j + sum_i E_ij P_ij + F_ij N_ij / beta_j     (E, F without beta)
+//   dg_t: every term that a token from t on has from one in front of t, summed as such (no difference of
+//   two sums, so that the gradient of a small decay, which has it as a factor, keeps its digits):
+//   sum_{i >= t > j} beta_j (E P + F N/beta)_ij + sum_{i >= t} (q . a2 dY S0^T - k . a1 dV S0^T)_i
+//     + sum_{j < t} beta_j (k . a3b X W^T)_j + e^G_last <S0, W>
+// A wave has a quarter of dk's columns; terms over dv go through LDS 32 at a time.
+__device__ __forceinline__ void gdr_tile(int tile, int& mt, int& nt) {
+    mt = tile < 1 ? 0 : tile < 3 ? 1 : tile < 6 ? 2 : 3;
+    nt = tile - mt * (mt + 1) / 2;
+}
+
+// eight fp32 values of a row, zeros past its end
+__device__ __forceinline__ gf8 gdr_ld8(const float* row, int c, int n, bool there, bool vec) {
+    gf8 v = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (!there) return v;
+    if (vec && c + 8 <= n) {
+        const gf4 a = *reinterpret_cast<const gf4*>(row + c), b = *reinterpret_cast<const gf4*>(row + c + 4);
+        return gdr_pair(a, b);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = c + j < n ? row[c + j] : 0.0f;
+    return v;
+}
+
+template <typename T, int DKP>
+__global__ void __launch_bounds__(256)
+k_gdr_grads(const LaunchGdr p) {
+    using M = Mx<T>;
+    constexpr int KD = DKP / 32, NS = DKP / 64, LD = 68;
+    constexpr int kSlice = 4 * 512;                              // 64 rows of 32 terms
+    constexpr int kPhase1 = (2 * M::NT + 1) * kSlice * (int)sizeof(T);
+    constexpr int kPhase2 = 64 * DKP * (int)sizeof(T) + 3 * 64 * LD * 4;
+    __shared__ alignas(16) char lds[kPhase1 > kPhase2 ? kPhase1 : kPhase2];
+    __shared__ alignas(16) float sco[kGdrCo][64];
+    __shared__ float rows[3][4][64], colsum[4][64], wsum[4];
+    T (*lx)[kSlice] = reinterpret_cast<T (*)[kSlice]>(lds), (*lv)[kSlice] = lx + M::NT, *lo = lx[2 * M::NT];
+    T* tk = reinterpret_cast<T*>(lds);
+    float (*me)[LD] = reinterpret_cast<float (*)[LD]>(lds + 64 * DKP * sizeof(T)), (*mf)[LD] = me + 64, (*mg)[LD] = mf + 64;
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, g = lane >> 4, m = lane & 15;
+    const int64_t id = blockIdx.x, nc = p.nchunks, n = id % nc, bh = id / nc, b = bh / p.H, t0 = n * kGdrC;
+    const int h = (int)(bh % p.H), hk = h / (p.H / p.Hk);
+    const bool vec = p.dv % 4 == 0;
+    const float *S0 = p.ckpt + id * p.dk * p.dv, *W = p.wS + id * p.dk * p.dv;
+    const bool vecs = vec && (reinterpret_cast<uintptr_t>(p.ckpt) & 15) == 0, vecx = vec && (reinterpret_cast<uintptr_t>(p.ckptX) & 15) == 0;
+    const int64_t row0 = (b * p.L + t0) * p.H + h;               // of tokens' rows of dv; H rows from token to token
+    const T* dy = static_cast<const T*>(p.gr.dy);
+    for (int e = tid; e < kGdrCo * 64; e += 256) sco[e >> 6][e & 63] = p.co[id * (kGdrCo * 64) + e];
+    for (int e = tid; e < 4 * 64; e += 256) colsum[e >> 6][e & 63] = 0.0f;
+
+    gf4 aq[NS][4] = {}, av[NS][4] = {}, ax[NS][4] = {}, ae[3] = {}, af[3] = {};
+    float ww = 0.0f;
+    for (int c0 = 0; c0 < p.dv; c0 += 32) {
+        __syncthreads();
+        {
+            const int t = tid >> 2, o = tid & 3, c = c0 + o * 8, at = ((t >> 4) * 64 + o * 16 + (t & 15)) * 8;
+            const bool there = t0 + t < p.L;
+            const int64_t row = (row0 + (int64_t)t * p.H) * p.dv;
+            const auto x = M::template split<M::NT>(gdr_ld8(p.ckptX + row, c, p.dv, there, vecx));
+            const auto v = M::template split<M::NT>(gdr_ld8(p.wV + row, c, p.dv, there, vec));
+#pragma unroll
+            for (int k = 0; k < M::NT; ++k) {
+                *reinterpret_cast<typename M::F*>(&lx[k][at]) = x.t[k];
+                *reinterpret_cast<typename M::F*>(&lv[k][at]) = v.t[k];
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) lo[at + j] = there && c + j < p.dv ? dy[row + c + j] : T(0);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < NS; ++u) {
+            const int r = (w * NS + u) * 16 + m, c = c0 + 8 * g;
+            const gf8 s0 = gdr_ld8(S0 + (int64_t)r * p.dv, c, p.dv, r < p.dk, vecs), s1 = gdr_ld8(W + (int64_t)r * p.dv, c, p.dv, r < p.dk, vec);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) ww = __builtin_fmaf(s0[j], s1[j], ww);
+            const auto sb = M::template split<M::NT>(s0), wb = M::template split<M::NT>(s1);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int at = (i * 64 + lane) * 8;
+                typename M::template S<M::NT> xf, vf;
+#pragma unroll
+                for (int k = 0; k < M::NT; ++k) { xf.t[k] = M::ld(&lx[k][at]); vf.t[k] = M::ld(&lv[k][at]); }
+                aq[u][i] = M::template mul<M::NT>(M::ld(lo + at), sb, aq[u][i]);
+                av[u][i] = M::mul(vf, sb, av[u][i]);
+                ax[u][i] = M::mul(xf, wb, ax[u][i]);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 3; ++u) {
+            const int tile = w + 4 * u;
+            if (tile < 10) {
+                int mt, nt;
+                gdr_tile(tile, mt, nt);
+                typename M::template S<M::NT> xf, vf;
+#pragma unroll
+                for (int k = 0; k < M::NT; ++k) { xf.t[k] = M::ld(&lx[k][(nt * 64 + lane) * 8]); vf.t[k] = M::ld(&lv[k][(mt * 64 + lane) * 8]); }
+                ae[u] = M::template mul<M::NT>(M::ld(lo + (mt * 64 + lane) * 8), xf, ae[u]);
+                af[u] = M::mul(vf, xf, af[u]);
+            }
+        }
+    }
+    __syncthreads();
+    // keys to LDS; the pairs of tokens: E', F + F^T and the terms of dg to LDS
+    gdr_stage<T, KD>(tk, p.k, b, t0, p.L, hk, p.dk, p.vec);
+    for (int e = tid; e < 64 * 64; e += 256)
+        if ((e & 63) >= (e >> 6)) {
+            if ((e & 63) > (e >> 6)) me[e >> 6][e & 63] = 0.0f;
+            mg[e >> 6][e & 63] = 0.0f;
+        }
+#pragma unroll
+    for (int u = 0; u < 3; ++u) {
+        const int tile = w + 4 * u;
+        if (tile < 10) {
+            int mt, nt;
+            gdr_tile(tile, mt, nt);
+            const gf4* raw = reinterpret_cast<const gf4*>(p.raw + (id * 30 + tile) * 256) + lane;
+            const gf4 d = raw[0], nn = raw[640], pp = raw[1280];
+            const int j = nt * 16 + m;
+            const float beta = sco[kBeta][j];
+            float s = 0.0f;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int i = mt * 16 + 4 * g + r;
+                if (i < j) continue;
+                // where the decay is nothing no gradient passes
+                const float e = d[r] != 0.0f ? ae[u][r] : 0.0f, f = i > j && d[r] != 0.0f ? -af[u][r] : 0.0f;
+                const float term = e * pp[r] + f * nn[r];
+                s += term;
+                me[i][j] = e * beta * d[r] * (sco[kRq][i] * p.scale);
+                if (i > j) mg[i][j] = term * beta;
+                mf[i][j] = mf[j][i] = f * beta * d[r] * sco[kRk][i];
+            }
+            s += __shfl_xor(s, 16, 64);
+            s += __shfl_xor(s, 32, 64);
+            if (g == 0) colsum[mt][j] = s;
+        }
+    }
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) ww += __shfl_xor(ww, o, 64);
+    if (lane == 0) wsum[w] = ww;
+    __syncthreads();
+    // sums over dk of a token's row; q's values from memory
+    {
+        const T* qb = static_cast<const T*>(p.q.p) + b * p.q.batch_stride + hk * p.q.head_stride;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const gf4 a1 = *reinterpret_cast<const gf4*>(&sco[kA1][16 * i + 4 * g]), a2 = *reinterpret_cast<const gf4*>(&sco[kA2][16 * i + 4 * g]);
+            const gf4 a3 = *reinterpret_cast<const gf4*>(&sco[kA3b][16 * i + 4 * g]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                float y = 0.0f, z = 0.0f;
+                const int64_t t = t0 + 16 * i + 4 * g + r;
+#pragma unroll
+                for (int u = 0; u < NS; ++u) {
+                    const int d = (w * NS + u) * 16 + m;
+                    const float kv = gdr_f<T>(tk[((i * KD + (d >> 5)) * 64 + (d >> 2 & 3) * 16 + 4 * g + r) * 8 + (d >> 4 & 1) * 4 + (d & 3)]);
+                    const float qv = t < p.L && d < p.dk ? IO<T>::ld(qb + t * p.q.token_stride + d) : 0.0f;
+                    aq[u][i][r] = a2[r] != 0.0f ? a2[r] * aq[u][i][r] : 0.0f;
+                    av[u][i][r] = a1[r] != 0.0f ? a1[r] * av[u][i][r] : 0.0f;
+                    ax[u][i][r] = a3[r] != 0.0f ? a3[r] * ax[u][i][r] : 0.0f;
+                    y = __builtin_fmaf(qv, aq[u][i][r], y);
+                    y = __builtin_fmaf(-kv, av[u][i][r], y);
+                    z = __builtin_fmaf(kv, ax[u][i][r], z);
+                }
+#pragma unroll
+                for (int o = 1; o < 16; o <<= 1) {
+                    y += __shfl_xor(y, o, 64);
+                    z += __shfl_xor(z, o, 64);
+                }
+                if (m == 0) {
+                    rows[0][w][16 * i + 4 * g + r] = y;
+                    rows[1][w][16 * i + 4 * g + r] = z;
+                }
+            }
+        }
+    }
+    __syncthreads();
+    // gates
+    if (w == 0) {
+        const int t = lane;
+        float y = rows[0][0][t] + rows[0][1][t] + rows[0][2][t] + rows[0][3][t];
+        const float z = rows[1][0][t] + rows[1][1][t] + rows[1][2][t] + rows[1][3][t];
+        const float zb = z * sco[kBeta][t];
+        float run = 0.0f;                                        // mg's row t: sums in front of each column
+        for (int j = 0; j < 64; ++j) {
+            const float v = mg[t][j];
+            mg[t][j] = run;
+            run += v;
+        }
+        float before = zb;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const float u = __shfl_up(before, o, 64), v = __shfl_down(y, o, 64);
+            if (lane >= o) before += u;
+            if (lane + o < 64) y += v;
+        }
+        before = __shfl_up(before, 1, 64);
+        if (lane == 0) before = 0.0f;
+        const float end = sco[kEnd][0];
+        float dg = y + before + (end != 0.0f ? end * (wsum[0] + wsum[1] + wsum[2] + wsum[3]) : 0.0f);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");
+        __builtin_amdgcn_wave_barrier();
+        float s = 0.0f;
+        for (int i = 0; i < 64; ++i)
+            if (i >= t) s += mg[i][t];
+        dg += s;
+        if (t0 + t < p.L) {
+            const int64_t at = row0 + (int64_t)t * p.H;
+            p.gr.dg[at] = p.reset && p.reset[b * p.L + t0 + t] ? 0.0f : dg;
+            p.gr.dbeta[at] = z + colsum[0][t] + colsum[1][t] + colsum[2][t] + colsum[3][t];
+        }
+    }
+    // dq = aq + E' K;  dk = beta ax - av + (F + F^T) K + E'^T Q
+    gf4 dk[NS][4];
+#pragma unroll
+    for (int u = 0; u < NS; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dk[u][i] = ax[u][i] * *reinterpret_cast<const gf4*>(&sco[kBeta][16 * i + 4 * g]) - av[u][i];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        typename M::F kf[NS];
+#pragma unroll
+        for (int u = 0; u < NS; ++u) kf[u] = M::template ldt<KD>(tk, s, w * NS + u, lane);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = 16 * i + m, c = 32 * s + 4 * g;
+            const auto ef = M::template split<M::NP>(gdr_pair(*reinterpret_cast<const gf4*>(&me[r][c]), *reinterpret_cast<const gf4*>(&me[r][c + 16])));
+            const auto ff = M::template split<M::NP>(gdr_pair(*reinterpret_cast<const gf4*>(&mf[r][c]), *reinterpret_cast<const gf4*>(&mf[r][c + 16])));
+#pragma unroll
+            for (int u = 0; u < NS; ++u) {
+                if (i >= 2 * s) aq[u][i] = M::template mul<M::NP>(ef, kf[u], aq[u][i]);
+                dk[u][i] = M::template mul<M::NP>(ff, kf[u], dk[u][i]);
+            }
+        }
+    }
+    __syncthreads();
+    gdr_stage<T, KD>(tk, p.q, b, t0, p.L, hk, p.dk, p.vec);
+    __syncthreads();
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        typename M::F qf[NS];
+#pragma unroll
+        for (int u = 0; u < NS; ++u) qf[u] = M::template ldt<KD>(tk, s, w * NS + u, lane);
+#pragma unroll
+        for (int i = 0; i < 2 * s + 2; ++i) {
+            gf8 e;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) e[j] = me[32 * s + 16 * (j >> 2) + 4 * g + (j & 3)][16 * i + m];
+            const auto ef = M::template split<M::NP>(e);
+#pragma unroll
+            for (int u = 0; u < NS; ++u) dk[u][i] = M::template mul<M::NP>(ef, qf[u], dk[u][i]);
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < NS; ++u) {
+        const int d = (w * NS + u) * 16 + m;
+        if (d >= p.dk) continue;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int t = 16 * i + 4 * g + r;
+                if (t0 + t < p.L) {
+                    const int64_t at = (row0 + (int64_t)t * p.H) * p.dk + d;
+                    p.part_q[at] = aq[u][i][r];
+                    p.part_k[at] = dk[u][i][r];
+                }
+            }
+    }
+}
+
+// The heads' shares of a key's and a query's gradient, and through the division by the length:
+// d = s - x (x . s) / |x|^2. One wave a row, up to 256 columns.
+template <typename T>
+__global__ void __launch_bounds__(256)
+k_gdr_keys(const LaunchGdr p) {
+    const int lane = threadIdx.x & 63;
+    for (int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); row < p.B * p.L * p.Hk; row += (int64_t)gridDim.x * 4) {
+    const int hk = (int)(row % p.Hk), rep = p.H / p.Hk;
+    const int64_t bt = row / p.Hk, b = bt / p.L, t = bt % p.L;
+    const ss_head_view& v = blockIdx.y ? p.k : p.q;
+    const float* part = (blockIdx.y ? p.part_k : p.part_q) + (bt * p.H + (int64_t)hk * rep) * p.dk;
+    const T* x = static_cast<const T*>(v.p) + b * v.batch_stride + t * v.token_stride + hk * v.head_stride;
+    T* out = static_cast<T*>(blockIdx.y ? p.gr.dk : p.gr.dq) + row * p.dk;
+    float s[4], xv[4], dot = 0.0f, len = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int d = j * 64 + lane;
+        s[j] = 0.0f;
+        xv[j] = d < p.dk ? IO<T>::ld(x + d) : 0.0f;
+        if (d < p.dk)
+            for (int i = 0; i < rep; ++i) s[j] += part[(int64_t)i * p.dk + d];
+        dot = __builtin_fmaf(xv[j], s[j], dot);
+        len = __builtin_fmaf(xv[j], xv[j], len);
+    }
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        dot += __shfl_xor(dot, o, 64);
+        len += __shfl_xor(len, o, 64);
+    }
+    const float c = p.eps > 0.0f ? dot / (len + p.eps) : 0.0f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int d = j * 64 + lane;
+        if (d < p.dk) IO<T>::st(out + d, p.eps > 0.0f ? s[j] - xv[j] * c : s[j]);
+    }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// One token: bound by reading and writing the state. A workgroup has 32 CV columns of one head; eight
+// rows of lanes share the head's rows, all of which are in flight at once, and meet in LDS once:
+//   y = scale (e^g S^T q + (q . k) u),  u = beta (v - e^g S^T k)
+template <typename T, int RPT, int CV>
+__global__ void __launch_bounds__(256)
+k_gdr_step(const LaunchGdr p) {
+    typedef float fv __attribute__((ext_vector_type(CV)));
+    __shared__ float sq[8 * RPT], sk[8 * RPT], dots[3][4];
+    __shared__ alignas(16) float part[2][8][32 * CV];
+    const int tid = threadIdx.x, lane = tid & 31, rg = tid >> 5;
+    const int64_t BH = p.B * p.H, bh = blockIdx.x % BH, b = bh / p.H;
+    const int h = (int)(bh % p.H), hk = h / (p.H / p.Hk);
+    const int col = ((int)(blockIdx.x / BH) * 32 + lane) * CV;
+    float* st = p.state + bh * p.dk * p.dv + col;
+    const bool in = col < p.dv;
+    fv S[RPT];
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+        const int row = i * 8 + rg;
+        S[i] = in && row < p.dk ? __builtin_nontemporal_load(reinterpret_cast<const fv*>(st + row * p.dv)) : fv(0.0f);
+    }
+    float qv = 0.0f, kv = 0.0f;
+    if (tid < p.dk) {
+        qv = IO<T>::ld(static_cast<const T*>(p.q.p) + b * p.q.batch_stride + hk * p.q.head_stride + tid);
+        kv = IO<T>::ld(static_cast<const T*>(p.k.p) + b * p.k.batch_stride + hk * p.k.head_stride + tid);
+    }
+    if (tid < 8 * RPT) { sq[tid] = qv; sk[tid] = kv; }
+    float d[3] = {qv * qv, kv * kv, qv * kv};
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1)
+#pragma unroll
+        for (int j = 0; j < 3; ++j) d[j] += __shfl_xor(d[j], o, 64);
+    if ((tid & 63) == 0) { dots[0][tid >> 6] = d[0]; dots[1][tid >> 6] = d[1]; dots[2][tid >> 6] = d[2]; }
+    const float a = p.reset && p.reset[b] ? 0.0f : expf(p.g[bh]), beta = p.beta[bh];
+    __syncthreads();
+    float rq = 1.0f, rk = 1.0f;
+    if (p.eps > 0.0f) {
+        rq = 1.0f / sqrtf(dots[0][0] + dots[0][1] + dots[0][2] + dots[0][3] + p.eps);
+        rk = 1.0f / sqrtf(dots[1][0] + dots[1][1] + dots[1][2] + dots[1][3] + p.eps);
+    }
+    const float qk = (dots[2][0] + dots[2][1] + dots[2][2] + dots[2][3]) * rq * rk;
+    fv aq = fv(0.0f), ak = fv(0.0f);
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+        if (a == 0.0f) S[i] = fv(0.0f);                    // nothing passes, whatever it is
+        else S[i] *= a;
+        aq += S[i] * sq[i * 8 + rg];
+        ak += S[i] * sk[i * 8 + rg];
+    }
+    *reinterpret_cast<fv*>(&part[0][rg][lane * CV]) = aq;
+    *reinterpret_cast<fv*>(&part[1][rg][lane * CV]) = ak;
+    __syncthreads();
+    if (!in) return;
+    aq = ak = fv(0.0f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        aq += *reinterpret_cast<const fv*>(&part[0][i][lane * CV]);
+        ak += *reinterpret_cast<const fv*>(&part[1][i][lane * CV]);
+    }
+    const T* vp = static_cast<const T*>(p.v.p) + b * p.v.batch_stride + h * p.v.head_stride + col;
+    fv u;
+#pragma unroll
+    for (int j = 0; j < CV; ++j) u[j] = beta * (IO<T>::ld(vp + j) - rk * ak[j]);
+    if (rg == 0) {
+        T* yp = static_cast<T*>(p.y) + bh * p.dv + col;
+#pragma unroll
+        for (int j = 0; j < CV; ++j) IO<T>::st(yp + j, p.scale * (rq * aq[j] + qk * u[j]));
+    }
+    u *= rk;
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+        const int row = i * 8 + rg;
+        if (row < p.dk) __builtin_nontemporal_store(S[i] + u * sk[row], reinterpret_cast<fv*>(st + row * p.dv));
+    }
+}
+
+template <typename T, int DKP>
+hipError_t launch_gdr_d(const LaunchGdr& p) {
+    hipStream_t st = static_cast<hipStream_t>(p.stream);
+    const int64_t BH = p.B * p.H;
+    if (p.pass == LaunchGdr::kStep) {
+        constexpr int R = DKP / 8;
+        if (p.vec_state) hipLaunchKernelGGL((k_gdr_step<T, R, 4>), dim3((unsigned)(BH * ((p.dv + 127) / 128))), dim3(256), 0, st, p);
+        else hipLaunchKernelGGL((k_gdr_step<T, R, 1>), dim3((unsigned)(BH * ((p.dv + 31) / 32))), dim3(256), 0, st, p);
+        return hipGetLastError();
+    }
+    const unsigned chunks = (unsigned)(BH * p.nchunks);
+    const unsigned tiles = (unsigned)(BH * ((p.dv + 63) / 64));
+    if (p.pass == LaunchGdr::kFwd) {
+        hipLaunchKernelGGL((k_gdr_prep<T, DKP, false>), dim3(chunks), dim3(256), 0, st, p);
+        if (p.ckpt) hipLaunchKernelGGL((k_gdr_walk<T, DKP, 1, true>), dim3(tiles), dim3(256), 0, st, p);
+        else hipLaunchKernelGGL((k_gdr_walk<T, DKP, 1, false>), dim3(tiles), dim3(256), 0, st, p);
+    } else {
+        hipLaunchKernelGGL((k_gdr_prep<T, DKP, true>), dim3(chunks), dim3(256), 0, st, p);
+        hipLaunchKernelGGL((k_gdr_walk_back<T, DKP, 1>), dim3(tiles), dim3(256), 0, st, p);
+        hipLaunchKernelGGL((k_gdr_grads<T, DKP>), dim3(chunks), dim3(256), 0, st, p);
+        const int64_t rows = (p.B * p.L * p.Hk + 3) / 4;
+        hipLaunchKernelGGL((k_gdr_keys<T>), dim3((unsigned)(rows < 1 << 20 ? rows : 1 << 20), 2), dim3(256), 0, st, p);
+    }
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t launch_gdr_t(const LaunchGdr& p) {
+    if (p.dk <= 64) return launch_gdr_d<T, 64>(p);
+    if (p.dk <= 128) return launch_gdr_d<T, 128>(p);
+    return launch_gdr_d<T, 256>(p);
+}
+
+}  // namespace selscan

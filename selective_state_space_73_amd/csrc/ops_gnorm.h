@@ -1,0 +1,442 @@
+// Device code of the norms around a layer (ss_gnorm_fwd, ss_gnorm_bwd).
+//
+//   p = y / sqrt(mean_group y^2 + eps) w,  h = p silu(gate),  s = residual + scale h,
+//   n = s / sqrt(mean_row s^2 + eps) w_next
+//
+// Bound by memory: every value is read once and kept in registers through the sums it takes part in.
+// The backward makes everything again from the inputs: it reads y, gate, residual, ds and dn and writes
+// three gradients, no more bytes than with anything kept. Sums over rows (of w, scale, w_next) stay in
+// the registers of a workgroup that goes through many rows, and meet in a second kernel in a fixed order.
+#pragma once
+#include "ops_layer_internal.h"
+#include "ops_rows.h"
+
+namespace selscan {
+
+struct GnormShape { int lanes, nv, threads, rows; };     // lanes of a row, eights a lane, of a workgroup: threads, rows
+
+// A lane has eight columns: a row of up to 128 columns is 16 lanes, of up to 512 one wave, and above that as
+// many waves as it needs, with two eights a lane from 8192 on. `whole`: a row is a workgroup, whatever its length.
+inline GnormShape gnorm_shape(int64_t K, bool whole) {
+    if (!whole && K <= 128) return {16, 1, 256, 16};
+    if (!whole && K <= 512) return {64, 1, 256, 4};
+    const int nv = K <= 8192 ? 1 : 2, t = (int)((K + 512 * nv - 1) / (512 * nv)) * 64;
+    return {t, nv, t, 1};
+}
+
+// Eight values of the first norm's weight, which repeats with the groups (VEC: a group is whole eights).
+template <bool VEC, bool GROUPED>
+__device__ __forceinline__ void gnorm_w8(const float* w, int c, int K, int group, float* v) {
+    if constexpr (!GROUPED) {
+        ld8<float, VEC>(w, c, K, v);
+        ends8<VEC>(c, K, v);
+    } else if constexpr (VEC) {
+        ld8<float, true>(w, c < K ? c % group : 0, group, v);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = c + j < K ? w[(c + j) % group] : 0.0f;
+    }
+}
+
+// Sums over a row's lanes of N values at once. LANES 16 or 64: within a wave; 0: over the workgroup, `lds` of
+// 2 N floats a wave, of which calls use the halves in turn.
+template <int N, int LANES>
+__device__ __forceinline__ void gnorm_sum(float* v, float* lds) {
+#pragma unroll
+    for (int o = 1; o < (LANES ? LANES : 64); o <<= 1)
+#pragma unroll
+        for (int k = 0; k < N; ++k) v[k] += __shfl_xor(v[k], o, 64);
+    if constexpr (LANES == 0) {
+        const int waves = blockDim.x >> 6;
+        if ((threadIdx.x & 63) == 0)
+#pragma unroll
+            for (int k = 0; k < N; ++k) lds[k * 16 + (threadIdx.x >> 6)] = v[k];
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            float s = 0.0f;
+            for (int i = 0; i < waves; ++i) s += lds[k * 16 + i];
+            v[k] = s;
+        }
+    }
+}
+
+// For each of a lane's values, the sum over its group: the eights' sums (VEC) or the values themselves meet in
+// LDS, eight lanes sum a group, and every lane reads its groups' sums. buf: K / 8 (VEC) or K floats,
+// tot: a float a group. One row a workgroup.
+template <bool VEC, int NV>
+__device__ __forceinline__ void gnorm_groups_sum(float (*v)[8], int K, int group, float* buf, float* tot) {
+    const int tid = threadIdx.x, nth = blockDim.x;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int c = (k * nth + tid) * 8;
+        if constexpr (VEC) {
+            float s = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s += v[k][j];
+            if (c < K) buf[c >> 3] = s;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (c + j < K) buf[c + j] = v[k][j];
+        }
+    }
+    __syncthreads();
+    const int per = VEC ? group >> 3 : group, groups = K / group;
+    for (int g0 = 0; g0 < groups; g0 += nth >> 3) {
+        const int gi = g0 + (tid >> 3);
+        float s = 0.0f;
+        if (gi < groups)
+            for (int i = tid & 7; i < per; i += 8) s += buf[gi * per + i];
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) s += __shfl_xor(s, o, 64);
+        if (gi < groups && (tid & 7) == 0) tot[gi] = s;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int c = (k * nth + tid) * 8;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[k][j] = c + j < K ? tot[VEC ? c / group : (c + j) / group] : 0.0f;
+    }
+    __syncthreads();
+}
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void gnorm_ld(const void* base, int64_t row, int c, int K, float* v) {
+    if (base) {
+        ld8<T, VEC>(static_cast<const T*>(base) + row * K, c, K, v);
+        ends8<VEC>(c, K, v);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+    }
+}
+
+// Weights of the columns; `none` where there are none.
+template <bool VEC>
+__device__ __forceinline__ void gnorm_ldp(const float* w, int c, int K, float none, float* v) {
+    if (w) {
+        ld8<float, VEC>(w, c, K, v);
+        ends8<VEC>(c, K, v);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = none;
+    }
+}
+
+__device__ __forceinline__ float gnorm_sigmoid(float z) { return 1.0f / (1.0f + expf(-z)); }
+
+struct GnormArgs {
+    const void *y, *gate, *residual, *ds, *dn;
+    const float *w, *scale, *w_next;
+    void *s, *n, *dy, *dgate, *dresidual;
+    float* part;
+    int64_t M;
+    int K, group;
+    int per;                      // the forward by groups: groups of a row, whose scales follow each other
+    float eps;
+};
+
+template <typename T, bool VEC, int LANES, int NV, bool GROUPED, int MAXT>
+__global__ void __launch_bounds__(MAXT)
+k_gnorm_fwd(const GnormArgs p) {
+    extern __shared__ float lds[];
+    const int nl = LANES ? LANES : blockDim.x, lane = threadIdx.x % nl, K = p.K;
+    const int64_t at = (int64_t)blockIdx.x * (LANES ? MAXT / LANES : 1) + threadIdx.x / nl;
+    const bool there = at < p.M;
+    const int64_t row = there ? at : p.M - 1;
+    const float* scale = p.scale ? p.scale + row % p.per * K : nullptr;
+    float y[NV][8], z[NV][8], s[NV][8], q[1] = {0.0f};
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        const int c = (v * nl + lane) * 8;
+        gnorm_ld<T, VEC>(p.y, row, c, K, y[v]);
+        gnorm_ld<T, VEC>(p.gate, row, c, K, z[v]);
+        gnorm_ld<T, VEC>(p.residual, row, c, K, s[v]);
+    }
+    if constexpr (!VEC) {
+        // a row's last lane reads columns that others may write in place: not before its values are here
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) asm volatile("" : : "v"(y[v][j]), "v"(z[v][j]), "v"(s[v][j]));
+    }
+    float ry[NV][8];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        const bool in = (v * nl + lane) * 8 < K;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            ry[v][j] = in ? y[v][j] * y[v][j] : 0.0f;
+            q[0] += ry[v][j];
+        }
+    }
+    if constexpr (GROUPED) {
+        gnorm_groups_sum<VEC, NV>(ry, K, p.group, lds + 64, lds + 64 + (VEC ? K / 8 : K));
+    } else {
+        gnorm_sum<1, LANES>(q, lds);
+    }
+    const float inv = 1.0f / (GROUPED ? p.group : K);
+    const float r1 = GROUPED ? 0.0f : 1.0f / sqrtf(q[0] * inv + p.eps);
+    q[0] = 0.0f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        const int c = (v * nl + lane) * 8;
+        float w[8], a[8];
+        gnorm_w8<VEC, GROUPED>(p.w, c, K, p.group, w);
+        gnorm_ldp<VEC>(scale, c, K, 1.0f, a);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            float h = y[v][j] * (GROUPED ? 1.0f / sqrtf(ry[v][j] * inv + p.eps) : r1) * w[j];
+            if (p.gate) h *= z[v][j] * gnorm_sigmoid(z[v][j]);
+            s[v][j] = __builtin_fmaf(a[j], h, s[v][j]);
+            if (c < K) q[0] = __builtin_fmaf(s[v][j], s[v][j], q[0]);
+        }
+        if (there) st8<T, VEC>(static_cast<T*>(p.s) + row * K, c, K, s[v]);
+    }
+    if (!p.w_next) return;
+    gnorm_sum<1, LANES>(q, lds + 32);
+    const float r2 = 1.0f / sqrtf(q[0] / K + p.eps);
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        const int c = (v * nl + lane) * 8;
+        float w[8];
+        gnorm_ldp<VEC>(p.w_next, c, K, 0.0f, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] *= s[v][j] * r2;
+        if (there) st8<T, VEC>(static_cast<T*>(p.n) + row * K, c, K, w);
+    }
+}
+
+template <typename T, bool VEC, int LANES, int NV, bool GROUPED, int MAXT>
+__global__ void __launch_bounds__(MAXT)
+k_gnorm_bwd(const GnormArgs p) {
+    extern __shared__ float lds[];
+    constexpr int R = LANES ? MAXT / LANES : 1;
+    const int nl = LANES ? LANES : blockDim.x, lane = threadIdx.x % nl, K = p.K, slot = threadIdx.x / nl;
+    const int64_t step = (int64_t)gridDim.x * R;
+    float sw[NV][8] = {}, sa[NV][8] = {}, sn[NV][8] = {};
+    const float inv = 1.0f / (GROUPED ? p.group : K), invk = 1.0f / K;
+    for (int64_t row = (int64_t)blockIdx.x * R + slot; row < p.M; row += step) {
+        float y[NV][8], z[NV][8], s[NV][8], ds[NV][8], dn[NV][8], ry[NV][8], q[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int c = (v * nl + lane) * 8;
+            gnorm_ld<T, VEC>(p.y, row, c, K, y[v]);
+            gnorm_ld<T, VEC>(p.gate, row, c, K, z[v]);
+            gnorm_ld<T, VEC>(p.residual, row, c, K, s[v]);
+            gnorm_ld<T, VEC>(p.ds, row, c, K, ds[v]);
+            gnorm_ld<T, VEC>(p.dn, row, c, K, dn[v]);
+        }
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const bool in = (v * nl + lane) * 8 < K;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                ry[v][j] = in ? y[v][j] * y[v][j] : 0.0f;
+                q[0] += ry[v][j];
+            }
+        }
+        if constexpr (GROUPED) {
+            gnorm_groups_sum<VEC, NV>(ry, K, p.group, lds + 96, lds + 96 + (VEC ? K / 8 : K));
+        } else {
+            gnorm_sum<1, LANES>(q, lds);
+        }
+        const float r1 = GROUPED ? 0.0f : 1.0f / sqrtf(q[0] * inv + p.eps);
+        q[0] = 0.0f;
+        float w[NV][8], a[NV][8], pp[NV][8];
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int c = (v * nl + lane) * 8;
+            float wn[8];
+            gnorm_w8<VEC, GROUPED>(p.w, c, K, p.group, w[v]);
+            gnorm_ldp<VEC>(p.scale, c, K, 1.0f, a[v]);
+            gnorm_ldp<VEC>(p.w_next, c, K, 0.0f, wn);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                ry[v][j] = GROUPED ? 1.0f / sqrtf(ry[v][j] * inv + p.eps) : r1;
+                y[v][j] *= ry[v][j];                                               // y normed
+                pp[v][j] = y[v][j] * w[v][j];
+                float h = pp[v][j];
+                if (p.gate) h *= z[v][j] * gnorm_sigmoid(z[v][j]);
+                s[v][j] = __builtin_fmaf(a[v][j], h, s[v][j]);
+                if (c < K) {
+                    q[0] = __builtin_fmaf(s[v][j], s[v][j], q[0]);
+                    q[1] = __builtin_fmaf(s[v][j], dn[v][j] * wn[j], q[1]);
+                }
+            }
+        }
+        if (p.w_next) {
+            gnorm_sum<2, LANES>(q, lds + 32);
+            const float r2 = 1.0f / sqrtf(q[0] * invk + p.eps), m = q[1] * invk * r2 * r2;
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                const int c = (v * nl + lane) * 8;
+                float wn[8];
+                gnorm_ldp<VEC>(p.w_next, c, K, 0.0f, wn);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    sn[v][j] = __builtin_fmaf(dn[v][j], s[v][j] * r2, sn[v][j]);
+                    ds[v][j] = __builtin_fmaf(r2, dn[v][j] * wn[j] - s[v][j] * m, ds[v][j]);
+                }
+            }
+        }
+        q[0] = 0.0f;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int c = (v * nl + lane) * 8;
+            if (p.dresidual) st8<T, VEC>(static_cast<T*>(p.dresidual) + row * K, c, K, ds[v]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float dh = ds[v][j] * a[v][j];
+                float dp = dh, h = pp[v][j];
+                if (p.gate) {
+                    const float sig = gnorm_sigmoid(z[v][j]), act = z[v][j] * sig;
+                    dp = dh * act;
+                    h *= act;
+                    z[v][j] = dh * pp[v][j] * (sig + act * (1.0f - sig));          // gradient of the gate
+                }
+                sa[v][j] = __builtin_fmaf(ds[v][j], h, sa[v][j]);
+                sw[v][j] = __builtin_fmaf(dp, y[v][j], sw[v][j]);
+                s[v][j] = dp * w[v][j];
+                dn[v][j] = c < K ? s[v][j] * y[v][j] : 0.0f;
+                q[0] += dn[v][j];
+            }
+            if (p.dgate) st8<T, VEC>(static_cast<T*>(p.dgate) + row * K, c, K, z[v]);
+        }
+        if constexpr (GROUPED) {
+            gnorm_groups_sum<VEC, NV>(dn, K, p.group, lds + 96, lds + 96 + (VEC ? K / 8 : K));
+        } else {
+            gnorm_sum<1, LANES>(q, lds + 64);
+        }
+        const float m1 = q[0] * inv;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int c = (v * nl + lane) * 8;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s[v][j] = ry[v][j] * (s[v][j] - y[v][j] * (GROUPED ? dn[v][j] * inv : m1));
+            st8<T, VEC>(static_cast<T*>(p.dy) + row * K, c, K, s[v]);
+        }
+        if constexpr (LANES == 0) __syncthreads();        // the next row's sums go where this one's are still read
+    }
+    // the workgroup's sums of columns: its rows' slots one after the other
+    float* out = p.part + (int64_t)blockIdx.x * 3 * K;
+    for (int turn = 0; turn < R; ++turn) {
+        if (slot == turn) {
+#pragma unroll
+            for (int v = 0; v < NV; ++v)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int c = (v * nl + lane) * 8 + j;
+                    if (R == 1) {
+                        if (c < K) { out[c] = sw[v][j]; out[K + c] = sa[v][j]; out[2 * K + c] = sn[v][j]; }
+                    } else if (c < K) {
+                        float* l = lds + 96;
+                        l[c] = turn ? l[c] + sw[v][j] : sw[v][j];
+                        l[K + c] = turn ? l[K + c] + sa[v][j] : sa[v][j];
+                        l[2 * K + c] = turn ? l[2 * K + c] + sn[v][j] : sn[v][j];
+                    }
+                }
+        }
+        if (R > 1) __syncthreads();
+    }
+    if (R > 1)
+        for (int c = threadIdx.x; c < 3 * K; c += blockDim.x) out[c] = lds[96 + c];
+}
+
+// The sums of columns over the workgroups (and w's over the groups of a row), in a fixed order: 32 columns
+// by eight slices of the terms a workgroup.
+__global__ void __launch_bounds__(256)
+k_gnorm_sum(const float* part, int64_t n, int K, int group, float* dw, float* dscale, float* dw_next) {
+    __shared__ double lds[8][33];
+    const int cols = blockIdx.y ? K : group;
+    float* out = blockIdx.y == 0 ? dw : blockIdx.y == 1 ? dscale : dw_next;
+    const int c = blockIdx.x * 32 + (threadIdx.x & 31), slice = threadIdx.x >> 5;
+    if (!out || (int)blockIdx.x * 32 >= cols) return;
+    const int64_t per = blockIdx.y ? 1 : K / group, terms = n * per, a = terms * slice / 8, b = terms * (slice + 1) / 8;
+    double s = 0.0;                                     // thousands of terms, one after the other
+    if (c < cols)
+        for (int64_t i = a; i < b; ++i) s += part[i / per * 3 * K + (int64_t)blockIdx.y * K + i % per * group + c];
+    lds[slice][threadIdx.x & 31] = s;
+    __syncthreads();
+    if (slice == 0 && c < cols) {
+#pragma unroll
+        for (int k = 1; k < 8; ++k) s += lds[k][threadIdx.x & 31];
+        out[c] = (float)s;
+    }
+}
+
+// Dynamic LDS above 64 KiB is asked for (rows of thousands of columns in groups that are not whole eights).
+template <typename F>
+hipError_t gnorm_lds(F kernel, size_t bytes) {
+    if (bytes <= 65536) return hipSuccess;
+    return hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
+template <typename T, bool VEC>
+hipError_t launch_gnorm_t(const LaunchGnorm& p) {
+    GnormArgs a{p.y, p.gate, p.residual, p.ds, p.dn, p.w, p.scale, p.w_next, p.s, p.n, p.dy, p.dgate, p.dresidual, p.part,
+                p.M, (int)p.K, (int)p.group, 1, p.eps};
+    hipStream_t st = static_cast<hipStream_t>(p.stream);
+    bool grouped = p.group < p.K;
+    if (grouped && !p.back && !p.w_next) {
+        // no sum over the row: its groups are rows of their own
+        a.per = (int)(p.K / p.group);
+        a.M = p.M * a.per;
+        a.K = (int)p.group;
+        grouped = false;
+    }
+    const GnormShape sh = gnorm_shape(a.K, grouped);
+    const size_t sums = grouped ? (size_t)((VEC ? a.K / 8 : a.K) + a.K / a.group) * 4 : 0;
+    if (p.back) {
+        const size_t shm = 96 * 4 + (grouped ? sums : sh.rows > 1 ? (size_t)3 * a.K * 4 : 0);
+        const int64_t n = gnorm_groups(p.M, p.K);
+        hipError_t e = hipSuccess;
+        auto go = [&](auto kernel) {
+            if ((e = gnorm_lds(kernel, shm)) == hipSuccess) hipLaunchKernelGGL(kernel, dim3((unsigned)n), dim3(sh.threads), shm, st, a);
+        };
+        if (grouped) {
+            if (sh.nv == 2) go(k_gnorm_bwd<T, VEC, 0, 2, true, 1024>);
+            else if (sh.threads > 512) go(k_gnorm_bwd<T, VEC, 0, 1, true, 1024>);
+            else go(k_gnorm_bwd<T, VEC, 0, 1, true, 512>);
+        } else if (sh.lanes == 16) go(k_gnorm_bwd<T, VEC, 16, 1, false, 256>);
+        else if (sh.rows == 4) go(k_gnorm_bwd<T, VEC, 64, 1, false, 256>);
+        else if (sh.nv == 2) go(k_gnorm_bwd<T, VEC, 0, 2, false, 1024>);
+        else if (sh.threads > 512) go(k_gnorm_bwd<T, VEC, 0, 1, false, 1024>);
+        else go(k_gnorm_bwd<T, VEC, 0, 1, false, 512>);
+        if (e != hipSuccess) return e;
+        hipLaunchKernelGGL(k_gnorm_sum, dim3((unsigned)((p.K + 31) / 32), 3), dim3(256), 0, st, p.part, n, (int)p.K, (int)p.group, p.dw,
+                           p.dscale, p.dw_next);
+        return hipGetLastError();
+    }
+    const size_t shm = 64 * 4 + sums;
+    const int64_t n = (a.M + sh.rows - 1) / sh.rows;
+    if (n >= (int64_t(1) << 32) / 1024) {
+        // more rows than one launch holds lanes for: in pieces
+        LaunchGnorm q = p;
+        const int64_t half = p.M / 2, bytes = half * p.K * (int64_t)sizeof(T);
+        auto on = [&](const void* v) { return v ? static_cast<const char*>(v) + bytes : nullptr; };
+        q.M = half;
+        const hipError_t e = launch_gnorm_t<T, VEC>(q);
+        if (e != hipSuccess) return e;
+        q.M = p.M - half;
+        q.y = on(p.y); q.gate = on(p.gate); q.residual = on(p.residual);
+        q.s = const_cast<char*>(on(p.s)); q.n = const_cast<char*>(on(p.n));
+        return launch_gnorm_t<T, VEC>(q);
+    }
+    hipError_t e = hipSuccess;
+    auto go = [&](auto kernel) {
+        if ((e = gnorm_lds(kernel, shm)) == hipSuccess) hipLaunchKernelGGL(kernel, dim3((unsigned)n), dim3(sh.threads), shm, st, a);
+    };
+    if (grouped) {
+        if (sh.nv == 2) go(k_gnorm_fwd<T, VEC, 0, 2, true, 1024>);
+        else go(k_gnorm_fwd<T, VEC, 0, 1, true, 1024>);
+    } else if (sh.lanes == 16) go(k_gnorm_fwd<T, VEC, 16, 1, false, 256>);
+    else if (sh.rows == 4) go(k_gnorm_fwd<T, VEC, 64, 1, false, 256>);
+    else if (sh.nv == 2) go(k_gnorm_fwd<T, VEC, 0, 2, false, 1024>);
+    else go(k_gnorm_fwd<T, VEC, 0, 1, false, 1024>);
+    return e != hipSuccess ? e : hipGetLastError();
+}
+
+}  // namespace selscan

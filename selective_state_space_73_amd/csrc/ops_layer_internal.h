@@ -1,0 +1,55 @@
+// Internal interface between the C-ABI layer of the delta-rule layer's operators (the gated delta rule,
+// the norms around a layer; include/selscan_ops.h) and their HIP kernels.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "selscan_ops.h"
+
+namespace selscan {
+
+// One launch of the gated delta rule, already validated by the C-ABI layer.
+struct LaunchGdr {
+    enum Pass { kFwd, kBwd, kStep } pass;
+    bool bf16;
+    bool vec;                    // rows of q and k start on 16 bytes and hold whole accesses of 16 bytes
+    bool vec_state;              // the step: dv a multiple of 4, the state on 16 bytes
+    int64_t B, L, nchunks;
+    int H, Hk, dk, dv;
+    float scale, eps;
+    ss_head_view q, k, v;
+    const float* g; const float* beta; const uint8_t* reset; void* y; float* state;
+    float* ckpt;                 // [B, H, chunks, dk, dv] states in front of the chunks
+    float* ckptX;                // [B, L, H, dv] solutions x_t
+    ss_gdr_grads gr;
+    // workspace
+    float *co, *wT, *wP;         // [B, H, chunks]: factors of tokens, inverse and P in the order of operands
+    float* raw;                  // the backward: [B, H, chunks, 3, 10, 256] pairs of tokens, the triangle's ten tiles of 16 x 16
+    float *wS, *wV;              // the backward: [B, H, chunks, dk, dv] adjoints behind the chunks, [B, L, H, dv] gradients of v
+    float *part_q, *part_k;      // the backward: [B, L, H, dk] each head's share
+    void* stream;
+};
+hipError_t launch_gdr_bf16(const LaunchGdr& p);
+hipError_t launch_gdr_f32(const LaunchGdr& p);
+inline hipError_t launch_gdr(const LaunchGdr& p) { return p.bf16 ? launch_gdr_bf16(p) : launch_gdr_f32(p); }
+
+// The norms around a layer (forward or backward).
+struct LaunchGnorm {
+    bool bf16, vec, back;
+    int64_t M, K, group;
+    float eps;
+    const void *y, *gate, *residual;
+    const float *w, *scale, *w_next;
+    void *s, *n;
+    const void *ds, *dn;
+    void *dy, *dgate, *dresidual;
+    float *dw, *dscale, *dw_next;
+    float* part;                 // workspace of the backward: [gnorm_groups, 3, K] sums of columns
+    void* stream;
+};
+hipError_t launch_gnorm(const LaunchGnorm& p);
+// workgroups of the backward, each with its rows' sums of columns
+int64_t gnorm_groups(int64_t M, int64_t K);
+constexpr int64_t kGnormMaxCols = 16384;
+
+}  // namespace selscan

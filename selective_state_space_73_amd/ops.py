@@ -20,6 +20,7 @@ from . import (SS_BF16, SS_EULER, SS_F32, SS_ZOH, SelscanError, block_dims, lib,
                ss_block_weights)
 
 GLR_CKPT = 64    # SS_GLR_CKPT
+GDR_CHUNK = 64   # SS_GDR_CHUNK
 Q8_BLOCK = 128   # columns that share a scale
 
 _vp = ctypes.c_void_p
@@ -66,6 +67,35 @@ class ss_block_q8_weights(ctypes.Structure):
     _fields_ = [("w", ss_block_weights), ("S_in", _vp), ("S_out", _vp)]
 
 
+class ss_gdr_dims(ctypes.Structure):
+    _fields_ = [("batch", _i64), ("seqlen", _i64)] + [(n, ctypes.c_int32) for n in ("k_heads", "heads", "dk", "dv", "io_dtype")] + \
+               [("scale", ctypes.c_float), ("eps", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class ss_head_view(ctypes.Structure):
+    _fields_ = [("p", _vp), ("batch_stride", _i64), ("token_stride", _i64), ("head_stride", _i64)]
+
+
+class ss_gdr_args(ctypes.Structure):
+    _fields_ = [(n, ss_head_view) for n in ("q", "k", "v")] + [(n, _vp) for n in ("g", "beta", "reset", "y", "state", "ckpt")]
+
+
+class ss_gdr_grads(ctypes.Structure):
+    _fields_ = [(n, _vp) for n in ("dy", "dstate_final", "dq", "dk", "dv", "dg", "dbeta", "dstate_init")]
+
+
+class ss_gnorm_dims(ctypes.Structure):
+    _fields_ = [("rows", _i64), ("cols", _i64), ("group", _i64), ("io_dtype", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class ss_gnorm_args(ctypes.Structure):
+    _fields_ = [(n, _vp) for n in ("y", "w", "gate", "residual", "scale", "w_next", "s", "n")]
+
+
+class ss_gnorm_grads(ctypes.Structure):
+    _fields_ = [(n, _vp) for n in ("ds", "dn", "dy", "dgate", "dresidual", "dw", "dscale", "dw_next")]
+
+
 def _declare():
     P = ctypes.POINTER
     lib.ss_glr_workspace_bytes.argtypes = [P(ss_glr_dims), ctypes.c_int]
@@ -80,8 +110,18 @@ def _declare():
     lib.ss_block_q8_workspace_bytes.restype = ctypes.c_size_t
     block = [P(ss_block_dims), P(ss_block_q8_weights), _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]
     lib.ss_block_q8_fwd.argtypes = lib.ss_block_q8_step.argtypes = block
+    lib.ss_gdr_ckpt_floats.argtypes = [P(ss_gdr_dims)]
+    lib.ss_gdr_workspace_bytes.argtypes = [P(ss_gdr_dims), ctypes.c_int]
+    lib.ss_gdr_fwd.argtypes = [P(ss_gdr_dims), P(ss_gdr_args), _vp, ctypes.c_size_t, _vp]
+    lib.ss_gdr_step.argtypes = [P(ss_gdr_dims), P(ss_gdr_args), _vp]
+    lib.ss_gdr_bwd.argtypes = [P(ss_gdr_dims), P(ss_gdr_args), P(ss_gdr_grads), _vp, ctypes.c_size_t, _vp]
+    lib.ss_gnorm_workspace_bytes.argtypes = [P(ss_gnorm_dims)]
+    lib.ss_gnorm_fwd.argtypes = [P(ss_gnorm_dims), P(ss_gnorm_args), _vp]
+    lib.ss_gnorm_bwd.argtypes = [P(ss_gnorm_dims), P(ss_gnorm_args), P(ss_gnorm_grads), _vp, ctypes.c_size_t, _vp]
+    for name in ("ss_gdr_ckpt_floats", "ss_gdr_workspace_bytes", "ss_gnorm_workspace_bytes"):
+        getattr(lib, name).restype = ctypes.c_size_t
     for name in ("ss_glr_fwd", "ss_glr_step", "ss_glr_bwd", "ss_quant_q8", "ss_norm_q8", "ss_gemm_q8", "ss_block_q8_fwd",
-                 "ss_block_q8_step"):
+                 "ss_block_q8_step", "ss_gdr_fwd", "ss_gdr_step", "ss_gdr_bwd", "ss_gnorm_fwd", "ss_gnorm_bwd"):
         getattr(lib, name).restype = ctypes.c_int
 
 
@@ -93,7 +133,8 @@ def _check(status: int):
         raise SelscanError(status, lib.ss_last_error().decode())
 
 
-_EXTENSION = ("glr_fwd", "glr_step", "glr_bwd", "quant", "norm", "gemm")
+_EXTENSION = ("glr_fwd", "glr_step", "glr_bwd", "quant", "norm", "gemm", "gdr_fwd", "gdr_step", "gdr_bwd", "gnorm_fwd",
+              "gnorm_bwd")
 
 
 def _of_extension(name: str):
@@ -111,7 +152,8 @@ def _of_extension(name: str):
     return first
 
 
-_glr_fwd, _glr_step, _glr_bwd, _quant, _norm, _gemm = map(_of_extension, _EXTENSION)
+(_glr_fwd, _glr_step, _glr_bwd, _quant, _norm, _gemm, _gdr_fwd, _gdr_step, _gdr_bwd, _gnorm_fwd,
+ _gnorm_bwd) = map(_of_extension, _EXTENSION)
 
 
 def _done(result):
@@ -358,7 +400,119 @@ def ss_block_q8_step(x: torch.Tensor, W: dict, dt_rank: int, ssm_state: torch.Te
     return _block_q8(True, x, W, dt_rank, ssm_state, conv_state, out, workspace, norm_eps, zoh, stream)
 
 
+# ---------------------------------------------------------------------------
+# gated delta rule
+
+def _gdr_dims(batch, seqlen, heads, dk, dv):
+    return ss_gdr_dims(batch, seqlen, 1, heads, dk, dv, SS_F32, 1.0, 0.0, 0)
+
+
+def gdr_ckpt_shape(batch: int, seqlen: int, heads: int, dk: int, dv: int) -> tuple:
+    """Shape of the delta rule's checkpoints (float32): the states before every 64th token and what
+    each token writes, one behind the other."""
+    n = int(lib.ss_gdr_ckpt_floats(ctypes.byref(_gdr_dims(batch, seqlen, heads, dk, dv))))
+    if not n and seqlen:
+        raise ValueError(f"no such delta rule: {lib.ss_last_error().decode()}")
+    return (n,)
+
+
+def ss_gdr_workspace_bytes(dims: ss_gdr_dims, backward: bool = False) -> int:
+    return int(lib.ss_gdr_workspace_bytes(ctypes.byref(dims), int(bool(backward))))
+
+
+def ss_gdr_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor, *,
+               scale: Optional[float] = None, eps: Optional[float] = 1e-6, state: Optional[torch.Tensor] = None,
+               reset: Optional[torch.Tensor] = None, ckpt: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+               workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Gated delta rule over whole sequences, with a state S [dk, dv] per head:
+
+        S' = exp(g_t) S_{t-1}, u = beta_t (v_t - S'^T k_t), S_t = S' + k_t u^T, y_t = scale S_t^T q_t
+
+    q, k: [B,L,k_heads,dk], v [B,L,H,dv] (float32 or bfloat16, one dtype; the last dimension
+    contiguous, any strides otherwise; H a multiple of k_heads, whose keys and queries H / k_heads
+    neighbouring heads of v share; dk up to 256, dv up to 512); g (the logarithm of the decay) and
+    beta [B,L,H] float32. q and k are divided by their lengths, sqrt(sum x^2 + eps), unless eps is
+    None. scale: 1 / sqrt(dk) by default. state [B,H,dk,dv] float32, updated in place when given
+    (zero initial state otherwise); reset [B,L] uint8 or bool: the state in front of its nonzero
+    tokens counts as zero; ckpt: float32 tensor of gdr_ckpt_shape that receives what
+    ss_gdr_bwd needs. Returns y [B,L,H,dv] in the I/O dtype. Asynchronous."""
+    if stream is not None:
+        with _placed(_gpu(q, "q"), stream):
+            return ss_gdr_fwd(q, k, v, g, beta, scale=scale, eps=eps, state=state, reset=reset, ckpt=ckpt, y=y, workspace=workspace)
+    return _done(_gdr_fwd(q, k, v, g, beta, scale, eps, state, reset, ckpt, y, workspace))
+
+
+def ss_gdr_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
+                state: torch.Tensor, *, scale: Optional[float] = None, eps: Optional[float] = 1e-6,
+                reset: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """One token of each stream: q, k [S,k_heads,dk], v [S,H,dv] (any strides but the last), g, beta
+    [S,H]; state [S,H,dk,dv] float32, updated in place; reset [S]. Returns y [S,H,dv]."""
+    if stream is not None:
+        with _placed(_gpu(q, "q"), stream):
+            return ss_gdr_step(q, k, v, g, beta, state, scale=scale, eps=eps, reset=reset, y=y)
+    return _done(_gdr_step(q, k, v, g, beta, scale, eps, state, reset, y))
+
+
+def ss_gdr_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor, ckpt: torch.Tensor,
+               dy: torch.Tensor, *, scale: Optional[float] = None, eps: Optional[float] = 1e-6,
+               reset: Optional[torch.Tensor] = None, dstate_final: Optional[torch.Tensor] = None,
+               workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """Gradients of ss_gdr_fwd for the same inputs; ckpt as that call wrote it. dy [B,L,H,dv] in the I/O
+    dtype, dstate_final [B,H,dk,dv] float32 the gradient of the returned state. Returns a dict of new
+    tensors: dq, dk (summed over the heads that share them), dv (I/O dtype), dg, dbeta [B,L,H] and
+    dstate_init [B,H,dk,dv] (float32). Asynchronous."""
+    if stream is not None:
+        with _placed(_gpu(q, "q"), stream):
+            return ss_gdr_bwd(q, k, v, g, beta, ckpt, dy, scale=scale, eps=eps, reset=reset, dstate_final=dstate_final,
+                              workspace=workspace)
+    return dict(zip(("dq", "dk", "dv", "dg", "dbeta", "dstate_init"),
+                    _done(_gdr_bwd(q, k, v, g, beta, scale, eps, ckpt, dy, reset, dstate_final, workspace))))
+
+
+# ---------------------------------------------------------------------------
+# the norms around a layer
+
+def ss_gnorm_workspace_bytes(dims: ss_gnorm_dims) -> int:
+    return int(lib.ss_gnorm_workspace_bytes(ctypes.byref(dims)))
+
+
+def ss_gnorm_fwd(y: torch.Tensor, w: torch.Tensor, *, gate: Optional[torch.Tensor] = None,
+                 residual: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None,
+                 w_next: Optional[torch.Tensor] = None, eps: float = 1e-5, s: Optional[torch.Tensor] = None,
+                 n: Optional[torch.Tensor] = None, stream=None) -> tuple:
+    """The norms behind a layer and before the next, with its gate, its scale and the residual, in one pass:
+
+        p = y / rms(y) w,  h = p silu(gate),  s = residual + scale h,  n = s / rms(s) w_next
+
+    y, gate, residual [..., K] (float32 or bfloat16, contiguous, K up to 16384); w [group] float32, group a
+    divisor of K: y is normed in groups of so many columns (heads), each with the same weights; scale, w_next
+    [K] float32. Without a gate h = p, without scale 1, without residual 0, without w_next n is not made.
+    Returns (s, n) in y's dtype (n None without w_next); s may be y, gate or residual itself. Asynchronous."""
+    if stream is not None:
+        with _placed(_gpu(y, "y"), stream):
+            return ss_gnorm_fwd(y, w, gate=gate, residual=residual, scale=scale, w_next=w_next, eps=eps, s=s, n=n)
+    return _done(_gnorm_fwd(y, w, gate, residual, scale, w_next, eps, s, n))
+
+
+def ss_gnorm_bwd(y: torch.Tensor, w: torch.Tensor, ds: Optional[torch.Tensor], *, dn: Optional[torch.Tensor] = None,
+                 gate: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
+                 scale: Optional[torch.Tensor] = None, w_next: Optional[torch.Tensor] = None, eps: float = 1e-5,
+                 workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """Gradients of ss_gnorm_fwd for the same inputs (as they were: not where s was written over one of them);
+    ds and dn are those of s and n (None: zero; one is required). Returns a dict of new tensors: dy, dgate,
+    dresidual (y's dtype), dw [group], dscale, dw_next [K] (float32); None for what was not given. Asynchronous."""
+    if stream is not None:
+        with _placed(_gpu(y, "y"), stream):
+            return ss_gnorm_bwd(y, w, ds, dn=dn, gate=gate, residual=residual, scale=scale, w_next=w_next, eps=eps,
+                                workspace=workspace)
+    return dict(zip(("dy", "dw", "dgate", "dresidual", "dscale", "dw_next"),
+                    _done(_gnorm_bwd(y, w, gate, residual, scale, w_next, eps, ds, dn, workspace))))
+
+
 __all__ = ["GLR_CKPT", "ss_glr_dims", "ss_view", "ss_glr_args", "ss_glr_grads", "glr_ckpt_shape",
            "ss_glr_workspace_bytes", "ss_glr_fwd", "ss_glr_step", "ss_glr_bwd", "Q8_BLOCK", "ss_q8_dims",
            "ss_norm_q8_args", "ss_gemm_q8_dims", "ss_gemm_q8_args", "ss_quant_q8", "ss_norm_q8", "ss_gemm_q8",
-           "ss_block_q8_weights", "block_q8_weights", "ss_block_q8_workspace_bytes", "ss_block_q8_fwd", "ss_block_q8_step"]
+           "ss_block_q8_weights", "block_q8_weights", "ss_block_q8_workspace_bytes", "ss_block_q8_fwd", "ss_block_q8_step",
+           "GDR_CHUNK", "ss_gdr_dims", "ss_head_view", "ss_gdr_args", "ss_gdr_grads", "gdr_ckpt_shape", "ss_gdr_workspace_bytes",
+           "ss_gdr_fwd", "ss_gdr_step", "ss_gdr_bwd", "ss_gnorm_dims", "ss_gnorm_args", "ss_gnorm_grads",
+           "ss_gnorm_workspace_bytes", "ss_gnorm_fwd", "ss_gnorm_bwd"]
