@@ -59,6 +59,14 @@ template <> struct Mx<uint16_t> {
     static __device__ __forceinline__ gf4 mm(const gb8& a, const gb8& b, gf4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
     }
+    // the pairs of terms of a product of two sums, the smallest first
+    template <int N, typename Fn>
+    static __device__ __forceinline__ void each(Fn&& f) {
+        if constexpr (N == 3) { f(1, 1); f(2, 0); f(0, 2); }
+        f(1, 0);
+        f(0, 1);
+        f(0, 0);
+    }
     // an exact operand by a sum of terms
     template <int N>
     static __device__ __forceinline__ gf4 mul(const F& a, const S<N>& b, gf4 c) {
@@ -103,6 +111,8 @@ template <> struct Mx<float> {
     static constexpr int NT = 1, NP = 1;
     typedef gf8 F;
     template <int N> struct S { gf8 t[1]; };
+    template <int N, typename Fn>
+    static __device__ __forceinline__ void each(Fn&& f) { f(0, 0); }
     static __device__ __forceinline__ F ld(const float* p) { return *reinterpret_cast<const gf8*>(p); }
     template <int N>
     static __device__ __forceinline__ S<N> split(gf8 v) { return S<N>{{v}}; }
@@ -129,6 +139,9 @@ template <> struct Mx<float> {
 };
 
 __device__ __forceinline__ gf8 gdr_pair(gf4 a, gf4 b) { return gf8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}; }
+
+// This wave's number, known to be the same in all its lanes.
+__device__ __forceinline__ int gdr_wave() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
 
 // The blocks of a lower triangle of 64 x 64 that hold anything, 16 rows by 32 columns: (row tile, column
 // pair) 00 10 20 21 30 31; of an upper triangle 00 01 10 11 21 31.
@@ -344,176 +357,613 @@ k_gdr_prep(const LaunchGdr p) {
     }
 }
 
+__device__ __forceinline__ void gdr_tile(int tile, int& mt, int& nt) {
+    mt = tile < 1 ? 0 : tile < 3 ? 1 : tile < 6 ? 2 : 3;
+    nt = tile - mt * (mt + 1) / 2;
+}
+
 // ---------------------------------------------------------------------------
-// From chunk to chunk: a workgroup holds 64 CT columns of one head's state, a wave 16 CT of them.
-template <typename T, int DKP, int CT, bool CK>
-__global__ void __launch_bounds__(256)
-k_gdr_walk(const LaunchGdr p) {
-    using M = Mx<T>;
-    constexpr int KD = DKP / 32, ND = DKP / 16;
-    __shared__ alignas(16) T tk[64 * DKP], tq[64 * DKP];
-    __shared__ alignas(16) T tt[M::NT][6 * 512], tp[M::NP][6 * 512];
-    __shared__ alignas(16) float sco[kGdrCo][64];
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, g = lane >> 4, m = lane & 15;
-    const int64_t BH = p.B * p.H, bh = blockIdx.x % BH, b = bh / p.H, nc = p.nchunks;
-    const int h = (int)(bh % p.H), hk = h / (p.H / p.Hk);
-    const int col0 = ((int)(blockIdx.x / BH) * 4 + w) * (16 * CT) + m;
-    const T* vb = static_cast<const T*>(p.v.p) + b * p.v.batch_stride + h * p.v.head_stride;
-    T* yb = static_cast<T*>(p.y) + (b * p.L * p.H + h) * p.dv;
-    float* st = p.state ? p.state + bh * p.dk * p.dv : nullptr;
+// Operands in LDS: 64 rows of DKP columns as fragments (row tile i, columns 32 s to 32 s + 31): lane 16 g + m
+// reads row 16 i + m at columns 32 s + 8 g + j, 16 bytes (an fp32 fragment is two such units, j < 4 and the rest).
+// A unit goes from memory to LDS without registers, 16 bytes a lane at consecutive places: place
+// 4 m + (g ^ (m >> 1 & 3)), so that neither the lanes that read a fragment nor those that read across rows for the
+// transposed one meet in a bank. The state's tiles follow: row 4 g + r of tile 2 s + h is d = 32 s + 8 g + 4 h + r.
+__device__ __forceinline__ int gdr_place(int g, int m) { return 4 * m + (g ^ (m >> 1 & 3)); }
 
-    gf4 S[CT][ND];
+template <typename T>
+__device__ __forceinline__ typename Mx<T>::F gdr_rows_frag(const T* base, int unit, int place) {
+    if constexpr (sizeof(T) == 2) return *reinterpret_cast<const gb8*>(base + (unit * 64 + place) * 8);
+    else return gdr_pair(*reinterpret_cast<const gf4*>(base + (unit * 128 + place) * 4), *reinterpret_cast<const gf4*>(base + (unit * 128 + 64 + place) * 4));
+}
+// Operands that are made here lie by lane.
+template <typename T>
+__device__ __forceinline__ typename Mx<T>::F gdr_frag(const T* base, int unit, int lane) { return gdr_rows_frag<T>(base, unit, lane); }
+
+// The transposed operand: rows are the columns of the state's tile (sd, h), terms the tokens of the row
+// tiles 2 s and 2 s + 1.
+template <typename T, int KD>
+__device__ __forceinline__ typename Mx<T>::F gdr_frag_t(const T* base, int s, int sd, int h, int lane) {
+    const int g = lane >> 4, i = lane & 15;
+    if constexpr (sizeof(T) == 2) {
+        const int place = gdr_place(i & 3, 4 * g + (i >> 2));
+        gs4 a[2];
 #pragma unroll
-    for (int c = 0; c < CT; ++c)
+        for (int e = 0; e < 2; ++e) {
+            const T* q = base + (((2 * s + e) * KD + sd) * 64 + place) * 8 + 4 * h;
+            a[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((gs4 __attribute__((address_space(3)))*)q);
+        }
+        typedef short gs8 __attribute__((ext_vector_type(8)));
+        return __builtin_bit_cast(gb8, gs8{a[0][0], a[0][1], a[0][2], a[0][3], a[1][0], a[1][1], a[1][2], a[1][3]});
+    } else {
+        gf8 a;
 #pragma unroll
-        for (int d = 0; d < ND; ++d)
+        for (int j = 0; j < 8; ++j)
+            a[j] = base[((((2 * s + (j >> 2)) * KD + sd) * 2 + h) * 64 + gdr_place(i >> 2, 4 * g + (j & 3))) * 4 + (i & 3)];
+        return a;
+    }
+}
+// A term of an operand over tokens: block of the triangle's six (or any unit), as above.
+template <typename T, int N>
+__device__ __forceinline__ typename Mx<T>::template S<N> gdr_terms(const T* base, int plane, int unit, int lane) {
+    typename Mx<T>::template S<N> f;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = d * 16 + 4 * g + r, col = col0 + 16 * c;
-                S[c][d][r] = st && row < p.dk && col < p.dv ? st[row * p.dv + col] : 0.0f;
+    for (int k = 0; k < (sizeof(T) == 2 ? N : 1); ++k) f.t[k] = gdr_frag<T>(base + k * plane, unit, lane);
+    return f;
+}
+
+// Elements at a lane's offset and the wave's, in bytes, from a chunk's start: no 64-bit address per element.
+template <typename T>
+struct GdrBuf {
+    __amdgpu_buffer_rsrc_t r;
+    __device__ __forceinline__ explicit GdrBuf(const T* p) : r(__builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(p), 0, -1, kBufDword3)) {}
+    __device__ __forceinline__ T ld(unsigned lane, unsigned wave) const {
+        if constexpr (sizeof(T) == 2) return __builtin_amdgcn_raw_buffer_load_b16(r, lane, wave, 0);
+        else return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, lane, wave, 0));
+    }
+    __device__ __forceinline__ void st(float v, unsigned lane, unsigned wave) const {
+        if constexpr (sizeof(T) == 2) __builtin_amdgcn_raw_buffer_store_b16(IO<T>::bits(v), r, lane, wave, 0);
+        else __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), r, lane, wave, 0);
+    }
+    __device__ __forceinline__ void st4(gf4 v, unsigned lane, unsigned wave) const {
+        if constexpr (sizeof(T) == 2) {
+            typedef __bf16 gb4 __attribute__((ext_vector_type(4)));
+            typedef uint32_t gu2 __attribute__((ext_vector_type(2)));
+            __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(gu2, __builtin_convertvector(v, gb4)), r, lane, wave, 0);
+        } else {
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(gu4, v), r, lane, wave, 0);
+        }
+    }
+};
+
+// Where a head's keys or queries lie. AL: rows start on 16 bytes, hold whole accesses of 16 bytes, and 64 of them
+// lie within 32-bit offsets.
+template <typename T, int KD, bool AL>
+struct GdrRows {
+    const T* base;
+    int64_t stride;
+    int dk;
+    __device__ __forceinline__ GdrRows(const ss_head_view& v, int64_t b, int head, int dk_)
+        : base(static_cast<const T*>(v.p) + b * v.batch_stride + head * v.head_stride), stride(v.token_stride), dk(dk_) {}
+    // 64 rows from token t0 on into `tiles`, rows past the last token as copies of it (what they are multiplied by is
+    // 0). Columns past dk are left as they are. Complete once this wave's loads are.
+    __device__ __forceinline__ void load(T* tiles, int64_t t0, int64_t L) const {
+        const T* at = base + t0 * stride;
+        const int last = L - t0 < 64 ? (int)(L - t0) - 1 : 63;
+        if constexpr (AL) {
+            constexpr int H = sizeof(T) / 2, U = 4 * KD * H;          // units of 16 bytes a lane
+            const int lane = threadIdx.x & 63, w = gdr_wave(), m = lane >> 2, g = (lane & 3) ^ (m >> 1 & 3);
+            const auto rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(at), 0, -1, kBufDword3);
+            const unsigned row_bytes = (unsigned)stride * (unsigned)sizeof(T), lo = 8 * g * (unsigned)sizeof(T);
+#pragma unroll
+            for (int e = 0; e < U / 4; ++e) {
+                const int u = e * 4 + w, h = u % H, s = u / H % KD, row = 16 * (u / H / KD) + m;
+                const unsigned off = (row < last ? row : last) * row_bytes + lo;
+                if (32 * s + 8 * g < dk)
+                    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (gu4*)(tiles + u * (1024 / sizeof(T))), 16, off,
+                                                             (32 * s + 4 * h) * (unsigned)sizeof(T), 0, 0);
             }
-
-    for (int64_t n = 0; n < nc; ++n) {
-        const int64_t t0 = n * kGdrC, id = bh * nc + n;
-        __syncthreads();
-        gdr_stage<T, KD>(tk, p.k, b, t0, p.L, hk, p.dk, p.vec);
-        gdr_stage<T, KD>(tq, p.q, b, t0, p.L, hk, p.dk, p.vec);
-        for (int e = tid; e < 6 * 64; e += 256) {
-            const auto x = M::template split<M::NT>(*reinterpret_cast<const gf8*>(p.wT + id * 3072 + e * 8));
-            const auto y = M::template split<M::NP>(*reinterpret_cast<const gf8*>(p.wP + id * 3072 + e * 8));
-#pragma unroll
-            for (int k = 0; k < M::NT; ++k) *reinterpret_cast<typename M::F*>(&tt[k][e * 8]) = x.t[k];
-#pragma unroll
-            for (int k = 0; k < M::NP; ++k) *reinterpret_cast<typename M::F*>(&tp[k][e * 8]) = y.t[k];
-        }
-        for (int e = tid; e < kGdrCo * 64; e += 256) sco[e >> 6][e & 63] = p.co[id * (kGdrCo * 64) + e];
-        gf4 V[CT][4];
-#pragma unroll
-        for (int c = 0; c < CT; ++c)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int64_t t = t0 + 16 * i + 4 * g + r;
-                    V[c][i][r] = t < p.L && col0 + 16 * c < p.dv ? IO<T>::ld(vb + t * p.v.token_stride + col0 + 16 * c) : 0.0f;
+        } else {
+            for (int e = threadIdx.x; e < 64 * KD * 32; e += 256) {
+                const int j = e & 7, row = e >> 3 & 63, o = e >> 9, d = o * 8 + j, s = d >> 5, gg = d >> 3 & 3;
+                const T x = at[(row < last ? row : last) * stride + (d < dk ? d : dk - 1)];
+                const int i = row >> 4, ln = gdr_place(gg, row & 15);
+                if (d < dk) {
+                    if constexpr (sizeof(T) == 2) tiles[((i * KD + s) * 64 + ln) * 8 + j] = x;
+                    else tiles[(((i * KD + s) * 2 + (j >> 2)) * 64 + ln) * 4 + (j & 3)] = x;
                 }
-        __syncthreads();
-        if constexpr (CK) {
-            float* ck = p.ckpt + (bh * nc + n) * p.dk * p.dv;
-#pragma unroll
-            for (int c = 0; c < CT; ++c)
-#pragma unroll
-                for (int d = 0; d < ND; ++d)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int row = d * 16 + 4 * g + r, col = col0 + 16 * c;
-                        if (row < p.dk && col < p.dv) ck[(int64_t)row * p.dv + col] = S[c][d][r];
-                    }
+            }
         }
-        // K S0 and Q S0
-        gf4 ks[CT][4] = {}, qs[CT][4] = {};
+    }
+};
+
+// What k_gdr_solve leaves of a chunk's tokens: rows of 64 floats.
+//   a1 e^G / |k|, a2 e^G, a3 beta e^(G_last - G) / |k|, bk beta / |k|, misc { e^G_last, whether no factor is 0 },
+//   G itself, times log2 e, in 64 bits (two rows)
+enum GdrTok { tA1, tA2, tA3, tBk, tMisc, tG, kGdrTok = 7 };
+
+// Waits for this wave's transfers to LDS, then for the workgroup's.
+__device__ __forceinline__ void gdr_arrived() {
+    __builtin_amdgcn_s_waitcnt(0x0f70);               // vmcnt(0)
+    __syncthreads();
+}
+
+// ---------------------------------------------------------------------------
+// A chunk of one head: its factors and T = (1 + N)^-1, one wave each, so that nothing waits for a barrier.
+// Sums of g in 64 bits: a reset, or a decay of any size, is a term of -200 at least (e^-200 is 0 in
+// fp32), and the differences of what follows keep their digits. The inverse: blocks of 16 on the
+// diagonal row by row, below them block by block, T_ij = -T_ii sum_l N_il T_lj, in fp32 products
+// whose operands stay in registers.
+template <typename T, int DKP>
+__global__ void __launch_bounds__(256)
+k_gdr_solve(const LaunchGdr p) {
+    using M = Mx<T>;
+    constexpr int KD = DKP / 32, LD = 68;
+    __shared__ alignas(16) float mats[4][64 * LD];
+    __shared__ alignas(16) double sg[4][64];
+    __shared__ alignas(16) float sv[4][2][64];
+    const int lane = threadIdx.x & 63, w = gdr_wave(), g = lane >> 4, m = lane & 15;
+    const int64_t id = (int64_t)blockIdx.x * 4 + w, nc = p.nchunks;
+    if (id >= p.B * p.H * nc) return;                 // whole waves, and no barrier below
+    const int64_t n = id % nc, bh = id / nc, b = bh / p.H, t0 = n * kGdrC;
+    const int h = (int)(bh % p.H), hk = h / (p.H / p.Hk);
+    float* mat = mats[w];
+
+    double G = 0.0;
+    float beta = 0.0f;
+    bool cut = false;
+    if (t0 + lane < p.L) {
+        const int64_t at = (b * p.L + t0 + lane) * p.H + h;
+        G = (double)p.g[at];
+        beta = p.beta[at];
+        cut = p.reset && p.reset[b * p.L + t0 + lane];
+    }
+    // products of keys: the lower triangle's ten tiles
+    gf4 kk[10] = {};
+    {
+        const T* base = static_cast<const T*>(p.k.p) + b * p.k.batch_stride + hk * p.k.head_stride + t0 * p.k.token_stride;
+        const int last = p.L - t0 < 64 ? (int)(p.L - t0) - 1 : 63;
 #pragma unroll
         for (int s = 0; s < KD; ++s) {
-            typename M::template S<3> sb[CT];
-#pragma unroll
-            for (int c = 0; c < CT; ++c) sb[c] = M::template split<3>(gdr_pair(S[c][2 * s], S[c][2 * s + 1]));
+            typename M::F f[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const auto kf = M::ld(tk + ((i * KD + s) * 64 + lane) * 8), qf = M::ld(tq + ((i * KD + s) * 64 + lane) * 8);
+                const int row = 16 * i + m, d = 32 * s + 8 * g;
+                const T* at = base + (row < last ? row : last) * p.k.token_stride;
+                alignas(16) T x[8];
+                if (p.vec) {
+                    const T* from = at + (d < p.dk ? d : 0);
 #pragma unroll
-                for (int c = 0; c < CT; ++c) {
-                    ks[c][i] = M::template mul<3>(kf, sb[c], ks[c][i]);
-                    if constexpr (sizeof(T) == 2) qs[c][i] = M::mm(qf, sb[c].t[0], M::mm(qf, sb[c].t[1], qs[c][i]));
-                    else qs[c][i] = M::mm(qf, sb[c].t[0], qs[c][i]);
+                    for (int e = 0; e < (int)sizeof(T) / 2; ++e) reinterpret_cast<gu4*>(x)[e] = reinterpret_cast<const gu4*>(from)[e];
+                    if (d >= p.dk)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) x[j] = T(0);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const T v = at[d + j < p.dk ? d + j : p.dk - 1];
+                        x[j] = d + j < p.dk ? v : T(0);
+                    }
                 }
+                f[i] = __builtin_bit_cast(typename M::F, x);
             }
-        }
-        // X = T (V - e^G K S0); a factor of 0 leaves out what it multiplies
-        gf4 X[CT][4] = {};
-#pragma unroll
-        for (int c = 0; c < CT; ++c)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const gf4 a1 = *reinterpret_cast<const gf4*>(&sco[kA1][16 * i + 4 * g]), a2 = *reinterpret_cast<const gf4*>(&sco[kA2][16 * i + 4 * g]);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    V[c][i][r] -= a1[r] != 0.0f ? a1[r] * ks[c][i][r] : 0.0f;
-                    qs[c][i][r] = a2[r] != 0.0f ? a2[r] * qs[c][i][r] : 0.0f;
-                }
-            }
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            typename M::template S<M::NT> rb[CT];
-#pragma unroll
-            for (int c = 0; c < CT; ++c) rb[c] = M::template split<M::NT>(gdr_pair(V[c][2 * s], V[c][2 * s + 1]));
-#pragma unroll
-            for (int i = 2 * s; i < 4; ++i) {
-                typename M::template S<M::NT> tf;
-#pragma unroll
-                for (int k = 0; k < M::NT; ++k) tf.t[k] = M::ld(&tt[k][(gdr_low(i, s) * 64 + lane) * 8]);
-#pragma unroll
-                for (int c = 0; c < CT; ++c) X[c][i] = M::mul(tf, rb[c], X[c][i]);
-            }
-        }
-        // Y
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            typename M::template S<M::NP> xb[CT];
-#pragma unroll
-            for (int c = 0; c < CT; ++c) xb[c] = M::template split<M::NP>(gdr_pair(X[c][2 * s], X[c][2 * s + 1]));
-#pragma unroll
-            for (int i = 2 * s; i < 4; ++i) {
-                typename M::template S<M::NP> pf;
-#pragma unroll
-                for (int k = 0; k < M::NP; ++k) pf.t[k] = M::ld(&tp[k][(gdr_low(i, s) * 64 + lane) * 8]);
-#pragma unroll
-                for (int c = 0; c < CT; ++c) qs[c][i] = M::mul(pf, xb[c], qs[c][i]);
-            }
-        }
-#pragma unroll
-        for (int c = 0; c < CT; ++c)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int64_t t = t0 + 16 * i + 4 * g + r;
-                    const int col = col0 + 16 * c;
-                    if (t < p.L && col < p.dv) {
-                        IO<T>::st(yb + t * p.H * p.dv + col, qs[c][i][r]);
-                        if constexpr (CK) p.ckptX[((b * p.L + t) * p.H + h) * p.dv + col] = X[c][i][r];
-                    }
-                }
-        // the next state
-        const float end = sco[kEnd][0];
+                for (int j = 0; j <= i; ++j) kk[i * (i + 1) / 2 + j] = M::mm(f[i], f[j], kk[i * (i + 1) / 2 + j]);
+        }
+    }
+    G = (G < -200.0 || cut ? -200.0 : G) * 1.4426950408889634;
 #pragma unroll
-        for (int c = 0; c < CT; ++c)
+    for (int o = 1; o < 64; o <<= 1) {
+        const double u = __shfl_up(G, o, 64);
+        if (lane >= o) G += u;
+    }
+    const double Gl = __shfl(G, 63, 64);
+    sg[w][lane] = G;
+    // lengths of keys: the diagonal
 #pragma unroll
-            for (int d = 0; d < ND; ++d) S[c][d] = end != 0.0f ? S[c][d] * end : gf4{0, 0, 0, 0};
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            typename M::template S<3> xb[CT];
-            const gf4 a = *reinterpret_cast<const gf4*>(&sco[kA3][32 * s + 4 * g]), e = *reinterpret_cast<const gf4*>(&sco[kA3][32 * s + 16 + 4 * g]);
+        for (int r = 0; r < 4; ++r)
+            if (m == 4 * g + r) sv[w][0][16 * i + m] = p.eps > 0.0f ? 1.0f / sqrtf(kk[i * (i + 1) / 2 + i][r] + p.eps) : 1.0f;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    const float rk = sv[w][0][lane], bk = rk * beta;
+    sv[w][1][lane] = bk;
+    {
+        float* tok = p.co + id * (kGdrTok * 64) + lane;
+        const float e = __builtin_amdgcn_exp2f((float)G), a3 = __builtin_amdgcn_exp2f((float)(Gl - G)), a1 = e * rk;
+        tok[tA1 * 64] = a1;
+        tok[tA2 * 64] = e;
+        tok[tA3 * 64] = a3 * bk;
+        tok[tBk * 64] = bk;
+        const bool clean = __all(a1 != 0.0f && e != 0.0f);
+        tok[tMisc * 64] = lane == 0 ? __builtin_amdgcn_exp2f((float)Gl) : clean ? 1.0f : 0.0f;
+        *reinterpret_cast<double*>(p.co + id * (kGdrTok * 64) + tG * 64 + 2 * lane) = G;
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    // N, row by row
 #pragma unroll
-            for (int c = 0; c < CT; ++c) xb[c] = M::template split<3>(gdr_pair(X[c][2 * s] * a, X[c][2 * s + 1] * e));
+    for (int i = 0; i < 4; ++i) {
+        double gi[4];
+        const gf4 ri = *reinterpret_cast<const gf4*>(&sv[w][0][16 * i + 4 * g]);
 #pragma unroll
-            for (int d = 0; d < ND; ++d) {
-                const auto kf = M::template ldt<KD>(tk, s, d, lane);
+        for (int r = 0; r < 4; ++r) gi[r] = sg[w][16 * i + 4 * g + r];
 #pragma unroll
-                for (int c = 0; c < CT; ++c) S[c][d] = M::template mul<3>(kf, xb[c], S[c][d]);
+        for (int j = 0; j <= i; ++j) {
+            const double gj = sg[w][16 * j + m];
+            const float bj = sv[w][1][16 * j + m];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = 16 * i + 4 * g + r, col = 16 * j + m;
+                const float d = row > col ? __builtin_amdgcn_exp2f((float)(gi[r] - gj)) : 0.0f;
+                // a decay to nothing leaves out what it multiplies, whatever it is
+                mat[row * LD + col] = d != 0.0f ? kk[i * (i + 1) / 2 + j][r] * d * ri[r] * bj : 0.0f;
             }
         }
     }
-    if (st) {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    // operands of the blocks below the diagonal, then the diagonal's inverses: lanes of group g have block g
+    gf4 nb[6];
 #pragma unroll
-        for (int c = 0; c < CT; ++c)
+    for (int i = 1; i < 4; ++i)
 #pragma unroll
-            for (int d = 0; d < ND; ++d)
+        for (int j = 0; j < i; ++j) nb[i * (i - 1) / 2 + j] = *reinterpret_cast<const gf4*>(&mat[(16 * i + m) * LD + 16 * j + 4 * g]);
+    {
+        float x[16];
+        float* blk = mat + 16 * g * LD + 16 * g;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float s = i == m ? 1.0f : 0.0f;
+#pragma unroll
+            for (int l = 0; l < i; ++l) s = __builtin_fmaf(-blk[i * LD + l], x[l], s);
+            x[i] = s;
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+        for (int i = 0; i < 16; ++i) blk[i * LD + m] = x[i];
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    gf4 ti[4], tb[10];                                // -T_ii's rows; T's tiles as results lie
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        ti[i] = -*reinterpret_cast<const gf4*>(&mat[(16 * i + m) * LD + 16 * i + 4 * g]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) tb[i * (i + 1) / 2 + i][r] = mat[(16 * i + 4 * g + r) * LD + 16 * i + m];
+    }
+#pragma unroll
+    for (int lev = 1; lev < 4; ++lev)
+#pragma unroll
+        for (int j = 0; j + lev < 4; ++j) {
+            const int i = j + lev;
+            gf4 acc = {0, 0, 0, 0}, out = {0, 0, 0, 0};
+#pragma unroll
+            for (int l = j; l < i; ++l)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    acc = __builtin_amdgcn_mfma_f32_16x16x4f32(nb[i * (i - 1) / 2 + l][r], tb[l * (l + 1) / 2 + j][r], acc, 0, 0, 0);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) out = __builtin_amdgcn_mfma_f32_16x16x4f32(ti[i][r], acc[r], out, 0, 0, 0);
+            tb[i * (i + 1) / 2 + j] = out;
+        }
+    // to operands: through LDS, rows by lane
+#pragma unroll
+    for (int i = 1; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < i; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) mat[(16 * i + 4 * g + r) * LD + 16 * j + m] = tb[i * (i + 1) / 2 + j][r];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    T* out = reinterpret_cast<T*>(p.wT) + id * (M::NT * 3072);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int s = 0; s <= i >> 1; ++s) {
+            const gf4 a = *reinterpret_cast<const gf4*>(&mat[(16 * i + m) * LD + 32 * s + 4 * g]);
+            gf4 c = {0, 0, 0, 0};
+            if (2 * s + 1 <= i) c = *reinterpret_cast<const gf4*>(&mat[(16 * i + m) * LD + 32 * s + 16 + 4 * g]);
+            const int u = gdr_low(i, s);
+            if constexpr (sizeof(T) == 2) {
+                const auto sp = M::template split<M::NT>(gdr_pair(a, c));
+#pragma unroll
+                for (int k = 0; k < M::NT; ++k) *reinterpret_cast<gb8*>(out + k * 3072 + (u * 64 + lane) * 8) = sp.t[k];
+            } else {
+                *reinterpret_cast<gf4*>(out + (u * 128 + lane) * 4) = a;
+                *reinterpret_cast<gf4*>(out + (u * 128 + 64 + lane) * 4) = c;
+            }
+        }
+}
+
+// ---------------------------------------------------------------------------
+// From chunk to chunk: a workgroup holds 64 columns of one head's state, a wave 16 of them, in
+// registers. What all waves need lies in LDS: keys twice (the next chunk's come while this one's are in
+// use), queries, T and the tokens' factors once, loaded again as soon as the last wave has used them; P is
+// made here, two or three tiles a wave, since reading it back would cost as much as T.
+template <typename T, int DKP, bool TWO, bool AL>
+struct GdrWalk {
+    using M = Mx<T>;
+    static constexpr int KD = DKP / 32, ND = DKP / 16, TP = 3072;
+    const LaunchGdr& p;
+    GdrRows<T, KD, AL> rk, rq;
+    T *tq, *tt, *tp;
+    float *tok, *srq;
+    int64_t b, bh, nc;
+    int h, lane, w, g, m, col, place;
+    bool in;
+    const T* vb;
+    T* yb;
+    gf4 S[ND];
+    T v[16];                                          // the next values as they came, no use of them before they are needed
+
+    __device__ __forceinline__ GdrWalk(const LaunchGdr& a, T* q_, T* t_, T* p_, float* tok_, float* srq_, int64_t b_, int64_t bh_, int h_,
+                                       int hk, int col_)
+        : p(a), rk(a.k, b_, hk, a.dk), rq(a.q, b_, hk, a.dk), tq(q_), tt(t_), tp(p_), tok(tok_), srq(srq_), b(b_), bh(bh_),
+          nc(a.nchunks), h(h_), lane(threadIdx.x & 63), w(gdr_wave()), g(lane >> 4), m(lane & 15), col(col_), place(gdr_place(g, m)), in(col_ < a.dv),
+          vb(static_cast<const T*>(a.v.p) + b_ * a.v.batch_stride + h_ * a.v.head_stride),
+          yb(static_cast<T*>(a.y) + (b_ * a.L * a.H + h_) * a.dv) {}
+
+    __device__ __forceinline__ void rest(int64_t n) const {       // queries, T, factors of chunk n
+        rq.load(tq, n * kGdrC, p.L);
+        const int64_t id = bh * nc + n;
+        const auto rt = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<T*>(p.wT) + id * (M::NT * TP), 0, -1, kBufDword3);
+        constexpr int U = M::NT * TP * (int)sizeof(T) / 1024;
+#pragma unroll
+        for (int e = 0; e < (U + 3) / 4; ++e) {
+            const int u = e * 4 + w;
+            if (u < U) __builtin_amdgcn_raw_ptr_buffer_load_lds(rt, (gu4*)(tt + u * (1024 / sizeof(T))), 16, lane * 16, u * 1024, 0, 0);
+        }
+        const auto rc = __builtin_amdgcn_make_buffer_rsrc(p.co + id * (kGdrTok * 64), 0, -1, kBufDword3);
+        if (w * 64 + lane < kGdrTok * 16) __builtin_amdgcn_raw_ptr_buffer_load_lds(rc, (gu4*)(tok + w * 256), 16, lane * 16, w * 1024, 0, 0);
+    }
+    // rows past the last token as copies of it, as the keys'
+    __device__ __forceinline__ void values(int64_t n) {
+        const int64_t t0 = n * kGdrC;
+        const T* at = vb + t0 * p.v.token_stride;
+        const int c = in ? col : p.dv - 1, last = p.L - t0 < kGdrC ? (int)(p.L - t0) - 1 : kGdrC - 1;
+        const GdrBuf<T> buf(at);
+        const unsigned row = (unsigned)p.v.token_stride * (unsigned)sizeof(T);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int t = 16 * i + 4 * g + r, u = t < last ? t : last;
+                if constexpr (AL) v[4 * i + r] = buf.ld(u * row + c * (unsigned)sizeof(T), 0);
+                else v[4 * i + r] = at[u * p.v.token_stride + c];
+            }
+    }
+
+    // one chunk; keys in `tk`, the next chunk's on their way to `tn`
+    __device__ __forceinline__ void chunk(int64_t n, int64_t end_n, T* tk, T* tn) {
+        const int64_t t0 = n * kGdrC;
+        gdr_arrived();
+        if (TWO && n + 1 < end_n) rk.load(tn, t0 + kGdrC, p.L);
+        if (p.ckpt) {
+            const GdrBuf<float> ck(p.ckpt + (bh * nc + n) * p.dk * p.dv);
+            unsigned dvb = p.dv * 4;
+            asm volatile("" : "+s"(dvb));             // offsets made where they are used, not kept over the loop
+            const unsigned lo = 8 * g * dvb + col * 4;
+            if (in)
+#pragma unroll
+                for (int s = 0; s < KD; ++s) {
+                    if (AL && 32 * s + 8 * g >= p.dk) continue;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (AL || 32 * s + 8 * g + e < p.dk) ck.st(S[2 * s + (e >> 2)][e & 3], lo, (32 * s + e) * dvb);
+                }
+        }
+        // K S0; Q S0 transposed (a lane has a token's row), which is how it is stored; P's row tile of this wave, transposed
+        // too, without the queries' lengths; and these lengths, a diagonal. The next fragments are read ahead of
+        // the products of these.
+        gf4 ks[4] = {}, qs[4] = {}, pt[4] = {}, len = {0, 0, 0, 0};
+        {
+            typename M::F f[2][9];
+            auto read = [&](int s, typename M::F (&x)[9]) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[i] = gdr_rows_frag<T>(tk, i * KD + s, place);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[4 + i] = gdr_rows_frag<T>(tq, i * KD + s, place);
+                x[8] = gdr_rows_frag<T>(tq, w * KD + s, place);
+            };
+            read(0, f[0]);
+#pragma unroll
+            for (int s = 0; s < KD; ++s) {
+                if (s + 1 < KD) read(s + 1, f[(s + 1) & 1]);
+                __builtin_amdgcn_sched_barrier(0);
+                auto& x = f[s & 1];
+                const auto sb = M::template split<3>(gdr_pair(S[2 * s], S[2 * s + 1]));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) pt[i] = M::mm(x[i], x[8], pt[i]);
+                len = M::mm(x[8], x[8], len);
+#pragma unroll
+                for (int k = sizeof(T) == 2 ? 2 : 0; k >= 0; --k) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) ks[i] = M::mm(x[i], sb.t[k], ks[i]);
+                    if (k < 2)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) qs[i] = M::mm(sb.t[k], x[4 + i], qs[i]);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+        {
+            const double* G = reinterpret_cast<const double*>(tok + tG * 64);
+            const double gi = G[16 * w + m];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (i > w) break;                     // this wave's tiles above the diagonal stay 0 in LDS
+                const gf4 bk = *reinterpret_cast<const gf4*>(&tok[tBk * 64 + 16 * i + 4 * g]);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const int row = d * 16 + 4 * g + r, col = col0 + 16 * c;
-                    if (row < p.dk && col < p.dv) st[row * p.dv + col] = S[c][d][r];
+                    const float d = __builtin_amdgcn_exp2f((float)(gi - G[16 * i + 4 * g + r]));
+                    pt[i][r] = d != 0.0f && (i < w || m >= 4 * g + r) ? pt[i][r] * d * bk[r] : 0.0f;
                 }
+                const int unit = w < 2 ? w : 2 * w - 2 + (i >> 1);
+                if constexpr (sizeof(T) == 2) {
+                    typedef __bf16 gb4 __attribute__((ext_vector_type(4)));
+                    const gb4 a = __builtin_convertvector(pt[i], gb4), c = __builtin_convertvector(pt[i] - __builtin_convertvector(a, gf4), gb4);
+                    T* at = tp + (unit * 64 + lane) * 8 + 4 * (i & 1);
+                    *reinterpret_cast<gb4*>(at) = a;
+                    *reinterpret_cast<gb4*>(at + TP) = c;
+                } else {
+                    *reinterpret_cast<gf4*>(tp + ((unit * 2 + (i & 1)) * 64 + lane) * 4) = pt[i];
+                }
+            }
+            const float q2 = (m & 3) == 0 ? len[0] : (m & 3) == 1 ? len[1] : (m & 3) == 2 ? len[2] : len[3];
+            if (m >> 2 == g) srq[16 * w + m] = p.eps > 0.0f ? p.scale * __builtin_amdgcn_rsqf(q2 + p.eps) : p.scale;
+        }
+        // V - e^G K S0; where a decay is nothing it leaves out what it multiplies
+        const float end = tok[tMisc * 64];
+        const bool clean = tok[tMisc * 64 + 1] != 0.0f;
+        gf4 a3[4], V[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const gf4 a1 = *reinterpret_cast<const gf4*>(&tok[tA1 * 64 + 16 * i + 4 * g]);
+            const float a2 = tok[tA2 * 64 + 16 * i + m];
+            a3[i] = *reinterpret_cast<const gf4*>(&tok[tA3 * 64 + 16 * i + 4 * g]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) V[i][r] = IO<T>::cvt(v[4 * i + r]);
+            if (clean) {
+                V[i] -= a1 * ks[i];
+                qs[i] *= a2;
+            } else {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    V[i][r] -= a1[r] != 0.0f ? a1[r] * ks[i][r] : 0.0f;
+                    qs[i][r] = a2 != 0.0f ? a2 * qs[i][r] : 0.0f;
+                }
+            }
+        }
+        gf4 X[4] = {};
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            typename M::template S<M::NT> tf[4];
+#pragma unroll
+            for (int i = 2 * s; i < 4; ++i) tf[i] = gdr_terms<T, M::NT>(tt, TP, gdr_low(i, s), lane);
+            const auto rb = M::template split<M::NT>(gdr_pair(V[2 * s], V[2 * s + 1]));
+            M::template each<M::NT>([&](int a, int c) {
+#pragma unroll
+                for (int i = 2 * s; i < 4; ++i) X[i] = M::mm(tf[i].t[a], rb.t[c], X[i]);
+            });
+        }
+        __syncthreads();                              // P is there; queries, T and factors are used up
+        if (n + 1 < end_n) {
+            rest(n + 1);
+            values(n + 1);
+        }
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const auto xb = M::template split<M::NP>(gdr_pair(X[2 * s], X[2 * s + 1]));
+            typename M::template S<M::NP> pf[4];
+#pragma unroll
+            for (int i = 2 * s; i < 4; ++i) pf[i] = gdr_terms<T, M::NP>(tp, TP, gdr_low(i, s), lane);
+            M::template each<M::NP>([&](int a, int c) {
+#pragma unroll
+                for (int i = 2 * s; i < 4; ++i) qs[i] = M::mm(xb.t[a], pf[i].t[c], qs[i]);
+            });
+        }
+        {
+            const int left = p.L - t0 < kGdrC ? (int)(p.L - t0) : kGdrC;
+            unsigned row = (unsigned)(p.H * p.dv);
+            asm volatile("" : "+s"(row));
+            const GdrBuf<T> yt(yb + t0 * row);
+            const int c0 = col - m + 4 * g;
+            const unsigned lo = (m * row + c0) * (unsigned)sizeof(T);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                qs[i] *= srq[16 * i + m];
+                if constexpr (AL) {
+                    if (16 * i + m < left && c0 < p.dv) yt.st4(qs[i], lo, 16 * i * row * (unsigned)sizeof(T));
+                } else {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (16 * i + m < left && c0 + r < p.dv) yt.st(qs[i][r], lo + r * (unsigned)sizeof(T), 16 * i * row * (unsigned)sizeof(T));
+                }
+            }
+            if (p.ckpt && in) {
+                const GdrBuf<float> xt(p.ckptX + ((b * p.L + t0) * p.H + h) * p.dv);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (16 * i + 4 * g + r < left) xt.st(X[i][r], (4 * g * row + col) * 4, (16 * i + r) * row * 4);
+            }
+        }
+        // the next state
+        {
+            constexpr int NB = 2 * ND / 4;            // batches of four tiles, tokens' first half, then the second
+            typename M::F f[2][4];
+            auto read = [&](int q, typename M::F (&x)[4]) {
+#pragma unroll
+                for (int d = 0; d < 4; ++d) x[d] = gdr_frag_t<T, KD>(tk, q / (ND / 4), q % (ND / 4) * 2 + (d >> 1), d & 1, lane);
+            };
+            read(0, f[0]);
+#pragma unroll
+            for (int d = 0; d < ND; ++d) S[d] = end != 0.0f ? S[d] * end : gf4{0, 0, 0, 0};
+            typename M::template S<3> xb;
+#pragma unroll
+            for (int q = 0; q < NB; ++q) {
+                const int s = q / (ND / 4), d0 = q % (ND / 4) * 4;
+                if (q + 1 < NB) read(q + 1, f[(q + 1) & 1]);
+                if (d0 == 0) xb = M::template split<3>(gdr_pair(X[2 * s] * a3[2 * s], X[2 * s + 1] * a3[2 * s + 1]));
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int k = sizeof(T) == 2 ? 2 : 0; k >= 0; --k)
+#pragma unroll
+                    for (int d = 0; d < 4; ++d) S[d0 + d] = M::mm(f[q & 1][d], xb.t[k], S[d0 + d]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+        if (!TWO && n + 1 < end_n) {
+            __syncthreads();
+            rk.load(tk, t0 + kGdrC, p.L);
+        }
     }
+};
+
+template <typename T, int DKP, bool TWO, bool AL, int GROUPS>
+__global__ void __launch_bounds__(256, GROUPS)
+k_gdr_walk(const LaunchGdr p) {
+    using W = GdrWalk<T, DKP, TWO, AL>;
+    __shared__ alignas(16) T k0[64 * DKP], k1[TWO ? 64 * DKP : 8], tq[64 * DKP], tt[Mx<T>::NT * 3072], tp[Mx<T>::NP * 3072];
+    __shared__ alignas(16) float tok[kGdrTok * 64], srq[64];
+    const int tid = threadIdx.x, lane = tid & 63, w = gdr_wave(), g = lane >> 4, m = lane & 15;
+    const int64_t BH = p.B * p.H, bh = blockIdx.x % BH, b = bh / p.H, nc = p.nchunks;
+    const int h = (int)(bh % p.H), hk = h / (p.H / p.Hk), col = (int)(blockIdx.x / BH) * 64 + w * 16 + m;
+    W k(p, tq, tt, tp, tok, srq, b, bh, h, hk, col);
+    float* st = p.state ? p.state + bh * p.dk * p.dv : nullptr;
+#pragma unroll
+    for (int d = 0; d < W::ND; ++d)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int row = 32 * (d >> 1) + 8 * g + 4 * (d & 1) + r;
+            k.S[d][r] = st && row < p.dk && k.in ? st[row * p.dv + col] : 0.0f;
+        }
+    // what no load writes: columns past dk, the halves of blocks above P's diagonal
+    for (int e = tid; e < 64 * DKP; e += 256) {
+        k0[e] = T(0);
+        tq[e] = T(0);
+        if (TWO) k1[e] = T(0);
+    }
+    for (int e = tid; e < Mx<T>::NP * 3072; e += 256) tp[e] = T(0);
+    __syncthreads();
+    k.rk.load(k0, 0, p.L);
+    k.rest(0);
+    k.values(0);
+    if constexpr (TWO) {
+        for (int64_t n = 0; n < nc; n += 2) {
+            k.chunk(n, nc, k0, k1);
+            if (n + 1 < nc) k.chunk(n + 1, nc, k1, k0);
+        }
+    } else {
+        for (int64_t n = 0; n < nc; ++n) k.chunk(n, nc, k0, k0);
+    }
+    if (st && k.in)
+#pragma unroll
+        for (int d = 0; d < W::ND; ++d)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = 32 * (d >> 1) + 8 * g + 4 * (d & 1) + r;
+                if (row < p.dk) st[row * p.dv + col] = k.S[d][r];
+            }
 }
 
 // ---------------------------------------------------------------------------
@@ -702,11 +1152,6 @@ k_gdr_walk_back(const LaunchGdr p) {
 //   sum_{i >= t > j} beta_j (E P + F N/beta)_ij + sum_{i >= t} (q . a2 dY S0^T - k . a1 dV S0^T)_i
 //     + sum_{j < t} beta_j (k . a3b X W^T)_j + e^G_last <S0, W>
 // A wave has a quarter of dk's columns; terms over dv go through LDS 32 at a time.
-__device__ __forceinline__ void gdr_tile(int tile, int& mt, int& nt) {
-    mt = tile < 1 ? 0 : tile < 3 ? 1 : tile < 6 ? 2 : 3;
-    nt = tile - mt * (mt + 1) / 2;
-}
-
 // eight fp32 values of a row, zeros past its end
 __device__ __forceinline__ gf8 gdr_ld8(const float* row, int c, int n, bool there, bool vec) {
     gf8 v = {0, 0, 0, 0, 0, 0, 0, 0};
@@ -1094,9 +1539,11 @@ hipError_t launch_gdr_d(const LaunchGdr& p) {
     const unsigned chunks = (unsigned)(BH * p.nchunks);
     const unsigned tiles = (unsigned)(BH * ((p.dv + 63) / 64));
     if (p.pass == LaunchGdr::kFwd) {
-        hipLaunchKernelGGL((k_gdr_prep<T, DKP, false>), dim3(chunks), dim3(256), 0, st, p);
-        if (p.ckpt) hipLaunchKernelGGL((k_gdr_walk<T, DKP, 1, true>), dim3(tiles), dim3(256), 0, st, p);
-        else hipLaunchKernelGGL((k_gdr_walk<T, DKP, 1, false>), dim3(tiles), dim3(256), 0, st, p);
+        constexpr bool kTwo = DKP * sizeof(T) <= 512;       // keys twice in LDS
+        hipLaunchKernelGGL((k_gdr_solve<T, DKP>), dim3((chunks + 3) / 4), dim3(256), 0, st, p);
+        constexpr int kGroups = DKP <= 128 && sizeof(T) == 2 ? 2 : 1;
+        if (p.vec && p.vec_v && p.vec_y) hipLaunchKernelGGL((k_gdr_walk<T, DKP, kTwo, true, kGroups>), dim3(tiles), dim3(256), 0, st, p);
+        else hipLaunchKernelGGL((k_gdr_walk<T, DKP, kTwo, false, kGroups>), dim3(tiles), dim3(256), 0, st, p);
     } else {
         hipLaunchKernelGGL((k_gdr_prep<T, DKP, true>), dim3(chunks), dim3(256), 0, st, p);
         hipLaunchKernelGGL((k_gdr_walk_back<T, DKP, 1>), dim3(tiles), dim3(256), 0, st, p);

@@ -23,6 +23,8 @@ ss_status check_gdr_dims(const ss_gdr_dims* d, GdrCall call) {
     if (d->heads % d->k_heads) return fail(SS_ERR_INVALID_ARG, "heads %d not a multiple of k_heads %d", d->heads, d->k_heads);
     if (d->dk > 256 || d->dv > 512) return fail(SS_ERR_UNSUPPORTED, "dk %d above 256 or dv %d above 512", d->dk, d->dv);
     if (d->io_dtype != SS_F32 && d->io_dtype != SS_BF16) return fail(SS_ERR_UNSUPPORTED, "io_dtype %d unknown", d->io_dtype);
+    // 64 tokens of y lie within 32-bit offsets
+    if ((int64_t)d->heads * d->dv > (int64_t(1) << 22)) return fail(SS_ERR_UNSUPPORTED, "heads x dv above 2^22");
     if (!std::isfinite(d->scale)) return fail(SS_ERR_INVALID_ARG, "scale must be finite");
     if (!(d->eps >= 0.0f) || !std::isfinite(d->eps)) return fail(SS_ERR_INVALID_ARG, "eps must be finite and not negative");
     if (d->reserved != 0) return fail(SS_ERR_INVALID_ARG, "reserved must be 0");
@@ -52,7 +54,7 @@ GdrLayout gdr_layout(const ss_gdr_dims& d, bool backward) {
     size_t off = 0;
     auto take = [&](size_t& at, size_t floats) { at = off; off = align256(off + floats * 4); };
     take(l.co, n * 8 * 64);
-    take(l.wT, n * 6 * 512);
+    take(l.wT, n * 9216);
     take(l.wP, n * 6 * 512);
     if (backward) {
         take(l.raw, n * 30 * 256);
@@ -77,10 +79,10 @@ ss_status check_view(const ss_head_view& v, int64_t B, int64_t L, int64_t H, int
     return SS_OK;
 }
 
-// every row of a view starts on 16 bytes and is whole accesses of 16 bytes
+// every row of a view starts on 16 bytes and is whole accesses of 16 bytes, 64 tokens within 32-bit offsets
 bool view_vec(const ss_head_view& v, int64_t B, int64_t L, int64_t H, int64_t d, int64_t es) {
     const int64_t per = 16 / es;
-    return (uintptr_t)v.p % 16 == 0 && d % 8 == 0 && (B == 1 || v.batch_stride % per == 0) && (L == 1 || v.token_stride % per == 0) &&
+    return (uintptr_t)v.p % 16 == 0 && d % 8 == 0 && v.token_stride < (int64_t(1) << 24) && (B == 1 || v.batch_stride % per == 0) && (L == 1 || v.token_stride % per == 0) &&
            (H == 1 || v.head_stride % per == 0);
 }
 
@@ -113,6 +115,8 @@ ss_status check_gdr_args(const ss_gdr_dims& d, const ss_gdr_args* a, GdrCall cal
     if (call != kBwd && (uintptr_t)a->y % es) return fail(SS_ERR_INVALID_ARG, "y not aligned to its element");
     p->bf16 = d.io_dtype == SS_BF16;
     p->vec = view_vec(a->q, B, L, d.k_heads, d.dk, es) && view_vec(a->k, B, L, d.k_heads, d.dk, es);
+    p->vec_v = L == 1 || a->v.token_stride < (int64_t(1) << 24);
+    p->vec_y = d.dv % 4 == 0 && (uintptr_t)a->y % (4 * es) == 0;
     p->vec_state = d.dv % 4 == 0 && (uintptr_t)a->state % 16 == 0;
     p->B = B;
     p->L = L;

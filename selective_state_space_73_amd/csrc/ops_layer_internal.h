@@ -13,6 +13,8 @@ struct LaunchGdr {
     enum Pass { kFwd, kBwd, kStep } pass;
     bool bf16;
     bool vec;                    // rows of q and k start on 16 bytes and hold whole accesses of 16 bytes
+    bool vec_v;                  // 64 tokens of v lie within 32-bit offsets
+    bool vec_y;                  // four columns of y are one access
     bool vec_state;              // the step: dv a multiple of 4, the state on 16 bytes
     int64_t B, L, nchunks;
     int H, Hk, dk, dv;
