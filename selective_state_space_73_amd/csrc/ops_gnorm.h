@@ -102,6 +102,32 @@ __device__ __forceinline__ void gnorm_groups_sum(float (*v)[8], int K, int group
     __syncthreads();
 }
 
+// Eight values as they came; converted where they are used, so that a row's loads are in flight over the one before.
+// What is not there is read from somewhere that is and masked, with no branch between the loads.
+template <typename T, bool VEC> struct GnormRaw {
+    float x[8];
+    __device__ __forceinline__ void ld(const void* base, int64_t row, int c, int K) { ld8<T, VEC>(static_cast<const T*>(base) + row * K, c, K, x); }
+    __device__ __forceinline__ void get(uint32_t mask, int c, int K, float* v) const {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, x[j]) & mask);
+        ends8<VEC>(c, K, v);
+    }
+};
+template <> struct GnormRaw<uint16_t, true> {
+    typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+    u4 u;
+    __device__ __forceinline__ void ld(const void* base, int64_t row, int c, int K) {
+        u = *reinterpret_cast<const u4*>(static_cast<const uint16_t*>(base) + row * K + (c < K ? c : K - 8));
+    }
+    __device__ __forceinline__ void get(uint32_t mask, int, int, float* v) const {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[2 * j] = __builtin_bit_cast(float, (u[j] & mask) << 16);
+            v[2 * j + 1] = __builtin_bit_cast(float, u[j] & mask & 0xffff0000u);
+        }
+    }
+};
+
 template <typename T, bool VEC>
 __device__ __forceinline__ void gnorm_ld(const void* base, int64_t row, int c, int K, float* v) {
     if (base) {
@@ -125,7 +151,10 @@ __device__ __forceinline__ void gnorm_ldp(const float* w, int c, int K, float no
     }
 }
 
-__device__ __forceinline__ float gnorm_sigmoid(float z) { return 1.0f / (1.0f + expf(-z)); }
+// v_exp and v_rcp, each within one step: the exponent's rounding adds |z| 2^-24 of e^-z
+__device__ __forceinline__ float gnorm_sigmoid(float z) {
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.44269504088896341f));
+}
 
 struct GnormArgs {
     const void *y, *gate, *residual, *ds, *dn;
@@ -134,6 +163,7 @@ struct GnormArgs {
     float* part;
     int64_t M;
     int K, group;
+    int woff;                     // the backward: where the weights lie in LDS, in floats
     int per;                      // the forward by groups: groups of a row, whose scales follow each other
     float eps;
 };
@@ -147,6 +177,7 @@ k_gnorm_fwd(const GnormArgs p) {
     const bool there = at < p.M;
     const int64_t row = there ? at : p.M - 1;
     const float* scale = p.scale ? p.scale + row % p.per * K : nullptr;
+    const bool gated = p.gate != nullptr;
     float y[NV][8], z[NV][8], s[NV][8], q[1] = {0.0f};
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
@@ -188,8 +219,8 @@ k_gnorm_fwd(const GnormArgs p) {
         gnorm_ldp<VEC>(scale, c, K, 1.0f, a);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            float h = y[v][j] * (GROUPED ? 1.0f / sqrtf(ry[v][j] * inv + p.eps) : r1) * w[j];
-            if (p.gate) h *= z[v][j] * gnorm_sigmoid(z[v][j]);
+            const float act = z[v][j] * gnorm_sigmoid(z[v][j]);
+            const float h = y[v][j] * (GROUPED ? 1.0f / sqrtf(ry[v][j] * inv + p.eps) : r1) * w[j] * (gated ? act : 1.0f);
             s[v][j] = __builtin_fmaf(a[j], h, s[v][j]);
             if (c < K) q[0] = __builtin_fmaf(s[v][j], s[v][j], q[0]);
         }
@@ -209,58 +240,99 @@ k_gnorm_fwd(const GnormArgs p) {
     }
 }
 
-template <typename T, bool VEC, int LANES, int NV, bool GROUPED, int MAXT>
-__global__ void __launch_bounds__(MAXT)
+// A lane's columns are the same in every row: their sums over rows stay in its registers, and (AHEAD) the next row is on its way while this one is worked on.
+template <typename T, bool VEC, int LANES, int NV, bool GROUPED, int MAXT, bool AHEAD, int WAVES>
+__global__ void __launch_bounds__(MAXT, WAVES)
 k_gnorm_bwd(const GnormArgs p) {
     extern __shared__ float lds[];
     constexpr int R = LANES ? MAXT / LANES : 1;
     const int nl = LANES ? LANES : blockDim.x, lane = threadIdx.x % nl, K = p.K, slot = threadIdx.x / nl;
     const int64_t step = (int64_t)gridDim.x * R;
     float sw[NV][8] = {}, sa[NV][8] = {}, sn[NV][8] = {};
+    // the weights by column, zeros past the last, in LDS (NV 1): three eights more in registers spill
+    constexpr bool IN_LDS = NV == 1;
+    float* lw = lds + p.woff;
+    const int KP = nl * 8;
+    auto weights = [&](int c, int which, float* x) {
+        if constexpr (IN_LDS) {
+            typedef float f4 __attribute__((ext_vector_type(4)));
+            const f4 a = *reinterpret_cast<const f4*>(lw + which * KP + c), b = *reinterpret_cast<const f4*>(lw + which * KP + c + 4);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) { x[j] = a[j]; x[4 + j] = b[j]; }
+        } else if (which == 0) {
+            gnorm_w8<VEC, GROUPED>(p.w, c, K, p.group, x);
+        } else {
+            gnorm_ldp<VEC>(which == 1 ? p.scale : p.w_next, c, K, which == 1 ? 1.0f : 0.0f, x);
+        }
+    };
+    if constexpr (IN_LDS) {
+        for (int c = threadIdx.x; c < KP; c += blockDim.x) {
+            lw[c] = c < K ? p.w[GROUPED ? c % p.group : c] : 0.0f;
+            lw[KP + c] = c < K ? p.scale ? p.scale[c] : 1.0f : 0.0f;
+            lw[2 * KP + c] = c < K && p.w_next ? p.w_next[c] : 0.0f;
+        }
+        __syncthreads();
+    }
     const float inv = 1.0f / (GROUPED ? p.group : K), invk = 1.0f / K;
-    for (int64_t row = (int64_t)blockIdx.x * R + slot; row < p.M; row += step) {
-        float y[NV][8], z[NV][8], s[NV][8], ds[NV][8], dn[NV][8], ry[NV][8], q[2] = {0.0f, 0.0f};
+    GnormRaw<T, VEC> raw[NV][5];
+    const void* const from[5] = {p.y, p.gate ? p.gate : p.y, p.residual ? p.residual : p.y, p.ds ? p.ds : p.y, p.dn ? p.dn : p.y};
+    const uint32_t mask[5] = {~0u, p.gate ? ~0u : 0u, p.residual ? ~0u : 0u, p.ds ? ~0u : 0u, p.dn ? ~0u : 0u};
+    const bool gated = p.gate != nullptr;
+    auto fetch = [&](int64_t row) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int k = 0; k < 5; ++k) raw[v][k].ld(from[k], row, (v * nl + lane) * 8, K);
+    };
+    const int64_t first = (int64_t)blockIdx.x * R + slot;
+    if (AHEAD && first < p.M) fetch(first);
+    for (int64_t row = first; row < p.M; row += step) {
+        float y[NV][8], z[NV][8], s[NV][8], ds[NV][8], dn[NV][8], ry[GROUPED ? NV : 1][8], sg[NV][8], q[2] = {0.0f, 0.0f};
+        if (!AHEAD) fetch(row);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int c = (v * nl + lane) * 8;
-            gnorm_ld<T, VEC>(p.y, row, c, K, y[v]);
-            gnorm_ld<T, VEC>(p.gate, row, c, K, z[v]);
-            gnorm_ld<T, VEC>(p.residual, row, c, K, s[v]);
-            gnorm_ld<T, VEC>(p.ds, row, c, K, ds[v]);
-            gnorm_ld<T, VEC>(p.dn, row, c, K, dn[v]);
+            raw[v][0].get(mask[0], c, K, y[v]);
+            raw[v][1].get(mask[1], c, K, z[v]);
+            raw[v][2].get(mask[2], c, K, s[v]);
+            raw[v][3].get(mask[3], c, K, ds[v]);
+            raw[v][4].get(mask[4], c, K, dn[v]);
         }
+        if (AHEAD) fetch(row + step < p.M ? row + step : row);
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            const bool in = (v * nl + lane) * 8 < K;
+        for (int v = 0; v < NV; ++v)
+            if ((v * nl + lane) * 8 < K) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                ry[v][j] = in ? y[v][j] * y[v][j] : 0.0f;
-                q[0] += ry[v][j];
+                for (int j = 0; j < 8; ++j) q[0] = __builtin_fmaf(y[v][j], y[v][j], q[0]);
             }
-        }
         if constexpr (GROUPED) {
+#pragma unroll
+            for (int v = 0; v < NV; ++v)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) ry[v][j] = y[v][j] * y[v][j];
             gnorm_groups_sum<VEC, NV>(ry, K, p.group, lds + 96, lds + 96 + (VEC ? K / 8 : K));
+#pragma unroll
+            for (int v = 0; v < NV; ++v)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) ry[v][j] = 1.0f / sqrtf(ry[v][j] * inv + p.eps);
         } else {
             gnorm_sum<1, LANES>(q, lds);
         }
         const float r1 = GROUPED ? 0.0f : 1.0f / sqrtf(q[0] * inv + p.eps);
         q[0] = 0.0f;
-        float w[NV][8], a[NV][8], pp[NV][8];
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int c = (v * nl + lane) * 8;
-            float wn[8];
-            gnorm_w8<VEC, GROUPED>(p.w, c, K, p.group, w[v]);
-            gnorm_ldp<VEC>(p.scale, c, K, 1.0f, a[v]);
-            gnorm_ldp<VEC>(p.w_next, c, K, 0.0f, wn);
+            float w[8], a[8], wn[8];
+            weights(c, 0, w);
+            weights(c, 1, a);
+            weights(c, 2, wn);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                ry[v][j] = GROUPED ? 1.0f / sqrtf(ry[v][j] * inv + p.eps) : r1;
-                y[v][j] *= ry[v][j];                                               // y normed
-                pp[v][j] = y[v][j] * w[v][j];
-                float h = pp[v][j];
-                if (p.gate) h *= z[v][j] * gnorm_sigmoid(z[v][j]);
-                s[v][j] = __builtin_fmaf(a[v][j], h, s[v][j]);
+                y[v][j] *= GROUPED ? ry[GROUPED ? v : 0][j] : r1;                  // y normed
+                sg[v][j] = gnorm_sigmoid(z[v][j]);
+                const float h = y[v][j] * w[j] * (gated ? z[v][j] * sg[v][j] : 1.0f);
+                s[v][j] = __builtin_fmaf(a[j], h, s[v][j]);
                 if (c < K) {
                     q[0] = __builtin_fmaf(s[v][j], s[v][j], q[0]);
                     q[1] = __builtin_fmaf(s[v][j], dn[v][j] * wn[j], q[1]);
@@ -272,9 +344,8 @@ k_gnorm_bwd(const GnormArgs p) {
             const float r2 = 1.0f / sqrtf(q[0] * invk + p.eps), m = q[1] * invk * r2 * r2;
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
-                const int c = (v * nl + lane) * 8;
                 float wn[8];
-                gnorm_ldp<VEC>(p.w_next, c, K, 0.0f, wn);
+                weights((v * nl + lane) * 8, 2, wn);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     sn[v][j] = __builtin_fmaf(dn[v][j], s[v][j] * r2, sn[v][j]);
@@ -287,19 +358,18 @@ k_gnorm_bwd(const GnormArgs p) {
         for (int v = 0; v < NV; ++v) {
             const int c = (v * nl + lane) * 8;
             if (p.dresidual) st8<T, VEC>(static_cast<T*>(p.dresidual) + row * K, c, K, ds[v]);
+            float w[8], a[8];
+            weights(c, 0, w);
+            weights(c, 1, a);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float dh = ds[v][j] * a[v][j];
-                float dp = dh, h = pp[v][j];
-                if (p.gate) {
-                    const float sig = gnorm_sigmoid(z[v][j]), act = z[v][j] * sig;
-                    dp = dh * act;
-                    h *= act;
-                    z[v][j] = dh * pp[v][j] * (sig + act * (1.0f - sig));          // gradient of the gate
-                }
+                const float dh = ds[v][j] * a[j], pp = y[v][j] * w[j];
+                const float sig = sg[v][j], silu = z[v][j] * sig, act = gated ? silu : 1.0f;
+                const float dp = dh * act, h = pp * act;
+                z[v][j] = dh * pp * (sig + silu * (1.0f - sig));                   // gradient of the gate
                 sa[v][j] = __builtin_fmaf(ds[v][j], h, sa[v][j]);
                 sw[v][j] = __builtin_fmaf(dp, y[v][j], sw[v][j]);
-                s[v][j] = dp * w[v][j];
+                s[v][j] = dp * w[j];
                 dn[v][j] = c < K ? s[v][j] * y[v][j] : 0.0f;
                 q[0] += dn[v][j];
             }
@@ -315,7 +385,8 @@ k_gnorm_bwd(const GnormArgs p) {
         for (int v = 0; v < NV; ++v) {
             const int c = (v * nl + lane) * 8;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) s[v][j] = ry[v][j] * (s[v][j] - y[v][j] * (GROUPED ? dn[v][j] * inv : m1));
+            for (int j = 0; j < 8; ++j)
+                s[v][j] = (GROUPED ? ry[GROUPED ? v : 0][j] : r1) * (s[v][j] - y[v][j] * (GROUPED ? dn[v][j] * inv : m1));
             st8<T, VEC>(static_cast<T*>(p.dy) + row * K, c, K, s[v]);
         }
         if constexpr (LANES == 0) __syncthreads();        // the next row's sums go where this one's are still read
@@ -346,23 +417,33 @@ k_gnorm_bwd(const GnormArgs p) {
 }
 
 // The sums of columns over the workgroups (and w's over the groups of a row), in a fixed order: 32 columns
-// by eight slices of the terms a workgroup.
-__global__ void __launch_bounds__(256)
+// by 32 slices of the terms a workgroup, eight terms of a slice in flight.
+__global__ void __launch_bounds__(1024)
 k_gnorm_sum(const float* part, int64_t n, int K, int group, float* dw, float* dscale, float* dw_next) {
-    __shared__ double lds[8][33];
+    __shared__ double lds[32][33];
     const int cols = blockIdx.y ? K : group;
     float* out = blockIdx.y == 0 ? dw : blockIdx.y == 1 ? dscale : dw_next;
     const int c = blockIdx.x * 32 + (threadIdx.x & 31), slice = threadIdx.x >> 5;
     if (!out || (int)blockIdx.x * 32 >= cols) return;
-    const int64_t per = blockIdx.y ? 1 : K / group, terms = n * per, a = terms * slice / 8, b = terms * (slice + 1) / 8;
-    double s = 0.0;                                     // thousands of terms, one after the other
-    if (c < cols)
-        for (int64_t i = a; i < b; ++i) s += part[i / per * 3 * K + (int64_t)blockIdx.y * K + i % per * group + c];
+    const unsigned per = blockIdx.y ? 1 : K / group, terms = (unsigned)n * per;
+    const float* at = part + (int64_t)blockIdx.y * K + (c < cols ? c : 0);
+    double s = 0.0;                                    // thousands of terms
+    for (unsigned i = slice; i < terms; i += 32 * 8) {
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const unsigned t = i + 32 * k < terms ? i + 32 * k : i;
+            v[k] = at[(int64_t)(t / per) * 3 * K + (int64_t)(t % per) * group];
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (i + 32 * k < terms) s += v[k];
+    }
     lds[slice][threadIdx.x & 31] = s;
     __syncthreads();
     if (slice == 0 && c < cols) {
 #pragma unroll
-        for (int k = 1; k < 8; ++k) s += lds[k][threadIdx.x & 31];
+        for (int k = 1; k < 32; ++k) s += lds[k][threadIdx.x & 31];
         out[c] = (float)s;
     }
 }
@@ -377,7 +458,7 @@ hipError_t gnorm_lds(F kernel, size_t bytes) {
 template <typename T, bool VEC>
 hipError_t launch_gnorm_t(const LaunchGnorm& p) {
     GnormArgs a{p.y, p.gate, p.residual, p.ds, p.dn, p.w, p.scale, p.w_next, p.s, p.n, p.dy, p.dgate, p.dresidual, p.part,
-                p.M, (int)p.K, (int)p.group, 1, p.eps};
+                p.M, (int)p.K, (int)p.group, 0, 1, p.eps};
     hipStream_t st = static_cast<hipStream_t>(p.stream);
     bool grouped = p.group < p.K;
     if (grouped && !p.back && !p.w_next) {
@@ -390,23 +471,24 @@ hipError_t launch_gnorm_t(const LaunchGnorm& p) {
     const GnormShape sh = gnorm_shape(a.K, grouped);
     const size_t sums = grouped ? (size_t)((VEC ? a.K / 8 : a.K) + a.K / a.group) * 4 : 0;
     if (p.back) {
-        const size_t shm = 96 * 4 + (grouped ? sums : sh.rows > 1 ? (size_t)3 * a.K * 4 : 0);
+        a.woff = (int)((96 * 4 + (grouped ? sums : sh.rows > 1 ? (size_t)3 * a.K * 4 : 0) + 15) / 16 * 4);
+        const size_t shm = (size_t)a.woff * 4 + (sh.nv == 1 ? (size_t)3 * sh.lanes * 8 * 4 : 0);
         const int64_t n = gnorm_groups(p.M, p.K);
         hipError_t e = hipSuccess;
         auto go = [&](auto kernel) {
             if ((e = gnorm_lds(kernel, shm)) == hipSuccess) hipLaunchKernelGGL(kernel, dim3((unsigned)n), dim3(sh.threads), shm, st, a);
         };
         if (grouped) {
-            if (sh.nv == 2) go(k_gnorm_bwd<T, VEC, 0, 2, true, 1024>);
-            else if (sh.threads > 512) go(k_gnorm_bwd<T, VEC, 0, 1, true, 1024>);
-            else go(k_gnorm_bwd<T, VEC, 0, 1, true, 512>);
-        } else if (sh.lanes == 16) go(k_gnorm_bwd<T, VEC, 16, 1, false, 256>);
-        else if (sh.rows == 4) go(k_gnorm_bwd<T, VEC, 64, 1, false, 256>);
-        else if (sh.nv == 2) go(k_gnorm_bwd<T, VEC, 0, 2, false, 1024>);
-        else if (sh.threads > 512) go(k_gnorm_bwd<T, VEC, 0, 1, false, 1024>);
-        else go(k_gnorm_bwd<T, VEC, 0, 1, false, 512>);
+            if (sh.nv == 2) go(k_gnorm_bwd<T, VEC, 0, 2, true, 1024, false, 4>);
+            else if (sh.threads > 512) go(k_gnorm_bwd<T, VEC, 0, 1, true, 1024, false, 4>);
+            else go(k_gnorm_bwd<T, VEC, 0, 1, true, 512, true, 3>);
+        } else if (sh.lanes == 16) go(k_gnorm_bwd<T, VEC, 16, 1, false, 256, true, 3>);
+        else if (sh.rows == 4) go(k_gnorm_bwd<T, VEC, 64, 1, false, 256, true, 3>);
+        else if (sh.nv == 2) go(k_gnorm_bwd<T, VEC, 0, 2, false, 1024, false, 4>);
+        else if (sh.threads > 512) go(k_gnorm_bwd<T, VEC, 0, 1, false, 1024, false, 4>);
+        else go(k_gnorm_bwd<T, VEC, 0, 1, false, 512, true, 3>);
         if (e != hipSuccess) return e;
-        hipLaunchKernelGGL(k_gnorm_sum, dim3((unsigned)((p.K + 31) / 32), 3), dim3(256), 0, st, p.part, n, (int)p.K, (int)p.group, p.dw,
+        hipLaunchKernelGGL(k_gnorm_sum, dim3((unsigned)((p.K + 31) / 32), 3), dim3(1024), 0, st, p.part, n, (int)p.K, (int)p.group, p.dw,
                            p.dscale, p.dw_next);
         return hipGetLastError();
     }
