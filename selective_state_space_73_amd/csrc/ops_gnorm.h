@@ -38,27 +38,46 @@ __device__ __forceinline__ void gnorm_w8(const float* w, int c, int K, int group
     }
 }
 
-// Sums over a row's lanes of N values at once. LANES 16 or 64: within a wave; 0: over the workgroup, `lds` of
-// 2 N floats a wave, of which calls use the halves in turn.
+// A lane's value from another of its 16: moves inside the vector unit, where a shuffle through LDS takes ten times as long.
+template <int CTRL>
+__device__ __forceinline__ float gnorm_dpp(float v) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
+}
+__device__ __forceinline__ float gnorm_sum16(float v) {
+    v += gnorm_dpp<0xb1>(v);                               // lane ^ 1
+    v += gnorm_dpp<0x4e>(v);                               // lane ^ 2
+    v += gnorm_dpp<0x141>(v);                              // the other four of eight
+    return v + gnorm_dpp<0x140>(v);                        // the other eight
+}
+__device__ __forceinline__ float gnorm_lane(float v, int lane) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+}
+
+// Sums over a row's lanes of N values at once. LANES 16 or 64: within a wave; 0: over the workgroup, `lds` of 16 floats a
+// value, zeros behind the last wave's; calls that follow each other use other places.
 template <int N, int LANES>
 __device__ __forceinline__ void gnorm_sum(float* v, float* lds) {
 #pragma unroll
-    for (int o = 1; o < (LANES ? LANES : 64); o <<= 1)
-#pragma unroll
-        for (int k = 0; k < N; ++k) v[k] += __shfl_xor(v[k], o, 64);
+    for (int k = 0; k < N; ++k) {
+        v[k] = gnorm_sum16(v[k]);
+        if (LANES != 16) v[k] = (gnorm_lane(v[k], 0) + gnorm_lane(v[k], 16)) + (gnorm_lane(v[k], 32) + gnorm_lane(v[k], 48));
+    }
     if constexpr (LANES == 0) {
-        const int waves = blockDim.x >> 6;
         if ((threadIdx.x & 63) == 0)
 #pragma unroll
             for (int k = 0; k < N; ++k) lds[k * 16 + (threadIdx.x >> 6)] = v[k];
         __syncthreads();
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-            float s = 0.0f;
-            for (int i = 0; i < waves; ++i) s += lds[k * 16 + i];
-            v[k] = s;
-        }
+        for (int k = 0; k < N; ++k) v[k] = gnorm_lane(gnorm_sum16(lds[k * 16 + (threadIdx.x & 15)]), 0);
     }
+}
+
+// Zeros behind the last wave's places of the six sums (no wave writes there, so no barrier).
+template <int LANES>
+__device__ __forceinline__ void gnorm_zero(float* lds) {
+    if (LANES == 0)
+        for (int i = threadIdx.x; i < 96; i += 64)
+            if (threadIdx.x < 64 && (i & 15) >= (int)(blockDim.x >> 6)) lds[i] = 0.0f;
 }
 
 // For each of a lane's values, the sum over its group: the eights' sums (VEC) or the values themselves meet in
@@ -178,6 +197,7 @@ k_gnorm_fwd(const GnormArgs p) {
     const int64_t row = there ? at : p.M - 1;
     const float* scale = p.scale ? p.scale + row % p.per * K : nullptr;
     const bool gated = p.gate != nullptr;
+    gnorm_zero<LANES>(lds);
     float y[NV][8], z[NV][8], s[NV][8], q[1] = {0.0f};
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
@@ -204,7 +224,7 @@ k_gnorm_fwd(const GnormArgs p) {
         }
     }
     if constexpr (GROUPED) {
-        gnorm_groups_sum<VEC, NV>(ry, K, p.group, lds + 64, lds + 64 + (VEC ? K / 8 : K));
+        gnorm_groups_sum<VEC, NV>(ry, K, p.group, lds + 96, lds + 96 + (VEC ? K / 8 : K));
     } else {
         gnorm_sum<1, LANES>(q, lds);
     }
@@ -284,6 +304,7 @@ k_gnorm_bwd(const GnormArgs p) {
 #pragma unroll
             for (int k = 0; k < 5; ++k) raw[v][k].ld(from[k], row, (v * nl + lane) * 8, K);
     };
+    gnorm_zero<LANES>(lds);
     const int64_t first = (int64_t)blockIdx.x * R + slot;
     if (AHEAD && first < p.M) fetch(first);
     for (int64_t row = first; row < p.M; row += step) {
@@ -481,18 +502,18 @@ hipError_t launch_gnorm_t(const LaunchGnorm& p) {
         if (grouped) {
             if (sh.nv == 2) go(k_gnorm_bwd<T, VEC, 0, 2, true, 1024, false, 4>);
             else if (sh.threads > 512) go(k_gnorm_bwd<T, VEC, 0, 1, true, 1024, false, 4>);
-            else go(k_gnorm_bwd<T, VEC, 0, 1, true, 512, true, 3>);
-        } else if (sh.lanes == 16) go(k_gnorm_bwd<T, VEC, 16, 1, false, 256, true, 3>);
-        else if (sh.rows == 4) go(k_gnorm_bwd<T, VEC, 64, 1, false, 256, true, 3>);
+            else go(k_gnorm_bwd<T, VEC, 0, 1, true, 512, true, 2>);
+        } else if (sh.lanes == 16) go(k_gnorm_bwd<T, VEC, 16, 1, false, 256, true, 2>);
+        else if (sh.rows == 4) go(k_gnorm_bwd<T, VEC, 64, 1, false, 256, true, 2>);
         else if (sh.nv == 2) go(k_gnorm_bwd<T, VEC, 0, 2, false, 1024, false, 4>);
         else if (sh.threads > 512) go(k_gnorm_bwd<T, VEC, 0, 1, false, 1024, false, 4>);
-        else go(k_gnorm_bwd<T, VEC, 0, 1, false, 512, true, 3>);
+        else go(k_gnorm_bwd<T, VEC, 0, 1, false, 512, true, 2>);
         if (e != hipSuccess) return e;
         hipLaunchKernelGGL(k_gnorm_sum, dim3((unsigned)((p.K + 31) / 32), 3), dim3(1024), 0, st, p.part, n, (int)p.K, (int)p.group, p.dw,
                            p.dscale, p.dw_next);
         return hipGetLastError();
     }
-    const size_t shm = 64 * 4 + sums;
+    const size_t shm = 96 * 4 + sums;
     const int64_t n = (a.M + sh.rows - 1) / sh.rows;
     if (n >= (int64_t(1) << 32) / 1024) {
         // more rows than one launch holds lanes for: in pieces

@@ -4,9 +4,9 @@
 namespace selscan {
 
 int64_t gnorm_groups(int64_t M, int64_t K) {
-    // as many workgroups as 256 CUs hold at 12 waves each, so that none waits for another to end
+    // as many workgroups as 256 CUs hold at 8 waves each, so that none waits for another to end
     const GnormShape sh = gnorm_shape(K, false);
-    const int64_t n = (M + sh.rows - 1) / sh.rows, waves = sh.threads / 64, most = 256 * (waves <= 12 ? 12 / waves : 1);
+    const int64_t n = (M + sh.rows - 1) / sh.rows, waves = sh.threads / 64, most = 256 * (waves <= 8 ? 8 / waves : 1);
     return n < most ? n : most;
 }
 
