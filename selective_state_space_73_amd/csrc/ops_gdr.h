@@ -46,13 +46,24 @@ template <> struct Mx<uint16_t> {
     typedef gb8 F;
     template <int N> struct S { gb8 t[N]; };
     static __device__ __forceinline__ F ld(const uint16_t* p) { return *reinterpret_cast<const gb8*>(p); }
+    // (two values a conversion, and their floats back from its halves)
     template <int N>
     static __device__ __forceinline__ S<N> split(gf8 v) {
+        typedef __bf16 gb2 __attribute__((ext_vector_type(2)));
+        typedef float gf2 __attribute__((ext_vector_type(2)));
         S<N> s;
 #pragma unroll
         for (int k = 0; k < N; ++k) {
-            s.t[k] = __builtin_convertvector(v, gb8);
-            if (k + 1 < N) v -= __builtin_convertvector(s.t[k], gf8);
+            gu4 u;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                u[j] = __builtin_bit_cast(uint32_t, __builtin_convertvector(gf2{v[2 * j], v[2 * j + 1]}, gb2));
+                if (k + 1 < N) {
+                    v[2 * j] -= __builtin_bit_cast(float, u[j] << 16);
+                    v[2 * j + 1] -= __builtin_bit_cast(float, u[j] & 0xffff0000u);
+                }
+            }
+            s.t[k] = __builtin_bit_cast(gb8, u);
         }
         return s;
     }
@@ -363,6 +374,20 @@ __device__ __forceinline__ void gdr_tile(int tile, int& mt, int& nt) {
 }
 
 // ---------------------------------------------------------------------------
+// eight fp32 values of a row, zeros past its end
+__device__ __forceinline__ gf8 gdr_ld8(const float* row, int c, int n, bool there, bool vec) {
+    gf8 v = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (!there) return v;
+    if (vec && c >= n) return v;
+    if (vec && c + 8 <= n) {
+        const gf4 a = *reinterpret_cast<const gf4*>(row + c), b = *reinterpret_cast<const gf4*>(row + c + 4);
+        return gdr_pair(a, b);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = c + j < n ? row[c + j] : 0.0f;
+    return v;
+}
+
 // Operands in LDS: 64 rows of DKP columns as fragments (row tile i, columns 32 s to 32 s + 31): lane 16 g + m
 // reads row 16 i + m at columns 32 s + 8 g + j, 16 bytes (an fp32 fragment is two such units, j < 4 and the rest).
 // A unit goes from memory to LDS without registers, 16 bytes a lane at consecutive places: place
@@ -435,6 +460,15 @@ struct GdrBuf {
     }
 };
 
+// 64 lanes' 16 bytes from memory straight into 1024 consecutive bytes of LDS, a lane's offset and the wave's.
+struct GdrSource {
+    __amdgpu_buffer_rsrc_t r;
+    __device__ __forceinline__ explicit GdrSource(const void* p) : r(__builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, -1, kBufDword3)) {}
+    __device__ __forceinline__ void to_lds(gu4* lds, unsigned lane, unsigned wave) const {
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, lds, 16, lane, wave, 0, 0);
+    }
+};
+
 // Where a head's keys or queries lie. AL: rows start on 16 bytes, hold whole accesses of 16 bytes, and 64 of them
 // lie within 32-bit offsets.
 template <typename T, int KD, bool AL>
@@ -452,15 +486,24 @@ struct GdrRows {
         if constexpr (AL) {
             constexpr int H = sizeof(T) / 2, U = 4 * KD * H;          // units of 16 bytes a lane
             const int lane = threadIdx.x & 63, w = gdr_wave(), m = lane >> 2, g = (lane & 3) ^ (m >> 1 & 3);
-            const auto rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(at), 0, -1, kBufDword3);
+            const GdrSource from(at);
             const unsigned row_bytes = (unsigned)stride * (unsigned)sizeof(T), lo = 8 * g * (unsigned)sizeof(T);
+            if (last == 63) {
 #pragma unroll
-            for (int e = 0; e < U / 4; ++e) {
-                const int u = e * 4 + w, h = u % H, s = u / H % KD, row = 16 * (u / H / KD) + m;
-                const unsigned off = (row < last ? row : last) * row_bytes + lo;
-                if (32 * s + 8 * g < dk)
-                    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (gu4*)(tiles + u * (1024 / sizeof(T))), 16, off,
-                                                             (32 * s + 4 * h) * (unsigned)sizeof(T), 0, 0);
+                for (int e = 0; e < U / 4; ++e) {
+                    const int u = e * 4 + w, h = u % H, s = u / H % KD;
+                    if (32 * s + 8 * g < dk)
+                        from.to_lds(reinterpret_cast<gu4*>(tiles + u * (1024 / sizeof(T))), m * row_bytes + lo,
+                                    16 * (u / H / KD) * row_bytes + (32 * s + 4 * h) * (unsigned)sizeof(T));
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < U / 4; ++e) {
+                    const int u = e * 4 + w, h = u % H, s = u / H % KD, row = 16 * (u / H / KD) + m;
+                    if (32 * s + 8 * g < dk)
+                        from.to_lds(reinterpret_cast<gu4*>(tiles + u * (1024 / sizeof(T))), (row < last ? row : last) * row_bytes + lo,
+                                    (32 * s + 4 * h) * (unsigned)sizeof(T));
+                }
             }
         } else {
             for (int e = threadIdx.x; e < 64 * KD * 32; e += 256) {
@@ -477,7 +520,8 @@ struct GdrRows {
 };
 
 // What k_gdr_solve leaves of a chunk's tokens: rows of 64 floats.
-//   a1 e^G / |k|, a2 e^G, a3 beta e^(G_last - G) / |k|, bk beta / |k|, misc { e^G_last, whether no factor is 0 },
+//   a1 e^G / |k|, a2 e^G, a3 beta e^(G_last - G) / |k|, bk beta / |k|, misc { e^G_last, whether no factor is 0,
+//   G_last in powers of two, whether every beta is in [0, 2] },
 //   G itself, times log2 e, in 64 bits (two rows)
 enum GdrTok { tA1, tA2, tA3, tBk, tMisc, tG, kGdrTok = 7 };
 
@@ -577,7 +621,8 @@ k_gdr_solve(const LaunchGdr p) {
         tok[tA3 * 64] = a3 * bk;
         tok[tBk * 64] = bk;
         const bool clean = __all(a1 != 0.0f && e != 0.0f);
-        tok[tMisc * 64] = lane == 0 ? __builtin_amdgcn_exp2f((float)Gl) : clean ? 1.0f : 0.0f;
+        const bool tame = __all(beta >= 0.0f && beta <= 2.0f);
+        tok[tMisc * 64] = lane == 0 ? __builtin_amdgcn_exp2f((float)Gl) : lane == 2 ? (float)Gl : (lane == 1 ? clean : tame) ? 1.0f : 0.0f;
         *reinterpret_cast<double*>(p.co + id * (kGdrTok * 64) + tG * 64 + 2 * lane) = G;
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -682,13 +727,14 @@ template <typename T, int DKP, bool TWO, bool AL>
 struct GdrWalk {
     using M = Mx<T>;
     static constexpr int KD = DKP / 32, ND = DKP / 16, TP = 3072;
+    static constexpr bool kTwo = TWO;
     const LaunchGdr& p;
     GdrRows<T, KD, AL> rk, rq;
     T *tq, *tt, *tp;
     float *tok, *srq;
     int64_t b, bh, nc;
     int h, lane, w, g, m, col, place;
-    bool in;
+    bool in, from_v = true;
     const T* vb;
     T* yb;
     gf4 S[ND];
@@ -701,18 +747,38 @@ struct GdrWalk {
           vb(static_cast<const T*>(a.v.p) + b_ * a.v.batch_stride + h_ * a.v.head_stride),
           yb(static_cast<T*>(a.y) + (b_ * a.L * a.H + h_) * a.dv) {}
 
+    // this wave's columns of a state [dk, n]; zeros where there is none
+    __device__ __forceinline__ void load_state(const float* from, int n) {
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = 32 * (d >> 1) + 8 * g + 4 * (d & 1) + r;
+                S[d][r] = from && row < p.dk && in ? from[row * n + col] : 0.0f;
+            }
+    }
+    __device__ __forceinline__ void store_state(float* to, int n) const {
+        if (in)
+#pragma unroll
+            for (int d = 0; d < ND; ++d)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int row = 32 * (d >> 1) + 8 * g + 4 * (d & 1) + r;
+                    if (row < p.dk) to[row * n + col] = S[d][r];
+                }
+    }
+    template <bool OUT>
     __device__ __forceinline__ void rest(int64_t n) const {       // queries, T, factors of chunk n
-        rq.load(tq, n * kGdrC, p.L);
+        if (OUT) rq.load(tq, n * kGdrC, p.L);
         const int64_t id = bh * nc + n;
-        const auto rt = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<T*>(p.wT) + id * (M::NT * TP), 0, -1, kBufDword3);
+        const GdrSource from(reinterpret_cast<T*>(p.wT) + id * (M::NT * TP)), tokens(p.co + id * (kGdrTok * 64));
         constexpr int U = M::NT * TP * (int)sizeof(T) / 1024;
 #pragma unroll
         for (int e = 0; e < (U + 3) / 4; ++e) {
             const int u = e * 4 + w;
-            if (u < U) __builtin_amdgcn_raw_ptr_buffer_load_lds(rt, (gu4*)(tt + u * (1024 / sizeof(T))), 16, lane * 16, u * 1024, 0, 0);
+            if (u < U) from.to_lds(reinterpret_cast<gu4*>(tt + u * (1024 / sizeof(T))), lane * 16, u * 1024);
         }
-        const auto rc = __builtin_amdgcn_make_buffer_rsrc(p.co + id * (kGdrTok * 64), 0, -1, kBufDword3);
-        if (w * 64 + lane < kGdrTok * 16) __builtin_amdgcn_raw_ptr_buffer_load_lds(rc, (gu4*)(tok + w * 256), 16, lane * 16, w * 1024, 0, 0);
+        if (w * 64 + lane < kGdrTok * 16) tokens.to_lds(reinterpret_cast<gu4*>(tok + w * 256), lane * 16, w * 1024);
     }
     // rows past the last token as copies of it, as the keys'
     __device__ __forceinline__ void values(int64_t n) {
@@ -720,23 +786,29 @@ struct GdrWalk {
         const T* at = vb + t0 * p.v.token_stride;
         const int c = in ? col : p.dv - 1, last = p.L - t0 < kGdrC ? (int)(p.L - t0) - 1 : kGdrC - 1;
         const GdrBuf<T> buf(at);
-        const unsigned row = (unsigned)p.v.token_stride * (unsigned)sizeof(T);
+        unsigned row = (unsigned)p.v.token_stride * (unsigned)sizeof(T);
+        if (AL && last == kGdrC - 1) {
+            const unsigned lo = 4 * g * row + c * (unsigned)sizeof(T);
+            asm volatile("" : "+s"(row));
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 16; ++i) v[i] = buf.ld(lo, (16 * (i >> 2) + (i & 3)) * row);
+        } else {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int t = 16 * i + 4 * g + r, u = t < last ? t : last;
-                if constexpr (AL) v[4 * i + r] = buf.ld(u * row + c * (unsigned)sizeof(T), 0);
-                else v[4 * i + r] = at[u * p.v.token_stride + c];
+            for (int i = 0; i < 16; ++i) {
+                const int t = 16 * (i >> 2) + 4 * g + (i & 3), u = t < last ? t : last;
+                if constexpr (AL) v[i] = buf.ld(u * row + c * (unsigned)sizeof(T), 0);
+                else v[i] = at[u * p.v.token_stride + c];
             }
+        }
     }
 
-    // one chunk; keys in `tk`, the next chunk's on their way to `tn`
+    // one chunk; keys in `tk`, the next chunk's on their way to `tn`. OUT: with outputs, else the state alone
+    template <bool OUT>
     __device__ __forceinline__ void chunk(int64_t n, int64_t end_n, T* tk, T* tn) {
         const int64_t t0 = n * kGdrC;
         gdr_arrived();
         if (TWO && n + 1 < end_n) rk.load(tn, t0 + kGdrC, p.L);
-        if (p.ckpt) {
+        if (OUT && p.ckpt) {
             const GdrBuf<float> ck(p.ckpt + (bh * nc + n) * p.dk * p.dv);
             unsigned dvb = p.dv * 4;
             asm volatile("" : "+s"(dvb));             // offsets made where they are used, not kept over the loop
@@ -755,36 +827,40 @@ struct GdrWalk {
         // the products of these.
         gf4 ks[4] = {}, qs[4] = {}, pt[4] = {}, len = {0, 0, 0, 0};
         {
-            typename M::F f[2][9];
-            auto read = [&](int s, typename M::F (&x)[9]) {
+            typename M::F f[2][8];
+            auto read = [&](int s, typename M::F (&x)[8]) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) x[i] = gdr_rows_frag<T>(tk, i * KD + s, place);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) x[4 + i] = gdr_rows_frag<T>(tq, i * KD + s, place);
-                x[8] = gdr_rows_frag<T>(tq, w * KD + s, place);
+                for (int i = 0; i < 4; ++i)
+                    if (OUT) x[4 + i] = gdr_rows_frag<T>(tq, i * KD + s, place);
             };
             read(0, f[0]);
 #pragma unroll
             for (int s = 0; s < KD; ++s) {
+                typename M::F own;
+                if (OUT) own = gdr_rows_frag<T>(tq, w * KD + s, place);
                 if (s + 1 < KD) read(s + 1, f[(s + 1) & 1]);
                 __builtin_amdgcn_sched_barrier(0);
                 auto& x = f[s & 1];
                 const auto sb = M::template split<3>(gdr_pair(S[2 * s], S[2 * s + 1]));
+                if (OUT) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) pt[i] = M::mm(x[i], x[8], pt[i]);
-                len = M::mm(x[8], x[8], len);
+                    for (int i = 0; i < 4; ++i) pt[i] = M::mm(x[i], own, pt[i]);
+                    len = M::mm(own, own, len);
+                }
 #pragma unroll
                 for (int k = sizeof(T) == 2 ? 2 : 0; k >= 0; --k) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) ks[i] = M::mm(x[i], sb.t[k], ks[i]);
-                    if (k < 2)
+                    if (OUT && k < 2)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) qs[i] = M::mm(sb.t[k], x[4 + i], qs[i]);
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
-        {
+        if constexpr (OUT) {
             const double* G = reinterpret_cast<const double*>(tok + tG * 64);
             const double gi = G[16 * w + m];
 #pragma unroll
@@ -798,11 +874,14 @@ struct GdrWalk {
                 }
                 const int unit = w < 2 ? w : 2 * w - 2 + (i >> 1);
                 if constexpr (sizeof(T) == 2) {
-                    typedef __bf16 gb4 __attribute__((ext_vector_type(4)));
-                    const gb4 a = __builtin_convertvector(pt[i], gb4), c = __builtin_convertvector(pt[i] - __builtin_convertvector(a, gf4), gb4);
+                    const auto both = M::template split<M::NP>(gdr_pair(pt[i], gf4{0, 0, 0, 0}));
                     T* at = tp + (unit * 64 + lane) * 8 + 4 * (i & 1);
-                    *reinterpret_cast<gb4*>(at) = a;
-                    *reinterpret_cast<gb4*>(at + TP) = c;
+#pragma unroll
+                    for (int k = 0; k < M::NP; ++k) {
+                        typedef uint32_t gu2 __attribute__((ext_vector_type(2)));
+                        const gu4 u = __builtin_bit_cast(gu4, both.t[k]);
+                        *reinterpret_cast<gu2*>(at + k * TP) = gu2{u[0], u[1]};
+                    }
                 } else {
                     *reinterpret_cast<gf4*>(tp + ((unit * 2 + (i & 1)) * 64 + lane) * 4) = pt[i];
                 }
@@ -823,12 +902,12 @@ struct GdrWalk {
             for (int r = 0; r < 4; ++r) V[i][r] = IO<T>::cvt(v[4 * i + r]);
             if (clean) {
                 V[i] -= a1 * ks[i];
-                qs[i] *= a2;
+                if (OUT) qs[i] *= a2;
             } else {
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     V[i][r] -= a1[r] != 0.0f ? a1[r] * ks[i][r] : 0.0f;
-                    qs[i][r] = a2 != 0.0f ? a2 * qs[i][r] : 0.0f;
+                    if (OUT) qs[i][r] = a2 != 0.0f ? a2 * qs[i][r] : 0.0f;
                 }
             }
         }
@@ -846,9 +925,10 @@ struct GdrWalk {
         }
         __syncthreads();                              // P is there; queries, T and factors are used up
         if (n + 1 < end_n) {
-            rest(n + 1);
-            values(n + 1);
+            rest<OUT>(n + 1);
+            if (from_v) values(n + 1);
         }
+        if constexpr (OUT) {
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             const auto xb = M::template split<M::NP>(gdr_pair(X[2 * s], X[2 * s + 1]));
@@ -887,6 +967,7 @@ struct GdrWalk {
                         if (16 * i + 4 * g + r < left) xt.st(X[i][r], (4 * g * row + col) * 4, (16 * i + r) * row * 4);
             }
         }
+        }
         // the next state
         {
             constexpr int NB = 2 * ND / 4;            // batches of four tiles, tokens' first half, then the second
@@ -919,52 +1000,171 @@ struct GdrWalk {
     }
 };
 
+// The chunks [n0, n1) of one head and 64 columns, from the state in k.S on.
+template <bool OUT, typename W, typename T>
+__device__ __forceinline__ void gdr_walk(W& k, int64_t n0, int64_t n1, T* k0, T* k1) {
+    k.rk.load(k0, n0 * kGdrC, k.p.L);
+    k.template rest<OUT>(n0);
+    if (k.from_v) k.values(n0);
+    if constexpr (W::kTwo) {
+        for (int64_t n = n0; n < n1; n += 2) {
+            k.template chunk<OUT>(n, n1, k0, k1);
+            if (n + 1 < n1) k.template chunk<OUT>(n + 1, n1, k1, k0);
+        }
+    } else {
+        for (int64_t n = n0; n < n1; ++n) k.template chunk<OUT>(n, n1, k0, k0);
+    }
+}
+
+// LDS columns past dk, which no load writes.
+template <int N, typename T>
+__device__ __forceinline__ void gdr_clear(T* lds) {
+    for (int e = threadIdx.x; e < N; e += 256) lds[e] = T(0);
+}
+
 template <typename T, int DKP, bool TWO, bool AL, int GROUPS>
 __global__ void __launch_bounds__(256, GROUPS)
 k_gdr_walk(const LaunchGdr p) {
     using W = GdrWalk<T, DKP, TWO, AL>;
     __shared__ alignas(16) T k0[64 * DKP], k1[TWO ? 64 * DKP : 8], tq[64 * DKP], tt[Mx<T>::NT * 3072], tp[Mx<T>::NP * 3072];
     __shared__ alignas(16) float tok[kGdrTok * 64], srq[64];
-    const int tid = threadIdx.x, lane = tid & 63, w = gdr_wave(), g = lane >> 4, m = lane & 15;
-    const int64_t BH = p.B * p.H, bh = blockIdx.x % BH, b = bh / p.H, nc = p.nchunks;
-    const int h = (int)(bh % p.H), hk = h / (p.H / p.Hk), col = (int)(blockIdx.x / BH) * 64 + w * 16 + m;
+    const int64_t BH = p.B * p.H, rest = blockIdx.x / BH, bh = blockIdx.x % BH, b = bh / p.H, nc = p.nchunks;
+    const int tiles = (p.dv + 63) / 64, seg = (int)(rest / tiles);
+    const int h = (int)(bh % p.H), hk = h / (p.H / p.Hk), col = (int)(rest % tiles) * 64 + gdr_wave() * 16 + (threadIdx.x & 15);
     W k(p, tq, tt, tp, tok, srq, b, bh, h, hk, col);
-    float* st = p.state ? p.state + bh * p.dk * p.dv : nullptr;
-#pragma unroll
-    for (int d = 0; d < W::ND; ++d)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int row = 32 * (d >> 1) + 8 * g + 4 * (d & 1) + r;
-            k.S[d][r] = st && row < p.dk && k.in ? st[row * p.dv + col] : 0.0f;
-        }
-    // what no load writes: columns past dk, the halves of blocks above P's diagonal
-    for (int e = tid; e < 64 * DKP; e += 256) {
-        k0[e] = T(0);
-        tq[e] = T(0);
-        if (TWO) k1[e] = T(0);
-    }
-    for (int e = tid; e < Mx<T>::NP * 3072; e += 256) tp[e] = T(0);
+    const int64_t kv = (int64_t)p.dk * p.dv, n0 = seg * p.seg, n1 = n0 + p.seg < nc ? n0 + p.seg : nc;
+    k.load_state(seg ? p.wE + ((seg - 1) * BH + bh) * kv : p.state ? p.state + bh * kv : nullptr, p.dv);
+    gdr_clear<64 * DKP>(k0);
+    gdr_clear<64 * DKP>(tq);
+    if (TWO) gdr_clear<64 * DKP>(k1);
+    gdr_clear<Mx<T>::NP * 3072>(tp);                  // the halves of blocks above P's diagonal, too
     __syncthreads();
-    k.rk.load(k0, 0, p.L);
-    k.rest(0);
-    k.values(0);
-    if constexpr (TWO) {
-        for (int64_t n = 0; n < nc; n += 2) {
-            k.chunk(n, nc, k0, k1);
-            if (n + 1 < nc) k.chunk(n + 1, nc, k1, k0);
+    gdr_walk<true>(k, n0, n1, k0, k1);
+    if (p.state && n1 == nc) k.store_state(p.state + bh * kv, p.dv);
+}
+
+// The last chunk of [n0, n1) from which on the decay to n1 is below 2^-48, n0 if there is none; `gone` says whether
+// there is one. With keys of length 1 at most and beta in [0, 2] no state grows on the way, so that what was in front
+// of that chunk is below 2^-48 of its own size at n1: not a bit of an fp32 state. (Any other key or beta on the way: n0.)
+__device__ __forceinline__ int64_t gdr_reach(const LaunchGdr& p, int64_t bh, int64_t n0, int64_t n1, bool& gone) {
+    const int lane = threadIdx.x & 63;
+    gone = false;
+    if (!(p.eps > 0.0f)) return n0;
+    float sum = 0.0f;
+    for (int64_t top = n1; top > n0; top -= 64) {
+        const int64_t n = top - 1 - lane;
+        float g = 0.0f;
+        bool tame = true;
+        if (n >= n0) {
+            const float* misc = p.co + (bh * p.nchunks + n) * (kGdrTok * 64) + tMisc * 64;
+            g = misc[2];
+            tame = misc[3] != 0.0f;
         }
-    } else {
-        for (int64_t n = 0; n < nc; ++n) k.chunk(n, nc, k0, k0);
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const float u = __shfl_up(g, o, 64);
+            if (lane >= o) g += u;
+        }
+        const uint64_t low = __ballot(n >= n0 && sum + g < -48.0f), wild = __ballot(!tame);
+        const int at = low ? __builtin_ctzll(low) : 64, bad = wild ? __builtin_ctzll(wild) : 64;
+        if (bad <= at && bad < 64) return n0;
+        if (at < 64) {
+            gone = true;
+            return top - 1 - at;
+        }
+        sum += __shfl(g, 63, 64);
     }
-    if (st && k.in)
+    return n0;
+}
+
+// A long sequence in few heads, cut into segments that run at the same time. First the state behind each segment, from
+// nothing in front of it (or, the first, from the caller's) and from where it still matters on; and, as dk columns more that
+// start as the identity and get no values, what the segment makes of the state in front of it, where anything is
+// left of that. k_gdr_join puts the ends together.
+template <typename T, int DKP, bool TWO, bool AL, int GROUPS>
+__global__ void __launch_bounds__(256, GROUPS)
+k_gdr_ends(const LaunchGdr p) {
+    using W = GdrWalk<T, DKP, TWO, AL>;
+    __shared__ alignas(16) T k0[64 * DKP], k1[TWO ? 64 * DKP : 8], tt[Mx<T>::NT * 3072];
+    __shared__ alignas(16) float tok[kGdrTok * 64];
+    const int64_t BH = p.B * p.H, rest = blockIdx.x / BH, bh = blockIdx.x % BH, b = bh / p.H, kv = (int64_t)p.dk * p.dv;
+    const int tv = (p.dv + 63) / 64, tiles = tv + (p.dk + 63) / 64, seg = (int)(rest / tiles), tile = (int)(rest % tiles);
+    const int h = (int)(bh % p.H), hk = h / (p.H / p.Hk), wave = gdr_wave(), lane = threadIdx.x & 63;
+    const bool map = tile >= tv;
+    const int col = (map ? tile - tv : tile) * 64 + wave * 16 + (lane & 15);
+    const int64_t n1 = (seg + 1) * p.seg;
+    bool gone;
+    const int64_t reach = gdr_reach(p, bh, seg * p.seg, n1, gone);
+    const int64_t n0 = (int64_t)__builtin_amdgcn_readfirstlane((int)reach);
+    if (map) {
+        if (seg == 0) return;
+        if (tile == tv && threadIdx.x == 0) p.wF[seg * BH + bh] = gone ? 0.0f : 1.0f;
+        if (gone) return;
+    }
+    W k(p, nullptr, tt, nullptr, tok, nullptr, b, bh, h, hk, col);
+    if (map) {
+        k.from_v = false;
+        k.in = col < p.dk;
 #pragma unroll
         for (int d = 0; d < W::ND; ++d)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = 32 * (d >> 1) + 8 * g + 4 * (d & 1) + r;
-                if (row < p.dk) st[row * p.dv + col] = k.S[d][r];
-            }
+            for (int r = 0; r < 4; ++r) k.S[d][r] = 32 * (d >> 1) + 8 * k.g + 4 * (d & 1) + r == col ? 1.0f : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) k.v[i] = T(0);
+    } else {
+        k.load_state(seg == 0 && n0 == 0 && p.state ? p.state + bh * kv : nullptr, p.dv);
+    }
+    gdr_clear<64 * DKP>(k0);
+    if (TWO) gdr_clear<64 * DKP>(k1);
+    __syncthreads();
+    gdr_walk<false>(k, n0, n1, k0, k1);
+    if (map) k.store_state(p.wM + (seg * BH + bh) * (int64_t)p.dk * p.dk, p.dk);
+    else k.store_state(p.wE + (seg * BH + bh) * kv, p.dv);
 }
+
+// The states between segments, one after the other: E_s <- M_s E_(s-1) + E_s, where M_s is there. Waves as in the walk.
+template <typename T, int DKP>
+__global__ void __launch_bounds__(256)
+k_gdr_join(const LaunchGdr p) {
+    using M = Mx<T>;
+    using W = GdrWalk<T, DKP, false, false>;
+    const int64_t BH = p.B * p.H, bh = blockIdx.x % BH, kv = (int64_t)p.dk * p.dv;
+    const int lane = threadIdx.x & 63, col = (int)(blockIdx.x / BH) * 64 + gdr_wave() * 16 + (lane & 15), g = lane >> 4, m = lane & 15;
+    W k(p, nullptr, nullptr, nullptr, nullptr, nullptr, 0, bh, 0, 0, col);
+    k.load_state(p.wE + bh * kv, p.dv);
+    const int64_t kk = (int64_t)p.dk * p.dk;
+    const bool vec = p.dk % 4 == 0;
+    gf8 x[2][W::ND];                                  // the map's rows of this lane, 32 columns ahead
+    auto read = [&](const float* map, int s, gf8 (&to)[W::ND]) {
+#pragma unroll
+        for (int d = 0; d < W::ND; ++d) {
+            const int row = 32 * (d >> 1) + 8 * (m >> 2) + 4 * (d & 1) + (m & 3);
+            to[d] = gdr_ld8(map + (int64_t)row * p.dk, 32 * s + 8 * g, p.dk, row < p.dk, vec);
+        }
+    };
+    for (int seg = 1; seg < p.nseg - 1; ++seg) {
+        float* end = p.wE + (seg * BH + bh) * kv;
+        if (p.wF[seg * BH + bh] == 0.0f) {
+            k.load_state(end, p.dv);
+            continue;
+        }
+        const float* map = p.wM + (seg * BH + bh) * kk;
+        read(map, 0, x[0]);
+        typename M::template S<M::NT> sb[W::KD];
+#pragma unroll
+        for (int s = 0; s < W::KD; ++s) sb[s] = M::template split<M::NT>(gdr_pair(k.S[2 * s], k.S[2 * s + 1]));
+        k.load_state(end, p.dv);
+#pragma unroll
+        for (int s = 0; s < W::KD; ++s) {
+            if (s + 1 < W::KD) read(map, s + 1, x[(s + 1) & 1]);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int d = 0; d < W::ND; ++d) k.S[d] = M::mul(M::template split<M::NT>(x[s & 1][d]), sb[s], k.S[d]);
+        }
+        k.store_state(end, p.dv);
+    }
+}
+
 
 // ---------------------------------------------------------------------------
 // The backward from chunk to chunk, the last first, with W the gradient of the state behind a chunk in
@@ -1152,19 +1352,6 @@ k_gdr_walk_back(const LaunchGdr p) {
 //   sum_{i >= t > j} beta_j (E P + F N/beta)_ij + sum_{i >= t} (q . a2 dY S0^T - k . a1 dV S0^T)_i
 //     + sum_{j < t} beta_j (k . a3b X W^T)_j + e^G_last <S0, W>
 // A wave has a quarter of dk's columns; terms over dv go through LDS 32 at a time.
-// eight fp32 values of a row, zeros past its end
-__device__ __forceinline__ gf8 gdr_ld8(const float* row, int c, int n, bool there, bool vec) {
-    gf8 v = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (!there) return v;
-    if (vec && c + 8 <= n) {
-        const gf4 a = *reinterpret_cast<const gf4*>(row + c), b = *reinterpret_cast<const gf4*>(row + c + 4);
-        return gdr_pair(a, b);
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = c + j < n ? row[c + j] : 0.0f;
-    return v;
-}
-
 template <typename T, int DKP>
 __global__ void __launch_bounds__(256)
 k_gdr_grads(const LaunchGdr p) {
@@ -1540,10 +1727,18 @@ hipError_t launch_gdr_d(const LaunchGdr& p) {
     const unsigned tiles = (unsigned)(BH * ((p.dv + 63) / 64));
     if (p.pass == LaunchGdr::kFwd) {
         constexpr bool kTwo = DKP * sizeof(T) <= 512;       // keys twice in LDS
-        hipLaunchKernelGGL((k_gdr_solve<T, DKP>), dim3((chunks + 3) / 4), dim3(256), 0, st, p);
         constexpr int kGroups = DKP <= 128 && sizeof(T) == 2 ? 2 : 1;
-        if (p.vec && p.vec_v && p.vec_y) hipLaunchKernelGGL((k_gdr_walk<T, DKP, kTwo, true, kGroups>), dim3(tiles), dim3(256), 0, st, p);
-        else hipLaunchKernelGGL((k_gdr_walk<T, DKP, kTwo, false, kGroups>), dim3(tiles), dim3(256), 0, st, p);
+        hipLaunchKernelGGL((k_gdr_solve<T, DKP>), dim3((chunks + 3) / 4), dim3(256), 0, st, p);
+        const bool al = p.vec && p.vec_v && p.vec_y;
+        if (p.nseg > 1) {
+            const dim3 ends((unsigned)(BH * ((p.dv + 63) / 64 + (p.dk + 63) / 64) * (p.nseg - 1)));
+            if (al) hipLaunchKernelGGL((k_gdr_ends<T, DKP, kTwo, true, kGroups>), ends, dim3(256), 0, st, p);
+            else hipLaunchKernelGGL((k_gdr_ends<T, DKP, kTwo, false, kGroups>), ends, dim3(256), 0, st, p);
+            if (p.nseg > 2) hipLaunchKernelGGL((k_gdr_join<T, DKP>), dim3(tiles), dim3(256), 0, st, p);
+        }
+        const dim3 walk((unsigned)(tiles * p.nseg));
+        if (al) hipLaunchKernelGGL((k_gdr_walk<T, DKP, kTwo, true, kGroups>), walk, dim3(256), 0, st, p);
+        else hipLaunchKernelGGL((k_gdr_walk<T, DKP, kTwo, false, kGroups>), walk, dim3(256), 0, st, p);
     } else {
         hipLaunchKernelGGL((k_gdr_prep<T, DKP, true>), dim3(chunks), dim3(256), 0, st, p);
         hipLaunchKernelGGL((k_gdr_walk_back<T, DKP, 1>), dim3(tiles), dim3(256), 0, st, p);

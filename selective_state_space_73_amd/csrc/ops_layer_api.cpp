@@ -9,6 +9,18 @@
 #include "ops_check.h"
 #include "ops_layer_internal.h"
 
+namespace selscan {
+
+int64_t gdr_segment(int64_t BH, int64_t dv, int64_t nchunks) {
+    const int64_t groups = BH * ((dv + 63) / 64);           // workgroups of one segment
+    const int64_t n = 512 / groups;                         // segments that run at the same time, two workgroups a CU
+    if (n < 2 || nchunks < 8) return nchunks;
+    const int64_t seg = (nchunks + n - 1) / n;
+    return seg < 4 ? 4 : seg;
+}
+
+}  // namespace selscan
+
 namespace {
 
 // ---------------------------------------------------------------------------
@@ -46,7 +58,7 @@ size_t ckpt_floats(const ss_gdr_dims& d) { return ckpt_states(d) + (size_t)d.bat
 // Per chunk and head: the tokens' factors, the inverse and P (6 blocks of 16 x 32 each). The backward
 // as well: the pairs of tokens, the state's gradient behind every chunk; the gradients of v in fp32, and those
 // of q and k by head of v.
-struct GdrLayout { size_t co, wT, wP, raw, wS, wV, pq, pk, total; };
+struct GdrLayout { size_t co, wT, wP, raw, wS, wV, pq, pk, wE, wM, wF, total; int64_t seg, nseg; };
 GdrLayout gdr_layout(const ss_gdr_dims& d, bool backward) {
     GdrLayout l{};
     const size_t n = (size_t)d.batch * d.heads * (size_t)ceil_div(d.seqlen, SS_GDR_CHUNK);
@@ -55,8 +67,21 @@ GdrLayout gdr_layout(const ss_gdr_dims& d, bool backward) {
     auto take = [&](size_t& at, size_t floats) { at = off; off = align256(off + floats * 4); };
     take(l.co, n * 8 * 64);
     take(l.wT, n * 9216);
-    take(l.wP, n * 6 * 512);
+    l.seg = ceil_div(d.seqlen, SS_GDR_CHUNK);
+    l.nseg = 1;
+    if (!backward) {
+        const int64_t chunks = l.seg;
+        l.seg = selscan::gdr_segment(d.batch * d.heads, d.dv, chunks);
+        l.nseg = ceil_div(chunks, l.seg > 0 ? l.seg : 1);
+        if (l.nseg > 1) {
+            const size_t ends = (size_t)(l.nseg - 1) * d.batch * d.heads;
+            take(l.wE, ends * d.dk * d.dv);
+            take(l.wM, ends * d.dk * d.dk);
+            take(l.wF, ends);
+        }
+    }
     if (backward) {
+        take(l.wP, n * 6 * 512);
         take(l.raw, n * 30 * 256);
         take(l.wS, n * d.dk * d.dv);
         take(l.wV, rows * d.dv);
@@ -137,8 +162,12 @@ ss_status check_gdr_args(const ss_gdr_dims& d, const ss_gdr_args* a, GdrCall cal
 void gdr_attach(selscan::LaunchGdr& p, const ss_gdr_dims& d, const GdrLayout& l, void* workspace, bool backward) {
     char* ws = static_cast<char*>(workspace);
     auto at = [&](size_t off) { return reinterpret_cast<float*>(ws + off); };
-    p.co = at(l.co); p.wT = at(l.wT); p.wP = at(l.wP);
+    p.co = at(l.co); p.wT = at(l.wT);
+    p.seg = l.seg;
+    p.nseg = (int)l.nseg;
+    p.wE = at(l.wE); p.wM = at(l.wM); p.wF = at(l.wF);
     if (backward) {
+        p.wP = at(l.wP);
         p.raw = at(l.raw); p.wS = at(l.wS); p.wV = at(l.wV);
         p.part_q = at(l.pq); p.part_k = at(l.pk);
     }

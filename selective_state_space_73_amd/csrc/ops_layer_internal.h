@@ -25,12 +25,19 @@ struct LaunchGdr {
     float* ckptX;                // [B, L, H, dv] solutions x_t
     ss_gdr_grads gr;
     // workspace
+    int64_t seg;                 // chunks of a segment of the forward (all of them: one segment)
+    int nseg;
+    float *wE, *wM, *wF;         // several segments: [nseg - 1, B, H, dk, dv] states behind the segments, [nseg - 1, B, H, dk, dk]
+                                 // what they make of the state in front, [nseg - 1, B, H] whether anything of it is left
     float *co, *wT, *wP;         // [B, H, chunks]: factors of tokens, inverse and P in the order of operands
     float* raw;                  // the backward: [B, H, chunks, 3, 10, 256] pairs of tokens, the triangle's ten tiles of 16 x 16
     float *wS, *wV;              // the backward: [B, H, chunks, dk, dv] adjoints behind the chunks, [B, L, H, dv] gradients of v
     float *part_q, *part_k;      // the backward: [B, L, H, dk] each head's share
     void* stream;
 };
+// Chunks of a segment. One after the other a chunk takes about as long as any work of its 64 columns; with segments the
+// states are made twice.
+int64_t gdr_segment(int64_t BH, int64_t dv, int64_t nchunks);
 hipError_t launch_gdr_bf16(const LaunchGdr& p);
 hipError_t launch_gdr_f32(const LaunchGdr& p);
 inline hipError_t launch_gdr(const LaunchGdr& p) { return p.bf16 ? launch_gdr_bf16(p) : launch_gdr_f32(p); }
