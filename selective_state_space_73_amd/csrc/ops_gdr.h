@@ -102,20 +102,6 @@ template <> struct Mx<uint16_t> {
         c = mm(a.t[0], b.t[1], c);
         return mm(a.t[0], b.t[0], c);
     }
-    // The transposed operand from tiles that lie for the other one: row d0 + m of A, from tokens' rows of
-    // [tile][kd][lane][8]; tokens of the tiles 2 s and 2 s + 1 are the terms.
-    template <int KD>
-    static __device__ __forceinline__ F ldt(const uint16_t* tiles, int s, int dt, int lane) {
-        const int g = lane >> 4, i = lane & 15;
-        gs4 a[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint16_t* p = tiles + (((2 * s + h) * KD + (dt >> 1)) * 64 + (i & 3) * 16 + 4 * g + (i >> 2)) * 8 + (dt & 1) * 4;
-            a[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((gs4 __attribute__((address_space(3)))*)p);
-        }
-        typedef short gs8 __attribute__((ext_vector_type(8)));
-        return __builtin_bit_cast(gb8, gs8{a[0][0], a[0][1], a[0][2], a[0][3], a[1][0], a[1][1], a[1][2], a[1][3]});
-    }
 };
 
 template <> struct Mx<float> {
@@ -138,15 +124,6 @@ template <> struct Mx<float> {
     static __device__ __forceinline__ gf4 mul(const S<N>& a, const F& b, gf4 c) { return mm(a.t[0], b, c); }
     template <int N>
     static __device__ __forceinline__ gf4 mul(const S<N>& a, const S<N>& b, gf4 c) { return mm(a.t[0], b.t[0], c); }
-    template <int KD>
-    static __device__ __forceinline__ F ldt(const float* tiles, int s, int dt, int lane) {
-        const int g = lane >> 4, i = lane & 15;
-        F a;
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            a[j] = tiles[(((2 * s + (j >> 2)) * KD + (dt >> 1)) * 64 + (i >> 2) * 16 + 4 * g + (j & 3)) * 8 + (dt & 1) * 4 + (i & 3)];
-        return a;
-    }
 };
 
 __device__ __forceinline__ gf8 gdr_pair(gf4 a, gf4 b) { return gf8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}; }
@@ -177,196 +154,6 @@ __device__ __forceinline__ void gdr_row8(const T* row, int d, int dk, bool vec, 
 
 template <typename T>
 __device__ __forceinline__ float gdr_f(T v) { return IO<T>::ld(&v); }
-
-// 64 rows of one head from token t0 on, in the order of A operands. KD = padded width / 32.
-template <typename T, int KD, int NTH = 256>
-__device__ __forceinline__ void gdr_stage(T* tiles, const ss_head_view& v, int64_t b, int64_t t0, int64_t L, int head, int dk, bool vec) {
-    constexpr int PER = KD * 4;                      // accesses of eight values a row
-    const T* base = static_cast<const T*>(v.p) + b * v.batch_stride + head * v.head_stride;
-#pragma unroll
-    for (int it = 0; it < kGdrC * PER / NTH; ++it) {
-        const int id = it * NTH + threadIdx.x, t = id / PER, d = id % PER * 8;
-        alignas(16) T x[8];
-        gdr_row8<T>(base + (t0 + t) * v.token_stride, d, dk, vec, t0 + t < L, x);
-        const int g = d >> 2 & 3, h = d >> 4 & 1;
-        T* at = tiles + (((t >> 4) * KD + (d >> 5)) * 64 + g * 16 + (t & 15)) * 8 + h * 4;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) { at[j] = x[j]; at[128 + j] = x[4 + j]; }
-    }
-}
-
-// Factors of a chunk's tokens that k_gdr_prep leaves, rows of 64 floats.
-enum GdrCo { kA1, kA2, kA3, kA3b, kBeta, kRq, kRk, kEnd, kGdrCo };
-// kA1 e^G / |k|;  kA2 scale e^G / |q|;  kA3b e^(G_last - G) / |k|;  kA3 = beta kA3b;  kEnd e^G_last (all 64)
-
-// ---------------------------------------------------------------------------
-// A chunk of one head: its factors, (1 + N)^-1 and P. Sums of g in 64 bits: a reset, or a decay of
-// any size, is a term of -200 at least (e^-200 is 0 in fp32), and the differences of what
-// follows keep their digits. The inverse: blocks of 16 on the diagonal row by row, one wave each, and
-// below them block by block, T_ij = -T_ii sum_l N_il T_lj, in fp32 products.
-// BACK: the transposed operands, and D / |k_j|, N / beta and P tile by tile as the results lie.
-template <typename T, int DKP, bool BACK>
-__global__ void __launch_bounds__(256)
-k_gdr_prep(const LaunchGdr p) {
-    constexpr int KD = DKP / 32, LD = 65;
-    constexpr int kTiles = 2 * 64 * DKP * (int)sizeof(T), kMats = 3 * 64 * LD * 4;
-    __shared__ alignas(16) char lds[kTiles > kMats ? kTiles : kMats];
-    __shared__ double sg[64];
-    __shared__ float sco[kGdrCo][64];
-    T *tk = reinterpret_cast<T*>(lds), *tq = tk + 64 * DKP;
-    float (*mn)[LD] = reinterpret_cast<float (*)[LD]>(lds), (*mt_)[LD] = mn + 64, (*mp)[LD] = mn + 128;
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, g = lane >> 4, m = lane & 15;
-    const int64_t id = blockIdx.x, nc = p.nchunks;
-    const int64_t n = id % nc, bh = id / nc, b = bh / p.H, t0 = n * kGdrC;
-    const int h = (int)(bh % p.H), hk = h / (p.H / p.Hk);
-
-    gdr_stage<T, KD>(tk, p.k, b, t0, p.L, hk, p.dk, p.vec);
-    gdr_stage<T, KD>(tq, p.q, b, t0, p.L, hk, p.dk, p.vec);
-    if (w == 0) {
-        const int64_t t = t0 + lane;
-        double G = 0.0;
-        float beta = 0.0f;
-        if (t < p.L) {
-            const int64_t at = (b * p.L + t) * p.H + h;
-            G = (double)p.g[at];
-            beta = p.beta[at];
-            if (G < -200.0 || (p.reset && p.reset[b * p.L + t])) G = -200.0;
-        }
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const double u = __shfl_up(G, o, 64);
-            if (lane >= o) G += u;
-        }
-        sg[lane] = G;
-        const double last = __shfl(G, 63, 64);
-        sco[kBeta][lane] = beta;
-        sco[kA1][lane] = expf((float)G);
-        sco[kA3b][lane] = expf((float)(last - G));
-        sco[kEnd][lane] = expf((float)last);
-    }
-    __syncthreads();
-    // lengths: wave 0 of k's rows, wave 1 of q's; a lane sums one row from LDS
-    if (w < 2) {
-        const T* tl = w ? tq : tk;
-        float r = 1.0f;
-        if (p.eps > 0.0f) {
-            float s = 0.0f;
-            for (int d = 0; d < KD; ++d)
-#pragma unroll
-                for (int gg = 0; gg < 4; ++gg)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float x = gdr_f<T>(tl[(((lane >> 4) * KD + d) * 64 + gg * 16 + (lane & 15)) * 8 + j]);
-                        s = __builtin_fmaf(x, x, s);
-                    }
-            r = 1.0f / sqrtf(s + p.eps);
-        }
-        sco[w ? kRq : kRk][lane] = r;
-    }
-    // products of keys, and of queries and keys, of the lower triangle's ten tiles
-    gf4 akk[3], aqk[3];
-#pragma unroll
-    for (int u = 0; u < 3; ++u) {
-        akk[u] = aqk[u] = gf4{0, 0, 0, 0};
-        const int tile = w + 4 * u;
-        if (tile < 10) {
-            const int mt = tile < 1 ? 0 : tile < 3 ? 1 : tile < 6 ? 2 : 3, nt = tile - mt * (mt + 1) / 2;
-#pragma unroll
-            for (int s = 0; s < KD; ++s) {
-                const auto kb = Mx<T>::ld(tk + ((nt * KD + s) * 64 + lane) * 8);
-                akk[u] = Mx<T>::mm(Mx<T>::ld(tk + ((mt * KD + s) * 64 + lane) * 8), kb, akk[u]);
-                aqk[u] = Mx<T>::mm(Mx<T>::ld(tq + ((mt * KD + s) * 64 + lane) * 8), kb, aqk[u]);
-            }
-        }
-    }
-    __syncthreads();
-    if (tid < 64) {
-        const float rk = sco[kRk][tid], rq = sco[kRq][tid], e = sco[kA1][tid];
-        sco[kA1][tid] = e * rk;
-        sco[kA2][tid] = e * rq * p.scale;
-        sco[kA3b][tid] *= rk;
-        sco[kA3][tid] = sco[kA3b][tid] * sco[kBeta][tid];
-    }
-    __syncthreads();
-    float* co = p.co + id * (kGdrCo * 64);
-    for (int e = tid; e < kGdrCo * 64; e += 256) co[e] = sco[e >> 6][e & 63];
-    // tiles of N / beta (no beta yet) and P to LDS; zeros on and above N's diagonal, above P's
-    for (int e = tid; e < 64 * 64; e += 256) {
-        const int i = e >> 6, j = e & 63;
-        if ((j >> 4) > (i >> 4)) mn[i][j] = mp[i][j] = mt_[i][j] = 0.0f;
-    }
-#pragma unroll
-    for (int u = 0; u < 3; ++u) {
-        const int tile = w + 4 * u;
-        if (tile < 10) {
-            const int mt = tile < 1 ? 0 : tile < 3 ? 1 : tile < 6 ? 2 : 3, nt = tile - mt * (mt + 1) / 2;
-            const int j = nt * 16 + m;
-            const float rk = sco[kRk][j];
-            gf4 vd, vn, vp;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int i = mt * 16 + 4 * g + r;
-                const float d = i >= j ? expf((float)(sg[i] - sg[j])) * rk : 0.0f;
-                // a factor of 0 is a decay to nothing: what it multiplies is left out, whatever it is
-                vd[r] = d;
-                mn[i][j] = vn[r] = i > j && d != 0.0f ? akk[u][r] * sco[kRk][i] * d : 0.0f;
-                mp[i][j] = vp[r] = i >= j && d != 0.0f ? aqk[u][r] * (sco[kRq][i] * p.scale) * d : 0.0f;
-            }
-            if constexpr (BACK) {
-                gf4* raw = reinterpret_cast<gf4*>(p.raw + (id * 30 + tile) * 256) + lane;
-                raw[0] = vd;
-                raw[640] = vn;
-                raw[1280] = vp;
-            }
-        }
-    }
-    __syncthreads();
-    // the inverse's diagonal blocks: lane m of wave w has column m of block w
-    if (lane < 16) {
-        float x[16];
-        const int o = w * 16;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            float s = i == lane ? 1.0f : 0.0f;
-#pragma unroll
-            for (int l = 0; l < i; ++l) s = __builtin_fmaf(-mn[o + i][o + l] * sco[kBeta][o + l], x[l], s);
-            x[i] = s;
-            mt_[o + i][o + lane] = s;
-        }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int lev = 1; lev < 4; ++lev) {
-        if (w + lev < 4) {
-            const int j = w, i = w + lev;
-            gf4 acc = {0, 0, 0, 0}, out = {0, 0, 0, 0};
-            for (int l = j; l < i; ++l)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int c = 16 * l + 4 * g + r;
-                    acc = __builtin_amdgcn_mfma_f32_16x16x4f32(mn[16 * i + m][c] * sco[kBeta][c], mt_[c][16 * j + m], acc, 0, 0, 0);
-                }
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                out = __builtin_amdgcn_mfma_f32_16x16x4f32(-mt_[16 * i + m][16 * i + 4 * g + r], acc[r], out, 0, 0, 0);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) mt_[16 * i + 4 * g + r][16 * j + m] = out[r];
-        }
-        __syncthreads();
-    }
-    // out, in the order of operands: T and P beta, or their transposes
-    float *ot = p.wT + id * (6 * 512), *op = p.wP + id * (6 * 512);
-    for (int e = tid; e < 6 * 512; e += 256) {
-        const int blk = e >> 9, l = e >> 3 & 63, j = e & 7;
-        int mt, s;
-        if constexpr (BACK) { mt = blk < 4 ? blk >> 1 : blk - 2; s = blk < 4 ? blk & 1 : 1; }
-        else { mt = blk < 2 ? blk : (blk + 2) >> 1; s = blk < 2 ? 0 : blk & 1; }
-        const int row = mt * 16 + (l & 15), col = s * 32 + (j >> 2) * 16 + 4 * (l >> 4) + (j & 3);
-        const int a = BACK ? col : row, c = BACK ? row : col;
-        ot[e] = mt_[a][c];
-        op[e] = mp[a][c] * sco[kBeta][c];
-    }
-}
 
 __device__ __forceinline__ void gdr_tile(int tile, int& mt, int& nt) {
     mt = tile < 1 ? 0 : tile < 3 ? 1 : tile < 6 ? 2 : 3;
@@ -523,7 +310,8 @@ struct GdrRows {
 //   a1 e^G / |k|, a2 e^G, a3 beta e^(G_last - G) / |k|, bk beta / |k|, misc { e^G_last, whether no factor is 0,
 //   G_last in powers of two, whether every beta is in [0, 2] },
 //   G itself, times log2 e, in 64 bits (two rows)
-enum GdrTok { tA1, tA2, tA3, tBk, tMisc, tG, kGdrTok = 7 };
+//   for the gradients as well: e^(G_last - G) / |k|, beta, 1 / |k|
+enum GdrTok { tA1, tA2, tA3, tBk, tMisc, tG, kGdrTok = 7, tA3b = 7, tBeta, tRk, kGdrTokAll };
 
 // Waits for this wave's transfers to LDS, then for the workgroup's.
 __device__ __forceinline__ void gdr_arrived() {
@@ -537,7 +325,8 @@ __device__ __forceinline__ void gdr_arrived() {
 // fp32), and the differences of what follows keep their digits. The inverse: blocks of 16 on the
 // diagonal row by row, below them block by block, T_ij = -T_ii sum_l N_il T_lj, in fp32 products
 // whose operands stay in registers.
-template <typename T, int DKP>
+// BACK: T transposed, which is how the results lie.
+template <typename T, int DKP, bool BACK>
 __global__ void __launch_bounds__(256)
 k_gdr_solve(const LaunchGdr p) {
     using M = Mx<T>;
@@ -614,16 +403,19 @@ k_gdr_solve(const LaunchGdr p) {
     const float rk = sv[w][0][lane], bk = rk * beta;
     sv[w][1][lane] = bk;
     {
-        float* tok = p.co + id * (kGdrTok * 64) + lane;
+        float* tok = p.co + id * (kGdrTokAll * 64) + lane;
         const float e = __builtin_amdgcn_exp2f((float)G), a3 = __builtin_amdgcn_exp2f((float)(Gl - G)), a1 = e * rk;
         tok[tA1 * 64] = a1;
         tok[tA2 * 64] = e;
         tok[tA3 * 64] = a3 * bk;
+        tok[tA3b * 64] = a3 * rk;
+        tok[tBeta * 64] = beta;
+        tok[tRk * 64] = rk;
         tok[tBk * 64] = bk;
         const bool clean = __all(a1 != 0.0f && e != 0.0f);
         const bool tame = __all(beta >= 0.0f && beta <= 2.0f);
         tok[tMisc * 64] = lane == 0 ? __builtin_amdgcn_exp2f((float)Gl) : lane == 2 ? (float)Gl : (lane == 1 ? clean : tame) ? 1.0f : 0.0f;
-        *reinterpret_cast<double*>(p.co + id * (kGdrTok * 64) + tG * 64 + 2 * lane) = G;
+        *reinterpret_cast<double*>(p.co + id * (kGdrTokAll * 64) + tG * 64 + 2 * lane) = G;
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     // N, row by row
@@ -690,32 +482,44 @@ k_gdr_solve(const LaunchGdr p) {
             for (int r = 0; r < 4; ++r) out = __builtin_amdgcn_mfma_f32_16x16x4f32(ti[i][r], acc[r], out, 0, 0, 0);
             tb[i * (i + 1) / 2 + j] = out;
         }
-    // to operands: through LDS, rows by lane
-#pragma unroll
-    for (int i = 1; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < i; ++j)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) mat[(16 * i + 4 * g + r) * LD + 16 * j + m] = tb[i * (i + 1) / 2 + j][r];
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     T* out = reinterpret_cast<T*>(p.wT) + id * (M::NT * 3072);
+    auto put = [&](int u, gf4 a, gf4 c) {
+        if constexpr (sizeof(T) == 2) {
+            const auto sp = M::template split<M::NT>(gdr_pair(a, c));
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int s = 0; s <= i >> 1; ++s) {
-            const gf4 a = *reinterpret_cast<const gf4*>(&mat[(16 * i + m) * LD + 32 * s + 4 * g]);
-            gf4 c = {0, 0, 0, 0};
-            if (2 * s + 1 <= i) c = *reinterpret_cast<const gf4*>(&mat[(16 * i + m) * LD + 32 * s + 16 + 4 * g]);
-            const int u = gdr_low(i, s);
-            if constexpr (sizeof(T) == 2) {
-                const auto sp = M::template split<M::NT>(gdr_pair(a, c));
-#pragma unroll
-                for (int k = 0; k < M::NT; ++k) *reinterpret_cast<gb8*>(out + k * 3072 + (u * 64 + lane) * 8) = sp.t[k];
-            } else {
-                *reinterpret_cast<gf4*>(out + (u * 128 + lane) * 4) = a;
-                *reinterpret_cast<gf4*>(out + (u * 128 + 64 + lane) * 4) = c;
-            }
+            for (int k = 0; k < M::NT; ++k) *reinterpret_cast<gb8*>(out + k * 3072 + (u * 64 + lane) * 8) = sp.t[k];
+        } else {
+            *reinterpret_cast<gf4*>(out + (u * 128 + lane) * 4) = a;
+            *reinterpret_cast<gf4*>(out + (u * 128 + 64 + lane) * 4) = c;
         }
+    };
+    if constexpr (BACK) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int s = j >> 1; s < 2; ++s) {
+                const int i = 2 * s;                  // row tiles i and i + 1 are the terms
+                put(gdr_up(j, s), i >= j ? tb[i * (i + 1) / 2 + j] : gf4{0, 0, 0, 0}, tb[(i + 1) * (i + 2) / 2 + j]);
+            }
+    } else {
+        // through LDS, rows by lane
+#pragma unroll
+        for (int i = 1; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < i; ++j)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) mat[(16 * i + 4 * g + r) * LD + 16 * j + m] = tb[i * (i + 1) / 2 + j][r];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int s = 0; s <= i >> 1; ++s) {
+                const gf4 a = *reinterpret_cast<const gf4*>(&mat[(16 * i + m) * LD + 32 * s + 4 * g]);
+                gf4 c = {0, 0, 0, 0};
+                if (2 * s + 1 <= i) c = *reinterpret_cast<const gf4*>(&mat[(16 * i + m) * LD + 32 * s + 16 + 4 * g]);
+                put(gdr_low(i, s), a, c);
+            }
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -771,7 +575,7 @@ struct GdrWalk {
     __device__ __forceinline__ void rest(int64_t n) const {       // queries, T, factors of chunk n
         if (OUT) rq.load(tq, n * kGdrC, p.L);
         const int64_t id = bh * nc + n;
-        const GdrSource from(reinterpret_cast<T*>(p.wT) + id * (M::NT * TP)), tokens(p.co + id * (kGdrTok * 64));
+        const GdrSource from(reinterpret_cast<T*>(p.wT) + id * (M::NT * TP)), tokens(p.co + id * (kGdrTokAll * 64));
         constexpr int U = M::NT * TP * (int)sizeof(T) / 1024;
 #pragma unroll
         for (int e = 0; e < (U + 3) / 4; ++e) {
@@ -1056,7 +860,7 @@ __device__ __forceinline__ int64_t gdr_reach(const LaunchGdr& p, int64_t bh, int
         float g = 0.0f;
         bool tame = true;
         if (n >= n0) {
-            const float* misc = p.co + (bh * p.nchunks + n) * (kGdrTok * 64) + tMisc * 64;
+            const float* misc = p.co + (bh * p.nchunks + n) * (kGdrTokAll * 64) + tMisc * 64;
             g = misc[2];
             tame = misc[3] != 0.0f;
         }
@@ -1171,173 +975,291 @@ k_gdr_join(const LaunchGdr p) {
 // registers as the forward has the state:
 //   dX = (P beta)^T dY + beta e^(G_last - G) K W,  dV = T^T dX,
 //   W' = e^G_last W + (scale e^G Q)^T dY - (e^G K)^T dV
-template <typename T, int DKP, int CT>
-__global__ void __launch_bounds__(256)
-k_gdr_walk_back(const LaunchGdr p) {
+// Keys and queries are needed to the end of a chunk and lie in LDS once, so that a CU holds two workgroups, of which
+// one waits for its next chunk while the other works.
+template <typename T, int DKP, bool AL>
+struct GdrWalkBack {
     using M = Mx<T>;
-    constexpr int KD = DKP / 32, ND = DKP / 16;
-    __shared__ alignas(16) T tk[64 * DKP], tq[64 * DKP];
-    __shared__ alignas(16) T tt[M::NT][6 * 512], tp[M::NT][6 * 512];
-    __shared__ alignas(16) float sco[kGdrCo][64];
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, g = lane >> 4, m = lane & 15;
-    const int64_t BH = p.B * p.H, bh = blockIdx.x % BH, b = bh / p.H, nc = p.nchunks;
-    const int h = (int)(bh % p.H), hk = h / (p.H / p.Hk);
-    const int col0 = ((int)(blockIdx.x / BH) * 4 + w) * (16 * CT) + m;
-    const T* dyb = static_cast<const T*>(p.gr.dy) + (b * p.L * p.H + h) * p.dv;
-    T* dvb = static_cast<T*>(p.gr.dv) + (b * p.L * p.H + h) * p.dv;
-    float* wvb = p.wV + (b * p.L * p.H + h) * p.dv;
+    static constexpr int KD = DKP / 32, ND = DKP / 16, TP = 3072;
+    const LaunchGdr& p;
+    GdrRows<T, KD, AL> rk, rq;
+    T *tk, *tq, *tt, *tp;
+    float *tok, *srq;
+    int64_t b, bh, nc;
+    int h, lane, w, g, m, col, place;
+    bool in;
+    gf4 S[ND];
+    T v[16];                                          // the next gradients of y, as they came
 
-    gf4 S[CT][ND];
-#pragma unroll
-    for (int c = 0; c < CT; ++c)
-#pragma unroll
-        for (int d = 0; d < ND; ++d)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = d * 16 + 4 * g + r, col = col0 + 16 * c;
-                S[c][d][r] = p.gr.dstate_final && row < p.dk && col < p.dv ? p.gr.dstate_final[(bh * p.dk + row) * p.dv + col] : 0.0f;
-            }
+    __device__ __forceinline__ GdrWalkBack(const LaunchGdr& a, T* k_, T* q_, T* t_, T* p_, float* tok_, float* srq_, int64_t b_, int64_t bh_,
+                                           int h_, int hk, int col_)
+        : p(a), rk(a.k, b_, hk, a.dk), rq(a.q, b_, hk, a.dk), tk(k_), tq(q_), tt(t_), tp(p_), tok(tok_), srq(srq_), b(b_), bh(bh_),
+          nc(a.nchunks), h(h_), lane(threadIdx.x & 63), w(gdr_wave()), g(lane >> 4), m(lane & 15), col(col_), place(gdr_place(g, m)),
+          in(col_ < a.dv) {}
 
-    for (int64_t n = nc - 1; n >= 0; --n) {
-        const int64_t t0 = n * kGdrC, id = bh * nc + n;
-        __syncthreads();
-        gdr_stage<T, KD>(tk, p.k, b, t0, p.L, hk, p.dk, p.vec);
-        gdr_stage<T, KD>(tq, p.q, b, t0, p.L, hk, p.dk, p.vec);
-        for (int e = tid; e < 6 * 64; e += 256) {
-            const auto x = M::template split<M::NT>(*reinterpret_cast<const gf8*>(p.wT + id * 3072 + e * 8));
-            const auto y = M::template split<M::NT>(*reinterpret_cast<const gf8*>(p.wP + id * 3072 + e * 8));
+    __device__ __forceinline__ void factors(int64_t n) const {    // T^T and the tokens' factors of chunk n
+        const int64_t id = bh * nc + n;
+        const GdrSource from(reinterpret_cast<T*>(p.wT) + id * (M::NT * TP)), tokens(p.co + id * (kGdrTokAll * 64));
+        constexpr int U = M::NT * TP * (int)sizeof(T) / 1024;
 #pragma unroll
-            for (int k = 0; k < M::NT; ++k) *reinterpret_cast<typename M::F*>(&tt[k][e * 8]) = x.t[k];
-#pragma unroll
-            for (int k = 0; k < M::NT; ++k) *reinterpret_cast<typename M::F*>(&tp[k][e * 8]) = y.t[k];
+        for (int e = 0; e < (U + 3) / 4; ++e) {
+            const int u = e * 4 + w;
+            if (u < U) from.to_lds(reinterpret_cast<gu4*>(tt + u * (1024 / sizeof(T))), lane * 16, u * 1024);
         }
-        for (int e = tid; e < kGdrCo * 64; e += 256) sco[e >> 6][e & 63] = p.co[id * (kGdrCo * 64) + e];
-        gf4 dY[CT][4];
+        if (w * 64 + lane < kGdrTok * 16) tokens.to_lds(reinterpret_cast<gu4*>(tok + w * 256), lane * 16, w * 1024);
+    }
+    __device__ __forceinline__ void values(int64_t n) {
+        const int64_t t0 = n * kGdrC;
+        unsigned row = (unsigned)(p.H * p.dv) * (unsigned)sizeof(T);
+        const GdrBuf<T> buf(static_cast<const T*>(p.gr.dy) + ((b * p.L + t0) * p.H + h) * p.dv);
+        const int c = in ? col : p.dv - 1, last = p.L - t0 < kGdrC ? (int)(p.L - t0) - 1 : kGdrC - 1;
+        asm volatile("" : "+s"(row));
+        if (last == kGdrC - 1) {
+            const unsigned lo = 4 * g * row + c * (unsigned)sizeof(T);
 #pragma unroll
-        for (int c = 0; c < CT; ++c)
+            for (int i = 0; i < 16; ++i) v[i] = buf.ld(lo, (16 * (i >> 2) + (i & 3)) * row);
+        } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int64_t t = t0 + 16 * i + 4 * g + r;
-                    dY[c][i][r] = t < p.L && col0 + 16 * c < p.dv ? IO<T>::ld(dyb + t * p.H * p.dv + col0 + 16 * c) : 0.0f;
-                }
-        float* ws = p.wS + id * p.dk * p.dv;
-#pragma unroll
-        for (int c = 0; c < CT; ++c)
-#pragma unroll
-            for (int d = 0; d < ND; ++d)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int row = d * 16 + 4 * g + r, col = col0 + 16 * c;
-                    if (row < p.dk && col < p.dv) ws[row * p.dv + col] = S[c][d][r];
-                }
-        __syncthreads();
-        gf4 dX[CT][4] = {};
-#pragma unroll
-        for (int s = 0; s < KD; ++s) {
-            typename M::template S<3> sb[CT];
-#pragma unroll
-            for (int c = 0; c < CT; ++c) sb[c] = M::template split<3>(gdr_pair(S[c][2 * s], S[c][2 * s + 1]));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const auto kf = M::ld(tk + ((i * KD + s) * 64 + lane) * 8);
-#pragma unroll
-                for (int c = 0; c < CT; ++c) dX[c][i] = M::template mul<3>(kf, sb[c], dX[c][i]);
-            }
-        }
-#pragma unroll
-        for (int c = 0; c < CT; ++c)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const gf4 a3 = *reinterpret_cast<const gf4*>(&sco[kA3][16 * i + 4 * g]);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) dX[c][i][r] = a3[r] != 0.0f ? a3[r] * dX[c][i][r] : 0.0f;
-            }
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            typename M::template S<1> ob[CT];           // exact: one term
-#pragma unroll
-            for (int c = 0; c < CT; ++c) ob[c] = M::template split<1>(gdr_pair(dY[c][2 * s], dY[c][2 * s + 1]));
-#pragma unroll
-            for (int i = 0; i < 2 * s + 2; ++i) {
-                typename M::template S<M::NT> pf;
-#pragma unroll
-                for (int k = 0; k < M::NT; ++k) pf.t[k] = M::ld(&tp[k][(gdr_up(i, s) * 64 + lane) * 8]);
-#pragma unroll
-                for (int c = 0; c < CT; ++c) dX[c][i] = M::template mul<M::NT>(pf, ob[c].t[0], dX[c][i]);
-            }
-        }
-        gf4 dV[CT][4] = {};
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            typename M::template S<M::NT> xb[CT];
-#pragma unroll
-            for (int c = 0; c < CT; ++c) xb[c] = M::template split<M::NT>(gdr_pair(dX[c][2 * s], dX[c][2 * s + 1]));
-#pragma unroll
-            for (int i = 0; i < 2 * s + 2; ++i) {
-                typename M::template S<M::NT> tf;
-#pragma unroll
-                for (int k = 0; k < M::NT; ++k) tf.t[k] = M::ld(&tt[k][(gdr_up(i, s) * 64 + lane) * 8]);
-#pragma unroll
-                for (int c = 0; c < CT; ++c) dV[c][i] = M::mul(tf, xb[c], dV[c][i]);
-            }
-        }
-#pragma unroll
-        for (int c = 0; c < CT; ++c)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int64_t t = t0 + 16 * i + 4 * g + r;
-                    const int col = col0 + 16 * c;
-                    if (t < p.L && col < p.dv) {
-                        IO<T>::st(dvb + t * p.H * p.dv + col, dV[c][i][r]);
-                        wvb[t * p.H * p.dv + col] = dV[c][i][r];
-                    }
-                }
-        const float end = sco[kEnd][0];
-#pragma unroll
-        for (int c = 0; c < CT; ++c)
-#pragma unroll
-            for (int d = 0; d < ND; ++d) S[c][d] = end != 0.0f ? S[c][d] * end : gf4{0, 0, 0, 0};
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            typename M::template S<3> ob[CT], vb[CT];
-#pragma unroll
-            for (int c = 0; c < CT; ++c) {
-                gf4 o[2], v[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const gf4 a1 = *reinterpret_cast<const gf4*>(&sco[kA1][32 * s + 16 * e + 4 * g]);
-                    const gf4 a2 = *reinterpret_cast<const gf4*>(&sco[kA2][32 * s + 16 * e + 4 * g]);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        o[e][r] = a2[r] != 0.0f ? a2[r] * dY[c][2 * s + e][r] : 0.0f;
-                        v[e][r] = a1[r] != 0.0f ? -a1[r] * dV[c][2 * s + e][r] : 0.0f;
-                    }
-                }
-                ob[c] = M::template split<3>(gdr_pair(o[0], o[1]));
-                vb[c] = M::template split<3>(gdr_pair(v[0], v[1]));
-            }
-#pragma unroll
-            for (int d = 0; d < ND; ++d) {
-                const auto kf = M::template ldt<KD>(tk, s, d, lane), qf = M::template ldt<KD>(tq, s, d, lane);
-#pragma unroll
-                for (int c = 0; c < CT; ++c) S[c][d] = M::template mul<3>(kf, vb[c], M::template mul<3>(qf, ob[c], S[c][d]));
+            for (int i = 0; i < 16; ++i) {
+                const int t = 16 * (i >> 2) + 4 * g + (i & 3);
+                const T x = buf.ld((t < last ? t : last) * row + c * (unsigned)sizeof(T), 0);
+                v[i] = t <= last ? x : T(0);
             }
         }
     }
-    if (p.gr.dstate_init) {
+
+    __device__ __forceinline__ void chunk(int64_t n) {
+        const int64_t t0 = n * kGdrC, id = bh * nc + n;
+        gdr_arrived();
+        {
+            const GdrBuf<float> ws(p.wS + id * p.dk * p.dv);
+            unsigned dvb = p.dv * 4;
+            asm volatile("" : "+s"(dvb));
+            const unsigned lo = 8 * g * dvb + col * 4;
+            if (in)
 #pragma unroll
-        for (int c = 0; c < CT; ++c)
+                for (int s = 0; s < KD; ++s) {
+                    if (AL && 32 * s + 8 * g >= p.dk) continue;
 #pragma unroll
-            for (int d = 0; d < ND; ++d)
+                    for (int e = 0; e < 8; ++e)
+                        if (AL || 32 * s + 8 * g + e < p.dk) ws.st(S[2 * s + (e >> 2)][e & 3], lo, (32 * s + e) * dvb);
+                }
+        }
+        // K W, and P's row tile of this wave (a lane has a key's column) with its queries' lengths, a diagonal
+        gf4 dX[4] = {}, pt[4] = {}, len = {0, 0, 0, 0};
+        {
+            typename M::F f[2][4];
+            auto read = [&](int s, typename M::F (&x)[4]) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[i] = gdr_rows_frag<T>(tk, i * KD + s, place);
+            };
+            read(0, f[0]);
+#pragma unroll
+            for (int s = 0; s < KD; ++s) {
+                const auto own = gdr_rows_frag<T>(tq, w * KD + s, place);
+                if (s + 1 < KD) read(s + 1, f[(s + 1) & 1]);
+                __builtin_amdgcn_sched_barrier(0);
+                auto& x = f[s & 1];
+                const auto sb = M::template split<3>(gdr_pair(S[2 * s], S[2 * s + 1]));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) pt[i] = M::mm(own, x[i], pt[i]);
+                len = M::mm(own, own, len);
+#pragma unroll
+                for (int k = sizeof(T) == 2 ? 2 : 0; k >= 0; --k)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) dX[i] = M::mm(x[i], sb.t[k], dX[i]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+        {
+            const double* G = reinterpret_cast<const double*>(tok + tG * 64);
+            gf4 q;
+            double gi[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float q2 = __shfl(len[r], g * 16 + 4 * g + r, 64);
+                q[r] = p.eps > 0.0f ? p.scale * __builtin_amdgcn_rsqf(q2 + p.eps) : p.scale;
+                gi[r] = G[16 * w + 4 * g + r];
+            }
+            if (m == 0) *reinterpret_cast<gf4*>(&srq[16 * w + 4 * g]) = q;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (i > w) break;                     // this wave's tiles above the diagonal stay 0 in LDS
+                const float bk = tok[tBk * 64 + 16 * i + m];
+                const double gj = G[16 * i + m];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const int row = d * 16 + 4 * g + r, col = col0 + 16 * c;
-                    if (row < p.dk && col < p.dv) p.gr.dstate_init[(bh * p.dk + row) * p.dv + col] = S[c][d][r];
+                    const float d = __builtin_amdgcn_exp2f((float)(gi[r] - gj));
+                    pt[i][r] = d != 0.0f && (i < w || 4 * g + r >= m) ? pt[i][r] * d * bk * q[r] : 0.0f;
                 }
+                const int unit = i < 2 ? 2 * i + (w >> 1) : i + 2;
+                if constexpr (sizeof(T) == 2) {
+                    const auto both = M::template split<M::NT>(gdr_pair(pt[i], gf4{0, 0, 0, 0}));
+                    T* at = tp + (unit * 64 + lane) * 8 + 4 * (w & 1);
+#pragma unroll
+                    for (int k = 0; k < M::NT; ++k) {
+                        typedef uint32_t gu2 __attribute__((ext_vector_type(2)));
+                        const gu4 u = __builtin_bit_cast(gu4, both.t[k]);
+                        *reinterpret_cast<gu2*>(at + k * TP) = gu2{u[0], u[1]};
+                    }
+                } else {
+                    *reinterpret_cast<gf4*>(tp + ((unit * 2 + (w & 1)) * 64 + lane) * 4) = pt[i];
+                }
+            }
+        }
+        const float end = tok[tMisc * 64];
+        const bool clean = tok[tMisc * 64 + 1] != 0.0f;
+        gf4 a1[4], a2[4], dY[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const gf4 a3 = *reinterpret_cast<const gf4*>(&tok[tA3 * 64 + 16 * i + 4 * g]);
+            a1[i] = *reinterpret_cast<const gf4*>(&tok[tA1 * 64 + 16 * i + 4 * g]);
+            a2[i] = *reinterpret_cast<const gf4*>(&tok[tA2 * 64 + 16 * i + 4 * g]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                dY[i][r] = IO<T>::cvt(v[4 * i + r]);
+                dX[i][r] = a3[r] != 0.0f ? a3[r] * dX[i][r] : 0.0f;
+            }
+        }
+        __syncthreads();                              // P and the queries' lengths are there
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const auto ob = M::template split<1>(gdr_pair(dY[2 * s], dY[2 * s + 1]));     // exact
+            typename M::template S<M::NT> pf[4];
+#pragma unroll
+            for (int i = 0; i < 2 * s + 2; ++i) pf[i] = gdr_terms<T, M::NT>(tp, TP, gdr_up(i, s), lane);
+#pragma unroll
+            for (int k = M::NT - 1; k >= 0; --k)
+#pragma unroll
+                for (int i = 0; i < 2 * s + 2; ++i) dX[i] = M::mm(pf[i].t[k], ob.t[0], dX[i]);
+        }
+        gf4 dV[4] = {};
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            typename M::template S<M::NT> tf[4];
+#pragma unroll
+            for (int i = 0; i < 2 * s + 2; ++i) tf[i] = gdr_terms<T, M::NT>(tt, TP, gdr_up(i, s), lane);
+            const auto xb = M::template split<M::NT>(gdr_pair(dX[2 * s], dX[2 * s + 1]));
+            M::template each<M::NT>([&](int a, int c) {
+#pragma unroll
+                for (int i = 0; i < 2 * s + 2; ++i) dV[i] = M::mm(tf[i].t[a], xb.t[c], dV[i]);
+            });
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a2[i] *= *reinterpret_cast<const gf4*>(&srq[16 * i + 4 * g]);
+        __syncthreads();                              // T, P and factors are used up
+        if (n > 0) {
+            factors(n - 1);
+            values(n - 1);
+        }
+        if (in) {
+            unsigned row = (unsigned)(p.H * p.dv);
+            asm volatile("" : "+s"(row));
+            const int64_t at = ((b * p.L + t0) * p.H + h) * p.dv;
+            const GdrBuf<T> dvt(static_cast<T*>(p.gr.dv) + at);
+            const GdrBuf<float> wvt(p.wV + at);
+            const int left = p.L - t0 < kGdrC ? (int)(p.L - t0) : kGdrC;
+            const unsigned lo = 4 * g * row + col;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (16 * i + 4 * g + r < left) {
+                        dvt.st(dV[i][r], lo * (unsigned)sizeof(T), (16 * i + r) * row * (unsigned)sizeof(T));
+                        wvt.st(dV[i][r], lo * 4, (16 * i + r) * row * 4);
+                    }
+        }
+        // the gradient of the state in front
+        {
+            constexpr int NB = 2 * ND / 2;            // batches of two tiles, tokens' first half, then the second
+            typename M::F f[2][4];
+            auto read = [&](int q, typename M::F (&x)[4]) {
+                const int s = q / (ND / 2), sd = q % (ND / 2);
+#pragma unroll
+                for (int d = 0; d < 2; ++d) {
+                    x[d] = gdr_frag_t<T, KD>(tk, s, sd, d, lane);
+                    x[2 + d] = gdr_frag_t<T, KD>(tq, s, sd, d, lane);
+                }
+            };
+            read(0, f[0]);
+#pragma unroll
+            for (int d = 0; d < ND; ++d) S[d] = end != 0.0f ? S[d] * end : gf4{0, 0, 0, 0};
+            typename M::template S<3> ob, vb;
+#pragma unroll
+            for (int q = 0; q < NB; ++q) {
+                const int s = q / (ND / 2), d0 = q % (ND / 2) * 2;
+                if (q + 1 < NB) read(q + 1, f[(q + 1) & 1]);
+                if (d0 == 0) {
+                    gf4 o[2], x[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        o[e] = dY[2 * s + e] * a2[2 * s + e];
+                        x[e] = dV[2 * s + e] * -a1[2 * s + e];
+                        if (!clean)
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) {
+                                o[e][r] = a2[2 * s + e][r] != 0.0f ? o[e][r] : 0.0f;
+                                x[e][r] = a1[2 * s + e][r] != 0.0f ? x[e][r] : 0.0f;
+                            }
+                    }
+                    ob = M::template split<3>(gdr_pair(o[0], o[1]));
+                    vb = M::template split<3>(gdr_pair(x[0], x[1]));
+                }
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int k = sizeof(T) == 2 ? 2 : 0; k >= 0; --k) {
+#pragma unroll
+                    for (int d = 0; d < 2; ++d) S[d0 + d] = M::mm(f[q & 1][d], vb.t[k], S[d0 + d]);
+#pragma unroll
+                    for (int d = 0; d < 2; ++d) S[d0 + d] = M::mm(f[q & 1][2 + d], ob.t[k], S[d0 + d]);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+        if (n > 0) {
+            __syncthreads();
+            rk.load(tk, t0 - kGdrC, p.L);
+            rq.load(tq, t0 - kGdrC, p.L);
+        }
+    }
+};
+
+template <typename T, int DKP, bool AL, int GROUPS>
+__global__ void __launch_bounds__(256, GROUPS)
+k_gdr_walk_back(const LaunchGdr p) {
+    using W = GdrWalkBack<T, DKP, AL>;
+    __shared__ alignas(16) T tk[64 * DKP], tq[64 * DKP], tt[Mx<T>::NT * 3072], tp[Mx<T>::NT * 3072];
+    __shared__ alignas(16) float tok[kGdrTok * 64], srq[64];
+    const int64_t BH = p.B * p.H, bh = blockIdx.x % BH, b = bh / p.H, kv = (int64_t)p.dk * p.dv;
+    const int h = (int)(bh % p.H), hk = h / (p.H / p.Hk), col = (int)(blockIdx.x / BH) * 64 + gdr_wave() * 16 + (threadIdx.x & 15);
+    W k(p, tk, tq, tt, tp, tok, srq, b, bh, h, hk, col);
+    const float* from = p.gr.dstate_final ? p.gr.dstate_final + bh * kv : nullptr;
+#pragma unroll
+    for (int d = 0; d < W::ND; ++d)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int row = 32 * (d >> 1) + 8 * k.g + 4 * (d & 1) + r;
+            k.S[d][r] = from && row < p.dk && k.in ? from[row * p.dv + col] : 0.0f;
+        }
+    gdr_clear<64 * DKP>(tk);
+    gdr_clear<64 * DKP>(tq);
+    gdr_clear<Mx<T>::NT * 3072>(tp);
+    __syncthreads();
+    k.rk.load(tk, (p.nchunks - 1) * kGdrC, p.L);
+    k.rq.load(tq, (p.nchunks - 1) * kGdrC, p.L);
+    k.factors(p.nchunks - 1);
+    k.values(p.nchunks - 1);
+#pragma unroll 1
+    for (int64_t n = p.nchunks - 1; n >= 0; --n) k.chunk(n);
+    if (p.gr.dstate_init && k.in) {
+        float* to = p.gr.dstate_init + bh * kv;
+#pragma unroll
+        for (int d = 0; d < W::ND; ++d)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = 32 * (d >> 1) + 8 * k.g + 4 * (d & 1) + r;
+                if (row < p.dk) to[row * p.dv + col] = k.S[d][r];
+            }
     }
 }
 
@@ -1351,68 +1273,109 @@ k_gdr_walk_back(const LaunchGdr p) {
 //   two sums, so that the gradient of a small decay, which has it as a factor, keeps its digits):
 //   sum_{i >= t > j} beta_j (E P + F N/beta)_ij + sum_{i >= t} (q . a2 dY S0^T - k . a1 dV S0^T)_i
 //     + sum_{j < t} beta_j (k . a3b X W^T)_j + e^G_last <S0, W>
-// A wave has a quarter of dk's columns; terms over dv go through LDS 32 at a time.
-template <typename T, int DKP>
-__global__ void __launch_bounds__(256)
+// A wave has a quarter of dk, transposed (a lane has a token): sums over dk are sums over registers and two moves, factors
+// of tokens one register, and four neighbouring columns one store. Terms over dv go through LDS 32 at a time, the next
+// ones on their way to registers meanwhile.
+template <typename T, int DKP, bool AL, int GROUPS>
+__global__ void __launch_bounds__(256, GROUPS)
 k_gdr_grads(const LaunchGdr p) {
     using M = Mx<T>;
-    constexpr int KD = DKP / 32, NS = DKP / 64, LD = 68;
-    constexpr int kSlice = 4 * 512;                              // 64 rows of 32 terms
-    constexpr int kPhase1 = (2 * M::NT + 1) * kSlice * (int)sizeof(T);
-    constexpr int kPhase2 = 64 * DKP * (int)sizeof(T) + 3 * 64 * LD * 4;
+    constexpr int KD = DKP / 32, NS = DKP / 64, LD = 68, SL = 4 * 512;      // SL: 64 rows of 32 terms
+    constexpr bool BOTH = 2 * 64 * DKP * (int)sizeof(T) <= 98304;          // keys and queries fit in LDS side by side
+    constexpr int kPhase1 = (2 * M::NT + 1) * SL * (int)sizeof(T), kPhase2 = 2 * 64 * LD * 4;
+    __shared__ alignas(16) T tk[64 * DKP], tq_[BOTH ? 64 * DKP : 8];
     __shared__ alignas(16) char lds[kPhase1 > kPhase2 ? kPhase1 : kPhase2];
-    __shared__ alignas(16) float sco[kGdrCo][64];
-    __shared__ float rows[3][4][64], colsum[4][64], wsum[4];
-    T (*lx)[kSlice] = reinterpret_cast<T (*)[kSlice]>(lds), (*lv)[kSlice] = lx + M::NT, *lo = lx[2 * M::NT];
-    T* tk = reinterpret_cast<T*>(lds);
-    float (*me)[LD] = reinterpret_cast<float (*)[LD]>(lds + 64 * DKP * sizeof(T)), (*mf)[LD] = me + 64, (*mg)[LD] = mf + 64;
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, g = lane >> 4, m = lane & 15;
+    __shared__ alignas(16) float tok[kGdrTokAll * 64];
+    __shared__ alignas(16) float srq[64], rows[2][4][64], colsum[4][64], wsum[4];
+    T (*lx)[SL] = reinterpret_cast<T (*)[SL]>(lds), (*lv)[SL] = lx + M::NT, *lo = lx[2 * M::NT], *tq = BOTH ? tq_ : tk;
+    float (*me)[LD] = reinterpret_cast<float (*)[LD]>(lds), (*mf)[LD] = me + 64;
+    const int tid = threadIdx.x, lane = tid & 63, w = gdr_wave(), g = lane >> 4, m = lane & 15, place = gdr_place(g, m);
     const int64_t id = blockIdx.x, nc = p.nchunks, n = id % nc, bh = id / nc, b = bh / p.H, t0 = n * kGdrC;
-    const int h = (int)(bh % p.H), hk = h / (p.H / p.Hk);
-    const bool vec = p.dv % 4 == 0;
-    const float *S0 = p.ckpt + id * p.dk * p.dv, *W = p.wS + id * p.dk * p.dv;
-    const bool vecs = vec && (reinterpret_cast<uintptr_t>(p.ckpt) & 15) == 0, vecx = vec && (reinterpret_cast<uintptr_t>(p.ckptX) & 15) == 0;
-    const int64_t row0 = (b * p.L + t0) * p.H + h;               // of tokens' rows of dv; H rows from token to token
-    const T* dy = static_cast<const T*>(p.gr.dy);
-    for (int e = tid; e < kGdrCo * 64; e += 256) sco[e >> 6][e & 63] = p.co[id * (kGdrCo * 64) + e];
-    for (int e = tid; e < 4 * 64; e += 256) colsum[e >> 6][e & 63] = 0.0f;
+    const int h = (int)(bh % p.H), hk = h / (p.H / p.Hk), left = p.L - t0 < kGdrC ? (int)(p.L - t0) : kGdrC;
+    const GdrRows<T, KD, AL> rk(p.k, b, hk, p.dk), rq(p.q, b, hk, p.dk);
+    const T* qg = rq.base + t0 * rq.stride;
+    if (!AL || p.dk < DKP) {
+        gdr_clear<64 * DKP>(tk);
+        if (BOTH) gdr_clear<64 * DKP>(tq_);
+        __syncthreads();
+    }
+    rk.load(tk, t0, p.L);
+    if (BOTH) rq.load(tq, t0, p.L);
+    for (int e = tid; e < kGdrTokAll * 64; e += 256) tok[e] = p.co[id * (kGdrTokAll * 64) + e];
+    colsum[tid >> 6][tid & 63] = 0.0f;
 
+    // what a lane brings of 32 columns: an eight of X, dV and dY for LDS, and its rows of S0 and W
+    const int64_t kv = (int64_t)p.dk * p.dv, row0 = (b * p.L + t0) * p.H + h;
+    const int ts = tid >> 2, tr = ts < left ? ts : left - 1, octet = tid & 3;
+    const int64_t at0 = (row0 + (int64_t)tr * p.H) * p.dv;
+    const float *S0 = p.ckpt + id * kv, *W = p.wS + id * kv;
+    gf8 nx, nv, ns[NS], nw[NS];
+    alignas(16) T ny[8];
+    auto fetch = [&](int c0) {
+        const int c = c0 + octet * 8;
+        nx = gdr_ld8(p.ckptX + at0, c, p.dv, true, p.vec_ck);
+        nv = gdr_ld8(p.wV + at0, c, p.dv, true, p.vec_ck);
+        gdr_row8<T>(static_cast<const T*>(p.gr.dy) + at0, c, p.dv, p.vec_dy, true, ny);
+#pragma unroll
+        for (int u = 0; u < NS; ++u) {
+            const int q = w * NS + u, d = 32 * (q >> 1) + 8 * (m >> 2) + 4 * (q & 1) + (m & 3);
+            ns[u] = gdr_ld8(S0 + (int64_t)d * p.dv, c0 + 8 * g, p.dv, d < p.dk, p.vec_ck);
+            nw[u] = gdr_ld8(W + (int64_t)d * p.dv, c0 + 8 * g, p.dv, d < p.dk, p.vec_ck);
+        }
+    };
     gf4 aq[NS][4] = {}, av[NS][4] = {}, ax[NS][4] = {}, ae[3] = {}, af[3] = {};
     float ww = 0.0f;
+    fetch(0);
     for (int c0 = 0; c0 < p.dv; c0 += 32) {
         __syncthreads();
         {
-            const int t = tid >> 2, o = tid & 3, c = c0 + o * 8, at = ((t >> 4) * 64 + o * 16 + (t & 15)) * 8;
-            const bool there = t0 + t < p.L;
-            const int64_t row = (row0 + (int64_t)t * p.H) * p.dv;
-            const auto x = M::template split<M::NT>(gdr_ld8(p.ckptX + row, c, p.dv, there, vecx));
-            const auto v = M::template split<M::NT>(gdr_ld8(p.wV + row, c, p.dv, there, vec));
+            // rows behind the last token are copies of it: their gradients are not
+            if (ts >= left) {
+                nx = nv = gf8{0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
-            for (int k = 0; k < M::NT; ++k) {
-                *reinterpret_cast<typename M::F*>(&lx[k][at]) = x.t[k];
-                *reinterpret_cast<typename M::F*>(&lv[k][at]) = v.t[k];
+                for (int j = 0; j < 8; ++j) ny[j] = T(0);
             }
+            const auto x = M::template split<M::NT>(nx), v = M::template split<M::NT>(nv);
+            const int unit = ts >> 4, pl = gdr_place(octet, ts & 15);
+            auto put = [&](T* to, const typename M::F& f) {
+                if constexpr (sizeof(T) == 2) {
+                    *reinterpret_cast<gb8*>(to + (unit * 64 + pl) * 8) = f;
+                } else {
+                    *reinterpret_cast<gf4*>(to + (unit * 128 + pl) * 4) = gf4{f[0], f[1], f[2], f[3]};
+                    *reinterpret_cast<gf4*>(to + (unit * 128 + 64 + pl) * 4) = gf4{f[4], f[5], f[6], f[7]};
+                }
+            };
 #pragma unroll
-            for (int j = 0; j < 8; ++j) lo[at + j] = there && c + j < p.dv ? dy[row + c + j] : T(0);
+            for (int k = 0; k < M::NT; ++k) { put(lx[k], x.t[k]); put(lv[k], v.t[k]); }
+            put(lo, __builtin_bit_cast(typename M::F, ny));
         }
-        __syncthreads();
+        typename M::template S<M::NT> sb[NS], wb[NS];
 #pragma unroll
         for (int u = 0; u < NS; ++u) {
-            const int r = (w * NS + u) * 16 + m, c = c0 + 8 * g;
-            const gf8 s0 = gdr_ld8(S0 + (int64_t)r * p.dv, c, p.dv, r < p.dk, vecs), s1 = gdr_ld8(W + (int64_t)r * p.dv, c, p.dv, r < p.dk, vec);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) ww = __builtin_fmaf(s0[j], s1[j], ww);
-            const auto sb = M::template split<M::NT>(s0), wb = M::template split<M::NT>(s1);
+            for (int j = 0; j < 8; ++j) ww = __builtin_fmaf(ns[u][j], nw[u][j], ww);
+            sb[u] = M::template split<M::NT>(ns[u]);
+            wb[u] = M::template split<M::NT>(nw[u]);
+        }
+        __syncthreads();
+        if (c0 + 32 < p.dv) fetch(c0 + 32);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int at = (i * 64 + lane) * 8;
-                typename M::template S<M::NT> xf, vf;
+        for (int i = 0; i < 4; ++i) {
+            typename M::template S<M::NT> xf, vf;
 #pragma unroll
-                for (int k = 0; k < M::NT; ++k) { xf.t[k] = M::ld(&lx[k][at]); vf.t[k] = M::ld(&lv[k][at]); }
-                aq[u][i] = M::template mul<M::NT>(M::ld(lo + at), sb, aq[u][i]);
-                av[u][i] = M::mul(vf, sb, av[u][i]);
-                ax[u][i] = M::mul(xf, wb, ax[u][i]);
-            }
+            for (int k = 0; k < M::NT; ++k) { xf.t[k] = gdr_rows_frag<T>(lx[k], i, place); vf.t[k] = gdr_rows_frag<T>(lv[k], i, place); }
+            const auto of = gdr_rows_frag<T>(lo, i, place);
+            M::template each<M::NT>([&](int a, int c) {
+#pragma unroll
+                for (int u = 0; u < NS; ++u) {
+                    av[u][i] = M::mm(sb[u].t[a], vf.t[c], av[u][i]);
+                    ax[u][i] = M::mm(wb[u].t[a], xf.t[c], ax[u][i]);
+                }
+            });
+#pragma unroll
+            for (int k = M::NT - 1; k >= 0; --k)
+#pragma unroll
+                for (int u = 0; u < NS; ++u) aq[u][i] = M::mm(sb[u].t[k], of, aq[u][i]);
         }
 #pragma unroll
         for (int u = 0; u < 3; ++u) {
@@ -1422,42 +1385,76 @@ k_gdr_grads(const LaunchGdr p) {
                 gdr_tile(tile, mt, nt);
                 typename M::template S<M::NT> xf, vf;
 #pragma unroll
-                for (int k = 0; k < M::NT; ++k) { xf.t[k] = M::ld(&lx[k][(nt * 64 + lane) * 8]); vf.t[k] = M::ld(&lv[k][(mt * 64 + lane) * 8]); }
-                ae[u] = M::template mul<M::NT>(M::ld(lo + (mt * 64 + lane) * 8), xf, ae[u]);
-                af[u] = M::mul(vf, xf, af[u]);
+                for (int k = 0; k < M::NT; ++k) { xf.t[k] = gdr_rows_frag<T>(lx[k], nt, place); vf.t[k] = gdr_rows_frag<T>(lv[k], mt, place); }
+                const auto of = gdr_rows_frag<T>(lo, mt, place);
+#pragma unroll
+                for (int k = M::NT - 1; k >= 0; --k) ae[u] = M::mm(of, xf.t[k], ae[u]);
+                M::template each<M::NT>([&](int a, int c) { af[u] = M::mm(vf.t[a], xf.t[c], af[u]); });
             }
         }
     }
-    __syncthreads();
-    // keys to LDS; the pairs of tokens: E', F + F^T and the terms of dg to LDS
-    gdr_stage<T, KD>(tk, p.k, b, t0, p.L, hk, p.dk, p.vec);
-    for (int e = tid; e < 64 * 64; e += 256)
-        if ((e & 63) >= (e >> 6)) {
-            if ((e & 63) > (e >> 6)) me[e >> 6][e & 63] = 0.0f;
-            mg[e >> 6][e & 63] = 0.0f;
+    // a query's fragment, from LDS or memory
+    auto query = [&](int i, int s) {
+        if constexpr (BOTH) {
+            return gdr_rows_frag<T>(tq, i * KD + s, place);
+        } else {
+            alignas(16) T x[8];
+            const int t = 16 * i + m;
+            gdr_row8<T>(qg + (t < left ? t : left - 1) * rq.stride, 32 * s + 8 * g, p.dk, AL, true, x);
+            return __builtin_bit_cast(typename M::F, x);
         }
+    };
+    {
+        gf4 len = {0, 0, 0, 0};
+#pragma unroll
+        for (int s = 0; s < KD; ++s) {
+            const auto f = query(w, s);
+            len = M::mm(f, f, len);
+        }
+        const float q2 = (m & 3) == 0 ? len[0] : (m & 3) == 1 ? len[1] : (m & 3) == 2 ? len[2] : len[3];
+        if (m >> 2 == g) srq[16 * w + m] = p.eps > 0.0f ? __builtin_amdgcn_rsqf(q2 + p.eps) : 1.0f;
+    }
+    gf4 kk[3] = {}, qk[3] = {};
 #pragma unroll
     for (int u = 0; u < 3; ++u) {
         const int tile = w + 4 * u;
         if (tile < 10) {
             int mt, nt;
             gdr_tile(tile, mt, nt);
-            const gf4* raw = reinterpret_cast<const gf4*>(p.raw + (id * 30 + tile) * 256) + lane;
-            const gf4 d = raw[0], nn = raw[640], pp = raw[1280];
+#pragma unroll
+            for (int s = 0; s < KD; ++s) {
+                const auto kn = gdr_rows_frag<T>(tk, nt * KD + s, place);
+                kk[u] = M::mm(gdr_rows_frag<T>(tk, mt * KD + s, place), kn, kk[u]);
+                qk[u] = M::mm(query(mt, s), kn, qk[u]);
+            }
+        }
+    }
+    __syncthreads();                                  // the terms' LDS becomes the pairs', and the queries' lengths are there
+    // pairs of tokens: E' on and below me's diagonal, the terms of dg transposed above it; F + F^T in mf
+    const double* G = reinterpret_cast<const double*>(tok + tG * 64);
+#pragma unroll
+    for (int u = 0; u < 3; ++u) {
+        const int tile = w + 4 * u;
+        if (tile < 10) {
+            int mt, nt;
+            gdr_tile(tile, mt, nt);
             const int j = nt * 16 + m;
-            const float beta = sco[kBeta][j];
+            const float beta = tok[tBeta * 64 + j], rkj = tok[tRk * 64 + j];
+            const double gj = G[j];
             float s = 0.0f;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int i = mt * 16 + 4 * g + r;
                 if (i < j) continue;
                 // where the decay is nothing no gradient passes
-                const float e = d[r] != 0.0f ? ae[u][r] : 0.0f, f = i > j && d[r] != 0.0f ? -af[u][r] : 0.0f;
-                const float term = e * pp[r] + f * nn[r];
-                s += term;
-                me[i][j] = e * beta * d[r] * (sco[kRq][i] * p.scale);
-                if (i > j) mg[i][j] = term * beta;
-                mf[i][j] = mf[j][i] = f * beta * d[r] * sco[kRk][i];
+                const float d = __builtin_amdgcn_exp2f((float)(G[i] - gj)) * rkj;
+                const float fq = d * srq[i] * p.scale, fk = d * tok[tRk * 64 + i];
+                const float e = d != 0.0f ? ae[u][r] : 0.0f, f = i > j && d != 0.0f ? -af[u][r] : 0.0f;
+                const float term = e * fq * qk[u][r] + f * fk * kk[u][r];
+                s += d != 0.0f ? term : 0.0f;
+                me[i][j] = e * beta * fq;
+                if (i > j) me[j][i] = d != 0.0f ? term * beta : 0.0f;
+                mf[i][j] = mf[j][i] = f * beta * fk;
             }
             s += __shfl_xor(s, 16, 64);
             s += __shfl_xor(s, 32, 64);
@@ -1467,56 +1464,109 @@ k_gdr_grads(const LaunchGdr p) {
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) ww += __shfl_xor(ww, o, 64);
     if (lane == 0) wsum[w] = ww;
-    __syncthreads();
-    // sums over dk of a token's row; q's values from memory
-    {
-        const T* qb = static_cast<const T*>(p.q.p) + b * p.q.batch_stride + hk * p.q.head_stride;
+    // sums over dk of a token's row
+    auto key4 = [&](const T* tiles, int i, int q) {   // four neighbouring columns of this lane's token
+        const int d = 8 * g + 4 * (q & 1), unit = i * KD + (q >> 1), pl = gdr_place(g, m);
+        gf4 x;
+        if constexpr (sizeof(T) == 2) {
+            typedef uint32_t gu2 __attribute__((ext_vector_type(2)));
+            const gu2 u = *reinterpret_cast<const gu2*>(tiles + (unit * 64 + pl) * 8 + (d & 7));
+            x = gf4{__builtin_bit_cast(float, u[0] << 16), __builtin_bit_cast(float, u[0] & 0xffff0000u),
+                    __builtin_bit_cast(float, u[1] << 16), __builtin_bit_cast(float, u[1] & 0xffff0000u)};
+        } else {
+            x = *reinterpret_cast<const gf4*>(tiles + (unit * 128 + (q & 1) * 64 + pl) * 4);
+        }
+        return x;
+    };
+    auto query4 = [&](int i, int q) {
+        if constexpr (BOTH) return key4(tq, i, q);
+        else {
+            gf4 x;
+            const int t = 16 * i + m, d = 32 * (q >> 1) + 8 * g + 4 * (q & 1);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const gf4 a1 = *reinterpret_cast<const gf4*>(&sco[kA1][16 * i + 4 * g]), a2 = *reinterpret_cast<const gf4*>(&sco[kA2][16 * i + 4 * g]);
-            const gf4 a3 = *reinterpret_cast<const gf4*>(&sco[kA3b][16 * i + 4 * g]);
+            for (int r = 0; r < 4; ++r) x[r] = d + r < p.dk ? gdr_f<T>(qg[(t < left ? t : left - 1) * rq.stride + d + r]) : 0.0f;
+            return x;
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int t = 16 * i + m;
+        const float a1 = tok[tA1 * 64 + t], a2 = tok[tA2 * 64 + t] * srq[t] * p.scale, a3 = tok[tA3b * 64 + t], beta = tok[tBeta * 64 + t];
+        float y = 0.0f, z = 0.0f;
+#pragma unroll
+        for (int u = 0; u < NS; ++u) {
+            const gf4 k4 = key4(tk, i, w * NS + u), q4 = query4(i, w * NS + u);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                float y = 0.0f, z = 0.0f;
-                const int64_t t = t0 + 16 * i + 4 * g + r;
-#pragma unroll
-                for (int u = 0; u < NS; ++u) {
-                    const int d = (w * NS + u) * 16 + m;
-                    const float kv = gdr_f<T>(tk[((i * KD + (d >> 5)) * 64 + (d >> 2 & 3) * 16 + 4 * g + r) * 8 + (d >> 4 & 1) * 4 + (d & 3)]);
-                    const float qv = t < p.L && d < p.dk ? IO<T>::ld(qb + t * p.q.token_stride + d) : 0.0f;
-                    aq[u][i][r] = a2[r] != 0.0f ? a2[r] * aq[u][i][r] : 0.0f;
-                    av[u][i][r] = a1[r] != 0.0f ? a1[r] * av[u][i][r] : 0.0f;
-                    ax[u][i][r] = a3[r] != 0.0f ? a3[r] * ax[u][i][r] : 0.0f;
-                    y = __builtin_fmaf(qv, aq[u][i][r], y);
-                    y = __builtin_fmaf(-kv, av[u][i][r], y);
-                    z = __builtin_fmaf(kv, ax[u][i][r], z);
-                }
-#pragma unroll
-                for (int o = 1; o < 16; o <<= 1) {
-                    y += __shfl_xor(y, o, 64);
-                    z += __shfl_xor(z, o, 64);
-                }
-                if (m == 0) {
-                    rows[0][w][16 * i + 4 * g + r] = y;
-                    rows[1][w][16 * i + 4 * g + r] = z;
-                }
+                aq[u][i][r] = a2 != 0.0f ? a2 * aq[u][i][r] : 0.0f;
+                av[u][i][r] = a1 != 0.0f ? a1 * av[u][i][r] : 0.0f;
+                ax[u][i][r] = a3 != 0.0f ? a3 * ax[u][i][r] : 0.0f;
+                y = __builtin_fmaf(q4[r], aq[u][i][r], y);
+                y = __builtin_fmaf(-k4[r], av[u][i][r], y);
+                z = __builtin_fmaf(k4[r], ax[u][i][r], z);
+                av[u][i][r] = beta * ax[u][i][r] - av[u][i][r];                    // from here on the key's gradient
             }
+        }
+        y += __shfl_xor(y, 16, 64);
+        z += __shfl_xor(z, 16, 64);
+        y += __shfl_xor(y, 32, 64);
+        z += __shfl_xor(z, 32, 64);
+        if (g == 0) {
+            rows[0][w][t] = y;
+            rows[1][w][t] = z;
         }
     }
     __syncthreads();
-    // gates
-    if (w == 0) {
+    // dq += E' K, dk += (F + F^T) K, transposed: keys' rows as the first operand
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        typename M::F kf[NS];
+#pragma unroll
+        for (int u = 0; u < NS; ++u) kf[u] = gdr_frag_t<T, KD>(tk, s, (w * NS + u) >> 1, (w * NS + u) & 1, lane);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = 16 * i + m, c = 32 * s + 4 * g;
+            gf8 e = gdr_pair(*reinterpret_cast<const gf4*>(&me[r][c]), *reinterpret_cast<const gf4*>(&me[r][c + 16]));
+#pragma unroll
+            for (int j = 0; j < 8; ++j) e[j] = c + 16 * (j >> 2) + (j & 3) <= r ? e[j] : 0.0f;
+            const auto ef = M::template split<M::NP>(e);
+            const auto ff = M::template split<M::NP>(gdr_pair(*reinterpret_cast<const gf4*>(&mf[r][c]), *reinterpret_cast<const gf4*>(&mf[r][c + 16])));
+#pragma unroll
+            for (int u = 0; u < NS; ++u) {
+                if (i >= 2 * s) aq[u][i] = M::template mul<M::NP>(kf[u], ef, aq[u][i]);
+                av[u][i] = M::template mul<M::NP>(kf[u], ff, av[u][i]);
+            }
+        }
+    }
+    if (!BOTH) {
+        __syncthreads();
+        rq.load(tk, t0, p.L);
+        gdr_arrived();
+    }
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        typename M::F qf[NS];
+#pragma unroll
+        for (int u = 0; u < NS; ++u) qf[u] = gdr_frag_t<T, KD>(tq, s, (w * NS + u) >> 1, (w * NS + u) & 1, lane);
+#pragma unroll
+        for (int i = 0; i < 2 * s + 2; ++i) {
+            gf8 e;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int r = 32 * s + 16 * (j >> 2) + 4 * g + (j & 3);
+                e[j] = r >= 16 * i + m ? me[r][16 * i + m] : 0.0f;
+            }
+            const auto ef = M::template split<M::NP>(e);
+#pragma unroll
+            for (int u = 0; u < NS; ++u) av[u][i] = M::template mul<M::NP>(qf[u], ef, av[u][i]);
+        }
+    }
+    // gates: wave 3, whose tokens' sums go over the terms above me's diagonal
+    if (w == 3) {
         const int t = lane;
         float y = rows[0][0][t] + rows[0][1][t] + rows[0][2][t] + rows[0][3][t];
         const float z = rows[1][0][t] + rows[1][1][t] + rows[1][2][t] + rows[1][3][t];
-        const float zb = z * sco[kBeta][t];
-        float run = 0.0f;                                        // mg's row t: sums in front of each column
-        for (int j = 0; j < 64; ++j) {
-            const float v = mg[t][j];
-            mg[t][j] = run;
-            run += v;
-        }
-        float before = zb;
+        float before = z * tok[tBeta * 64 + t];
 #pragma unroll
         for (int o = 1; o < 64; o <<= 1) {
             const float u = __shfl_up(before, o, 64), v = __shfl_down(y, o, 64);
@@ -1525,76 +1575,124 @@ k_gdr_grads(const LaunchGdr p) {
         }
         before = __shfl_up(before, 1, 64);
         if (lane == 0) before = 0.0f;
-        const float end = sco[kEnd][0];
+        const float end = tok[tMisc * 64];
         float dg = y + before + (end != 0.0f ? end * (wsum[0] + wsum[1] + wsum[2] + wsum[3]) : 0.0f);
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");
-        __builtin_amdgcn_wave_barrier();
-        float s = 0.0f;
-        for (int i = 0; i < 64; ++i)
-            if (i >= t) s += mg[i][t];
-        dg += s;
-        if (t0 + t < p.L) {
+        // lane i adds up its terms (i, j') over j' <= j, in place; then lane t what its row t - 1 holds of i >= t
+        float run = 0.0f;
+#pragma unroll 9
+        for (int j = 0; j < 63; ++j) {
+            run += t > j ? me[j][t] : 0.0f;
+            if (t > j) me[j][t] = run;
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        float mine = 0.0f;
+        if (t > 0) {
+#pragma unroll 8
+            for (int i = 0; i < 64; i += 4) {
+                const gf4 x = *reinterpret_cast<const gf4*>(&me[t - 1][i]);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) mine += i + r >= t ? x[r] : 0.0f;
+            }
+        }
+        dg += mine;
+        if (t < left) {
             const int64_t at = row0 + (int64_t)t * p.H;
             p.gr.dg[at] = p.reset && p.reset[b * p.L + t0 + t] ? 0.0f : dg;
             p.gr.dbeta[at] = z + colsum[0][t] + colsum[1][t] + colsum[2][t] + colsum[3][t];
         }
     }
-    // dq = aq + E' K;  dk = beta ax - av + (F + F^T) K + E'^T Q
-    gf4 dk[NS][4];
-#pragma unroll
-    for (int u = 0; u < NS; ++u)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) dk[u][i] = ax[u][i] * *reinterpret_cast<const gf4*>(&sco[kBeta][16 * i + 4 * g]) - av[u][i];
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-        typename M::F kf[NS];
-#pragma unroll
-        for (int u = 0; u < NS; ++u) kf[u] = M::template ldt<KD>(tk, s, w * NS + u, lane);
+    if (p.part_q) {
+        // heads that share keys: each head's share
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int r = 16 * i + m, c = 32 * s + 4 * g;
-            const auto ef = M::template split<M::NP>(gdr_pair(*reinterpret_cast<const gf4*>(&me[r][c]), *reinterpret_cast<const gf4*>(&me[r][c + 16])));
-            const auto ff = M::template split<M::NP>(gdr_pair(*reinterpret_cast<const gf4*>(&mf[r][c]), *reinterpret_cast<const gf4*>(&mf[r][c + 16])));
+            const int t = 16 * i + m;
+            if (t >= left) continue;
+            const int64_t at = (row0 + (int64_t)t * p.H) * p.dk;
 #pragma unroll
             for (int u = 0; u < NS; ++u) {
-                if (i >= 2 * s) aq[u][i] = M::template mul<M::NP>(ef, kf[u], aq[u][i]);
-                dk[u][i] = M::template mul<M::NP>(ff, kf[u], dk[u][i]);
+                const int q = w * NS + u, d = 32 * (q >> 1) + 8 * g + 4 * (q & 1);
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (d + r < p.dk) {
+                        p.part_q[at + d + r] = aq[u][i][r];
+                        p.part_k[at + d + r] = av[u][i][r];
+                    }
             }
         }
+        return;
     }
-    __syncthreads();
-    gdr_stage<T, KD>(tk, p.q, b, t0, p.L, hk, p.dk, p.vec);
-    __syncthreads();
+    // through the division by the length: d - x (x . d) / |x|^2
+    __syncthreads();                                  // (where both do not fit, LDS holds the queries by now)
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-        typename M::F qf[NS];
+    for (int i = 0; i < 4; ++i) {
+        float y = 0.0f, z = 0.0f;
 #pragma unroll
-        for (int u = 0; u < NS; ++u) qf[u] = M::template ldt<KD>(tk, s, w * NS + u, lane);
+        for (int u = 0; u < NS; ++u) {
+            const gf4 q4 = query4(i, w * NS + u);
+            gf4 k4;
+            if constexpr (BOTH) {
+                k4 = key4(tk, i, w * NS + u);
+            } else {
+                const int t = 16 * i + m, d = 32 * ((w * NS + u) >> 1) + 8 * g + 4 * ((w * NS + u) & 1);
 #pragma unroll
-        for (int i = 0; i < 2 * s + 2; ++i) {
-            gf8 e;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) e[j] = me[32 * s + 16 * (j >> 2) + 4 * g + (j & 3)][16 * i + m];
-            const auto ef = M::template split<M::NP>(e);
-#pragma unroll
-            for (int u = 0; u < NS; ++u) dk[u][i] = M::template mul<M::NP>(ef, qf[u], dk[u][i]);
-        }
-    }
-#pragma unroll
-    for (int u = 0; u < NS; ++u) {
-        const int d = (w * NS + u) * 16 + m;
-        if (d >= p.dk) continue;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
+                for (int r = 0; r < 4; ++r) k4[r] = d + r < p.dk ? gdr_f<T>(rk.base[(t0 + (t < left ? t : left - 1)) * rk.stride + d + r]) : 0.0f;
+            }
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int t = 16 * i + 4 * g + r;
-                if (t0 + t < p.L) {
-                    const int64_t at = (row0 + (int64_t)t * p.H) * p.dk + d;
-                    p.part_q[at] = aq[u][i][r];
-                    p.part_k[at] = dk[u][i][r];
-                }
+                y = __builtin_fmaf(q4[r], aq[u][i][r], y);
+                z = __builtin_fmaf(k4[r], av[u][i][r], z);
             }
+        }
+        y += __shfl_xor(y, 16, 64);
+        z += __shfl_xor(z, 16, 64);
+        y += __shfl_xor(y, 32, 64);
+        z += __shfl_xor(z, 32, 64);
+        if (g == 0) {
+            rows[0][w][16 * i + m] = y;
+            rows[1][w][16 * i + m] = z;
+        }
+    }
+    __syncthreads();
+    const unsigned row = (unsigned)(p.Hk * p.dk);
+    const GdrBuf<T> dqt(static_cast<T*>(p.gr.dq) + ((b * p.L + t0) * p.Hk + hk) * p.dk);
+    const GdrBuf<T> dkt(static_cast<T*>(p.gr.dk) + ((b * p.L + t0) * p.Hk + hk) * p.dk);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int t = 16 * i + m;
+        float cq = 0.0f, ck = 0.0f;
+        if (p.eps > 0.0f) {
+            const float rk2 = tok[tRk * 64 + t], rq2 = srq[t];
+            cq = (rows[0][0][t] + rows[0][1][t] + rows[0][2][t] + rows[0][3][t]) * rq2 * rq2;
+            ck = (rows[1][0][t] + rows[1][1][t] + rows[1][2][t] + rows[1][3][t]) * rk2 * rk2;
+        }
+        if (t >= left) continue;
+#pragma unroll
+        for (int u = 0; u < NS; ++u) {
+            const int q = w * NS + u, d = 32 * (q >> 1) + 8 * g + 4 * (q & 1);
+            const gf4 q4 = query4(i, q);
+            gf4 k4;
+            if constexpr (BOTH) {
+                k4 = key4(tk, i, q);
+            } else {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) k4[r] = d + r < p.dk ? gdr_f<T>(rk.base[(t0 + t) * rk.stride + d + r]) : 0.0f;
+            }
+            const gf4 oq = aq[u][i] - q4 * cq, ok = av[u][i] - k4 * ck;
+            const unsigned at = (t * row + d) * (unsigned)sizeof(T);
+            if (AL && p.vec_dk) {
+                if (d < p.dk) {
+                    dqt.st4(oq, at, 0);
+                    dkt.st4(ok, at, 0);
+                }
+            } else {
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (d + r < p.dk) {
+                        dqt.st(oq[r], at + r * (unsigned)sizeof(T), 0);
+                        dkt.st(ok[r], at + r * (unsigned)sizeof(T), 0);
+                    }
+            }
+        }
     }
 }
 
@@ -1725,11 +1823,11 @@ hipError_t launch_gdr_d(const LaunchGdr& p) {
     }
     const unsigned chunks = (unsigned)(BH * p.nchunks);
     const unsigned tiles = (unsigned)(BH * ((p.dv + 63) / 64));
+    constexpr bool kTwo = DKP * sizeof(T) <= 512;       // keys twice in LDS
+    constexpr int kGroups = DKP <= 128 && sizeof(T) == 2 ? 2 : 1;
+    const bool al = p.vec && p.vec_v && p.vec_y;
     if (p.pass == LaunchGdr::kFwd) {
-        constexpr bool kTwo = DKP * sizeof(T) <= 512;       // keys twice in LDS
-        constexpr int kGroups = DKP <= 128 && sizeof(T) == 2 ? 2 : 1;
-        hipLaunchKernelGGL((k_gdr_solve<T, DKP>), dim3((chunks + 3) / 4), dim3(256), 0, st, p);
-        const bool al = p.vec && p.vec_v && p.vec_y;
+        hipLaunchKernelGGL((k_gdr_solve<T, DKP, false>), dim3((chunks + 3) / 4), dim3(256), 0, st, p);
         if (p.nseg > 1) {
             const dim3 ends((unsigned)(BH * ((p.dv + 63) / 64 + (p.dk + 63) / 64) * (p.nseg - 1)));
             if (al) hipLaunchKernelGGL((k_gdr_ends<T, DKP, kTwo, true, kGroups>), ends, dim3(256), 0, st, p);
@@ -1739,10 +1837,17 @@ hipError_t launch_gdr_d(const LaunchGdr& p) {
         const dim3 walk((unsigned)(tiles * p.nseg));
         if (al) hipLaunchKernelGGL((k_gdr_walk<T, DKP, kTwo, true, kGroups>), walk, dim3(256), 0, st, p);
         else hipLaunchKernelGGL((k_gdr_walk<T, DKP, kTwo, false, kGroups>), walk, dim3(256), 0, st, p);
+        return hipGetLastError();
+    }
+    hipLaunchKernelGGL((k_gdr_solve<T, DKP, true>), dim3((chunks + 3) / 4), dim3(256), 0, st, p);
+    if (p.vec) {
+        hipLaunchKernelGGL((k_gdr_walk_back<T, DKP, true, kGroups>), dim3(tiles), dim3(256), 0, st, p);
+        hipLaunchKernelGGL((k_gdr_grads<T, DKP, true, kGroups>), dim3(chunks), dim3(256), 0, st, p);
     } else {
-        hipLaunchKernelGGL((k_gdr_prep<T, DKP, true>), dim3(chunks), dim3(256), 0, st, p);
-        hipLaunchKernelGGL((k_gdr_walk_back<T, DKP, 1>), dim3(tiles), dim3(256), 0, st, p);
-        hipLaunchKernelGGL((k_gdr_grads<T, DKP>), dim3(chunks), dim3(256), 0, st, p);
+        hipLaunchKernelGGL((k_gdr_walk_back<T, DKP, false, kGroups>), dim3(tiles), dim3(256), 0, st, p);
+        hipLaunchKernelGGL((k_gdr_grads<T, DKP, false, kGroups>), dim3(chunks), dim3(256), 0, st, p);
+    }
+    if (p.part_q) {
         const int64_t rows = (p.B * p.L * p.Hk + 3) / 4;
         hipLaunchKernelGGL((k_gdr_keys<T>), dim3((unsigned)(rows < 1 << 20 ? rows : 1 << 20), 2), dim3(256), 0, st, p);
     }

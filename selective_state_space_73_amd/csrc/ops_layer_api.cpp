@@ -13,7 +13,8 @@ namespace selscan {
 
 int64_t gdr_segment(int64_t BH, int64_t dv, int64_t nchunks) {
     const int64_t groups = BH * ((dv + 63) / 64);           // workgroups of one segment
-    const int64_t n = 512 / groups;                         // segments that run at the same time, two workgroups a CU
+    int64_t n = 512 / groups;                               // segments that run at the same time, two workgroups a CU
+    if (nchunks < 16 * n) n = 256 / groups;                 // short ones: one, which is faster alone, and fewer to join
     if (n < 2 || nchunks < 8) return nchunks;
     const int64_t seg = (nchunks + n - 1) / n;
     return seg < 4 ? 4 : seg;
@@ -35,8 +36,9 @@ ss_status check_gdr_dims(const ss_gdr_dims* d, GdrCall call) {
     if (d->heads % d->k_heads) return fail(SS_ERR_INVALID_ARG, "heads %d not a multiple of k_heads %d", d->heads, d->k_heads);
     if (d->dk > 256 || d->dv > 512) return fail(SS_ERR_UNSUPPORTED, "dk %d above 256 or dv %d above 512", d->dk, d->dv);
     if (d->io_dtype != SS_F32 && d->io_dtype != SS_BF16) return fail(SS_ERR_UNSUPPORTED, "io_dtype %d unknown", d->io_dtype);
-    // 64 tokens of y lie within 32-bit offsets
-    if ((int64_t)d->heads * d->dv > (int64_t(1) << 22)) return fail(SS_ERR_UNSUPPORTED, "heads x dv above 2^22");
+    // 64 tokens of y, and of the gradients of q and k, lie within 32-bit offsets
+    if ((int64_t)d->heads * d->dv > (int64_t(1) << 22) || (int64_t)d->k_heads * d->dk > (int64_t(1) << 22))
+        return fail(SS_ERR_UNSUPPORTED, "heads x dv or k_heads x dk above 2^22");
     if (!std::isfinite(d->scale)) return fail(SS_ERR_INVALID_ARG, "scale must be finite");
     if (!(d->eps >= 0.0f) || !std::isfinite(d->eps)) return fail(SS_ERR_INVALID_ARG, "eps must be finite and not negative");
     if (d->reserved != 0) return fail(SS_ERR_INVALID_ARG, "reserved must be 0");
@@ -55,17 +57,17 @@ size_t ckpt_states(const ss_gdr_dims& d) {
 }
 size_t ckpt_floats(const ss_gdr_dims& d) { return ckpt_states(d) + (size_t)d.batch * (size_t)d.seqlen * d.heads * d.dv; }
 
-// Per chunk and head: the tokens' factors, the inverse and P (6 blocks of 16 x 32 each). The backward
-// as well: the pairs of tokens, the state's gradient behind every chunk; the gradients of v in fp32, and those
-// of q and k by head of v.
-struct GdrLayout { size_t co, wT, wP, raw, wS, wV, pq, pk, wE, wM, wF, total; int64_t seg, nseg; };
+// Per chunk and head: the tokens' factors and the inverse (6 blocks of 16 x 32, three bf16 terms or fp32). The forward in
+// segments: the states behind them and what they make of the ones in front. The backward: the state's gradient behind every
+// chunk, the gradients of v in fp32, and those of q and k by head of v where heads share them.
+struct GdrLayout { size_t co, wT, wS, wV, pq, pk, wE, wM, wF, total; int64_t seg, nseg; };
 GdrLayout gdr_layout(const ss_gdr_dims& d, bool backward) {
     GdrLayout l{};
     const size_t n = (size_t)d.batch * d.heads * (size_t)ceil_div(d.seqlen, SS_GDR_CHUNK);
     const size_t rows = (size_t)d.batch * (size_t)d.seqlen * d.heads;
     size_t off = 0;
     auto take = [&](size_t& at, size_t floats) { at = off; off = align256(off + floats * 4); };
-    take(l.co, n * 8 * 64);
+    take(l.co, n * 10 * 64);
     take(l.wT, n * 9216);
     l.seg = ceil_div(d.seqlen, SS_GDR_CHUNK);
     l.nseg = 1;
@@ -81,12 +83,12 @@ GdrLayout gdr_layout(const ss_gdr_dims& d, bool backward) {
         }
     }
     if (backward) {
-        take(l.wP, n * 6 * 512);
-        take(l.raw, n * 30 * 256);
         take(l.wS, n * d.dk * d.dv);
         take(l.wV, rows * d.dv);
-        take(l.pq, rows * d.dk);
-        take(l.pk, rows * d.dk);
+        if (d.heads > d.k_heads) {
+            take(l.pq, rows * d.dk);
+            take(l.pk, rows * d.dk);
+        }
     }
     l.total = off;
     return l;
@@ -167,9 +169,8 @@ void gdr_attach(selscan::LaunchGdr& p, const ss_gdr_dims& d, const GdrLayout& l,
     p.nseg = (int)l.nseg;
     p.wE = at(l.wE); p.wM = at(l.wM); p.wF = at(l.wF);
     if (backward) {
-        p.wP = at(l.wP);
-        p.raw = at(l.raw); p.wS = at(l.wS); p.wV = at(l.wV);
-        p.part_q = at(l.pq); p.part_k = at(l.pk);
+        p.wS = at(l.wS); p.wV = at(l.wV);
+        if (d.heads > d.k_heads) { p.part_q = at(l.pq); p.part_k = at(l.pk); }
     }
 }
 
@@ -292,6 +293,9 @@ ss_status ss_gdr_bwd(const ss_gdr_dims* d, const ss_gdr_args* a, const ss_gdr_gr
     if ((s = check_overlaps(outs, 7, ins, 9)) != SS_OK) return s;
     gdr_attach(p, *d, l, workspace, true);
     p.gr = *g;
+    p.vec_dy = d->dv % 8 == 0 && (uintptr_t)g->dy % 16 == 0;
+    p.vec_ck = d->dv % 4 == 0 && d->dk * d->dv % 4 == 0 && (uintptr_t)a->ckpt % 16 == 0;
+    p.vec_dk = d->dk % 4 == 0 && (uintptr_t)g->dq % (4 * es) == 0 && (uintptr_t)g->dk % (4 * es) == 0;
     p.pass = selscan::LaunchGdr::kBwd;
     p.stream = stream;
     return launched(selscan::launch_gdr(p));

@@ -15,6 +15,8 @@ struct LaunchGdr {
     bool vec;                    // rows of q and k start on 16 bytes and hold whole accesses of 16 bytes
     bool vec_v;                  // 64 tokens of v lie within 32-bit offsets
     bool vec_y;                  // four columns of y are one access
+    bool vec_dy, vec_ck, vec_dk; // the backward: whole accesses of 16 bytes of the gradient of y, of the checkpoints and of the
+                                 // workspace, four columns of the gradients of q and k
     bool vec_state;              // the step: dv a multiple of 4, the state on 16 bytes
     int64_t B, L, nchunks;
     int H, Hk, dk, dv;
@@ -29,10 +31,9 @@ struct LaunchGdr {
     int nseg;
     float *wE, *wM, *wF;         // several segments: [nseg - 1, B, H, dk, dv] states behind the segments, [nseg - 1, B, H, dk, dk]
                                  // what they make of the state in front, [nseg - 1, B, H] whether anything of it is left
-    float *co, *wT, *wP;         // [B, H, chunks]: factors of tokens, inverse and P in the order of operands
-    float* raw;                  // the backward: [B, H, chunks, 3, 10, 256] pairs of tokens, the triangle's ten tiles of 16 x 16
+    float *co, *wT;              // [B, H, chunks]: factors of tokens, inverses in the order of operands
     float *wS, *wV;              // the backward: [B, H, chunks, dk, dv] adjoints behind the chunks, [B, L, H, dv] gradients of v
-    float *part_q, *part_k;      // the backward: [B, L, H, dk] each head's share
+    float *part_q, *part_k;      // the backward where heads share keys: [B, L, H, dk] each head's share
     void* stream;
 };
 // Chunks of a segment. One after the other a chunk takes about as long as any work of its 64 columns; with segments the
