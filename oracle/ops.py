@@ -174,3 +174,136 @@ def rounded_product(y, slack, wq, ws, out_half):
     off = half_step(y, per) + 2 * torch.as_tensor(slack, dtype=F64)
     sums = 2.0 ** -15
     return y @ values(wq, ws, square=True).T, off @ w.T + sums * ((y.abs() + off) @ w.T)
+
+
+# ---------------------------------------------------------------------------
+# the gated delta rule
+
+def _unit(x, eps):
+    return x if eps is None else x / torch.sqrt((x * x).sum(-1, keepdim=True) + eps)
+
+
+def gdr_fwd(q, k, v, g, beta, state=None, reset=None, scale=None, eps=1e-6):
+    """(y, final state), token after token; differentiable where an input asks for it. A log decay of
+    -200 or less, and a reset, is a decay of 0: the state in front of it is not read."""
+    q, k, v, g, beta = (t if t.requires_grad else t.detach().cpu().to(F64) for t in (q, k, v, g, beta))
+    B, L, Hk, K = q.shape
+    H, V = v.shape[2:]
+    q, k = (_unit(x, eps).repeat_interleave(H // Hk, 2) for x in (q, k))
+    scale = K ** -0.5 if scale is None else scale
+    S = torch.zeros(B, H, K, V, dtype=F64) if state is None else (state if state.requires_grad else state.cpu().to(F64))
+    cut = g <= -200.0
+    if reset is not None:
+        cut = cut | (reset.cpu() != 0)[..., None]
+    ys = []
+    for t in range(L):
+        gone = cut[:, t, :, None, None]
+        a = torch.exp(torch.where(gone, torch.zeros_like(g[:, t, :, None, None]), g[:, t, :, None, None]))
+        S = torch.where(gone, torch.zeros_like(S), S * a)
+        kt, qt = k[:, t, :, :, None], q[:, t, :, :, None]
+        u = beta[:, t, :, None] * (v[:, t] - (S * kt).sum(2))
+        S = S + kt * u[:, :, None, :]
+        ys.append(scale * (S * qt).sum(2))
+    y = torch.stack(ys, 1) if ys else torch.zeros(B, 0, H, V, dtype=F64)
+    return y, S
+
+
+def gdr_bwd(q, k, v, g, beta, dy, state=None, reset=None, dstate_final=None, scale=None, eps=1e-6):
+    """Gradients by the chain rule in reverse order, token after token: {name: value}."""
+    q0, k0, v, g, beta, dy = (t.detach().cpu().to(F64) for t in (q, k, v, g, beta, dy))
+    B, L, Hk, K = q0.shape
+    H, V = v.shape[2:]
+    rep = H // Hk
+    q, k = (_unit(x, eps).repeat_interleave(rep, 2) for x in (q0, k0))
+    scale = K ** -0.5 if scale is None else scale
+    a = torch.exp(g)
+    cut = g <= -200.0
+    if reset is not None:
+        cut = cut | (reset.cpu() != 0)[..., None]
+    S = torch.zeros(B, H, K, V, dtype=F64) if state is None else state.cpu().to(F64)
+    before, lack, after = [], [], []
+    for t in range(L):
+        S = torch.where(cut[:, t, :, None, None], torch.zeros_like(S), S * a[:, t, :, None, None])
+        before.append(S)
+        lack.append(v[:, t] - (S * k[:, t, :, :, None]).sum(2))
+        S = S + k[:, t, :, :, None] * (beta[:, t, :, None] * lack[t])[:, :, None, :]
+        after.append(S)
+    W = torch.zeros(B, H, K, V, dtype=F64) if dstate_final is None else dstate_final.cpu().to(F64)
+    dq, dk, dv, dg, db = (torch.zeros_like(x) for x in (q, k, v, g, beta))
+    for t in range(L - 1, -1, -1):
+        kt = k[:, t, :, :, None]
+        dq[:, t] = scale * (after[t] * dy[:, t, :, None, :]).sum(-1)
+        W = W + scale * q[:, t, :, :, None] * dy[:, t, :, None, :]
+        wk = (W * kt).sum(2)
+        db[:, t] = (wk * lack[t]).sum(-1)
+        dv[:, t] = beta[:, t, :, None] * wk
+        dk[:, t] = (W * (beta[:, t, :, None] * lack[t])[:, :, None, :]).sum(-1) - (before[t] * dv[:, t, :, None, :]).sum(-1)
+        W = W - kt * dv[:, t, :, None, :]
+        dg[:, t] = (before[t] * W).sum((-1, -2))
+        W = torch.where(cut[:, t, :, None, None], torch.zeros_like(W), W * a[:, t, :, None, None])
+
+    def keys(d, x):
+        d = d.reshape(B, L, Hk, rep, K).sum(3)
+        if eps is None:
+            return d
+        n2 = (x * x).sum(-1, keepdim=True) + eps
+        return (d - x * (x * d).sum(-1, keepdim=True) / n2) / torch.sqrt(n2)
+
+    return {"dq": keys(dq, q0), "dk": keys(dk, k0), "dv": dv, "dg": dg, "dbeta": db, "dstate_init": W}
+
+
+# ---------------------------------------------------------------------------
+# the norms around a layer
+
+def gnorm_fwd(y, w, gate=None, residual=None, scale=None, w_next=None, eps=1e-5):
+    """(s, n or None), differentiable where an input asks for it."""
+    y, w, gate, residual, scale, w_next = (t if t is None or t.requires_grad else t.detach().cpu().to(F64)
+                                           for t in (y, w, gate, residual, scale, w_next))
+    G = w.numel()
+    p = y.reshape(*y.shape[:-1], -1, G)
+    p = (p / torch.sqrt((p * p).mean(-1, keepdim=True) + eps) * w).reshape(y.shape)
+    h = p if gate is None else p * gate / (1.0 + torch.exp(-gate))
+    s = h if scale is None else scale * h
+    s = s if residual is None else residual + s
+    n = None if w_next is None else s / torch.sqrt((s * s).mean(-1, keepdim=True) + eps) * w_next
+    return s, n
+
+
+def gnorm_bwd(y, w, ds, dn=None, gate=None, residual=None, scale=None, w_next=None, eps=1e-5):
+    """Gradients by hand: {name: (value, what its terms reach)}."""
+    y, w, ds, dn, gate, residual, scale, w_next = (None if t is None else t.detach().cpu().to(F64)
+                                                   for t in (y, w, ds, dn, gate, residual, scale, w_next))
+    G, K = w.numel(), y.shape[-1]
+    y = y.reshape(-1, K)
+    M = y.shape[0]
+    ds = torch.zeros_like(y) if ds is None else ds.reshape(M, K)
+    yg = y.reshape(M, -1, G)
+    ly = torch.sqrt((yg * yg).mean(-1, keepdim=True) + eps)
+    yn = yg / ly
+    p = (yn * w).reshape(M, K)
+    z = None if gate is None else gate.reshape(M, K)
+    sig = None if z is None else 1.0 / (1.0 + torch.exp(-z))
+    act = torch.ones_like(p) if z is None else z * sig
+    al = torch.ones(K, dtype=F64) if scale is None else scale
+    s = al * act * p + (0.0 if residual is None else residual.reshape(M, K))
+    out = {}
+    if w_next is not None:
+        ls = torch.sqrt((s * s).mean(-1, keepdim=True) + eps)
+        dn = torch.zeros_like(y) if dn is None else dn.reshape(M, K)
+        out["dw_next"] = ((dn * s / ls).sum(0), (dn * s / ls).abs().sum(0))
+        t = dn * w_next
+        ds = ds + (t - s * (t * s).mean(-1, keepdim=True) / ls ** 2) / ls
+    if residual is not None:
+        out["dresidual"] = (ds, ds.abs().amax(-1, keepdim=True))
+    if scale is not None:
+        out["dscale"] = ((ds * act * p).sum(0), (ds * act * p).abs().sum(0))
+    dh = ds * al
+    if z is not None:
+        dz = dh * p * (sig + act * (1.0 - sig))
+        out["dgate"] = (dz, (dh * p).abs().amax(-1, keepdim=True))
+    dp = (dh * act).reshape(M, -1, G)
+    out["dw"] = ((dp * yn).sum((0, 1)), (dp * yn).abs().sum((0, 1)))
+    t = dp * w
+    dy = (t - yn * (t * yn).mean(-1, keepdim=True)) / ly
+    out["dy"] = (dy.reshape(M, K), (t.abs().amax(-1, keepdim=True) / ly).expand_as(t).reshape(M, K))
+    return out

@@ -1,0 +1,410 @@
+"""GPU: the gated delta rule against its 64-bit definition.
+
+Tolerances, with u = 2^-24. A token's value passes, per chunk of 64, sums of dk and of three times 64
+terms; every term and every addition rounds once, independently, at the size of its operands, which stay
+within what the definition has (|k^| = 1, beta <= 1: no state grows; the inverse's entries are at most
+1). So after c chunks of memory a value is off by about sqrt(2 (dk + 192) (c + 1)) u / sqrt(3) of the
+largest, and the worst of the up to 10^6 values that a test looks at by five times that. Operands as
+sums of three bf16 terms leave out u / 2 of themselves, the exponential of a decay adds the rounding of its argument,
+at most 2^-24 * 16 of a factor that is 2^-16 then. Gradients are products of two such quantities and sums over dv
+and dk. Hence
+    rel(dk, chunks) = 5 sqrt(2 (dk + 192) (min(chunks, 8) + 1)) 2^-24     forward (8 chunks remember all that counts here)
+twice that with dv in place of 192 added for gradients, all relative to the largest value of the tensor, plus half a
+step of the I/O type. Keys that are used as they are (eps None) have a length of about 1.
+"""
+import pytest
+import torch
+
+from oracle import ops as O
+
+pytestmark = pytest.mark.gpu
+
+ss = pytest.importorskip("selective_state_space_73_amd")
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+HALF = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8}
+GRADS = ("dq", "dk", "dv", "dg", "dbeta", "dstate_init")
+
+
+def rel(dk, L, more=0):
+    chunks = min(-(-L // 64), 8)
+    return 5 * (2 * (dk + 192 + more) * (chunks + 1)) ** 0.5 * 2.0 ** -24
+
+
+def make(B, L, Hk, H, K, V, io, seed=0, layout="plain", slow=False):
+    r = torch.Generator().manual_seed(300 + seed)
+    n = lambda *s: torch.randn(*s, generator=r).to(DT[io]).cuda()  # noqa: E731
+    if layout == "fused":                       # slices of one projection's output
+        p = n(B, L, 2 * Hk * K + H * V)
+        q, k, v = p[..., :Hk * K].view(B, L, Hk, K), p[..., Hk * K:2 * Hk * K].view(B, L, Hk, K), p[..., 2 * Hk * K:].view(B, L, H, V)
+    elif layout == "heads":                     # [B, H, L, d]
+        q, k, v = n(B, Hk, L, K).transpose(1, 2), n(B, Hk, L, K).transpose(1, 2), n(B, H, L, V).transpose(1, 2)
+    elif layout == "odd":                       # odd strides and an odd start
+        q, k = n(B, L + 1, Hk, K + 3)[:, 1:, :, 1:K + 1], n(B, L + 2, Hk, K + 5)[:, 2:, :, 3:K + 3]
+        v = n(B, L, H + 1, V + 1)[:, :, 1:, 1:]
+    else:
+        q, k, v = n(B, L, Hk, K), n(B, L, Hk, K), n(B, L, H, V)
+    g = -torch.rand(B, L, H, generator=r) * (2e-3 if slow else 0.3)
+    beta = torch.rand(B, L, H, generator=r)
+    return (q, k, v, g.cuda(), beta.cuda()), torch.randn(B, H, K, V, generator=r).cuda(), n(B, L, H, V), torch.randn(B, H, K, V, generator=r).cuda(), r
+
+
+def near(got, want, tol, io, scale=None, roundings=1):
+    got, want = got.detach().double().cpu(), want.double()
+    assert got.shape == want.shape
+    if not want.numel():
+        return
+    scale = want.abs().amax() if scale is None else scale
+    bound = tol * scale + roundings * HALF[io] * want.abs() * (1 + tol) + 1e-30
+    worst = ((got - want).abs() / bound).max().item()
+    print(f"worst error over bound {worst:.3f}", flush=True)
+    assert torch.isfinite(got).all() and worst <= 1.0
+
+
+def of_terms(name, want, x, dy, S0=None, dS=None):
+    """What an error is relative to. The gradient through a normalised key of one number is all but zero: r - k^ (k^ r)
+    with k^ = +-1 up to eps, so that r, the gradient of k^ over the key's length, is the size of the terms that cancel;
+    they are rounded at that size whatever is left of them. With more numbers than one something of that size is left."""
+    if name not in ("dq", "dk") or x[0].shape[-1] > 1:
+        return None
+    unit = [t.double() / (t.double() ** 2 + 1e-6).sqrt() for t in x[:2]]
+    r = O.gdr_bwd(*unit, *x[2:], dy, S0, None, dS, eps=None)[name]
+    return max(want.abs().max(), (r.cpu() / x[0 if name == "dq" else 1].double().cpu().abs()).abs().max())
+
+
+def run(x, S0=None, ck=True, **kw):
+    B, L, H, V = x[2].shape
+    S = None if S0 is None else S0.clone()
+    ckpt = torch.full(ss.gdr_ckpt_shape(B, L, H, x[0].shape[-1], V), float("nan"), device="cuda") if ck else None
+    return ss.ss_gdr_fwd(*x, state=S, ckpt=ckpt, **kw), S, ckpt
+
+
+def check(x, S0, dy, dS, io, reset=None, eps=1e-6, scale=None):
+    B, L, Hk, K = x[0].shape
+    V = x[2].shape[-1]
+    y, S, ck = run(x, S0, reset=reset, eps=eps, scale=scale)
+    yw, Sw = O.gdr_fwd(*x, S0, reset, scale, eps)
+    tol = rel(K, L)
+    near(y, yw, tol, io)
+    near(S, Sw, tol, "f32", torch.maximum(Sw.abs().max(), S0.abs().max().double().cpu()))
+    got = ss.ss_gdr_bwd(*x, ck, dy, reset=reset, dstate_final=dS, eps=eps, scale=scale)
+    want = O.gdr_bwd(*x, dy, S0, reset, dS, scale, eps)
+    for n in GRADS:
+        print(n, end=" ")
+        near(got[n], want[n], 2 * rel(K, L, V), io if n in ("dq", "dk", "dv") else "f32", of_terms(n, want[n], x, dy, S0, dS))
+    return y, S, got
+
+
+SHAPES = [(1, 1, 1, 1, 1, 1), (2, 1, 1, 2, 64, 64), (1, 2, 1, 1, 3, 5), (1, 63, 1, 1, 64, 16), (2, 64, 2, 2, 64, 64), (1, 65, 1, 3, 32, 33),
+          (1, 129, 2, 2, 128, 128), (2, 200, 1, 2, 100, 70), (1, 130, 1, 1, 129, 65), (1, 70, 1, 1, 256, 256), (1, 100, 3, 6, 96, 129),
+          (1, 66, 1, 1, 8, 300), (3, 80, 1, 1, 65, 512)]
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_forward_and_gradients(shape, io):
+    x, S0, dy, dS, _ = make(*shape, io, seed=sum(shape))
+    check(x, S0, dy, dS, io)
+    # without states: from zero, nothing returned, no gradient from behind
+    y, _, ck = run(x)
+    near(y, O.gdr_fwd(*x)[0], rel(shape[4], shape[1]), io)
+    got, want = ss.ss_gdr_bwd(*x, ck, dy), O.gdr_bwd(*x, dy)
+    for n in GRADS:
+        near(got[n], want[n], 2 * rel(shape[4], shape[1], shape[5]), io if n in ("dq", "dk", "dv") else "f32", of_terms(n, want[n], x, dy))
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("layout", ["fused", "heads", "odd"])
+@pytest.mark.parametrize("K,V", [(128, 128), (64, 40), (33, 17)])
+def test_layouts(layout, io, K, V):
+    x, S0, dy, dS, _ = make(2, 150, 2, 4, K, V, io, seed=K, layout=layout)
+    y, S, g = check(x, S0, dy, dS, io)
+    c = tuple(t.contiguous() for t in x)
+    y2, S2, ck = run(c, S0)
+    # two results, each within the tolerance and half a step of one definition
+    near(y, y2.double().cpu(), 2 * rel(K, 150) + HALF[io] ** 2, io, roundings=2)
+    near(S, S2.double().cpu(), 2 * rel(K, 150), "f32")
+    g2 = ss.ss_gdr_bwd(*c, ck, dy, dstate_final=dS)
+    for n in GRADS:
+        near(g[n], g2[n].double().cpu(), 4 * rel(K, 150, V) + HALF[io] ** 2, io if n in ("dq", "dk", "dv") else "f32", roundings=2)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("kind", ["dense", "rare", "all", "ends"])
+def test_resets(kind, io):
+    B, L = 2, 210
+    x, S0, dy, dS, r = make(B, L, 1, 2, 64, 48, io, seed=5)
+    z = (torch.rand(B, L, generator=r) < (0.5 if kind == "dense" else 0.02)).to(torch.uint8)
+    if kind == "all":
+        z = torch.ones(B, L, dtype=torch.uint8)
+    if kind == "ends":
+        z.zero_()
+        z[:, 0], z[:, -1] = 7, 1                 # any nonzero value
+    reset = z.cuda()
+    y, S, got = check(x, S0, dy, dS, io, reset=reset)
+    assert (got["dg"][reset != 0] == 0).all()
+    yb, Sb, _ = run(x, S0, reset=reset != 0)     # bool, too
+    assert torch.equal(y, yb) and torch.equal(S, Sb)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_decays_from_none_to_all(io):
+    """Log decays of 0, of minus infinity, of -250, of -1e-7, and far between."""
+    x, S0, dy, dS, r = make(1, 200, 1, 2, 64, 64, io, seed=9)
+    g = x[3]
+    g[:, 20:60] = 0.0
+    g[:, 70] = float("-inf")
+    g[:, 71] = -250.0
+    g[:, 90:100] = -1e-7
+    g[:, 110:130] = -30.0
+    g[:, 140] = -90.0
+    y, S, got = check(x, S0, dy, dS, io)
+    assert (got["dg"][:, 70:72] == 0).all()
+    x[4][:, 150:160] = 0.0                       # tokens that write nothing
+    check(x, S0, dy, dS, io)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_small_gradients_of_decays_keep_their_digits(io):
+    """A token whose decay is e^-20: the gradient of its log has that factor, and is right relative to itself."""
+    x, S0, dy, dS, _ = make(1, 100, 1, 1, 64, 64, io, seed=11)
+    x[3][:, 40] = -20.0
+    _, _, ck = run(x, S0)
+    got, want = ss.ss_gdr_bwd(*x, ck, dy, dstate_final=dS)["dg"], O.gdr_bwd(*x, dy, S0, None, dS)["dg"]
+    scale = want[:, 40].abs()
+    assert 0 < scale < 1e-6 * want.abs().max()
+    # its terms are the other tokens' times e^-20; they are no larger than the largest gradient of a decay of about 1
+    near(got[:, 40], want[:, 40], 2 * rel(64, 100, 64), "f32", want.abs().max() * 2.1e-9 * 64)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_keys_as_they_are_and_a_scale(io):
+    x, S0, dy, dS, _ = make(1, 140, 2, 2, 64, 32, io, seed=13)
+    x[1].mul_(64 ** -0.5)
+    check(x, S0, dy, dS, io, eps=None, scale=0.3)
+    check(x, S0, dy, dS, io, eps=None, scale=-1.0)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("slow", [False, True])
+@pytest.mark.parametrize("shape", [(1, 1100, 1, 1, 64, 64), (1, 1500, 1, 2, 100, 70), (2, 900, 1, 1, 128, 128)])
+def test_segments(shape, io, slow):
+    """Long sequences in few heads run as several segments; with slow decays a segment hands on what it makes of
+    the state in front, with fast ones nothing of that is left."""
+    x, S0, dy, dS, r = make(*shape, io, seed=17, slow=slow)
+    check(x, S0, dy, dS, io)
+    z = torch.zeros(shape[0], shape[1], dtype=torch.uint8)
+    z[:, shape[1] // 2] = 1
+    check(x, S0, dy, dS, io, reset=z.cuda())
+    if slow:
+        x[4].mul_(2.5)                           # beyond 2, where a state may grow: nothing is left out
+        x[3].sub_(0.05)
+        y, S, _ = run(x, S0)
+        yw, Sw = O.gdr_fwd(*x, S0)
+        # a state may grow by |1 - beta| = 1.5 e^-0.05 = 1.43 a token in the worst case; what it did grow to is the scale
+        near(S, Sw, 64 * rel(shape[4], shape[1]), "f32", max(Sw.abs().max(), yw.abs().max() * shape[4] ** 0.5))
+
+
+def test_pieces_equal_the_whole():
+    B, L, K, V = 2, 300, 64, 48
+    x, S0, _, _, _ = make(B, L, 1, 2, K, V, "f32")
+    y, S, _ = run(x, S0)
+    T, parts = S0.clone(), []
+    for a, b in ((0, 1), (1, 130), (130, 130), (130, 300)):
+        parts.append(ss.ss_gdr_fwd(*(t[:, a:b] if t.dim() == 4 else t[:, a:b].contiguous() for t in x), state=T))
+    near(torch.cat(parts, 1), y.double().cpu(), 2 * rel(K, L), "f32")
+    near(T, S.double().cpu(), 2 * rel(K, L), "f32")
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("S,Hk,H,K,V", [(1, 1, 1, 1, 1), (3, 2, 4, 64, 64), (5, 1, 3, 100, 70), (2, 1, 1, 256, 512), (64, 4, 4, 128, 128), (2, 1, 2, 33, 6)])
+def test_step(S, Hk, H, K, V, io):
+    x, S0, _, _, r = make(S, 4, Hk, H, K, V, io, seed=S + K)
+    rs = (torch.rand(S, generator=r) < 0.3).to(torch.uint8).cuda()
+    T, Sw = S0.clone(), S0
+    for t in range(4):
+        xt = tuple(a[:, t] if a.dim() == 4 else a[:, t].contiguous() for a in x)
+        y = ss.ss_gdr_step(*xt, T, reset=rs if t == 2 else None)
+        yw, Sw = O.gdr_fwd(*(a[:, None] for a in xt), Sw, rs[:, None] if t == 2 else None)
+        near(y, yw[:, 0], rel(K, 4), io)
+        near(T, Sw, rel(K, 4), "f32", S0.abs().max().double().cpu() + Sw.abs().max())
+    # keys as they are, a scale, rows at a stride
+    xt = tuple(a[:, 1] if a.dim() == 4 else a[:, 1].contiguous() for a in x)
+    T = S0.clone()
+    y = ss.ss_gdr_step(xt[0], xt[1] * 0 + 0.05, *xt[2:], T, eps=None, scale=2.0)
+    yw, Sw = O.gdr_fwd(xt[0][:, None], (xt[1] * 0 + 0.05)[:, None], *(a[:, None] for a in xt[2:]), S0, scale=2.0, eps=None)
+    near(y, yw[:, 0], rel(K, 4), io)
+    near(T, Sw, rel(K, 4), "f32", S0.abs().max().double().cpu() + Sw.abs().max())
+
+
+def test_step_continues_a_sequence():
+    x, S0, _, _, _ = make(2, 70, 1, 2, 64, 64, "bf16", seed=3)
+    y, S, _ = run(x, S0)
+    T = S0.clone()
+    ss.ss_gdr_fwd(*(t[:, :69] if t.dim() == 4 else t[:, :69].contiguous() for t in x), state=T)
+    yt = ss.ss_gdr_step(*(t[:, 69] if t.dim() == 4 else t[:, 69].contiguous() for t in x), T)
+    near(yt, y[:, 69].double().cpu(), 2 * rel(64, 70) + HALF["bf16"] ** 2, "bf16", roundings=2)
+    near(T, S.double().cpu(), 2 * rel(64, 70), "f32")
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_nothing_passes_a_decay_of_zero_between_chunks(io):
+    """A state of NaN in front of a reset, NaN and infinity in the chunk before one, gradients of NaN behind one."""
+    x, S0, dy, dS, _ = make(1, 320, 1, 1, 64, 64, io, seed=21)
+    z = torch.zeros(1, 320, dtype=torch.uint8, device="cuda")
+    z[0, 0] = z[0, 128] = 1
+    x[2][0, 70, 0, 3] = float("nan")
+    x[1][0, 80, 0, 5] = float("inf")
+    S0[:] = float("nan")
+    y, S, ck = run(x, S0, reset=z)
+    yw, _ = O.gdr_fwd(*(t[:, 128:] for t in x), None, z[:, 128:])
+    y1, _ = O.gdr_fwd(*(t[:, :64] for t in x), None, z[:, :64])
+    near(y[:, 128:], yw, rel(64, 320), io)
+    near(y[:, :64], y1, rel(64, 64), io)
+    assert torch.isnan(y[0, 64:128]).any() and torch.isfinite(S).all()
+    dy[0, 200] = float("nan")
+    got = ss.ss_gdr_bwd(*x, ck, dy, reset=z, dstate_final=dS)
+    want = O.gdr_bwd(*(t[:, :64] for t in x), dy[:, :64], None, z[:, :64])
+    for n in ("dq", "dv", "dbeta"):
+        assert torch.isfinite(got[n][:, 256:]).all()
+    assert (got["dstate_init"] == 0).all()
+    T = torch.full_like(S0, float("nan"))
+    one = tuple(t[:, 0] if t.dim() == 4 else t[:, 0].contiguous() for t in x)
+    ys = ss.ss_gdr_step(*one, T, reset=z[:, 0].contiguous())
+    near(ys, y1[:, 0], rel(64, 1), io)
+    assert torch.isfinite(T).all()
+
+
+def test_nan_reaches_what_depends_on_it():
+    x, S0, _, _, _ = make(1, 200, 1, 1, 64, 64, "f32", seed=23)
+    x[2][0, 100, 0, 7] = float("nan")
+    y, S, _ = run(x, S0)
+    assert torch.isfinite(y[0, :64]).all() and torch.isnan(y[0, 100:, 0, 7]).all() and torch.isfinite(y[..., 8:]).all()
+    assert torch.isnan(S[0, 0, :, 7]).all() and torch.isfinite(S[0, 0, :, 8:]).all()
+
+
+def test_runs_are_bit_equal_and_streams_do_not_mix():
+    sets = [make(1, 1300, 1, 2, 128, 64, io, seed=k) for k, io in ((1, "bf16"), (2, "bf16"))]
+    want = []
+    for x, S0, dy, dS, _ in sets:
+        y, S, ck = run(x, S0)
+        want.append([y, S, ck, *ss.ss_gdr_bwd(*x, ck, dy, dstate_final=dS).values()])
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    dims = ss.ss_gdr_dims(1, 1300, 1, 2, 128, 64, ss.SS_BF16, 1.0, 1e-6, 0)
+    torch.cuda.synchronize()
+    got = []
+    for n in range(6):
+        x, S0, dy, dS, _ = sets[n % 2]
+        ws = [torch.full((ss.ss_gdr_workspace_bytes(dims, b) + 64,), 0xAB, dtype=torch.uint8, device="cuda") for b in (False, True)]
+        S, ck = S0.clone(), torch.empty(ss.gdr_ckpt_shape(1, 1300, 2, 128, 64), device="cuda")
+        torch.cuda.synchronize()
+        y = ss.ss_gdr_fwd(*x, state=S, ckpt=ck, workspace=ws[0], stream=streams[n % 2])
+        g = ss.ss_gdr_bwd(*x, ck, dy, dstate_final=dS, workspace=ws[1], stream=streams[n % 2])
+        got.append([y, S, ck, *g.values(), *ws])
+    torch.cuda.synchronize()
+    for n, t in enumerate(got):
+        assert all(torch.equal(a, b) for a, b in zip(t, want[n % 2]))
+
+
+@pytest.mark.parametrize("shape", [(2, 150, 1, 2, 64, 64), (1, 1000, 1, 1, 64, 64)])
+def test_graph_replays(shape):
+    """A captured training step and decode step, replayed between eager work on the same tensors."""
+    x, S0, dy, dS, _ = make(*shape, "bf16", seed=31)
+    ck = torch.empty(ss.gdr_ckpt_shape(shape[0], shape[1], shape[3], shape[4], shape[5]), device="cuda")
+    one = tuple(t[:, 0] if t.dim() == 4 else t[:, 0].contiguous() for t in x)
+
+    def step(S):
+        y = ss.ss_gdr_fwd(*x, state=S, ckpt=ck)
+        g = ss.ss_gdr_bwd(*x, ck, dy, dstate_final=dS)
+        return [y, ss.ss_gdr_step(*one, S), *g.values()]
+
+    S = S0.clone()
+    step(S)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step(S)
+    for _ in range(4):
+        x[2].copy_(torch.randn_like(x[2]))
+        S.copy_(S0)
+        eager = [t.clone() for t in step(S)]
+        Se = S.clone()
+        torch.cuda.synchronize()
+        S.copy_(S0)
+        for t in outs:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(S, Se) and all(torch.equal(a, b) for a, b in zip(outs, eager))
+
+
+def test_outputs_end_where_they_should():
+    B, L, H, K, V = 1, 77, 2, 40, 30
+    x, S0, dy, _, _ = make(B, L, 1, H, K, V, "f32")
+    n = B * L * H * V
+    buf = torch.full((n + 256,), 5.0, device="cuda")
+    y = buf[128:128 + n].view(B, L, H, V)
+    m = S0.numel()
+    sb = torch.full((m + 256,), 7.0, device="cuda")
+    S = sb[128:128 + m].view_as(S0)
+    S.copy_(S0)
+    assert ss.ss_gdr_fwd(*x, state=S, y=y) is y
+    assert (buf[:128] == 5.0).all() and (buf[128 + n:] == 5.0).all() and (sb[:128] == 7.0).all() and (sb[128 + m:] == 7.0).all()
+
+
+def test_no_tokens():
+    x, S0, _, _, _ = make(2, 0, 1, 2, 64, 32, "bf16")
+    S = S0.clone()
+    assert ss.ss_gdr_fwd(*x, state=S).shape == (2, 0, 2, 32) and torch.equal(S, S0)
+
+
+def test_inference_mode_and_gradient_leaves():
+    x, S0, _, _, _ = make(1, 20, 1, 1, 16, 16, "f32")
+    want = run(x, S0)[0]
+    with torch.inference_mode():
+        assert torch.equal(ss.ss_gdr_fwd(*x, state=S0.clone()), want)
+    leaf = x[2].detach().clone().requires_grad_(True)
+    assert torch.equal(ss.ss_gdr_fwd(x[0], x[1], leaf, *x[3:], state=S0.clone()), want)
+
+
+def test_binding_refusals():
+    x, S0, dy, _, _ = make(1, 20, 1, 2, 16, 8, "f32")
+    q, k, v, g, beta = x
+    ck = torch.empty(ss.gdr_ckpt_shape(1, 20, 2, 16, 8), device="cuda")
+    for bad in ((q, k.bfloat16(), v, g, beta), (q.double(), k.double(), v.double(), g, beta), (q, k, v, g.bfloat16(), beta)):
+        with pytest.raises(TypeError):
+            ss.ss_gdr_fwd(*bad)
+    for bad in ((q[0], k[0], v[0], g, beta), (q, k[:, :10], v, g, beta), (q, k, v[:, :10], g, beta), (q, k, v, g[..., :1], beta),
+                (q, k.transpose(2, 3), v, g, beta), (q, k, v, g.transpose(0, 1), beta)):
+        with pytest.raises((ValueError, ss.SelscanError)):
+            ss.ss_gdr_fwd(*bad)
+    with pytest.raises(ValueError):
+        ss.ss_gdr_fwd(*x, state=S0[..., :4])
+    with pytest.raises(ValueError):
+        ss.ss_gdr_fwd(*x, ckpt=ck[:-1])
+    with pytest.raises(ValueError):
+        ss.ss_gdr_fwd(*x, workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError):
+        ss.ss_gdr_bwd(*x, None, dy)
+    with pytest.raises(ValueError):
+        ss.ss_gdr_step(*(t[:, 0] for t in x), None)
+    with pytest.raises(ss.SelscanError):
+        ss.ss_gdr_fwd(*x, eps=float("nan"))
+    with pytest.raises(ss.SelscanError):
+        ss.ss_gdr_fwd(*x, y=v)
+
+
+def test_offsets_past_32_bits():
+    """q and k as views with a stride of zero over a sequence whose values and outputs pass 4 GiB; the last tokens
+    against a short sequence, since a decay of e^-1 a token leaves nothing of what is more than 64 tokens back."""
+    L, V = (1 << 17) + 3, 512
+    H = 34
+    q, k = torch.randn(1, 1, 1, 16, device="cuda").bfloat16(), torch.randn(1, 1, 1, 16, device="cuda").bfloat16()
+    v = torch.randn(1, 1, H, V, device="cuda").bfloat16().expand(1, L, H, V)
+    g, beta = torch.full((1, L, H), -1.0, device="cuda"), torch.full((1, L, H), 0.5, device="cuda")
+    S = torch.zeros(1, H, 16, V, device="cuda")
+    y = ss.ss_gdr_fwd(q.expand(1, L, 1, 16), k.expand(1, L, 1, 16), v, g, beta, state=S)
+    assert y.numel() * 2 > 1 << 32
+    yw, Sw = O.gdr_fwd(q.expand(1, 100, 1, 16), k.expand(1, 100, 1, 16), v[:, :100], g[:, :100], beta[:, :100])
+    near(y[:, :100], yw, rel(16, 128), "bf16")
+    near(y[:, -1], yw[:, -1], rel(16, 512), "bf16")
+    near(S, Sw, rel(16, 512), "f32")
