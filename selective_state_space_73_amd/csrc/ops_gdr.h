@@ -46,21 +46,26 @@ template <> struct Mx<uint16_t> {
     typedef gb8 F;
     template <int N> struct S { gb8 t[N]; };
     static __device__ __forceinline__ F ld(const uint16_t* p) { return *reinterpret_cast<const gb8*>(p); }
-    // (two values a conversion, and their floats back from its halves)
+    // Two values a conversion; what each leaves, v - its term, by the product of two pairs with (-1, 0) or (0, -1), which is
+    // exact and one instruction where taking the term out of its half would be another. (The pair is a register: as
+    // an immediate it is taken for a float's, with -1 in the upper half.)
     template <int N>
     static __device__ __forceinline__ S<N> split(gf8 v) {
         typedef __bf16 gb2 __attribute__((ext_vector_type(2)));
         typedef float gf2 __attribute__((ext_vector_type(2)));
+        uint32_t lower = 0x0000bf80u, upper = 0xbf800000u;
+        asm("" : "+s"(lower), "+s"(upper));
         S<N> s;
 #pragma unroll
         for (int k = 0; k < N; ++k) {
             gu4 u;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                u[j] = __builtin_bit_cast(uint32_t, __builtin_convertvector(gf2{v[2 * j], v[2 * j + 1]}, gb2));
+                const gb2 t = __builtin_convertvector(gf2{v[2 * j], v[2 * j + 1]}, gb2);
+                u[j] = __builtin_bit_cast(uint32_t, t);
                 if (k + 1 < N) {
-                    v[2 * j] -= __builtin_bit_cast(float, u[j] << 16);
-                    v[2 * j + 1] -= __builtin_bit_cast(float, u[j] & 0xffff0000u);
+                    v[2 * j] = __builtin_amdgcn_fdot2_f32_bf16(t, __builtin_bit_cast(gb2, lower), v[2 * j], false);
+                    v[2 * j + 1] = __builtin_amdgcn_fdot2_f32_bf16(t, __builtin_bit_cast(gb2, upper), v[2 * j + 1], false);
                 }
             }
             s.t[k] = __builtin_bit_cast(gb8, u);
@@ -223,14 +228,35 @@ __device__ __forceinline__ typename Mx<T>::template S<N> gdr_terms(const T* base
     return f;
 }
 
-// Elements at a lane's offset and the wave's, in bytes, from a chunk's start: no 64-bit address per element.
+// Elements at a lane's offset and the wave's, in bytes, from a chunk's start: no 64-bit address per element. At `bytes` and
+// behind it nothing is stored and zeros are read, so that the last rows and columns need no branch: a lane that has none is
+// at kGdrOut. (The wave's part is below `bytes` wherever it is used.)
+constexpr unsigned kGdrOut = 0x80000000u;
 template <typename T>
 struct GdrBuf {
     __amdgpu_buffer_rsrc_t r;
-    __device__ __forceinline__ explicit GdrBuf(const T* p) : r(__builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(p), 0, -1, kBufDword3)) {}
+    __device__ __forceinline__ explicit GdrBuf(const T* p, unsigned bytes = ~0u)
+        : r(__builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(p), 0, (int)bytes, kBufDword3)) {}
     __device__ __forceinline__ T ld(unsigned lane, unsigned wave) const {
         if constexpr (sizeof(T) == 2) return __builtin_amdgcn_raw_buffer_load_b16(r, lane, wave, 0);
         else return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, lane, wave, 0));
+    }
+    __device__ __forceinline__ gu4 ld16(unsigned lane) const { return __builtin_amdgcn_raw_buffer_load_b128(r, lane, 0, 0); }
+    // eight values from column c of n on, `at` bytes from the start: vec: rows are whole accesses
+    __device__ __forceinline__ void ld8(unsigned at, int c, int n, bool vec, T* out) const {
+        constexpr int E = 16 / (int)sizeof(T);
+        if (vec) {
+#pragma unroll
+            for (int e = 0; e < 8 / E; ++e) reinterpret_cast<gu4*>(out)[e] = ld16(c + e * E < n ? at + e * 16 : kGdrOut);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) out[j] = ld(c + j < n ? at + j * (unsigned)sizeof(T) : kGdrOut, 0);
+        }
+    }
+    __device__ __forceinline__ gf8 ld8(unsigned at, int c, int n, bool vec) const {
+        alignas(16) T x[8];
+        ld8(at, c, n, vec, x);
+        return __builtin_bit_cast(gf8, x);
     }
     __device__ __forceinline__ void st(float v, unsigned lane, unsigned wave) const {
         if constexpr (sizeof(T) == 2) __builtin_amdgcn_raw_buffer_store_b16(IO<T>::bits(v), r, lane, wave, 0);
@@ -589,14 +615,15 @@ struct GdrWalk {
         const int64_t t0 = n * kGdrC;
         const T* at = vb + t0 * p.v.token_stride;
         const int c = in ? col : p.dv - 1, last = p.L - t0 < kGdrC ? (int)(p.L - t0) - 1 : kGdrC - 1;
-        const GdrBuf<T> buf(at);
         unsigned row = (unsigned)p.v.token_stride * (unsigned)sizeof(T);
         if (AL && last == kGdrC - 1) {
-            const unsigned lo = 4 * g * row + c * (unsigned)sizeof(T);
             asm volatile("" : "+s"(row));
+            const GdrBuf<T> buf(at);
+            const unsigned lo = 4 * g * row + c * (unsigned)sizeof(T);
 #pragma unroll
             for (int i = 0; i < 16; ++i) v[i] = buf.ld(lo, (16 * (i >> 2) + (i & 3)) * row);
         } else {
+            const GdrBuf<T> buf(at);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 const int t = 16 * (i >> 2) + 4 * g + (i & 3), u = t < last ? t : last;
@@ -613,18 +640,19 @@ struct GdrWalk {
         gdr_arrived();
         if (TWO && n + 1 < end_n) rk.load(tn, t0 + kGdrC, p.L);
         if (OUT && p.ckpt) {
-            const GdrBuf<float> ck(p.ckpt + (bh * nc + n) * p.dk * p.dv);
             unsigned dvb = p.dv * 4;
             asm volatile("" : "+s"(dvb));             // offsets made where they are used, not kept over the loop
-            const unsigned lo = 8 * g * dvb + col * 4;
-            if (in)
+            const GdrBuf<float> ck(p.ckpt + (bh * nc + n) * p.dk * p.dv, p.dk * dvb);
+            const unsigned lo = in ? 8 * g * dvb + col * 4 : kGdrOut;
 #pragma unroll
-                for (int s = 0; s < KD; ++s) {
-                    if (AL && 32 * s + 8 * g >= p.dk) continue;
+            for (int s = 0; s < KD; ++s) {
+                if (32 * s >= p.dk) break;            // (aligned rows: dk is a multiple of 8, whole eights are there or not)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (AL || 32 * s + 8 * g + e < p.dk) ck.st(S[2 * s + (e >> 2)][e & 3], lo, (32 * s + e) * dvb);
+                for (int e = 0; e < 8; ++e) {
+                    if constexpr (AL) ck.st(S[2 * s + (e >> 2)][e & 3], lo, (32 * s + e) * dvb);
+                    else ck.st(S[2 * s + (e >> 2)][e & 3], lo + (32 * s + e) * dvb, 0);
                 }
+            }
         }
         // K S0; Q S0 transposed (a lane has a token's row), which is how it is stored; P's row tile of this wave, transposed
         // too, without the queries' lengths; and these lengths, a diagonal. The next fragments are read ahead of
@@ -748,27 +776,29 @@ struct GdrWalk {
             const int left = p.L - t0 < kGdrC ? (int)(p.L - t0) : kGdrC;
             unsigned row = (unsigned)(p.H * p.dv);
             asm volatile("" : "+s"(row));
-            const GdrBuf<T> yt(yb + t0 * row);
+            const unsigned size = (left - 1) * row + p.dv;
+            const GdrBuf<T> yt(yb + t0 * row, size * (unsigned)sizeof(T));
             const int c0 = col - m + 4 * g;
             const unsigned lo = (m * row + c0) * (unsigned)sizeof(T);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
+                if (16 * i >= left) break;
                 qs[i] *= srq[16 * i + m];
                 if constexpr (AL) {
-                    if (16 * i + m < left && c0 < p.dv) yt.st4(qs[i], lo, 16 * i * row * (unsigned)sizeof(T));
+                    yt.st4(qs[i], c0 < p.dv ? lo : kGdrOut, 16 * i * row * (unsigned)sizeof(T));
                 } else {
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        if (16 * i + m < left && c0 + r < p.dv) yt.st(qs[i][r], lo + r * (unsigned)sizeof(T), 16 * i * row * (unsigned)sizeof(T));
+                    for (int r = 0; r < 4; ++r) yt.st(qs[i][r], c0 + r < p.dv ? lo + r * (unsigned)sizeof(T) : kGdrOut, 16 * i * row * (unsigned)sizeof(T));
                 }
             }
-            if (p.ckpt && in) {
-                const GdrBuf<float> xt(p.ckptX + ((b * p.L + t0) * p.H + h) * p.dv);
+            if (p.ckpt) {
+                const GdrBuf<float> xt(p.ckptX + ((b * p.L + t0) * p.H + h) * p.dv, size * 4);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < 4; ++i) {
+                    if (16 * i >= left) break;
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        if (16 * i + 4 * g + r < left) xt.st(X[i][r], (4 * g * row + col) * 4, (16 * i + r) * row * 4);
+                    for (int r = 0; r < 4; ++r) xt.st(X[i][r], in ? ((4 * g + r) * row + col) * 4 : kGdrOut, 16 * i * row * 4);
+                }
             }
         }
         }
@@ -1032,18 +1062,19 @@ struct GdrWalkBack {
         const int64_t t0 = n * kGdrC, id = bh * nc + n;
         gdr_arrived();
         {
-            const GdrBuf<float> ws(p.wS + id * p.dk * p.dv);
             unsigned dvb = p.dv * 4;
             asm volatile("" : "+s"(dvb));
-            const unsigned lo = 8 * g * dvb + col * 4;
-            if (in)
+            const GdrBuf<float> ws(p.wS + id * p.dk * p.dv, p.dk * dvb);
+            const unsigned lo = in ? 8 * g * dvb + col * 4 : kGdrOut;
 #pragma unroll
-                for (int s = 0; s < KD; ++s) {
-                    if (AL && 32 * s + 8 * g >= p.dk) continue;
+            for (int s = 0; s < KD; ++s) {
+                if (32 * s >= p.dk) break;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (AL || 32 * s + 8 * g + e < p.dk) ws.st(S[2 * s + (e >> 2)][e & 3], lo, (32 * s + e) * dvb);
+                for (int e = 0; e < 8; ++e) {
+                    if constexpr (AL) ws.st(S[2 * s + (e >> 2)][e & 3], lo, (32 * s + e) * dvb);
+                    else ws.st(S[2 * s + (e >> 2)][e & 3], lo + (32 * s + e) * dvb, 0);
                 }
+            }
         }
         // K W, and P's row tile of this wave (a lane has a key's column) with its queries' lengths, a diagonal
         gf4 dX[4] = {}, pt[4] = {}, len = {0, 0, 0, 0};
@@ -1152,22 +1183,24 @@ struct GdrWalkBack {
             factors(n - 1);
             values(n - 1);
         }
-        if (in) {
+        {
             unsigned row = (unsigned)(p.H * p.dv);
             asm volatile("" : "+s"(row));
             const int64_t at = ((b * p.L + t0) * p.H + h) * p.dv;
-            const GdrBuf<T> dvt(static_cast<T*>(p.gr.dv) + at);
-            const GdrBuf<float> wvt(p.wV + at);
             const int left = p.L - t0 < kGdrC ? (int)(p.L - t0) : kGdrC;
-            const unsigned lo = 4 * g * row + col;
+            const unsigned size = (left - 1) * row + p.dv;
+            const GdrBuf<T> dvt(static_cast<T*>(p.gr.dv) + at, size * (unsigned)sizeof(T));
+            const GdrBuf<float> wvt(p.wV + at, size * 4);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 4; ++i) {
+                if (16 * i >= left) break;
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    if (16 * i + 4 * g + r < left) {
-                        dvt.st(dV[i][r], lo * (unsigned)sizeof(T), (16 * i + r) * row * (unsigned)sizeof(T));
-                        wvt.st(dV[i][r], lo * 4, (16 * i + r) * row * 4);
-                    }
+                for (int r = 0; r < 4; ++r) {
+                    const unsigned lo = (4 * g + r) * row + col;
+                    dvt.st(dV[i][r], in ? lo * (unsigned)sizeof(T) : kGdrOut, 16 * i * row * (unsigned)sizeof(T));
+                    wvt.st(dV[i][r], in ? lo * 4 : kGdrOut, 16 * i * row * 4);
+                }
+            }
         }
         // the gradient of the state in front
         {
@@ -1306,21 +1339,26 @@ k_gdr_grads(const LaunchGdr p) {
 
     // what a lane brings of 32 columns: an eight of X, dV and dY for LDS, and its rows of S0 and W
     const int64_t kv = (int64_t)p.dk * p.dv, row0 = (b * p.L + t0) * p.H + h;
-    const int ts = tid >> 2, tr = ts < left ? ts : left - 1, octet = tid & 3;
-    const int64_t at0 = (row0 + (int64_t)tr * p.H) * p.dv;
-    const float *S0 = p.ckpt + id * kv, *W = p.wS + id * kv;
+    const int ts = tid >> 2, octet = tid & 3;
+    const unsigned row_v = (unsigned)(p.H * p.dv), size_v = (left - 1) * row_v + p.dv, size_s = (unsigned)kv * 4;
+    const GdrBuf<float> bx(p.ckptX + row0 * p.dv, size_v * 4), bv(p.wV + row0 * p.dv, size_v * 4);
+    const GdrBuf<T> bo(static_cast<const T*>(p.gr.dy) + row0 * p.dv, size_v * (unsigned)sizeof(T));
+    const GdrBuf<float> bs(p.ckpt + id * kv, size_s), bw(p.wS + id * kv, size_s);
+    const int d0 = 8 * (m >> 2) + (m & 3);
     gf8 nx, nv, ns[NS], nw[NS];
     alignas(16) T ny[8];
-    auto fetch = [&](int c0) {
+    auto fetch = [&](int c0) {                        // zeros behind the last token, as it has no gradient, and past dk and dv
         const int c = c0 + octet * 8;
-        nx = gdr_ld8(p.ckptX + at0, c, p.dv, true, p.vec_ck);
-        nv = gdr_ld8(p.wV + at0, c, p.dv, true, p.vec_ck);
-        gdr_row8<T>(static_cast<const T*>(p.gr.dy) + at0, c, p.dv, p.vec_dy, true, ny);
+        const unsigned at = ts * row_v + c;
+        nx = bx.ld8(at * 4, c, p.dv, p.vec_ck);
+        nv = bv.ld8(at * 4, c, p.dv, p.vec_ck);
+        bo.ld8(at * (unsigned)sizeof(T), c, p.dv, p.vec_dy, ny);
 #pragma unroll
         for (int u = 0; u < NS; ++u) {
-            const int q = w * NS + u, d = 32 * (q >> 1) + 8 * (m >> 2) + 4 * (q & 1) + (m & 3);
-            ns[u] = gdr_ld8(S0 + (int64_t)d * p.dv, c0 + 8 * g, p.dv, d < p.dk, p.vec_ck);
-            nw[u] = gdr_ld8(W + (int64_t)d * p.dv, c0 + 8 * g, p.dv, d < p.dk, p.vec_ck);
+            const int q = w * NS + u, e = c0 + 8 * g;
+            const unsigned to = (unsigned)((32 * (q >> 1) + 4 * (q & 1) + d0) * p.dv + e) * 4;
+            ns[u] = bs.ld8(to, e, p.dv, p.vec_ck);
+            nw[u] = bw.ld8(to, e, p.dv, p.vec_ck);
         }
     };
     gf4 aq[NS][4] = {}, av[NS][4] = {}, ax[NS][4] = {}, ae[3] = {}, af[3] = {};
@@ -1329,12 +1367,6 @@ k_gdr_grads(const LaunchGdr p) {
     for (int c0 = 0; c0 < p.dv; c0 += 32) {
         __syncthreads();
         {
-            // rows behind the last token are copies of it: their gradients are not
-            if (ts >= left) {
-                nx = nv = gf8{0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll
-                for (int j = 0; j < 8; ++j) ny[j] = T(0);
-            }
             const auto x = M::template split<M::NT>(nx), v = M::template split<M::NT>(nv);
             const int unit = ts >> 4, pl = gdr_place(octet, ts & 15);
             auto put = [&](T* to, const typename M::F& f) {
