@@ -242,10 +242,12 @@ struct GdrBuf {
         else return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, lane, wave, 0));
     }
     __device__ __forceinline__ gu4 ld16(unsigned lane) const { return __builtin_amdgcn_raw_buffer_load_b128(r, lane, 0, 0); }
-    // eight values from column c of n on, `at` bytes from the start: vec: rows are whole accesses
-    __device__ __forceinline__ void ld8(unsigned at, int c, int n, bool vec, T* out) const {
+    // eight values from column c of n on, `at` bytes from the start. VEC: rows are whole accesses of 16 bytes (known when
+    // compiling: where two ways to load meet, the values are copied, and the copy waits for them)
+    template <bool VEC>
+    __device__ __forceinline__ void ld8(unsigned at, int c, int n, T* out) const {
         constexpr int E = 16 / (int)sizeof(T);
-        if (vec) {
+        if constexpr (VEC) {
 #pragma unroll
             for (int e = 0; e < 8 / E; ++e) reinterpret_cast<gu4*>(out)[e] = ld16(c + e * E < n ? at + e * 16 : kGdrOut);
         } else {
@@ -253,9 +255,10 @@ struct GdrBuf {
             for (int j = 0; j < 8; ++j) out[j] = ld(c + j < n ? at + j * (unsigned)sizeof(T) : kGdrOut, 0);
         }
     }
-    __device__ __forceinline__ gf8 ld8(unsigned at, int c, int n, bool vec) const {
+    template <bool VEC>
+    __device__ __forceinline__ gf8 ld8(unsigned at, int c, int n) const {
         alignas(16) T x[8];
-        ld8(at, c, n, vec, x);
+        ld8<VEC>(at, c, n, x);
         return __builtin_bit_cast(gf8, x);
     }
     __device__ __forceinline__ void st(float v, unsigned lane, unsigned wave) const {
@@ -1309,12 +1312,12 @@ k_gdr_walk_back(const LaunchGdr p) {
 // A wave has a quarter of dk, transposed (a lane has a token): sums over dk are sums over registers and two moves, factors
 // of tokens one register, and four neighbouring columns one store. Terms over dv go through LDS 32 at a time, the next
 // ones on their way to registers meanwhile.
-template <typename T, int DKP, bool AL, int GROUPS>
+template <typename T, int DKP, bool AL, bool VEC, int GROUPS>
 __global__ void __launch_bounds__(256, GROUPS)
 k_gdr_grads(const LaunchGdr p) {
     using M = Mx<T>;
     constexpr int KD = DKP / 32, NS = DKP / 64, LD = 68, SL = 4 * 512;      // SL: 64 rows of 32 terms
-    constexpr bool BOTH = 2 * 64 * DKP * (int)sizeof(T) <= 98304;          // keys and queries fit in LDS side by side
+    constexpr bool BOTH = 2 * 64 * DKP * (int)sizeof(T) <= 32768;          // keys and queries lie in LDS side by side
     constexpr int kPhase1 = (2 * M::NT + 1) * SL * (int)sizeof(T), kPhase2 = 2 * 64 * LD * 4;
     __shared__ alignas(16) T tk[64 * DKP], tq_[BOTH ? 64 * DKP : 8];
     __shared__ alignas(16) char lds[kPhase1 > kPhase2 ? kPhase1 : kPhase2];
@@ -1332,11 +1335,6 @@ k_gdr_grads(const LaunchGdr p) {
         if (BOTH) gdr_clear<64 * DKP>(tq_);
         __syncthreads();
     }
-    rk.load(tk, t0, p.L);
-    if (BOTH) rq.load(tq, t0, p.L);
-    for (int e = tid; e < kGdrTokAll * 64; e += 256) tok[e] = p.co[id * (kGdrTokAll * 64) + e];
-    colsum[tid >> 6][tid & 63] = 0.0f;
-
     // what a lane brings of 32 columns: an eight of X, dV and dY for LDS, and its rows of S0 and W
     const int64_t kv = (int64_t)p.dk * p.dv, row0 = (b * p.L + t0) * p.H + h;
     const int ts = tid >> 2, octet = tid & 3;
@@ -1347,23 +1345,31 @@ k_gdr_grads(const LaunchGdr p) {
     const int d0 = 8 * (m >> 2) + (m & 3);
     gf8 nx, nv, ns[NS], nw[NS];
     alignas(16) T ny[8];
-    auto fetch = [&](int c0) {                        // zeros behind the last token, as it has no gradient, and past dk and dv
+    // (zeros behind the last token, as it has no gradient, and past dk and dv)
+    auto fetch_rows = [&](int c0) {
         const int c = c0 + octet * 8;
         const unsigned at = ts * row_v + c;
-        nx = bx.ld8(at * 4, c, p.dv, p.vec_ck);
-        nv = bv.ld8(at * 4, c, p.dv, p.vec_ck);
-        bo.ld8(at * (unsigned)sizeof(T), c, p.dv, p.vec_dy, ny);
+        nx = bx.template ld8<VEC>(at * 4, c, p.dv);
+        nv = bv.template ld8<VEC>(at * 4, c, p.dv);
+        bo.template ld8<VEC>(at * (unsigned)sizeof(T), c, p.dv, ny);
+    };
+    auto fetch_state = [&](const GdrBuf<float>& from, int c0, gf8 (&to)[NS]) {
 #pragma unroll
         for (int u = 0; u < NS; ++u) {
             const int q = w * NS + u, e = c0 + 8 * g;
-            const unsigned to = (unsigned)((32 * (q >> 1) + 4 * (q & 1) + d0) * p.dv + e) * 4;
-            ns[u] = bs.ld8(to, e, p.dv, p.vec_ck);
-            nw[u] = bw.ld8(to, e, p.dv, p.vec_ck);
+            to[u] = from.template ld8<VEC>((unsigned)((32 * (q >> 1) + 4 * (q & 1) + d0) * p.dv + e) * 4, e, p.dv);
         }
     };
     gf4 aq[NS][4] = {}, av[NS][4] = {}, ax[NS][4] = {}, ae[3] = {}, af[3] = {};
     float ww = 0.0f;
-    fetch(0);
+    fetch_rows(0);
+    fetch_state(bs, 0, ns);
+    fetch_state(bw, 0, nw);
+    rk.load(tk, t0, p.L);                             // behind what is needed first
+    if (BOTH) rq.load(tq, t0, p.L);
+    if (w * 64 + lane < kGdrTokAll * 16)
+        GdrSource(p.co + id * (kGdrTokAll * 64)).to_lds(reinterpret_cast<gu4*>(tok + w * 256), lane * 16, w * 1024);
+    colsum[tid >> 6][tid & 63] = 0.0f;
     for (int c0 = 0; c0 < p.dv; c0 += 32) {
         __syncthreads();
         {
@@ -1381,34 +1387,56 @@ k_gdr_grads(const LaunchGdr p) {
             for (int k = 0; k < M::NT; ++k) { put(lx[k], x.t[k]); put(lv[k], v.t[k]); }
             put(lo, __builtin_bit_cast(typename M::F, ny));
         }
-        typename M::template S<M::NT> sb[NS], wb[NS];
-#pragma unroll
-        for (int u = 0; u < NS; ++u) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) ww = __builtin_fmaf(ns[u][j], nw[u][j], ww);
-            sb[u] = M::template split<M::NT>(ns[u]);
-            wb[u] = M::template split<M::NT>(nw[u]);
-        }
         __syncthreads();
-        if (c0 + 32 < p.dv) fetch(c0 + 32);
+        // one of S0 and W as terms at a time, the next of its kind on the way into its registers meanwhile: both at once
+        // would not fit
+        const bool more = c0 + 32 < p.dv;
+        if (more) fetch_rows(c0 + 32);
+        {
+            typename M::template S<M::NT> sb[NS];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            typename M::template S<M::NT> xf, vf;
+            for (int u = 0; u < NS; ++u) {
 #pragma unroll
-            for (int k = 0; k < M::NT; ++k) { xf.t[k] = gdr_rows_frag<T>(lx[k], i, place); vf.t[k] = gdr_rows_frag<T>(lv[k], i, place); }
-            const auto of = gdr_rows_frag<T>(lo, i, place);
-            M::template each<M::NT>([&](int a, int c) {
+                for (int j = 0; j < 8; ++j) ww = __builtin_fmaf(ns[u][j], nw[u][j], ww);
+                sb[u] = M::template split<M::NT>(ns[u]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            if (more) fetch_state(bs, c0 + 32, ns);
 #pragma unroll
-                for (int u = 0; u < NS; ++u) {
-                    av[u][i] = M::mm(sb[u].t[a], vf.t[c], av[u][i]);
-                    ax[u][i] = M::mm(wb[u].t[a], xf.t[c], ax[u][i]);
-                }
-            });
+            for (int i = 0; i < 4; ++i) {
+                typename M::template S<M::NT> vf;
 #pragma unroll
-            for (int k = M::NT - 1; k >= 0; --k)
+                for (int k = 0; k < M::NT; ++k) vf.t[k] = gdr_rows_frag<T>(lv[k], i, place);
+                const auto of = gdr_rows_frag<T>(lo, i, place);
+                M::template each<M::NT>([&](int a, int c) {
 #pragma unroll
-                for (int u = 0; u < NS; ++u) aq[u][i] = M::mm(sb[u].t[k], of, aq[u][i]);
+                    for (int u = 0; u < NS; ++u) av[u][i] = M::mm(sb[u].t[a], vf.t[c], av[u][i]);
+                });
+#pragma unroll
+                for (int k = M::NT - 1; k >= 0; --k)
+#pragma unroll
+                    for (int u = 0; u < NS; ++u) aq[u][i] = M::mm(sb[u].t[k], of, aq[u][i]);
+            }
         }
+        __builtin_amdgcn_sched_barrier(0);
+        {
+            typename M::template S<M::NT> wb[NS];
+#pragma unroll
+            for (int u = 0; u < NS; ++u) wb[u] = M::template split<M::NT>(nw[u]);
+            __builtin_amdgcn_sched_barrier(0);
+            if (more) fetch_state(bw, c0 + 32, nw);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                typename M::template S<M::NT> xf;
+#pragma unroll
+                for (int k = 0; k < M::NT; ++k) xf.t[k] = gdr_rows_frag<T>(lx[k], i, place);
+                M::template each<M::NT>([&](int a, int c) {
+#pragma unroll
+                    for (int u = 0; u < NS; ++u) ax[u][i] = M::mm(wb[u].t[a], xf.t[c], ax[u][i]);
+                });
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int u = 0; u < 3; ++u) {
             const int tile = w + 4 * u;
@@ -1425,6 +1453,7 @@ k_gdr_grads(const LaunchGdr p) {
             }
         }
     }
+    gdr_arrived();                                    // keys, queries and factors are there
     // a query's fragment, from LDS or memory
     auto query = [&](int i, int s) {
         if constexpr (BOTH) {
@@ -1470,23 +1499,30 @@ k_gdr_grads(const LaunchGdr p) {
         if (tile < 10) {
             int mt, nt;
             gdr_tile(tile, mt, nt);
-            const int j = nt * 16 + m;
+            const int j = nt * 16 + m, i0 = mt * 16 + 4 * g;
             const float beta = tok[tBeta * 64 + j], rkj = tok[tRk * 64 + j];
+            const gf4 ri = *reinterpret_cast<const gf4*>(&tok[tRk * 64 + i0]), qi = *reinterpret_cast<const gf4*>(&srq[i0]);
             const double gj = G[j];
+            double gi[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) gi[r] = G[i0 + r];
             float s = 0.0f;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int i = mt * 16 + 4 * g + r;
-                if (i < j) continue;
+                const int i = i0 + r;
                 // where the decay is nothing no gradient passes
-                const float d = __builtin_amdgcn_exp2f((float)(G[i] - gj)) * rkj;
-                const float fq = d * srq[i] * p.scale, fk = d * tok[tRk * 64 + i];
+                const float d = i < j ? 0.0f : __builtin_amdgcn_exp2f((float)(gi[r] - gj)) * rkj;
+                const float fq = d * qi[r] * p.scale, fk = d * ri[r];
                 const float e = d != 0.0f ? ae[u][r] : 0.0f, f = i > j && d != 0.0f ? -af[u][r] : 0.0f;
-                const float term = e * fq * qk[u][r] + f * fk * kk[u][r];
-                s += d != 0.0f ? term : 0.0f;
-                me[i][j] = e * beta * fq;
-                if (i > j) me[j][i] = d != 0.0f ? term * beta : 0.0f;
-                mf[i][j] = mf[j][i] = f * beta * fk;
+                const float term = d != 0.0f ? e * fq * qk[u][r] + f * fk * kk[u][r] : 0.0f;
+                s += term;
+                if (i >= j) me[i][j] = e * beta * fq;
+                if (i > j) {
+                    me[j][i] = term * beta;
+                    mf[i][j] = mf[j][i] = f * beta * fk;
+                } else if (i == j) {
+                    mf[i][i] = 0.0f;
+                }
             }
             s += __shfl_xor(s, 16, 64);
             s += __shfl_xor(s, 32, 64);
@@ -1593,12 +1629,33 @@ k_gdr_grads(const LaunchGdr p) {
             for (int u = 0; u < NS; ++u) av[u][i] = M::template mul<M::NP>(qf[u], ef, av[u][i]);
         }
     }
-    // gates: wave 3, whose tokens' sums go over the terms above me's diagonal
-    if (w == 3) {
-        const int t = lane;
-        float y = rows[0][0][t] + rows[0][1][t] + rows[0][2][t] + rows[0][3][t];
-        const float z = rows[1][0][t] + rows[1][1][t] + rows[1][2][t] + rows[1][3][t];
-        float before = z * tok[tBeta * 64 + t];
+    // gates: a wave has 16 tokens t. Sums over j < t of the terms (i, j) are products with a triangle of ones, and a lane adds
+    // its rows i >= t of them.
+    {
+        gf4 sum = {0, 0, 0, 0};
+        float mine = 0.0f;
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {
+            if (it < w) continue;
+            sum = gf4{0, 0, 0, 0};
+#pragma unroll
+            for (int jt = 0; jt < 4; ++jt) {
+                if (jt > w) break;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int i = 16 * it + m, j = 16 * jt + 4 * k + g;
+                    const float x = me[j][i];
+                    sum = __builtin_amdgcn_mfma_f32_16x16x4f32(i > j ? x : 0.0f, j < 16 * w + m ? 1.0f : 0.0f, sum, 0, 0, 0);
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) mine += 16 * it + 4 * g + r >= 16 * w + m ? sum[r] : 0.0f;
+        }
+        mine += __shfl_xor(mine, 16, 64);
+        mine += __shfl_xor(mine, 32, 64);
+        float y = rows[0][0][lane] + rows[0][1][lane] + rows[0][2][lane] + rows[0][3][lane];
+        const float z = rows[1][0][lane] + rows[1][1][lane] + rows[1][2][lane] + rows[1][3][lane];
+        float before = z * tok[tBeta * 64 + lane];
 #pragma unroll
         for (int o = 1; o < 64; o <<= 1) {
             const float u = __shfl_up(before, o, 64), v = __shfl_down(y, o, 64);
@@ -1608,29 +1665,13 @@ k_gdr_grads(const LaunchGdr p) {
         before = __shfl_up(before, 1, 64);
         if (lane == 0) before = 0.0f;
         const float end = tok[tMisc * 64];
-        float dg = y + before + (end != 0.0f ? end * (wsum[0] + wsum[1] + wsum[2] + wsum[3]) : 0.0f);
-        // lane i adds up its terms (i, j') over j' <= j, in place; then lane t what its row t - 1 holds of i >= t
-        float run = 0.0f;
-#pragma unroll 9
-        for (int j = 0; j < 63; ++j) {
-            run += t > j ? me[j][t] : 0.0f;
-            if (t > j) me[j][t] = run;
-        }
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        float mine = 0.0f;
-        if (t > 0) {
-#pragma unroll 8
-            for (int i = 0; i < 64; i += 4) {
-                const gf4 x = *reinterpret_cast<const gf4*>(&me[t - 1][i]);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) mine += i + r >= t ? x[r] : 0.0f;
-            }
-        }
-        dg += mine;
-        if (t < left) {
+        mine += __shfl(y + before, 16 * w + m, 64) + (end != 0.0f ? end * (wsum[0] + wsum[1] + wsum[2] + wsum[3]) : 0.0f);
+        const int t = 16 * w + m;
+        const float db = __shfl(z, t, 64) + colsum[0][t] + colsum[1][t] + colsum[2][t] + colsum[3][t];
+        if (g == 0 && t < left) {
             const int64_t at = row0 + (int64_t)t * p.H;
-            p.gr.dg[at] = p.reset && p.reset[b * p.L + t0 + t] ? 0.0f : dg;
-            p.gr.dbeta[at] = z + colsum[0][t] + colsum[1][t] + colsum[2][t] + colsum[3][t];
+            p.gr.dg[at] = p.reset && p.reset[b * p.L + t0 + t] ? 0.0f : mine;
+            p.gr.dbeta[at] = db;
         }
     }
     if (p.part_q) {
@@ -1857,6 +1898,7 @@ hipError_t launch_gdr_d(const LaunchGdr& p) {
     const unsigned tiles = (unsigned)(BH * ((p.dv + 63) / 64));
     constexpr bool kTwo = DKP * sizeof(T) <= 512;       // keys twice in LDS
     constexpr int kGroups = DKP <= 128 && sizeof(T) == 2 ? 2 : 1;
+    constexpr int kGrads = DKP <= 128 ? 2 : 1;
     const bool al = p.vec && p.vec_v && p.vec_y;
     if (p.pass == LaunchGdr::kFwd) {
         hipLaunchKernelGGL((k_gdr_solve<T, DKP, false>), dim3((chunks + 3) / 4), dim3(256), 0, st, p);
@@ -1874,10 +1916,11 @@ hipError_t launch_gdr_d(const LaunchGdr& p) {
     hipLaunchKernelGGL((k_gdr_solve<T, DKP, true>), dim3((chunks + 3) / 4), dim3(256), 0, st, p);
     if (p.vec) {
         hipLaunchKernelGGL((k_gdr_walk_back<T, DKP, true, kGroups>), dim3(tiles), dim3(256), 0, st, p);
-        hipLaunchKernelGGL((k_gdr_grads<T, DKP, true, kGroups>), dim3(chunks), dim3(256), 0, st, p);
+        if (p.vec_ck && p.vec_dy) hipLaunchKernelGGL((k_gdr_grads<T, DKP, true, true, kGrads>), dim3(chunks), dim3(256), 0, st, p);
+        else hipLaunchKernelGGL((k_gdr_grads<T, DKP, true, false, kGrads>), dim3(chunks), dim3(256), 0, st, p);
     } else {
         hipLaunchKernelGGL((k_gdr_walk_back<T, DKP, false, kGroups>), dim3(tiles), dim3(256), 0, st, p);
-        hipLaunchKernelGGL((k_gdr_grads<T, DKP, false, kGroups>), dim3(chunks), dim3(256), 0, st, p);
+        hipLaunchKernelGGL((k_gdr_grads<T, DKP, false, false, kGrads>), dim3(chunks), dim3(256), 0, st, p);
     }
     if (p.part_q) {
         const int64_t rows = (p.B * p.L * p.Hk + 3) / 4;
