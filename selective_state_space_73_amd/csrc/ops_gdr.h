@@ -613,25 +613,23 @@ struct GdrWalk {
         }
         if (w * 64 + lane < kGdrTok * 16) tokens.to_lds(reinterpret_cast<gu4*>(tok + w * 256), lane * 16, w * 1024);
     }
-    // rows past the last token as copies of it, as the keys'
+    // (rows past the last token: zeros, or copies of it as the keys'; their beta is 0)
     __device__ __forceinline__ void values(int64_t n) {
         const int64_t t0 = n * kGdrC;
         const T* at = vb + t0 * p.v.token_stride;
         const int c = in ? col : p.dv - 1, last = p.L - t0 < kGdrC ? (int)(p.L - t0) - 1 : kGdrC - 1;
-        unsigned row = (unsigned)p.v.token_stride * (unsigned)sizeof(T);
-        if (AL && last == kGdrC - 1) {
+        if constexpr (AL) {
+            unsigned row = (unsigned)p.v.token_stride * (unsigned)sizeof(T);
             asm volatile("" : "+s"(row));
-            const GdrBuf<T> buf(at);
+            const GdrBuf<T> buf(at, last * row + p.dv * (unsigned)sizeof(T));
             const unsigned lo = 4 * g * row + c * (unsigned)sizeof(T);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = buf.ld(lo, (16 * (i >> 2) + (i & 3)) * row);
+            for (int i = 0; i < 16; ++i) v[i] = buf.ld(lo + (i & 3) * row, 16 * (i >> 2) <= last ? 16 * (i >> 2) * row : 0);
         } else {
-            const GdrBuf<T> buf(at);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 const int t = 16 * (i >> 2) + 4 * g + (i & 3), u = t < last ? t : last;
-                if constexpr (AL) v[i] = buf.ld(u * row + c * (unsigned)sizeof(T), 0);
-                else v[i] = at[u * p.v.token_stride + c];
+                v[i] = at[u * p.v.token_stride + c];
             }
         }
     }
@@ -1044,20 +1042,14 @@ struct GdrWalkBack {
     __device__ __forceinline__ void values(int64_t n) {
         const int64_t t0 = n * kGdrC;
         unsigned row = (unsigned)(p.H * p.dv) * (unsigned)sizeof(T);
-        const GdrBuf<T> buf(static_cast<const T*>(p.gr.dy) + ((b * p.L + t0) * p.H + h) * p.dv);
-        const int c = in ? col : p.dv - 1, last = p.L - t0 < kGdrC ? (int)(p.L - t0) - 1 : kGdrC - 1;
+        const int last = p.L - t0 < kGdrC ? (int)(p.L - t0) - 1 : kGdrC - 1;
         asm volatile("" : "+s"(row));
-        if (last == kGdrC - 1) {
-            const unsigned lo = 4 * g * row + c * (unsigned)sizeof(T);
+        const GdrBuf<T> buf(static_cast<const T*>(p.gr.dy) + ((b * p.L + t0) * p.H + h) * p.dv, last * row + p.dv * (unsigned)sizeof(T));
+        const unsigned lo = in ? 4 * g * row + col * (unsigned)sizeof(T) : kGdrOut;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = buf.ld(lo, (16 * (i >> 2) + (i & 3)) * row);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int t = 16 * (i >> 2) + 4 * g + (i & 3);
-                const T x = buf.ld((t < last ? t : last) * row + c * (unsigned)sizeof(T), 0);
-                v[i] = t <= last ? x : T(0);
-            }
+        for (int i = 0; i < 16; ++i) {                // none behind the last token
+            const unsigned at = lo + (i & 3) * row;
+            v[i] = buf.ld(16 * (i >> 2) <= last ? at : kGdrOut, 16 * (i >> 2) <= last ? 16 * (i >> 2) * row : 0);
         }
     }
 
