@@ -337,7 +337,7 @@ struct GdrRows {
 
 // What k_gdr_solve leaves of a chunk's tokens: rows of 64 floats.
 //   a1 e^G / |k|, a2 e^G, a3 beta e^(G_last - G) / |k|, bk beta / |k|, misc { e^G_last, whether no factor is 0,
-//   G_last in powers of two, whether every beta is in [0, 2] },
+//   G_last in powers of two, whether every beta |k|^2 is in [0, 2] },
 //   G itself, times log2 e, in 64 bits (two rows)
 //   for the gradients as well: e^(G_last - G) / |k|, beta, 1 / |k|
 enum GdrTok { tA1, tA2, tA3, tBk, tMisc, tG, kGdrTok = 7, tA3b = 7, tBeta, tRk, kGdrTokAll };
@@ -427,9 +427,10 @@ k_gdr_solve(const LaunchGdr p) {
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-            if (m == 4 * g + r) sv[w][0][16 * i + m] = p.eps > 0.0f ? 1.0f / sqrtf(kk[i * (i + 1) / 2 + i][r] + p.eps) : 1.0f;
+            if (m == 4 * g + r) sv[w][0][16 * i + m] = kk[i * (i + 1) / 2 + i][r];
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    const float rk = sv[w][0][lane], bk = rk * beta;
+    const float k2 = sv[w][0][lane], rk = p.eps > 0.0f ? 1.0f / sqrtf(k2 + p.eps) : 1.0f, bk = rk * beta;
+    sv[w][0][lane] = rk;
     sv[w][1][lane] = bk;
     {
         float* tok = p.co + id * (kGdrTokAll * 64) + lane;
@@ -442,7 +443,8 @@ k_gdr_solve(const LaunchGdr p) {
         tok[tRk * 64] = rk;
         tok[tBk * 64] = bk;
         const bool clean = __all(a1 != 0.0f && e != 0.0f);
-        const bool tame = __all(beta >= 0.0f && beta <= 2.0f);
+        const float grow = p.eps > 0.0f ? beta : beta * k2;
+        const bool tame = __all(grow >= 0.0f && grow <= 2.0f);
         tok[tMisc * 64] = lane == 0 ? __builtin_amdgcn_exp2f((float)Gl) : lane == 2 ? (float)Gl : (lane == 1 ? clean : tame) ? 1.0f : 0.0f;
         *reinterpret_cast<double*>(p.co + id * (kGdrTokAll * 64) + tG * 64 + 2 * lane) = G;
     }
@@ -878,20 +880,21 @@ k_gdr_walk(const LaunchGdr p) {
     if (p.state && n1 == nc) k.store_state(p.state + bh * kv, p.dv);
 }
 
-// The last chunk of [n0, n1) from which on the decay to n1 is below 2^-48, n0 if there is none; `gone` says whether
-// there is one. With keys of length 1 at most and beta in [0, 2] no state grows on the way, so that what was in front
-// of that chunk is below 2^-48 of its own size at n1: not a bit of an fp32 state. (Any other key or beta on the way: n0.)
+// How many of the chunks [n0, n1), from its end backwards or (AHEAD) from its start on, it takes until they leave less than
+// 2^-48 of a state that passes them; all if they never do, `gone` says whether they do. Where no beta |k|^2 is outside
+// [0, 2] no state, and no gradient of one, grows on the way but by what is added to it, so that behind those chunks nothing in
+// front of them is left but 2^-48 of its own size: not a bit of an fp32 state of that size. (Any other one on the way: all.)
+template <bool AHEAD>
 __device__ __forceinline__ int64_t gdr_reach(const LaunchGdr& p, int64_t bh, int64_t n0, int64_t n1, bool& gone) {
     const int lane = threadIdx.x & 63;
     gone = false;
-    if (!(p.eps > 0.0f)) return n0;
     float sum = 0.0f;
-    for (int64_t top = n1; top > n0; top -= 64) {
-        const int64_t n = top - 1 - lane;
+    for (int64_t done = 0; done < n1 - n0; done += 64) {
+        const int64_t at = done + lane;
         float g = 0.0f;
         bool tame = true;
-        if (n >= n0) {
-            const float* misc = p.co + (bh * p.nchunks + n) * (kGdrTokAll * 64) + tMisc * 64;
+        if (at < n1 - n0) {
+            const float* misc = p.co + (bh * p.nchunks + (AHEAD ? n0 + at : n1 - 1 - at)) * (kGdrTokAll * 64) + tMisc * 64;
             g = misc[2];
             tame = misc[3] != 0.0f;
         }
@@ -900,16 +903,16 @@ __device__ __forceinline__ int64_t gdr_reach(const LaunchGdr& p, int64_t bh, int
             const float u = __shfl_up(g, o, 64);
             if (lane >= o) g += u;
         }
-        const uint64_t low = __ballot(n >= n0 && sum + g < -48.0f), wild = __ballot(!tame);
-        const int at = low ? __builtin_ctzll(low) : 64, bad = wild ? __builtin_ctzll(wild) : 64;
-        if (bad <= at && bad < 64) return n0;
-        if (at < 64) {
+        const uint64_t low = __ballot(at < n1 - n0 && sum + g < -48.0f), wild = __ballot(!tame);
+        const int to = low ? __builtin_ctzll(low) : 64, bad = wild ? __builtin_ctzll(wild) : 64;
+        if (bad <= to && bad < 64) break;
+        if (to < 64) {
             gone = true;
-            return top - 1 - at;
+            return done + to + 1;
         }
         sum += __shfl(g, 63, 64);
     }
-    return n0;
+    return n1 - n0;
 }
 
 // A long sequence in few heads, cut into segments that run at the same time. First the state behind each segment, from
@@ -929,8 +932,8 @@ k_gdr_ends(const LaunchGdr p) {
     const int col = (map ? tile - tv : tile) * 64 + wave * 16 + (lane & 15);
     const int64_t n1 = (seg + 1) * p.seg;
     bool gone;
-    const int64_t reach = gdr_reach(p, bh, seg * p.seg, n1, gone);
-    const int64_t n0 = (int64_t)__builtin_amdgcn_readfirstlane((int)reach);
+    const int64_t reach = gdr_reach<false>(p, bh, seg * p.seg, n1, gone);
+    const int64_t n0 = n1 - __builtin_amdgcn_readfirstlane((int)reach);
     if (map) {
         if (seg == 0) return;
         if (tile == tv && threadIdx.x == 0) p.wF[seg * BH + bh] = gone ? 0.0f : 1.0f;
@@ -1007,7 +1010,10 @@ k_gdr_join(const LaunchGdr p) {
 //   dX = (P beta)^T dY + beta e^(G_last - G) K W,  dV = T^T dX,
 //   W' = e^G_last W + (scale e^G Q)^T dY - (e^G K)^T dV
 // Keys and queries are needed to the end of a chunk and lie in LDS once, so that a CU holds two workgroups, of which
-// one waits for its next chunk while the other works.
+// one waits for its next chunk while the other works. A long sequence in few heads is cut into segments that run at the
+// same time, each of which first takes what it needs of the state's gradient from the chunks behind it, as far back as they
+// count: all of them in the worst case, when the first segment takes as long as one workgroup did, on a card that
+// is not full.
 template <typename T, int DKP, bool AL>
 struct GdrWalkBack {
     using M = Mx<T>;
@@ -1053,10 +1059,12 @@ struct GdrWalkBack {
         }
     }
 
-    __device__ __forceinline__ void chunk(int64_t n) {
+    // one chunk. OUT: with gradients, else the state's alone
+    template <bool OUT>
+    __device__ __forceinline__ void chunk(int64_t n, int64_t first) {
         const int64_t t0 = n * kGdrC, id = bh * nc + n;
         gdr_arrived();
-        {
+        if constexpr (OUT) {
             unsigned dvb = p.dv * 4;
             asm volatile("" : "+s"(dvb));
             const GdrBuf<float> ws(p.wS + id * p.dk * p.dv, p.dk * dvb);
@@ -1174,11 +1182,11 @@ struct GdrWalkBack {
 #pragma unroll
         for (int i = 0; i < 4; ++i) a2[i] *= *reinterpret_cast<const gf4*>(&srq[16 * i + 4 * g]);
         __syncthreads();                              // T, P and factors are used up
-        if (n > 0) {
+        if (n > first) {
             factors(n - 1);
             values(n - 1);
         }
-        {
+        if constexpr (OUT) {
             unsigned row = (unsigned)(p.H * p.dv);
             asm volatile("" : "+s"(row));
             const int64_t at = ((b * p.L + t0) * p.H + h) * p.dv;
@@ -1244,7 +1252,7 @@ struct GdrWalkBack {
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
-        if (n > 0) {
+        if (n > first) {
             __syncthreads();
             rk.load(tk, t0 - kGdrC, p.L);
             rq.load(tq, t0 - kGdrC, p.L);
@@ -1258,10 +1266,15 @@ k_gdr_walk_back(const LaunchGdr p) {
     using W = GdrWalkBack<T, DKP, AL>;
     __shared__ alignas(16) T tk[64 * DKP], tq[64 * DKP], tt[Mx<T>::NT * 3072], tp[Mx<T>::NT * 3072];
     __shared__ alignas(16) float tok[kGdrTok * 64], srq[64];
-    const int64_t BH = p.B * p.H, bh = blockIdx.x % BH, b = bh / p.H, kv = (int64_t)p.dk * p.dv;
-    const int h = (int)(bh % p.H), hk = h / (p.H / p.Hk), col = (int)(blockIdx.x / BH) * 64 + gdr_wave() * 16 + (threadIdx.x & 15);
+    const int64_t BH = p.B * p.H, rest = blockIdx.x / BH, bh = blockIdx.x % BH, b = bh / p.H, kv = (int64_t)p.dk * p.dv;
+    const int tiles = (p.dv + 63) / 64, seg = (int)(rest / tiles);
+    const int h = (int)(bh % p.H), hk = h / (p.H / p.Hk), col = (int)(rest % tiles) * 64 + gdr_wave() * 16 + (threadIdx.x & 15);
+    const int64_t n0 = seg * p.seg, n1 = n0 + p.seg < p.nchunks ? n0 + p.seg : p.nchunks;
+    bool gone;
+    const int64_t reach = gdr_reach<true>(p, bh, n1, p.nchunks, gone);
+    const int64_t from_n = n1 + __builtin_amdgcn_readfirstlane((int)reach);
     W k(p, tk, tq, tt, tp, tok, srq, b, bh, h, hk, col);
-    const float* from = p.gr.dstate_final ? p.gr.dstate_final + bh * kv : nullptr;
+    const float* from = p.gr.dstate_final && !gone ? p.gr.dstate_final + bh * kv : nullptr;
 #pragma unroll
     for (int d = 0; d < W::ND; ++d)
 #pragma unroll
@@ -1273,12 +1286,15 @@ k_gdr_walk_back(const LaunchGdr p) {
     gdr_clear<64 * DKP>(tq);
     gdr_clear<Mx<T>::NT * 3072>(tp);
     __syncthreads();
-    k.rk.load(tk, (p.nchunks - 1) * kGdrC, p.L);
-    k.rq.load(tq, (p.nchunks - 1) * kGdrC, p.L);
-    k.factors(p.nchunks - 1);
-    k.values(p.nchunks - 1);
+    k.rk.load(tk, (from_n - 1) * kGdrC, p.L);
+    k.rq.load(tq, (from_n - 1) * kGdrC, p.L);
+    k.factors(from_n - 1);
+    k.values(from_n - 1);
 #pragma unroll 1
-    for (int64_t n = p.nchunks - 1; n >= 0; --n) k.chunk(n);
+    for (int64_t n = from_n - 1; n >= n1; --n) k.template chunk<false>(n, n0);
+#pragma unroll 1
+    for (int64_t n = n1 - 1; n >= n0; --n) k.template chunk<true>(n, n0);
+    if (n0 > 0) return;
     if (p.gr.dstate_init && k.in) {
         float* to = p.gr.dstate_init + bh * kv;
 #pragma unroll
@@ -1907,11 +1923,11 @@ hipError_t launch_gdr_d(const LaunchGdr& p) {
     }
     hipLaunchKernelGGL((k_gdr_solve<T, DKP, true>), dim3((chunks + 3) / 4), dim3(256), 0, st, p);
     if (p.vec) {
-        hipLaunchKernelGGL((k_gdr_walk_back<T, DKP, true, kGroups>), dim3(tiles), dim3(256), 0, st, p);
+        hipLaunchKernelGGL((k_gdr_walk_back<T, DKP, true, kGroups>), dim3((unsigned)(tiles * p.nseg)), dim3(256), 0, st, p);
         if (p.vec_ck && p.vec_dy) hipLaunchKernelGGL((k_gdr_grads<T, DKP, true, true, kGrads>), dim3(chunks), dim3(256), 0, st, p);
         else hipLaunchKernelGGL((k_gdr_grads<T, DKP, true, false, kGrads>), dim3(chunks), dim3(256), 0, st, p);
     } else {
-        hipLaunchKernelGGL((k_gdr_walk_back<T, DKP, false, kGroups>), dim3(tiles), dim3(256), 0, st, p);
+        hipLaunchKernelGGL((k_gdr_walk_back<T, DKP, false, kGroups>), dim3((unsigned)(tiles * p.nseg)), dim3(256), 0, st, p);
         hipLaunchKernelGGL((k_gdr_grads<T, DKP, false, false, kGrads>), dim3(chunks), dim3(256), 0, st, p);
     }
     if (p.part_q) {

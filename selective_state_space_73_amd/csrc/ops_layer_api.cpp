@@ -20,6 +20,13 @@ int64_t gdr_segment(int64_t BH, int64_t dv, int64_t nchunks) {
     return seg < 4 ? 4 : seg;
 }
 
+int64_t gdr_segment_back(int64_t BH, int64_t dv, int64_t nchunks) {
+    const int64_t n = 256 / (BH * ((dv + 63) / 64));        // one workgroup a CU: what a segment does for itself slows no other
+    if (n < 2) return nchunks;
+    const int64_t seg = (nchunks + n - 1) / n;
+    return seg < 2 ? 2 : seg;
+}
+
 }  // namespace selscan
 
 namespace {
@@ -83,6 +90,8 @@ GdrLayout gdr_layout(const ss_gdr_dims& d, bool backward) {
         }
     }
     if (backward) {
+        l.seg = selscan::gdr_segment_back(d.batch * d.heads, d.dv, l.seg);
+        l.nseg = ceil_div(ceil_div(d.seqlen, SS_GDR_CHUNK), l.seg);
         take(l.wS, n * d.dk * d.dv);
         take(l.wV, rows * d.dv);
         if (d.heads > d.k_heads) {

@@ -39,6 +39,7 @@ struct LaunchGdr {
 // Chunks of a segment. One after the other a chunk takes about as long as any work of its 64 columns; with segments the
 // states are made twice.
 int64_t gdr_segment(int64_t BH, int64_t dv, int64_t nchunks);
+int64_t gdr_segment_back(int64_t BH, int64_t dv, int64_t nchunks);
 hipError_t launch_gdr_bf16(const LaunchGdr& p);
 hipError_t launch_gdr_f32(const LaunchGdr& p);
 inline hipError_t launch_gdr(const LaunchGdr& p) { return p.bf16 ? launch_gdr_bf16(p) : launch_gdr_f32(p); }
