@@ -787,7 +787,7 @@ struct GdrWalk {
             for (int i = 0; i < 4; ++i) {
                 if (16 * i >= left) break;
                 qs[i] *= srq[16 * i + m];
-                if constexpr (AL) {
+                if (p.vec_y) {
                     yt.st4(qs[i], c0 < p.dv ? lo : kGdrOut, 16 * i * row * (unsigned)sizeof(T));
                 } else {
 #pragma unroll
@@ -853,10 +853,10 @@ __device__ __forceinline__ void gdr_walk(W& k, int64_t n0, int64_t n1, T* k0, T*
     }
 }
 
-// LDS columns past dk, which no load writes.
+// Zeros where no load writes: LDS columns past dk, blocks above P's diagonal.
 template <int N, typename T>
 __device__ __forceinline__ void gdr_clear(T* lds) {
-    for (int e = threadIdx.x; e < N; e += 256) lds[e] = T(0);
+    for (int e = threadIdx.x; e < N * (int)sizeof(T) / 16; e += 256) reinterpret_cast<gu4*>(lds)[e] = gu4{0, 0, 0, 0};
 }
 
 template <typename T, int DKP, bool TWO, bool AL, int GROUPS>
@@ -871,9 +871,11 @@ k_gdr_walk(const LaunchGdr p) {
     W k(p, tq, tt, tp, tok, srq, b, bh, h, hk, col);
     const int64_t kv = (int64_t)p.dk * p.dv, n0 = seg * p.seg, n1 = n0 + p.seg < nc ? n0 + p.seg : nc;
     k.load_state(seg ? p.wE + ((seg - 1) * BH + bh) * kv : p.state ? p.state + bh * kv : nullptr, p.dv);
-    gdr_clear<64 * DKP>(k0);
-    gdr_clear<64 * DKP>(tq);
-    if (TWO) gdr_clear<64 * DKP>(k1);
+    if (p.dk < DKP) {
+        gdr_clear<64 * DKP>(k0);
+        gdr_clear<64 * DKP>(tq);
+        if (TWO) gdr_clear<64 * DKP>(k1);
+    }
     gdr_clear<Mx<T>::NP * 3072>(tp);                  // the halves of blocks above P's diagonal, too
     __syncthreads();
     gdr_walk<true>(k, n0, n1, k0, k1);
@@ -952,8 +954,10 @@ k_gdr_ends(const LaunchGdr p) {
     } else {
         k.load_state(seg == 0 && n0 == 0 && p.state ? p.state + bh * kv : nullptr, p.dv);
     }
-    gdr_clear<64 * DKP>(k0);
-    if (TWO) gdr_clear<64 * DKP>(k1);
+    if (p.dk < DKP) {
+        gdr_clear<64 * DKP>(k0);
+        if (TWO) gdr_clear<64 * DKP>(k1);
+    }
     __syncthreads();
     gdr_walk<false>(k, n0, n1, k0, k1);
     if (map) k.store_state(p.wM + (seg * BH + bh) * (int64_t)p.dk * p.dk, p.dk);
@@ -1282,8 +1286,10 @@ k_gdr_walk_back(const LaunchGdr p) {
             const int row = 32 * (d >> 1) + 8 * k.g + 4 * (d & 1) + r;
             k.S[d][r] = from && row < p.dk && k.in ? from[row * p.dv + col] : 0.0f;
         }
-    gdr_clear<64 * DKP>(tk);
-    gdr_clear<64 * DKP>(tq);
+    if (p.dk < DKP) {
+        gdr_clear<64 * DKP>(tk);
+        gdr_clear<64 * DKP>(tq);
+    }
     gdr_clear<Mx<T>::NT * 3072>(tp);
     __syncthreads();
     k.rk.load(tk, (from_n - 1) * kGdrC, p.L);
@@ -1338,7 +1344,7 @@ k_gdr_grads(const LaunchGdr p) {
     const int h = (int)(bh % p.H), hk = h / (p.H / p.Hk), left = p.L - t0 < kGdrC ? (int)(p.L - t0) : kGdrC;
     const GdrRows<T, KD, AL> rk(p.k, b, hk, p.dk), rq(p.q, b, hk, p.dk);
     const T* qg = rq.base + t0 * rq.stride;
-    if (!AL || p.dk < DKP) {
+    if (p.dk < DKP) {
         gdr_clear<64 * DKP>(tk);
         if (BOTH) gdr_clear<64 * DKP>(tq_);
         __syncthreads();
@@ -1907,7 +1913,7 @@ hipError_t launch_gdr_d(const LaunchGdr& p) {
     constexpr bool kTwo = DKP * sizeof(T) <= 512;       // keys twice in LDS
     constexpr int kGroups = DKP <= 128 && sizeof(T) == 2 ? 2 : 1;
     constexpr int kGrads = DKP <= 128 ? 2 : 1;
-    const bool al = p.vec && p.vec_v && p.vec_y;
+    const bool al = p.vec && p.vec_v;
     if (p.pass == LaunchGdr::kFwd) {
         hipLaunchKernelGGL((k_gdr_solve<T, DKP, false>), dim3((chunks + 3) / 4), dim3(256), 0, st, p);
         if (p.nseg > 1) {
