@@ -119,9 +119,8 @@ template <> struct Mx<float> {
     template <int N>
     static __device__ __forceinline__ S<N> split(gf8 v) { return S<N>{{v}}; }
     static __device__ __forceinline__ gf4 mm(const gf8& a, const gf8& b, gf4 c) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[j], b[j], c, 0, 0, 0);
-        return c;
+        const auto x = Mx<uint16_t>::split<3>(a), y = Mx<uint16_t>::split<3>(b);
+        return Mx<uint16_t>::mul(x, y, c);
     }
     template <int N>
     static __device__ __forceinline__ gf4 mul(const F& a, const S<N>& b, gf4 c) { return mm(a, b.t[0], c); }
