@@ -294,7 +294,7 @@ struct GdrRows {
     __device__ __forceinline__ GdrRows(const ss_head_view& v, int64_t b, int head, int dk_)
         : base(static_cast<const T*>(v.p) + b * v.batch_stride + head * v.head_stride), stride(v.token_stride), dk(dk_) {}
     // 64 rows from token t0 on into `tiles`, rows past the last token as copies of it (what they are multiplied by is
-    // 0). Columns past dk are left as they are. Complete once this wave's loads are.
+    // 0). Columns past dk are left as they are (AL) or 0. Complete once this wave's loads are.
     __device__ __forceinline__ void load(T* tiles, int64_t t0, int64_t L) const {
         const T* at = base + t0 * stride;
         const int last = L - t0 < 64 ? (int)(L - t0) - 1 : 63;
@@ -321,13 +321,28 @@ struct GdrRows {
                 }
             }
         } else {
-            for (int e = threadIdx.x; e < 64 * KD * 32; e += 256) {
-                const int j = e & 7, row = e >> 3 & 63, o = e >> 9, d = o * 8 + j, s = d >> 5, gg = d >> 3 & 3;
-                const T x = at[(row < last ? row : last) * stride + (d < dk ? d : dk - 1)];
-                const int i = row >> 4, ln = gdr_place(gg, row & 15);
-                if (d < dk) {
-                    if constexpr (sizeof(T) == 2) tiles[((i * KD + s) * 64 + ln) * 8 + j] = x;
-                    else tiles[(((i * KD + s) * 2 + (j >> 2)) * 64 + ln) * 4 + (j & 3)] = x;
+            // eights of a row, element by element, two of them in flight
+#pragma unroll 1
+            for (int e = threadIdx.x; e < 256 * KD; e += 512) {
+                alignas(16) T x[2][8];
+                int to[2];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int o = (e + 256 * u) % (4 * KD), row = (e + 256 * u) / (4 * KD);
+                    const T* from = at + (row < last ? row : last) * stride;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[u][j] = from[8 * o + j < dk ? 8 * o + j : dk - 1];
+                    to[u] = ((row >> 4) * KD + (o >> 2)) * 512 + gdr_place(o & 3, row & 15) * (16 / (int)sizeof(T));
+                }
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int o = (e + 256 * u) % (4 * KD);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (8 * o + j >= dk) x[u][j] = T(0);
+#pragma unroll
+                    for (int h = 0; h < (int)sizeof(T) / 2; ++h)
+                        *reinterpret_cast<gu4*>(tiles + to[u] + 256 * h) = reinterpret_cast<const gu4*>(x[u])[h];
                 }
             }
         }
