@@ -241,14 +241,21 @@ struct GdrBuf {
         else return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, lane, wave, 0));
     }
     __device__ __forceinline__ gu4 ld16(unsigned lane) const { return __builtin_amdgcn_raw_buffer_load_b128(r, lane, 0, 0); }
-    // eight values from column c of n on, `at` bytes from the start. VEC: rows are whole accesses of 16 bytes (known when
-    // compiling: where two ways to load meet, the values are copied, and the copy waits for them)
+    // eight values from column c of n on, `at` bytes from the start, zeros past n. VEC: rows are whole accesses of 16 bytes
+    // (known when compiling: where two ways to load meet, the values are copied, and the copy waits for them). An access of
+    // 16 bytes may start at any dword, so that fp32 needs no others, only its last columns cut.
     template <bool VEC>
     __device__ __forceinline__ void ld8(unsigned at, int c, int n, T* out) const {
         constexpr int E = 16 / (int)sizeof(T);
         if constexpr (VEC) {
 #pragma unroll
             for (int e = 0; e < 8 / E; ++e) reinterpret_cast<gu4*>(out)[e] = ld16(c + e * E < n ? at + e * 16 : kGdrOut);
+        } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int e = 0; e < 8 / E; ++e) reinterpret_cast<gu4*>(out)[e] = ld16(c + e * E < n ? at + e * 16 : kGdrOut);
+            if (n - c < 8)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) out[j] = c + j < n ? out[j] : T(0);
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j) out[j] = ld(c + j < n ? at + j * (unsigned)sizeof(T) : kGdrOut, 0);
