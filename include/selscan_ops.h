@@ -202,15 +202,18 @@ ss_status ss_block_q8_step(const ss_block_dims* dims, const ss_block_q8_weights*
  *
  * A log decay of -200 or less (minus infinity among them) is a decay of 0, as a reset is. A decay
  * of 0 leaves out what it multiplies between chunks of 64 tokens (tokens 0 to 63, 64 to 127, ...) and
- * in a step, so that not even a NaN passes it there; within a chunk, and everywhere else, values that are
- * not finite propagate. g > 0, beta and the lengths of keys that are used as they are (eps = 0) are
- * the caller's: with |k^| <= 1 and 0 <= beta <= 2 no state grows; nothing is checked.
+ * in a step, so that not even a NaN passes it there. Within a chunk a value that is not finite may reach every
+ * token of the chunk, earlier ones as well; everywhere else it propagates to later tokens. Where whole
+ * chunks leave less than 2^-48 of a state (or of a state's gradient) that passes them and every
+ * beta |k^|^2 in them is in [0, 2], so that nothing grows on the way, that may be taken for 0, too.
+ * g > 0, beta and the lengths of keys that are used as they are (eps = 0) are the caller's: with
+ * 0 <= beta |k^|^2 <= 2 no state grows; nothing is checked.
  *
  * q, k and v are views whose last dimension is contiguous and whose rows, tokens and heads lie at any
  * strides (columns of one projection's output, [B, H, L, d] layouts); every other tensor is contiguous
  * row-major. q, k, v, y and the gradients of q, k, v and y have the I/O dtype (fp32 or bf16); gates,
- * states, checkpoints and their gradients are fp32. Sums and states are fp32 (bf16 inputs: products
- * on the bf16 matrix instructions, operands that are made in fp32 as sums of two or three bf16 terms). */
+ * states, checkpoints and their gradients are fp32. Sums and states are fp32; products are made on the
+ * bf16 matrix instructions, fp32 operands as sums of three bf16 terms (two for what is only stored in bf16). */
 
 #define SS_GDR_CHUNK 64   /* tokens between two checkpoints */
 

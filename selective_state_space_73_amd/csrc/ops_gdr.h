@@ -9,9 +9,11 @@
 //   Y = scale e^G (Q S0) + (P beta) X,    P_ij = scale D_ij (q_i . k_j), i >= j
 //   S = e^G_last S0 + (beta e^(G_last - G) K)^T X
 //
-// k_gdr_prep makes (1 + N)^-1, P and the tokens' factors for every chunk at once; k_gdr_walk goes from
+// k_gdr_solve makes (1 + N)^-1 and the tokens' factors for every chunk at once; k_gdr_walk goes from
 // chunk to chunk with the state in registers. The columns of S are independent, so a head is split over
 // workgroups by them. q and k enter the matrix cores as they came; their lengths are factors of tokens.
+// The backward makes the transposed inverses, goes through the chunks from the last to the first
+// (k_gdr_walk_back) and then makes every chunk's gradients at once from the states on both sides (k_gdr_grads).
 //
 // Layout of the matrix instructions (16 x 16 tiles, 32 terms of a sum): lane l = 16 g + m holds row m of
 // A, or column m of B, at the terms 4 g + r and 16 + 4 g + r, r < 4, of its 32 (any order of the terms
@@ -34,11 +36,12 @@ typedef uint32_t gu4 __attribute__((ext_vector_type(4)));
 constexpr int kGdrC = SS_GDR_CHUNK;           // 64
 static_assert(kGdrC == 64, "a wave is a chunk's tokens");
 
-// Operands by I/O type. fp32: the fp32 matrix instructions, as they are. bf16: q, k, v and gradients of y
-// are exact operands; what is made in fp32 (states, inverses, solutions) goes in as a sum of bf16 terms,
-// three of them where the result is a state or a gradient in fp32 (24 bits, and the six largest of the
-// nine products of two such: 2^-24 of their size is left out), two where it is only stored in
-// bf16. Six bf16 products cost 2.7 times less than one fp32 product.
+// Operands by I/O type. bf16: q, k, v and gradients of y are exact operands; what is made in fp32
+// (states, inverses, solutions) goes in as a sum of bf16 terms, three of them where the result is a
+// state or a gradient in fp32 (24 bits, and the six largest of the nine products of two such: 2^-24 of
+// their size is left out), two where it is only stored in bf16. fp32: every operand as three terms, made where
+// it is read: six bf16 products take 2.7 times less of the matrix cores than one fp32 product, and with
+// their terms made a chunk still takes a fifth less (a prompt of 64 tokens: 20.6 to 16.2 us).
 template <typename T> struct Mx;
 
 template <> struct Mx<uint16_t> {
@@ -376,6 +379,8 @@ __device__ __forceinline__ void gdr_arrived() {
 // diagonal row by row, below them block by block, T_ij = -T_ii sum_l N_il T_lj, in fp32 products
 // whose operands stay in registers.
 // BACK: T transposed, which is how the results lie.
+// 32768 chunks of keys of 128 in bf16: 290 us, 4.1 TB/s of keys read and factors written, which is what bounds
+// it; 4 chunks: 11 us, one wave's chain of products.
 template <typename T, int DKP, bool BACK>
 __global__ void __launch_bounds__(256)
 k_gdr_solve(const LaunchGdr p) {
@@ -578,7 +583,11 @@ k_gdr_solve(const LaunchGdr p) {
 // From chunk to chunk: a workgroup holds 64 columns of one head's state, a wave 16 of them, in
 // registers. What all waves need lies in LDS: keys twice (the next chunk's come while this one's are in
 // use), queries, T and the tokens' factors once, loaded again as soon as the last wave has used them; P is
-// made here, two or three tiles a wave, since reading it back would cost as much as T.
+// made here, two or three tiles a wave, since reading it back would cost as much as T. Two workgroups a CU
+// in bf16 (registers and LDS hold no third). 131072 tokens of 16 heads of 128 x 128 in bf16: 1.0 ms, a chunk 18,000 cycles
+// for two workgroups and 11,800 for one alone on its CU: what bounds it is a chunk's chain (read, multiply, solve,
+// multiply), with the matrix cores and the vector units each busy for about 40%. With checkpoints it writes more
+// than it reads: 8 x 2048 tokens of 40 heads 593 us, 3.2 TB/s (640 workgroups for 512 places: about a quarter of it).
 template <typename T, int DKP, bool TWO, bool AL>
 struct GdrWalk {
     using M = Mx<T>;
@@ -941,7 +950,8 @@ __device__ __forceinline__ int64_t gdr_reach(const LaunchGdr& p, int64_t bh, int
 // A long sequence in few heads, cut into segments that run at the same time. First the state behind each segment, from
 // nothing in front of it (or, the first, from the caller's) and from where it still matters on; and, as dk columns more that
 // start as the identity and get no values, what the segment makes of the state in front of it, where anything is
-// left of that. k_gdr_join puts the ends together.
+// left of that. k_gdr_join puts the ends together. (2048 tokens of 40 heads: 51 and 17 us, 65 for the walk of three
+// segments. 131072 tokens of 16 heads: 261, 23 and 996 us; the whole call 1.7 ms, 10.6 in one segment.)
 template <typename T, int DKP, bool TWO, bool AL, int GROUPS>
 __global__ void __launch_bounds__(256, GROUPS)
 k_gdr_ends(const LaunchGdr p) {
@@ -1038,7 +1048,8 @@ k_gdr_join(const LaunchGdr p) {
 // one waits for its next chunk while the other works. A long sequence in few heads is cut into segments that run at the
 // same time, each of which first takes what it needs of the state's gradient from the chunks behind it, as far back as they
 // count: all of them in the worst case, when the first segment takes as long as one workgroup did, on a card that
-// is not full.
+// is not full. 8 x 2048 tokens of 40 heads of 128 x 128 in bf16: 633 us, 3.0 TB/s, bound as the forward's; 3 x 1001
+// tokens of 6 heads of 96 x 129 in fp32, with resets: 114 us (239 in one segment).
 template <typename T, int DKP, bool AL>
 struct GdrWalkBack {
     using M = Mx<T>;
@@ -1346,7 +1357,9 @@ k_gdr_walk_back(const LaunchGdr p) {
 //     + sum_{j < t} beta_j (k . a3b X W^T)_j + e^G_last <S0, W>
 // A wave has a quarter of dk, transposed (a lane has a token): sums over dk are sums over registers and two moves, factors
 // of tokens one register, and four neighbouring columns one store. Terms over dv go through LDS 32 at a time, the next
-// ones on their way to registers meanwhile.
+// ones on their way to registers meanwhile. 10240 chunks of 128 x 128 in bf16: 723 us, 3.9 TB/s of what it reads and
+// writes; a workgroup waits for its first and its last rows while the other of its CU works (with one way to load
+// a kernel: where aligned and unaligned loads met, the copies between them waited for memory, 1005 us).
 template <typename T, int DKP, bool AL, bool VEC, int GROUPS>
 __global__ void __launch_bounds__(256, GROUPS)
 k_gdr_grads(const LaunchGdr p) {

@@ -11,17 +11,24 @@
 
 namespace selscan {
 
-int64_t gdr_segment(int64_t BH, int64_t dv, int64_t nchunks) {
+// Segments that run at the same time: two workgroups a CU where it holds two (bf16, dk up to 128) and a segment
+// then has 16 chunks at least, else one, which is faster alone, with fewer to join. 128 x 128 in bf16, two and one: 32768
+// tokens of 16 heads 722 and 748 us, 8192 of 16 322 and 255, 2048 of 40 168 and 150 (in fp32, where a CU
+// holds one: 1822 and 1711, 610 and 501, 346 and 245). A segment has four chunks at least, as each is
+// one more to join.
+int64_t gdr_segment(int64_t BH, int64_t dv, int64_t nchunks, bool two) {
     const int64_t groups = BH * ((dv + 63) / 64);           // workgroups of one segment
-    int64_t n = 512 / groups;                               // segments that run at the same time, two workgroups a CU
-    if (nchunks < 16 * n) n = 256 / groups;                 // short ones: one, which is faster alone, and fewer to join
+    int64_t n = two ? 512 / groups : 0;
+    if (nchunks < 16 * n || !two) n = 256 / groups;
     if (n < 2 || nchunks < 8) return nchunks;
     const int64_t seg = (nchunks + n - 1) / n;
     return seg < 4 ? 4 : seg;
 }
 
+// The backward's: one workgroup a CU, so that what a segment does for itself slows no other. 32768 tokens of 16 heads of
+// 128 x 128, no segments, one and two workgroups a CU: 4.2, 1.76 and 1.79 ms in bf16, 8.8, 3.9 and 5.3 in fp32.
 int64_t gdr_segment_back(int64_t BH, int64_t dv, int64_t nchunks) {
-    const int64_t n = 256 / (BH * ((dv + 63) / 64));        // one workgroup a CU: what a segment does for itself slows no other
+    const int64_t n = 256 / (BH * ((dv + 63) / 64));
     if (n < 2) return nchunks;
     const int64_t seg = (nchunks + n - 1) / n;
     return seg < 2 ? 2 : seg;
@@ -80,7 +87,7 @@ GdrLayout gdr_layout(const ss_gdr_dims& d, bool backward) {
     l.nseg = 1;
     if (!backward) {
         const int64_t chunks = l.seg;
-        l.seg = selscan::gdr_segment(d.batch * d.heads, d.dv, chunks);
+        l.seg = selscan::gdr_segment(d.batch * d.heads, d.dv, chunks, d.io_dtype == SS_BF16 && d.dk <= 128);
         l.nseg = ceil_div(chunks, l.seg > 0 ? l.seg : 1);
         if (l.nseg > 1) {
             const size_t ends = (size_t)(l.nseg - 1) * d.batch * d.heads;

@@ -36,9 +36,9 @@ struct LaunchGdr {
     float *part_q, *part_k;      // the backward where heads share keys: [B, L, H, dk] each head's share
     void* stream;
 };
-// Chunks of a segment. One after the other a chunk takes about as long as any work of its 64 columns; with segments the
-// states are made twice.
-int64_t gdr_segment(int64_t BH, int64_t dv, int64_t nchunks);
+// Chunks of a segment, forward and backward. One after the other a chunk takes about as long as any work of its 64 columns;
+// with segments the states, or their gradients, are made twice.
+int64_t gdr_segment(int64_t BH, int64_t dv, int64_t nchunks, bool two);
 int64_t gdr_segment_back(int64_t BH, int64_t dv, int64_t nchunks);
 hipError_t launch_gdr_bf16(const LaunchGdr& p);
 hipError_t launch_gdr_f32(const LaunchGdr& p);
