@@ -1871,20 +1871,20 @@ k_gdr_step(const LaunchGdr p) {
     __shared__ float sq[DKP], sk[DKP], dots[3][4];
     __shared__ alignas(16) float part[2][RG][LANES * CV];
     const int tid = threadIdx.x, lane = tid % LANES, rg = tid / LANES;
-    const int tiles = (p.dv + LANES * CV - 1) / (LANES * CV), tile = (int)(blockIdx.x / 8 % tiles);
-    const int64_t BH = p.B * p.H, bh = (int64_t)(blockIdx.x / 8 / tiles) * 8 + blockIdx.x % 8, b = bh / p.H;
-    if (bh >= BH) return;
-    const int h = (int)(bh % p.H), hk = h / (p.H / p.Hk);
-    const int col = (tile * LANES + lane) * CV;
-    float* st = p.state + bh * p.dk * p.dv + col;
+    const unsigned tiles = (unsigned)(p.dv + LANES * CV - 1) / (LANES * CV), eight = blockIdx.x / 8, H = (unsigned)p.H;
+    const unsigned head = eight / tiles * 8 + blockIdx.x % 8, tile = eight % tiles, h = head % H, hk = h / (H / (unsigned)p.Hk);
+    if (head >= (unsigned)p.B * H) return;
+    const int64_t bh = head, b = head / H;
+    const int col = (int)(tile * LANES + lane) * CV;
     const bool in = col < p.dv;
+    float* st = p.state + bh * p.dk * p.dv + col;
+    const float* some = in ? st : st - col;                // what is not there is read from somewhere that is, with no branch between the loads
     fv S[RPT];
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
         const int row = i * RG + rg;
-        const fv* from = reinterpret_cast<const fv*>(st + row * p.dv);
-        S[i] = fv(0.0f);
-        if (in && row < p.dk) S[i] = CV == 4 ? __builtin_nontemporal_load(from) : *from;
+        const fv* from = reinterpret_cast<const fv*>(some + (row < p.dk ? row : 0) * p.dv);
+        S[i] = CV == 4 ? __builtin_nontemporal_load(from) : *from;
     }
     float qv = 0.0f, kv = 0.0f;
     if (tid < p.dk) {
@@ -1909,8 +1909,7 @@ k_gdr_step(const LaunchGdr p) {
     fv aq = fv(0.0f), ak = fv(0.0f);
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
-        if (a == 0.0f) S[i] = fv(0.0f);                    // nothing passes, whatever it is
-        else S[i] *= a;
+        S[i] = a != 0.0f && i * RG + rg < p.dk ? S[i] * a : fv(0.0f);      // a decay of 0: nothing passes, whatever it is
         aq += S[i] * sq[i * RG + rg];
         ak += S[i] * sk[i * RG + rg];
     }
