@@ -35,6 +35,7 @@ typedef uint32_t gu4 __attribute__((ext_vector_type(4)));
 
 constexpr int kGdrC = SS_GDR_CHUNK;           // 64
 static_assert(kGdrC == 64, "a wave is a chunk's tokens");
+constexpr int kGdrTri = 6 * 16 * 32;         // values of a triangle of 64 x 64 in its blocks of 16 x 32
 
 // Operands by I/O type. bf16: q, k, v and gradients of y are exact operands; what is made in fp32
 // (states, inverses, solutions) goes in as a sum of bf16 terms, three of them where the result is a
@@ -539,12 +540,12 @@ k_gdr_solve(const LaunchGdr p) {
             for (int r = 0; r < 4; ++r) out = __builtin_amdgcn_mfma_f32_16x16x4f32(ti[i][r], acc[r], out, 0, 0, 0);
             tb[i * (i + 1) / 2 + j] = out;
         }
-    T* out = reinterpret_cast<T*>(p.wT) + id * (M::NT * 3072);
+    T* out = reinterpret_cast<T*>(p.wT) + id * (M::NT * kGdrTri);
     auto put = [&](int u, gf4 a, gf4 c) {
         if constexpr (sizeof(T) == 2) {
             const auto sp = M::template split<M::NT>(gdr_pair(a, c));
 #pragma unroll
-            for (int k = 0; k < M::NT; ++k) *reinterpret_cast<gb8*>(out + k * 3072 + (u * 64 + lane) * 8) = sp.t[k];
+            for (int k = 0; k < M::NT; ++k) *reinterpret_cast<gb8*>(out + k * kGdrTri + (u * 64 + lane) * 8) = sp.t[k];
         } else {
             *reinterpret_cast<gf4*>(out + (u * 128 + lane) * 4) = a;
             *reinterpret_cast<gf4*>(out + (u * 128 + 64 + lane) * 4) = c;
@@ -591,7 +592,7 @@ k_gdr_solve(const LaunchGdr p) {
 template <typename T, int DKP, bool TWO, bool AL>
 struct GdrWalk {
     using M = Mx<T>;
-    static constexpr int KD = DKP / 32, ND = DKP / 16, TP = 3072;
+    static constexpr int KD = DKP / 32, ND = DKP / 16, TP = kGdrTri;
     static constexpr bool kTwo = TWO;
     const LaunchGdr& p;
     GdrRows<T, KD, AL> rk, rq;
@@ -893,7 +894,7 @@ template <typename T, int DKP, bool TWO, bool AL, int GROUPS>
 __global__ void __launch_bounds__(256, GROUPS)
 k_gdr_walk(const LaunchGdr p) {
     using W = GdrWalk<T, DKP, TWO, AL>;
-    __shared__ alignas(16) T k0[64 * DKP], k1[TWO ? 64 * DKP : 8], tq[64 * DKP], tt[Mx<T>::NT * 3072], tp[Mx<T>::NP * 3072];
+    __shared__ alignas(16) T k0[64 * DKP], k1[TWO ? 64 * DKP : 8], tq[64 * DKP], tt[Mx<T>::NT * kGdrTri], tp[Mx<T>::NP * kGdrTri];
     __shared__ alignas(16) float tok[kGdrTok * 64], srq[64];
     const int64_t BH = p.B * p.H, rest = blockIdx.x / BH, bh = blockIdx.x % BH, b = bh / p.H, nc = p.nchunks;
     const int tiles = (p.dv + 63) / 64, seg = (int)(rest / tiles);
@@ -906,7 +907,7 @@ k_gdr_walk(const LaunchGdr p) {
         gdr_clear<64 * DKP>(tq);
         if (TWO) gdr_clear<64 * DKP>(k1);
     }
-    gdr_clear<Mx<T>::NP * 3072>(tp);                  // the halves of blocks above P's diagonal, too
+    gdr_clear<Mx<T>::NP * kGdrTri>(tp);                  // the halves of blocks above P's diagonal, too
     __syncthreads();
     gdr_walk<true>(k, n0, n1, k0, k1);
     if (p.state && n1 == nc) k.store_state(p.state + bh * kv, p.dv);
@@ -956,7 +957,7 @@ template <typename T, int DKP, bool TWO, bool AL, int GROUPS>
 __global__ void __launch_bounds__(256, GROUPS)
 k_gdr_ends(const LaunchGdr p) {
     using W = GdrWalk<T, DKP, TWO, AL>;
-    __shared__ alignas(16) T k0[64 * DKP], k1[TWO ? 64 * DKP : 8], tt[Mx<T>::NT * 3072];
+    __shared__ alignas(16) T k0[64 * DKP], k1[TWO ? 64 * DKP : 8], tt[Mx<T>::NT * kGdrTri];
     __shared__ alignas(16) float tok[kGdrTok * 64];
     const int64_t BH = p.B * p.H, rest = blockIdx.x / BH, bh = blockIdx.x % BH, b = bh / p.H, kv = (int64_t)p.dk * p.dv;
     const int tv = (p.dv + 63) / 64, tiles = tv + (p.dk + 63) / 64, seg = (int)(rest / tiles), tile = (int)(rest % tiles);
@@ -1053,7 +1054,7 @@ k_gdr_join(const LaunchGdr p) {
 template <typename T, int DKP, bool AL>
 struct GdrWalkBack {
     using M = Mx<T>;
-    static constexpr int KD = DKP / 32, ND = DKP / 16, TP = 3072;
+    static constexpr int KD = DKP / 32, ND = DKP / 16, TP = kGdrTri;
     const LaunchGdr& p;
     GdrRows<T, KD, AL> rk, rq;
     T *tk, *tq, *tt, *tp;
@@ -1300,7 +1301,7 @@ template <typename T, int DKP, bool AL, int GROUPS>
 __global__ void __launch_bounds__(256, GROUPS)
 k_gdr_walk_back(const LaunchGdr p) {
     using W = GdrWalkBack<T, DKP, AL>;
-    __shared__ alignas(16) T tk[64 * DKP], tq[64 * DKP], tt[Mx<T>::NT * 3072], tp[Mx<T>::NT * 3072];
+    __shared__ alignas(16) T tk[64 * DKP], tq[64 * DKP], tt[Mx<T>::NT * kGdrTri], tp[Mx<T>::NT * kGdrTri];
     __shared__ alignas(16) float tok[kGdrTok * 64], srq[64];
     const int64_t BH = p.B * p.H, rest = blockIdx.x / BH, bh = blockIdx.x % BH, b = bh / p.H, kv = (int64_t)p.dk * p.dv;
     const int tiles = (p.dv + 63) / 64, seg = (int)(rest / tiles);
@@ -1322,7 +1323,7 @@ k_gdr_walk_back(const LaunchGdr p) {
         gdr_clear<64 * DKP>(tk);
         gdr_clear<64 * DKP>(tq);
     }
-    gdr_clear<Mx<T>::NT * 3072>(tp);
+    gdr_clear<Mx<T>::NT * kGdrTri>(tp);
     __syncthreads();
     k.rk.load(tk, (from_n - 1) * kGdrC, p.L);
     k.rq.load(tq, (from_n - 1) * kGdrC, p.L);
@@ -1861,8 +1862,8 @@ k_gdr_keys(const LaunchGdr p) {
 // which are in flight at once, and meet in LDS once:
 //   y = scale (e^g S^T q + (q . k) u),  u = beta (v - e^g S^T k)
 // Workgroups of one head are eight apart, on the same XCD: rows that share a line meet in its L2, for which
-// whole lines only go past it. 64 streams of 64 heads of 128 x 128: 100 us, 5.4 TB/s; 224 streams of 20 heads of
-// 128 x 99: 79 us, 5.8 TB/s (300 us with tiles of 32 columns, far apart and past the L2).
+// whole lines only go past it. 64 streams of 64 heads of 128 x 128: 99 us, 5.4 TB/s; 224 streams of 20 heads of
+// 128 x 99: 77 us, 5.9 TB/s (300 us with tiles of 32 columns, far apart and past the L2).
 template <typename T, int DKP, int CV>
 __global__ void __launch_bounds__(256)
 k_gdr_step(const LaunchGdr p) {

@@ -204,6 +204,25 @@ def test_segments(shape, io, slow):
         near(S, Sw, 64 * rel(shape[4], shape[1]), "f32", max(Sw.abs().max(), yw.abs().max() * shape[4] ** 0.5))
 
 
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("length", [1.0, 1.5])
+def test_segments_of_keys_as_they_are(length, io):
+    """Lengths of about 1, and of 1.5, where beta |k|^2 is above 2 for some tokens: segments then start at their first chunk.
+    With g = -1 no entry of N is above 2.25 e^-1 = 0.83 and no state grows (|1 - 2.25| e^-1 < 1), so the tolerance is that
+    of keys of length 1 times the square of their length."""
+    x, S0, dy, dS, _ = make(1, 1000, 1, 2, 64, 48, io, seed=19)
+    x[1].copy_(x[1].float() / x[1].float().norm(dim=-1, keepdim=True) * length)
+    x[3].fill_(-1.0)
+    x[3][:, ::7] = -0.01 if length == 1.0 else -1.5
+    y, S, ck = run(x, S0, eps=None)
+    yw, Sw = O.gdr_fwd(*x, S0, None, None, None)
+    near(y, yw, length ** 2 * rel(64, 1000), io)
+    near(S, Sw, length ** 2 * rel(64, 1000), "f32", torch.maximum(Sw.abs().max(), S0.abs().max().double().cpu()))
+    got, want = ss.ss_gdr_bwd(*x, ck, dy, dstate_final=dS, eps=None), O.gdr_bwd(*x, dy, S0, None, dS, None, None)
+    for n in GRADS:
+        near(got[n], want[n], length ** 4 * 2 * rel(64, 1000, 48), io if n in ("dq", "dk", "dv") else "f32")
+
+
 def test_pieces_equal_the_whole():
     B, L, K, V = 2, 300, 64, 48
     x, S0, _, _, _ = make(B, L, 1, 2, K, V, "f32")
