@@ -1004,38 +1004,43 @@ k_gdr_join(const LaunchGdr p) {
     using W = GdrWalk<T, DKP, false, false>;
     const int64_t BH = p.B * p.H, bh = blockIdx.x % BH, kv = (int64_t)p.dk * p.dv;
     const int lane = threadIdx.x & 63, col = (int)(blockIdx.x / BH) * 64 + gdr_wave() * 16 + (lane & 15), g = lane >> 4, m = lane & 15;
+    // nothing in front of any segment counts: its end is as it should be
+    const int last = p.nseg - 2;
+    bool any = false;
+    for (int seg = 1 + lane; seg <= last; seg += 64) any |= p.wF[seg * BH + bh] != 0.0f;
+    if (!__any(any)) return;
     W k(p, nullptr, nullptr, nullptr, nullptr, nullptr, 0, bh, 0, 0, col);
-    k.load_state(p.wE + bh * kv, p.dv);
     const int64_t kk = (int64_t)p.dk * p.dk;
     const bool vec = p.dk % 4 == 0;
-    gf8 x[2][W::ND];                                  // the map's rows of this lane, 32 columns ahead
-    auto read = [&](const float* map, int s, gf8 (&to)[W::ND]) {
+    gf8 x[2][W::ND];                                  // the map's rows of this lane, 32 columns ahead, the next segment's behind the last
+    auto read = [&](int seg, int s, gf8 (&to)[W::ND]) {
+        const float* map = p.wM + (seg * BH + bh) * kk;
 #pragma unroll
         for (int d = 0; d < W::ND; ++d) {
             const int row = 32 * (d >> 1) + 8 * (m >> 2) + 4 * (d & 1) + (m & 3);
             to[d] = gdr_ld8(map + (int64_t)row * p.dk, 32 * s + 8 * g, p.dk, row < p.dk, vec);
         }
     };
-    for (int seg = 1; seg < p.nseg - 1; ++seg) {
+    k.load_state(p.wE + bh * kv, p.dv);
+    read(1, 0, x[0]);
+#pragma unroll 1
+    for (int seg = 1; seg <= last; ++seg) {
         float* end = p.wE + (seg * BH + bh) * kv;
-        if (p.wF[seg * BH + bh] == 0.0f) {
-            k.load_state(end, p.dv);
-            continue;
-        }
-        const float* map = p.wM + (seg * BH + bh) * kk;
-        read(map, 0, x[0]);
+        const bool on = p.wF[seg * BH + bh] != 0.0f;  // (without it the map is not written: what is made of it is dropped)
+        const int next = seg < last ? seg + 1 : last;
         typename M::template S<M::NT> sb[W::KD];
 #pragma unroll
         for (int s = 0; s < W::KD; ++s) sb[s] = M::template split<M::NT>(gdr_pair(k.S[2 * s], k.S[2 * s + 1]));
         k.load_state(end, p.dv);
 #pragma unroll
         for (int s = 0; s < W::KD; ++s) {
-            if (s + 1 < W::KD) read(map, s + 1, x[(s + 1) & 1]);
+            read(s + 1 < W::KD ? seg : next, (s + 1) % W::KD, x[(s + 1) & 1]);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int d = 0; d < W::ND; ++d) k.S[d] = M::mul(M::template split<M::NT>(x[s & 1][d]), sb[s], k.S[d]);
         }
-        k.store_state(end, p.dv);
+        if (on) k.store_state(end, p.dv);
+        else k.load_state(end, p.dv);
     }
 }
 
