@@ -169,20 +169,6 @@ __device__ __forceinline__ void gdr_tile(int tile, int& mt, int& nt) {
 }
 
 // ---------------------------------------------------------------------------
-// eight fp32 values of a row, zeros past its end
-__device__ __forceinline__ gf8 gdr_ld8(const float* row, int c, int n, bool there, bool vec) {
-    gf8 v = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (!there) return v;
-    if (vec && c >= n) return v;
-    if (vec && c + 8 <= n) {
-        const gf4 a = *reinterpret_cast<const gf4*>(row + c), b = *reinterpret_cast<const gf4*>(row + c + 4);
-        return gdr_pair(a, b);
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = c + j < n ? row[c + j] : 0.0f;
-    return v;
-}
-
 // Operands in LDS: 64 rows of DKP columns as fragments (row tile i, columns 32 s to 32 s + 31): lane 16 g + m
 // reads row 16 i + m at columns 32 s + 8 g + j, 16 bytes (an fp32 fragment is two such units, j < 4 and the rest).
 // A unit goes from memory to LDS without registers, 16 bytes a lane at consecutive places: place
@@ -615,12 +601,13 @@ struct GdrWalk {
 
     // this wave's columns of a state [dk, n]; zeros where there is none
     __device__ __forceinline__ void load_state(const float* from, int n) {
+        const GdrBuf<float> buf(from, from ? (unsigned)(p.dk * n) * 4 : 0);
 #pragma unroll
         for (int d = 0; d < ND; ++d)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int row = 32 * (d >> 1) + 8 * g + 4 * (d & 1) + r;
-                S[d][r] = from && row < p.dk && in ? from[row * n + col] : 0.0f;
+                S[d][r] = buf.ld(in ? (unsigned)(row * n + col) * 4 : kGdrOut, 0);
             }
     }
     __device__ __forceinline__ void store_state(float* to, int n) const {
@@ -951,8 +938,8 @@ __device__ __forceinline__ int64_t gdr_reach(const LaunchGdr& p, int64_t bh, int
 // A long sequence in few heads, cut into segments that run at the same time. First the state behind each segment, from
 // nothing in front of it (or, the first, from the caller's) and from where it still matters on; and, as dk columns more that
 // start as the identity and get no values, what the segment makes of the state in front of it, where anything is
-// left of that. k_gdr_join puts the ends together. (2048 tokens of 40 heads: 51 and 17 us, 65 for the walk of three
-// segments. 131072 tokens of 16 heads: 261, 23 and 996 us; the whole call 1.7 ms, 10.6 in one segment.)
+// left of that. k_gdr_join puts the ends together. (2048 tokens of 40 heads: 49 and 13 us, 64 for the walk of three
+// segments. 131072 tokens of 16 heads: 268, 5 and 1076 us; the whole call 1.7 ms, 10.6 in one segment.)
 template <typename T, int DKP, bool TWO, bool AL, int GROUPS>
 __global__ void __launch_bounds__(256, GROUPS)
 k_gdr_ends(const LaunchGdr p) {
@@ -1011,14 +998,13 @@ k_gdr_join(const LaunchGdr p) {
     if (!__any(any)) return;
     W k(p, nullptr, nullptr, nullptr, nullptr, nullptr, 0, bh, 0, 0, col);
     const int64_t kk = (int64_t)p.dk * p.dk;
-    const bool vec = p.dk % 4 == 0;
     gf8 x[2][W::ND];                                  // the map's rows of this lane, 32 columns ahead, the next segment's behind the last
     auto read = [&](int seg, int s, gf8 (&to)[W::ND]) {
-        const float* map = p.wM + (seg * BH + bh) * kk;
+        const GdrBuf<float> map(p.wM + (seg * BH + bh) * kk, (unsigned)kk * 4);
 #pragma unroll
         for (int d = 0; d < W::ND; ++d) {
             const int row = 32 * (d >> 1) + 8 * (m >> 2) + 4 * (d & 1) + (m & 3);
-            to[d] = gdr_ld8(map + (int64_t)row * p.dk, 32 * s + 8 * g, p.dk, row < p.dk, vec);
+            to[d] = map.template ld8<false>((unsigned)(row * p.dk + 32 * s + 8 * g) * 4, 32 * s + 8 * g, p.dk);
         }
     };
     k.load_state(p.wE + bh * kv, p.dv);
