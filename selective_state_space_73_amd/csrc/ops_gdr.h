@@ -888,7 +888,10 @@ k_gdr_walk(const LaunchGdr p) {
     const int h = (int)(bh % p.H), hk = h / (p.H / p.Hk), col = (int)(rest % tiles) * 64 + gdr_wave() * 16 + (threadIdx.x & 15);
     W k(p, tq, tt, tp, tok, srq, b, bh, h, hk, col);
     const int64_t kv = (int64_t)p.dk * p.dv, n0 = seg * p.seg, n1 = n0 + p.seg < nc ? n0 + p.seg : nc;
-    k.load_state(seg ? p.wE + ((seg - 1) * BH + bh) * kv : p.state ? p.state + bh * kv : nullptr, p.dv);
+    // several segments: never the caller's state, which the last of them overwrites whenever it gets there
+    const float* from = p.state ? p.state + bh * kv : nullptr;
+    if (p.nseg > 1) from = seg || p.state ? p.wE + (seg * BH + bh) * kv : nullptr;
+    k.load_state(from, p.dv);
     if (p.dk < DKP) {
         gdr_clear<64 * DKP>(k0);
         gdr_clear<64 * DKP>(tq);
@@ -938,7 +941,7 @@ __device__ __forceinline__ int64_t gdr_reach(const LaunchGdr& p, int64_t bh, int
 // A long sequence in few heads, cut into segments that run at the same time. First the state behind each segment, from
 // nothing in front of it (or, the first, from the caller's) and from where it still matters on; and, as dk columns more that
 // start as the identity and get no values, what the segment makes of the state in front of it, where anything is
-// left of that. k_gdr_join puts the ends together. (2048 tokens of 40 heads: 49 and 13 us, 64 for the walk of three
+// left of that. The caller's state is copied for the walk's first segment, as its last one overwrites it. k_gdr_join puts the ends together. (2048 tokens of 40 heads: 49 and 13 us, 64 for the walk of three
 // segments. 131072 tokens of 16 heads: 268, 5 and 1076 us; the whole call 1.7 ms, 10.6 in one segment.)
 template <typename T, int DKP, bool TWO, bool AL, int GROUPS>
 __global__ void __launch_bounds__(256, GROUPS)
@@ -971,7 +974,12 @@ k_gdr_ends(const LaunchGdr p) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) k.v[i] = T(0);
     } else {
-        k.load_state(seg == 0 && n0 == 0 && p.state ? p.state + bh * kv : nullptr, p.dv);
+        const float* init = seg == 0 && p.state ? p.state + bh * kv : nullptr;
+        k.load_state(init, p.dv);
+        if (init) k.store_state(p.wE + bh * kv, p.dv);
+        if (n0 > 0)
+#pragma unroll
+            for (int d = 0; d < W::ND; ++d) k.S[d] = gf4{0, 0, 0, 0};
     }
     if (p.dk < DKP) {
         gdr_clear<64 * DKP>(k0);
@@ -980,7 +988,7 @@ k_gdr_ends(const LaunchGdr p) {
     __syncthreads();
     gdr_walk<false>(k, n0, n1, k0, k1);
     if (map) k.store_state(p.wM + (seg * BH + bh) * (int64_t)p.dk * p.dk, p.dk);
-    else k.store_state(p.wE + (seg * BH + bh) * kv, p.dv);
+    else k.store_state(p.wE + ((seg + 1) * BH + bh) * kv, p.dv);
 }
 
 // The states between segments, one after the other: E_s <- M_s E_(s-1) + E_s, where M_s is there. Waves as in the walk.
@@ -1007,11 +1015,11 @@ k_gdr_join(const LaunchGdr p) {
             to[d] = map.template ld8<false>((unsigned)(row * p.dk + 32 * s + 8 * g) * 4, 32 * s + 8 * g, p.dk);
         }
     };
-    k.load_state(p.wE + bh * kv, p.dv);
+    k.load_state(p.wE + (BH + bh) * kv, p.dv);
     read(1, 0, x[0]);
 #pragma unroll 1
     for (int seg = 1; seg <= last; ++seg) {
-        float* end = p.wE + (seg * BH + bh) * kv;
+        float* end = p.wE + ((seg + 1) * BH + bh) * kv;
         const bool on = p.wF[seg * BH + bh] != 0.0f;  // (without it the map is not written: what is made of it is dropped)
         const int next = seg < last ? seg + 1 : last;
         typename M::template S<M::NT> sb[W::KD];

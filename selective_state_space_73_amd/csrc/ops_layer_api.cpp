@@ -72,7 +72,7 @@ size_t ckpt_states(const ss_gdr_dims& d) {
 size_t ckpt_floats(const ss_gdr_dims& d) { return ckpt_states(d) + (size_t)d.batch * (size_t)d.seqlen * d.heads * d.dv; }
 
 // Per chunk and head: the tokens' factors and the inverse (6 blocks of 16 x 32, three bf16 terms or fp32). The forward in
-// segments: the states behind them and what they make of the ones in front. The backward: the state's gradient behind every
+// segments: the states in front of them and what they make of these. The backward: the state's gradient behind every
 // chunk, the gradients of v in fp32, and those of q and k by head of v where heads share them.
 struct GdrLayout { size_t co, wT, wS, wV, pq, pk, wE, wM, wF, total; int64_t seg, nseg; };
 GdrLayout gdr_layout(const ss_gdr_dims& d, bool backward) {
@@ -91,7 +91,7 @@ GdrLayout gdr_layout(const ss_gdr_dims& d, bool backward) {
         l.nseg = ceil_div(chunks, l.seg > 0 ? l.seg : 1);
         if (l.nseg > 1) {
             const size_t ends = (size_t)(l.nseg - 1) * d.batch * d.heads;
-            take(l.wE, ends * d.dk * d.dv);
+            take(l.wE, (size_t)l.nseg * d.batch * d.heads * d.dk * d.dv);
             take(l.wM, ends * d.dk * d.dk);
             take(l.wF, ends);
         }

@@ -29,8 +29,9 @@ struct LaunchGdr {
     // workspace
     int64_t seg;                 // chunks of a segment of the forward (all of them: one segment)
     int nseg;
-    float *wE, *wM, *wF;         // several segments: [nseg - 1, B, H, dk, dv] states behind the segments, [nseg - 1, B, H, dk, dk]
-                                 // what they make of the state in front, [nseg - 1, B, H] whether anything of it is left
+    float *wE, *wM, *wF;         // several segments: [nseg, B, H, dk, dv] states in front of the segments (the first: the caller's, if
+                                 // there is one), [nseg - 1, B, H, dk, dk] what they make of these, [nseg - 1, B, H] whether
+                                 // anything of it is left
     float *co, *wT;              // [B, H, chunks]: factors of tokens, inverses in the order of operands
     float *wS, *wV;              // the backward: [B, H, chunks, dk, dv] adjoints behind the chunks, [B, L, H, dv] gradients of v
     float *part_q, *part_k;      // the backward where heads share keys: [B, L, H, dk] each head's share

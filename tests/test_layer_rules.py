@@ -1,0 +1,16 @@
+"""CPU: sizes that the delta rule's and the norms' C ABI gives, where a wrong one is a race or ends the process."""
+import selective_state_space_73_amd as ss
+
+
+def rdims(**kw):
+    d = dict(batch=1, seqlen=64 * 9, k_heads=1, heads=1, dk=64, dv=64, io_dtype=ss.SS_BF16, scale=0.125, eps=1e-6, reserved=0)
+    d.update(kw)
+    return ss.ss_gdr_dims(*d.values())
+
+
+def test_segments_have_a_state_in_front_of_every_one():
+    """Nine chunks of one head run as segments of 4, 4 and 1. All of them start from the workspace, the first one too: the last
+    segment overwrites the caller's state in the same launch. Only these states depend on dv."""
+    for io in (ss.SS_BF16, ss.SS_F32):
+        more = ss.ss_gdr_workspace_bytes(rdims(dv=128, io_dtype=io)) - ss.ss_gdr_workspace_bytes(rdims(io_dtype=io))
+        assert more == 3 * 64 * 64 * 4
