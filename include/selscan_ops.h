@@ -213,7 +213,7 @@ ss_status ss_block_q8_step(const ss_block_dims* dims, const ss_block_q8_weights*
  * strides (columns of one projection's output, [B, H, L, d] layouts); every other tensor is contiguous
  * row-major. q, k, v, y and the gradients of q, k, v and y have the I/O dtype (fp32 or bf16); gates,
  * states, checkpoints and their gradients are fp32. Sums and states are fp32; products are made on the
- * bf16 matrix instructions, fp32 operands as sums of three bf16 terms (two for what is only stored in bf16). */
+ * bf16 matrix instructions, fp32 operands as sums of three bf16 terms (24 bits). */
 
 #define SS_GDR_CHUNK 64   /* tokens between two checkpoints */
 

@@ -35,18 +35,18 @@ typedef uint32_t gu4 __attribute__((ext_vector_type(4)));
 
 constexpr int kGdrC = SS_GDR_CHUNK;           // 64
 static_assert(kGdrC == 64, "a wave is a chunk's tokens");
-constexpr int kGdrTri = 6 * 16 * 32;         // values of a triangle of 64 x 64 in its blocks of 16 x 32
+constexpr int kGdrTri = 6 * 16 * 32;         // values of an upper triangle of 64 x 64 in its blocks of 16 x 32
+constexpr int kGdrLow = 10 * 16 * 16;        // of a lower one in its tiles of 16 x 16
 
 // Operands by I/O type. bf16: q, k, v and gradients of y are exact operands; what is made in fp32
-// (states, inverses, solutions) goes in as a sum of bf16 terms, three of them where the result is a
-// state or a gradient in fp32 (24 bits, and the six largest of the nine products of two such: 2^-24 of
-// their size is left out), two where it is only stored in bf16. fp32: every operand as three terms, made where
+// (states, inverses, solutions) goes in as a sum of three bf16 terms (24 bits, and the six largest of the nine products of
+// two such: 2^-24 of their size is left out, as a rounding to fp32 leaves it out). fp32: every operand as three terms, made where
 // it is read: six bf16 products take 2.7 times less of the matrix cores than one fp32 product, and with
 // their terms made a chunk still takes a fifth less (a prompt of 64 tokens: 20.6 to 16.2 us).
 template <typename T> struct Mx;
 
 template <> struct Mx<uint16_t> {
-    static constexpr int NT = 3, NP = 2;                        // terms of the inverse, of P
+    static constexpr int NT = 3;                                // terms of what is made in fp32
     typedef gb8 F;
     template <int N> struct S { gb8 t[N]; };
     static __device__ __forceinline__ F ld(const uint16_t* p) { return *reinterpret_cast<const gb8*>(p); }
@@ -114,7 +114,7 @@ template <> struct Mx<uint16_t> {
 };
 
 template <> struct Mx<float> {
-    static constexpr int NT = 1, NP = 1;
+    static constexpr int NT = 1;
     typedef gf8 F;
     template <int N> struct S { gf8 t[1]; };
     template <int N, typename Fn>
@@ -139,10 +139,13 @@ __device__ __forceinline__ gf8 gdr_pair(gf4 a, gf4 b) { return gf8{a[0], a[1], a
 // This wave's number, known to be the same in all its lanes.
 __device__ __forceinline__ int gdr_wave() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
 
-// The blocks of a lower triangle of 64 x 64 that hold anything, 16 rows by 32 columns: (row tile, column
-// pair) 00 10 20 21 30 31; of an upper triangle 00 01 10 11 21 31.
-__device__ __forceinline__ constexpr int gdr_low(int mt, int s) { return mt < 2 ? mt : 2 * mt - 2 + s; }
+// The blocks of an upper triangle of 64 x 64 that hold anything, 16 rows by 32 columns: (row tile, column
+// pair) 00 01 10 11 21 31.
 __device__ __forceinline__ constexpr int gdr_up(int mt, int s) { return mt < 2 ? 2 * mt + s : mt + 2; }
+// Where a block of a lower triangle lies, in values: 10 20 30 31, then the first halves of 00 and 21, whose others are above the
+// diagonal. (Three terms of T and of P then take what three and two would in whole blocks, and two workgroups' LDS fits a CU.)
+__device__ __forceinline__ constexpr bool gdr_half(int mt, int s) { return mt == 2 * s; }
+__device__ __forceinline__ constexpr int gdr_low(int mt, int s) { return gdr_half(mt, s) ? 4 * 512 + s * 256 : (mt - 1 + s) * 512; }
 
 // Eight values of a row at d, zeros past dk or (none) in a row that is not there.
 template <typename T>
@@ -214,6 +217,26 @@ __device__ __forceinline__ typename Mx<T>::template S<N> gdr_terms(const T* base
     typename Mx<T>::template S<N> f;
 #pragma unroll
     for (int k = 0; k < (sizeof(T) == 2 ? N : 1); ++k) f.t[k] = gdr_frag<T>(base + k * plane, unit, lane);
+    return f;
+}
+
+// The same of a lower triangle.
+template <typename T>
+__device__ __forceinline__ typename Mx<T>::template S<Mx<T>::NT> gdr_low_terms(const T* base, int mt, int s, int lane) {
+    typename Mx<T>::template S<Mx<T>::NT> f;
+#pragma unroll
+    for (int k = 0; k < Mx<T>::NT; ++k) {
+        const T* at = base + k * kGdrLow + gdr_low(mt, s);
+        if (!gdr_half(mt, s)) {
+            f.t[k] = gdr_frag<T>(at, 0, lane);
+        } else if constexpr (sizeof(T) == 2) {
+            typedef short gs8 __attribute__((ext_vector_type(8)));
+            const gs4 a = *reinterpret_cast<const gs4*>(at + lane * 4);
+            f.t[k] = __builtin_bit_cast(gb8, gs8{a[0], a[1], a[2], a[3], 0, 0, 0, 0});
+        } else {
+            f.t[k] = gdr_pair(*reinterpret_cast<const gf4*>(at + lane * 4), gf4{0, 0, 0, 0});
+        }
+    }
     return f;
 }
 
@@ -526,15 +549,16 @@ k_gdr_solve(const LaunchGdr p) {
             for (int r = 0; r < 4; ++r) out = __builtin_amdgcn_mfma_f32_16x16x4f32(ti[i][r], acc[r], out, 0, 0, 0);
             tb[i * (i + 1) / 2 + j] = out;
         }
-    T* out = reinterpret_cast<T*>(p.wT) + id * (M::NT * kGdrTri);
-    auto put = [&](int u, gf4 a, gf4 c) {
+    constexpr int TP = BACK ? kGdrTri : kGdrLow;
+    T* out = reinterpret_cast<T*>(p.wT) + id * (M::NT * TP);
+    auto put = [&](int at, gf4 a, gf4 c) {
         if constexpr (sizeof(T) == 2) {
             const auto sp = M::template split<M::NT>(gdr_pair(a, c));
 #pragma unroll
-            for (int k = 0; k < M::NT; ++k) *reinterpret_cast<gb8*>(out + k * kGdrTri + (u * 64 + lane) * 8) = sp.t[k];
+            for (int k = 0; k < M::NT; ++k) *reinterpret_cast<gb8*>(out + k * TP + at + lane * 8) = sp.t[k];
         } else {
-            *reinterpret_cast<gf4*>(out + (u * 128 + lane) * 4) = a;
-            *reinterpret_cast<gf4*>(out + (u * 128 + 64 + lane) * 4) = c;
+            *reinterpret_cast<gf4*>(out + at + lane * 4) = a;
+            *reinterpret_cast<gf4*>(out + at + (64 + lane) * 4) = c;
         }
     };
     if constexpr (BACK) {
@@ -543,7 +567,7 @@ k_gdr_solve(const LaunchGdr p) {
 #pragma unroll
             for (int s = j >> 1; s < 2; ++s) {
                 const int i = 2 * s;                  // row tiles i and i + 1 are the terms
-                put(gdr_up(j, s), i >= j ? tb[i * (i + 1) / 2 + j] : gf4{0, 0, 0, 0}, tb[(i + 1) * (i + 2) / 2 + j]);
+                put(gdr_up(j, s) * 512, i >= j ? tb[i * (i + 1) / 2 + j] : gf4{0, 0, 0, 0}, tb[(i + 1) * (i + 2) / 2 + j]);
             }
     } else {
         // through LDS, rows by lane
@@ -559,9 +583,19 @@ k_gdr_solve(const LaunchGdr p) {
 #pragma unroll
             for (int s = 0; s <= i >> 1; ++s) {
                 const gf4 a = *reinterpret_cast<const gf4*>(&mat[(16 * i + m) * LD + 32 * s + 4 * g]);
-                gf4 c = {0, 0, 0, 0};
-                if (2 * s + 1 <= i) c = *reinterpret_cast<const gf4*>(&mat[(16 * i + m) * LD + 32 * s + 16 + 4 * g]);
-                put(gdr_low(i, s), a, c);
+                if (!gdr_half(i, s)) {
+                    put(gdr_low(i, s), a, *reinterpret_cast<const gf4*>(&mat[(16 * i + m) * LD + 32 * s + 16 + 4 * g]));
+                } else if constexpr (sizeof(T) == 2) {
+                    const auto sp = M::template split<M::NT>(gdr_pair(a, gf4{0, 0, 0, 0}));
+#pragma unroll
+                    for (int k = 0; k < M::NT; ++k) {
+                        typedef uint32_t gu2 __attribute__((ext_vector_type(2)));
+                        const gu4 u = __builtin_bit_cast(gu4, sp.t[k]);
+                        *reinterpret_cast<gu2*>(out + k * TP + gdr_low(i, s) + lane * 4) = gu2{u[0], u[1]};
+                    }
+                } else {
+                    *reinterpret_cast<gf4*>(out + gdr_low(i, s) + lane * 4) = a;
+                }
             }
     }
 }
@@ -578,7 +612,7 @@ k_gdr_solve(const LaunchGdr p) {
 template <typename T, int DKP, bool TWO, bool AL>
 struct GdrWalk {
     using M = Mx<T>;
-    static constexpr int KD = DKP / 32, ND = DKP / 16, TP = kGdrTri;
+    static constexpr int KD = DKP / 32, ND = DKP / 16, TP = kGdrLow;
     static constexpr bool kTwo = TWO;
     const LaunchGdr& p;
     GdrRows<T, KD, AL> rk, rq;
@@ -657,6 +691,10 @@ struct GdrWalk {
     // one chunk; keys in `tk`, the next chunk's on their way to `tn`. OUT: with outputs, else the state alone
     template <bool OUT>
     __device__ __forceinline__ void chunk(int64_t n, int64_t end_n, T* tk, T* tn) {
+        // places in LDS are made again for every chunk: kept over the loop they would spill
+        int lane = this->lane;
+        asm volatile("" : "+v"(lane));
+        const int g = lane >> 4, m = lane & 15, place = gdr_place(g, m);
         const int64_t t0 = n * kGdrC;
         gdr_arrived();
         if (TWO && n + 1 < end_n) rk.load(tn, t0 + kGdrC, p.L);
@@ -706,7 +744,7 @@ struct GdrWalk {
                 for (int k = sizeof(T) == 2 ? 2 : 0; k >= 0; --k) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) ks[i] = M::mm(x[i], sb.t[k], ks[i]);
-                    if (OUT && k < 2)
+                    if (OUT)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) qs[i] = M::mm(sb.t[k], x[4 + i], qs[i]);
                 }
@@ -716,27 +754,30 @@ struct GdrWalk {
         if constexpr (OUT) {
             const double* G = reinterpret_cast<const double*>(tok + tG * 64);
             const double gi = G[16 * w + m];
+            int tile = w;
+            asm volatile("" : "+s"(tile));
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                if (i > w) break;                     // this wave's tiles above the diagonal stay 0 in LDS
+                if (i > w) break;
                 const gf4 bk = *reinterpret_cast<const gf4*>(&tok[tBk * 64 + 16 * i + 4 * g]);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const float d = __builtin_amdgcn_exp2f((float)(gi - G[16 * i + 4 * g + r]));
                     pt[i][r] = d != 0.0f && (i < w || m >= 4 * g + r) ? pt[i][r] * d * bk[r] : 0.0f;
                 }
-                const int unit = w < 2 ? w : 2 * w - 2 + (i >> 1);
+                const bool half = gdr_half(tile, i >> 1);
+                T* at = tp + gdr_low(tile, i >> 1);
                 if constexpr (sizeof(T) == 2) {
-                    const auto both = M::template split<M::NP>(gdr_pair(pt[i], gf4{0, 0, 0, 0}));
-                    T* at = tp + (unit * 64 + lane) * 8 + 4 * (i & 1);
+                    const auto both = M::template split<M::NT>(gdr_pair(pt[i], gf4{0, 0, 0, 0}));
+                    at += half ? lane * 4 : lane * 8 + 4 * (i & 1);
 #pragma unroll
-                    for (int k = 0; k < M::NP; ++k) {
+                    for (int k = 0; k < M::NT; ++k) {
                         typedef uint32_t gu2 __attribute__((ext_vector_type(2)));
                         const gu4 u = __builtin_bit_cast(gu4, both.t[k]);
                         *reinterpret_cast<gu2*>(at + k * TP) = gu2{u[0], u[1]};
                     }
                 } else {
-                    *reinterpret_cast<gf4*>(tp + ((unit * 2 + (i & 1)) * 64 + lane) * 4) = pt[i];
+                    *reinterpret_cast<gf4*>(at + ((i & 1) * 64 + lane) * 4) = pt[i];
                 }
             }
             const float q2 = (m & 3) == 0 ? len[0] : (m & 3) == 1 ? len[1] : (m & 3) == 2 ? len[2] : len[3];
@@ -769,7 +810,7 @@ struct GdrWalk {
         for (int s = 0; s < 2; ++s) {
             typename M::template S<M::NT> tf[4];
 #pragma unroll
-            for (int i = 2 * s; i < 4; ++i) tf[i] = gdr_terms<T, M::NT>(tt, TP, gdr_low(i, s), lane);
+            for (int i = 2 * s; i < 4; ++i) tf[i] = gdr_low_terms(tt, i, s, lane);
             const auto rb = M::template split<M::NT>(gdr_pair(V[2 * s], V[2 * s + 1]));
             M::template each<M::NT>([&](int a, int c) {
 #pragma unroll
@@ -784,11 +825,12 @@ struct GdrWalk {
         if constexpr (OUT) {
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            const auto xb = M::template split<M::NP>(gdr_pair(X[2 * s], X[2 * s + 1]));
-            typename M::template S<M::NP> pf[4];
+            __builtin_amdgcn_sched_barrier(0);        // the second half's operands are not read over the first's
+            const auto xb = M::template split<M::NT>(gdr_pair(X[2 * s], X[2 * s + 1]));
+            typename M::template S<M::NT> pf[4];
 #pragma unroll
-            for (int i = 2 * s; i < 4; ++i) pf[i] = gdr_terms<T, M::NP>(tp, TP, gdr_low(i, s), lane);
-            M::template each<M::NP>([&](int a, int c) {
+            for (int i = 2 * s; i < 4; ++i) pf[i] = gdr_low_terms(tp, i, s, lane);
+            M::template each<M::NT>([&](int a, int c) {
 #pragma unroll
                 for (int i = 2 * s; i < 4; ++i) qs[i] = M::mm(xb.t[a], pf[i].t[c], qs[i]);
             });
@@ -871,7 +913,7 @@ __device__ __forceinline__ void gdr_walk(W& k, int64_t n0, int64_t n1, T* k0, T*
     }
 }
 
-// Zeros where no load writes: LDS columns past dk, blocks above P's diagonal.
+// Zeros where no load writes: LDS columns past dk, blocks above the diagonal of the backward's P.
 template <int N, typename T>
 __device__ __forceinline__ void gdr_clear(T* lds) {
     for (int e = threadIdx.x; e < N * (int)sizeof(T) / 16; e += 256) reinterpret_cast<gu4*>(lds)[e] = gu4{0, 0, 0, 0};
@@ -881,7 +923,7 @@ template <typename T, int DKP, bool TWO, bool AL, int GROUPS>
 __global__ void __launch_bounds__(256, GROUPS)
 k_gdr_walk(const LaunchGdr p) {
     using W = GdrWalk<T, DKP, TWO, AL>;
-    __shared__ alignas(16) T k0[64 * DKP], k1[TWO ? 64 * DKP : 8], tq[64 * DKP], tt[Mx<T>::NT * kGdrTri], tp[Mx<T>::NP * kGdrTri];
+    __shared__ alignas(16) T k0[64 * DKP], k1[TWO ? 64 * DKP : 8], tq[64 * DKP], tt[Mx<T>::NT * kGdrLow], tp[Mx<T>::NT * kGdrLow];
     __shared__ alignas(16) float tok[kGdrTok * 64], srq[64];
     const int64_t BH = p.B * p.H, rest = blockIdx.x / BH, bh = blockIdx.x % BH, b = bh / p.H, nc = p.nchunks;
     const int tiles = (p.dv + 63) / 64, seg = (int)(rest / tiles);
@@ -897,7 +939,6 @@ k_gdr_walk(const LaunchGdr p) {
         gdr_clear<64 * DKP>(tq);
         if (TWO) gdr_clear<64 * DKP>(k1);
     }
-    gdr_clear<Mx<T>::NP * kGdrTri>(tp);                  // the halves of blocks above P's diagonal, too
     __syncthreads();
     gdr_walk<true>(k, n0, n1, k0, k1);
     if (p.state && n1 == nc) k.store_state(p.state + bh * kv, p.dv);
@@ -947,7 +988,7 @@ template <typename T, int DKP, bool TWO, bool AL, int GROUPS>
 __global__ void __launch_bounds__(256, GROUPS)
 k_gdr_ends(const LaunchGdr p) {
     using W = GdrWalk<T, DKP, TWO, AL>;
-    __shared__ alignas(16) T k0[64 * DKP], k1[TWO ? 64 * DKP : 8], tt[Mx<T>::NT * kGdrTri];
+    __shared__ alignas(16) T k0[64 * DKP], k1[TWO ? 64 * DKP : 8], tt[Mx<T>::NT * kGdrLow];
     __shared__ alignas(16) float tok[kGdrTok * 64];
     const int64_t BH = p.B * p.H, rest = blockIdx.x / BH, bh = blockIdx.x % BH, b = bh / p.H, kv = (int64_t)p.dk * p.dv;
     const int tv = (p.dv + 63) / 64, tiles = tv + (p.dk + 63) / 64, seg = (int)(rest / tiles), tile = (int)(rest % tiles);
@@ -1373,7 +1414,8 @@ k_gdr_grads(const LaunchGdr p) {
     __shared__ alignas(16) float srq[64], rows[2][4][64], colsum[4][64], wsum[4];
     T (*lx)[SL] = reinterpret_cast<T (*)[SL]>(lds), (*lv)[SL] = lx + M::NT, *lo = lx[2 * M::NT], *tq = BOTH ? tq_ : tk;
     float (*me)[LD] = reinterpret_cast<float (*)[LD]>(lds), (*mf)[LD] = me + 64;
-    const int tid = threadIdx.x, lane = tid & 63, w = gdr_wave(), g = lane >> 4, m = lane & 15, place = gdr_place(g, m);
+    const int tid = threadIdx.x, w = gdr_wave();
+    int lane = tid & 63, g = lane >> 4, m = lane & 15, place = gdr_place(g, m);
     const int64_t id = blockIdx.x, nc = p.nchunks, n = id % nc, bh = id / nc, b = bh / p.H, t0 = n * kGdrC;
     const int h = (int)(bh % p.H), hk = h / (p.H / p.Hk), left = p.L - t0 < kGdrC ? (int)(p.L - t0) : kGdrC;
     const GdrRows<T, KD, AL> rk(p.k, b, hk, p.dk), rq(p.q, b, hk, p.dk);
@@ -1418,7 +1460,15 @@ k_gdr_grads(const LaunchGdr p) {
     if (w * 64 + lane < kGdrTokAll * 16)
         GdrSource(p.co + id * (kGdrTokAll * 64)).to_lds(reinterpret_cast<gu4*>(tok + w * 256), lane * 16, w * 1024);
     colsum[tid >> 6][tid & 63] = 0.0f;
+    // a lane's places are made again in every turn and behind the last: kept over the loop they would spill
+    auto places = [&] {
+        asm volatile("" : "+v"(lane));
+        g = lane >> 4;
+        m = lane & 15;
+        place = gdr_place(g, m);
+    };
     for (int c0 = 0; c0 < p.dv; c0 += 32) {
+        places();
         __syncthreads();
         {
             const auto x = M::template split<M::NT>(nx), v = M::template split<M::NT>(nv);
@@ -1502,6 +1552,7 @@ k_gdr_grads(const LaunchGdr p) {
         }
     }
     gdr_arrived();                                    // keys, queries and factors are there
+    places();
     // a query's fragment, from LDS or memory
     auto query = [&](int i, int s) {
         if constexpr (BOTH) {
@@ -1645,12 +1696,12 @@ k_gdr_grads(const LaunchGdr p) {
             gf8 e = gdr_pair(*reinterpret_cast<const gf4*>(&me[r][c]), *reinterpret_cast<const gf4*>(&me[r][c + 16]));
 #pragma unroll
             for (int j = 0; j < 8; ++j) e[j] = c + 16 * (j >> 2) + (j & 3) <= r ? e[j] : 0.0f;
-            const auto ef = M::template split<M::NP>(e);
-            const auto ff = M::template split<M::NP>(gdr_pair(*reinterpret_cast<const gf4*>(&mf[r][c]), *reinterpret_cast<const gf4*>(&mf[r][c + 16])));
+            const auto ef = M::template split<M::NT>(e);
+            const auto ff = M::template split<M::NT>(gdr_pair(*reinterpret_cast<const gf4*>(&mf[r][c]), *reinterpret_cast<const gf4*>(&mf[r][c + 16])));
 #pragma unroll
             for (int u = 0; u < NS; ++u) {
-                if (i >= 2 * s) aq[u][i] = M::template mul<M::NP>(kf[u], ef, aq[u][i]);
-                av[u][i] = M::template mul<M::NP>(kf[u], ff, av[u][i]);
+                if (i >= 2 * s) aq[u][i] = M::template mul<M::NT>(kf[u], ef, aq[u][i]);
+                av[u][i] = M::template mul<M::NT>(kf[u], ff, av[u][i]);
             }
         }
     }
@@ -1672,9 +1723,9 @@ k_gdr_grads(const LaunchGdr p) {
                 const int r = 32 * s + 16 * (j >> 2) + 4 * g + (j & 3);
                 e[j] = r >= 16 * i + m ? me[r][16 * i + m] : 0.0f;
             }
-            const auto ef = M::template split<M::NP>(e);
+            const auto ef = M::template split<M::NT>(e);
 #pragma unroll
-            for (int u = 0; u < NS; ++u) av[u][i] = M::template mul<M::NP>(qf[u], ef, av[u][i]);
+            for (int u = 0; u < NS; ++u) av[u][i] = M::template mul<M::NT>(qf[u], ef, av[u][i]);
         }
     }
     // gates: a wave has 16 tokens t. Sums over j < t of the terms (i, j) are products with a triangle of ones, and a lane adds

@@ -29,3 +29,43 @@ def test_state_in_and_out_beside_other_work(shape, io):
         assert all(torch.equal(s, t) for s, t in zip(got, want))
         torch.cuda.synchronize()
     assert torch.isfinite(b[0, 0])
+
+
+@pytest.mark.parametrize("K", [2, 8, 100, 128, 256])
+def test_what_is_made_in_32_bits_keeps_them(K):
+    """States, products with beta, solutions and pairs of tokens of 1 + 2^-8 + 2^-20, each times 1 and next to zeros: every
+    product and sum is exact in 32 bits, and the result is 2^-20 above a tie of bf16, so that it rounds up to 1 + 2^-7. With
+    fewer than 20 bits of any of them it would be the tie, which goes to 1."""
+    up, tie = 1.0 + 2.0 ** -7, 1.0 + 2.0 ** -8 + 2.0 ** -20
+    z = lambda *s: torch.zeros(*s, device="cuda")  # noqa: E731
+    q, k, v = z(1, 2, 1, K), z(1, 2, 1, K), z(1, 2, 1, 1)
+    g, beta = z(1, 2, 1), z(1, 2, 1)
+
+    def call(S=None, dy=None):
+        x = (*(t.bfloat16() for t in (q, k, v)), g, beta)
+        ck = torch.empty(ss.gdr_ckpt_shape(1, 2, 1, K, 1), device="cuda")
+        y = ss.ss_gdr_fwd(*x, scale=1.0, eps=None, state=S, ckpt=ck)
+        return y if dy is None else ss.ss_gdr_bwd(*x, ck, dy.bfloat16(), scale=1.0, eps=None)
+
+    # y = S^T q
+    q[..., 0] = 1.0
+    S = z(1, 1, K, 1)
+    S[..., 0, 0] = tie
+    assert (call(S).float() == up).all()
+    # y_0 = (q . k) beta v
+    k[0, 0, 0, 0], v[0, 0, 0, 0], beta[0, 0, 0] = 1.0, 1.0, tie
+    assert call()[0, 0, 0, 0].item() == up
+    # and its gradients: beta (dy . v) k and beta (dy . v) q
+    dy = z(1, 2, 1, 1)
+    dy[0, 0] = 1.0
+    got = call(dy=dy)
+    assert got["dq"][0, 0, 0, 0].item() == up and got["dk"][0, 0, 0, 0].item() == up and got["dv"][0, 0, 0, 0].item() == up
+    # x_1 = v_1 - beta_0 (k_1 . k_0) v_0, alone in y_1
+    k[0, 1, 0, :2] = 1.0
+    q[0, 1, 0, 0], q[0, 1, 0, 1] = 0.0, 1.0
+    v[0, 1], beta[0, 0, 0], beta[0, 1, 0] = up, 2.0 ** -8 - 2.0 ** -20, 1.0
+    assert call()[0, 1, 0, 0].item() == up
+    # -beta_0 (dv_1 . x_0) k_0 in the gradient of k_1
+    k[0, 1, 0, 0], beta[0, 0, 0], v[0, 1] = 0.0, tie, 0.0
+    dy[0, 0], dy[0, 1] = 0.0, 1.0
+    assert call(dy=dy)["dk"][0, 1, 0, 0].item() == -up
