@@ -77,6 +77,7 @@ size_t ckpt_floats(const ss_gdr_dims& d) { return ckpt_states(d) + (size_t)d.bat
 struct GdrLayout { size_t co, wT, wS, wV, pq, pk, wE, wM, wF, total; int64_t seg, nseg; };
 GdrLayout gdr_layout(const ss_gdr_dims& d, bool backward) {
     GdrLayout l{};
+    if (d.seqlen == 0) return l;
     const size_t n = (size_t)d.batch * d.heads * (size_t)ceil_div(d.seqlen, SS_GDR_CHUNK);
     const size_t rows = (size_t)d.batch * (size_t)d.seqlen * d.heads;
     size_t off = 0;
@@ -88,7 +89,7 @@ GdrLayout gdr_layout(const ss_gdr_dims& d, bool backward) {
     if (!backward) {
         const int64_t chunks = l.seg;
         l.seg = selscan::gdr_segment(d.batch * d.heads, d.dv, chunks, d.io_dtype == SS_BF16 && d.dk <= 128);
-        l.nseg = ceil_div(chunks, l.seg > 0 ? l.seg : 1);
+        l.nseg = ceil_div(chunks, l.seg);
         if (l.nseg > 1) {
             const size_t ends = (size_t)(l.nseg - 1) * d.batch * d.heads;
             take(l.wE, (size_t)l.nseg * d.batch * d.heads * d.dk * d.dv);

@@ -69,3 +69,11 @@ def test_what_is_made_in_32_bits_keeps_them(K):
     k[0, 1, 0, 0], beta[0, 0, 0], v[0, 1] = 0.0, tie, 0.0
     dy[0, 0], dy[0, 1] = 0.0, 1.0
     assert call(dy=dy)["dk"][0, 1, 0, 0].item() == -up
+
+
+@pytest.mark.parametrize("heads", [2, 300])
+def test_gradients_of_no_tokens_are_refused(heads):
+    x, _, dy, _, _ = T.make(1, 0, 1, heads, 16, 32, "bf16")
+    with pytest.raises(ss.SelscanError):
+        ss.ss_gdr_bwd(*x, torch.empty(0, device="cuda"), dy)
+    assert ss.ss_gdr_fwd(*x).shape == (1, 0, heads, 32)

@@ -1,4 +1,9 @@
 """CPU: sizes that the delta rule's and the norms' C ABI gives, where a wrong one is a race or ends the process."""
+import subprocess
+import sys
+
+import pytest
+
 import selective_state_space_73_amd as ss
 
 
@@ -14,3 +19,13 @@ def test_segments_have_a_state_in_front_of_every_one():
     for io in (ss.SS_BF16, ss.SS_F32):
         more = ss.ss_gdr_workspace_bytes(rdims(dv=128, io_dtype=io)) - ss.ss_gdr_workspace_bytes(rdims(io_dtype=io))
         assert more == 3 * 64 * 64 * 4
+
+
+@pytest.mark.parametrize("backward", [False, True])
+@pytest.mark.parametrize("kw", [dict(), dict(batch=8, heads=40, dk=128, dv=128), dict(batch=4, heads=64, k_heads=2, dv=512)])
+def test_no_tokens_need_no_workspace(kw, backward):
+    """Whatever the number of heads (in a process of its own: a division by zero ends it)."""
+    code = f"import sys; sys.path[:0] = {sys.path!r}; import test_layer_rules as t; " \
+           f"print(t.ss.ss_gdr_workspace_bytes(t.rdims(**{dict(kw, seqlen=0)!r}), {backward}))"
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True)
+    assert r.returncode == 0 and r.stdout.split() == ["0"], r.stderr[-500:]
