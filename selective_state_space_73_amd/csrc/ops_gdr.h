@@ -371,7 +371,7 @@ struct GdrRows {
 
 // What k_gdr_solve leaves of a chunk's tokens: rows of 64 floats.
 //   a1 e^G / |k|, a2 e^G, a3 beta e^(G_last - G) / |k|, bk beta / |k|, misc { e^G_last, whether no factor is 0,
-//   G_last in powers of two, whether every beta |k|^2 is in [0, 2] },
+//   G_last in powers of two, whether every beta |k|^2 is in [0, 2], whether a decay is 0 },
 //   G itself, times log2 e, in 64 bits (two rows)
 //   for the gradients as well: e^(G_last - G) / |k|, beta, 1 / |k|
 enum GdrTok { tA1, tA2, tA3, tBk, tMisc, tG, kGdrTok = 7, tA3b = 7, tBeta, tRk, kGdrTokAll };
@@ -450,7 +450,8 @@ k_gdr_solve(const LaunchGdr p) {
                 for (int j = 0; j <= i; ++j) kk[i * (i + 1) / 2 + j] = M::mm(f[i], f[j], kk[i * (i + 1) / 2 + j]);
         }
     }
-    G = (G < -200.0 || cut ? -200.0 : G) * 1.4426950408889634;
+    cut |= G <= -200.0;
+    G = (cut ? -200.0 : G) * 1.4426950408889634;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
         const double u = __shfl_up(G, o, 64);
@@ -480,8 +481,8 @@ k_gdr_solve(const LaunchGdr p) {
         tok[tBk * 64] = bk;
         const bool clean = __all(a1 != 0.0f && e != 0.0f);
         const float grow = p.eps > 0.0f ? beta : beta * k2;
-        const bool tame = __all(grow >= 0.0f && grow <= 2.0f);
-        tok[tMisc * 64] = lane == 0 ? __builtin_amdgcn_exp2f((float)Gl) : lane == 2 ? (float)Gl : (lane == 1 ? clean : tame) ? 1.0f : 0.0f;
+        const bool tame = __all(grow >= 0.0f && grow <= 2.0f), any_cut = __any(cut);
+        tok[tMisc * 64] = lane == 0 ? __builtin_amdgcn_exp2f((float)Gl) : lane == 2 ? (float)Gl : (lane == 1 ? clean : lane == 3 ? tame : any_cut) ? 1.0f : 0.0f;
         *reinterpret_cast<double*>(p.co + id * (kGdrTokAll * 64) + tG * 64 + 2 * lane) = G;
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -947,29 +948,35 @@ k_gdr_walk(const LaunchGdr p) {
 // How many of the chunks [n0, n1), from its end backwards or (AHEAD) from its start on, it takes until they leave less than
 // 2^-48 of a state that passes them; all if they never do, `gone` says whether they do. Where no beta |k|^2 is outside
 // [0, 2] no state, and no gradient of one, grows on the way but by what is added to it, so that behind those chunks nothing in
-// front of them is left but 2^-48 of its own size: not a bit of an fp32 state of that size. (Any other one on the way: all.)
+// front of them is left but 2^-48 of its own size: not a bit of an fp32 state of that size. A chunk with a decay of 0 leaves
+// nothing, whatever its beta and theirs, of a state of NaN neither (which a map of zeros would not stop).
 template <bool AHEAD>
 __device__ __forceinline__ int64_t gdr_reach(const LaunchGdr& p, int64_t bh, int64_t n0, int64_t n1, bool& gone) {
     const int lane = threadIdx.x & 63;
     gone = false;
     float sum = 0.0f;
+    bool shrinks = true;
     for (int64_t done = 0; done < n1 - n0; done += 64) {
         const int64_t at = done + lane;
         float g = 0.0f;
-        bool tame = true;
+        bool tame = true, cut = false;
         if (at < n1 - n0) {
             const float* misc = p.co + (bh * p.nchunks + (AHEAD ? n0 + at : n1 - 1 - at)) * (kGdrTokAll * 64) + tMisc * 64;
             g = misc[2];
             tame = misc[3] != 0.0f;
+            cut = misc[4] != 0.0f;
         }
 #pragma unroll
         for (int o = 1; o < 64; o <<= 1) {
             const float u = __shfl_up(g, o, 64);
             if (lane >= o) g += u;
         }
-        const uint64_t low = __ballot(at < n1 - n0 && sum + g < -48.0f), wild = __ballot(!tame);
-        const int to = low ? __builtin_ctzll(low) : 64, bad = wild ? __builtin_ctzll(wild) : 64;
-        if (bad <= to && bad < 64) break;
+        const uint64_t low = __ballot(at < n1 - n0 && sum + g < -48.0f), wild = __ballot(!tame), zero = __ballot(cut);
+        const int bad = wild ? __builtin_ctzll(wild) : 64;
+        int to = low && shrinks ? __builtin_ctzll(low) : 64;
+        if (bad <= to) to = 64;
+        if (zero && (int)__builtin_ctzll(zero) < to) to = __builtin_ctzll(zero);
+        shrinks &= bad == 64;
         if (to < 64) {
             gone = true;
             return done + to + 1;

@@ -77,3 +77,28 @@ def test_gradients_of_no_tokens_are_refused(heads):
     with pytest.raises(ss.SelscanError):
         ss.ss_gdr_bwd(*x, torch.empty(0, device="cuda"), dy)
     assert ss.ss_gdr_fwd(*x).shape == (1, 0, heads, 32)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("beta", [2.5, -0.5])
+def test_a_reset_ends_a_segments_memory_whatever_beta_is_behind_it(beta, io):
+    """Nine chunks in segments of 4, 4 and 1. The state in front is NaN up to a reset in the middle segment; behind the reset one
+    beta is outside [0, 2]. A state grows by at most 1.5 there, and an error with it."""
+    x, _, dy, dS, _ = T.make(1, 64 * 9, 1, 2, 64, 48, io, seed=43)
+    S0 = torch.full((1, 2, 64, 48), float("nan"), device="cuda")
+    at = 64 * 5
+    x[4][0, at + 70] = beta
+    z = torch.zeros(1, 64 * 9, dtype=torch.uint8, device="cuda")
+    z[0, at] = 1
+    y, S, ck = T.run(x, S0, reset=z)
+    tail = tuple(t[:, at:] for t in x)
+    yw, Sw = O.gdr_fwd(*tail)
+    T.near(y[:, at:], yw, 1.5 * T.rel(64, 256), io)
+    T.near(S, Sw, 1.5 * T.rel(64, 256), "f32")
+    assert torch.isnan(y[:, :at]).all()
+    got, want = ss.ss_gdr_bwd(*x, ck, dy, reset=z, dstate_final=dS), O.gdr_bwd(*tail, dy[:, at:], None, None, dS)
+    for n in ("dq", "dk", "dv", "dbeta"):
+        T.near(got[n][:, at:], want[n], 1.5 ** 2 * 2 * T.rel(64, 256, 48), io if n != "dbeta" else "f32")
+    # the state's gradient does not depend on the state
+    want = O.gdr_bwd(*(t[:, :at] for t in x), dy[:, :at])["dstate_init"]
+    T.near(got["dstate_init"], want, 2 * T.rel(64, at, 48), "f32")
