@@ -646,6 +646,8 @@ struct GdrWalk {
             }
     }
     __device__ __forceinline__ void store_state(float* to, int n) const {
+        int g = this->g, col = this->col;
+        asm volatile("" : "+v"(g), "+v"(col));
         if (in)
 #pragma unroll
             for (int d = 0; d < ND; ++d)
@@ -654,6 +656,32 @@ struct GdrWalk {
                     const int row = 32 * (d >> 1) + 8 * g + 4 * (d & 1) + r;
                     if (row < p.dk) to[row * n + col] = S[d][r];
                 }
+    }
+    // Whether this wave's columns are those of the state at `with`: within 2^-16 of the largest of a column, or the smallest
+    // normal number. Not for NaN and infinities. (Two ways through a segment without decay differ by up to 2^-20, by the
+    // roundings of both; with that as the bound 65536 tokens of 4 heads took 3.3 ms, with this 0.82.)
+    __device__ __forceinline__ bool agrees(const float* with) const {
+        const GdrBuf<float> buf(with, (unsigned)(p.dk * p.dv) * 4);
+        int g = this->g, col = this->col;             // places are made here, not kept from where the state was loaded
+        asm volatile("" : "+v"(g), "+v"(col));
+        float most = 0.0f, off = 0.0f;
+        bool same = true;
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = 32 * (d >> 1) + 8 * g + 4 * (d & 1) + r;
+                const float by = fabsf(S[d][r] - buf.ld(in ? (unsigned)(row * p.dv + col) * 4 : kGdrOut, 0));
+                most = fmaxf(most, fabsf(S[d][r]));
+                off = fmaxf(off, by);
+                same &= by < __builtin_inff();
+            }
+#pragma unroll
+        for (int o = 16; o < 64; o <<= 1) {
+            most = fmaxf(most, __shfl_xor(most, o, 64));
+            off = fmaxf(off, __shfl_xor(off, o, 64));
+        }
+        return __all(!in || (same && off <= fmaxf(most * 0x1p-16f, 0x1p-126f)));
     }
     template <bool OUT>
     __device__ __forceinline__ void rest(int64_t n) const {       // queries, T, factors of chunk n
@@ -943,12 +971,19 @@ k_gdr_walk(const LaunchGdr p) {
     __syncthreads();
     gdr_walk<true>(k, n0, n1, k0, k1);
     if (p.state && n1 == nc) k.store_state(p.state + bh * kv, p.dv);
+    if (n1 < nc) {
+        const int64_t next = (seg + 1) * BH + bh;
+        const bool same = k.agrees(p.wE + next * kv);
+        if (!same) k.store_state(p.wX + (next - BH) * kv, p.dv);
+        if ((threadIdx.x & 63) == 0) p.wQ[((bh * tiles + rest % tiles) * (p.nseg - 1) + seg) * 4 + k.w] = same ? 0.0f : 1.0f;
+    }
 }
 
 // How many of the chunks [n0, n1), from its end backwards or (AHEAD) from its start on, it takes until they leave less than
 // 2^-48 of a state that passes them; all if they never do, `gone` says whether they do. Where no beta |k|^2 is outside
 // [0, 2] no state, and no gradient of one, grows on the way but by what is added to it, so that behind those chunks nothing in
-// front of them is left but 2^-48 of its own size: not a bit of an fp32 state of that size. A chunk with a decay of 0 leaves
+// front of them is left but 2^-48 of its own size. That is nothing beside a state of that size; whether it is nothing beside
+// what the segment makes is seen when the walk gets to its end (k_gdr_again). A chunk with a decay of 0 leaves
 // nothing, whatever its beta and theirs, of a state of NaN neither (which a map of zeros would not stop).
 template <bool AHEAD>
 __device__ __forceinline__ int64_t gdr_reach(const LaunchGdr& p, int64_t bh, int64_t n0, int64_t n1, bool& gone) {
@@ -1086,6 +1121,44 @@ k_gdr_join(const LaunchGdr p) {
     }
 }
 
+// Segments that did not start from what the one in front came to, once more from there, one after the other: where a segment's
+// decays leave little of the state in front, but the segment makes less (values that end, states of very different sizes), and
+// where that state is NaN or infinite. Where there is none of them it takes 5 us.
+template <typename T, int DKP, bool TWO, bool AL>
+__global__ void __launch_bounds__(256, 1)
+k_gdr_again(const LaunchGdr p) {
+    using W = GdrWalk<T, DKP, TWO, AL>;
+    __shared__ alignas(16) T k0[64 * DKP], k1[TWO ? 64 * DKP : 8], tq[64 * DKP], tt[Mx<T>::NT * kGdrLow], tp[Mx<T>::NT * kGdrLow];
+    __shared__ alignas(16) float tok[kGdrTok * 64], srq[64];
+    const int64_t BH = p.B * p.H, bh = blockIdx.x % BH, tile = blockIdx.x / BH, b = bh / p.H, nc = p.nchunks, kv = (int64_t)p.dk * p.dv;
+    const int tiles = (p.dv + 63) / 64, h = (int)(bh % p.H), hk = h / (p.H / p.Hk), lane = threadIdx.x & 63;
+    const float* off = p.wQ + (bh * tiles + tile) * (p.nseg - 1) * 4;
+    bool any = false;
+    for (int i = lane; i < (p.nseg - 1) * 4; i += 64) any |= off[i] != 0.0f;
+    if (!__any(any)) return;
+    W k(p, tq, tt, tp, tok, srq, b, bh, h, hk, (int)tile * 64 + gdr_wave() * 16 + (lane & 15));
+    if (p.dk < DKP) {
+        gdr_clear<64 * DKP>(k0);
+        gdr_clear<64 * DKP>(tq);
+        if (TWO) gdr_clear<64 * DKP>(k1);
+    }
+    bool here = false;                                // the state in front of the segment is in registers
+    for (int seg = 1; seg < p.nseg; ++seg) {
+        const float* from = p.wE + (seg * BH + bh) * kv;
+        const float* o = off + (seg - 1) * 4;
+        const bool own = here ? !k.agrees(from) : o[k.w] != 0.0f;
+        // (a barrier, too: the last segment's LDS is used up, the zeros are there)
+        if (!__syncthreads_or(own)) {
+            here = false;
+            continue;
+        }
+        if (!here) k.load_state(own ? p.wX + ((seg - 1) * BH + bh) * kv : from, p.dv);
+        const int64_t n0 = seg * p.seg, n1 = n0 + p.seg < nc ? n0 + p.seg : nc;
+        gdr_walk<true>(k, n0, n1, k0, k1);
+        here = true;
+        if (p.state && n1 == nc) k.store_state(p.state + bh * kv, p.dv);
+    }
+}
 
 // ---------------------------------------------------------------------------
 // The backward from chunk to chunk, the last first, with W the gradient of the state behind a chunk in
@@ -2028,6 +2101,10 @@ hipError_t launch_gdr_d(const LaunchGdr& p) {
         const dim3 walk((unsigned)(tiles * p.nseg));
         if (al) hipLaunchKernelGGL((k_gdr_walk<T, DKP, kTwo, true, kGroups>), walk, dim3(256), 0, st, p);
         else hipLaunchKernelGGL((k_gdr_walk<T, DKP, kTwo, false, kGroups>), walk, dim3(256), 0, st, p);
+        if (p.nseg > 1) {
+            if (al) hipLaunchKernelGGL((k_gdr_again<T, DKP, kTwo, true>), dim3(tiles), dim3(256), 0, st, p);
+            else hipLaunchKernelGGL((k_gdr_again<T, DKP, kTwo, false>), dim3(tiles), dim3(256), 0, st, p);
+        }
         return hipGetLastError();
     }
     hipLaunchKernelGGL((k_gdr_solve<T, DKP, true>), dim3((chunks + 3) / 4), dim3(256), 0, st, p);

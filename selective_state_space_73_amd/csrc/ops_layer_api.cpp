@@ -72,9 +72,9 @@ size_t ckpt_states(const ss_gdr_dims& d) {
 size_t ckpt_floats(const ss_gdr_dims& d) { return ckpt_states(d) + (size_t)d.batch * (size_t)d.seqlen * d.heads * d.dv; }
 
 // Per chunk and head: the tokens' factors and the inverse (6 blocks of 16 x 32, three bf16 terms or fp32). The forward in
-// segments: the states in front of them and what they make of these. The backward: the state's gradient behind every
+// segments: the states in front of them, what they make of these, and the states behind them. The backward: the state's gradient behind every
 // chunk, the gradients of v in fp32, and those of q and k by head of v where heads share them.
-struct GdrLayout { size_t co, wT, wS, wV, pq, pk, wE, wM, wF, total; int64_t seg, nseg; };
+struct GdrLayout { size_t co, wT, wS, wV, pq, pk, wE, wM, wF, wX, wQ, total; int64_t seg, nseg; };
 GdrLayout gdr_layout(const ss_gdr_dims& d, bool backward) {
     GdrLayout l{};
     if (d.seqlen == 0) return l;
@@ -95,6 +95,8 @@ GdrLayout gdr_layout(const ss_gdr_dims& d, bool backward) {
             take(l.wE, (size_t)l.nseg * d.batch * d.heads * d.dk * d.dv);
             take(l.wM, ends * d.dk * d.dk);
             take(l.wF, ends);
+            take(l.wX, ends * d.dk * d.dv);
+            take(l.wQ, ends * (size_t)ceil_div(d.dv, 64) * 4);
         }
     }
     if (backward) {
@@ -184,7 +186,7 @@ void gdr_attach(selscan::LaunchGdr& p, const ss_gdr_dims& d, const GdrLayout& l,
     p.co = at(l.co); p.wT = at(l.wT);
     p.seg = l.seg;
     p.nseg = (int)l.nseg;
-    p.wE = at(l.wE); p.wM = at(l.wM); p.wF = at(l.wF);
+    p.wE = at(l.wE); p.wM = at(l.wM); p.wF = at(l.wF); p.wX = at(l.wX); p.wQ = at(l.wQ);
     if (backward) {
         p.wS = at(l.wS); p.wV = at(l.wV);
         if (d.heads > d.k_heads) { p.part_q = at(l.pq); p.part_k = at(l.pk); }

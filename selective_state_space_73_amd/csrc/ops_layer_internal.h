@@ -32,6 +32,8 @@ struct LaunchGdr {
     float *wE, *wM, *wF;         // several segments: [nseg, B, H, dk, dv] states in front of the segments (the first: the caller's, if
                                  // there is one), [nseg - 1, B, H, dk, dk] what they make of these, [nseg - 1, B, H] whether
                                  // anything of it is left
+    float *wX, *wQ;              // and [nseg - 1, B, H, dk, dv] states behind the segments, written where they are not those in front of
+                                 // the next ones, [B, H, tiles of 64 columns, nseg - 1, 4 waves] where that is
     float *co, *wT;              // [B, H, chunks]: factors of tokens, inverses in the order of operands
     float *wS, *wV;              // the backward: [B, H, chunks, dk, dv] adjoints behind the chunks, [B, L, H, dv] gradients of v
     float *part_q, *part_k;      // the backward where heads share keys: [B, L, H, dk] each head's share

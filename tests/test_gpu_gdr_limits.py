@@ -102,3 +102,56 @@ def test_a_reset_ends_a_segments_memory_whatever_beta_is_behind_it(beta, io):
     # the state's gradient does not depend on the state
     want = O.gdr_bwd(*(t[:, :at] for t in x), dy[:, :at])["dstate_init"]
     T.near(got["dstate_init"], want, 2 * T.rel(64, at, 48), "f32")
+
+
+def fading(K, V, io, heads=1):
+    """Nine chunks, in segments of 4, 4 and 1, each of which brings a state down by 2^-13, and nothing beside it. A power of two
+    is the state's own size, so that 2^60 stays within fp32 in products of a state and a gradient."""
+    x, S0, dy, dS, _ = T.make(1, 64 * 9, heads, heads, K, V, io, seed=47 + K)
+    x[2].zero_()
+    x[4].zero_()
+    dy.zero_()
+    x[3].fill_(-13 / 64 * 0.6931471805599453)
+    return x, S0 * 2.0 ** 60, dy, dS * 2.0 ** 60
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("K,V", [(64, 64), (100, 70), (128, 128), (256, 80)])
+def test_segments_keep_what_is_left_of_large_states(K, V, io):
+    """2^60 down to 2^-57: every result is relative to what is left, with states from the forward and by a copy of a row at
+    a later chunk."""
+    x, S0, _, _ = fading(K, V, io)
+    y, S, _ = T.run(x, S0)
+    yw, Sw = O.gdr_fwd(*x, S0)
+    for n in range(0, 9):
+        at = slice(64 * n + 60, 64 * n + 64)
+        T.near(y[:, at], yw[:, at], T.rel(K, 512), io)
+    T.near(S, Sw, T.rel(K, 512), "f32")
+    # a value in one chunk of a segment, nothing in the next ones, and a short segment behind them
+    x[2][:, 200] = 2.0 ** 40
+    x[4][:, 200] = 1.0
+    y, S, ck = T.run(x, S0)
+    yw, Sw = O.gdr_fwd(*x, S0)
+    for n in range(4, 9):
+        at = slice(64 * n + 60, 64 * n + 64)
+        T.near(y[:, at], yw[:, at], T.rel(K, 512), io)
+    T.near(S, Sw, T.rel(K, 512), "f32")
+    T.near(ck[:-64 * 9 * V].view(9, K, V)[8], O.gdr_fwd(*(t[:, :512] for t in x), S0)[1][0, 0], T.rel(K, 512), "f32")
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_nan_stays_however_the_call_is_cut(io):
+    """One head of one row runs in segments, of many rows in one: a NaN, which no decay but one of 0 ends, reaches the same
+    tokens."""
+    x, S0, _, _ = fading(64, 96, io)
+    x[2].copy_(torch.randn_like(x[2]))
+    x[4].fill_(0.5)
+    x[2][0, 10, 0, 3] = float("nan")
+    S0[0, 0, 7, 70] = float("inf")
+    y, S, _ = T.run(x, S0)
+    many = tuple(t.expand(300, *t.shape[1:]).contiguous() for t in x)
+    ym, Sm, _ = T.run(many, S0.expand(300, -1, -1, -1))
+    bad = torch.zeros(96, dtype=torch.bool, device="cuda")
+    bad[3] = bad[70] = True
+    for a, b in ((y, S), (ym[:1], Sm[:1])):
+        assert (torch.isfinite(a[0, 64:, 0]) == ~bad).all() and (torch.isfinite(b[0, 0]) == ~bad).all()
