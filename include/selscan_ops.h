@@ -203,9 +203,7 @@ ss_status ss_block_q8_step(const ss_block_dims* dims, const ss_block_q8_weights*
  * A log decay of -200 or less (minus infinity among them) is a decay of 0, as a reset is. A decay
  * of 0 leaves out what it multiplies between chunks of 64 tokens (tokens 0 to 63, 64 to 127, ...) and
  * in a step, so that not even a NaN passes it there. Within a chunk a value that is not finite may reach every
- * token of the chunk, earlier ones as well; everywhere else it propagates to later tokens. Where whole
- * chunks leave less than 2^-48 of a state's gradient that passes them and every
- * beta |k^|^2 in them is in [0, 2], so that nothing grows on the way, that may be taken for 0, too.
+ * token of the chunk, earlier ones as well; everywhere else it propagates to later tokens.
  * g > 0, beta and the lengths of keys that are used as they are (eps = 0) are the caller's: with
  * 0 <= beta |k^|^2 <= 2 no state grows; nothing is checked.
  *

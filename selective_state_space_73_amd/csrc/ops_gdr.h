@@ -602,37 +602,16 @@ k_gdr_solve(const LaunchGdr p) {
 }
 
 // ---------------------------------------------------------------------------
-// From chunk to chunk: a workgroup holds 64 columns of one head's state, a wave 16 of them, in
-// registers. What all waves need lies in LDS: keys twice (the next chunk's come while this one's are in
-// use), queries, T and the tokens' factors once, loaded again as soon as the last wave has used them; P is
-// made here, two or three tiles a wave, since reading it back would cost as much as T. Two workgroups a CU
-// in bf16 (registers and LDS hold no third). 131072 tokens of 16 heads of 128 x 128 in bf16: 1.0 ms, a chunk 18,000 cycles
-// for two workgroups and 11,800 for one alone on its CU: what bounds it is a chunk's chain (read, multiply, solve,
-// multiply), with the matrix cores and the vector units each busy for about 40%. With checkpoints it writes more
-// than it reads: 8 x 2048 tokens of 40 heads 593 us, 3.2 TB/s (640 workgroups for 512 places: about a quarter of it).
-template <typename T, int DKP, bool TWO, bool AL>
-struct GdrWalk {
-    using M = Mx<T>;
-    static constexpr int KD = DKP / 32, ND = DKP / 16, TP = kGdrLow;
-    static constexpr bool kTwo = TWO;
+// A wave's 16 columns of a state, or of its gradient, in registers.
+template <int ROWS>
+struct GdrState {
+    static constexpr int ND = ROWS / 16;
     const LaunchGdr& p;
-    GdrRows<T, KD, AL> rk, rq;
-    T *tq, *tt, *tp;
-    float *tok, *srq;
-    int64_t b, bh, nc;
-    int h, lane, w, g, m, col, place;
-    bool in, from_v = true;
-    const T* vb;
-    T* yb;
+    int lane, w, g, m, col;
+    bool in;
     gf4 S[ND];
-    T v[16];                                          // the next values as they came, no use of them before they are needed
-
-    __device__ __forceinline__ GdrWalk(const LaunchGdr& a, T* q_, T* t_, T* p_, float* tok_, float* srq_, int64_t b_, int64_t bh_, int h_,
-                                       int hk, int col_)
-        : p(a), rk(a.k, b_, hk, a.dk), rq(a.q, b_, hk, a.dk), tq(q_), tt(t_), tp(p_), tok(tok_), srq(srq_), b(b_), bh(bh_),
-          nc(a.nchunks), h(h_), lane(threadIdx.x & 63), w(gdr_wave()), g(lane >> 4), m(lane & 15), col(col_), place(gdr_place(g, m)), in(col_ < a.dv),
-          vb(static_cast<const T*>(a.v.p) + b_ * a.v.batch_stride + h_ * a.v.head_stride),
-          yb(static_cast<T*>(a.y) + (b_ * a.L * a.H + h_) * a.dv) {}
+    __device__ __forceinline__ GdrState(const LaunchGdr& a, int col_)
+        : p(a), lane(threadIdx.x & 63), w(gdr_wave()), g(lane >> 4), m(lane & 15), col(col_), in(col_ < a.dv) {}
 
     // this wave's columns of a state [dk, n]; zeros where there is none
     __device__ __forceinline__ void load_state(const float* from, int n) {
@@ -683,6 +662,40 @@ struct GdrWalk {
         }
         return __all(!in || (same && off <= fmaxf(most * 0x1p-16f, 0x1p-126f)));
     }
+};
+
+// ---------------------------------------------------------------------------
+// From chunk to chunk: a workgroup holds 64 columns of one head's state, a wave 16 of them, in
+// registers. What all waves need lies in LDS: keys twice (the next chunk's come while this one's are in
+// use), queries, T and the tokens' factors once, loaded again as soon as the last wave has used them; P is
+// made here, two or three tiles a wave, since reading it back would cost as much as T. Two workgroups a CU
+// in bf16 (registers and LDS hold no third). 131072 tokens of 16 heads of 128 x 128 in bf16: 1.0 ms, a chunk 18,000 cycles
+// for two workgroups and 11,800 for one alone on its CU: what bounds it is a chunk's chain (read, multiply, solve,
+// multiply), with the matrix cores and the vector units each busy for about 40%. With checkpoints it writes more
+// than it reads: 8 x 2048 tokens of 40 heads 593 us, 3.2 TB/s (640 workgroups for 512 places: about a quarter of it).
+template <typename T, int DKP, bool TWO, bool AL>
+struct GdrWalk : GdrState<DKP> {
+    using M = Mx<T>;
+    using B = GdrState<DKP>;
+    using B::p; using B::lane; using B::w; using B::g; using B::m; using B::col; using B::in; using B::S;
+    static constexpr int KD = DKP / 32, ND = DKP / 16, TP = kGdrLow;
+    static constexpr bool kTwo = TWO;
+    GdrRows<T, KD, AL> rk, rq;
+    T *tq, *tt, *tp;
+    float *tok, *srq;
+    int64_t b, bh, nc;
+    int h, place;
+    bool from_v = true;
+    const T* vb;
+    T* yb;
+    T v[16];                                          // the next values as they came, no use of them before they are needed
+
+    __device__ __forceinline__ GdrWalk(const LaunchGdr& a, T* q_, T* t_, T* p_, float* tok_, float* srq_, int64_t b_, int64_t bh_, int h_,
+                                       int hk, int col_)
+        : B(a, col_), rk(a.k, b_, hk, a.dk), rq(a.q, b_, hk, a.dk), tq(q_), tt(t_), tp(p_), tok(tok_), srq(srq_), b(b_), bh(bh_),
+          nc(a.nchunks), h(h_), place(gdr_place(g, m)), vb(static_cast<const T*>(a.v.p) + b_ * a.v.batch_stride + h_ * a.v.head_stride),
+          yb(static_cast<T*>(a.y) + (b_ * a.L * a.H + h_) * a.dv) {}
+
     template <bool OUT>
     __device__ __forceinline__ void rest(int64_t n) const {       // queries, T, factors of chunk n
         if (OUT) rq.load(tq, n * kGdrC, p.L);
@@ -1167,29 +1180,27 @@ k_gdr_again(const LaunchGdr p) {
 //   W' = e^G_last W + (scale e^G Q)^T dY - (e^G K)^T dV
 // Keys and queries are needed to the end of a chunk and lie in LDS once, so that a CU holds two workgroups, of which
 // one waits for its next chunk while the other works. A long sequence in few heads is cut into segments that run at the
-// same time, each of which first takes what it needs of the state's gradient from the chunks behind it, as far back as they
+// same time. k_gdr_ends_back first makes the gradient behind each of them from the chunks behind it, as far back as they
 // count: all of them in the worst case, when the first segment takes as long as one workgroup did, on a card that
-// is not full. 8 x 2048 tokens of 40 heads of 128 x 128 in bf16: 633 us, 3.0 TB/s, bound as the forward's; 3 x 1001
+// is not full; what the walk comes to says whether that was far enough, and k_gdr_again_back repeats where it was not. 8 x 2048 tokens of 40 heads of 128 x 128 in bf16: 633 us, 3.0 TB/s, bound as the forward's; 3 x 1001
 // tokens of 6 heads of 96 x 129 in fp32, with resets: 114 us (239 in one segment).
 template <typename T, int DKP, bool AL>
-struct GdrWalkBack {
+struct GdrWalkBack : GdrState<DKP> {
     using M = Mx<T>;
+    using B = GdrState<DKP>;
+    using B::p; using B::lane; using B::w; using B::g; using B::m; using B::col; using B::in; using B::S;
     static constexpr int KD = DKP / 32, ND = DKP / 16, TP = kGdrTri;
-    const LaunchGdr& p;
     GdrRows<T, KD, AL> rk, rq;
     T *tk, *tq, *tt, *tp;
     float *tok, *srq;
     int64_t b, bh, nc;
-    int h, lane, w, g, m, col, place;
-    bool in;
-    gf4 S[ND];
+    int h, place;
     T v[16];                                          // the next gradients of y, as they came
 
     __device__ __forceinline__ GdrWalkBack(const LaunchGdr& a, T* k_, T* q_, T* t_, T* p_, float* tok_, float* srq_, int64_t b_, int64_t bh_,
                                            int h_, int hk, int col_)
-        : p(a), rk(a.k, b_, hk, a.dk), rq(a.q, b_, hk, a.dk), tk(k_), tq(q_), tt(t_), tp(p_), tok(tok_), srq(srq_), b(b_), bh(bh_),
-          nc(a.nchunks), h(h_), lane(threadIdx.x & 63), w(gdr_wave()), g(lane >> 4), m(lane & 15), col(col_), place(gdr_place(g, m)),
-          in(col_ < a.dv) {}
+        : B(a, col_), rk(a.k, b_, hk, a.dk), rq(a.q, b_, hk, a.dk), tk(k_), tq(q_), tt(t_), tp(p_), tok(tok_), srq(srq_), b(b_), bh(bh_),
+          nc(a.nchunks), h(h_), place(gdr_place(g, m)) {}
 
     __device__ __forceinline__ void factors(int64_t n) const {    // T^T and the tokens' factors of chunk n
         const int64_t id = bh * nc + n;
@@ -1417,6 +1428,47 @@ struct GdrWalkBack {
     }
 };
 
+// The chunks [n0, n1), the last first, from the gradient in k.S on; LDS as gdr_clear_back leaves it.
+template <bool OUT, typename W>
+__device__ __forceinline__ void gdr_walk_back(W& k, int64_t n0, int64_t n1) {
+    k.rk.load(k.tk, (n1 - 1) * kGdrC, k.p.L);
+    k.rq.load(k.tq, (n1 - 1) * kGdrC, k.p.L);
+    k.factors(n1 - 1);
+    k.values(n1 - 1);
+#pragma unroll 1
+    for (int64_t n = n1 - 1; n >= n0; --n) k.template chunk<OUT>(n, n0);
+}
+template <typename T, int DKP>
+__device__ __forceinline__ void gdr_clear_back(const LaunchGdr& p, T* tk, T* tq, T* tp) {
+    if (p.dk < DKP) {
+        gdr_clear<64 * DKP>(tk);
+        gdr_clear<64 * DKP>(tq);
+    }
+    gdr_clear<Mx<T>::NT * kGdrTri>(tp);
+    __syncthreads();
+}
+
+// Several segments: the gradient of the state behind each but the last.
+template <typename T, int DKP, bool AL, int GROUPS>
+__global__ void __launch_bounds__(256, GROUPS)
+k_gdr_ends_back(const LaunchGdr p) {
+    using W = GdrWalkBack<T, DKP, AL>;
+    __shared__ alignas(16) T tk[64 * DKP], tq[64 * DKP], tt[Mx<T>::NT * kGdrTri], tp[Mx<T>::NT * kGdrTri];
+    __shared__ alignas(16) float tok[kGdrTok * 64], srq[64];
+    const int64_t BH = p.B * p.H, rest = blockIdx.x / BH, bh = blockIdx.x % BH, b = bh / p.H, kv = (int64_t)p.dk * p.dv;
+    const int tiles = (p.dv + 63) / 64, seg = (int)(rest / tiles);
+    const int h = (int)(bh % p.H), hk = h / (p.H / p.Hk), col = (int)(rest % tiles) * 64 + gdr_wave() * 16 + (threadIdx.x & 15);
+    const int64_t n1 = (seg + 1) * p.seg;
+    bool gone;
+    const int64_t reach = gdr_reach<true>(p, bh, n1, p.nchunks, gone);
+    const int64_t from_n = n1 + __builtin_amdgcn_readfirstlane((int)reach);
+    W k(p, tk, tq, tt, tp, tok, srq, b, bh, h, hk, col);
+    k.load_state(p.gr.dstate_final && !gone ? p.gr.dstate_final + bh * kv : nullptr, p.dv);
+    gdr_clear_back<T, DKP>(p, tk, tq, tp);
+    gdr_walk_back<false>(k, n1, from_n);
+    k.store_state(p.wE + (seg * BH + bh) * kv, p.dv);
+}
+
 template <typename T, int DKP, bool AL, int GROUPS>
 __global__ void __launch_bounds__(256, GROUPS)
 k_gdr_walk_back(const LaunchGdr p) {
@@ -1427,42 +1479,47 @@ k_gdr_walk_back(const LaunchGdr p) {
     const int tiles = (p.dv + 63) / 64, seg = (int)(rest / tiles);
     const int h = (int)(bh % p.H), hk = h / (p.H / p.Hk), col = (int)(rest % tiles) * 64 + gdr_wave() * 16 + (threadIdx.x & 15);
     const int64_t n0 = seg * p.seg, n1 = n0 + p.seg < p.nchunks ? n0 + p.seg : p.nchunks;
-    bool gone;
-    const int64_t reach = gdr_reach<true>(p, bh, n1, p.nchunks, gone);
-    const int64_t from_n = n1 + __builtin_amdgcn_readfirstlane((int)reach);
     W k(p, tk, tq, tt, tp, tok, srq, b, bh, h, hk, col);
-    const float* from = p.gr.dstate_final && !gone ? p.gr.dstate_final + bh * kv : nullptr;
-#pragma unroll
-    for (int d = 0; d < W::ND; ++d)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int row = 32 * (d >> 1) + 8 * k.g + 4 * (d & 1) + r;
-            k.S[d][r] = from && row < p.dk && k.in ? from[row * p.dv + col] : 0.0f;
-        }
-    if (p.dk < DKP) {
-        gdr_clear<64 * DKP>(tk);
-        gdr_clear<64 * DKP>(tq);
+    k.load_state(seg < p.nseg - 1 ? p.wE + (seg * BH + bh) * kv : p.gr.dstate_final ? p.gr.dstate_final + bh * kv : nullptr, p.dv);
+    gdr_clear_back<T, DKP>(p, tk, tq, tp);
+    gdr_walk_back<true>(k, n0, n1);
+    if (seg == 0) {
+        if (p.gr.dstate_init) k.store_state(p.gr.dstate_init + bh * kv, p.dv);
+    } else {
+        const int64_t in_front = (seg - 1) * BH + bh;
+        const bool same = k.agrees(p.wE + in_front * kv);
+        if (!same) k.store_state(p.wX + in_front * kv, p.dv);
+        if ((threadIdx.x & 63) == 0) p.wQ[((bh * tiles + rest % tiles) * (p.nseg - 1) + seg - 1) * 4 + k.w] = same ? 0.0f : 1.0f;
     }
-    gdr_clear<Mx<T>::NT * kGdrTri>(tp);
-    __syncthreads();
-    k.rk.load(tk, (from_n - 1) * kGdrC, p.L);
-    k.rq.load(tq, (from_n - 1) * kGdrC, p.L);
-    k.factors(from_n - 1);
-    k.values(from_n - 1);
-#pragma unroll 1
-    for (int64_t n = from_n - 1; n >= n1; --n) k.template chunk<false>(n, n0);
-#pragma unroll 1
-    for (int64_t n = n1 - 1; n >= n0; --n) k.template chunk<true>(n, n0);
-    if (n0 > 0) return;
-    if (p.gr.dstate_init && k.in) {
-        float* to = p.gr.dstate_init + bh * kv;
-#pragma unroll
-        for (int d = 0; d < W::ND; ++d)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = 32 * (d >> 1) + 8 * k.g + 4 * (d & 1) + r;
-                if (row < p.dk) to[row * p.dv + col] = k.S[d][r];
-            }
+}
+
+// As k_gdr_again, from the last segment to the first.
+template <typename T, int DKP, bool AL>
+__global__ void __launch_bounds__(256, 1)
+k_gdr_again_back(const LaunchGdr p) {
+    using W = GdrWalkBack<T, DKP, AL>;
+    __shared__ alignas(16) T tk[64 * DKP], tq[64 * DKP], tt[Mx<T>::NT * kGdrTri], tp[Mx<T>::NT * kGdrTri];
+    __shared__ alignas(16) float tok[kGdrTok * 64], srq[64];
+    const int64_t BH = p.B * p.H, bh = blockIdx.x % BH, tile = blockIdx.x / BH, b = bh / p.H, kv = (int64_t)p.dk * p.dv;
+    const int tiles = (p.dv + 63) / 64, h = (int)(bh % p.H), hk = h / (p.H / p.Hk), lane = threadIdx.x & 63;
+    const float* off = p.wQ + (bh * tiles + tile) * (p.nseg - 1) * 4;
+    bool any = false;
+    for (int i = lane; i < (p.nseg - 1) * 4; i += 64) any |= off[i] != 0.0f;
+    if (!__any(any)) return;
+    W k(p, tk, tq, tt, tp, tok, srq, b, bh, h, hk, (int)tile * 64 + gdr_wave() * 16 + (lane & 15));
+    gdr_clear_back<T, DKP>(p, tk, tq, tp);
+    bool here = false;                                // the gradient behind the segment is in registers
+    for (int seg = p.nseg - 2; seg >= 0; --seg) {
+        const int64_t at = (seg * BH + bh) * kv;
+        const bool own = here ? !k.agrees(p.wE + at) : off[seg * 4 + k.w] != 0.0f;
+        if (!__syncthreads_or(own)) {                 // (a barrier, too: the last segment's LDS is used up)
+            here = false;
+            continue;
+        }
+        if (!here) k.load_state(own ? p.wX + at : p.wE + at, p.dv);
+        gdr_walk_back<true>(k, seg * p.seg, (seg + 1) * p.seg);
+        here = true;
+        if (seg == 0 && p.gr.dstate_init) k.store_state(p.gr.dstate_init + bh * kv, p.dv);
     }
 }
 
@@ -2108,12 +2165,17 @@ hipError_t launch_gdr_d(const LaunchGdr& p) {
         return hipGetLastError();
     }
     hipLaunchKernelGGL((k_gdr_solve<T, DKP, true>), dim3((chunks + 3) / 4), dim3(256), 0, st, p);
+    const dim3 ends(tiles * (p.nseg - 1)), walk(tiles * p.nseg);
     if (p.vec) {
-        hipLaunchKernelGGL((k_gdr_walk_back<T, DKP, true, kGroups>), dim3((unsigned)(tiles * p.nseg)), dim3(256), 0, st, p);
+        if (p.nseg > 1) hipLaunchKernelGGL((k_gdr_ends_back<T, DKP, true, kGroups>), ends, dim3(256), 0, st, p);
+        hipLaunchKernelGGL((k_gdr_walk_back<T, DKP, true, kGroups>), walk, dim3(256), 0, st, p);
+        if (p.nseg > 1) hipLaunchKernelGGL((k_gdr_again_back<T, DKP, true>), dim3(tiles), dim3(256), 0, st, p);
         if (p.vec_ck && p.vec_dy) hipLaunchKernelGGL((k_gdr_grads<T, DKP, true, true, kGrads>), dim3(chunks), dim3(256), 0, st, p);
         else hipLaunchKernelGGL((k_gdr_grads<T, DKP, true, false, kGrads>), dim3(chunks), dim3(256), 0, st, p);
     } else {
-        hipLaunchKernelGGL((k_gdr_walk_back<T, DKP, false, kGroups>), dim3((unsigned)(tiles * p.nseg)), dim3(256), 0, st, p);
+        if (p.nseg > 1) hipLaunchKernelGGL((k_gdr_ends_back<T, DKP, false, kGroups>), ends, dim3(256), 0, st, p);
+        hipLaunchKernelGGL((k_gdr_walk_back<T, DKP, false, kGroups>), walk, dim3(256), 0, st, p);
+        if (p.nseg > 1) hipLaunchKernelGGL((k_gdr_again_back<T, DKP, false>), dim3(tiles), dim3(256), 0, st, p);
         hipLaunchKernelGGL((k_gdr_grads<T, DKP, false, false, kGrads>), dim3(chunks), dim3(256), 0, st, p);
     }
     if (p.part_q) {

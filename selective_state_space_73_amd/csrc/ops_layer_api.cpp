@@ -72,8 +72,8 @@ size_t ckpt_states(const ss_gdr_dims& d) {
 size_t ckpt_floats(const ss_gdr_dims& d) { return ckpt_states(d) + (size_t)d.batch * (size_t)d.seqlen * d.heads * d.dv; }
 
 // Per chunk and head: the tokens' factors and the inverse (6 blocks of 16 x 32, three bf16 terms or fp32). The forward in
-// segments: the states in front of them, what they make of these, and the states behind them. The backward: the state's gradient behind every
-// chunk, the gradients of v in fp32, and those of q and k by head of v where heads share them.
+// segments: the states in front of them, what they make of these, and the states behind them. The backward: these of
+// gradients, the state's gradient behind every chunk, the gradients of v in fp32, and those of q and k by head of v where heads share them.
 struct GdrLayout { size_t co, wT, wS, wV, pq, pk, wE, wM, wF, wX, wQ, total; int64_t seg, nseg; };
 GdrLayout gdr_layout(const ss_gdr_dims& d, bool backward) {
     GdrLayout l{};
@@ -102,6 +102,12 @@ GdrLayout gdr_layout(const ss_gdr_dims& d, bool backward) {
     if (backward) {
         l.seg = selscan::gdr_segment_back(d.batch * d.heads, d.dv, l.seg);
         l.nseg = ceil_div(ceil_div(d.seqlen, SS_GDR_CHUNK), l.seg);
+        if (l.nseg > 1) {
+            const size_t ends = (size_t)(l.nseg - 1) * d.batch * d.heads;
+            take(l.wE, ends * d.dk * d.dv);
+            take(l.wX, ends * d.dk * d.dv);
+            take(l.wQ, ends * (size_t)ceil_div(d.dv, 64) * 4);
+        }
         take(l.wS, n * d.dk * d.dv);
         take(l.wV, rows * d.dv);
         if (d.heads > d.k_heads) {

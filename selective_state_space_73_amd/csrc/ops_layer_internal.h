@@ -27,13 +27,14 @@ struct LaunchGdr {
     float* ckptX;                // [B, L, H, dv] solutions x_t
     ss_gdr_grads gr;
     // workspace
-    int64_t seg;                 // chunks of a segment of the forward (all of them: one segment)
+    int64_t seg;                 // chunks of a segment (all of them: one segment)
     int nseg;
     float *wE, *wM, *wF;         // several segments: [nseg, B, H, dk, dv] states in front of the segments (the first: the caller's, if
                                  // there is one), [nseg - 1, B, H, dk, dk] what they make of these, [nseg - 1, B, H] whether
                                  // anything of it is left
+                                 // The backward: [nseg - 1, B, H, dk, dv] gradients of the states behind the segments in wE
     float *wX, *wQ;              // and [nseg - 1, B, H, dk, dv] states behind the segments, written where they are not those in front of
-                                 // the next ones, [B, H, tiles of 64 columns, nseg - 1, 4 waves] where that is
+                                 // the next ones (the backward: in front, and behind the one in front of it), [B, H, tiles of 64 columns, nseg - 1, 4 waves] where that is
     float *co, *wT;              // [B, H, chunks]: factors of tokens, inverses in the order of operands
     float *wS, *wV;              // the backward: [B, H, chunks, dk, dv] adjoints behind the chunks, [B, L, H, dv] gradients of v
     float *part_q, *part_k;      // the backward where heads share keys: [B, L, H, dk] each head's share

@@ -155,3 +155,42 @@ def test_nan_stays_however_the_call_is_cut(io):
     bad[3] = bad[70] = True
     for a, b in ((y, S), (ym[:1], Sm[:1])):
         assert (torch.isfinite(a[0, 64:, 0]) == ~bad).all() and (torch.isfinite(b[0, 0]) == ~bad).all()
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("K,V", [(64, 64), (100, 70), (128, 128), (256, 80)])
+def test_segments_keep_what_is_left_of_large_gradients(K, V, io):
+    """A gradient of the final state of 2^60 that comes down to 2^-57, beside a state of that size in front."""
+    x, S0, dy, dS = fading(K, V, io)
+    _, _, ck = T.run(x, S0)
+    got, want = ss.ss_gdr_bwd(*x, ck, dy, dstate_final=dS), O.gdr_bwd(*x, dy, S0, None, dS)
+    for n in ("dg", "dbeta", "dstate_init"):
+        assert want[n].abs().max() > 0
+        T.near(got[n], want[n], 2 * T.rel(K, 512, V), "f32")
+    # and the other way round: a gradient of an output in a late chunk, nothing in front of it
+    dy[:, 400] = 2.0 ** 40
+    x[4][:, 300:] = 0.5
+    x[4][:, 400:] = 0.0
+    _, _, ck = T.run(x, S0)
+    got, want = ss.ss_gdr_bwd(*x, ck, dy, dstate_final=dS), O.gdr_bwd(*x, dy, S0, None, dS)
+    T.near(got["dstate_init"], want["dstate_init"], 2 * T.rel(K, 512, V), "f32")
+    for n in range(6):
+        at = slice(64 * n, 64 * n + 4)
+        T.near(got["dg"][:, at], want["dg"][:, at], 2 * T.rel(K, 512, V), "f32")
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_nan_gradients_stay_however_the_call_is_cut(io):
+    x, S0, dy, dS = fading(64, 96, io)
+    x[4].fill_(0.5)
+    dy.copy_(torch.randn_like(dy))
+    dS[0, 0, 9, 70] = float("inf")
+    dy[0, 500, 0, 3] = float("nan")
+    bad = torch.zeros(96, dtype=torch.bool, device="cuda")
+    bad[3] = bad[70] = True
+    for B in (1, 300):
+        many = tuple(t.expand(B, *t.shape[1:]).contiguous() for t in x)
+        _, _, ck = T.run(many, S0.expand(B, -1, -1, -1))
+        got = ss.ss_gdr_bwd(*many, ck, dy.expand(B, -1, -1, -1).contiguous(), dstate_final=dS.expand(B, -1, -1, -1).contiguous())
+        assert (torch.isfinite(got["dv"][0, :448, 0]) == ~bad).all()
+        assert (torch.isfinite(got["dstate_init"][0, 0]) == ~bad).all()
