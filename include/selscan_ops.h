@@ -201,9 +201,10 @@ ss_status ss_block_q8_step(const ss_block_dims* dims, const ss_block_q8_weights*
  *   y_t = scale S_t^T q^_t
  *
  * A log decay of -200 or less (minus infinity among them) is a decay of 0, as a reset is. A decay
- * of 0 leaves out what it multiplies between chunks of 64 tokens (tokens 0 to 63, 64 to 127, ...) and
- * in a step, so that not even a NaN passes it there. Within a chunk a value that is not finite may reach every
- * token of the chunk, earlier ones as well; everywhere else it propagates to later tokens.
+ * of 0 leaves out what it multiplies, so that not even a NaN passes it. A value that is not finite
+ * reaches what the formulas say and nothing else (its columns then go token by token, which takes as long
+ * as some ten thousand tokens a millisecond); only the gradients of tokens of one chunk of 64 (tokens 0 to 63, 64 to 127,
+ * ...) may all be reached by one.
  * g > 0, beta and the lengths of keys that are used as they are (eps = 0) are the caller's: with
  * 0 <= beta |k^|^2 <= 2 no state grows; nothing is checked.
  *

@@ -371,7 +371,8 @@ struct GdrRows {
 
 // What k_gdr_solve leaves of a chunk's tokens: rows of 64 floats.
 //   a1 e^G / |k|, a2 e^G, a3 beta e^(G_last - G) / |k|, bk beta / |k|, misc { e^G_last, whether no factor is 0,
-//   G_last in powers of two, whether every beta |k|^2 is in [0, 2], whether a decay is 0 },
+//   G_last in powers of two, whether every beta |k|^2 is in [0, 2], whether a decay is 0,
+//   whether a key, a beta or a log decay is not finite },
 //   G itself, times log2 e, in 64 bits (two rows)
 //   for the gradients as well: e^(G_last - G) / |k|, beta, 1 / |k|
 enum GdrTok { tA1, tA2, tA3, tBk, tMisc, tG, kGdrTok = 7, tA3b = 7, tBeta, tRk, kGdrTokAll };
@@ -482,7 +483,8 @@ k_gdr_solve(const LaunchGdr p) {
         const bool clean = __all(a1 != 0.0f && e != 0.0f);
         const float grow = p.eps > 0.0f ? beta : beta * k2;
         const bool tame = __all(grow >= 0.0f && grow <= 2.0f), any_cut = __any(cut);
-        tok[tMisc * 64] = lane == 0 ? __builtin_amdgcn_exp2f((float)Gl) : lane == 2 ? (float)Gl : (lane == 1 ? clean : lane == 3 ? tame : any_cut) ? 1.0f : 0.0f;
+        const bool wrong = !__all(fabsf(k2) < __builtin_inff() && fabsf(beta) < __builtin_inff() && fabsf((float)G) < __builtin_inff());
+        tok[tMisc * 64] = lane == 0 ? __builtin_amdgcn_exp2f((float)Gl) : lane == 2 ? (float)Gl : (lane == 1 ? clean : lane == 3 ? tame : lane == 4 ? any_cut : wrong) ? 1.0f : 0.0f;
         *reinterpret_cast<double*>(p.co + id * (kGdrTokAll * 64) + tG * 64 + 2 * lane) = G;
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -685,7 +687,7 @@ struct GdrWalk : GdrState<DKP> {
     float *tok, *srq;
     int64_t b, bh, nc;
     int h, place;
-    bool from_v = true;
+    bool from_v = true, wrong = false;                // wrong: something that was not finite came by
     const T* vb;
     T* yb;
     T v[16];                                          // the next values as they came, no use of them before they are needed
@@ -859,6 +861,13 @@ struct GdrWalk : GdrState<DKP> {
                 for (int i = 2 * s; i < 4; ++i) X[i] = M::mm(tf[i].t[a], rb.t[c], X[i]);
             });
         }
+        if (OUT) {
+            // zeros above the diagonals do not keep what is not finite from other tokens, in front of it and behind a reset
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum += (X[i][0] + X[i][1]) + (X[i][2] + X[i][3]);
+            wrong |= tok[tMisc * 64 + 5] != 0.0f || !__all(fabsf(sum) < __builtin_inff());
+        }
         __syncthreads();                              // P is there; queries, T and factors are used up
         if (n + 1 < end_n) {
             rest<OUT>(n + 1);
@@ -939,6 +948,57 @@ struct GdrWalk : GdrState<DKP> {
     }
 };
 
+// This wave's columns token after token, from the state at `init` to k.S: where a value is not finite, so that it reaches what
+// the formulas say and nothing else. 2 us a token.
+template <typename T, typename W>
+__device__ __forceinline__ void gdr_tokens(W& k, const float* init) {
+    const LaunchGdr& p = k.p;
+    const int64_t kv = (int64_t)p.dk * p.dv;
+    const int c = k.in ? k.col : p.dv - 1;
+    k.load_state(init, p.dv);
+    auto sum = [](float v) {
+        v += __shfl_xor(v, 16, 64);
+        return v + __shfl_xor(v, 32, 64);
+    };
+#pragma unroll 1
+    for (int64_t t = 0; t < p.L; ++t) {
+        if (p.ckpt && t % kGdrC == 0) k.store_state(p.ckpt + (k.bh * k.nc + t / kGdrC) * kv, p.dv);
+        const int64_t at = (k.b * p.L + t) * p.H + k.h;
+        const float beta = p.beta[at], decay = p.reset && p.reset[k.b * p.L + t] ? 0.0f : expf(p.g[at]);
+        const T *kr = k.rk.base + t * k.rk.stride, *qr = k.rq.base + t * k.rq.stride;
+        gf4 kt[W::ND], qt[W::ND];
+        float k2 = 0.0f, q2 = 0.0f, sk = 0.0f, sq = 0.0f;
+#pragma unroll
+        for (int d = 0; d < W::ND; ++d)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = 32 * (d >> 1) + 8 * k.g + 4 * (d & 1) + r, some = row < p.dk ? row : 0;
+                const float kx = gdr_f<T>(kr[some]), qx = gdr_f<T>(qr[some]);
+                kt[d][r] = row < p.dk ? kx : 0.0f;
+                qt[d][r] = row < p.dk ? qx : 0.0f;
+                k.S[d][r] = decay != 0.0f && row < p.dk ? k.S[d][r] * decay : 0.0f;
+                k2 = __builtin_fmaf(kt[d][r], kt[d][r], k2);
+                q2 = __builtin_fmaf(qt[d][r], qt[d][r], q2);
+                sk = __builtin_fmaf(k.S[d][r], kt[d][r], sk);
+            }
+        const float rk = p.eps > 0.0f ? 1.0f / sqrtf(sum(k2) + p.eps) : 1.0f, rq = p.eps > 0.0f ? 1.0f / sqrtf(sum(q2) + p.eps) : 1.0f;
+        const float x = gdr_f<T>(k.vb[t * p.v.token_stride + c]) - rk * sum(sk), u = beta * x;
+#pragma unroll
+        for (int d = 0; d < W::ND; ++d)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (32 * (d >> 1) + 8 * k.g + 4 * (d & 1) + r < p.dk) {
+                    k.S[d][r] = __builtin_fmaf(kt[d][r] * rk, u, k.S[d][r]);
+                    sq = __builtin_fmaf(k.S[d][r], qt[d][r], sq);
+                }
+        const float y = p.scale * rq * sum(sq);
+        if (k.g == 0 && k.in) {
+            IO<T>::st(k.yb + t * p.H * p.dv + k.col, y);
+            if (p.ckpt) p.ckptX[at * p.dv + k.col] = x;
+        }
+    }
+}
+
 // The chunks [n0, n1) of one head and 64 columns, from the state in k.S on.
 template <bool OUT, typename W, typename T>
 __device__ __forceinline__ void gdr_walk(W& k, int64_t n0, int64_t n1, T* k0, T* k1) {
@@ -983,12 +1043,13 @@ k_gdr_walk(const LaunchGdr p) {
     }
     __syncthreads();
     gdr_walk<true>(k, n0, n1, k0, k1);
+    if (p.nseg == 1 && k.wrong) gdr_tokens<T>(k, from);
     if (p.state && n1 == nc) k.store_state(p.state + bh * kv, p.dv);
-    if (n1 < nc) {
+    if (p.nseg > 1) {
         const int64_t next = (seg + 1) * BH + bh;
-        const bool same = k.agrees(p.wE + next * kv);
+        const bool same = n1 == nc || k.agrees(p.wE + next * kv);
         if (!same) k.store_state(p.wX + (next - BH) * kv, p.dv);
-        if ((threadIdx.x & 63) == 0) p.wQ[((bh * tiles + rest % tiles) * (p.nseg - 1) + seg) * 4 + k.w] = same ? 0.0f : 1.0f;
+        if ((threadIdx.x & 63) == 0) p.wQ[((bh * tiles + rest % tiles) * p.nseg + seg) * 4 + k.w] = (same ? 0 : 1) + (k.wrong ? 2 : 0);
     }
 }
 
@@ -1135,8 +1196,8 @@ k_gdr_join(const LaunchGdr p) {
 }
 
 // Segments that did not start from what the one in front came to, once more from there, one after the other: where a segment's
-// decays leave little of the state in front, but the segment makes less (values that end, states of very different sizes), and
-// where that state is NaN or infinite. Where there is none of them it takes 5 us.
+// decays leave little of the state in front, but the segment makes less (values that end, states of very different sizes). And
+// columns with anything that is not finite, token after token. Where there is none of them it takes 5 us.
 template <typename T, int DKP, bool TWO, bool AL>
 __global__ void __launch_bounds__(256, 1)
 k_gdr_again(const LaunchGdr p) {
@@ -1145,11 +1206,15 @@ k_gdr_again(const LaunchGdr p) {
     __shared__ alignas(16) float tok[kGdrTok * 64], srq[64];
     const int64_t BH = p.B * p.H, bh = blockIdx.x % BH, tile = blockIdx.x / BH, b = bh / p.H, nc = p.nchunks, kv = (int64_t)p.dk * p.dv;
     const int tiles = (p.dv + 63) / 64, h = (int)(bh % p.H), hk = h / (p.H / p.Hk), lane = threadIdx.x & 63;
-    const float* off = p.wQ + (bh * tiles + tile) * (p.nseg - 1) * 4;
-    bool any = false;
-    for (int i = lane; i < (p.nseg - 1) * 4; i += 64) any |= off[i] != 0.0f;
+    const uint32_t* off = p.wQ + (bh * tiles + tile) * p.nseg * 4;
+    bool any = false, wrong = false;
+    for (int i = lane; i < p.nseg * 4; i += 64) {
+        any |= off[i] != 0;
+        wrong |= i % 4 == gdr_wave() && off[i] >= 2;
+    }
     if (!__any(any)) return;
     W k(p, tq, tt, tp, tok, srq, b, bh, h, hk, (int)tile * 64 + gdr_wave() * 16 + (lane & 15));
+    k.wrong = __any(wrong);
     if (p.dk < DKP) {
         gdr_clear<64 * DKP>(k0);
         gdr_clear<64 * DKP>(tq);
@@ -1158,8 +1223,7 @@ k_gdr_again(const LaunchGdr p) {
     bool here = false;                                // the state in front of the segment is in registers
     for (int seg = 1; seg < p.nseg; ++seg) {
         const float* from = p.wE + (seg * BH + bh) * kv;
-        const float* o = off + (seg - 1) * 4;
-        const bool own = here ? !k.agrees(from) : o[k.w] != 0.0f;
+        const bool own = !k.wrong && (here ? !k.agrees(from) : off[(seg - 1) * 4 + k.w] != 0);
         // (a barrier, too: the last segment's LDS is used up, the zeros are there)
         if (!__syncthreads_or(own)) {
             here = false;
@@ -1170,6 +1234,10 @@ k_gdr_again(const LaunchGdr p) {
         gdr_walk<true>(k, n0, n1, k0, k1);
         here = true;
         if (p.state && n1 == nc) k.store_state(p.state + bh * kv, p.dv);
+    }
+    if (k.wrong) {
+        gdr_tokens<T>(k, p.state ? p.wE + bh * kv : nullptr);
+        if (p.state) k.store_state(p.state + bh * kv, p.dv);
     }
 }
 
@@ -1489,7 +1557,7 @@ k_gdr_walk_back(const LaunchGdr p) {
         const int64_t in_front = (seg - 1) * BH + bh;
         const bool same = k.agrees(p.wE + in_front * kv);
         if (!same) k.store_state(p.wX + in_front * kv, p.dv);
-        if ((threadIdx.x & 63) == 0) p.wQ[((bh * tiles + rest % tiles) * (p.nseg - 1) + seg - 1) * 4 + k.w] = same ? 0.0f : 1.0f;
+        if ((threadIdx.x & 63) == 0) p.wQ[((bh * tiles + rest % tiles) * p.nseg + seg) * 4 + k.w] = same ? 0 : 1;
     }
 }
 
@@ -1502,16 +1570,16 @@ k_gdr_again_back(const LaunchGdr p) {
     __shared__ alignas(16) float tok[kGdrTok * 64], srq[64];
     const int64_t BH = p.B * p.H, bh = blockIdx.x % BH, tile = blockIdx.x / BH, b = bh / p.H, kv = (int64_t)p.dk * p.dv;
     const int tiles = (p.dv + 63) / 64, h = (int)(bh % p.H), hk = h / (p.H / p.Hk), lane = threadIdx.x & 63;
-    const float* off = p.wQ + (bh * tiles + tile) * (p.nseg - 1) * 4;
+    const uint32_t* off = p.wQ + (bh * tiles + tile) * p.nseg * 4 + 4;
     bool any = false;
-    for (int i = lane; i < (p.nseg - 1) * 4; i += 64) any |= off[i] != 0.0f;
+    for (int i = lane; i < (p.nseg - 1) * 4; i += 64) any |= off[i] != 0;
     if (!__any(any)) return;
     W k(p, tk, tq, tt, tp, tok, srq, b, bh, h, hk, (int)tile * 64 + gdr_wave() * 16 + (lane & 15));
     gdr_clear_back<T, DKP>(p, tk, tq, tp);
     bool here = false;                                // the gradient behind the segment is in registers
     for (int seg = p.nseg - 2; seg >= 0; --seg) {
         const int64_t at = (seg * BH + bh) * kv;
-        const bool own = here ? !k.agrees(p.wE + at) : off[seg * 4 + k.w] != 0.0f;
+        const bool own = here ? !k.agrees(p.wE + at) : off[seg * 4 + k.w] != 0;
         if (!__syncthreads_or(own)) {                 // (a barrier, too: the last segment's LDS is used up)
             here = false;
             continue;

@@ -96,7 +96,7 @@ GdrLayout gdr_layout(const ss_gdr_dims& d, bool backward) {
             take(l.wM, ends * d.dk * d.dk);
             take(l.wF, ends);
             take(l.wX, ends * d.dk * d.dv);
-            take(l.wQ, ends * (size_t)ceil_div(d.dv, 64) * 4);
+            take(l.wQ, (size_t)l.nseg * d.batch * d.heads * (size_t)ceil_div(d.dv, 64) * 4);
         }
     }
     if (backward) {
@@ -106,7 +106,7 @@ GdrLayout gdr_layout(const ss_gdr_dims& d, bool backward) {
             const size_t ends = (size_t)(l.nseg - 1) * d.batch * d.heads;
             take(l.wE, ends * d.dk * d.dv);
             take(l.wX, ends * d.dk * d.dv);
-            take(l.wQ, ends * (size_t)ceil_div(d.dv, 64) * 4);
+            take(l.wQ, (size_t)l.nseg * d.batch * d.heads * (size_t)ceil_div(d.dv, 64) * 4);
         }
         take(l.wS, n * d.dk * d.dv);
         take(l.wV, rows * d.dv);
@@ -192,7 +192,8 @@ void gdr_attach(selscan::LaunchGdr& p, const ss_gdr_dims& d, const GdrLayout& l,
     p.co = at(l.co); p.wT = at(l.wT);
     p.seg = l.seg;
     p.nseg = (int)l.nseg;
-    p.wE = at(l.wE); p.wM = at(l.wM); p.wF = at(l.wF); p.wX = at(l.wX); p.wQ = at(l.wQ);
+    p.wE = at(l.wE); p.wM = at(l.wM); p.wF = at(l.wF); p.wX = at(l.wX);
+    p.wQ = reinterpret_cast<uint32_t*>(ws + l.wQ);
     if (backward) {
         p.wS = at(l.wS); p.wV = at(l.wV);
         if (d.heads > d.k_heads) { p.part_q = at(l.pq); p.part_k = at(l.pk); }

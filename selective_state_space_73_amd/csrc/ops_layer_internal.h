@@ -33,8 +33,9 @@ struct LaunchGdr {
                                  // there is one), [nseg - 1, B, H, dk, dk] what they make of these, [nseg - 1, B, H] whether
                                  // anything of it is left
                                  // The backward: [nseg - 1, B, H, dk, dv] gradients of the states behind the segments in wE
-    float *wX, *wQ;              // and [nseg - 1, B, H, dk, dv] states behind the segments, written where they are not those in front of
-                                 // the next ones (the backward: in front, and behind the one in front of it), [B, H, tiles of 64 columns, nseg - 1, 4 waves] where that is
+    float* wX;                   // [nseg - 1, B, H, dk, dv] states behind the segments, written where they are not those in front of
+                                 // the next ones (the backward: in front of a segment, and behind the one in front of it)
+    uint32_t* wQ;                // [B, H, tiles of 64 columns, nseg, 4 waves] 1 where that is, 2 more where anything is not finite
     float *co, *wT;              // [B, H, chunks]: factors of tokens, inverses in the order of operands
     float *wS, *wV;              // the backward: [B, H, chunks, dk, dv] adjoints behind the chunks, [B, L, H, dv] gradients of v
     float *part_q, *part_k;      // the backward where heads share keys: [B, L, H, dk] each head's share

@@ -194,3 +194,71 @@ def test_nan_gradients_stay_however_the_call_is_cut(io):
         got = ss.ss_gdr_bwd(*many, ck, dy.expand(B, -1, -1, -1).contiguous(), dstate_final=dS.expand(B, -1, -1, -1).contiguous())
         assert (torch.isfinite(got["dv"][0, :448, 0]) == ~bad).all()
         assert (torch.isfinite(got["dstate_init"][0, 0]) == ~bad).all()
+
+
+def same_finite(got, want, tol, io):
+    """Finite in the same places, and there within the tolerance of the largest finite value."""
+    got, want = got.double().cpu(), want.double()
+    ok = torch.isfinite(want)
+    assert (torch.isfinite(got) == ok).all()
+    T.near(torch.where(ok, got, 0.0), torch.where(ok, want, 0.0), tol, io)
+
+
+PLACES = ["v", "inf v", "k", "inf k", "beta", "g", "q", "state", "k in front of a reset", "beta in front of a reset"]
+
+
+def not_finite(place, x, S0, n):
+    """One value of the document [n, n + 50) of x, or of the state."""
+    q, k, v, g, beta = x
+    if place in ("v", "inf v"):
+        v[0, n + 20, 0, 3] = float("nan") if place == "v" else float("-inf")
+    elif place in ("k", "inf k"):
+        k[0, n + 20, 0, 1] = float("nan") if place == "k" else float("inf")
+    elif place == "k in front of a reset":
+        k[0, n + 49, 0, 1] = float("nan")
+    elif place == "beta in front of a reset":
+        beta[0, n + 49, 0] = float("nan")
+    elif place == "beta":
+        beta[0, n + 20, 0] = float("inf")
+    elif place == "g":
+        g[0, n + 20, 0] = float("nan")
+    elif place == "q":
+        q[0, n + 20, 0, 1] = float("nan")
+    else:
+        S0[0, 0, 5, 2] = float("nan")
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("place", PLACES)
+@pytest.mark.parametrize("shape,at", [((1, 200, 1, 2, 64, 48), 70), ((1, 200, 2, 2, 100, 33), 0), ((1, 64 * 9, 1, 1, 64, 80), 330),
+                                      ((2, 64 * 9, 1, 2, 128, 128), 64 * 8 + 1)])
+def test_what_is_not_finite_keeps_to_its_document(shape, at, place, io):
+    """Documents of 50 tokens, their first ones anywhere in a chunk, one of them with a value that is not finite: it
+    reaches what the formulas say, no token in front of it and none behind the next reset, in one segment and in several."""
+    x, S0, _, _, _ = T.make(*shape, io, seed=53)
+    z = torch.zeros(shape[0], shape[1], dtype=torch.uint8, device="cuda")
+    z[:, at % 50::50] = 1
+    if place == "state":
+        z[:, :20] = 0
+    not_finite(place, x, S0, at)
+    y, S, ck = T.run(x, S0, reset=z)
+    yw, Sw = O.gdr_fwd(*x, S0, z)
+    same_finite(y, yw, T.rel(shape[4], 50), io)
+    same_finite(S, Sw, T.rel(shape[4], 50), "f32")
+    # the states in front of the chunks
+    n = -(-shape[1] // 64)
+    states = ck[:shape[0] * shape[3] * n * shape[4] * shape[5]].view(shape[0], shape[3], n, shape[4], shape[5])
+    for c in (1, n - 1):
+        same_finite(states[:, :, c], O.gdr_fwd(*(t[:, :64 * c] for t in x), S0, z[:, :64 * c])[1], T.rel(shape[4], 50), "f32")
+
+
+def test_a_state_that_is_reset_may_hold_anything():
+    """Nothing of it is looked at, so that starting over costs nothing."""
+    x, S0, _, _, _ = T.make(1, 64 * 9, 1, 2, 64, 64, "bf16", seed=59)
+    z = torch.zeros(1, 64 * 9, dtype=torch.uint8, device="cuda")
+    z[0, 0] = 1
+    S0.fill_(float("nan"))
+    y, S, _ = T.run(x, S0, reset=z)
+    yw, Sw = O.gdr_fwd(*x)
+    T.near(y, yw, T.rel(64, 512), "bf16")
+    T.near(S, Sw, T.rel(64, 512), "f32")
