@@ -202,9 +202,8 @@ ss_status ss_block_q8_step(const ss_block_dims* dims, const ss_block_q8_weights*
  *
  * A log decay of -200 or less (minus infinity among them) is a decay of 0, as a reset is. A decay
  * of 0 leaves out what it multiplies, so that not even a NaN passes it. A value that is not finite
- * reaches what the formulas say and nothing else (its columns then go token by token, which takes as long
- * as some ten thousand tokens a millisecond); only the gradients of tokens of one chunk of 64 (tokens 0 to 63, 64 to 127,
- * ...) may all be reached by one.
+ * reaches what the formulas say and nothing else, tokens in front of it and documents
+ * behind the next reset neither; what it may reach is then made token by token, some microseconds each.
  * g > 0, beta and the lengths of keys that are used as they are (eps = 0) are the caller's: with
  * 0 <= beta |k^|^2 <= 2 no state grows; nothing is checked.
  *

@@ -949,7 +949,7 @@ struct GdrWalk : GdrState<DKP> {
 };
 
 // This wave's columns token after token, from the state at `init` to k.S: where a value is not finite, so that it reaches what
-// the formulas say and nothing else. 2 us a token.
+// the formulas say and nothing else. 128 x 128: 2.5 to 3.5 us a token.
 template <typename T, typename W>
 __device__ __forceinline__ void gdr_tokens(W& k, const float* init) {
     const LaunchGdr& p = k.p;
@@ -1263,6 +1263,7 @@ struct GdrWalkBack : GdrState<DKP> {
     float *tok, *srq;
     int64_t b, bh, nc;
     int h, place;
+    bool wrong = false;                               // something that was not finite came by
     T v[16];                                          // the next gradients of y, as they came
 
     __device__ __forceinline__ GdrWalkBack(const LaunchGdr& a, T* k_, T* q_, T* t_, T* p_, float* tok_, float* srq_, int64_t b_, int64_t bh_,
@@ -1417,6 +1418,15 @@ struct GdrWalkBack : GdrState<DKP> {
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) a2[i] *= *reinterpret_cast<const gf4*>(&srq[16 * i + 4 * g]);
+        if (OUT) {
+            // as in the forward; and the state's gradient, which a beta of 0 would hide
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum += (dV[i][0] + dV[i][1]) + (dV[i][2] + dV[i][3]);
+#pragma unroll
+            for (int d = 0; d < ND; ++d) sum += (S[d][0] + S[d][1]) + (S[d][2] + S[d][3]);
+            wrong |= tok[tMisc * 64 + 5] != 0.0f || !__all(fabsf(sum) < __builtin_inff());
+        }
         __syncthreads();                              // T, P and factors are used up
         if (n > first) {
             factors(n - 1);
@@ -1516,6 +1526,61 @@ __device__ __forceinline__ void gdr_clear_back(const LaunchGdr& p, T* tk, T* tq,
     __syncthreads();
 }
 
+// As gdr_tokens, from the last token to the first.
+template <typename T, typename W>
+__device__ __forceinline__ void gdr_tokens_back(W& k) {
+    const LaunchGdr& p = k.p;
+    const int64_t kv = (int64_t)p.dk * p.dv;
+    const int c = k.in ? k.col : p.dv - 1;
+    k.load_state(p.gr.dstate_final ? p.gr.dstate_final + k.bh * kv : nullptr, p.dv);
+    auto sum = [](float v) {
+        v += __shfl_xor(v, 16, 64);
+        return v + __shfl_xor(v, 32, 64);
+    };
+#pragma unroll 1
+    for (int64_t t = p.L - 1; t >= 0; --t) {
+        if (t == p.L - 1 || t % kGdrC == kGdrC - 1) k.store_state(p.wS + (k.bh * k.nc + t / kGdrC) * kv, p.dv);
+        const int64_t at = (k.b * p.L + t) * p.H + k.h;
+        const float beta = p.beta[at], decay = p.reset && p.reset[k.b * p.L + t] ? 0.0f : expf(p.g[at]);
+        const T *kr = k.rk.base + t * k.rk.stride, *qr = k.rq.base + t * k.rq.stride;
+        gf4 kt[W::ND], qt[W::ND];
+        float k2 = 0.0f, q2 = 0.0f, wk = 0.0f;
+#pragma unroll
+        for (int d = 0; d < W::ND; ++d)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = 32 * (d >> 1) + 8 * k.g + 4 * (d & 1) + r, some = row < p.dk ? row : 0;
+                const float kx = gdr_f<T>(kr[some]), qx = gdr_f<T>(qr[some]);
+                kt[d][r] = row < p.dk ? kx : 0.0f;
+                qt[d][r] = row < p.dk ? qx : 0.0f;
+                k2 = __builtin_fmaf(kt[d][r], kt[d][r], k2);
+                q2 = __builtin_fmaf(qt[d][r], qt[d][r], q2);
+            }
+        const float rk = p.eps > 0.0f ? 1.0f / sqrtf(sum(k2) + p.eps) : 1.0f, rq = p.scale * (p.eps > 0.0f ? 1.0f / sqrtf(sum(q2) + p.eps) : 1.0f);
+        const float dy = gdr_f<T>(static_cast<const T*>(p.gr.dy)[at * p.dv + c]);
+#pragma unroll
+        for (int d = 0; d < W::ND; ++d)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (32 * (d >> 1) + 8 * k.g + 4 * (d & 1) + r < p.dk) {
+                    k.S[d][r] = __builtin_fmaf(qt[d][r] * rq, dy, k.S[d][r]);
+                    wk = __builtin_fmaf(k.S[d][r], kt[d][r], wk);
+                }
+        const float dv = beta * rk * sum(wk);
+#pragma unroll
+        for (int d = 0; d < W::ND; ++d)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const bool row = 32 * (d >> 1) + 8 * k.g + 4 * (d & 1) + r < p.dk;
+                k.S[d][r] = decay != 0.0f && row ? __builtin_fmaf(kt[d][r] * -rk, dv, k.S[d][r]) * decay : 0.0f;
+            }
+        if (k.g == 0 && k.in) {
+            IO<T>::st(static_cast<T*>(p.gr.dv) + at * p.dv + k.col, dv);
+            p.wV[at * p.dv + k.col] = dv;
+        }
+    }
+}
+
 // Several segments: the gradient of the state behind each but the last.
 template <typename T, int DKP, bool AL, int GROUPS>
 __global__ void __launch_bounds__(256, GROUPS)
@@ -1551,13 +1616,13 @@ k_gdr_walk_back(const LaunchGdr p) {
     k.load_state(seg < p.nseg - 1 ? p.wE + (seg * BH + bh) * kv : p.gr.dstate_final ? p.gr.dstate_final + bh * kv : nullptr, p.dv);
     gdr_clear_back<T, DKP>(p, tk, tq, tp);
     gdr_walk_back<true>(k, n0, n1);
-    if (seg == 0) {
-        if (p.gr.dstate_init) k.store_state(p.gr.dstate_init + bh * kv, p.dv);
-    } else {
+    if (p.nseg == 1 && k.wrong) gdr_tokens_back<T>(k);
+    if (seg == 0 && p.gr.dstate_init) k.store_state(p.gr.dstate_init + bh * kv, p.dv);
+    if (p.nseg > 1) {
         const int64_t in_front = (seg - 1) * BH + bh;
-        const bool same = k.agrees(p.wE + in_front * kv);
+        const bool same = seg == 0 || k.agrees(p.wE + in_front * kv);
         if (!same) k.store_state(p.wX + in_front * kv, p.dv);
-        if ((threadIdx.x & 63) == 0) p.wQ[((bh * tiles + rest % tiles) * p.nseg + seg) * 4 + k.w] = same ? 0 : 1;
+        if ((threadIdx.x & 63) == 0) p.wQ[((bh * tiles + rest % tiles) * p.nseg + seg) * 4 + k.w] = (same ? 0 : 1) + (k.wrong ? 2 : 0);
     }
 }
 
@@ -1570,16 +1635,20 @@ k_gdr_again_back(const LaunchGdr p) {
     __shared__ alignas(16) float tok[kGdrTok * 64], srq[64];
     const int64_t BH = p.B * p.H, bh = blockIdx.x % BH, tile = blockIdx.x / BH, b = bh / p.H, kv = (int64_t)p.dk * p.dv;
     const int tiles = (p.dv + 63) / 64, h = (int)(bh % p.H), hk = h / (p.H / p.Hk), lane = threadIdx.x & 63;
-    const uint32_t* off = p.wQ + (bh * tiles + tile) * p.nseg * 4 + 4;
-    bool any = false;
-    for (int i = lane; i < (p.nseg - 1) * 4; i += 64) any |= off[i] != 0;
+    const uint32_t* off = p.wQ + (bh * tiles + tile) * p.nseg * 4;
+    bool any = false, wrong = false;
+    for (int i = lane; i < p.nseg * 4; i += 64) {
+        any |= off[i] != 0;
+        wrong |= i % 4 == gdr_wave() && off[i] >= 2;
+    }
     if (!__any(any)) return;
     W k(p, tk, tq, tt, tp, tok, srq, b, bh, h, hk, (int)tile * 64 + gdr_wave() * 16 + (lane & 15));
+    k.wrong = __any(wrong);
     gdr_clear_back<T, DKP>(p, tk, tq, tp);
     bool here = false;                                // the gradient behind the segment is in registers
     for (int seg = p.nseg - 2; seg >= 0; --seg) {
         const int64_t at = (seg * BH + bh) * kv;
-        const bool own = here ? !k.agrees(p.wE + at) : off[seg * 4 + k.w] != 0;
+        const bool own = !k.wrong && (here ? !k.agrees(p.wE + at) : off[(seg + 1) * 4 + k.w] != 0);
         if (!__syncthreads_or(own)) {                 // (a barrier, too: the last segment's LDS is used up)
             here = false;
             continue;
@@ -1588,6 +1657,10 @@ k_gdr_again_back(const LaunchGdr p) {
         gdr_walk_back<true>(k, seg * p.seg, (seg + 1) * p.seg);
         here = true;
         if (seg == 0 && p.gr.dstate_init) k.store_state(p.gr.dstate_init + bh * kv, p.dv);
+    }
+    if (k.wrong) {
+        gdr_tokens_back<T>(k);
+        if (p.gr.dstate_init) k.store_state(p.gr.dstate_init + bh * kv, p.dv);
     }
 }
 
@@ -1977,6 +2050,16 @@ k_gdr_grads(const LaunchGdr p) {
             p.gr.dg[at] = p.reset && p.reset[b * p.L + t0 + t] ? 0.0f : mine;
             p.gr.dbeta[at] = db;
         }
+        // zeros of pairs do not keep what is not finite from other tokens
+        float of_all = mine + db;
+#pragma unroll
+        for (int u = 0; u < NS; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) of_all += aq[u][i][r] + av[u][i][r];
+        const bool wrong = tok[tMisc * 64 + 5] != 0.0f || !__all(fabsf(of_all) < __builtin_inff());
+        if (lane == 0) p.wG[id * 4 + w] = wrong;
     }
     if (p.part_q) {
         // heads that share keys: each head's share
@@ -2068,6 +2151,158 @@ k_gdr_grads(const LaunchGdr p) {
                         dqt.st(oq[r], at + r * (unsigned)sizeof(T), 0);
                         dkt.st(ok[r], at + r * (unsigned)sizeof(T), 0);
                     }
+            }
+        }
+    }
+}
+
+// The gradients of chunks with anything that is not finite, token by token: the state in front of a token from the chunk's
+// first one on, the gradient behind it from the last one back, so that it reaches what the formulas say and nothing else. A lane
+// has a row of 16 columns of both, a workgroup eight of a chunk's tokens (blockIdx.y) and some chunks one after the other: 16, or
+// 64 where there are thousands and looking at them takes longest. 5 to 10 us where every chunk is finite; where none is,
+// 10240 chunks of 128 x 128 take 130 ms.
+template <typename T>
+__global__ void __launch_bounds__(256)
+k_gdr_grads_again(const LaunchGdr p, int per) {
+    constexpr int CW = 16, TW = kGdrC / 8;
+    __shared__ float lx[kGdrC][CW], lv[kGdrC][CW], lo[kGdrC][CW], decay[kGdrC], beta[kGdrC], rk[kGdrC], rq[kGdrC], sums[4][4];
+    const int tid = threadIdx.x, lane = tid & 63, w = gdr_wave();
+    const int64_t chunks = p.B * p.H * p.nchunks, kv = (int64_t)p.dk * p.dv;
+    for (int64_t first = (int64_t)blockIdx.x * per; first < chunks; first += (int64_t)gridDim.x * per) {
+        bool off = false;
+        if (lane < per && first + lane < chunks) {
+            const gu4 u = *reinterpret_cast<const gu4*>(p.wG + (first + lane) * 4);
+            off = (u[0] | u[1] | u[2] | u[3]) != 0;
+        }
+        uint64_t todo = __ballot(off);                // the same in all waves
+        for (; todo; todo &= todo - 1) {
+            const int64_t id = first + __builtin_ctzll(todo), n = id % p.nchunks, bh = id / p.nchunks, b = bh / p.H, t0 = n * kGdrC;
+            const int h = (int)(bh % p.H), hk = h / (p.H / p.Hk), left = p.L - t0 < kGdrC ? (int)(p.L - t0) : kGdrC, d = tid;
+            const int64_t row0 = (b * p.L + t0) * p.H + h;
+            const bool row = d < p.dk;
+            const T* kr = static_cast<const T*>(p.k.p) + b * p.k.batch_stride + hk * p.k.head_stride + t0 * p.k.token_stride;
+            const T* qr = static_cast<const T*>(p.q.p) + b * p.q.batch_stride + hk * p.q.head_stride + t0 * p.q.token_stride;
+            __syncthreads();                          // the last chunk's values are used up
+            for (int t = w; t < left; t += 4) {
+                float k2 = 0.0f, q2 = 0.0f;
+                for (int e = lane; e < p.dk; e += 64) {
+                    const float kx = gdr_f<T>(kr[t * p.k.token_stride + e]), qx = gdr_f<T>(qr[t * p.q.token_stride + e]);
+                    k2 = __builtin_fmaf(kx, kx, k2);
+                    q2 = __builtin_fmaf(qx, qx, q2);
+                }
+#pragma unroll
+                for (int o = 1; o < 64; o <<= 1) {
+                    k2 += __shfl_xor(k2, o, 64);
+                    q2 += __shfl_xor(q2, o, 64);
+                }
+                if (lane == 0) {
+                    const int64_t at = row0 + (int64_t)t * p.H;
+                    rk[t] = p.eps > 0.0f ? 1.0f / sqrtf(k2 + p.eps) : 1.0f;
+                    rq[t] = p.eps > 0.0f ? 1.0f / sqrtf(q2 + p.eps) : 1.0f;
+                    decay[t] = p.reset && p.reset[b * p.L + t0 + t] ? 0.0f : expf(p.g[at]);
+                    beta[t] = p.beta[at];
+                }
+            }
+            float gq[TW] = {}, gk[TW] = {}, gb[TW] = {}, gg[TW] = {};
+            for (int c0 = 0; c0 < p.dv; c0 += CW) {
+                const int cols = p.dv - c0 < CW ? p.dv - c0 : CW;
+                __syncthreads();
+                for (int e = tid; e < kGdrC * CW; e += 256) {
+                    const int t = e / CW, c = e % CW;
+                    const bool there = t < left && c < cols;
+                    const int64_t at = (row0 + (int64_t)(there ? t : 0) * p.H) * p.dv + c0 + (there ? c : 0);
+                    lx[t][c] = there ? p.ckptX[at] : 0.0f;
+                    lv[t][c] = there ? p.wV[at] : 0.0f;
+                    lo[t][c] = there ? gdr_f<T>(static_cast<const T*>(p.gr.dy)[at]) : 0.0f;
+                }
+                __syncthreads();
+                if (!row) continue;                   // (every lane meets every barrier)
+                float S0[CW], W0[CW];
+#pragma unroll
+                for (int c = 0; c < CW; ++c) {
+                    S0[c] = c < cols ? p.ckpt[id * kv + (int64_t)d * p.dv + c0 + c] : 0.0f;
+                    W0[c] = c < cols ? p.wS[id * kv + (int64_t)d * p.dv + c0 + c] : 0.0f;
+                }
+                // to the first of the eight tokens, and the states in front of them; then back to the last
+                const int t1 = blockIdx.y * TW;
+                float S[TW][CW];                      // decayed
+#pragma unroll 4
+                for (int t = 0; t < t1 && t < left; ++t) {
+                    const float a = decay[t], kt = gdr_f<T>(kr[t * p.k.token_stride + d]) * rk[t], be = beta[t];
+#pragma unroll
+                    for (int c = 0; c < CW; ++c) S0[c] = __builtin_fmaf(kt, be * lx[t][c], a != 0.0f ? a * S0[c] : 0.0f);
+                }
+#pragma unroll
+                for (int e = 0; e < TW; ++e) {
+                    const int t = t1 + e;
+                    if (t >= left) break;
+                    const float a = decay[t], kt = gdr_f<T>(kr[t * p.k.token_stride + d]) * rk[t], be = beta[t];
+#pragma unroll
+                    for (int c = 0; c < CW; ++c) {
+                        S[e][c] = a != 0.0f ? a * S0[c] : 0.0f;
+                        S0[c] = __builtin_fmaf(kt, be * lx[t][c], S[e][c]);
+                    }
+                }
+#pragma unroll 4
+                for (int t = left - 1; t >= t1 + TW; --t) {
+                    const float a = decay[t], kt = gdr_f<T>(kr[t * p.k.token_stride + d]) * -rk[t];
+                    const float qt = gdr_f<T>(qr[t * p.q.token_stride + d]) * (rq[t] * p.scale);
+#pragma unroll
+                    for (int c = 0; c < CW; ++c)
+                        W0[c] = a != 0.0f ? a * __builtin_fmaf(kt, lv[t][c], __builtin_fmaf(qt, lo[t][c], W0[c])) : 0.0f;
+                }
+#pragma unroll
+                for (int e = TW - 1; e >= 0; --e) {
+                    const int t = t1 + e;
+                    if (t >= left) continue;
+                    const float a = decay[t], kt = gdr_f<T>(kr[t * p.k.token_stride + d]) * rk[t], be = beta[t];
+                    const float qt = gdr_f<T>(qr[t * p.q.token_stride + d]) * (rq[t] * p.scale);
+#pragma unroll
+                    for (int c = 0; c < CW; ++c)
+                        if (c < cols) {               // (a NaN times the zeros past dv would count)
+                            const float s = S[e][c], u = be * lx[t][c], wt = __builtin_fmaf(qt, lo[t][c], W0[c]), dw = __builtin_fmaf(-kt, lv[t][c], wt);
+                            gq[e] = __builtin_fmaf(__builtin_fmaf(kt, u, s), lo[t][c], gq[e]);
+                            gk[e] = __builtin_fmaf(wt, u, gk[e]);
+                            gk[e] = __builtin_fmaf(-s, lv[t][c], gk[e]);
+                            gb[e] = __builtin_fmaf(kt * wt, lx[t][c], gb[e]);
+                            gg[e] = __builtin_fmaf(s, dw, gg[e]);
+                            W0[c] = a != 0.0f ? a * dw : 0.0f;
+                        }
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < TW; ++e) {
+                const int t = blockIdx.y * TW + e;
+                if (t >= left) break;
+                const int64_t at = row0 + (int64_t)t * p.H;
+                const float kx = row ? gdr_f<T>(kr[t * p.k.token_stride + d]) : 0.0f, qx = row ? gdr_f<T>(qr[t * p.q.token_stride + d]) : 0.0f;
+                const float oq = gq[e] * (p.scale * rq[t]), ok = gk[e] * rk[t];
+                float v[4] = {gb[e], gg[e], row ? qx * oq : 0.0f, row ? kx * ok : 0.0f};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+#pragma unroll
+                    for (int o = 1; o < 64; o <<= 1) v[k] += __shfl_xor(v[k], o, 64);
+                }
+                __syncthreads();
+                if (lane == 0)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) sums[k][w] = v[k];
+                __syncthreads();
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[k] = sums[k][0] + sums[k][1] + sums[k][2] + sums[k][3];
+                if (tid == 0) {
+                    p.gr.dbeta[at] = v[0];
+                    p.gr.dg[at] = p.reset && p.reset[b * p.L + t0 + t] ? 0.0f : v[1];
+                }
+                if (!row) continue;
+                if (p.part_q) {
+                    p.part_q[at * p.dk + d] = oq;
+                    p.part_k[at * p.dk + d] = ok;
+                } else {
+                    const int64_t to = ((b * p.L + t0 + t) * p.Hk + hk) * p.dk + d;
+                    IO<T>::st(static_cast<T*>(p.gr.dq) + to, p.eps > 0.0f ? oq - qx * (v[2] * rq[t] * rq[t]) : oq);
+                    IO<T>::st(static_cast<T*>(p.gr.dk) + to, p.eps > 0.0f ? ok - kx * (v[3] * rk[t] * rk[t]) : ok);
+                }
             }
         }
     }
@@ -2246,6 +2481,9 @@ hipError_t launch_gdr_d(const LaunchGdr& p) {
         if (p.nseg > 1) hipLaunchKernelGGL((k_gdr_again_back<T, DKP, false>), dim3(tiles), dim3(256), 0, st, p);
         hipLaunchKernelGGL((k_gdr_grads<T, DKP, false, false, kGrads>), dim3(chunks), dim3(256), 0, st, p);
     }
+    const int per = chunks < 2048 ? 16 : 64;
+    const unsigned look = (chunks + per - 1) / per;
+    hipLaunchKernelGGL((k_gdr_grads_again<T>), dim3(look < 512 ? look : 512, 8), dim3(256), 0, st, p, per);
     if (p.part_q) {
         const int64_t rows = (p.B * p.L * p.Hk + 3) / 4;
         hipLaunchKernelGGL((k_gdr_keys<T>), dim3((unsigned)(rows < 1 << 20 ? rows : 1 << 20), 2), dim3(256), 0, st, p);

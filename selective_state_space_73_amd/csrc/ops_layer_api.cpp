@@ -74,7 +74,7 @@ size_t ckpt_floats(const ss_gdr_dims& d) { return ckpt_states(d) + (size_t)d.bat
 // Per chunk and head: the tokens' factors and the inverse (6 blocks of 16 x 32, three bf16 terms or fp32). The forward in
 // segments: the states in front of them, what they make of these, and the states behind them. The backward: these of
 // gradients, the state's gradient behind every chunk, the gradients of v in fp32, and those of q and k by head of v where heads share them.
-struct GdrLayout { size_t co, wT, wS, wV, pq, pk, wE, wM, wF, wX, wQ, total; int64_t seg, nseg; };
+struct GdrLayout { size_t co, wT, wS, wV, pq, pk, wE, wM, wF, wX, wQ, wG, total; int64_t seg, nseg; };
 GdrLayout gdr_layout(const ss_gdr_dims& d, bool backward) {
     GdrLayout l{};
     if (d.seqlen == 0) return l;
@@ -110,6 +110,7 @@ GdrLayout gdr_layout(const ss_gdr_dims& d, bool backward) {
         }
         take(l.wS, n * d.dk * d.dv);
         take(l.wV, rows * d.dv);
+        take(l.wG, n * 4);
         if (d.heads > d.k_heads) {
             take(l.pq, rows * d.dk);
             take(l.pk, rows * d.dk);
@@ -196,6 +197,7 @@ void gdr_attach(selscan::LaunchGdr& p, const ss_gdr_dims& d, const GdrLayout& l,
     p.wQ = reinterpret_cast<uint32_t*>(ws + l.wQ);
     if (backward) {
         p.wS = at(l.wS); p.wV = at(l.wV);
+        p.wG = reinterpret_cast<uint32_t*>(ws + l.wG);
         if (d.heads > d.k_heads) { p.part_q = at(l.pq); p.part_k = at(l.pk); }
     }
 }

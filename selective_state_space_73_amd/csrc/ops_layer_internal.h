@@ -38,6 +38,7 @@ struct LaunchGdr {
     uint32_t* wQ;                // [B, H, tiles of 64 columns, nseg, 4 waves] 1 where that is, 2 more where anything is not finite
     float *co, *wT;              // [B, H, chunks]: factors of tokens, inverses in the order of operands
     float *wS, *wV;              // the backward: [B, H, chunks, dk, dv] adjoints behind the chunks, [B, L, H, dv] gradients of v
+    uint32_t* wG;                // the backward: [B, H, chunks, 4 waves] whether a chunk's gradients hold anything that is not finite
     float *part_q, *part_k;      // the backward where heads share keys: [B, L, H, dk] each head's share
     void* stream;
 };

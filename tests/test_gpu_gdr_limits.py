@@ -262,3 +262,32 @@ def test_a_state_that_is_reset_may_hold_anything():
     yw, Sw = O.gdr_fwd(*x)
     T.near(y, yw, T.rel(64, 512), "bf16")
     T.near(S, Sw, T.rel(64, 512), "f32")
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("place", PLACES + ["dy", "inf dy", "dstate"])
+@pytest.mark.parametrize("shape,at,unit", [((1, 200, 1, 2, 64, 48), 70, True), ((1, 200, 2, 2, 100, 33), 0, False),
+                                           ((1, 64 * 9, 1, 1, 64, 80), 330, True), ((2, 64 * 9, 1, 2, 128, 128), 64 * 8 + 1, True),
+                                           ((1, 100, 1, 1, 200, 20), 31, True)])
+def test_gradients_of_what_is_not_finite_keep_to_its_document(shape, at, unit, place, io):
+    x, S0, dy, dS, _ = T.make(*shape, io, seed=61)
+    K, V, eps = shape[4], shape[5], 1e-6 if unit else None
+    if not unit:
+        x[1].mul_(K ** -0.5)
+    z = torch.zeros(shape[0], shape[1], dtype=torch.uint8, device="cuda")
+    z[:, at % 50::50] = 1
+    if place == "state":
+        z[:, :20] = 0
+    if place in ("dy", "inf dy"):
+        dy[0, at + 20, 0, 3] = float("nan") if place == "dy" else float("inf")
+    elif place == "dstate":
+        dS[0, 0, 5, 2] = float("nan")
+    else:
+        not_finite(place, x, S0, at)
+    _, _, ck = T.run(x, S0, reset=z, eps=eps)
+    got, want = ss.ss_gdr_bwd(*x, ck, dy, reset=z, dstate_final=dS, eps=eps), O.gdr_bwd(*x, dy, S0, z, dS, None, eps)
+    assert any(not torch.isfinite(v).all() for v in want.values()) or place in ("dy", "inf dy", "dstate")
+    want["dg"] = want["dg"].masked_fill((z != 0).cpu()[..., None], 0.0)
+    for n in T.GRADS:
+        print(n, end=" ")
+        same_finite(got[n], want[n], 2 * T.rel(K, 64, V), io if n in ("dq", "dk", "dv") else "f32")
