@@ -491,9 +491,15 @@ hipError_t launch_gnorm_t(const LaunchGnorm& p) {
         a.K = (int)p.group;
         grouped = false;
     }
-    const GnormShape sh = gnorm_shape(a.K, grouped);
+    GnormShape sh = gnorm_shape(a.K, grouped);
     const size_t sums = grouped ? (size_t)((VEC ? a.K / 8 : a.K) + a.K / a.group) * 4 : 0;
     if (p.back) {
+        // groups of one column in rows of just under 8192 have as many sums as values: with the weights beside them they exceed
+        // a CU's LDS, and two eights a lane, which read the weights from memory, do not
+        if (grouped && sh.nv == 1 && 96 * 4 + sums + 16 + (size_t)3 * sh.lanes * 8 * 4 > 160 * 1024) {
+            const int t = (int)((a.K + 1023) / 1024) * 64;
+            sh = {t, 2, t, 1};
+        }
         a.woff = (int)((96 * 4 + (grouped ? sums : sh.rows > 1 ? (size_t)3 * a.K * 4 : 0) + 15) / 16 * 4);
         const size_t shm = (size_t)a.woff * 4 + (sh.nv == 1 ? (size_t)3 * sh.lanes * 8 * 4 : 0);
         const int64_t n = gnorm_groups(p.M, p.K);
