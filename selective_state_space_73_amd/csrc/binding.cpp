@@ -334,6 +334,8 @@ bool gdr_inputs(const Call& c, PyObject* const* v, PyObject* reset, PyObject* sc
     if (sc == -1.0 && PyErr_Occurred()) return false;
     const double ep = eps == Py_None ? 0.0 : PyFloat_AsDouble(eps);
     if (ep == -1.0 && PyErr_Occurred()) return false;
+    // 0 is how the C ABI names keys that are used as they are; here that is None
+    if (eps != Py_None && (float)ep == 0.0f) refuse(PyExc_ValueError, "eps must be positive in 32 bits, or None: q and k are used as they are");
     out->dt = q.scalar_type();
     out->B = B; out->L = L; out->H = H;
     out->d = ss_gdr_dims{B, L, (int32_t)Hk, (int32_t)H, (int32_t)K, (int32_t)V, io_of(out->dt, "q"), (float)sc, (float)ep, 0};

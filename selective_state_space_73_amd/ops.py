@@ -431,8 +431,8 @@ def ss_gdr_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tenso
     q, k: [B,L,k_heads,dk], v [B,L,H,dv] (float32 or bfloat16, one dtype; the last dimension
     contiguous, any strides otherwise; H a multiple of k_heads, whose keys and queries H / k_heads
     neighbouring heads of v share; dk up to 256, dv up to 512); g (the logarithm of the decay) and
-    beta [B,L,H] float32. q and k are divided by their lengths, sqrt(sum x^2 + eps), unless eps is
-    None. scale: 1 / sqrt(dk) by default. state [B,H,dk,dv] float32, updated in place when given
+    beta [B,L,H] float32. q and k are divided by their lengths, sqrt(sum x^2 + eps) with eps > 0,
+    unless eps is None. scale: 1 / sqrt(dk) by default. state [B,H,dk,dv] float32, updated in place when given
     (zero initial state otherwise); reset [B,L] uint8 or bool: the state in front of its nonzero
     tokens counts as zero; ckpt: float32 tensor of gdr_ckpt_shape that receives what
     ss_gdr_bwd needs. Returns y [B,L,H,dv] in the I/O dtype. Asynchronous."""

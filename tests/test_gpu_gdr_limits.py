@@ -291,3 +291,16 @@ def test_gradients_of_what_is_not_finite_keep_to_its_document(shape, at, unit, p
     for n in T.GRADS:
         print(n, end=" ")
         same_finite(got[n], want[n], 2 * T.rel(K, 64, V), io if n in ("dq", "dk", "dv") else "f32")
+
+
+@pytest.mark.parametrize("eps", [0.0, -0.0, 1e-60])
+def test_an_eps_of_zero_is_refused(eps):
+    """It is not None, for which lengths are left alone: sqrt(sum x^2 + 0) has no value for a key of zeros."""
+    x, S0, dy, _, _ = T.make(1, 20, 1, 1, 16, 16, "f32")
+    _, _, ck = T.run(x)
+    with pytest.raises(ValueError):
+        ss.ss_gdr_fwd(*x, eps=eps)
+    with pytest.raises(ValueError):
+        ss.ss_gdr_bwd(*x, ck, dy, eps=eps)
+    with pytest.raises(ValueError):
+        ss.ss_gdr_step(*(t[:, 0] if t.dim() == 4 else t[:, 0].contiguous() for t in x), S0, eps=eps)
