@@ -35,8 +35,6 @@ typedef uint32_t gu4 __attribute__((ext_vector_type(4)));
 
 constexpr int kGdrC = SS_GDR_CHUNK;           // 64
 static_assert(kGdrC == 64, "a wave is a chunk's tokens");
-constexpr int kGdrTri = 6 * 16 * 32;         // values of an upper triangle of 64 x 64 in its blocks of 16 x 32
-constexpr int kGdrLow = 10 * 16 * 16;        // of a lower one in its tiles of 16 x 16
 
 // Operands by I/O type. bf16: q, k, v and gradients of y are exact operands; what is made in fp32
 // (states, inverses, solutions) goes in as a sum of three bf16 terms (24 bits, and the six largest of the nine products of
@@ -47,6 +45,7 @@ template <typename T> struct Mx;
 
 template <> struct Mx<uint16_t> {
     static constexpr int NT = 3;                                // terms of what is made in fp32
+    static_assert(NT * 2 == kGdrInverseBytes<true>);
     typedef gb8 F;
     template <int N> struct S { gb8 t[N]; };
     static __device__ __forceinline__ F ld(const uint16_t* p) { return *reinterpret_cast<const gb8*>(p); }
@@ -115,6 +114,7 @@ template <> struct Mx<uint16_t> {
 
 template <> struct Mx<float> {
     static constexpr int NT = 1;
+    static_assert(NT * 4 == kGdrInverseBytes<false>);
     typedef gf8 F;
     template <int N> struct S { gf8 t[1]; };
     template <int N, typename Fn>

@@ -71,7 +71,7 @@ size_t ckpt_states(const ss_gdr_dims& d) {
 }
 size_t ckpt_floats(const ss_gdr_dims& d) { return ckpt_states(d) + (size_t)d.batch * (size_t)d.seqlen * d.heads * d.dv; }
 
-// Per chunk and head: the tokens' factors and the inverse (6 blocks of 16 x 32, three bf16 terms or fp32). The forward in
+// Per chunk and head: the tokens' factors and the inverse (a triangle, in three bf16 terms or fp32). The forward in
 // segments: the states in front of them, what they make of these, and the states behind them. The backward: these of
 // gradients, the state's gradient behind every chunk, the gradients of v in fp32, and those of q and k by head of v where heads share them.
 struct GdrLayout { size_t co, wT, wS, wV, pq, pk, wE, wM, wF, wX, wQ, wG, total; int64_t seg, nseg; };
@@ -83,7 +83,8 @@ GdrLayout gdr_layout(const ss_gdr_dims& d, bool backward) {
     size_t off = 0;
     auto take = [&](size_t& at, size_t floats) { at = off; off = align256(off + floats * 4); };
     take(l.co, n * 10 * 64);
-    take(l.wT, n * 9216);
+    take(l.wT, n * ((backward ? selscan::kGdrTri : selscan::kGdrLow) *
+                    (d.io_dtype == SS_BF16 ? selscan::kGdrInverseBytes<true> : selscan::kGdrInverseBytes<false>) / 4));
     l.seg = ceil_div(d.seqlen, SS_GDR_CHUNK);
     l.nseg = 1;
     if (!backward) {

@@ -8,6 +8,11 @@
 
 namespace selscan {
 
+constexpr int kGdrTri = 6 * 16 * 32;         // values of an upper triangle of 64 x 64 in its blocks of 16 x 32
+constexpr int kGdrLow = 10 * 16 * 16;        // of a lower one in its tiles of 16 x 16
+// bytes of a value of the inverse: three bf16 terms, or fp32
+template <bool BF16> constexpr int kGdrInverseBytes = BF16 ? 6 : 4;
+
 // One launch of the gated delta rule, already validated by the C-ABI layer.
 struct LaunchGdr {
     enum Pass { kFwd, kBwd, kStep } pass;

@@ -29,3 +29,15 @@ def test_no_tokens_need_no_workspace(kw, backward):
            f"print(t.ss.ss_gdr_workspace_bytes(t.rdims(**{dict(kw, seqlen=0)!r}), {backward}))"
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True)
     assert r.returncode == 0 and r.stdout.split() == ["0"], r.stderr[-500:]
+
+
+@pytest.mark.parametrize("io,forward,backward", [(ss.SS_BF16, 3 * 10 * 256 * 2, 3 * 6 * 512 * 2), (ss.SS_F32, 10 * 256 * 4, 6 * 512 * 4)])
+def test_a_chunk_takes_what_it_uses(io, forward, backward):
+    """Ten rows of 64 factors, and the inverse: a lower triangle in tiles of 16 x 16, in the backward an upper one in blocks of
+    16 x 32, as three bf16 terms or in fp32. (300 heads are one segment.)"""
+    def more(back):
+        a, b = (ss.ss_gdr_workspace_bytes(rdims(heads=300, k_heads=300, seqlen=64 * n, io_dtype=io, dk=1, dv=1), back) for n in (9, 8))
+        return a - b
+    assert more(False) == 300 * (2560 + forward)
+    # the state's gradient and the flags of a chunk, the gradients of its values
+    assert abs(more(True) - 300 * (2560 + backward + 4 + 16 + 64 * 4)) < 1024
