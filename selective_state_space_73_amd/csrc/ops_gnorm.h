@@ -172,9 +172,12 @@ __device__ __forceinline__ void gnorm_ldp(const float* w, int c, int K, float no
     }
 }
 
-// v_exp and v_rcp, each within one step: the exponent's rounding adds |z| 2^-24 of e^-z
+// v_exp and v_rcp, each within one step. The exponent in two parts, since its rounding alone would be |z| 2^-24 of e^-z: what the
+// product with -log2 e rounds off, and what log2 e does, come back as a factor 1 + lo ln 2 (not where e^-z is infinite).
 __device__ __forceinline__ float gnorm_sigmoid(float z) {
-    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.44269504088896341f));
+    const float t = z * -1.44269504088896341f, lo = __builtin_fmaf(z, -1.925963033500011e-8f, __builtin_fmaf(z, -1.44269504088896341f, -t));
+    const float e = __builtin_amdgcn_exp2f(t);
+    return __builtin_amdgcn_rcpf(1.0f + (t < 127.0f ? __builtin_fmaf(e, lo * 0.693147180559945309f, e) : e));
 }
 
 struct GnormArgs {
@@ -268,7 +271,7 @@ __global__ void __launch_bounds__(MAXT, WAVES)
 k_gnorm_bwd(const GnormArgs p) {
     extern __shared__ float lds[];
     constexpr int R = LANES ? MAXT / LANES : 1;
-    const int nl = LANES ? LANES : blockDim.x, lane = threadIdx.x % nl, K = p.K, slot = threadIdx.x / nl;
+    const int nl = LANES ? LANES : blockDim.x, own = threadIdx.x % nl, K = p.K, slot = threadIdx.x / nl;
     const int64_t step = (int64_t)gridDim.x * R;
     float sw[NV][8] = {}, sa[NV][8] = {}, sn[NV][8] = {};
     // the weights by column, zeros past the last, in LDS (NV 1): three eights more in registers spill
@@ -304,12 +307,14 @@ k_gnorm_bwd(const GnormArgs p) {
 #pragma unroll
         for (int v = 0; v < NV; ++v)
 #pragma unroll
-            for (int k = 0; k < 5; ++k) raw[v][k].ld(from[k], row, (v * nl + lane) * 8, K);
+            for (int k = 0; k < 5; ++k) raw[v][k].ld(from[k], row, (v * nl + own) * 8, K);
     };
     gnorm_zero<LANES>(lds);
     const int64_t first = (int64_t)blockIdx.x * R + slot;
     if (AHEAD && first < p.M) fetch(first);
     for (int64_t row = first; row < p.M; row += step) {
+        int lane = own;                               // columns are made again for every row: kept over the loop they would spill
+        asm volatile("" : "+v"(lane));
         float y[NV][8], z[NV][8], s[NV][8], ds[NV][8], dn[NV][8], ry[GROUPED ? NV : 1][8], sg[NV][8], q[2] = {0.0f, 0.0f};
         if (!AHEAD) fetch(row);
 #pragma unroll
@@ -422,7 +427,7 @@ k_gnorm_bwd(const GnormArgs p) {
             for (int v = 0; v < NV; ++v)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const int c = (v * nl + lane) * 8 + j;
+                    const int c = (v * nl + own) * 8 + j;
                     if (R == 1) {
                         if (c < K) { out[c] = sw[v][j]; out[K + c] = sa[v][j]; out[2 * K + c] = sn[v][j]; }
                     } else if (c < K) {

@@ -43,3 +43,19 @@ def test_groups_of_a_few_columns_in_wide_rows(shape, io):
             size = (terms * h.abs()).sum(0)
         tol = 2.0 ** -24 * (4 * (24 + math.log2(K) + 1) + (math.ceil(M / 256) if sums else 0))
         T.near(v, val, 4 * tol * size + (2.0 ** -24 if sums else half) * val.abs())
+
+
+@pytest.mark.parametrize("sign", [-1.0, 1.0])
+@pytest.mark.parametrize("K,group", [(64, 64), (640, 128), (2560, 2560), (9000, 9000)])
+def test_gates_far_out_keep_their_digits(K, group, sign):
+    """Gates from 6 to 85, either way: e^-z is as near as near 0, whatever its size, so that silu and its slope are within what a
+    sigmoid is allowed near 0 (4 roundings, and as many products), relative to themselves. The slope is sig (1 + z (1 - sig)), whose two
+    terms are up to 1 + |z| times sig and do not cancel for |z| >= 6."""
+    u = 2.0 ** -24
+    x, ds, _ = T.make(5, K, group, "f32", ("gate",), seed=K)
+    x["gate"] = (sign * torch.linspace(6, 85, 5 * K).view(5, K)).cuda()
+    s, _ = ss.ss_gnorm_fwd(**x)
+    sw, _ = O.gnorm_fwd(**x)
+    T.near(s, sw, (T.rel(K) + 8 * u) * sw.abs())
+    got, want = ss.ss_gnorm_bwd(ds=ds, **x)["dgate"], O.gnorm_bwd(ds=ds, **x)["dgate"][0]
+    T.near(got, want, (T.rel(K) + 12 * u) * want.abs())
