@@ -12,9 +12,9 @@
 namespace selscan {
 
 // Segments that run at the same time: two workgroups a CU where it holds two (bf16, dk up to 128) and a segment
-// then has 16 chunks at least, else one, which is faster alone, with fewer to join. 128 x 128 in bf16, two and one: 32768
-// tokens of 16 heads 722 and 748 us, 8192 of 16 322 and 255, 2048 of 40 168 and 150 (in fp32, where a CU
-// holds one: 1822 and 1711, 610 and 501, 346 and 245). A segment has four chunks at least, as each is
+// then has 16 chunks at least, else one, which is faster alone, with fewer to join. 128 x 128 in bf16, none, two and one: 32768
+// tokens of 16 heads 2916, 708 and 760 us, 8192 of 16 723, 281 and 243, 2048 of 40 203, 163 and 157 (in fp32, where a CU
+// holds one: 5990, 1615 and 1560, 1508, 509 and 446, 399, 332 and 293). A segment has four chunks at least, as each is
 // one more to join.
 int64_t gdr_segment(int64_t BH, int64_t dv, int64_t nchunks, bool two) {
     const int64_t groups = BH * ((dv + 63) / 64);           // workgroups of one segment
@@ -26,10 +26,12 @@ int64_t gdr_segment(int64_t BH, int64_t dv, int64_t nchunks, bool two) {
 }
 
 // The backward's: one workgroup a CU, so that what a segment does for itself slows no other. 32768 tokens of 16 heads of
-// 128 x 128, no segments, one and two workgroups a CU: 4.2, 1.76 and 1.79 ms in bf16, 8.8, 3.9 and 5.3 in fp32.
+// 128 x 128, no segments, one and two workgroups a CU: 4.2, 1.84 and 1.89 ms in bf16, 8.9, 3.9 and 5.4 in fp32. Up to five chunks the
+// two launches more cost what they save (4 heads of 128 x 128 in bf16 at 256, 384 and 512 tokens, with segments and without: 77 and
+// 70 us, 77 and 81, 78 and 94, and 79, 88 and 98 with segments where decays are so slow that all chunks behind one count).
 int64_t gdr_segment_back(int64_t BH, int64_t dv, int64_t nchunks) {
     const int64_t n = 256 / (BH * ((dv + 63) / 64));
-    if (n < 2) return nchunks;
+    if (n < 2 || nchunks < 6) return nchunks;
     const int64_t seg = (nchunks + n - 1) / n;
     return seg < 2 ? 2 : seg;
 }
