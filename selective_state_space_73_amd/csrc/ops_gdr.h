@@ -40,7 +40,7 @@ static_assert(kGdrC == 64, "a wave is a chunk's tokens");
 // (states, inverses, solutions) goes in as a sum of three bf16 terms (24 bits, and the six largest of the nine products of
 // two such: 2^-24 of their size is left out, as a rounding to fp32 leaves it out). fp32: every operand as three terms, made where
 // it is read: six bf16 products take 2.7 times less of the matrix cores than one fp32 product, and with
-// their terms made a chunk still takes a fifth less (a prompt of 64 tokens: 20.6 to 16.2 us).
+// their terms made a chunk still takes less (a prompt of 64 tokens: 20.6 to 17 us).
 template <typename T> struct Mx;
 
 template <> struct Mx<uint16_t> {
@@ -390,7 +390,7 @@ __device__ __forceinline__ void gdr_arrived() {
 // diagonal row by row, below them block by block, T_ij = -T_ii sum_l N_il T_lj, in fp32 products
 // whose operands stay in registers.
 // BACK: T transposed, which is how the results lie.
-// 32768 chunks of keys of 128 in bf16: 290 us, 4.1 TB/s of keys read and factors written, which is what bounds
+// 32768 chunks of keys of 128 in bf16: 272 us, 4.1 TB/s of keys read and factors written, which is what bounds
 // it; 4 chunks: 11 us, one wave's chain of products.
 template <typename T, int DKP, bool BACK>
 __global__ void __launch_bounds__(256)
@@ -671,10 +671,10 @@ struct GdrState {
 // registers. What all waves need lies in LDS: keys twice (the next chunk's come while this one's are in
 // use), queries, T and the tokens' factors once, loaded again as soon as the last wave has used them; P is
 // made here, two or three tiles a wave, since reading it back would cost as much as T. Two workgroups a CU
-// in bf16 (registers and LDS hold no third). 131072 tokens of 16 heads of 128 x 128 in bf16: 1.0 ms, a chunk 18,000 cycles
-// for two workgroups and 11,800 for one alone on its CU: what bounds it is a chunk's chain (read, multiply, solve,
-// multiply), with the matrix cores and the vector units each busy for about 40%. With checkpoints it writes more
-// than it reads: 8 x 2048 tokens of 40 heads 593 us, 3.2 TB/s (640 workgroups for 512 places: about a quarter of it).
+// in bf16 (registers and LDS hold no third). 131072 tokens of 16 heads of 128 x 128 in bf16: 1.1 ms, a chunk 16,100 cycles
+// for two workgroups and 13,700 for one alone on its CU: what bounds it is a chunk's chain (read, multiply, solve,
+// multiply; 236 matrix instructions a wave). With checkpoints it writes more
+// than it reads: 8 x 2048 tokens of 40 heads 600 us, 3.1 TB/s (640 workgroups for 512 places: about a quarter of it).
 template <typename T, int DKP, bool TWO, bool AL>
 struct GdrWalk : GdrState<DKP> {
     using M = Mx<T>;
@@ -1098,8 +1098,10 @@ __device__ __forceinline__ int64_t gdr_reach(const LaunchGdr& p, int64_t bh, int
 // A long sequence in few heads, cut into segments that run at the same time. First the state behind each segment, from
 // nothing in front of it (or, the first, from the caller's) and from where it still matters on; and, as dk columns more that
 // start as the identity and get no values, what the segment makes of the state in front of it, where anything is
-// left of that. The caller's state is copied for the walk's first segment, as its last one overwrites it. k_gdr_join puts the ends together. (2048 tokens of 40 heads: 49 and 13 us, 64 for the walk of three
-// segments. 131072 tokens of 16 heads: 268, 5 and 1076 us; the whole call 1.7 ms, 10.6 in one segment.)
+// left of that. The caller's state is copied for the walk's first segment, as its last one overwrites it. k_gdr_join puts the
+// ends together. (2048 tokens of 40 heads: 49 and 13 us, 75 for the walk of three segments. 131072 tokens of 16 heads: 266, 5 and
+// 1166 us, or 1000 and 120 for ends and join where some heads decay so slowly that their segments let a state through; the
+// whole call 1.5 to 2.5 ms, 10.6 in one segment.)
 template <typename T, int DKP, bool TWO, bool AL, int GROUPS>
 __global__ void __launch_bounds__(256, GROUPS)
 k_gdr_ends(const LaunchGdr p) {
@@ -1250,8 +1252,9 @@ k_gdr_again(const LaunchGdr p) {
 // one waits for its next chunk while the other works. A long sequence in few heads is cut into segments that run at the
 // same time. k_gdr_ends_back first makes the gradient behind each of them from the chunks behind it, as far back as they
 // count: all of them in the worst case, when the first segment takes as long as one workgroup did, on a card that
-// is not full; what the walk comes to says whether that was far enough, and k_gdr_again_back repeats where it was not. 8 x 2048 tokens of 40 heads of 128 x 128 in bf16: 633 us, 3.0 TB/s, bound as the forward's; 3 x 1001
-// tokens of 6 heads of 96 x 129 in fp32, with resets: 114 us (239 in one segment).
+// is not full; what the walk comes to says whether that was far enough, and k_gdr_again_back repeats where it was not.
+// 8 x 2048 tokens of 40 heads of 128 x 128 in bf16: 634 us, 2.9 TB/s, bound as the forward's; 3 x 1001 tokens of 6 heads of 96 x 129
+// in fp32, with resets: 56 and 67 us (239 in one segment).
 template <typename T, int DKP, bool AL>
 struct GdrWalkBack : GdrState<DKP> {
     using M = Mx<T>;
@@ -1676,7 +1679,7 @@ k_gdr_again_back(const LaunchGdr p) {
 //     + sum_{j < t} beta_j (k . a3b X W^T)_j + e^G_last <S0, W>
 // A wave has a quarter of dk, transposed (a lane has a token): sums over dk are sums over registers and two moves, factors
 // of tokens one register, and four neighbouring columns one store. Terms over dv go through LDS 32 at a time, the next
-// ones on their way to registers meanwhile. 10240 chunks of 128 x 128 in bf16: 723 us, 3.9 TB/s of what it reads and
+// ones on their way to registers meanwhile. 10240 chunks of 128 x 128 in bf16: 745 us, 3.8 TB/s of what it reads and
 // writes; a workgroup waits for its first and its last rows while the other of its CU works (with one way to load
 // a kernel: where aligned and unaligned loads met, the copies between them waited for memory, 1005 us).
 template <typename T, int DKP, bool AL, bool VEC, int GROUPS>

@@ -7,8 +7,8 @@
 // The backward makes everything again from the inputs: it reads y, gate, residual, ds and dn and writes
 // three gradients, no more bytes than with anything kept. Sums over rows (of w, scale, w_next) stay in
 // the registers of a workgroup that goes through many rows, and meet in a second kernel in a fixed order.
-// bf16 with gate and residual: 16384 x 2560 and both norms 89 us forward, 4.7 TB/s, and 158 us backward, 4.3 TB/s
-// (a large copy reaches 4.9); 16384 x 5120 in heads of 128 87 us, 5.8 TB/s; 64 x 2560 4 us.
+// bf16 with gate and residual: 16384 x 2560 and both norms 89 us forward, 4.7 TB/s, and 247 us with its gradients, 4.4 TB/s
+// (a large copy reaches 4.9; the backward's kernel alone, under a profiler, 165 to 181); 16384 x 5120 in heads of 128 87 us, 5.8 TB/s; 64 x 2560 4 us.
 #pragma once
 #include "ops_layer_internal.h"
 #include "ops_rows.h"
