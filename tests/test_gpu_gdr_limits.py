@@ -304,3 +304,30 @@ def test_an_eps_of_zero_is_refused(eps):
         ss.ss_gdr_bwd(*x, ck, dy, eps=eps)
     with pytest.raises(ValueError):
         ss.ss_gdr_step(*(t[:, 0] if t.dim() == 4 else t[:, 0].contiguous() for t in x), S0, eps=eps)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("K,V,odd", [(64, 150, 3), (100, 70, 64), (128, 128, 127)])
+def test_one_column_that_runs_again(K, V, odd, io):
+    """Columns of a state do not depend on each other: one of 2^60 that nothing is added to, among others of about 1, with a NaN in
+    one more. Each is relative to its own size, over the last tokens of every chunk."""
+    x, S0, dy, dS, _ = T.make(1, 64 * 11, 1, 2, K, V, io, seed=67 + K)
+    x[3].fill_(-13 / 64 * 0.6931471805599453)
+    x[2][..., odd] = 0.0
+    S0[..., odd] *= 2.0 ** 60
+    x[2][0, 30, 1, 5] = float("nan")
+    y, S, ck = T.run(x, S0)
+    yw, Sw = O.gdr_fwd(*x, S0)
+    for n in range(11):
+        at = slice(64 * n + 48, 64 * n + 64)
+        for h in range(2):
+            ok = torch.isfinite(yw[0, at, h]).all(0)
+            assert ok.sum() == V - h
+            got, want = y[0, at, h].double().cpu()[:, ok], yw[0, at, h][:, ok]
+            size = want.abs().amax(0, keepdim=True)
+            T.near(got / size, want / size, T.rel(K, 512), io)
+    for h in range(2):
+        ok = torch.isfinite(Sw[0, h]).all(0)
+        assert (torch.isfinite(S[0, h]).all(0).cpu() == ok).all()
+        size = Sw[0, h].abs().amax(0)[ok]
+        T.near(S[0, h].double().cpu()[:, ok] / size, Sw[0, h][:, ok] / size, T.rel(K, 512), "f32")
