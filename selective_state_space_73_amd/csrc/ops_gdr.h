@@ -1165,13 +1165,17 @@ k_gdr_join(const LaunchGdr p) {
     if (!__any(any)) return;
     W k(p, nullptr, nullptr, nullptr, nullptr, nullptr, 0, bh, 0, 0, col);
     const int64_t kk = (int64_t)p.dk * p.dk;
-    gf8 x[2][W::ND];                                  // the map's rows of this lane, 32 columns ahead, the next segment's behind the last
-    auto read = [&](int seg, int s, gf8 (&to)[W::ND]) {
+    // The map's rows of this lane, 32 columns of eight tiles ahead, the next segment's behind the last (256 rows in two halves: all
+    // at once, twice, would be the registers there are).
+    constexpr int HALVES = W::ND > 8 ? 2 : 1, NH = W::ND / HALVES, STEPS = W::KD * HALVES;
+    gf8 x[2][NH];
+    auto read = [&](int seg, int step, gf8 (&to)[NH]) {
+        const int s = step / HALVES;
         const GdrBuf<float> map(p.wM + (seg * BH + bh) * kk, (unsigned)kk * 4);
 #pragma unroll
-        for (int d = 0; d < W::ND; ++d) {
-            const int row = 32 * (d >> 1) + 8 * (m >> 2) + 4 * (d & 1) + (m & 3);
-            to[d] = map.template ld8<false>((unsigned)(row * p.dk + 32 * s + 8 * g) * 4, 32 * s + 8 * g, p.dk);
+        for (int e = 0; e < NH; ++e) {
+            const int d = step % HALVES * NH + e, row = 32 * (d >> 1) + 8 * (m >> 2) + 4 * (d & 1) + (m & 3);
+            to[e] = map.template ld8<false>((unsigned)(row * p.dk + 32 * s + 8 * g) * 4, 32 * s + 8 * g, p.dk);
         }
     };
     k.load_state(p.wE + (BH + bh) * kv, p.dv);
@@ -1186,11 +1190,14 @@ k_gdr_join(const LaunchGdr p) {
         for (int s = 0; s < W::KD; ++s) sb[s] = M::template split<M::NT>(gdr_pair(k.S[2 * s], k.S[2 * s + 1]));
         k.load_state(end, p.dv);
 #pragma unroll
-        for (int s = 0; s < W::KD; ++s) {
-            read(s + 1 < W::KD ? seg : next, (s + 1) % W::KD, x[(s + 1) & 1]);
+        for (int q = 0; q < STEPS; ++q) {
+            read(q + 1 < STEPS ? seg : next, (q + 1) % STEPS, x[(q + 1) & 1]);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int d = 0; d < W::ND; ++d) k.S[d] = M::mul(M::template split<M::NT>(x[s & 1][d]), sb[s], k.S[d]);
+            for (int e = 0; e < NH; ++e) {
+                gf4& S = k.S[q % HALVES * NH + e];
+                S = M::mul(M::template split<M::NT>(x[q & 1][e]), sb[q / HALVES], S);
+            }
         }
         if (on) k.store_state(end, p.dv);
         else k.load_state(end, p.dv);
